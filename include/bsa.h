@@ -639,6 +639,170 @@ bsa_status bsa_upscale_threshold(const float* T_base, int64_t heads, int32_t Ub,
                                  int32_t Ut, int32_t Vt, float* T_target, void* stream);
 
 /*
+ * Paged key/value cache - serving a language model token by token.
+ *
+ * The cache is two arrays of pages, k and v, bf16 [n_pages, H_kv, page_size,
+ * D] (one page and head: page_size consecutive rows), and optionally a third,
+ * k_mean, bf16 [n_pages, H_kv, D].  A batch holds `seqs` sequences with any
+ * number of new tokens each (one, a chunk, a whole prompt, none); the new
+ * tokens of all of them are packed along one axis of `tokens` entries.
+ *
+ *   page_table  device int32 [seqs, max_pages]: position p of sequence s is
+ *               row p % page_size of page page_table[s][p / page_size].
+ *               Entries behind a sequence's last page are not read.  An entry
+ *               outside [0, n_pages) raises BSA_ERR_BOUNDS (bsa_paged_append
+ *               writes nothing there; what is read through it is unspecified).
+ *   q_start     device int32 [seqs + 1], ascending: sequence s owns packed
+ *               tokens q_start[s] .. q_start[s+1] - 1.  Packed tokens before
+ *               q_start[0] and from q_start[seqs] on belong to no sequence:
+ *               nothing is written for them.
+ *   kv_len      device int32 [seqs]: tokens of the sequence that the cache
+ *               holds with the new ones, which are its last; with n new
+ *               tokens, new token i has position kv_len[s] - n + i.
+ *   A sequence whose entries make no sense (a decreasing or negative start, a
+ *   start beyond `tokens`, a length that is negative or beyond max_pages *
+ *   page_size) raises BSA_ERR_BOUNDS and is left out.
+ *
+ * The host needs to know none of these values, so the calls can be captured
+ * into a graph once and replayed as the sequences grow.
+ *
+ *   seqs 0 .. 32768; tokens 0 .. 2^24 with tokens * H < 2^31 (0 of either:
+ *   nothing to do); page_size 16, 32, 64 or 128; max_pages * page_size <=
+ *   2^24; n_pages * H_kv * page_size < 2^31; D 64 or 128; H_kv divides H,
+ *   H / H_kv <= 128, H <= 65535.  Index arrays are 4-byte aligned, the caches
+ *   and k_mean 16-byte aligned.
+ *   Queries, keys and values of the new tokens are [tokens, heads, D] with D
+ *   and the heads contiguous; `*_stride` is the distance between tokens in
+ *   elements, a multiple of 8 and at least heads * D, so that they may be
+ *   views of one projection's output.
+ */
+typedef struct {
+    const int32_t* page_table;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    int32_t seqs;
+    int32_t tokens;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t n_pages;
+} bsa_paged_batch;
+
+/*
+ * bsa_paged_append - write the new tokens' keys and values into their pages,
+ * with the heads' norms and the position rotation applied on the way.
+ *
+ * For every head of the queries and keys, in fp32 and rounded once:
+ *     x <- x * w / sqrt(mean(x^2) + eps)           (with q_norm / k_norm = w)
+ *     (x_a, x_b) <- (x_a cos - x_b sin, x_b cos + x_a sin)     (with rope)
+ * over the pairs (a, b) = (i, i + rot/2), or (2i, 2i+1) when interleaved, i <
+ * rot/2; values rot .. D-1 are not rotated.  Queries go to q_out; keys and
+ * (unchanged) values to the cache.  When a 128-token block of a sequence is
+ * full after the call and was not before, k_mean at the page of the block's
+ * last token receives the mean of the block's keys as the cache holds them
+ * (fp32 sum, rounded to bf16).  The same tokens appended in other chunks leave
+ * the same bits.  A sequence cut back (kv_len lowered) is appended to again
+ * like any other.
+ *
+ *  q, k, v    device bf16, 16-byte aligned; q NULL: keys and values only.
+ *  rope       device fp32 [rope_len, rot], 16-byte aligned, or NULL: the
+ *             cosines of position p's rot/2 angles, then their sines.  A
+ *             position at or beyond rope_len raises BSA_ERR_BOUNDS (the last
+ *             row is used).
+ *  rot        16 .. D, a multiple of 16.   interleaved  0 or 1.
+ *  q_norm, k_norm  device bf16 [D], 16-byte aligned, or NULL.
+ *  eps        >= 0 and finite.
+ *  q_out      device bf16 [tokens, H, D], 16-byte aligned; may be q itself
+ *             (with the same stride).
+ *  k_cache, v_cache, k_mean  as above; k_mean NULL: no means.
+ *  Two new tokens must not share a slot of the cache (two sequences, or two
+ *  table entries of one, that name the same page for positions both written).
+ *  A sequence with more new tokens than kv_len raises BSA_ERR_BOUNDS; the
+ *  tokens before position 0 are left out.
+ */
+bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, int32_t H, int32_t H_kv,
+                            int32_t D, const float* rope, int32_t rope_len, int32_t rot,
+                            int32_t interleaved, const void* q_norm, const void* k_norm, float eps,
+                            void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                            void* k_mean, void* stream);
+
+/*
+ * bsa_forward_paged - attention of the new tokens over their sequences' pages.
+ *
+ * For the new token at position p of a sequence of L = kv_len tokens, query
+ * head h and the key/value head h / (H / H_kv), over the keys j < L with
+ *     (causal == 0 or j <= p)
+ *     and (window == 0 or j > p - window or j < sinks)
+ *     and (sel == NULL or j / 128 is among the token's listed blocks):
+ *     s_j = (q . k_j) * scale,  LSE = ln sum_j exp(s_j),
+ *     O = sum_j exp(s_j - LSE) v_j.
+ * Without any such key O = 0 and LSE = -inf.  What lies in slots behind the
+ * end of a sequence does not matter, NaN included.
+ *
+ *  q          device bf16, 16-byte aligned.
+ *  causal     0 or 1.   window, sinks  >= 0; window must be 0 with sel.
+ *  sel        device int32 [tokens, H_kv, sel_width] or NULL: blocks of 128
+ *             positions that each token attends to (bsa_select_paged, or any
+ *             lists; in any order, an entry twice counts once);
+ *  sel_cnt    device int32 [tokens, H_kv]: how many of them are valid.  A
+ *             count above sel_width is clamped and raises BSA_ERR_OVERFLOW;
+ *             a negative count (taken as 0) and an entry that is no block of
+ *             the sequence (left out) raise BSA_ERR_BOUNDS.  Blocks behind
+ *             the token's position are left out in silence when causal.
+ *  sel_width  >= 1 with sel, else 0.
+ *  scale      <= 0 selects 1/sqrt(D); a NaN or infinite scale is rejected.
+ *  workspace  device scratch of at least bsa_forward_paged_workspace_size()
+ *             bytes, 16-byte aligned; its contents on entry do not matter.
+ *             Calls that share a workspace must not overlap on the GPU.
+ *  o          device bf16 [tokens, H, D], 16-byte aligned, out.
+ *  lse        device fp32 [tokens, H] out.
+ *  A row's result does not depend on timing; it may depend in its last bits
+ *  on the rest of the batch (which decides where a long row is split).
+ */
+bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                             const void* k_cache, const void* v_cache, int32_t H, int32_t H_kv,
+                             int32_t D, int32_t causal, int32_t window, int32_t sinks,
+                             const int32_t* sel, const int32_t* sel_cnt, int32_t sel_width,
+                             float scale, void* workspace, size_t workspace_bytes, void* o,
+                             float* lse, void* stream);
+
+/* Bytes of workspace bsa_forward_paged needs (0 for sizes it rejects);
+ * sel_width 0: without lists.  Only b's sizes are read. */
+size_t bsa_forward_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
+                                        int32_t sel_width);
+
+/*
+ * bsa_select_paged - the blocks each new token attends to, by a cheap score.
+ *
+ * For the token at position p and a key/value head, own = p / 128: blocks 0 ..
+ * sink_blocks - 1 and own - local_blocks + 1 .. own are taken in any case, and
+ * of the blocks between them the topk with the highest
+ *     score_j = sum over the head's query heads of q . k_mean(block j)
+ * (all of them where there are no more than topk).  The comparison is that of
+ * the exact scores of the bf16 inputs, up to fp64 rounding; equal scores go to
+ * the lower block.  A NaN score is the lowest.  Blocks between are full, so
+ * that k_mean as bsa_paged_append leaves it covers them.
+ *
+ *  q          device bf16, 16-byte aligned (rotated, as bsa_forward_paged
+ *             takes it).
+ *  k_mean     device bf16 [n_pages, H_kv, D].
+ *  topk, sink_blocks  >= 0.   local_blocks  >= 1.
+ *  max_pages * page_size <= 2^20 (else BSA_ERR_UNSUPPORTED).
+ *  workspace  as in bsa_forward_paged (may be NULL where the size is 0).
+ *  sel        device int32 [tokens, H_kv, width] out: ascending, tail -1.
+ *  sel_cnt    device int32 [tokens, H_kv] out.
+ *  width      at least topk + sink_blocks + local_blocks.
+ */
+bsa_status bsa_select_paged(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                            const void* k_mean, int32_t H, int32_t H_kv, int32_t D, int32_t topk,
+                            int32_t sink_blocks, int32_t local_blocks, void* workspace,
+                            size_t workspace_bytes, int32_t* sel, int32_t* sel_cnt, int32_t width,
+                            void* stream);
+
+/* Bytes of workspace bsa_select_paged needs.  Only b's sizes are read. */
+size_t bsa_select_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D);
+
+/*
  * bsa_set_forward_options - how this host thread's later forward calls
  * launch (every bsa_forward* entry point).  The result does not depend on
  * the schedule: every choice computes the same per-row arithmetic, bit for

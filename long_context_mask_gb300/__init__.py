@@ -27,16 +27,21 @@ from .binding import (  # noqa: F401
     forward_gather0,
     forward_masked,
     forward_packed,
+    forward_paged,
+    forward_paged_workspace_size,
     forward_scatter,
     gather0_layout,
     gather0_sizes,
     gather_rows,
     lib_path,
     load_library,
+    paged_append,
     reorder_guard,
     reorder_rows,
     resident_ctas,
     sample_blocks,
+    select_paged,
+    select_paged_workspace_size,
     set_forward_options,
     selftest_exp2,
     selftest_wait_timeout,

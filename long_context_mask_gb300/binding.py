@@ -26,6 +26,8 @@ EXPORTS = ("bsa_build_index", "bsa_build_crm", "bsa_forward_crm", "bsa_upscale_t
            "bsa_forward", "bsa_forward_masked", "bsa_forward_packed", "bsa_gather_rows",
            "bsa_gather0_sizes", "bsa_gather0_layout", "bsa_forward_gather0",
            "bsa_forward_scatter",
+           "bsa_paged_append", "bsa_forward_paged", "bsa_forward_paged_workspace_size",
+           "bsa_select_paged", "bsa_select_paged_workspace_size",
            "bsa_device_status", "bsa_resident_ctas", "bsa_status_string", "bsa_selftest_exp2",
            "bsa_selftest_wait_timeout")
 
@@ -91,6 +93,19 @@ def load_library():
     lib.bsa_forward_gather0.restype = i32
     lib.bsa_forward_scatter.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32, P, P, i32, P, P, f32, P, P, P]
     lib.bsa_forward_scatter.restype = i32
+    sz = ctypes.c_size_t
+    lib.bsa_paged_append.argtypes = [P, P, i64, P, i64, P, i64, i32, i32, i32, P, i32, i32, i32, P, P, f32,
+                                     P, i64, P, P, P, P]
+    lib.bsa_paged_append.restype = i32
+    lib.bsa_forward_paged.argtypes = [P, P, i64, P, P, i32, i32, i32, i32, i32, i32, P, P, i32, f32, P, sz, P,
+                                      P, P]
+    lib.bsa_forward_paged.restype = i32
+    lib.bsa_forward_paged_workspace_size.argtypes = [P, i32, i32, i32, i32]
+    lib.bsa_forward_paged_workspace_size.restype = sz
+    lib.bsa_select_paged.argtypes = [P, P, i64, P, i32, i32, i32, i32, i32, i32, P, sz, P, P, i32, P]
+    lib.bsa_select_paged.restype = i32
+    lib.bsa_select_paged_workspace_size.argtypes = [P, i32, i32, i32]
+    lib.bsa_select_paged_workspace_size.restype = sz
     lib.bsa_set_forward_options.argtypes = [P]
     lib.bsa_set_forward_options.restype = i32
     lib.bsa_reorder_guard.argtypes = [P, P]
@@ -610,6 +625,175 @@ def forward_scatter(q, k, v, R: int, kv_idx, kv_cnt, o, lse, *, log_w=None, row_
     _check("bsa_forward_scatter", code)
 
 
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
+def _token_rows(t, name, tokens, heads, D):
+    """Distance between the tokens of t [tokens, heads, D] bf16 in elements;
+    the heads of a token must be contiguous, the tokens need not be."""
+    import torch
+    _dtype(t, name, torch.bfloat16)
+    if tuple(t.shape) != (tokens, heads, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
+    return t.stride(0) if tokens > 1 else heads * D
+
+
+def _strided_ptr(t):
+    """The address of a tensor whose strides the call passes on."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _paged_cache(k_cache, v_cache):
+    import torch
+    _dtype(k_cache, "k_cache", torch.bfloat16)
+    _dtype(v_cache, "v_cache", torch.bfloat16)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must share the shape [pages, H_kv, page_size, D]")
+    return k_cache.shape
+
+
+def _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages):
+    import torch
+    _dtype(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [seqs, max_pages]")
+    seqs, max_pages = page_table.shape
+    _flat(q_start, "q_start", seqs + 1, torch.int32)
+    _flat(kv_len, "kv_len", seqs, torch.int32)
+    return PagedBatch(_ptr(page_table), _ptr(q_start), _ptr(kv_len), seqs, tokens, max_pages, page_size, n_pages)
+
+
+def _scratch(need, workspace, device):
+    """(the tensor that holds the scratch, its address, its bytes)."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None, q_out=None, rope=None,
+                 interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, k_mean=None,
+                 stream=None):
+    """Write the new tokens' keys and values [tokens, H_kv, D] into the pages
+    [pages, H_kv, page_size, D] of the cache, keys (and q [tokens, H, D], into
+    q_out) normalised by q_norm / k_norm [D] and rotated by rope [positions,
+    rot] (cosines, then sines) on the way; k_mean [pages, H_kv, D] receives the
+    mean key of every 128-token block that fills up (see bsa.h)."""
+    import torch
+    n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+    tokens = k.shape[0]
+    ks, vs = _token_rows(k, "k", tokens, H_kv, D), _token_rows(v, "v", tokens, H_kv, D)
+    H, qs, os_ = H_kv, 0, 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("paged_append: pass q_out with q")
+        H = q.shape[1]
+        qs, os_ = _token_rows(q, "q", tokens, H, D), _token_rows(q_out, "q_out", tokens, H, D)
+    rope_len = rot = 0
+    if rope is not None:
+        _dtype(rope, "rope", torch.float32)
+        if rope.dim() != 2:
+            raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, rot]")
+        rope_len, rot = rope.shape
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        _flat(t, name, D, torch.bfloat16)
+    _flat(k_mean, "k_mean", n_pages * H_kv * D, torch.bfloat16)
+    _same_device(k_cache, v_cache, k, v, page_table, q_start, kv_len, q, q_out, rope, q_norm, k_norm, k_mean)
+    b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    code = load_library().bsa_paged_append(
+        ctypes.byref(b), _strided_ptr(q) if q is not None else None, qs, _strided_ptr(k), ks, _strided_ptr(v), vs,
+        H, H_kv, D, _ptr(rope), rope_len, rot, int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm), float(eps),
+        _strided_ptr(q_out) if q is not None else None, os_, _ptr(k_cache), _ptr(v_cache), _ptr(k_mean),
+        _stream(stream))
+    _check("bsa_paged_append", code)
+
+
+def forward_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
+                                 D: int, sel_width: int = 0) -> int:
+    b = PagedBatch(None, None, None, seqs, tokens, max_pages, page_size, 1)
+    return int(load_library().bsa_forward_paged_workspace_size(ctypes.byref(b), H, H_kv, D, sel_width))
+
+
+def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, causal: bool = True,
+                  window: int = 0, sinks: int = 0, sel=None, sel_cnt=None, scale: float = 0.0,
+                  workspace=None, stream=None):
+    """Attention of the new tokens q [tokens, H, D] over their sequences' pages:
+    fills o [tokens, H, D] bf16 and lse [tokens, H] fp32.  sel [tokens, H_kv,
+    width] / sel_cnt [tokens, H_kv] restrict each token to its listed 128-token
+    blocks (see bsa.h).  ``workspace`` is a CUDA tensor of at least
+    forward_paged_workspace_size() bytes (allocated here when omitted)."""
+    import torch
+    n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
+    tokens, H = q.shape[0], q.shape[1]
+    qs = _token_rows(q, "q", tokens, H, D)
+    _dtype(o, "o", torch.bfloat16)
+    if o.shape != q.shape:
+        raise ValueError("o must have q's shape [tokens, H, D]")
+    _flat(lse, "lse", tokens * H, torch.float32)
+    width = 0
+    if (sel is None) != (sel_cnt is None):
+        raise ValueError("forward_paged: sel and sel_cnt go together")
+    if sel is not None:
+        _dtype(sel, "sel", torch.int32)
+        if sel.dim() != 3 or sel.shape[0] < tokens or sel.shape[1] != H_kv:
+            raise ValueError(f"sel: shape {tuple(sel.shape)}, expected [>= {tokens}, {H_kv}, width]")
+        width = sel.shape[2]
+        _flat(sel_cnt, "sel_cnt", tokens * H_kv, torch.int32)
+    _same_device(k_cache, v_cache, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, workspace)
+    lib = load_library()
+    b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    need = lib.bsa_forward_paged_workspace_size(ctypes.byref(b), H, H_kv, D, width)
+    keep, ws, nbytes = _scratch(need, workspace, q.device)
+    code = lib.bsa_forward_paged(
+        ctypes.byref(b), _strided_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), H, H_kv, D, int(bool(causal)),
+        int(window), int(sinks), _ptr(sel), _ptr(sel_cnt), width, float(scale), ws, nbytes, _ptr(o), _ptr(lse),
+        _stream(stream))
+    _check("bsa_forward_paged", code)
+
+
+def select_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
+                                D: int) -> int:
+    b = PagedBatch(None, None, None, seqs, tokens, max_pages, page_size, 1)
+    return int(load_library().bsa_select_paged_workspace_size(ctypes.byref(b), H, H_kv, D))
+
+
+def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_size: int, topk: int,
+                 sink_blocks: int = 1, local_blocks: int = 1, workspace=None, stream=None):
+    """The 128-token blocks each new token and key/value head attends to: the
+    first sink_blocks, the last local_blocks and the topk best of the others by
+    the token's queries times k_mean [pages, H_kv, D].  Fills sel [tokens, H_kv,
+    width] (ascending, tail -1) and sel_cnt [tokens, H_kv] (see bsa.h)."""
+    import torch
+    _dtype(k_mean, "k_mean", torch.bfloat16)
+    if k_mean.dim() != 3 or q.dim() != 3:
+        raise ValueError("select_paged: q [tokens, H, D], k_mean [pages, H_kv, D]")
+    n_pages, H_kv, D = k_mean.shape
+    tokens, H = q.shape[0], q.shape[1]
+    qs = _token_rows(q, "q", tokens, H, D)
+    _dtype(sel, "sel", torch.int32)
+    if sel.dim() != 3 or sel.shape[0] < tokens or sel.shape[1] != H_kv:
+        raise ValueError(f"sel: shape {tuple(sel.shape)}, expected [>= {tokens}, {H_kv}, width]")
+    _flat(sel_cnt, "sel_cnt", tokens * H_kv, torch.int32)
+    _same_device(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, workspace)
+    lib = load_library()
+    b = _paged_batch(page_table, q_start, kv_len, tokens, int(page_size), n_pages)
+    need = lib.bsa_select_paged_workspace_size(ctypes.byref(b), H, H_kv, D)
+    keep, ws, nbytes = _scratch(need, workspace, q.device) if need or workspace is not None else (None, None, 0)
+    code = lib.bsa_select_paged(
+        ctypes.byref(b), _strided_ptr(q), qs, _ptr(k_mean), H, H_kv, D, int(topk), int(sink_blocks),
+        int(local_blocks), ws, nbytes, _ptr(sel), _ptr(sel_cnt), sel.shape[2], _stream(stream))
+    _check("bsa_select_paged", code)
+
+
 def device_status(stream=None) -> int:
     """Read and clear the device status word (synchronises the stream)."""
     out = ctypes.c_int32(0)
@@ -657,7 +841,8 @@ __all__ = ["BLOCK", "BsaError", "IDX_MASK_U8", "IDX_THRESHOLD_F32", "IDX_TOPK_F3
            "effective_flops", "dense_attention_flops", "load_library", "lib_path", "EXPORTS",
            "block_scores", "SCORE_MEAN_DOT", "SCORE_CENTROID_EXP", "build_crm", "forward_crm",
            "upscale_threshold", "gather_rows", "forward_masked", "forward_packed", "forward_gather0", "forward_scatter", "gather0_sizes",
-           "gather0_layout",
+           "gather0_layout", "paged_append", "forward_paged", "forward_paged_workspace_size", "select_paged",
+           "select_paged_workspace_size",
            "spectral_order", "spectral_order_workspace_size", "spectral_order_noalloc",
            "NOALLOC_SCRATCH_BYTES", "reorder_guard", "set_forward_options",
            "selftest_exp2", "selftest_wait_timeout"]

@@ -20,8 +20,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbsa.so")
 SOURCES = ["bsa_api.cu", "bsa_index.cu", "bsa_scores.cu", "bsa_order.cu", "bsa_attn.cu",
            "bsa_selftest.cu",
-           "bsa_noalloc.cu", "bsa_gather.cu"]
-HEADERS = ["bsa_internal.h", "bsa_ptx.cuh", "bsa_math.cuh", "bsa_gather0.cuh"]
+           "bsa_noalloc.cu", "bsa_gather.cu", "bsa_paged.cu", "bsa_paged_select.cu",
+           "bsa_paged_attn.cu"]
+HEADERS = ["bsa_internal.h", "bsa_ptx.cuh", "bsa_math.cuh", "bsa_gather0.cuh", "bsa_rows.cuh", "bsa_tma_host.h",
+           "bsa_paged.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -469,6 +469,200 @@ bsa_status bsa_gather_rows(const void* src, const int32_t* map, int64_t heads, i
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
+namespace {
+
+// Sizes every paged entry point accepts (the arrays behind b are not looked at).
+bsa_status paged_sizes(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D) {
+    if (!b) return BSA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
+    if (b->page_size != 16 && b->page_size != 32 && b->page_size != 64 && b->page_size != 128)
+        return BSA_ERR_UNSUPPORTED;
+    if (H_kv < 1 || H < H_kv || H % H_kv != 0 || H / H_kv > 128 || H > 65535) return BSA_ERR_INVALID_ARG;
+    if (b->seqs < 0 || b->seqs > 32768 || b->tokens < 0 || b->tokens > (1 << 24) ||
+        (int64_t)b->tokens * H >= ((int64_t)1 << 31))
+        return BSA_ERR_INVALID_ARG;
+    if (b->max_pages < 1 || (int64_t)b->max_pages * b->page_size > (1 << 24)) return BSA_ERR_INVALID_ARG;
+    if (b->n_pages < 1 || (int64_t)b->n_pages * H_kv * b->page_size >= ((int64_t)1 << 31)) return BSA_ERR_INVALID_ARG;
+    // query tiles of all key/value heads are counted in 32 bits
+    const int64_t tiles = b->tokens / (128 / (H / H_kv)) + (int64_t)b->seqs;
+    if (tiles * H_kv >= ((int64_t)1 << 31)) return BSA_ERR_INVALID_ARG;
+    return BSA_OK;
+}
+bool paged_arrays(const bsa_paged_batch* b) {
+    return b->page_table && b->q_start && b->kv_len && aligned(b->page_table, 4) && aligned(b->q_start, 4) &&
+           aligned(b->kv_len, 4);
+}
+bool token_rows(const void* p, int64_t stride, int32_t heads, int32_t D) {
+    return p && aligned(p, 16) && stride >= (int64_t)heads * D && stride % 8 == 0 && stride < ((int64_t)1 << 36);
+}
+
+bsa::PagedForwardArgs paged_forward_args(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
+                                         int32_t sel_width) {
+    bsa::PagedForwardArgs a{};
+    a.n_pages = b->n_pages;
+    a.page = b->page_size;
+    a.H = H;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.table = b->page_table;
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.seqs = b->seqs;
+    a.tokens = b->tokens;
+    a.max_pages = b->max_pages;
+    a.sel_width = sel_width;
+    return a;
+}
+bsa::PagedSelectArgs paged_select_args(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D) {
+    bsa::PagedSelectArgs a{};
+    a.n_pages = b->n_pages;
+    a.page = b->page_size;
+    a.H = H;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.table = b->page_table;
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.seqs = b->seqs;
+    a.tokens = b->tokens;
+    a.max_pages = b->max_pages;
+    return a;
+}
+
+}  // namespace
+
+bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, int32_t H, int32_t H_kv,
+                            int32_t D, const float* rope, int32_t rope_len, int32_t rot,
+                            int32_t interleaved, const void* q_norm, const void* k_norm, float eps,
+                            void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                            void* k_mean, void* stream) {
+    const bsa_status c = paged_sizes(b, H, H_kv, D);
+    if (c != BSA_OK) return c;
+    if (rope && (rope_len < 1 || rot < 16 || rot > D || rot % 16 != 0 || !aligned(rope, 16))) return BSA_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return BSA_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !scale_ok(eps)) return BSA_ERR_INVALID_ARG;
+    if ((q_norm && !aligned(q_norm, 16)) || (k_norm && !aligned(k_norm, 16))) return BSA_ERR_INVALID_ARG;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!paged_arrays(b) || !token_rows(k, k_stride, H_kv, D) || !token_rows(v, v_stride, H_kv, D))
+        return BSA_ERR_INVALID_ARG;
+    if (q && (!token_rows(q, q_stride, H, D) || !token_rows(q_out, q_out_stride, H, D))) return BSA_ERR_INVALID_ARG;
+    if (q && q == q_out && q_stride != q_out_stride) return BSA_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16) || (k_mean && !aligned(k_mean, 16)))
+        return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    bsa::PagedAppendArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.qo_stride = q_out_stride;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_mean = k_mean;
+    a.n_pages = b->n_pages;
+    a.page = b->page_size;
+    a.H = H;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.table = b->page_table;
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.seqs = b->seqs;
+    a.tokens = b->tokens;
+    a.max_pages = b->max_pages;
+    a.rope = rope;
+    a.rope_len = rope_len;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.q_norm = q ? q_norm : nullptr;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    return bsa::launch_paged_append(a, status, static_cast<cudaStream_t>(stream));
+}
+
+size_t bsa_forward_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
+                                        int32_t sel_width) {
+    if (paged_sizes(b, H, H_kv, D) != BSA_OK || sel_width < 0) return 0;
+    return bsa::paged_forward_workspace(paged_forward_args(b, H, H_kv, D, sel_width));
+}
+
+bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                             const void* k_cache, const void* v_cache, int32_t H, int32_t H_kv,
+                             int32_t D, int32_t causal, int32_t window, int32_t sinks,
+                             const int32_t* sel, const int32_t* sel_cnt, int32_t sel_width,
+                             float scale, void* workspace, size_t workspace_bytes, void* o,
+                             float* lse, void* stream) {
+    const bsa_status c = paged_sizes(b, H, H_kv, D);
+    if (c != BSA_OK) return c;
+    if ((causal != 0 && causal != 1) || window < 0 || sinks < 0 || !scale_ok(scale)) return BSA_ERR_INVALID_ARG;
+    if (sel ? (!sel_cnt || sel_width < 1 || window > 0 || !aligned(sel, 4) || !aligned(sel_cnt, 4)) : sel_width != 0)
+        return BSA_ERR_INVALID_ARG;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!paged_arrays(b) || !token_rows(q, q_stride, H, D)) return BSA_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !o || !lse || !workspace) return BSA_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+        return BSA_ERR_INVALID_ARG;
+    bsa::PagedForwardArgs a = paged_forward_args(b, H, H_kv, D, sel_width);
+    if (workspace_bytes < bsa::paged_forward_workspace(a)) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.causal = causal;
+    a.window = window;
+    a.sinks = sinks;
+    a.sel = sel;
+    a.sel_cnt = sel_cnt;
+    a.scale = scale;
+    a.o = o;
+    a.lse = lse;
+    return bsa::launch_paged_forward(a, workspace, status, static_cast<cudaStream_t>(stream));
+}
+
+size_t bsa_select_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D) {
+    if (paged_sizes(b, H, H_kv, D) != BSA_OK) return 0;
+    return bsa::paged_select_workspace(paged_select_args(b, H, H_kv, D));
+}
+
+bsa_status bsa_select_paged(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                            const void* k_mean, int32_t H, int32_t H_kv, int32_t D, int32_t topk,
+                            int32_t sink_blocks, int32_t local_blocks, void* workspace,
+                            size_t workspace_bytes, int32_t* sel, int32_t* sel_cnt, int32_t width,
+                            void* stream) {
+    const bsa_status c = paged_sizes(b, H, H_kv, D);
+    if (c != BSA_OK) return c;
+    if ((int64_t)b->max_pages * b->page_size > (int64_t)bsa::kMaxSelectBlocks * bsa::kBlock) return BSA_ERR_UNSUPPORTED;
+    if (topk < 0 || sink_blocks < 0 || local_blocks < 1 || width < 1 ||
+        (int64_t)topk + sink_blocks + local_blocks > width)
+        return BSA_ERR_INVALID_ARG;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!paged_arrays(b) || !token_rows(q, q_stride, H, D)) return BSA_ERR_INVALID_ARG;
+    if (!k_mean || !sel || !sel_cnt || !aligned(k_mean, 16) || !aligned(sel, 4) || !aligned(sel_cnt, 4))
+        return BSA_ERR_INVALID_ARG;
+    bsa::PagedSelectArgs a = paged_select_args(b, H, H_kv, D);
+    const size_t need = bsa::paged_select_workspace(a);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k_mean = k_mean;
+    a.topk = topk;
+    a.sink_blocks = sink_blocks;
+    a.local_blocks = local_blocks;
+    a.sel = sel;
+    a.sel_cnt = sel_cnt;
+    a.width = width;
+    return bsa::launch_paged_select(a, workspace, status, static_cast<cudaStream_t>(stream));
+}
+
 bsa_status bsa_set_forward_options(const bsa_forward_options* o) {
     if (o == nullptr) {
         bsa::forward_options() = bsa_forward_options{BSA_SCHEDULE_AUTO, 0};

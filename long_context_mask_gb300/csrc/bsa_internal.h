@@ -107,4 +107,59 @@ bsa_status launch_forward(const ForwardArgs& a, int32_t* status, cudaStream_t st
 bsa_forward_options& forward_options();
 int32_t forward_resident_ctas(int32_t D);
 
+// Paged key/value cache (sizes and pointers as bsa.h names them).
+struct PagedAppendArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, qo_stride;  // elements between tokens
+    void* q_out;
+    void *k_cache, *v_cache, *k_mean;
+    int32_t n_pages, page, H, H_kv, D;
+    const int32_t *table, *q_start, *kv_len;
+    int32_t seqs, tokens, max_pages;
+    const float* rope;
+    int32_t rope_len, rot, interleaved;
+    const void *q_norm, *k_norm;
+    float eps;
+};
+// bsa_paged.cu
+bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaStream_t stream);
+
+struct PagedForwardArgs {
+    const void* q;
+    int64_t q_stride;
+    const void *k_cache, *v_cache;
+    int32_t n_pages, page, H, H_kv, D;
+    const int32_t *table, *q_start, *kv_len;
+    int32_t seqs, tokens, max_pages;
+    int32_t causal, window, sinks;
+    const int32_t *sel, *sel_cnt;
+    int32_t sel_width;  // 0: no lists
+    float scale;
+    void* o;
+    float* lse;
+};
+// Thread blocks of the paged forward (its workspace holds two parts for each):
+// the 152 SMs of a GB300, one block each.
+constexpr int kPagedBlocks = 152;
+// bsa_paged_attn.cu
+size_t paged_forward_workspace(const PagedForwardArgs& a);
+bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int32_t* status, cudaStream_t stream);
+
+struct PagedSelectArgs {
+    const void* q;
+    int64_t q_stride;
+    const void* k_mean;
+    int32_t n_pages, page, H, H_kv, D;
+    const int32_t *table, *q_start, *kv_len;
+    int32_t seqs, tokens, max_pages;
+    int32_t topk, sink_blocks, local_blocks;
+    int32_t *sel, *sel_cnt;
+    int32_t width;
+};
+// Blocks of a sequence that bsa_paged_select can rank (2^20 tokens).
+constexpr int32_t kMaxSelectBlocks = 8192;
+// bsa_paged_select.cu
+size_t paged_select_workspace(const PagedSelectArgs& a);
+bsa_status launch_paged_select(const PagedSelectArgs& a, void* workspace, int32_t* status, cudaStream_t stream);
+
 }  // namespace bsa

@@ -1,0 +1,97 @@
+// The ragged batch over a paged key/value cache, as the paged kernels read it.
+//
+// Sequence s owns the new tokens q_start[s] .. q_start[s + 1] - 1 of the
+// packed token axis; kv_len[s] tokens of it are in the cache, the new ones
+// last, so new token i stands at position kv_len[s] - (number of new tokens)
+// + i.  Position p lives in slot p % page of page table[s][p / page].  All of
+// this is device data: the host knows only the capacities, so kernels are
+// launched for the largest count and find their own work.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bsa_internal.h"
+
+namespace bsa {
+
+struct PagedBatch {
+    const int32_t* q_start;  // [seqs + 1]
+    const int32_t* kv_len;   // [seqs]
+    const int32_t* table;    // [seqs, max_pages]
+    int32_t seqs, tokens, max_pages;
+    int32_t page, n_pages;   // tokens per page (16, 32, 64 or 128); pages of the cache
+    int32_t* status;
+};
+
+struct PagedSeq {
+    int32_t q0, nq, kl;  // first new token, new tokens (0: none, or a bad entry), tokens in the cache
+};
+
+// false (and no new tokens) where the entry makes no sense: a negative or
+// decreasing start, tokens beyond the packed axis, a length that is negative
+// or beyond the table's row.
+__device__ __forceinline__ bool paged_seq(const PagedBatch& b, int32_t s, PagedSeq& out) {
+    const int32_t a = b.q_start[s], e = b.q_start[s + 1], kl = b.kv_len[s];
+    const bool ok = a >= 0 && e >= a && e <= b.tokens && kl >= 0 && (int64_t)kl <= (int64_t)b.max_pages * b.page;
+    out.q0 = a;
+    out.nq = ok ? e - a : 0;
+    out.kl = ok ? kl : 0;
+    return ok;
+}
+
+// Exclusive prefix sum over the thread block (a multiple of 32 threads, at
+// most 1024); total receives the block's sum.  part: 33 words of shared memory.
+__device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* part, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int64_t incl = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    __syncthreads();  // an earlier call's readers are done with part
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+        const int64_t v = part[w];
+        before += w < warp ? v : 0;
+        all += v;
+    }
+    total = all;
+    return before + incl - x;
+}
+
+// Unit u of the batch, where sequence s counts count(seq) units: the sequence
+// (-1: u is beyond the last) and the unit within it.  Called by the whole
+// thread block; the same answer in every thread.  shared: see block_prefix,
+// and hit: 2 words.
+template <typename Count>
+__device__ __forceinline__ int32_t find_unit(const PagedBatch& b, int64_t u, Count&& count, int64_t* part, int32_t* hit,
+                                             int32_t& within) {
+    if (threadIdx.x == 0) hit[0] = -1;
+    int64_t base = 0;
+    for (int32_t s0 = 0; s0 < b.seqs; s0 += blockDim.x) {
+        const int32_t s = s0 + threadIdx.x;
+        PagedSeq q{0, 0, 0};
+        int64_t n = 0;
+        if (s < b.seqs) {
+            paged_seq(b, s, q);
+            n = count(q);
+        }
+        int64_t total;
+        const int64_t at = base + block_prefix(n, part, total);
+        if (n > 0 && u >= at && u < at + n) {
+            hit[0] = s;
+            hit[1] = (int32_t)(u - at);
+        }
+        base += total;
+        if (u < base) break;
+    }
+    __syncthreads();
+    within = hit[1];
+    return hit[0];
+}
+
+}  // namespace bsa

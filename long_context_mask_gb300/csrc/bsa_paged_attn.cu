@@ -1,0 +1,1035 @@
+// Attention of new tokens over a paged key/value cache for sm_103a
+// (tcgen05 + TMEM + TMA).
+//
+// What it computes.  For token i of sequence s at position p, query head h
+// and the keys j < kv_len[s] that the mask leaves (causal: j <= p; window:
+// j > p - window or j < sinks; lists: j / 128 among the token's blocks):
+//     s_j = scale q . k_j,   LSE = ln sum_j exp(s_j),   O = sum_j exp(s_j - LSE) v_j
+// in one pass over the keys with the running maximum and sum of the softmax.
+//
+// Tiles.  The G query heads that share a key/value head are rows of one
+// query tile: row r is head r % G of the tile's token r / G, 128 / G tokens
+// to a tile, so a single new token reads each key once for its G heads.  A
+// key tile is 128 positions: 128 / page pages, each one TMA box.  One tile
+// pair costs the tensor core about 0.6 us an SM and the memory about 1.5 us
+// (64 KB at a 152nd of the card's rate), so the same 128-row tile serves
+// single tokens, whose time is the cache's, and prompts, whose time is the
+// products'.
+//
+// Split.  All (key/value head, sequence, query tile, key tile) units are laid
+// out in that order and cut into equal runs, one for each of at most 152
+// thread blocks: long rows are split over many, short ones run several to a
+// block, and no host knowledge of the lengths is needed.  A row that a cut
+// splits leaves its parts (O, maximum, sum, all fp32) in the workspace;
+// k_paged_join adds them in key order, so a call's result does not depend on
+// timing.
+//
+// Warp roles (11 warps): 0 cuts the run into segments (one query tile's part
+// of the run), tells the others through a ring of descriptors and loads the
+// K/V tiles; 1 issues the MMAs; 2 .. 9 are the softmax (four threads a row,
+// see bsa_rows.cuh) and the epilogue; 10 loads the query tiles, so that K/V
+// loads of the next segment never wait for the last products on Q.
+// Shared memory: the Q tile and a ring of K/V tiles.  Tensor memory: three
+// score buffers and O, as in bsa_attn.cu, whose schedule (K_0 .. K_2, then
+// V_i, K_{i+3}) this kernel shares.
+//
+// Slots behind the end of a sequence hold anything, NaN included.  Their
+// scores are dropped by a select, and the value rows behind the end are
+// zeroed in shared memory before the product (0 times NaN is NaN).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "bsa_internal.h"
+#include "bsa_paged.cuh"
+#include "bsa_rows.cuh"
+#include "bsa_tma_host.h"
+
+namespace bsa {
+namespace {
+
+constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s per wait
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;                          // rescale O when a maximum grows by > 2^8
+constexpr float kSumLimit = 18446744073709551616.0f;      // 2^64, see softmax_rows
+constexpr int kSBuf = 3;                                  // TMEM score buffers
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 384;
+constexpr int kProducer = 0, kMma = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kQLoad = 10;
+constexpr int kThreads = 32 * 11;
+constexpr int kDesc = 4;                                  // segment descriptors in flight
+constexpr int kConsumers = kSoftmaxWarps + 2;             // warps that read a descriptor
+constexpr int kBox = 128 * 128;                           // 128 rows of 64 bf16
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = kBox * kHalves;
+    static constexpr int kStages = D == 128 ? 6 : 12;
+    static constexpr int kData = kTile * (1 + kStages);
+    static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+};
+
+// One query tile's part of the run, as the producer tells it.
+struct Segment {
+    int32_t n;          // key tiles (0: none, the rows are empty; -1: no more segments)
+    int32_t seq;
+    int32_t q0, ntok;   // first token (packed axis) and tokens of the query tile
+    int32_t kvh;
+    int32_t pos0, kl;   // position of the first token, keys in the cache
+    int32_t j0;         // first of the tile's key tiles in this segment
+    int32_t lo, ns;     // key tile of number j: j < ns ? j : lo + j - ns (without lists)
+    int32_t list;       // with lists: row of the tile lists
+    int32_t slot;       // -1: the whole row is here; else the block's part slot (0 or 1)
+};
+
+struct Shared {
+    uint64_t full[16];
+    uint64_t empty[16];
+    uint64_t q_full, q_empty;
+    uint64_t p_full[kSBuf];
+    uint64_t o_free;
+    uint64_t mma_done;
+    uint64_t seg_full[kDesc], seg_empty[kDesc];
+    Segment seg[kDesc];
+    int64_t part[33];
+    int32_t start[5];  // first unit: key/value head, sequence, query tile, key tile; tile within the head
+    uint32_t tmem_base;
+    int32_t abort;
+};
+
+struct Params {
+    CUtensorMap map_q, map_q1;  // (D, H, tokens): box 64 x G x (128 / G), 64 x G x 1
+    CUtensorMap map_k, map_v;   // (64, slots, D / 64): box 64 x page x boxed halves
+    PagedBatch b;
+    int32_t H, H_kv, group, tpt;  // tpt: tokens of a query tile
+    int32_t causal, window, sinks;
+    float scale_log2;
+    __nv_bfloat16* o;
+    float* lse;
+    // lists (null: every visible key tile): tile f = kvh * nt_cap + i
+    const int32_t* list;      // [H_kv * nt_cap, cap] key tiles, ascending
+    const int32_t* list_cnt;  // [H_kv * nt_cap]
+    const uint32_t* list_who; // [H_kv * nt_cap, cap, words] bit t: token t of the query tile sees the key tile
+    int32_t nt_cap, cap, words;
+    // workspace of split rows
+    float* part_o;            // [blocks, 2, 128, D]
+    float2* part_ml;          // [blocks, 2, 128] maximum (log2) and sum
+    int4* joins;              // [blocks] parts (0: none), q0, ntok, kvh
+};
+
+__device__ __forceinline__ bool aborted(const Shared* sh) {
+    return *reinterpret_cast<const volatile int32_t*>(&sh->abort) != 0;
+}
+__device__ __forceinline__ void set_abort(Shared* sh, int32_t* status) {
+    *reinterpret_cast<volatile int32_t*>(&sh->abort) = 1;
+    raise_status(status, BSA_ERR_TIMEOUT);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int32_t* status) {
+    return mbar_wait(bar, parity, kWaitNs, status, BSA_ERR_TIMEOUT);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* status) {
+    return __all_sync(0xffffffffu, wait(bar, parity, status));
+}
+
+// Key tiles that the tokens at positions pos0 .. pos0 + ntok - 1 see some key
+// of: the sink tiles 0 .. ns - 1 and lo .. lo + (n - ns) - 1.
+__device__ __forceinline__ int32_t key_tiles(const Params& P, int32_t pos0, int32_t ntok, int32_t kl, int32_t& lo,
+                                             int32_t& ns) {
+    const int32_t hi = P.causal ? min(kl, pos0 + ntok) : kl;  // keys 0 .. hi - 1
+    lo = ns = 0;
+    if (hi <= 0) return 0;
+    const int32_t hi_t = (hi + 127) >> 7;
+    if (P.window > 0) {
+        lo = min(max(pos0 - P.window + 1, 0) >> 7, hi_t);
+        ns = min((min(P.sinks, hi) + 127) >> 7, lo);
+    }
+    return hi_t - lo + ns;
+}
+
+// Positions in the K/V load order K_0, K_1, K_2, then V_i, K_{i+3} (see bsa_attn.cu).
+__device__ __forceinline__ uint32_t ring_pos_k(int32_t j) { return (uint32_t)(j < kSBuf ? j : 2 * j - 2); }
+__device__ __forceinline__ uint32_t ring_pos_v(int32_t i, int32_t n) {
+    const int32_t lead = min(n, kSBuf);
+    return (uint32_t)(lead + i + max(min(i, n - kSBuf), 0));
+}
+
+// One key tile of the online softmax for this thread's shares of rows a and b.
+// dead: the row holds no token (its scores are anything; m = 0, and it takes
+// part in no decision).  A live row that has seen no key yet has m = -inf.
+// As long as no row is in that state the exponentials are taken against the
+// running maxima without computing the tile's own; only a tile whose sums
+// leave 2^64 (or are NaN) is redone with its maxima.  Returns true
+// (warp-uniform) when O must be multiplied by alpha first.
+template <typename Reload>
+__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], float sl2, float (&m)[2],
+                                             float (&l)[2], float (&alpha)[2], Reload&& reload) {
+    alpha[0] = alpha[1] = 1.0f;
+    float la, lb;
+    if (!__any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY)) {
+        exp_rows<0>(s, sl2, -m[0], -m[1], la, lb);
+        if (!__any_sync(0xffffffffu, (!dead[0] && !(la <= kSumLimit)) || (!dead[1] && !(lb <= kSumLimit)))) {
+            l[0] += la;
+            l[1] += lb;
+            return false;
+        }
+        reload();
+    }
+    float mt[2];
+    max_rows(s, mt[0], mt[1]);
+    mt[0] *= sl2;
+    mt[1] *= sl2;
+    const bool rescale = __any_sync(0xffffffffu, (!dead[0] && m[0] != -INFINITY && mt[0] > m[0] + kRescale) ||
+                                                     (!dead[1] && m[1] != -INFINITY && mt[1] > m[1] + kRescale));
+    float bias[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (!dead[i]) {
+            if (m[i] == -INFINITY) {
+                m[i] = mt[i];  // O and l of the row are still 0
+            } else if (rescale) {
+                const float m_new = fmaxf(m[i], mt[i]);
+                alpha[i] = ex2(m[i] - m_new);
+                l[i] *= alpha[i];
+                m[i] = m_new;
+            }
+        }
+        bias[i] = m[i] == -INFINITY ? 0.0f : -m[i];  // (no key yet: every exponential is 0)
+    }
+    exp_rows<0>(s, sl2, bias[0], bias[1], la, lb);
+    l[0] += la;
+    l[1] += lb;
+    return rescale;
+}
+
+template <int D, bool kLists>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_constant__ Params P) {
+    using C = Cfg<D>;
+    constexpr uint32_t S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_q = smem_u32(smem);
+    const uint32_t s_ring = s_q + C::kTile;
+    Shared* sh = reinterpret_cast<Shared*>(smem + C::kData);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    int32_t* const status = P.b.status;
+
+    // ---------------------------------------------------------------- this block's run
+    // cum[s]: query tiles of the sequences before s (the data area is free here)
+    int32_t* cum = reinterpret_cast<int32_t*>(smem);
+    int64_t nt = 0;  // query tiles of one key/value head
+    {
+        const int32_t per = (P.b.seqs + kThreads - 1) / kThreads;
+        const int32_t a = min((int32_t)threadIdx.x * per, P.b.seqs), e = min(a + per, P.b.seqs);
+        int64_t mine = 0;
+        for (int32_t s = a; s < e; ++s) {
+            PagedSeq q;
+            if (!paged_seq(P.b, s, q) && blockIdx.x == 0) raise_status(status, BSA_ERR_BOUNDS);
+            mine += (q.nq + P.tpt - 1) / P.tpt;
+        }
+        int64_t at = block_prefix(mine, sh->part, nt);
+        for (int32_t s = a; s < e; ++s) {
+            PagedSeq q;
+            paged_seq(P.b, s, q);
+            cum[s] = (int32_t)min(at, (int64_t)P.nt_cap);
+            at += (q.nq + P.tpt - 1) / P.tpt;
+        }
+        nt = min(nt, (int64_t)P.nt_cap);  // (beyond: only with starts that decrease, reported above)
+    }
+    __syncthreads();
+    const int64_t rows = kLists ? nt * P.H_kv : nt;  // tiles whose counts differ
+    const int64_t per_row = (rows + kThreads - 1) / kThreads;
+    const int64_t f0 = min((int64_t)threadIdx.x * per_row, rows), f1 = min(f0 + per_row, rows);
+    // walks this thread's tiles: visit(kvh, i, s, t, units), tile i of the head being query tile t of sequence s
+    auto walk = [&](auto&& visit) {
+        int64_t f = f0;
+        if (f >= f1) return;
+        int32_t i = (int32_t)(f % nt), kvh = (int32_t)(f / nt);
+        int32_t s = 0;
+        auto find = [&]() {
+            int32_t lo = 0, hi = P.b.seqs;  // the last s with cum[s] <= i
+            while (hi - lo > 1) {
+                const int32_t mid = (lo + hi) >> 1;
+                if (cum[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            s = lo;
+        };
+        find();
+        PagedSeq q;
+        paged_seq(P.b, s, q);
+        for (; f < f1; ++f) {
+            const int32_t t = i - cum[s];
+            int32_t n;
+            if constexpr (kLists) {
+                n = P.list_cnt[(int64_t)kvh * P.nt_cap + i];
+            } else {
+                int32_t lo, ns;
+                const int32_t first = t * P.tpt;
+                n = key_tiles(P, q.kl - q.nq + first, min(P.tpt, q.nq - first), q.kl, lo, ns);
+            }
+            if (visit(kvh, i, s, t, max(n, 1))) return;  // an empty row is one unit: it is written
+            ++i;
+            if (i == nt) {
+                i = 0;
+                ++kvh;
+                find();
+                paged_seq(P.b, s, q);
+            } else if (s + 1 < P.b.seqs && cum[s + 1] <= i) {
+                find();
+                paged_seq(P.b, s, q);
+            }
+        }
+    };
+    int64_t mine = 0, total;
+    walk([&](int32_t, int32_t, int32_t, int32_t, int32_t n) {
+        mine += n;
+        return false;
+    });
+    const int64_t before = block_prefix(mine, sh->part, total);
+    const int64_t units = kLists ? total : total * P.H_kv;
+    const int64_t blocks = min((int64_t)gridDim.x, units);
+    if (threadIdx.x == 0) {
+        P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);  // (the producer writes it again where a row is split)
+        // a block of this launch (or an unread earlier one) timed out: abandon
+        sh->abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
+    }
+    if ((int64_t)blockIdx.x >= blocks) return;
+    const int64_t u0 = units * blockIdx.x / blocks, u1 = units * (blockIdx.x + 1) / blocks;
+    {
+        const int64_t head = kLists ? 0 : u0 / total, r = kLists ? u0 : u0 % total;
+        if (r >= before && r < before + mine) {
+            int64_t at = before;
+            walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
+                if (r < at + n) {
+                    sh->start[0] = kLists ? kvh : (int32_t)head;
+                    sh->start[1] = s;
+                    sh->start[2] = t;
+                    sh->start[3] = (int32_t)(r - at);
+                    sh->start[4] = i;
+                    return true;
+                }
+                at += n;
+                return false;
+            });
+        }
+    }
+    __syncthreads();
+    if (sh->abort != 0) return;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&sh->full[s]), 1);
+            mbar_init(smem_u32(&sh->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh->q_full), 1);
+        mbar_init(smem_u32(&sh->q_empty), 1);
+        for (int s = 0; s < kSBuf; ++s) mbar_init(smem_u32(&sh->p_full[s]), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->o_free), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->mma_done), 1);
+        for (int d = 0; d < kDesc; ++d) {
+            mbar_init(smem_u32(&sh->seg_full[d]), 1);
+            mbar_init(smem_u32(&sh->seg_empty[d]), kConsumers);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kMma) {
+        tmem_alloc(smem_u32(&sh->tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    // cum, written by ordinary stores, makes room for TMA loads
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+
+    // The next segment, for the warps that read descriptors; false: no more.
+    auto next_segment = [&](uint32_t k, Segment& sg, bool& ok) -> bool {
+        if (!wait_warp(smem_u32(&sh->seg_full[k % kDesc]), (k / kDesc) & 1u, status)) {
+            ok = false;
+            return false;
+        }
+        sg = sh->seg[k % kDesc];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->seg_empty[k % kDesc]));
+        return sg.n >= 0;
+    };
+
+    if (warp == kProducer) {
+        // ------------------------------------------------------------ segments and K/V tiles
+        int32_t kvh = sh->start[0], s = sh->start[1], t = sh->start[2], j0 = sh->start[3];
+        int64_t left = u1 - u0, u = u0;
+        PagedSeq q;
+        paged_seq(P.b, s, q);
+        const int32_t page = P.b.page, pieces = 128 / page;
+        // a load is one page of one 64-column half, or of both where the page fills the tile
+        const int32_t boxed = page == 128 ? C::kHalves : 1, halves = C::kHalves / boxed;
+        const int32_t n_loads = pieces * halves;
+        const int32_t my_piece = lane / halves, my_half = lane % halves;
+        const uint32_t my_dst = (uint32_t)(my_half * kBox + my_piece * page * 128);
+        const uint32_t piece_bytes = (uint32_t)(page * D * 2);
+        const int32_t per_window = 32 / pieces;  // key tiles whose pages one 32-lane read brings
+        uint32_t pos = 0, issued = 0, k = 0;
+        bool ok = true;
+        int32_t i = sh->start[4];
+        while (left > 0 && ok) {
+            const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
+            Segment sg;
+            sg.seq = s;
+            sg.q0 = q.q0 + first;
+            sg.ntok = ntok;
+            sg.kvh = kvh;
+            sg.pos0 = q.kl - q.nq + first;
+            sg.kl = q.kl;
+            sg.lo = sg.ns = 0;
+            sg.list = 0;
+            int32_t n_row;
+            if constexpr (kLists) {
+                sg.list = kvh * P.nt_cap + i;
+                n_row = P.list_cnt[sg.list];
+            } else {
+                n_row = key_tiles(P, sg.pos0, ntok, q.kl, sg.lo, sg.ns);
+            }
+            const int32_t n_eff = max(n_row, 1);
+            const int32_t take = (int32_t)min((int64_t)(n_eff - j0), left);
+            sg.j0 = j0;
+            sg.n = n_row == 0 ? 0 : take;
+            sg.slot = j0 == 0 && take == n_eff ? -1 : (j0 == 0 ? 1 : 0);
+            if (lane == 0 && left == take) {
+                // the last segment: does a split row begin in this block?
+                int4 jn = make_int4(0, 0, 0, 0);
+                if (j0 == 0 && take < n_eff) {
+                    // the block that holds the row's last unit: the least c with units (c + 1) / blocks >= end
+                    const int64_t end = u + n_eff;
+                    const int64_t last = (end * blocks + units - 1) / units - 1;
+                    jn = make_int4((int32_t)(last - blockIdx.x + 1), sg.q0, ntok, kvh);
+                }
+                P.joins[blockIdx.x] = jn;
+            }
+            if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                sh->seg[k % kDesc] = sg;
+                mbar_arrive(smem_u32(&sh->seg_full[k % kDesc]));
+            }
+            __syncwarp();
+            ++k;
+            // tiles in the order K_0 .. K_2, then V_i, K_{i+3}, then the last V
+            const int32_t n = sg.n;
+            const int32_t* list = kLists ? P.list + (int64_t)sg.list * P.cap + j0 : nullptr;
+            auto tile_of = [&](int32_t j) -> int32_t {
+                if constexpr (kLists) return list[j];
+                const int32_t x = j0 + j;
+                return x < sg.ns ? x : sg.lo + x - sg.ns;
+            };
+            const int32_t* table = P.b.table + (int64_t)s * P.b.max_pages;
+            // lane l of a window: the slot row of piece l % pieces of key tile w0 + l / pieces
+            // (-1: behind the sequence's end)
+            auto fetch = [&](int32_t w0) -> int32_t {
+                const int32_t j = w0 + lane / pieces, pc = lane % pieces;
+                if (j >= n) return -1;
+                const int32_t pg = tile_of(j) * pieces + pc;
+                if (pg * page >= q.kl) return -1;
+                int32_t id = table[pg];
+                if (id < 0 || id >= P.b.n_pages) {
+                    raise_status(status, BSA_ERR_BOUNDS);
+                    id = 0;  // keeps the pipeline in step; this row's result is unspecified
+                }
+                return (id * P.H_kv + kvh) * page;
+            };
+            int32_t w0 = 0, cur = fetch(0), nxt = fetch(per_window);
+            int32_t r0 = -1, r1 = -1, r2 = -1;  // this lane's slot rows of the last three K tiles
+            const int32_t lead = min(n, kSBuf), inter = 2 * (n - lead);
+            for (int32_t x = 0; x < 2 * n; ++x) {
+                const bool is_v = x >= lead && (x - lead >= inter || ((x - lead) & 1) == 0);
+                int32_t row;
+                if (!is_v) {
+                    const int32_t j = x < lead ? x : ((x - lead) >> 1) + kSBuf;
+                    if (j >= w0 + per_window) {
+                        w0 += per_window;
+                        cur = nxt;
+                        nxt = fetch(w0 + per_window);
+                    }
+                    row = __shfl_sync(0xffffffffu, cur, (j - w0) * pieces + my_piece);
+                    r0 = r1;
+                    r1 = r2;
+                    r2 = row;
+                } else {
+                    const int32_t v = x - lead < inter ? (x - lead) >> 1 : (n - lead) + (x - lead - inter);
+                    // V_v follows the load of K_{min(v + 2, n - 1)}
+                    const int32_t back = min(v + kSBuf - 1, n - 1) - v;
+                    row = back == 2 ? r0 : (back == 1 ? r1 : r2);
+                }
+                const uint32_t slot = pos % S;
+                if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, status) || aborted(sh)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = smem_u32(&sh->full[slot]);
+                const bool go = lane < n_loads && row >= 0;
+                const uint32_t mask = __ballot_sync(0xffffffffu, go);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(fb, (uint32_t)(__popc(mask) / halves) * piece_bytes);
+                __syncwarp();
+                if (go)
+                    tma_load_3d(s_ring + slot * C::kTile + my_dst, is_v ? &P.map_v : &P.map_k, 0, row, my_half, fb);
+                __syncwarp();
+                ++pos;
+                issued = pos;
+            }
+            // on to the next query tile
+            left -= take;
+            u += take;
+            j0 = 0;
+            if (left > 0) {
+                ++t;
+                if (++i == (int32_t)nt) {  // the next head
+                    i = t = s = 0;
+                    ++kvh;
+                    paged_seq(P.b, 0, q);
+                }
+                while (t * P.tpt >= q.nq && s + 1 < P.b.seqs) {
+                    t = 0;
+                    paged_seq(P.b, ++s, q);
+                }
+            }
+        }
+        if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
+            if (lane == 0) {
+                sh->seg[k % kDesc].n = -1;
+                mbar_arrive(smem_u32(&sh->seg_full[k % kDesc]));
+            }
+        } else {
+            ok = false;
+        }
+        if (!ok && lane == 0) set_abort(sh, status);
+        // every issued copy must land before the block exits
+        if (lane == 0) {
+            for (uint32_t x = issued > S ? issued - S : 0; x < issued; ++x)
+                if (!wait(smem_u32(&sh->full[x % S]), (x / S) & 1u, status)) raise_status(status, BSA_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == kQLoad) {
+        // ------------------------------------------------------------ query tiles
+        uint32_t nq = 0;
+        bool ok = true;
+        Segment sg;
+        for (uint32_t k = 0; next_segment(k, sg, ok); ++k) {
+            if (sg.n == 0) continue;
+            if (nq > 0 && !wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, status)) {
+                ok = false;
+                break;
+            }
+            if (aborted(sh)) break;
+            if (lane == 0) {
+                const bool one = sg.ntok == 1;
+                const uint32_t bar = smem_u32(&sh->q_full);
+                mbar_arrive_expect_tx(bar, (uint32_t)((one ? 1 : P.tpt) * P.group * D * 2));
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, sg.kvh * P.group, sg.q0, bar);
+            }
+            __syncwarp();
+            ++nq;
+        }
+        if (!ok && lane == 0) set_abort(sh, status);
+        if (lane == 0 && nq > 0 && !wait(smem_u32(&sh->q_full), (nq - 1u) & 1u, status))
+            raise_status(status, BSA_ERR_TIMEOUT);
+        __syncwarp();
+    } else if (warp == kMma) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint64_t dq = smem_desc_sw128(s_q, 16, 1024);
+        const uint64_t dk = smem_desc_sw128(s_ring, 16, 1024);
+        const uint64_t dv = smem_desc_sw128(s_ring, kBox, 1024);
+        uint32_t pos = 0, gb0 = 0, nq = 0;
+        bool ok = true;
+        Segment sg;
+        for (uint32_t k = 0; ok && next_segment(k, sg, ok); ++k) {
+            const int32_t n = sg.n;
+            if (n == 0) continue;
+            // the segment's last tile may hold the sequence's end: rows behind it are zeroed
+            int32_t last_kt;
+            if constexpr (kLists) last_kt = P.list[(int64_t)sg.list * P.cap + sg.j0 + n - 1];
+            else last_kt = sg.j0 + n - 1 < sg.ns ? sg.j0 + n - 1 : sg.lo + sg.j0 + n - 1 - sg.ns;
+            const int32_t tail = min(sg.kl - last_kt * 128, 128);
+            ok = wait_warp(smem_u32(&sh->q_full), nq & 1u, status);
+            if (!ok) break;
+            tc_fence_after();
+            auto issue_qk = [&](int32_t j) -> bool {
+                const uint32_t slot = pos % S;
+                if (!wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status)) return false;
+                tc_fence_after();
+                const uint64_t ks = dk + (uint64_t)((slot * C::kTile) >> 4);
+                const uint32_t d_col = ((gb0 + (uint32_t)j) % kSBuf) * 128u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+                        mma_ss(tmem + d_col, dq + off, ks + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(smem_u32(&sh->empty[slot]));  // also signals S_j to the softmax
+                    if (j == n - 1) mma_commit(smem_u32(&sh->q_empty));
+                }
+                __syncwarp();
+                ++pos;
+                return true;
+            };
+            for (int32_t j = 0; ok && j < n && j < kSBuf; ++j) ok = issue_qk(j);
+            for (int32_t i = 0; ok && i < n; ++i) {
+                const uint32_t gb = gb0 + (uint32_t)i;
+                ok = wait_warp(smem_u32(&sh->p_full[gb % kSBuf]), (gb / kSBuf) & 1u, status);
+                // the first PV of a segment overwrites O: the previous epilogue must have read it
+                if (ok && i == 0 && nq > 0) ok = wait_warp(smem_u32(&sh->o_free), (nq - 1u) & 1u, status);
+                if (!ok) break;
+                const uint32_t slot = pos % S;
+                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
+                if (!ok) break;
+                if (i == n - 1 && tail < 128) {
+                    // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
+                    const uint32_t tile = s_ring + slot * C::kTile;
+                    for (int32_t x = tail * 8 + lane; x < 128 * 8; x += 32)
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + h * kBox + x * 16), "r"(0)
+                                         : "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
+                const uint32_t p_col = (gb % kSBuf) * 128u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + kColO, tmem + p_col + kk * 8, vs + (uint64_t)(kk * 2048 >> 4), C::kIdescPV,
+                               (i > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(smem_u32(&sh->empty[slot]));  // also signals PV_i to the softmax
+                }
+                __syncwarp();
+                ++pos;
+                if (i + kSBuf < n) ok = issue_qk(i + kSBuf);
+            }
+            gb0 += (uint32_t)n;
+            ++nq;
+        }
+        if (!ok && lane == 0) set_abort(sh, status);
+        // nothing of ours may still be running when TMEM is freed
+        if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
+        __syncwarp();
+        if (!wait(smem_u32(&sh->mma_done), 0, status) && lane == 0) raise_status(status, BSA_ERR_TIMEOUT);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax and epilogue
+        const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
+        const int half = (warp - kSoftmax0) >> 2;
+        const int row[2] = {qd * 32 + half * 16 + (lane >> 2), qd * 32 + half * 16 + (lane >> 2) + 8};
+        const int tok[2] = {row[0] / P.group, row[1] / P.group};
+        const int head[2] = {row[0] % P.group, row[1] % P.group};
+        const uint32_t t_base = tmem + ((uint32_t)(qd * 32 + half * 16) << 16);
+        const int c0 = 2 * (lane & 3);  // this thread's columns: c0 + 8 k, c0 + 8 k + 1
+        const float sl2 = P.scale_log2;
+        uint32_t pos0 = 0, gb0 = 0;
+        bool ok = true;
+        Segment sg;
+        for (uint32_t k = 0; next_segment(k, sg, ok); ++k) {
+            const int32_t n = sg.n;
+            bool dead[2];
+            __nv_bfloat16* orow[2];
+            float* lrow[2];
+            int32_t hi[2], lo[2], sk[2];  // keys lo .. hi - 1 and 0 .. sk - 1
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                dead[x] = tok[x] >= sg.ntok;
+                const int64_t at = (int64_t)(sg.q0 + tok[x]) * P.H + sg.kvh * P.group + head[x];
+                orow[x] = dead[x] ? nullptr : P.o + at * D;
+                lrow[x] = P.lse + at;
+                const int32_t p = sg.pos0 + tok[x];
+                hi[x] = P.causal ? min(sg.kl, p + 1) : sg.kl;
+                lo[x] = P.window > 0 ? p - P.window + 1 : 0;
+                sk[x] = P.window > 0 ? min(P.sinks, hi[x]) : 0;
+            }
+            if (n == 0) {
+                // no key at all: O = 0, LSE = -inf
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (dead[x]) continue;
+#pragma unroll
+                    for (int kk = 0; kk < D / 8; ++kk) *reinterpret_cast<uint32_t*>(orow[x] + 8 * kk + c0) = 0u;
+                    if ((lane & 3) == 0) *lrow[x] = -INFINITY;
+                }
+                continue;
+            }
+            const int32_t* list = kLists ? P.list + (int64_t)sg.list * P.cap + sg.j0 : nullptr;
+            const uint32_t* who = kLists ? P.list_who + ((int64_t)sg.list * P.cap + sg.j0) * P.words : nullptr;
+            float m[2] = {dead[0] ? 0.0f : -INFINITY, dead[1] ? 0.0f : -INFINITY};
+            float l[2] = {0.0f, 0.0f};  // this thread's share of each row
+            int32_t kt_next = 0;
+            uint32_t who_next[2] = {0u, 0u};
+            auto look = [&](int32_t j) {
+                if constexpr (kLists) {
+                    kt_next = list[j];
+                    // (a row without a token may lie behind the last word)
+                    who_next[0] = dead[0] ? 0u : who[(int64_t)j * P.words + (tok[0] >> 5)];
+                    who_next[1] = dead[1] ? 0u : who[(int64_t)j * P.words + (tok[1] >> 5)];
+                }
+            };
+            look(0);
+            for (int32_t j = 0; j < n; ++j) {
+                const uint32_t gb = gb0 + (uint32_t)j;
+                const uint32_t sbuf = (gb % kSBuf) * 128u;
+                int32_t kt;
+                if constexpr (kLists) kt = kt_next;
+                else kt = sg.j0 + j < sg.ns ? sg.j0 + j : sg.lo + sg.j0 + j - sg.ns;
+                const int32_t kb = kt * 128;
+                int32_t h[2], w[2], z[2];  // visible columns of this tile: [w, h) and [0, z)
+                bool part = false, any = false;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    h[x] = min(hi[x] - kb, 128);
+                    w[x] = max(lo[x] - kb, 0);
+                    z[x] = min(sk[x] - kb, 128);
+                    if (kLists && !((who_next[x] >> (tok[x] & 31)) & 1u)) h[x] = z[x] = 0;
+                    part |= !dead[x] && !((h[x] == 128 && w[x] == 0) || z[x] == 128);
+                    any |= !dead[x] && (h[x] > w[x] || z[x] > 0);
+                }
+                if (kLists && j + 1 < n) look(j + 1);
+                const bool masked = __any_sync(0xffffffffu, part);
+                const bool visible = __any_sync(0xffffffffu, any);
+                const uint32_t pk = pos0 + ring_pos_k(j);
+                const bool wt = wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, status);
+                if (__any_sync(0xffffffffu, !wt || aborted(sh))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (!visible) {
+                    // no row of this warp sees a key of the tile: P = 0
+                    store_p_zero(t_base + sbuf);
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sh->p_full[gb % kSBuf]));
+                    continue;
+                }
+                uint32_t sc[64];
+                auto load_s = [&]() {
+                    tmem_ld16x256_x16(t_base + sbuf, sc);
+                    tmem_wait_ld();
+                    if (masked) {
+                        const uint32_t ninf = __float_as_uint(-INFINITY);
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int c = c0 + 8 * kk + e;
+                                    const bool see = (c < h[x] && c >= w[x]) || c < z[x];
+                                    sc[4 * kk + 2 * x + e] = see ? sc[4 * kk + 2 * x + e] : ninf;
+                                }
+                    }
+                };
+                load_s();
+                float alpha[2];
+                const bool rescale = softmax_rows(sc, dead, sl2, m, l, alpha, load_s);
+                tmem_st16x128_x16(t_base + sbuf, sc);
+                if (rescale) {
+                    // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
+                    const uint32_t pv = pos0 + ring_pos_v(j - 1, n);
+                    const bool wv = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
+                    if (__any_sync(0xffffffffu, !wv)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    scale_o_rows<D>(t_base + kColO, alpha[0], alpha[1]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh->p_full[gb % kSBuf]));
+            }
+            if (!ok) break;
+            {
+                const uint32_t pv = pos0 + ring_pos_v(n - 1, n);
+                const bool wt = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
+                if (__any_sync(0xffffffffu, !wt)) {
+                    ok = false;
+                    break;
+                }
+            }
+            tc_fence_after();
+            const float la = row_sum4(l[0]), lb = row_sum4(l[1]);
+            uint32_t o[D / 2];
+            if constexpr (D == 128) tmem_ld16x256_x16(t_base + kColO, o);
+            else tmem_ld16x256_x8(t_base + kColO, o);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh->o_free));
+            if (sg.slot < 0) {
+                store_o_pairs<D>(o, la > 0.0f ? 1.0f / la : (la == 0.0f ? 0.0f : la), lb > 0.0f ? 1.0f / lb : (lb == 0.0f ? 0.0f : lb),
+                                 orow[0], orow[1]);
+                if ((lane & 3) == 0) {
+                    if (!dead[0]) *lrow[0] = la == 0.0f ? -INFINITY : (m[0] + log2f(la)) * kLn2;
+                    if (!dead[1]) *lrow[1] = lb == 0.0f ? -INFINITY : (m[1] + log2f(lb)) * kLn2;
+                }
+            } else {
+                const int64_t at = ((int64_t)blockIdx.x * 2 + sg.slot) * 128;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (dead[x]) continue;
+                    float* dst = P.part_o + (at + row[x]) * D + c0;
+#pragma unroll
+                    for (int kk = 0; kk < D / 8; ++kk)
+                        *reinterpret_cast<uint2*>(dst + 8 * kk) = make_uint2(o[4 * kk + 2 * x], o[4 * kk + 2 * x + 1]);
+                    if ((lane & 3) == 0) P.part_ml[at + row[x]] = make_float2(m[x], x ? lb : la);
+                }
+            }
+            pos0 += 2u * (uint32_t)n;
+            gb0 += (uint32_t)n;
+        }
+        if (!ok && lane == 0) set_abort(sh, status);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the parts of split rows: O = sum_c 2^(m_c - M) O_c / l with M the
+// largest m_c and l = sum_c 2^(m_c - M) l_c, parts in key order.  Thread block
+// (c, y) takes rows 32 y .. 32 y + 31 of the row tile that begins in thread
+// block c of k_paged_forward: its slot 1, then slot 0 of the following blocks.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ Params P) {
+    const int4 jn = P.joins[blockIdx.x];
+    const int32_t rows = jn.z * P.group;
+    if (jn.x == 0) return;
+    constexpr int kLanes = D / 4;                       // threads of a row, four columns each
+    constexpr int kRows = kJoinThreads / kLanes;
+    const int c = threadIdx.x % kLanes;
+    for (int32_t r = blockIdx.y * 32 + threadIdx.x / kLanes; r < min(rows, (int32_t)blockIdx.y * 32 + 32); r += kRows) {
+        auto part = [&](int32_t x) -> int64_t { return (((int64_t)blockIdx.x + x) * 2 + (x == 0 ? 1 : 0)) * 128 + r; };
+        float M = -INFINITY;
+        for (int32_t x = 0; x < jn.x; ++x) M = fmaxf(M, P.part_ml[part(x)].x);
+        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int32_t x = 0; x < jn.x; ++x) {
+            const float2 ml = P.part_ml[part(x)];
+            const float4 v = *reinterpret_cast<const float4*>(P.part_o + part(x) * D + 4 * c);
+            if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // no visible key in this part
+            const float f = exp2f(ml.x - M);
+            l = fmaf(f, ml.y, l);
+            o[0] = fmaf(f, v.x, o[0]);
+            o[1] = fmaf(f, v.y, o[1]);
+            o[2] = fmaf(f, v.z, o[2]);
+            o[3] = fmaf(f, v.w, o[3]);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t at = (int64_t)(jn.y + r / P.group) * P.H + jn.w * P.group + r % P.group;
+        *reinterpret_cast<uint2*>(P.o + at * D + 4 * c) =
+            make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        if (c == 0) P.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+}
+
+// Tile lists from the tokens' lists: for each (query tile, key/value head)
+// the blocks that some token of the tile lists and sees, ascending, each with
+// one bit per token.  One thread block per tile; the bits of up to kUnionWords
+// / words blocks at a time are set in shared memory.
+constexpr int kUnionThreads = 128;
+constexpr int kUnionWords = 8192;
+struct UnionParams {
+    PagedBatch b;
+    const int32_t *sel, *sel_cnt;  // [tokens, H_kv, width], [tokens, H_kv]
+    int32_t width, H_kv, tpt, causal;
+    int32_t *list, *cnt;
+    uint32_t* who;
+    int32_t nt_cap, cap, words;
+};
+__global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_constant__ UnionParams P) {
+    __shared__ uint32_t bits[kUnionWords];
+    __shared__ int64_t part[33];
+    __shared__ int32_t hit[2];
+    int32_t t;
+    const int32_t s = find_unit(
+        P.b, blockIdx.x, [&](const PagedSeq& q) -> int64_t { return (q.nq + P.tpt - 1) / P.tpt; }, part, hit, t);
+    if (s < 0) return;
+    PagedSeq q;
+    paged_seq(P.b, s, q);
+    const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
+    const int32_t kvh = blockIdx.y;
+    const int32_t nkb = (q.kl + 127) / 128;  // blocks of the sequence
+    const int64_t f = (int64_t)kvh * P.nt_cap + blockIdx.x;
+    const int32_t span = kUnionWords / P.words;
+    int32_t done = 0;
+    for (int32_t b0 = 0; b0 < nkb; b0 += span) {
+        const int32_t nb = min(span, nkb - b0);
+        for (int32_t x = threadIdx.x; x < nb * P.words; x += kUnionThreads) bits[x] = 0u;
+        __syncthreads();
+        for (int32_t x = threadIdx.x; x < ntok * P.width; x += kUnionThreads) {
+            const int32_t tt = x / P.width, e = x % P.width;
+            const int64_t tk = ((int64_t)(q.q0 + first + tt)) * P.H_kv + kvh;
+            const int32_t n = P.sel_cnt[tk];
+            if (e == 0 && b0 == 0 && (n < 0 || n > P.width))
+                atomicCAS(P.b.status, 0, n < 0 ? BSA_ERR_BOUNDS : BSA_ERR_OVERFLOW);
+            if (e >= n) continue;
+            const int32_t blk = P.sel[tk * P.width + e];
+            if (blk < 0 || blk >= nkb) {
+                if (b0 == 0) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
+                continue;
+            }
+            const int32_t pos = q.kl - q.nq + first + tt;
+            if (blk < b0 || blk >= b0 + nb || (P.causal && blk * 128 > pos)) continue;
+            atomicOr(&bits[(blk - b0) * P.words + (tt >> 5)], 1u << (tt & 31));
+        }
+        __syncthreads();
+        for (int32_t x0 = 0; x0 < nb; x0 += kUnionThreads) {
+            const int32_t x = x0 + threadIdx.x;
+            uint32_t any = 0u;
+            if (x < nb)
+                for (int32_t w = 0; w < P.words; ++w) any |= bits[x * P.words + w];
+            int64_t total;
+            const int32_t at = done + (int32_t)block_prefix(any != 0u ? 1 : 0, part, total);
+            if (any != 0u && at < P.cap) {
+                P.list[f * P.cap + at] = b0 + x;
+                for (int32_t w = 0; w < P.words; ++w) P.who[(f * P.cap + at) * P.words + w] = bits[x * P.words + w];
+            }
+            done += (int32_t)total;
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) P.cnt[f] = min(done, P.cap);
+}
+
+// ---------------------------------------------------------------- host side
+bool encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
+               ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace: joins, maxima and sums, O parts; then the tile lists.
+struct Layout {
+    size_t joins, ml, o, cnt, list, who, total;
+    int32_t nt_cap, cap, words, tpt;
+};
+Layout layout(const PagedForwardArgs& a) {
+    Layout L{};
+    const int32_t G = a.H / a.H_kv;
+    L.tpt = 128 / G;
+    // sum over sequences of ceil(n / tpt) <= tokens / tpt + seqs
+    L.nt_cap = a.tokens / L.tpt + a.seqs;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    L.joins = take(sizeof(int4) * kPagedBlocks);
+    L.ml = take(sizeof(float2) * kPagedBlocks * 2 * 128);
+    L.o = take(sizeof(float) * kPagedBlocks * 2 * 128 * (size_t)a.D);
+    if (a.sel_width > 0) {
+        const int64_t blocks = ((int64_t)a.max_pages * a.page + 127) / 128;
+        const int64_t most = (int64_t)L.tpt * a.sel_width;
+        L.cap = (int32_t)(blocks < most ? blocks : most);
+        L.words = (L.tpt + 31) / 32;
+        const size_t rows = (size_t)a.H_kv * L.nt_cap;
+        L.cnt = take(sizeof(int32_t) * rows);
+        L.list = take(sizeof(int32_t) * rows * L.cap);
+        L.who = take(sizeof(uint32_t) * rows * L.cap * L.words);
+    }
+    L.total = at;
+    return L;
+}
+
+template <int D, bool kLists>
+bsa_status launch_d(const Params& P, cudaStream_t stream) {
+    const size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
+    static int done[64] = {0};
+    static int sms[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return BSA_ERR_CUDA;
+    if (!done[dev]) {
+        if (cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(k_paged_forward<D, kLists>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+                cudaSuccess)
+            return BSA_ERR_CUDA;
+        done[dev] = 1;
+    }
+    const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
+    k_paged_forward<D, kLists><<<grid, kThreads, smem, stream>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+    k_paged_join<D><<<dim3(grid, 4), kJoinThreads, 0, stream>>>(P);
+    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t paged_forward_workspace(const PagedForwardArgs& a) { return layout(a).total; }
+
+bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int32_t* status, cudaStream_t stream) {
+    const Layout L = layout(a);
+    Params P;
+    memset(&P, 0, sizeof(P));
+    const int32_t G = a.H / a.H_kv, D = a.D;
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.tokens};
+        const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)L.tpt}, box1[3] = {64, (cuuint32_t)G, 1};
+        if (!encode(&P.map_q, a.q, 3, dims, strides, box) || !encode(&P.map_q1, a.q, 3, dims, strides, box1))
+            return BSA_ERR_CUDA;
+    }
+    {
+        const cuuint64_t slots = (cuuint64_t)a.n_pages * a.H_kv * a.page;
+        const cuuint64_t dims[3] = {64, slots, (cuuint64_t)(D / 64)};
+        const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
+        const cuuint32_t box[3] = {64, (cuuint32_t)a.page, (cuuint32_t)(a.page == 128 ? D / 64 : 1)};
+        if (!encode(&P.map_k, a.k_cache, 3, dims, strides, box) || !encode(&P.map_v, a.v_cache, 3, dims, strides, box))
+            return BSA_ERR_CUDA;
+    }
+    P.b = PagedBatch{a.q_start, a.kv_len, a.table, a.seqs, a.tokens, a.max_pages, a.page, a.n_pages, status};
+    P.H = a.H;
+    P.H_kv = a.H_kv;
+    P.group = G;
+    P.tpt = L.tpt;
+    P.causal = a.causal;
+    P.window = a.window;
+    P.sinks = a.sinks;
+    P.scale_log2 = (a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D)) * kLog2e;
+    P.o = static_cast<__nv_bfloat16*>(a.o);
+    P.lse = a.lse;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    P.nt_cap = L.nt_cap;
+    P.joins = reinterpret_cast<int4*>(ws + L.joins);
+    P.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+    P.part_o = reinterpret_cast<float*>(ws + L.o);
+    if (a.sel != nullptr) {
+        P.cap = L.cap;
+        P.words = L.words;
+        int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
+        int32_t* list = reinterpret_cast<int32_t*>(ws + L.list);
+        uint32_t* who = reinterpret_cast<uint32_t*>(ws + L.who);
+        P.list_cnt = cnt;
+        P.list = list;
+        P.list_who = who;
+        UnionParams U{P.b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, L.tpt, a.causal, list, cnt, who, L.nt_cap, L.cap, L.words};
+        k_paged_union<<<dim3((unsigned)L.nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream>>>(U);
+        if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+        return D == 128 ? launch_d<128, true>(P, stream) : launch_d<64, true>(P, stream);
+    }
+    return D == 128 ? launch_d<128, false>(P, stream) : launch_d<64, false>(P, stream);
+}
+
+}  // namespace bsa
