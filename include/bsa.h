@@ -666,7 +666,7 @@ bsa_status bsa_upscale_threshold(const float* T_base, int64_t heads, int32_t Ub,
  * The host needs to know none of these values, so the calls can be captured
  * into a graph once and replayed as the sequences grow.
  *
- *   seqs 0 .. 32768; tokens 0 .. 2^24 with tokens * H < 2^31 (0 of either:
+ *   seqs 0 .. 16384; tokens 0 .. 2^24 with tokens * H < 2^31 (0 of either:
  *   nothing to do); page_size 16, 32, 64 or 128; max_pages * page_size <=
  *   2^24; n_pages * H_kv * page_size < 2^31; D 64 or 128; H_kv divides H,
  *   H / H_kv <= 128, H <= 65535.  Index arrays are 4-byte aligned, the caches

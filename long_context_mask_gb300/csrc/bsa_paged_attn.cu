@@ -30,8 +30,10 @@
 // see bsa_rows.cuh) and the epilogue; 10 loads the query tiles, so that K/V
 // loads of the next segment never wait for the last products on Q.
 // Shared memory: the Q tile and a ring of K/V tiles.  Tensor memory: three
-// score buffers and O, as in bsa_attn.cu, whose schedule (K_0 .. K_2, then
-// V_i, K_{i+3}) this kernel shares.
+// score buffers and O.  Tiles are numbered through the whole run: K_g is loaded
+// and Q K_g issued right after V_{g-3} and its product, across the borders of
+// segments, so that the next segment's scores are there when the softmax comes
+// to them.
 //
 // Slots behind the end of a sequence hold anything, NaN included.  Their
 // scores are dropped by a select, and the value rows behind the end are
@@ -92,13 +94,13 @@ struct Shared {
     uint64_t full[16];
     uint64_t empty[16];
     uint64_t q_full, q_empty;
-    uint64_t p_full[kSBuf];
-    uint64_t o_free;
+    uint64_t p_full[kSBuf];   // P_g has been written (and O rescaled)
+    uint64_t o_free;          // the segment's O has been read
     uint64_t mma_done;
     uint64_t seg_full[kDesc], seg_empty[kDesc];
     Segment seg[kDesc];
     int64_t part[33];
-    int32_t start[5];  // first unit: key/value head, sequence, query tile, key tile; tile within the head
+    int32_t start[5];  // first unit: key/value head, sequence, query tile, unit; tile within the head
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -137,6 +139,20 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t
     return __all_sync(0xffffffffu, wait(bar, parity, status));
 }
 
+// a / b; nearly every dividend fits 32 bits, whose division is much shorter.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (a >> 32) == 0 && (b >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Place of tile K_g (V_g) in the order of loads K_0, K_1, K_2, V_0, K_3, V_1, ..;
+// behind the run's last K tile every other place stays empty.  Ring slot: place %
+// stages.  The empty barrier of K_g's slot also tells the softmax that S_g is
+// there, V_g's that O holds P_g V_g (one commit for both): the barrier's next
+// completion needs a later P from that softmax, and who waits for PV_g has seen
+// S_{g+1} or S_g, so that PV_{g-3}, the completion before it, is known to be done.
+__device__ __forceinline__ uint32_t place_k(uint32_t g) { return g < kSBuf ? g : 2u * g - 2u; }
+__device__ __forceinline__ uint32_t place_v(uint32_t g) { return 2u * g + 3u; }
+
 // Key tiles that the tokens at positions pos0 .. pos0 + ntok - 1 see some key
 // of: the sink tiles 0 .. ns - 1 and lo .. lo + (n - ns) - 1.
 __device__ __forceinline__ int32_t key_tiles(const Params& P, int32_t pos0, int32_t ntok, int32_t kl, int32_t& lo,
@@ -152,11 +168,19 @@ __device__ __forceinline__ int32_t key_tiles(const Params& P, int32_t pos0, int3
     return hi_t - lo + ns;
 }
 
-// Positions in the K/V load order K_0, K_1, K_2, then V_i, K_{i+3} (see bsa_attn.cu).
-__device__ __forceinline__ uint32_t ring_pos_k(int32_t j) { return (uint32_t)(j < kSBuf ? j : 2 * j - 2); }
-__device__ __forceinline__ uint32_t ring_pos_v(int32_t i, int32_t n) {
-    const int32_t lead = min(n, kSBuf);
-    return (uint32_t)(lead + i + max(min(i, n - kSBuf), 0));
+// The run is cut by cost: a query tile of n key tiles counts n + kRowCost, the
+// constant for its start and epilogue (measured: a causal prompt's blocks, 7 to
+// 58 query tiles each, end within 3 % of each other with it, 20 % without).
+// A cut x units into the query tile leaves cut_at(x) of its key tiles on the left.
+constexpr int32_t kRowCost = 2;
+__device__ __forceinline__ int32_t row_units(int32_t n) { return max(n, 1) + kRowCost; }
+__device__ __forceinline__ int32_t cut_at(int32_t x) { return max(x - kRowCost, 0); }
+
+// Which of a thread's columns 8 kk and 8 kk + 1 (kk = 0 .. 15; bit 2 kk and the
+// next) are below v.
+__device__ __forceinline__ uint32_t columns_below(int32_t v) {
+    const int32_t n = v <= 0 ? 0 : 2 * (v >> 3) + min(v & 7, 2);
+    return n >= 32 ? ~0u : (1u << n) - 1u;
 }
 
 // One key tile of the online softmax for this thread's shares of rows a and b.
@@ -207,8 +231,12 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
     return rescale;
 }
 
-template <int D, bool kLists>
+// kMode: which keys a row sees besides the causal and length limits.
+enum { kPlain = 0, kWindow = 1, kListed = 2 };
+
+template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_constant__ Params P) {
+    constexpr bool kLists = kMode == kListed;
     using C = Cfg<D>;
     constexpr uint32_t S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -220,38 +248,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     const int lane = threadIdx.x & 31;
     int32_t* const status = P.b.status;
 
+    if (threadIdx.x == kThreads - 32) {
+        for (uint32_t s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&sh->full[s]), 1);
+            mbar_init(smem_u32(&sh->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh->q_full), 1);
+        mbar_init(smem_u32(&sh->q_empty), 1);
+        for (int s = 0; s < kSBuf; ++s) mbar_init(smem_u32(&sh->p_full[s]), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->o_free), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->mma_done), 1);
+        for (int d = 0; d < kDesc; ++d) {
+            mbar_init(smem_u32(&sh->seg_full[d]), 1);
+            mbar_init(smem_u32(&sh->seg_empty[d]), kConsumers);
+        }
+        fence_mbar_init();
+        prefetch_tensormap(&P.map_k);
+        prefetch_tensormap(&P.map_v);
+        prefetch_tensormap(&P.map_q);
+        prefetch_tensormap(&P.map_q1);
+    }
+    if (threadIdx.x == 0) {
+        P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);  // (the producer writes it again where a row is split)
+        // a block of this launch (or an unread earlier one) timed out: abandon
+        sh->abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
+    }
+    launch_dependents();
+
     // ---------------------------------------------------------------- this block's run
-    // cum[s]: query tiles of the sequences before s (the data area is free here)
+    // of sequence s: the query tiles of the sequences before it, its new tokens and
+    // its length (the data area is free here)
     int32_t* cum = reinterpret_cast<int32_t*>(smem);
-    int64_t nt = 0;  // query tiles of one key/value head
+    int32_t* seq_nq = cum + P.b.seqs;
+    int32_t* seq_kl = seq_nq + P.b.seqs;
+    int32_t nt;  // query tiles of one key/value head
     {
         const int32_t per = (P.b.seqs + kThreads - 1) / kThreads;
         const int32_t a = min((int32_t)threadIdx.x * per, P.b.seqs), e = min(a + per, P.b.seqs);
-        int64_t mine = 0;
+        int64_t mine = 0, all;
         for (int32_t s = a; s < e; ++s) {
             PagedSeq q;
             if (!paged_seq(P.b, s, q) && blockIdx.x == 0) raise_status(status, BSA_ERR_BOUNDS);
+            seq_nq[s] = q.nq;
+            seq_kl[s] = q.kl;
             mine += (q.nq + P.tpt - 1) / P.tpt;
         }
-        int64_t at = block_prefix(mine, sh->part, nt);
+        int64_t at = block_prefix(mine, sh->part, all);
         for (int32_t s = a; s < e; ++s) {
-            PagedSeq q;
-            paged_seq(P.b, s, q);
             cum[s] = (int32_t)min(at, (int64_t)P.nt_cap);
-            at += (q.nq + P.tpt - 1) / P.tpt;
+            at += (seq_nq[s] + P.tpt - 1) / P.tpt;
         }
-        nt = min(nt, (int64_t)P.nt_cap);  // (beyond: only with starts that decrease, reported above)
+        nt = (int32_t)min(all, (int64_t)P.nt_cap);  // (beyond: only with starts that decrease, reported above)
     }
+    if constexpr (kLists) wait_primary();  // the lists are there
     __syncthreads();
-    const int64_t rows = kLists ? nt * P.H_kv : nt;  // tiles whose counts differ
-    const int64_t per_row = (rows + kThreads - 1) / kThreads;
-    const int64_t f0 = min((int64_t)threadIdx.x * per_row, rows), f1 = min(f0 + per_row, rows);
+    const int32_t rows = kLists ? nt * P.H_kv : nt;  // tiles whose counts differ
+    const int32_t per_row = (rows + kThreads - 1) / kThreads;
+    const int32_t f0 = min((int32_t)threadIdx.x * per_row, rows), f1 = min(f0 + per_row, rows);
     // walks this thread's tiles: visit(kvh, i, s, t, units), tile i of the head being query tile t of sequence s
     auto walk = [&](auto&& visit) {
-        int64_t f = f0;
-        if (f >= f1) return;
-        int32_t i = (int32_t)(f % nt), kvh = (int32_t)(f / nt);
-        int32_t s = 0;
+        if (f0 >= f1) return;
+        int32_t kvh = kLists ? f0 / nt : 0, i = f0 - kvh * nt, s = 0;
         auto find = [&]() {
             int32_t lo = 0, hi = P.b.seqs;  // the last s with cum[s] <= i
             while (hi - lo > 1) {
@@ -262,28 +319,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             s = lo;
         };
         find();
-        PagedSeq q;
-        paged_seq(P.b, s, q);
-        for (; f < f1; ++f) {
+        for (int32_t f = f0; f < f1; ++f) {
             const int32_t t = i - cum[s];
             int32_t n;
             if constexpr (kLists) {
                 n = P.list_cnt[(int64_t)kvh * P.nt_cap + i];
             } else {
                 int32_t lo, ns;
-                const int32_t first = t * P.tpt;
-                n = key_tiles(P, q.kl - q.nq + first, min(P.tpt, q.nq - first), q.kl, lo, ns);
+                const int32_t first = t * P.tpt, nq = seq_nq[s], kl = seq_kl[s];
+                n = key_tiles(P, kl - nq + first, min(P.tpt, nq - first), kl, lo, ns);
             }
-            if (visit(kvh, i, s, t, max(n, 1))) return;  // an empty row is one unit: it is written
+            if (visit(kvh, i, s, t, row_units(n))) return;
             ++i;
             if (i == nt) {
                 i = 0;
                 ++kvh;
                 find();
-                paged_seq(P.b, s, q);
             } else if (s + 1 < P.b.seqs && cum[s + 1] <= i) {
                 find();
-                paged_seq(P.b, s, q);
             }
         }
     };
@@ -294,16 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     });
     const int64_t before = block_prefix(mine, sh->part, total);
     const int64_t units = kLists ? total : total * P.H_kv;
-    const int64_t blocks = min((int64_t)gridDim.x, units);
-    if (threadIdx.x == 0) {
-        P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);  // (the producer writes it again where a row is split)
-        // a block of this launch (or an unread earlier one) timed out: abandon
-        sh->abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
-    }
-    if ((int64_t)blockIdx.x >= blocks) return;
-    const int64_t u0 = units * blockIdx.x / blocks, u1 = units * (blockIdx.x + 1) / blocks;
+    const int32_t blocks = (int32_t)min((int64_t)gridDim.x, units);
+    if ((int32_t)blockIdx.x >= blocks) return;
+    // equal runs, the first `extra` of them one unit longer
+    const int64_t share = divide(units, blocks);
+    const int32_t extra = (int32_t)(units - share * blocks);
+    const int64_t u0 = share * blockIdx.x + min((int32_t)blockIdx.x, extra);
+    const int64_t u1 = u0 + share + ((int32_t)blockIdx.x < extra ? 1 : 0);
     {
-        const int64_t head = kLists ? 0 : u0 / total, r = kLists ? u0 : u0 % total;
+        const int64_t head = kLists ? 0 : divide(u0, total), r = kLists ? u0 : u0 - head * total;
         if (r >= before && r < before + mine) {
             int64_t at = before;
             walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
@@ -320,26 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             });
         }
     }
-    __syncthreads();
-    if (sh->abort != 0) return;
-
-    if (threadIdx.x == 0) {
-        for (uint32_t s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&sh->full[s]), 1);
-            mbar_init(smem_u32(&sh->empty[s]), 1);
-        }
-        mbar_init(smem_u32(&sh->q_full), 1);
-        mbar_init(smem_u32(&sh->q_empty), 1);
-        for (int s = 0; s < kSBuf; ++s) mbar_init(smem_u32(&sh->p_full[s]), 32 * kSoftmaxWarps);
-        mbar_init(smem_u32(&sh->o_free), 32 * kSoftmaxWarps);
-        mbar_init(smem_u32(&sh->mma_done), 1);
-        for (int d = 0; d < kDesc; ++d) {
-            mbar_init(smem_u32(&sh->seg_full[d]), 1);
-            mbar_init(smem_u32(&sh->seg_empty[d]), kConsumers);
-        }
-        fence_mbar_init();
-    }
-    if (warp == kMma) {
+    const bool abandoned = sh->abort != 0;
+    if (warp == kMma && !abandoned) {
         tmem_alloc(smem_u32(&sh->tmem_base), kTmemCols);
         tmem_relinquish();
     }
@@ -348,23 +382,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (abandoned) return;
     const uint32_t tmem = sh->tmem_base;
 
-    // The next segment, for the warps that read descriptors; false: no more.
-    auto next_segment = [&](uint32_t k, Segment& sg, bool& ok) -> bool {
+    // Segment k, for the warps that read descriptors (null: no more); they hand
+    // it back when they are through with it.
+    auto next_segment = [&](uint32_t k, bool& ok) -> const Segment* {
         if (!wait_warp(smem_u32(&sh->seg_full[k % kDesc]), (k / kDesc) & 1u, status)) {
             ok = false;
-            return false;
+            return nullptr;
         }
-        sg = sh->seg[k % kDesc];
+        const Segment* sg = &sh->seg[k % kDesc];
+        return sg->n >= 0 ? sg : nullptr;
+    };
+    auto hand_back = [&](uint32_t k) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh->seg_empty[k % kDesc]));
-        return sg.n >= 0;
     };
 
     if (warp == kProducer) {
         // ------------------------------------------------------------ segments and K/V tiles
-        int32_t kvh = sh->start[0], s = sh->start[1], t = sh->start[2], j0 = sh->start[3];
+        int32_t kvh = sh->start[0], s = sh->start[1], t = sh->start[2], x0 = sh->start[3], i = sh->start[4];
         int64_t left = u1 - u0, u = u0;
         PagedSeq q;
         paged_seq(P.b, s, q);
@@ -376,9 +414,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         const uint32_t my_dst = (uint32_t)(my_half * kBox + my_piece * page * 128);
         const uint32_t piece_bytes = (uint32_t)(page * D * 2);
         const int32_t per_window = 32 / pieces;  // key tiles whose pages one 32-lane read brings
-        uint32_t pos = 0, issued = 0, k = 0;
+        uint32_t k = 0;
+        uint32_t g = 0, gv = 0;            // K and V tiles so far
+        int32_t r0 = -1, r1 = -1, r2 = -1;  // this lane's slot rows of the last three K tiles
         bool ok = true;
-        int32_t i = sh->start[4];
+        // one tile: this lane's slot row (-1: no page there)
+        auto load = [&](int32_t row, bool is_v) -> bool {
+            const uint32_t pos = is_v ? place_v(gv) : place_k(g);
+            const uint32_t slot = pos % S;
+            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, status) || aborted(sh)) return false;
+            const uint32_t fb = smem_u32(&sh->full[slot]);
+            const bool go = lane < n_loads && row >= 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, go);
+            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(__popc(mask) / halves) * piece_bytes);
+            __syncwarp();
+            if (go) tma_load_3d(s_ring + slot * C::kTile + my_dst, is_v ? &P.map_v : &P.map_k, 0, row, my_half, fb);
+            __syncwarp();
+            if (is_v) ++gv;
+            else ++g;
+            return true;
+        };
         while (left > 0 && ok) {
             const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
             Segment sg;
@@ -397,21 +452,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             } else {
                 n_row = key_tiles(P, sg.pos0, ntok, q.kl, sg.lo, sg.ns);
             }
-            const int32_t n_eff = max(n_row, 1);
-            const int32_t take = (int32_t)min((int64_t)(n_eff - j0), left);
+            const int32_t n_eff = max(n_row, 1), w = row_units(n_row);
+            const bool last = left < w - x0;  // the run ends within this query tile
+            const int32_t j0 = cut_at(x0), j1 = last ? cut_at(x0 + (int32_t)left) : n_eff;
+            if (j1 <= j0) break;              // (only where it ends)
             sg.j0 = j0;
-            sg.n = n_row == 0 ? 0 : take;
-            sg.slot = j0 == 0 && take == n_eff ? -1 : (j0 == 0 ? 1 : 0);
-            if (lane == 0 && left == take) {
-                // the last segment: does a split row begin in this block?
-                int4 jn = make_int4(0, 0, 0, 0);
-                if (j0 == 0 && take < n_eff) {
-                    // the block that holds the row's last unit: the least c with units (c + 1) / blocks >= end
-                    const int64_t end = u + n_eff;
-                    const int64_t last = (end * blocks + units - 1) / units - 1;
-                    jn = make_int4((int32_t)(last - blockIdx.x + 1), sg.q0, ntok, kvh);
-                }
-                P.joins[blockIdx.x] = jn;
+            sg.n = n_row == 0 ? 0 : j1 - j0;
+            sg.slot = j0 == 0 && j1 == n_eff ? -1 : (j0 == 0 ? 1 : 0);
+            if (lane == 0 && last && j0 == 0) {
+                // a split row begins here; its last part is in the block of its last unit
+                const int64_t end = u + (w - x0);
+                const int64_t longer = (share + 1) * extra;  // units of the longer runs
+                const int64_t c = end <= longer ? (end - 1) / (share + 1) : extra + (end - 1 - longer) / share;
+                P.joins[blockIdx.x] = make_int4((int32_t)(c - blockIdx.x + 1), sg.q0, ntok, kvh);
             }
             if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
                 ok = false;
@@ -420,10 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             if (lane == 0) {
                 sh->seg[k % kDesc] = sg;
                 mbar_arrive(smem_u32(&sh->seg_full[k % kDesc]));
+                // the query tile is loaded when its buffer is free; on its way into L2 now
+                if (k > 0)
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_prefetch_3d(ntok == 1 ? &P.map_q1 : &P.map_q, h * 64, kvh * P.group, sg.q0);
             }
             __syncwarp();
             ++k;
-            // tiles in the order K_0 .. K_2, then V_i, K_{i+3}, then the last V
             const int32_t n = sg.n;
             const int32_t* list = kLists ? P.list + (int64_t)sg.list * P.cap + j0 : nullptr;
             auto tile_of = [&](int32_t j) -> int32_t {
@@ -447,49 +504,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 return (id * P.H_kv + kvh) * page;
             };
             int32_t w0 = 0, cur = fetch(0), nxt = fetch(per_window);
-            int32_t r0 = -1, r1 = -1, r2 = -1;  // this lane's slot rows of the last three K tiles
-            const int32_t lead = min(n, kSBuf), inter = 2 * (n - lead);
-            for (int32_t x = 0; x < 2 * n; ++x) {
-                const bool is_v = x >= lead && (x - lead >= inter || ((x - lead) & 1) == 0);
-                int32_t row;
-                if (!is_v) {
-                    const int32_t j = x < lead ? x : ((x - lead) >> 1) + kSBuf;
-                    if (j >= w0 + per_window) {
-                        w0 += per_window;
-                        cur = nxt;
-                        nxt = fetch(w0 + per_window);
-                    }
-                    row = __shfl_sync(0xffffffffu, cur, (j - w0) * pieces + my_piece);
-                    r0 = r1;
-                    r1 = r2;
-                    r2 = row;
-                } else {
-                    const int32_t v = x - lead < inter ? (x - lead) >> 1 : (n - lead) + (x - lead - inter);
-                    // V_v follows the load of K_{min(v + 2, n - 1)}
-                    const int32_t back = min(v + kSBuf - 1, n - 1) - v;
-                    row = back == 2 ? r0 : (back == 1 ? r1 : r2);
+            for (int32_t j = 0; j < n && ok; ++j) {
+                if (j >= w0 + per_window) {
+                    w0 += per_window;
+                    cur = nxt;
+                    nxt = fetch(w0 + per_window);
                 }
-                const uint32_t slot = pos % S;
-                if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, status) || aborted(sh)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t fb = smem_u32(&sh->full[slot]);
-                const bool go = lane < n_loads && row >= 0;
-                const uint32_t mask = __ballot_sync(0xffffffffu, go);
-                if (lane == 0)
-                    mbar_arrive_expect_tx(fb, (uint32_t)(__popc(mask) / halves) * piece_bytes);
-                __syncwarp();
-                if (go)
-                    tma_load_3d(s_ring + slot * C::kTile + my_dst, is_v ? &P.map_v : &P.map_k, 0, row, my_half, fb);
-                __syncwarp();
-                ++pos;
-                issued = pos;
+                const int32_t row = __shfl_sync(0xffffffffu, cur, (j - w0) * pieces + my_piece);
+                if (g >= kSBuf) ok = load(r0, true);   // V_{g-3}
+                ok = ok && load(row, false);           // K_g
+                r0 = r1;
+                r1 = r2;
+                r2 = row;
             }
             // on to the next query tile
-            left -= take;
-            u += take;
-            j0 = 0;
+            left -= w - x0;
+            u += w - x0;
+            x0 = 0;
             if (left > 0) {
                 ++t;
                 if (++i == (int32_t)nt) {  // the next head
@@ -503,6 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 }
             }
         }
+        // the last V tiles
+        while (gv < g && ok) {
+            const uint32_t back = g - gv;
+            ok = load(back == 3 ? r0 : (back == 2 ? r1 : r2), true);
+        }
         if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
             if (lane == 0) {
                 sh->seg[k % kDesc].n = -1;
@@ -514,32 +550,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         if (!ok && lane == 0) set_abort(sh, status);
         // every issued copy must land before the block exits
         if (lane == 0) {
-            for (uint32_t x = issued > S ? issued - S : 0; x < issued; ++x)
-                if (!wait(smem_u32(&sh->full[x % S]), (x / S) & 1u, status)) raise_status(status, BSA_ERR_TIMEOUT);
+            // (the last copy of each slot; earlier ones were used up before it)
+            const uint32_t end = max(g > 0 ? place_k(g - 1) : 0u, gv > 0 ? place_v(gv - 1) : 0u);
+            for (uint32_t x = end >= S ? end - S + 1 : 0; x <= end; ++x) {
+                const bool is_k = x < kSBuf || (x & 1u) == 0;
+                const bool used = is_k ? (x < kSBuf ? x < g : (x + 2u) / 2u < g) : (x - 3u) / 2u < gv;
+                if (used && !wait(smem_u32(&sh->full[x % S]), (x / S) & 1u, status)) raise_status(status, BSA_ERR_TIMEOUT);
+            }
         }
         __syncwarp();
     } else if (warp == kQLoad) {
         // ------------------------------------------------------------ query tiles
         uint32_t nq = 0;
         bool ok = true;
-        Segment sg;
-        for (uint32_t k = 0; next_segment(k, sg, ok); ++k) {
-            if (sg.n == 0) continue;
-            if (nq > 0 && !wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, status)) {
-                ok = false;
-                break;
-            }
-            if (aborted(sh)) break;
-            if (lane == 0) {
-                const bool one = sg.ntok == 1;
-                const uint32_t bar = smem_u32(&sh->q_full);
-                mbar_arrive_expect_tx(bar, (uint32_t)((one ? 1 : P.tpt) * P.group * D * 2));
+        for (uint32_t k = 0;; ++k) {
+            const Segment* sg = next_segment(k, ok);
+            if (sg == nullptr) break;
+            if (sg->n > 0) {
+                if (nq > 0 && !wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, status)) {
+                    ok = false;
+                    break;
+                }
+                if (aborted(sh)) break;
+                if (lane == 0) {
+                    const bool one = sg->ntok == 1;
+                    const uint32_t bar = smem_u32(&sh->q_full);
+                    mbar_arrive_expect_tx(bar, (uint32_t)((one ? 1 : P.tpt) * P.group * D * 2));
 #pragma unroll
-                for (int h = 0; h < C::kHalves; ++h)
-                    tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, sg.kvh * P.group, sg.q0, bar);
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, sg->kvh * P.group, sg->q0, bar);
+                }
+                __syncwarp();
+                ++nq;
             }
-            __syncwarp();
-            ++nq;
+            hand_back(k);
         }
         if (!ok && lane == 0) set_abort(sh, status);
         if (lane == 0 && nq > 0 && !wait(smem_u32(&sh->q_full), (nq - 1u) & 1u, status))
@@ -550,77 +594,102 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         const uint64_t dq = smem_desc_sw128(s_q, 16, 1024);
         const uint64_t dk = smem_desc_sw128(s_ring, 16, 1024);
         const uint64_t dv = smem_desc_sw128(s_ring, kBox, 1024);
-        uint32_t pos = 0, gb0 = 0, nq = 0;
+        uint32_t g = 0, pv = 0, nq = 0, pv_segs = 0;  // QKs and PVs so far, query tiles, segments of the PVs
+        // of the last three tiles: value rows before the sequence's end, + 256 where
+        // the tile is its segment's first
+        int32_t f0 = 0, f1 = 0, f2 = 0;
         bool ok = true;
-        Segment sg;
-        for (uint32_t k = 0; ok && next_segment(k, sg, ok); ++k) {
-            const int32_t n = sg.n;
-            if (n == 0) continue;
-            // the segment's last tile may hold the sequence's end: rows behind it are zeroed
-            int32_t last_kt;
-            if constexpr (kLists) last_kt = P.list[(int64_t)sg.list * P.cap + sg.j0 + n - 1];
-            else last_kt = sg.j0 + n - 1 < sg.ns ? sg.j0 + n - 1 : sg.lo + sg.j0 + n - 1 - sg.ns;
-            const int32_t tail = min(sg.kl - last_kt * 128, 128);
-            ok = wait_warp(smem_u32(&sh->q_full), nq & 1u, status);
-            if (!ok) break;
+        // O += P_x V_x for the next tile x of the run
+        auto issue_pv = [&]() -> bool {
+            const uint32_t x = pv, pos = place_v(x), back = g - x;
+            const int32_t f = back == 3 ? f0 : (back == 2 ? f1 : f2);
+            if (!wait_warp(smem_u32(&sh->p_full[x % kSBuf]), (x / kSBuf) & 1u, status)) return false;
+            const bool first = (f & 256) != 0;
+            if (first) {
+                // it overwrites O: the previous segment's epilogue must have read it
+                if (pv_segs > 0 && !wait_warp(smem_u32(&sh->o_free), (pv_segs - 1u) & 1u, status)) return false;
+                ++pv_segs;
+            }
+            const uint32_t slot = pos % S;
+            if (!wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status)) return false;
+            const int32_t tail = f & 255;
+            if (tail < 128) {
+                // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
+                const uint32_t tile = s_ring + slot * C::kTile;
+                for (int32_t y = tail * 8 + lane; y < 128 * 8; y += 32)
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + h * kBox + y * 16), "r"(0)
+                                     : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
             tc_fence_after();
-            auto issue_qk = [&](int32_t j) -> bool {
-                const uint32_t slot = pos % S;
-                if (!wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status)) return false;
+            const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
+            const uint32_t p_col = (x % kSBuf) * 128u;
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(tmem + kColO, tmem + p_col + kk * 8, vs + (uint64_t)(kk * 2048 >> 4), C::kIdescPV,
+                           (!first || kk > 0) ? 1u : 0u);
+                mma_commit(smem_u32(&sh->empty[slot]));
+            }
+            __syncwarp();
+            ++pv;
+            return true;
+        };
+        for (uint32_t k = 0; ok; ++k) {
+            const Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const int32_t n = sp->n;
+            int32_t tail = 128;
+            if (n > 0) {
+                // the segment's last tile may hold the sequence's end: value rows behind it are zeroed
+                const int32_t x = sp->j0 + n - 1;
+                int32_t kt;
+                if constexpr (kLists) kt = P.list[(int64_t)sp->list * P.cap + x];
+                else kt = x < sp->ns ? x : sp->lo + x - sp->ns;
+                tail = min(sp->kl - kt * 128, 128);
+            }
+            hand_back(k);
+            for (int32_t j = 0; j < n && ok; ++j, ++g) {
+                // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
+                if (pv + kSBuf == g) ok = issue_pv();
+                if (j == 0 && ok) {
+                    // while the query tile is on its way, the products of the segment before
+                    const uint64_t t0 = globaltimer();
+                    while (!__all_sync(0xffffffffu, mbar_test(smem_u32(&sh->q_full), nq & 1u))) {
+                        if (pv < g && __all_sync(0xffffffffu, mbar_test(smem_u32(&sh->p_full[pv % kSBuf]), (pv / kSBuf) & 1u)))
+                            ok = issue_pv();
+                        if (__any_sync(0xffffffffu, !ok || aborted(sh) || globaltimer() - t0 > kWaitNs)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    ++nq;
+                }
+                const uint32_t pos = place_k(g), slot = pos % S;
+                ok = ok && wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
+                if (!ok) break;
                 tc_fence_after();
                 const uint64_t ks = dk + (uint64_t)((slot * C::kTile) >> 4);
-                const uint32_t d_col = ((gb0 + (uint32_t)j) % kSBuf) * 128u;
+                const uint32_t d_col = (g % kSBuf) * 128u;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
                         mma_ss(tmem + d_col, dq + off, ks + off, C::kIdescQK, kk > 0 ? 1u : 0u);
                     }
-                    mma_commit(smem_u32(&sh->empty[slot]));  // also signals S_j to the softmax
+                    mma_commit(smem_u32(&sh->empty[slot]));
                     if (j == n - 1) mma_commit(smem_u32(&sh->q_empty));
                 }
                 __syncwarp();
-                ++pos;
-                return true;
-            };
-            for (int32_t j = 0; ok && j < n && j < kSBuf; ++j) ok = issue_qk(j);
-            for (int32_t i = 0; ok && i < n; ++i) {
-                const uint32_t gb = gb0 + (uint32_t)i;
-                ok = wait_warp(smem_u32(&sh->p_full[gb % kSBuf]), (gb / kSBuf) & 1u, status);
-                // the first PV of a segment overwrites O: the previous epilogue must have read it
-                if (ok && i == 0 && nq > 0) ok = wait_warp(smem_u32(&sh->o_free), (nq - 1u) & 1u, status);
-                if (!ok) break;
-                const uint32_t slot = pos % S;
-                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
-                if (!ok) break;
-                if (i == n - 1 && tail < 128) {
-                    // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
-                    const uint32_t tile = s_ring + slot * C::kTile;
-                    for (int32_t x = tail * 8 + lane; x < 128 * 8; x += 32)
-#pragma unroll
-                        for (int h = 0; h < C::kHalves; ++h)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + h * kBox + x * 16), "r"(0)
-                                         : "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                tc_fence_after();
-                const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
-                const uint32_t p_col = (gb % kSBuf) * 128u;
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + kColO, tmem + p_col + kk * 8, vs + (uint64_t)(kk * 2048 >> 4), C::kIdescPV,
-                               (i > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(smem_u32(&sh->empty[slot]));  // also signals PV_i to the softmax
-                }
-                __syncwarp();
-                ++pos;
-                if (i + kSBuf < n) ok = issue_qk(i + kSBuf);
+                f0 = f1;
+                f1 = f2;
+                f2 = (j == n - 1 ? tail : 128) + (j == 0 ? 256 : 0);
             }
-            gb0 += (uint32_t)n;
-            ++nq;
         }
+        while (pv < g && ok) ok = issue_pv();
         if (!ok && lane == 0) set_abort(sh, status);
         // nothing of ours may still be running when TMEM is freed
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
@@ -637,39 +706,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         const uint32_t t_base = tmem + ((uint32_t)(qd * 32 + half * 16) << 16);
         const int c0 = 2 * (lane & 3);  // this thread's columns: c0 + 8 k, c0 + 8 k + 1
         const float sl2 = P.scale_log2;
-        uint32_t pos0 = 0, gb0 = 0;
+        uint32_t gb0 = 0;
         bool ok = true;
-        Segment sg;
-        for (uint32_t k = 0; next_segment(k, sg, ok); ++k) {
-            const int32_t n = sg.n;
-            bool dead[2];
-            __nv_bfloat16* orow[2];
-            float* lrow[2];
-            int32_t hi[2], lo[2], sk[2];  // keys lo .. hi - 1 and 0 .. sk - 1
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                dead[x] = tok[x] >= sg.ntok;
-                const int64_t at = (int64_t)(sg.q0 + tok[x]) * P.H + sg.kvh * P.group + head[x];
-                orow[x] = dead[x] ? nullptr : P.o + at * D;
-                lrow[x] = P.lse + at;
-                const int32_t p = sg.pos0 + tok[x];
-                hi[x] = P.causal ? min(sg.kl, p + 1) : sg.kl;
-                lo[x] = P.window > 0 ? p - P.window + 1 : 0;
-                sk[x] = P.window > 0 ? min(P.sinks, hi[x]) : 0;
-            }
+        for (uint32_t k = 0;; ++k) {
+            const Segment* sg = next_segment(k, ok);
+            if (sg == nullptr) break;
+            const int32_t n = sg->n, j0 = sg->j0, lo_t = sg->lo, ns = sg->ns;
+            const bool dead[2] = {tok[0] >= sg->ntok, tok[1] >= sg->ntok};
+            // where row x's result goes
+            auto out_row = [&](int x) -> int64_t { return (int64_t)(sg->q0 + tok[x]) * P.H + sg->kvh * P.group + head[x]; };
             if (n == 0) {
                 // no key at all: O = 0, LSE = -inf
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (dead[x]) continue;
+                    __nv_bfloat16* orow = P.o + out_row(x) * D + c0;
 #pragma unroll
-                    for (int kk = 0; kk < D / 8; ++kk) *reinterpret_cast<uint32_t*>(orow[x] + 8 * kk + c0) = 0u;
-                    if ((lane & 3) == 0) *lrow[x] = -INFINITY;
+                    for (int kk = 0; kk < D / 8; ++kk) *reinterpret_cast<uint32_t*>(orow + 8 * kk) = 0u;
+                    if ((lane & 3) == 0) P.lse[out_row(x)] = -INFINITY;
                 }
+                hand_back(k);
                 continue;
             }
-            const int32_t* list = kLists ? P.list + (int64_t)sg.list * P.cap + sg.j0 : nullptr;
-            const uint32_t* who = kLists ? P.list_who + ((int64_t)sg.list * P.cap + sg.j0) * P.words : nullptr;
+            // Row x sees keys lo[x] .. hi[x] - 1 and 0 .. sk[x] - 1.  Key tiles below
+            // all_hi, and with a window from all_lo on or inside the sinks, are seen
+            // whole by every row of the query tile.
+            int32_t hi[2], lo[2] = {0, 0}, sk[2] = {0, 0};
+            int32_t all_hi, all_lo = 0, all_sk = 0;
+            {
+                const int32_t kl = sg->kl, p0 = sg->pos0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    hi[x] = P.causal ? min(kl, p0 + tok[x] + 1) : kl;
+                    if constexpr (kMode == kWindow) {
+                        lo[x] = p0 + tok[x] - P.window + 1;
+                        sk[x] = min(P.sinks, hi[x]);
+                    }
+                }
+                all_hi = (P.causal ? max(min(kl, p0 + 1), 0) : kl) >> 7;
+                if constexpr (kMode == kWindow) {
+                    all_lo = (max(p0 + sg->ntok - P.window, 0) + 127) >> 7;
+                    all_sk = P.sinks >> 7;
+                }
+            }
+            const int32_t* list = kLists ? P.list + (int64_t)sg->list * P.cap + j0 : nullptr;
+            const uint32_t* who = kLists ? P.list_who + ((int64_t)sg->list * P.cap + j0) * P.words : nullptr;
             float m[2] = {dead[0] ? 0.0f : -INFINITY, dead[1] ? 0.0f : -INFINITY};
             float l[2] = {0.0f, 0.0f};  // this thread's share of each row
             int32_t kt_next = 0;
@@ -688,23 +769,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 const uint32_t sbuf = (gb % kSBuf) * 128u;
                 int32_t kt;
                 if constexpr (kLists) kt = kt_next;
-                else kt = sg.j0 + j < sg.ns ? sg.j0 + j : sg.lo + sg.j0 + j - sg.ns;
+                else if constexpr (kMode == kWindow) kt = j0 + j < ns ? j0 + j : lo_t + j0 + j - ns;
+                else kt = j0 + j;
                 const int32_t kb = kt * 128;
-                int32_t h[2], w[2], z[2];  // visible columns of this tile: [w, h) and [0, z)
-                bool part = false, any = false;
+                bool listed[2] = {true, true};
+                bool masked = true, visible = true;
+                if constexpr (kLists) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    h[x] = min(hi[x] - kb, 128);
-                    w[x] = max(lo[x] - kb, 0);
-                    z[x] = min(sk[x] - kb, 128);
-                    if (kLists && !((who_next[x] >> (tok[x] & 31)) & 1u)) h[x] = z[x] = 0;
-                    part |= !dead[x] && !((h[x] == 128 && w[x] == 0) || z[x] == 128);
-                    any |= !dead[x] && (h[x] > w[x] || z[x] > 0);
+                    for (int x = 0; x < 2; ++x) listed[x] = (who_next[x] >> (tok[x] & 31)) & 1u;
+                    if (j + 1 < n) look(j + 1);
+                } else {
+                    masked = kt >= all_hi || (kMode == kWindow && kt < all_lo && kt >= all_sk);
                 }
-                if (kLists && j + 1 < n) look(j + 1);
-                const bool masked = __any_sync(0xffffffffu, part);
-                const bool visible = __any_sync(0xffffffffu, any);
-                const uint32_t pk = pos0 + ring_pos_k(j);
+                // bit 2 kk + e of vis[x]: row x sees this thread's column c0 + 8 kk + e
+                uint32_t vis[2] = {~0u, ~0u};
+                if (masked) {
+                    bool part = false, any = false;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        vis[x] = columns_below(hi[x] - kb - c0);
+                        if constexpr (kMode == kWindow)
+                            vis[x] = (vis[x] & ~columns_below(lo[x] - kb - c0)) | columns_below(sk[x] - kb - c0);
+                        if (kLists && !listed[x]) vis[x] = 0u;
+                        part |= !dead[x] && vis[x] != ~0u;
+                        any |= !dead[x] && vis[x] != 0u;
+                    }
+                    masked = __any_sync(0xffffffffu, part);
+                    visible = __any_sync(0xffffffffu, any);
+                }
+                const uint32_t pk = place_k(gb);
                 const bool wt = wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, status);
                 if (__any_sync(0xffffffffu, !wt || aborted(sh))) {
                     ok = false;
@@ -725,15 +818,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     if (masked) {
                         const uint32_t ninf = __float_as_uint(-INFINITY);
 #pragma unroll
-                        for (int kk = 0; kk < 16; ++kk)
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
+                            for (int kk = 0; kk < 16; ++kk)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int c = c0 + 8 * kk + e;
-                                    const bool see = (c < h[x] && c >= w[x]) || c < z[x];
-                                    sc[4 * kk + 2 * x + e] = see ? sc[4 * kk + 2 * x + e] : ninf;
-                                }
+                                for (int e = 0; e < 2; ++e)
+                                    sc[4 * kk + 2 * x + e] = (vis[x] >> (2 * kk + e)) & 1u ? sc[4 * kk + 2 * x + e] : ninf;
                     }
                 };
                 load_s();
@@ -742,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 tmem_st16x128_x16(t_base + sbuf, sc);
                 if (rescale) {
                     // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
-                    const uint32_t pv = pos0 + ring_pos_v(j - 1, n);
+                    const uint32_t pv = place_v(gb - 1u);
                     const bool wv = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
                     if (__any_sync(0xffffffffu, !wv)) {
                         ok = false;
@@ -757,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
             if (!ok) break;
             {
-                const uint32_t pv = pos0 + ring_pos_v(n - 1, n);
+                const uint32_t pv = place_v(gb0 + (uint32_t)n - 1u);
                 const bool wt = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
                 if (__any_sync(0xffffffffu, !wt)) {
                     ok = false;
@@ -772,15 +862,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(smem_u32(&sh->o_free));
-            if (sg.slot < 0) {
-                store_o_pairs<D>(o, la > 0.0f ? 1.0f / la : (la == 0.0f ? 0.0f : la), lb > 0.0f ? 1.0f / lb : (lb == 0.0f ? 0.0f : lb),
-                                 orow[0], orow[1]);
+            if (sg->slot < 0) {
+                // 1 / l; 0 for a row without a key, NaN where l is
+                const float inv_a = la == 0.0f ? 0.0f : 1.0f / la, inv_b = lb == 0.0f ? 0.0f : 1.0f / lb;
+                store_o_pairs<D>(o, inv_a, inv_b, dead[0] ? nullptr : P.o + out_row(0) * D,
+                                 dead[1] ? nullptr : P.o + out_row(1) * D);
                 if ((lane & 3) == 0) {
-                    if (!dead[0]) *lrow[0] = la == 0.0f ? -INFINITY : (m[0] + log2f(la)) * kLn2;
-                    if (!dead[1]) *lrow[1] = lb == 0.0f ? -INFINITY : (m[1] + log2f(lb)) * kLn2;
+                    if (!dead[0]) P.lse[out_row(0)] = la == 0.0f ? -INFINITY : (m[0] + log2f(la)) * kLn2;
+                    if (!dead[1]) P.lse[out_row(1)] = lb == 0.0f ? -INFINITY : (m[1] + log2f(lb)) * kLn2;
                 }
             } else {
-                const int64_t at = ((int64_t)blockIdx.x * 2 + sg.slot) * 128;
+                const int64_t at = ((int64_t)blockIdx.x * 2 + sg->slot) * 128;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (dead[x]) continue;
@@ -791,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     if ((lane & 3) == 0) P.part_ml[at + row[x]] = make_float2(m[x], x ? lb : la);
                 }
             }
-            pos0 += 2u * (uint32_t)n;
+            hand_back(k);
             gb0 += (uint32_t)n;
         }
         if (!ok && lane == 0) set_abort(sh, status);
@@ -810,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ Params P) {
+    wait_primary();
     const int4 jn = P.joins[blockIdx.x];
     const int32_t rows = jn.z * P.group;
     if (jn.x == 0) return;
@@ -858,6 +951,7 @@ __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_cons
     __shared__ uint32_t bits[kUnionWords];
     __shared__ int64_t part[33];
     __shared__ int32_t hit[2];
+    launch_dependents();
     int32_t t;
     const int32_t s = find_unit(
         P.b, blockIdx.x, [&](const PagedSeq& q) -> int64_t { return (q.nq + P.tpt - 1) / P.tpt; }, part, hit, t);
@@ -954,7 +1048,7 @@ Layout layout(const PagedForwardArgs& a) {
     return L;
 }
 
-template <int D, bool kLists>
+template <int D, int kMode>
 bsa_status launch_d(const Params& P, cudaStream_t stream) {
     const size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
     static int done[64] = {0};
@@ -963,16 +1057,30 @@ bsa_status launch_d(const Params& P, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return BSA_ERR_CUDA;
     if (!done[dev]) {
         if (cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(k_paged_forward<D, kLists>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaFuncSetAttribute(k_paged_forward<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
                 cudaSuccess)
             return BSA_ERR_CUDA;
         done[dev] = 1;
     }
     const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
-    k_paged_forward<D, kLists><<<grid, kThreads, smem, stream>>>(P);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-    k_paged_join<D><<<dim3(grid, 4), kJoinThreads, 0, stream>>>(P);
-    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    // a kernel that begins while the one before it in the stream ends (each waits for
+    // that one's results itself, see wait_primary)
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = kMode == kListed ? 1 : 0;  // (after k_paged_union)
+    if (cudaLaunchKernelEx(&cfg, k_paged_forward<D, kMode>, P) != cudaSuccess) return BSA_ERR_CUDA;
+    cfg.gridDim = dim3((unsigned)grid, 4);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_paged_join<D>, P) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1027,9 +1135,10 @@ bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int3
         UnionParams U{P.b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, L.tpt, a.causal, list, cnt, who, L.nt_cap, L.cap, L.words};
         k_paged_union<<<dim3((unsigned)L.nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream>>>(U);
         if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-        return D == 128 ? launch_d<128, true>(P, stream) : launch_d<64, true>(P, stream);
+        return D == 128 ? launch_d<128, kListed>(P, stream) : launch_d<64, kListed>(P, stream);
     }
-    return D == 128 ? launch_d<128, false>(P, stream) : launch_d<64, false>(P, stream);
+    if (a.window > 0) return D == 128 ? launch_d<128, kWindow>(P, stream) : launch_d<64, kWindow>(P, stream);
+    return D == 128 ? launch_d<128, kPlain>(P, stream) : launch_d<64, kPlain>(P, stream);
 }
 
 }  // namespace bsa

@@ -62,7 +62,7 @@ def test_sizes_that_every_call_rejects(lib, call):
     assert call(lib, H=129, H_kv=1) == INVALID                        # more than 128 heads to a tile row
     assert call(lib, H=70000, H_kv=70000) == INVALID
     assert call(lib, batch(seqs=-1)) == INVALID
-    assert call(lib, batch(seqs=32769)) == INVALID
+    assert call(lib, batch(seqs=16385)) == INVALID
     assert call(lib, batch(tokens=-1)) == INVALID
     assert call(lib, batch(tokens=(1 << 24) + 1)) == INVALID
     assert call(lib, batch(tokens=1 << 24), H=128, H_kv=128) == INVALID   # tokens * H
