@@ -138,9 +138,10 @@ struct PagedForwardArgs {
     void* o;
     float* lse;
 };
-// Thread blocks of the paged forward (its workspace holds two parts for each):
-// the 152 SMs of a GB300, one block each.
+// Thread blocks of the paged forward, one for each of a GB300's 152 SMs, and its
+// runs of work, up to four for each block (the workspace holds two parts of each).
 constexpr int kPagedBlocks = 152;
+constexpr int kPagedRuns = 4 * kPagedBlocks;
 // bsa_paged_attn.cu
 size_t paged_forward_workspace(const PagedForwardArgs& a);
 bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int32_t* status, cudaStream_t stream);

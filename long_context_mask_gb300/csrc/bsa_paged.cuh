@@ -12,8 +12,30 @@
 #include <stdint.h>
 
 #include "bsa_internal.h"
+#include "bsa_ptx.cuh"
 
 namespace bsa {
+
+// Every paged kernel is launched to begin while the kernel before it in the
+// stream ends, and waits for that one's results (ptx::wait_primary, in all
+// of its blocks and before it touches any tensor) once it has set itself up;
+// it lets the next one do the same from its first instruction on.  A decoding
+// step is a chain of four to seven short kernels, about 2 us apart otherwise.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                           const Args&... args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 struct PagedBatch {
     const int32_t* q_start;  // [seqs + 1]

@@ -19,7 +19,11 @@
 // Split.  All (key/value head, sequence, query tile, key tile) units are laid
 // out in that order and cut into equal runs, one for each of at most 152
 // thread blocks: long rows are split over many, short ones run several to a
-// block, and no host knowledge of the lengths is needed.  A row that a cut
+// block, and no host knowledge of the lengths is needed.  Where the cache is
+// read by many query tiles and is larger than L2, each block takes up to four
+// runs, a quarter of the units apart: at any time all blocks work on
+// neighbouring heads, whose keys and values stay in L2 (a chunk of 1024 tokens
+// over 65536, 268 MB: 1.8 GB of DRAM reads with one run each).  A row that a cut
 // splits leaves its parts (O, maximum, sum, all fp32) in the workspace;
 // k_paged_join adds them in key order, so a call's result does not depend on
 // timing.
@@ -87,8 +91,11 @@ struct Segment {
     int32_t j0;         // first of the tile's key tiles in this segment
     int32_t lo, ns;     // key tile of number j: j < ns ? j : lo + j - ns (without lists)
     int32_t list;       // with lists: row of the tile lists
-    int32_t slot;       // -1: the whole row is here; else the block's part slot (0 or 1)
+    int32_t slot;       // -1: the whole row is here; else its part slot: 2 run + 0 or 1
 };
+
+constexpr int kPhases = kPagedRuns / kPagedBlocks;     // runs of a thread block, at most
+constexpr int64_t kPhaseBytes = 64ll << 20;            // of keys and values that a run's heads may hold (half of L2)
 
 struct Shared {
     uint64_t full[16];
@@ -100,7 +107,7 @@ struct Shared {
     uint64_t seg_full[kDesc], seg_empty[kDesc];
     Segment seg[kDesc];
     int64_t part[33];
-    int32_t start[5];  // first unit: key/value head, sequence, query tile, unit; tile within the head
+    int32_t start[kPhases][5];  // of each run the first unit: key/value head, sequence, query tile, unit; tile within the head
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -120,9 +127,9 @@ struct Params {
     const uint32_t* list_who; // [H_kv * nt_cap, cap, words] bit t: token t of the query tile sees the key tile
     int32_t nt_cap, cap, words;
     // workspace of split rows
-    float* part_o;            // [blocks, 2, 128, D]
-    float2* part_ml;          // [blocks, 2, 128] maximum (log2) and sum
-    int4* joins;              // [blocks] parts (0: none), q0, ntok, kvh
+    float* part_o;            // [runs, 2, 128, D]
+    float2* part_ml;          // [runs, 2, 128] maximum (log2) and sum
+    int4* joins;              // [runs] parts (0: none), q0, ntok, kvh
 };
 
 __device__ __forceinline__ bool aborted(const Shared* sh) {
@@ -268,12 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         prefetch_tensormap(&P.map_q);
         prefetch_tensormap(&P.map_q1);
     }
+    launch_dependents();
+    wait_primary();
     if (threadIdx.x == 0) {
-        P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);  // (the producer writes it again where a row is split)
+        // (the producer writes them again where a row is split)
+#pragma unroll
+        for (int p = 0; p < kPhases; ++p) P.joins[p * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
         // a block of this launch (or an unread earlier one) timed out: abandon
         sh->abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
     }
-    launch_dependents();
 
     // ---------------------------------------------------------------- this block's run
     // of sequence s: the query tiles of the sequences before it, its new tokens and
@@ -281,26 +291,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     int32_t* cum = reinterpret_cast<int32_t*>(smem);
     int32_t* seq_nq = cum + P.b.seqs;
     int32_t* seq_kl = seq_nq + P.b.seqs;
-    int32_t nt;  // query tiles of one key/value head
+    int32_t nt;       // query tiles of one key/value head
+    int64_t kv_tiles;  // key tiles of one key/value head's cache
     {
         const int32_t per = (P.b.seqs + kThreads - 1) / kThreads;
         const int32_t a = min((int32_t)threadIdx.x * per, P.b.seqs), e = min(a + per, P.b.seqs);
+        // (both counts in one word: neither reaches 2^32)
         int64_t mine = 0, all;
         for (int32_t s = a; s < e; ++s) {
             PagedSeq q;
             if (!paged_seq(P.b, s, q) && blockIdx.x == 0) raise_status(status, BSA_ERR_BOUNDS);
             seq_nq[s] = q.nq;
             seq_kl[s] = q.kl;
-            mine += (q.nq + P.tpt - 1) / P.tpt;
+            mine += (q.nq + P.tpt - 1) / P.tpt + (q.nq > 0 ? (int64_t)((q.kl + 127) >> 7) << 32 : 0);
         }
-        int64_t at = block_prefix(mine, sh->part, all);
+        int64_t at = block_prefix(mine, sh->part, all) & 0xffffffff;
+        kv_tiles = all >> 32;
+        all &= 0xffffffff;
         for (int32_t s = a; s < e; ++s) {
             cum[s] = (int32_t)min(at, (int64_t)P.nt_cap);
             at += (seq_nq[s] + P.tpt - 1) / P.tpt;
         }
         nt = (int32_t)min(all, (int64_t)P.nt_cap);  // (beyond: only with starts that decrease, reported above)
     }
-    if constexpr (kLists) wait_primary();  // the lists are there
     __syncthreads();
     const int32_t rows = kLists ? nt * P.H_kv : nt;  // tiles whose counts differ
     const int32_t per_row = (rows + kThreads - 1) / kThreads;
@@ -347,24 +360,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     });
     const int64_t before = block_prefix(mine, sh->part, total);
     const int64_t units = kLists ? total : total * P.H_kv;
+    // runs: one for each thread block, or where key tiles are read several times and
+    // do not all stay in L2, several (of 16 units at least)
+    int32_t phases = 1;
+    const int64_t heads_tiles = kv_tiles * P.H_kv, kv_bytes = heads_tiles * (128 * D * 4);
+    if (kv_bytes > kPhaseBytes && units - (int64_t)kRowCost * nt * P.H_kv > 2 * heads_tiles)
+        phases = (int32_t)min(min((int64_t)kPhases, (kv_bytes + kPhaseBytes - 1) / kPhaseBytes),
+                              max(units / (16 * (int64_t)gridDim.x), (int64_t)1));
     const int32_t blocks = (int32_t)min((int64_t)gridDim.x, units);
     if ((int32_t)blockIdx.x >= blocks) return;
+    const int32_t runs = blocks * phases;
     // equal runs, the first `extra` of them one unit longer
-    const int64_t share = divide(units, blocks);
-    const int32_t extra = (int32_t)(units - share * blocks);
-    const int64_t u0 = share * blockIdx.x + min((int32_t)blockIdx.x, extra);
-    const int64_t u1 = u0 + share + ((int32_t)blockIdx.x < extra ? 1 : 0);
-    {
+    const int64_t share = divide(units, runs);
+    const int32_t extra = (int32_t)(units - share * runs);
+    auto run_start = [&](int32_t r) -> int64_t { return share * r + min(r, extra); };
+    for (int32_t p = 0; p < phases; ++p) {
+        const int64_t u0 = run_start(p * blocks + blockIdx.x);
         const int64_t head = kLists ? 0 : divide(u0, total), r = kLists ? u0 : u0 - head * total;
         if (r >= before && r < before + mine) {
             int64_t at = before;
             walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
                 if (r < at + n) {
-                    sh->start[0] = kLists ? kvh : (int32_t)head;
-                    sh->start[1] = s;
-                    sh->start[2] = t;
-                    sh->start[3] = (int32_t)(r - at);
-                    sh->start[4] = i;
+                    sh->start[p][0] = kLists ? kvh : (int32_t)head;
+                    sh->start[p][1] = s;
+                    sh->start[p][2] = t;
+                    sh->start[p][3] = (int32_t)(r - at);
+                    sh->start[p][4] = i;
                     return true;
                 }
                 at += n;
@@ -402,10 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
 
     if (warp == kProducer) {
         // ------------------------------------------------------------ segments and K/V tiles
-        int32_t kvh = sh->start[0], s = sh->start[1], t = sh->start[2], x0 = sh->start[3], i = sh->start[4];
-        int64_t left = u1 - u0, u = u0;
-        PagedSeq q;
-        paged_seq(P.b, s, q);
         const int32_t page = P.b.page, pieces = 128 / page;
         // a load is one page of one 64-column half, or of both where the page fills the tile
         const int32_t boxed = page == 128 ? C::kHalves : 1, halves = C::kHalves / boxed;
@@ -434,6 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             else ++g;
             return true;
         };
+        for (int32_t p = 0; p < phases && ok; ++p) {
+        const int32_t run = p * blocks + blockIdx.x;
+        int32_t kvh = sh->start[p][0], s = sh->start[p][1], t = sh->start[p][2], x0 = sh->start[p][3], i = sh->start[p][4];
+        int64_t u = run_start(run), left = run_start(run + 1) - u;
+        PagedSeq q;
+        paged_seq(P.b, s, q);
         while (left > 0 && ok) {
             const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
             Segment sg;
@@ -458,13 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             if (j1 <= j0) break;              // (only where it ends)
             sg.j0 = j0;
             sg.n = n_row == 0 ? 0 : j1 - j0;
-            sg.slot = j0 == 0 && j1 == n_eff ? -1 : (j0 == 0 ? 1 : 0);
+            sg.slot = j0 == 0 && j1 == n_eff ? -1 : 2 * run + (j0 == 0 ? 1 : 0);
             if (lane == 0 && last && j0 == 0) {
-                // a split row begins here; its last part is in the block of its last unit
+                // a split row begins here; its last part is in the run of its last unit
                 const int64_t end = u + (w - x0);
                 const int64_t longer = (share + 1) * extra;  // units of the longer runs
                 const int64_t c = end <= longer ? (end - 1) / (share + 1) : extra + (end - 1 - longer) / share;
-                P.joins[blockIdx.x] = make_int4((int32_t)(c - blockIdx.x + 1), sg.q0, ntok, kvh);
+                P.joins[run] = make_int4((int32_t)(c - run + 1), sg.q0, ntok, kvh);
             }
             if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
                 ok = false;
@@ -533,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     paged_seq(P.b, ++s, q);
                 }
             }
+        }
         }
         // the last V tiles
         while (gv < g && ok) {
@@ -872,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     if (!dead[1]) P.lse[out_row(1)] = lb == 0.0f ? -INFINITY : (m[1] + log2f(lb)) * kLn2;
                 }
             } else {
-                const int64_t at = ((int64_t)blockIdx.x * 2 + sg->slot) * 128;
+                const int64_t at = (int64_t)sg->slot * 128;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (dead[x]) continue;
@@ -897,33 +921,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
 
 // Joins the parts of split rows: O = sum_c 2^(m_c - M) O_c / l with M the
 // largest m_c and l = sum_c 2^(m_c - M) l_c, parts in key order.  Thread block
-// (c, y) takes rows 32 y .. 32 y + 31 of the row tile that begins in thread
-// block c of k_paged_forward: its slot 1, then slot 0 of the following blocks.
+// (c, y) takes rows y kJoinRows .. of the row tile that begins in each run p c of
+// k_paged_forward: the run's slot 1, then slot 0 of the following runs.
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ Params P) {
+    launch_dependents();
     wait_primary();
-    const int4 jn = P.joins[blockIdx.x];
-    const int32_t rows = jn.z * P.group;
-    if (jn.x == 0) return;
     constexpr int kLanes = D / 4;                       // threads of a row, four columns each
     constexpr int kRows = kJoinThreads / kLanes;
     const int c = threadIdx.x % kLanes;
-    for (int32_t r = blockIdx.y * 32 + threadIdx.x / kLanes; r < min(rows, (int32_t)blockIdx.y * 32 + 32); r += kRows) {
-        auto part = [&](int32_t x) -> int64_t { return (((int64_t)blockIdx.x + x) * 2 + (x == 0 ? 1 : 0)) * 128 + r; };
+    const int32_t r = blockIdx.y * kRows + threadIdx.x / kLanes;
+    for (int32_t p = 0; p < kPhases; ++p) {
+        const int32_t run = p * gridDim.x + blockIdx.x;
+        const int4 jn = P.joins[run];
+        if (jn.x == 0 || r >= jn.z * P.group) continue;
+        auto part = [&](int32_t x) -> int64_t { return (((int64_t)run + x) * 2 + (x == 0 ? 1 : 0)) * 128 + r; };
         float M = -INFINITY;
+#pragma unroll 4
         for (int32_t x = 0; x < jn.x; ++x) M = fmaxf(M, P.part_ml[part(x)].x);
         float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int32_t x = 0; x < jn.x; ++x) {
             const float2 ml = P.part_ml[part(x)];
             const float4 v = *reinterpret_cast<const float4*>(P.part_o + part(x) * D + 4 * c);
-            if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // no visible key in this part
+            // (none: no visible key in this part)
+            const bool none = ml.x == -INFINITY && ml.y == 0.0f;
             const float f = exp2f(ml.x - M);
-            l = fmaf(f, ml.y, l);
-            o[0] = fmaf(f, v.x, o[0]);
-            o[1] = fmaf(f, v.y, o[1]);
-            o[2] = fmaf(f, v.z, o[2]);
-            o[3] = fmaf(f, v.w, o[3]);
+            l = none ? l : fmaf(f, ml.y, l);
+            o[0] = none ? o[0] : fmaf(f, v.x, o[0]);
+            o[1] = none ? o[1] : fmaf(f, v.y, o[1]);
+            o[2] = none ? o[2] : fmaf(f, v.z, o[2]);
+            o[3] = none ? o[3] : fmaf(f, v.w, o[3]);
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at = (int64_t)(jn.y + r / P.group) * P.H + jn.w * P.group + r % P.group;
@@ -952,6 +981,7 @@ __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_cons
     __shared__ int64_t part[33];
     __shared__ int32_t hit[2];
     launch_dependents();
+    wait_primary();
     int32_t t;
     const int32_t s = find_unit(
         P.b, blockIdx.x, [&](const PagedSeq& q) -> int64_t { return (q.nq + P.tpt - 1) / P.tpt; }, part, hit, t);
@@ -1031,9 +1061,9 @@ Layout layout(const PagedForwardArgs& a) {
         at += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    L.joins = take(sizeof(int4) * kPagedBlocks);
-    L.ml = take(sizeof(float2) * kPagedBlocks * 2 * 128);
-    L.o = take(sizeof(float) * kPagedBlocks * 2 * 128 * (size_t)a.D);
+    L.joins = take(sizeof(int4) * kPagedRuns);
+    L.ml = take(sizeof(float2) * kPagedRuns * 2 * 128);
+    L.o = take(sizeof(float) * kPagedRuns * 2 * 128 * (size_t)a.D);
     if (a.sel_width > 0) {
         const int64_t blocks = ((int64_t)a.max_pages * a.page + 127) / 128;
         const int64_t most = (int64_t)L.tpt * a.sel_width;
@@ -1063,24 +1093,10 @@ bsa_status launch_d(const Params& P, cudaStream_t stream) {
         done[dev] = 1;
     }
     const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
-    // a kernel that begins while the one before it in the stream ends (each waits for
-    // that one's results itself, see wait_primary)
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = kMode == kListed ? 1 : 0;  // (after k_paged_union)
-    if (cudaLaunchKernelEx(&cfg, k_paged_forward<D, kMode>, P) != cudaSuccess) return BSA_ERR_CUDA;
-    cfg.gridDim = dim3((unsigned)grid, 4);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_join<D>, P) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    if (launch_chained(k_paged_forward<D, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P) != cudaSuccess ||
+        launch_chained(k_paged_join<D>, dim3((unsigned)grid, 128 / (kJoinThreads / (D / 4))), kJoinThreads, 0, stream, P) != cudaSuccess)
+        return BSA_ERR_CUDA;
+    return BSA_OK;
 }
 
 }  // namespace
@@ -1133,8 +1149,8 @@ bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int3
         P.list = list;
         P.list_who = who;
         UnionParams U{P.b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, L.tpt, a.causal, list, cnt, who, L.nt_cap, L.cap, L.words};
-        k_paged_union<<<dim3((unsigned)L.nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream>>>(U);
-        if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+        if (launch_chained(k_paged_union, dim3((unsigned)L.nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream, U) != cudaSuccess)
+            return BSA_ERR_CUDA;
         return D == 128 ? launch_d<128, kListed>(P, stream) : launch_d<64, kListed>(P, stream);
     }
     if (a.window > 0) return D == 128 ? launch_d<128, kWindow>(P, stream) : launch_d<64, kWindow>(P, stream);
