@@ -631,43 +631,74 @@ class PagedBatch(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
 
 
-def _token_rows(t, name, tokens, heads, D):
-    """Distance between the tokens of t [tokens, heads, D] bf16 in elements;
-    the heads of a token must be contiguous, the tokens need not be."""
+# A decoding step makes these calls for every layer and its kernels take a few
+# microseconds, so the host's share counts: sizes and types are compared in
+# place, and what fails goes to the helpers above for its message.
+
+def _where(ref, *ts):
+    """The device index of the call, all of whose tensors must be there."""
     import torch
-    _dtype(t, name, torch.bfloat16)
-    if tuple(t.shape) != (tokens, heads, D):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
-    return t.stride(0) if tokens > 1 else heads * D
-
-
-def _strided_ptr(t):
-    """The address of a tensor whose strides the call passes on."""
-    if not t.is_cuda:
+    dev = ref.device
+    for t in ts:
+        if t is not None and t.device != dev:
+            _same_device(ref, t)
+    if dev.type != "cuda":
         raise ValueError("expected a CUDA tensor")
+    if dev.index != torch.cuda.current_device():
+        _current_device(dev)
+    return dev.index
+
+
+def _array(t, name, dtype, n):
+    """The address of a contiguous array of `dtype` with at least n entries (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n:
+        _flat(t, name, n, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
 
 
-def _paged_cache(k_cache, v_cache):
+def _token_rows(t, name, tokens, heads, D):
+    """The address of t [tokens, heads, D] bf16 and the distance between its
+    tokens in elements; the heads of a token must be contiguous, the tokens
+    need not be."""
     import torch
-    _dtype(k_cache, "k_cache", torch.bfloat16)
-    _dtype(v_cache, "v_cache", torch.bfloat16)
+    if t.dtype is not torch.bfloat16:
+        _dtype(t, name, torch.bfloat16)
+    if t.shape != (tokens, heads, D):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
+    a, b, c = t.stride()
+    if c != 1 or (heads > 1 and b != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), a if tokens > 1 else heads * D
+
+
+def _paged_cache(k_cache, v_cache):
+    """(k's address, v's address, pages, H_kv, page_size, D)."""
+    import torch
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must share the shape [pages, H_kv, page_size, D]")
-    return k_cache.shape
+    return (_array(k_cache, "k_cache", torch.bfloat16, 0), _array(v_cache, "v_cache", torch.bfloat16, 0),
+            *k_cache.shape)
 
 
 def _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages):
     import torch
-    _dtype(page_table, "page_table", torch.int32)
     if page_table.dim() != 2:
         raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [seqs, max_pages]")
     seqs, max_pages = page_table.shape
-    _flat(q_start, "q_start", seqs + 1, torch.int32)
-    _flat(kv_len, "kv_len", seqs, torch.int32)
-    return PagedBatch(_ptr(page_table), _ptr(q_start), _ptr(kv_len), seqs, tokens, max_pages, page_size, n_pages)
+    return PagedBatch(_array(page_table, "page_table", torch.int32, 0), _array(q_start, "q_start", torch.int32, seqs + 1),
+                      _array(kv_len, "kv_len", torch.int32, seqs), seqs, tokens, max_pages, page_size, n_pages)
+
+
+def _block_lists(sel, sel_cnt, tokens, H_kv):
+    """(address of sel, of sel_cnt, width)."""
+    import torch
+    if sel.dim() != 3 or sel.shape[0] < tokens or sel.shape[1] != H_kv:
+        raise ValueError(f"sel: shape {tuple(sel.shape)}, expected [>= {tokens}, {H_kv}, width]")
+    return (_array(sel, "sel", torch.int32, 0), _array(sel_cnt, "sel_cnt", torch.int32, tokens * H_kv), sel.shape[2])
 
 
 def _scratch(need, workspace, device):
@@ -675,7 +706,14 @@ def _scratch(need, workspace, device):
     import torch
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _raw_stream(stream, device_index):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device_index) if stream is None else stream.cuda_stream
 
 
 def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None, q_out=None, rope=None,
@@ -687,32 +725,32 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
     rot] (cosines, then sines) on the way; k_mean [pages, H_kv, D] receives the
     mean key of every 128-token block that fills up (see bsa.h)."""
     import torch
-    n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+    bf16 = torch.bfloat16
+    kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
     tokens = k.shape[0]
-    ks, vs = _token_rows(k, "k", tokens, H_kv, D), _token_rows(v, "v", tokens, H_kv, D)
-    H, qs, os_ = H_kv, 0, 0
+    kp, ks = _token_rows(k, "k", tokens, H_kv, D)
+    vp, vs = _token_rows(v, "v", tokens, H_kv, D)
+    H, qp, qs, op, os_ = H_kv, None, 0, None, 0
     if q is not None:
         if q_out is None:
             raise ValueError("paged_append: pass q_out with q")
         H = q.shape[1]
-        qs, os_ = _token_rows(q, "q", tokens, H, D), _token_rows(q_out, "q_out", tokens, H, D)
+        qp, qs = _token_rows(q, "q", tokens, H, D)
+        op, os_ = _token_rows(q_out, "q_out", tokens, H, D)
     rope_len = rot = 0
     if rope is not None:
-        _dtype(rope, "rope", torch.float32)
         if rope.dim() != 2:
             raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, rot]")
         rope_len, rot = rope.shape
-    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        _flat(t, name, D, torch.bfloat16)
-    _flat(k_mean, "k_mean", n_pages * H_kv * D, torch.bfloat16)
-    _same_device(k_cache, v_cache, k, v, page_table, q_start, kv_len, q, q_out, rope, q_norm, k_norm, k_mean)
+    rp, qn, kn = _array(rope, "rope", torch.float32, 0), _array(q_norm, "q_norm", bf16, D), _array(k_norm, "k_norm", bf16, D)
+    km = _array(k_mean, "k_mean", bf16, n_pages * H_kv * D)
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    dev = _where(k_cache, v_cache, k, v, page_table, q_start, kv_len, q, q_out, rope, q_norm, k_norm, k_mean)
     code = load_library().bsa_paged_append(
-        ctypes.byref(b), _strided_ptr(q) if q is not None else None, qs, _strided_ptr(k), ks, _strided_ptr(v), vs,
-        H, H_kv, D, _ptr(rope), rope_len, rot, int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm), float(eps),
-        _strided_ptr(q_out) if q is not None else None, os_, _ptr(k_cache), _ptr(v_cache), _ptr(k_mean),
-        _stream(stream))
-    _check("bsa_paged_append", code)
+        ctypes.byref(b), qp, qs, kp, ks, vp, vs, H, H_kv, D, rp, rope_len, rot, 1 if interleaved else 0, qn, kn, eps,
+        op, os_, kc, vc, km, _raw_stream(stream, dev))
+    if code:
+        _check("bsa_paged_append", code)
 
 
 def forward_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
@@ -730,34 +768,29 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
     blocks (see bsa.h).  ``workspace`` is a CUDA tensor of at least
     forward_paged_workspace_size() bytes (allocated here when omitted)."""
     import torch
-    n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+    kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
-    tokens, H = q.shape[0], q.shape[1]
-    qs = _token_rows(q, "q", tokens, H, D)
-    _dtype(o, "o", torch.bfloat16)
+    tokens, H, _ = q.shape
+    qp, qs = _token_rows(q, "q", tokens, H, D)
     if o.shape != q.shape:
         raise ValueError("o must have q's shape [tokens, H, D]")
-    _flat(lse, "lse", tokens * H, torch.float32)
+    op, lp = _array(o, "o", torch.bfloat16, 0), _array(lse, "lse", torch.float32, tokens * H)
+    sp = cp = None
     width = 0
-    if (sel is None) != (sel_cnt is None):
-        raise ValueError("forward_paged: sel and sel_cnt go together")
-    if sel is not None:
-        _dtype(sel, "sel", torch.int32)
-        if sel.dim() != 3 or sel.shape[0] < tokens or sel.shape[1] != H_kv:
-            raise ValueError(f"sel: shape {tuple(sel.shape)}, expected [>= {tokens}, {H_kv}, width]")
-        width = sel.shape[2]
-        _flat(sel_cnt, "sel_cnt", tokens * H_kv, torch.int32)
-    _same_device(k_cache, v_cache, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, workspace)
-    lib = load_library()
+    if sel is not None or sel_cnt is not None:
+        if sel is None or sel_cnt is None:
+            raise ValueError("forward_paged: sel and sel_cnt go together")
+        sp, cp, width = _block_lists(sel, sel_cnt, tokens, H_kv)
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
-    need = lib.bsa_forward_paged_workspace_size(ctypes.byref(b), H, H_kv, D, width)
-    keep, ws, nbytes = _scratch(need, workspace, q.device)
-    code = lib.bsa_forward_paged(
-        ctypes.byref(b), _strided_ptr(q), qs, _ptr(k_cache), _ptr(v_cache), H, H_kv, D, int(bool(causal)),
-        int(window), int(sinks), _ptr(sel), _ptr(sel_cnt), width, float(scale), ws, nbytes, _ptr(o), _ptr(lse),
-        _stream(stream))
-    _check("bsa_forward_paged", code)
+    dev = _where(k_cache, v_cache, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, workspace)
+    lib = load_library()
+    ref = ctypes.byref(b)
+    keep, ws, nbytes = _scratch(lib.bsa_forward_paged_workspace_size(ref, H, H_kv, D, width), workspace, q.device)
+    code = lib.bsa_forward_paged(ref, qp, qs, kc, vc, H, H_kv, D, 1 if causal else 0, window, sinks, sp, cp, width,
+                                 scale, ws, nbytes, op, lp, _raw_stream(stream, dev))
+    if code:
+        _check("bsa_forward_paged", code)
 
 
 def select_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
@@ -771,27 +804,26 @@ def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_s
     """The 128-token blocks each new token and key/value head attends to: the
     first sink_blocks, the last local_blocks and the topk best of the others by
     the token's queries times k_mean [pages, H_kv, D].  Fills sel [tokens, H_kv,
-    width] (ascending, tail -1) and sel_cnt [tokens, H_kv] (see bsa.h)."""
+    width] (ascending, tail -1) and sel_cnt [tokens, H_kv] (see bsa.h).
+    ``workspace`` is a CUDA tensor of at least select_paged_workspace_size()
+    bytes (allocated here when omitted)."""
     import torch
-    _dtype(k_mean, "k_mean", torch.bfloat16)
     if k_mean.dim() != 3 or q.dim() != 3:
         raise ValueError("select_paged: q [tokens, H, D], k_mean [pages, H_kv, D]")
     n_pages, H_kv, D = k_mean.shape
-    tokens, H = q.shape[0], q.shape[1]
-    qs = _token_rows(q, "q", tokens, H, D)
-    _dtype(sel, "sel", torch.int32)
-    if sel.dim() != 3 or sel.shape[0] < tokens or sel.shape[1] != H_kv:
-        raise ValueError(f"sel: shape {tuple(sel.shape)}, expected [>= {tokens}, {H_kv}, width]")
-    _flat(sel_cnt, "sel_cnt", tokens * H_kv, torch.int32)
-    _same_device(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, workspace)
+    tokens, H, _ = q.shape
+    mp = _array(k_mean, "k_mean", torch.bfloat16, 0)
+    qp, qs = _token_rows(q, "q", tokens, H, D)
+    sp, cp, width = _block_lists(sel, sel_cnt, tokens, H_kv)
+    b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    dev = _where(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, workspace)
     lib = load_library()
-    b = _paged_batch(page_table, q_start, kv_len, tokens, int(page_size), n_pages)
-    need = lib.bsa_select_paged_workspace_size(ctypes.byref(b), H, H_kv, D)
-    keep, ws, nbytes = _scratch(need, workspace, q.device) if need or workspace is not None else (None, None, 0)
-    code = lib.bsa_select_paged(
-        ctypes.byref(b), _strided_ptr(q), qs, _ptr(k_mean), H, H_kv, D, int(topk), int(sink_blocks),
-        int(local_blocks), ws, nbytes, _ptr(sel), _ptr(sel_cnt), sel.shape[2], _stream(stream))
-    _check("bsa_select_paged", code)
+    ref = ctypes.byref(b)
+    keep, ws, nbytes = _scratch(lib.bsa_select_paged_workspace_size(ref, H, H_kv, D), workspace, q.device)
+    code = lib.bsa_select_paged(ref, qp, qs, mp, H, H_kv, D, topk, sink_blocks, local_blocks, ws, nbytes, sp, cp, width,
+                                _raw_stream(stream, dev))
+    if code:
+        _check("bsa_select_paged", code)
 
 
 def device_status(stream=None) -> int:
