@@ -28,16 +28,20 @@
 // k_paged_join adds them in key order, so a call's result does not depend on
 // timing.
 //
-// Warp roles (11 warps): 0 cuts the run into segments (one query tile's part
+// Warp roles (12 warps): 0 cuts the run into segments (one query tile's part
 // of the run), tells the others through a ring of descriptors and loads the
-// K/V tiles; 1 issues the MMAs; 2 .. 9 are the softmax (four threads a row,
-// see bsa_rows.cuh) and the epilogue; 10 loads the query tiles, so that K/V
-// loads of the next segment never wait for the last products on Q.
+// K/V tiles; 1 issues the products Q K^T, 11 the products P V; 2 .. 9 are the
+// softmax (four threads a row, see bsa_rows.cuh) and the epilogue; 10 loads the
+// query tiles, so that K/V loads of the next segment never wait for the last
+// products on Q.  Two issuing warps, because a warp that issues both spends as
+// long waiting and committing as the tensor core has work queued: with one, a
+// tile pair (1,112 cycles of tensor work) took 1,830 cycles, of which the
+// softmax waited 720 for scores.
 // Shared memory: the Q tile and a ring of K/V tiles.  Tensor memory: three
-// score buffers and O.  Tiles are numbered through the whole run: K_g is loaded
-// and Q K_g issued right after V_{g-3} and its product, across the borders of
-// segments, so that the next segment's scores are there when the softmax comes
-// to them.
+// score buffers and O.  Tiles are numbered through the whole run, across the
+// borders of segments: Q K_g is issued as soon as its score buffer is free (P V of
+// tile g - 3 has read it), so that the next segment's scores are there when the
+// softmax comes to them.
 //
 // Slots behind the end of a sequence hold anything, NaN included.  Their
 // scores are dropped by a select, and the value rows behind the end are
@@ -65,10 +69,10 @@ constexpr float kSumLimit = 18446744073709551616.0f;      // 2^64, see softmax_r
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 384;
-constexpr int kProducer = 0, kMma = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kQLoad = 10;
-constexpr int kThreads = 32 * 11;
+constexpr int kProducer = 0, kMmaQK = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kQLoad = 10, kMmaPV = 11;
+constexpr int kThreads = 32 * 12;
 constexpr int kDesc = 4;                                  // segment descriptors in flight
-constexpr int kConsumers = kSoftmaxWarps + 2;             // warps that read a descriptor
+constexpr int kConsumers = kSoftmaxWarps + 3;             // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 bf16
 
 template <int D>
@@ -154,9 +158,10 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 // Place of tile K_g (V_g) in the order of loads K_0, K_1, K_2, V_0, K_3, V_1, ..;
 // behind the run's last K tile every other place stays empty.  Ring slot: place %
 // stages.  The empty barrier of K_g's slot also tells the softmax that S_g is
-// there, V_g's that O holds P_g V_g (one commit for both): the barrier's next
-// completion needs a later P from that softmax, and who waits for PV_g has seen
-// S_{g+1} or S_g, so that PV_{g-3}, the completion before it, is known to be done.
+// there, V_g's tells it that O holds P_g V_g, and the issuer of Q K_{g+3} that the
+// score buffer is free (one commit for all): the barrier's next completion needs a
+// P of a later tile, which needs those who wait, and the one before it (PV_{g-3}) is
+// known to be done to who has seen S_g.
 __device__ __forceinline__ uint32_t place_k(uint32_t g) { return g < kSBuf ? g : 2u * g - 2u; }
 __device__ __forceinline__ uint32_t place_v(uint32_t g) { return 2u * g + 3u; }
 
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     const int lane = threadIdx.x & 31;
     int32_t* const status = P.b.status;
 
-    if (threadIdx.x == kThreads - 32) {
+    if (threadIdx.x == 32 * kQLoad) {
         for (uint32_t s = 0; s < S; ++s) {
             mbar_init(smem_u32(&sh->full[s]), 1);
             mbar_init(smem_u32(&sh->empty[s]), 1);
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         mbar_init(smem_u32(&sh->q_empty), 1);
         for (int s = 0; s < kSBuf; ++s) mbar_init(smem_u32(&sh->p_full[s]), 32 * kSoftmaxWarps);
         mbar_init(smem_u32(&sh->o_free), 32 * kSoftmaxWarps);
-        mbar_init(smem_u32(&sh->mma_done), 1);
+        mbar_init(smem_u32(&sh->mma_done), 2);
         for (int d = 0; d < kDesc; ++d) {
             mbar_init(smem_u32(&sh->seg_full[d]), 1);
             mbar_init(smem_u32(&sh->seg_empty[d]), kConsumers);
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         }
     }
     const bool abandoned = sh->abort != 0;
-    if (warp == kMma && !abandoned) {
+    if (warp == kMmaQK && !abandoned) {
         tmem_alloc(smem_u32(&sh->tmem_base), kTmemCols);
         tmem_relinquish();
     }
@@ -613,84 +618,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         if (lane == 0 && nq > 0 && !wait(smem_u32(&sh->q_full), (nq - 1u) & 1u, status))
             raise_status(status, BSA_ERR_TIMEOUT);
         __syncwarp();
-    } else if (warp == kMma) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp == kMmaQK) {
+        // ------------------------------------------------------------ S = Q K^T
+        // (the whole warp walks the schedule; one elected lane issues a tile's MMAs
+        // and their commit)
         const uint64_t dq = smem_desc_sw128(s_q, 16, 1024);
         const uint64_t dk = smem_desc_sw128(s_ring, 16, 1024);
-        const uint64_t dv = smem_desc_sw128(s_ring, kBox, 1024);
-        uint32_t g = 0, pv = 0, nq = 0, pv_segs = 0;  // QKs and PVs so far, query tiles, segments of the PVs
-        // of the last three tiles: value rows before the sequence's end, + 256 where
-        // the tile is its segment's first
-        int32_t f0 = 0, f1 = 0, f2 = 0;
+        uint32_t g = 0, nq = 0;
         bool ok = true;
-        // O += P_x V_x for the next tile x of the run
-        auto issue_pv = [&]() -> bool {
-            const uint32_t x = pv, pos = place_v(x), back = g - x;
-            const int32_t f = back == 3 ? f0 : (back == 2 ? f1 : f2);
-            if (!wait_warp(smem_u32(&sh->p_full[x % kSBuf]), (x / kSBuf) & 1u, status)) return false;
-            const bool first = (f & 256) != 0;
-            if (first) {
-                // it overwrites O: the previous segment's epilogue must have read it
-                if (pv_segs > 0 && !wait_warp(smem_u32(&sh->o_free), (pv_segs - 1u) & 1u, status)) return false;
-                ++pv_segs;
-            }
-            const uint32_t slot = pos % S;
-            if (!wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status)) return false;
-            const int32_t tail = f & 255;
-            if (tail < 128) {
-                // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
-                const uint32_t tile = s_ring + slot * C::kTile;
-                for (int32_t y = tail * 8 + lane; y < 128 * 8; y += 32)
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + h * kBox + y * 16), "r"(0)
-                                     : "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            tc_fence_after();
-            const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
-            const uint32_t p_col = (x % kSBuf) * 128u;
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + kColO, tmem + p_col + kk * 8, vs + (uint64_t)(kk * 2048 >> 4), C::kIdescPV,
-                           (!first || kk > 0) ? 1u : 0u);
-                mma_commit(smem_u32(&sh->empty[slot]));
-            }
-            __syncwarp();
-            ++pv;
-            return true;
-        };
         for (uint32_t k = 0; ok; ++k) {
             const Segment* sp = next_segment(k, ok);
             if (sp == nullptr) break;
             const int32_t n = sp->n;
-            int32_t tail = 128;
-            if (n > 0) {
-                // the segment's last tile may hold the sequence's end: value rows behind it are zeroed
-                const int32_t x = sp->j0 + n - 1;
-                int32_t kt;
-                if constexpr (kLists) kt = P.list[(int64_t)sp->list * P.cap + x];
-                else kt = x < sp->ns ? x : sp->lo + x - sp->ns;
-                tail = min(sp->kl - kt * 128, 128);
-            }
             hand_back(k);
+            if (n == 0) continue;
+            ok = wait_warp(smem_u32(&sh->q_full), nq++ & 1u, status);
             for (int32_t j = 0; j < n && ok; ++j, ++g) {
-                // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
-                if (pv + kSBuf == g) ok = issue_pv();
-                if (j == 0 && ok) {
-                    // while the query tile is on its way, the products of the segment before
-                    const uint64_t t0 = globaltimer();
-                    while (!__all_sync(0xffffffffu, mbar_test(smem_u32(&sh->q_full), nq & 1u))) {
-                        if (pv < g && __all_sync(0xffffffffu, mbar_test(smem_u32(&sh->p_full[pv % kSBuf]), (pv / kSBuf) & 1u)))
-                            ok = issue_pv();
-                        if (__any_sync(0xffffffffu, !ok || aborted(sh) || globaltimer() - t0 > kWaitNs)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    ++nq;
+                if (g >= kSBuf) {
+                    // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
+                    const uint32_t pv = place_v(g - kSBuf);
+                    ok = wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
                 }
                 const uint32_t pos = place_k(g), slot = pos % S;
                 ok = ok && wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
@@ -708,14 +655,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     if (j == n - 1) mma_commit(smem_u32(&sh->q_empty));
                 }
                 __syncwarp();
-                f0 = f1;
-                f1 = f2;
-                f2 = (j == n - 1 ? tail : 128) + (j == 0 ? 256 : 0);
             }
         }
-        while (pv < g && ok) ok = issue_pv();
         if (!ok && lane == 0) set_abort(sh, status);
         // nothing of ours may still be running when TMEM is freed
+        if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
+        __syncwarp();
+        if (!wait(smem_u32(&sh->mma_done), 0, status) && lane == 0) raise_status(status, BSA_ERR_TIMEOUT);
+        __syncwarp();
+    } else if (warp == kMmaPV) {
+        // ------------------------------------------------------------ O += P V
+        const uint64_t dv = smem_desc_sw128(s_ring, kBox, 1024);
+        uint32_t g = 0, segs = 0;
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const int32_t n = sp->n;
+            int32_t tail = 128;
+            if (n > 0) {
+                // the segment's last tile may hold the sequence's end: value rows behind it are zeroed
+                const int32_t x = sp->j0 + n - 1;
+                int32_t kt;
+                if constexpr (kLists) kt = P.list[(int64_t)sp->list * P.cap + x];
+                else kt = x < sp->ns ? x : sp->lo + x - sp->ns;
+                tail = min(sp->kl - kt * 128, 128);
+            }
+            hand_back(k);
+            if (n == 0) continue;
+            for (int32_t j = 0; j < n && ok; ++j, ++g) {
+                const uint32_t pos = place_v(g), slot = pos % S;
+                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
+                if (ok && j == n - 1 && tail < 128) {
+                    // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
+                    const uint32_t tile = s_ring + slot * C::kTile;
+                    for (int32_t y = tail * 8 + lane; y < 128 * 8; y += 32)
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + h * kBox + y * 16), "r"(0)
+                                         : "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                ok = ok && wait_warp(smem_u32(&sh->p_full[g % kSBuf]), (g / kSBuf) & 1u, status);
+                // a segment's first product overwrites O: the epilogue before must have read it
+                if (ok && j == 0 && segs > 0) ok = wait_warp(smem_u32(&sh->o_free), (segs - 1u) & 1u, status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
+                const uint32_t p_col = (g % kSBuf) * 128u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + kColO, tmem + p_col + kk * 8, vs + (uint64_t)(kk * 2048 >> 4), C::kIdescPV,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(smem_u32(&sh->empty[slot]));
+                }
+                __syncwarp();
+            }
+            ++segs;
+        }
+        if (!ok && lane == 0) set_abort(sh, status);
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
         __syncwarp();
         if (!wait(smem_u32(&sh->mma_done), 0, status) && lane == 0) raise_status(status, BSA_ERR_TIMEOUT);
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaQK) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the parts of split rows: O = sum_c 2^(m_c - M) O_c / l with M the
