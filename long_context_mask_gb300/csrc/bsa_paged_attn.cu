@@ -28,11 +28,13 @@
 // k_paged_join adds them in key order, so a call's result does not depend on
 // timing.
 //
-// Warp roles (12 warps): 0 cuts the run into segments (one query tile's part
-// of the run), tells the others through a ring of descriptors and loads the
-// K/V tiles; 1 issues the products Q K^T, 11 the products P V; 2 .. 9 are the
+// Warp roles (13 warps): 0 cuts the run into segments (one query tile's part
+// of the run), tells the others through a ring of descriptors and loads the K
+// tiles, 12 the V tiles (pages of 16 tokens are up to 16 copies a tile; with one
+// warp for both, each copy by a lane of its own, a pair took 2,000 cycles to
+// issue); 1 issues the products Q K^T, 11 the products P V; 2 .. 9 are the
 // softmax (four threads a row, see bsa_rows.cuh) and the epilogue; 10 loads the
-// query tiles, so that K/V loads of the next segment never wait for the last
+// query tiles, so that loads of the next segment's keys never wait for the last
 // products on Q.  Two issuing warps, because a warp that issues both spends as
 // long waiting and committing as the tensor core has work queued: with one, a
 // tile pair (1,112 cycles of tensor work) took 1,830 cycles, of which the
@@ -69,10 +71,10 @@ constexpr float kSumLimit = 18446744073709551616.0f;      // 2^64, see softmax_r
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 384;
-constexpr int kProducer = 0, kMmaQK = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kQLoad = 10, kMmaPV = 11;
-constexpr int kThreads = 32 * 12;
+constexpr int kProducer = 0, kMmaQK = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kQLoad = 10, kMmaPV = 11, kVLoad = 12;
+constexpr int kThreads = 32 * 13;
 constexpr int kDesc = 4;                                  // segment descriptors in flight
-constexpr int kConsumers = kSoftmaxWarps + 3;             // warps that read a descriptor
+constexpr int kConsumers = kSoftmaxWarps + 4;             // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 bf16
 
 template <int D>
@@ -116,6 +118,11 @@ struct Shared {
     int32_t abort;
 };
 
+template <int n>
+struct Pages {
+    static constexpr int value = n;
+};
+
 struct Params {
     CUtensorMap map_q, map_q1;  // (D, H, tokens): box 64 x G x (128 / G), 64 x G x 1
     CUtensorMap map_k, map_v;   // (64, slots, D / 64): box 64 x page x boxed halves
@@ -146,6 +153,10 @@ __device__ __forceinline__ void set_abort(Shared* sh, int32_t* status) {
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int32_t* status) {
     return mbar_wait(bar, parity, kWaitNs, status, BSA_ERR_TIMEOUT);
 }
+// For copies and products in flight, after a failure too.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int32_t* status) {
+    if (!mbar_wait(bar, parity, kWaitNs, status, -1)) raise_status(status, BSA_ERR_TIMEOUT);
+}
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* status) {
     return __all_sync(0xffffffffu, wait(bar, parity, status));
 }
@@ -155,15 +166,15 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
     return (a >> 32) == 0 && (b >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Place of tile K_g (V_g) in the order of loads K_0, K_1, K_2, V_0, K_3, V_1, ..;
-// behind the run's last K tile every other place stays empty.  Ring slot: place %
-// stages.  The empty barrier of K_g's slot also tells the softmax that S_g is
-// there, V_g's tells it that O holds P_g V_g, and the issuer of Q K_{g+3} that the
-// score buffer is free (one commit for all): the barrier's next completion needs a
-// P of a later tile, which needs those who wait, and the one before it (PV_{g-3}) is
-// known to be done to who has seen S_g.
-__device__ __forceinline__ uint32_t place_k(uint32_t g) { return g < kSBuf ? g : 2u * g - 2u; }
-__device__ __forceinline__ uint32_t place_v(uint32_t g) { return 2u * g + 3u; }
+// Tile K_g (V_g) of the run is use place / stages of ring slot place % stages: K
+// tiles have the even slots, V tiles the odd ones.  The empty barrier of K_g's slot
+// also tells the softmax that S_g is there, V_g's tells it that O holds P_g V_g, and
+// the issuer of Q K_{g+3} that the score buffer is free (one commit for all).  Its
+// next completion needs the P of a later tile, for which those who wait must come
+// first, and the one before it (of tile g - stages / 2, at most g - 3) is known to be
+// done to who has seen S_g.
+__device__ __forceinline__ uint32_t place_k(uint32_t g) { return 2u * g; }
+__device__ __forceinline__ uint32_t place_v(uint32_t g) { return 2u * g + 1u; }
 
 // Key tiles that the tokens at positions pos0 .. pos0 + ntok - 1 see some key
 // of: the sink tiles 0 .. ns - 1 and lo .. lo + (n - ns) - 1.
@@ -426,36 +437,75 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         if (lane == 0) mbar_arrive(smem_u32(&sh->seg_empty[k % kDesc]));
     };
 
-    if (warp == kProducer) {
-        // ------------------------------------------------------------ segments and K/V tiles
-        const int32_t page = P.b.page, pieces = 128 / page;
-        // a load is one page of one 64-column half, or of both where the page fills the tile
-        const int32_t boxed = page == 128 ? C::kHalves : 1, halves = C::kHalves / boxed;
-        const int32_t n_loads = pieces * halves;
-        const int32_t my_piece = lane / halves, my_half = lane % halves;
-        const uint32_t my_dst = (uint32_t)(my_half * kBox + my_piece * page * 128);
-        const uint32_t piece_bytes = (uint32_t)(page * D * 2);
-        const int32_t per_window = 32 / pieces;  // key tiles whose pages one 32-lane read brings
-        uint32_t k = 0;
-        uint32_t g = 0, gv = 0;            // K and V tiles so far
-        int32_t r0 = -1, r1 = -1, r2 = -1;  // this lane's slot rows of the last three K tiles
-        bool ok = true;
-        // one tile: this lane's slot row (-1: no page there)
-        auto load = [&](int32_t row, bool is_v) -> bool {
-            const uint32_t pos = is_v ? place_v(gv) : place_k(g);
-            const uint32_t slot = pos % S;
-            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, status) || aborted(sh)) return false;
-            const uint32_t fb = smem_u32(&sh->full[slot]);
-            const bool go = lane < n_loads && row >= 0;
-            const uint32_t mask = __ballot_sync(0xffffffffu, go);
-            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(__popc(mask) / halves) * piece_bytes);
-            __syncwarp();
-            if (go) tma_load_3d(s_ring + slot * C::kTile + my_dst, is_v ? &P.map_v : &P.map_k, 0, row, my_half, fb);
-            __syncwarp();
-            if (is_v) ++gv;
-            else ++g;
-            return true;
+    // The K (V) tiles of a segment, whose numbers in the run begin at g.  A tile is N
+    // pages, each one copy of either 64-column half, or one of both where the page
+    // fills the tile; the elected lane issues them back to back.
+    auto load_pages = [&](auto pages, const Segment& sg, bool is_v, uint32_t& g) -> bool {
+        constexpr int N = decltype(pages)::value, page = 128 / N;
+        constexpr int per_window = 32 / N;  // key tiles whose pages one 32-lane read brings
+        const int32_t n = sg.n, kl = sg.kl, kvh = sg.kvh;
+        const int32_t* table = P.b.table + (int64_t)sg.seq * P.b.max_pages;
+        const CUtensorMap* map = is_v ? &P.map_v : &P.map_k;
+        // lane l of a window: the cache row of page l % N of key tile w0 + l / N (-1: behind
+        // the sequence's end)
+        auto fetch = [&](int32_t w0) -> int32_t {
+            const int32_t j = w0 + lane / N;
+            if (j >= n) return -1;
+            int32_t kt;
+            if constexpr (kLists) kt = P.list[(int64_t)sg.list * P.cap + sg.j0 + j];
+            else kt = sg.j0 + j < sg.ns ? sg.j0 + j : sg.lo + sg.j0 + j - sg.ns;
+            const int32_t pg = kt * N + lane % N;
+            if (pg * page >= kl) return -1;
+            int32_t id = table[pg];
+            if (id < 0 || id >= P.b.n_pages) {
+                raise_status(status, BSA_ERR_BOUNDS);
+                id = 0;  // keeps the pipeline in step; this row's result is unspecified
+            }
+            return (id * P.H_kv + kvh) * page;
         };
+        int32_t w0 = 0, cur = fetch(0), nxt = fetch(per_window);
+        for (int32_t j = 0; j < n; ++j, ++g) {
+            if (j >= w0 + per_window) {
+                w0 += per_window;
+                cur = nxt;
+                nxt = fetch(w0 + per_window);
+            }
+            int32_t row[N], held = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                row[i] = __shfl_sync(0xffffffffu, cur, (j - w0) * N + i);
+                held += row[i] >= 0;
+            }
+            const uint32_t pos = is_v ? place_v(g) : place_k(g), slot = pos % S;
+            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, status)) return false;
+            if (elect_one()) {
+                const uint32_t fb = smem_u32(&sh->full[slot]), dst = s_ring + slot * C::kTile;
+                mbar_arrive_expect_tx(fb, (uint32_t)(held * page * D * 2));
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (row[i] >= 0) {
+#pragma unroll
+                        for (int h = 0; h < (N == 1 ? 1 : C::kHalves); ++h)
+                            tma_load_3d(dst + h * kBox + i * page * 128, map, 0, row[i], h, fb);
+                    }
+            }
+            __syncwarp();
+        }
+        return true;
+    };
+    auto load_tiles = [&](const Segment& sg, bool is_v, uint32_t& g) -> bool {
+        switch (P.b.page) {
+            case 128: return load_pages(Pages<1>{}, sg, is_v, g);
+            case 64: return load_pages(Pages<2>{}, sg, is_v, g);
+            case 32: return load_pages(Pages<4>{}, sg, is_v, g);
+            default: return load_pages(Pages<8>{}, sg, is_v, g);
+        }
+    };
+
+    if (warp == kProducer) {
+        // ------------------------------------------------------------ segments and K tiles
+        uint32_t k = 0, g = 0;  // segments and tiles so far
+        bool ok = true;
         for (int32_t p = 0; p < phases && ok; ++p) {
         const int32_t run = p * blocks + blockIdx.x;
         int32_t kvh = sh->start[p][0], s = sh->start[p][1], t = sh->start[p][2], x0 = sh->start[p][3], i = sh->start[p][4];
@@ -509,42 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
             __syncwarp();
             ++k;
-            const int32_t n = sg.n;
-            const int32_t* list = kLists ? P.list + (int64_t)sg.list * P.cap + j0 : nullptr;
-            auto tile_of = [&](int32_t j) -> int32_t {
-                if constexpr (kLists) return list[j];
-                const int32_t x = j0 + j;
-                return x < sg.ns ? x : sg.lo + x - sg.ns;
-            };
-            const int32_t* table = P.b.table + (int64_t)s * P.b.max_pages;
-            // lane l of a window: the slot row of piece l % pieces of key tile w0 + l / pieces
-            // (-1: behind the sequence's end)
-            auto fetch = [&](int32_t w0) -> int32_t {
-                const int32_t j = w0 + lane / pieces, pc = lane % pieces;
-                if (j >= n) return -1;
-                const int32_t pg = tile_of(j) * pieces + pc;
-                if (pg * page >= q.kl) return -1;
-                int32_t id = table[pg];
-                if (id < 0 || id >= P.b.n_pages) {
-                    raise_status(status, BSA_ERR_BOUNDS);
-                    id = 0;  // keeps the pipeline in step; this row's result is unspecified
-                }
-                return (id * P.H_kv + kvh) * page;
-            };
-            int32_t w0 = 0, cur = fetch(0), nxt = fetch(per_window);
-            for (int32_t j = 0; j < n && ok; ++j) {
-                if (j >= w0 + per_window) {
-                    w0 += per_window;
-                    cur = nxt;
-                    nxt = fetch(w0 + per_window);
-                }
-                const int32_t row = __shfl_sync(0xffffffffu, cur, (j - w0) * pieces + my_piece);
-                if (g >= kSBuf) ok = load(r0, true);   // V_{g-3}
-                ok = ok && load(row, false);           // K_g
-                r0 = r1;
-                r1 = r2;
-                r2 = row;
-            }
+            ok = load_tiles(sg, false, g);
             // on to the next query tile
             left -= w - x0;
             u += w - x0;
@@ -563,11 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
         }
         }
-        // the last V tiles
-        while (gv < g && ok) {
-            const uint32_t back = g - gv;
-            ok = load(back == 3 ? r0 : (back == 2 ? r1 : r2), true);
-        }
         if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
             if (lane == 0) {
                 sh->seg[k % kDesc].n = -1;
@@ -578,15 +588,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         }
         if (!ok && lane == 0) set_abort(sh, status);
         // every issued copy must land before the block exits
-        if (lane == 0) {
-            // (the last copy of each slot; earlier ones were used up before it)
-            const uint32_t end = max(g > 0 ? place_k(g - 1) : 0u, gv > 0 ? place_v(gv - 1) : 0u);
-            for (uint32_t x = end >= S ? end - S + 1 : 0; x <= end; ++x) {
-                const bool is_k = x < kSBuf || (x & 1u) == 0;
-                const bool used = is_k ? (x < kSBuf ? x < g : (x + 2u) / 2u < g) : (x - 3u) / 2u < gv;
-                if (used && !wait(smem_u32(&sh->full[x % S]), (x / S) & 1u, status)) raise_status(status, BSA_ERR_TIMEOUT);
-            }
+        if (lane == 0)
+            for (uint32_t x = g > S / 2 ? g - S / 2 : 0; x < g; ++x)
+                drain(smem_u32(&sh->full[place_k(x) % S]), (place_k(x) / S) & 1u, status);
+        __syncwarp();
+    } else if (warp == kVLoad) {
+        // ------------------------------------------------------------ V tiles
+        uint32_t g = 0;
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const Segment sg = *sp;
+            hand_back(k);
+            ok = load_tiles(sg, true, g);
         }
+        if (!ok && lane == 0) set_abort(sh, status);
+        if (lane == 0)
+            for (uint32_t x = g > S / 2 ? g - S / 2 : 0; x < g; ++x)
+                drain(smem_u32(&sh->full[place_v(x) % S]), (place_v(x) / S) & 1u, status);
         __syncwarp();
     } else if (warp == kQLoad) {
         // ------------------------------------------------------------ query tiles
@@ -615,8 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             hand_back(k);
         }
         if (!ok && lane == 0) set_abort(sh, status);
-        if (lane == 0 && nq > 0 && !wait(smem_u32(&sh->q_full), (nq - 1u) & 1u, status))
-            raise_status(status, BSA_ERR_TIMEOUT);
+        if (lane == 0 && nq > 0) drain(smem_u32(&sh->q_full), (nq - 1u) & 1u, status);
         __syncwarp();
     } else if (warp == kMmaQK) {
         // ------------------------------------------------------------ S = Q K^T
@@ -661,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         // nothing of ours may still be running when TMEM is freed
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
         __syncwarp();
-        if (!wait(smem_u32(&sh->mma_done), 0, status) && lane == 0) raise_status(status, BSA_ERR_TIMEOUT);
+        drain(smem_u32(&sh->mma_done), 0, status);
         __syncwarp();
     } else if (warp == kMmaPV) {
         // ------------------------------------------------------------ O += P V
@@ -718,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         if (!ok && lane == 0) set_abort(sh, status);
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
         __syncwarp();
-        if (!wait(smem_u32(&sh->mma_done), 0, status) && lane == 0) raise_status(status, BSA_ERR_TIMEOUT);
+        drain(smem_u32(&sh->mma_done), 0, status);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
