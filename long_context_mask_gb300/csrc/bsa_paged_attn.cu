@@ -28,17 +28,17 @@
 // k_paged_join adds them in key order, so a call's result does not depend on
 // timing.
 //
-// Warp roles (13 warps): 0 cuts the run into segments (one query tile's part
+// Warp roles (16 warps): 0 cuts the run into segments (one query tile's part
 // of the run), tells the others through a ring of descriptors and loads the K
-// tiles, 12 the V tiles (pages of 16 tokens are up to 16 copies a tile; with one
+// tiles, 11 the V tiles (pages of 16 tokens are up to 16 copies a tile; with one
 // warp for both, each copy by a lane of its own, a pair took 2,000 cycles to
-// issue); 1 issues the products Q K^T, 11 the products P V; 2 .. 9 are the
-// softmax (four threads a row, see bsa_rows.cuh) and the epilogue; 10 loads the
-// query tiles, so that loads of the next segment's keys never wait for the last
-// products on Q.  Two issuing warps, because a warp that issues both spends as
-// long waiting and committing as the tensor core has work queued: with one, a
-// tile pair (1,112 cycles of tensor work) took 1,830 cycles, of which the
-// softmax waited 720 for scores.
+// issue); 1 loads the query tiles and issues the products Q K^T, 10 the products
+// P V (a warp that issues both spends as long waiting and committing as the
+// tensor core has work queued: with one, a tile pair, 1,112 cycles of tensor
+// work, took 1,830 cycles, of which the softmax waited 720 for scores); 2 .. 9
+// are the softmax (four threads a row, see bsa_rows.cuh); 12 .. 15 normalise and
+// store a segment's rows while the softmax is at the next one (it lost about
+// 5,000 cycles a segment to that).
 // Shared memory: the Q tile and a ring of K/V tiles.  Tensor memory: three
 // score buffers and O.  Tiles are numbered through the whole run, across the
 // borders of segments: Q K_g is issued as soon as its score buffer is free (P V of
@@ -71,10 +71,11 @@ constexpr float kSumLimit = 18446744073709551616.0f;      // 2^64, see softmax_r
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 384;
-constexpr int kProducer = 0, kMmaQK = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kQLoad = 10, kMmaPV = 11, kVLoad = 12;
-constexpr int kThreads = 32 * 13;
+constexpr int kProducer = 0, kMmaQK = 1, kSoftmax0 = 2, kSoftmaxWarps = 8, kMmaPV = 10, kVLoad = 11;
+constexpr int kStore0 = 12, kStoreWarps = 4;
+constexpr int kThreads = 32 * 16;
 constexpr int kDesc = 4;                                  // segment descriptors in flight
-constexpr int kConsumers = kSoftmaxWarps + 4;             // warps that read a descriptor
+constexpr int kConsumers = kSoftmaxWarps + kStoreWarps + 3;  // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 bf16
 
 template <int D>
@@ -109,10 +110,11 @@ struct Shared {
     uint64_t q_full, q_empty;
     uint64_t p_full[kSBuf];   // P_g has been written (and O rescaled)
     uint64_t o_free;          // the segment's O has been read
+    uint64_t ml_full, ml_empty;  // a segment's maxima and sums are in ml, have been read
     uint64_t mma_done;
     uint64_t seg_full[kDesc], seg_empty[kDesc];
     Segment seg[kDesc];
-    int64_t part[33];
+    float2 ml[128];           // of a segment's rows: maximum (log2) and sum (before: block_prefix's words)
     int32_t start[kPhases][5];  // of each run the first unit: key/value head, sequence, query tile, unit; tile within the head
     uint32_t tmem_base;
     int32_t abort;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     const int lane = threadIdx.x & 31;
     int32_t* const status = P.b.status;
 
-    if (threadIdx.x == 32 * kQLoad) {
+    if (threadIdx.x == 32 * kStore0) {
         for (uint32_t s = 0; s < S; ++s) {
             mbar_init(smem_u32(&sh->full[s]), 1);
             mbar_init(smem_u32(&sh->empty[s]), 1);
@@ -279,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         mbar_init(smem_u32(&sh->q_full), 1);
         mbar_init(smem_u32(&sh->q_empty), 1);
         for (int s = 0; s < kSBuf; ++s) mbar_init(smem_u32(&sh->p_full[s]), 32 * kSoftmaxWarps);
-        mbar_init(smem_u32(&sh->o_free), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->o_free), 32 * kStoreWarps);
+        mbar_init(smem_u32(&sh->ml_full), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh->ml_empty), 32 * kStoreWarps);
         mbar_init(smem_u32(&sh->mma_done), 2);
         for (int d = 0; d < kDesc; ++d) {
             mbar_init(smem_u32(&sh->seg_full[d]), 1);
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             seq_kl[s] = q.kl;
             mine += (q.nq + P.tpt - 1) / P.tpt + (q.nq > 0 ? (int64_t)((q.kl + 127) >> 7) << 32 : 0);
         }
-        int64_t at = block_prefix(mine, sh->part, all) & 0xffffffff;
+        int64_t at = block_prefix(mine, reinterpret_cast<int64_t*>(sh->ml), all) & 0xffffffff;
         kv_tiles = all >> 32;
         all &= 0xffffffff;
         for (int32_t s = a; s < e; ++s) {
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         mine += n;
         return false;
     });
-    const int64_t before = block_prefix(mine, sh->part, total);
+    const int64_t before = block_prefix(mine, reinterpret_cast<int64_t*>(sh->ml), total);
     const int64_t units = kLists ? total : total * P.H_kv;
     // runs: one for each thread block, or where key tiles are read several times and
     // do not all stay in L2, several (of 16 units at least)
@@ -608,37 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             for (uint32_t x = g > S / 2 ? g - S / 2 : 0; x < g; ++x)
                 drain(smem_u32(&sh->full[place_v(x) % S]), (place_v(x) / S) & 1u, status);
         __syncwarp();
-    } else if (warp == kQLoad) {
-        // ------------------------------------------------------------ query tiles
-        uint32_t nq = 0;
-        bool ok = true;
-        for (uint32_t k = 0;; ++k) {
-            const Segment* sg = next_segment(k, ok);
-            if (sg == nullptr) break;
-            if (sg->n > 0) {
-                if (nq > 0 && !wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, status)) {
-                    ok = false;
-                    break;
-                }
-                if (aborted(sh)) break;
-                if (lane == 0) {
-                    const bool one = sg->ntok == 1;
-                    const uint32_t bar = smem_u32(&sh->q_full);
-                    mbar_arrive_expect_tx(bar, (uint32_t)((one ? 1 : P.tpt) * P.group * D * 2));
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, sg->kvh * P.group, sg->q0, bar);
-                }
-                __syncwarp();
-                ++nq;
-            }
-            hand_back(k);
-        }
-        if (!ok && lane == 0) set_abort(sh, status);
-        if (lane == 0 && nq > 0) drain(smem_u32(&sh->q_full), (nq - 1u) & 1u, status);
-        __syncwarp();
     } else if (warp == kMmaQK) {
-        // ------------------------------------------------------------ S = Q K^T
+        // ------------------------------------------------------------ query tiles, S = Q K^T
         // (the whole warp walks the schedule; one elected lane issues a tile's MMAs
         // and their commit)
         const uint64_t dq = smem_desc_sw128(s_q, 16, 1024);
@@ -648,9 +623,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         for (uint32_t k = 0; ok; ++k) {
             const Segment* sp = next_segment(k, ok);
             if (sp == nullptr) break;
-            const int32_t n = sp->n;
+            const int32_t n = sp->n, kvh = sp->kvh, q0 = sp->q0, ntok = sp->ntok;
             hand_back(k);
             if (n == 0) continue;
+            // the segment before is done with the query tile's place
+            if (nq > 0) ok = wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, status);
+            if (!ok) break;
+            if (elect_one()) {
+                const bool one = ntok == 1;
+                const uint32_t bar = smem_u32(&sh->q_full);
+                mbar_arrive_expect_tx(bar, (uint32_t)((one ? 1 : P.tpt) * P.group * D * 2));
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, kvh * P.group, q0, bar);
+            }
+            __syncwarp();
             ok = wait_warp(smem_u32(&sh->q_full), nq++ & 1u, status);
             for (int32_t j = 0; j < n && ok; ++j, ++g) {
                 if (g >= kSBuf) {
@@ -677,6 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
         }
         if (!ok && lane == 0) set_abort(sh, status);
+        if (nq > 0 && lane == 0) drain(smem_u32(&sh->q_full), (nq - 1u) & 1u, status);
+        __syncwarp();
         // nothing of ours may still be running when TMEM is freed
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
         __syncwarp();
@@ -739,35 +728,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         __syncwarp();
         drain(smem_u32(&sh->mma_done), 0, status);
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ softmax and epilogue
+    } else if (warp < kStore0) {
+        // ------------------------------------------------------------ softmax
         const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
         const int half = (warp - kSoftmax0) >> 2;
         const int row[2] = {qd * 32 + half * 16 + (lane >> 2), qd * 32 + half * 16 + (lane >> 2) + 8};
         const int tok[2] = {row[0] / P.group, row[1] / P.group};
-        const int head[2] = {row[0] % P.group, row[1] % P.group};
         const uint32_t t_base = tmem + ((uint32_t)(qd * 32 + half * 16) << 16);
         const int c0 = 2 * (lane & 3);  // this thread's columns: c0 + 8 k, c0 + 8 k + 1
         const float sl2 = P.scale_log2;
-        uint32_t gb0 = 0;
+        uint32_t gb0 = 0, segs = 0;  // key tiles, segments with a key so far
         bool ok = true;
         for (uint32_t k = 0;; ++k) {
             const Segment* sg = next_segment(k, ok);
             if (sg == nullptr) break;
             const int32_t n = sg->n, j0 = sg->j0, lo_t = sg->lo, ns = sg->ns;
             const bool dead[2] = {tok[0] >= sg->ntok, tok[1] >= sg->ntok};
-            // where row x's result goes
-            auto out_row = [&](int x) -> int64_t { return (int64_t)(sg->q0 + tok[x]) * P.H + sg->kvh * P.group + head[x]; };
             if (n == 0) {
-                // no key at all: O = 0, LSE = -inf
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (dead[x]) continue;
-                    __nv_bfloat16* orow = P.o + out_row(x) * D + c0;
-#pragma unroll
-                    for (int kk = 0; kk < D / 8; ++kk) *reinterpret_cast<uint32_t*>(orow + 8 * kk) = 0u;
-                    if ((lane & 3) == 0) P.lse[out_row(x)] = -INFINITY;
-                }
                 hand_back(k);
                 continue;
             }
@@ -889,45 +866,96 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 mbar_arrive(smem_u32(&sh->p_full[gb % kSBuf]));
             }
             if (!ok) break;
-            {
-                const uint32_t pv = place_v(gb0 + (uint32_t)n - 1u);
-                const bool wt = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
-                if (__any_sync(0xffffffffu, !wt)) {
-                    ok = false;
-                    break;
-                }
-            }
-            tc_fence_after();
-            const float la = row_sum4(l[0]), lb = row_sum4(l[1]);
-            uint32_t o[D / 2];
-            if constexpr (D == 128) tmem_ld16x256_x16(t_base + kColO, o);
-            else tmem_ld16x256_x8(t_base + kColO, o);
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(smem_u32(&sh->o_free));
-            if (sg->slot < 0) {
-                // 1 / l; 0 for a row without a key, NaN where l is
-                const float inv_a = la == 0.0f ? 0.0f : 1.0f / la, inv_b = lb == 0.0f ? 0.0f : 1.0f / lb;
-                store_o_pairs<D>(o, inv_a, inv_b, dead[0] ? nullptr : P.o + out_row(0) * D,
-                                 dead[1] ? nullptr : P.o + out_row(1) * D);
-                if ((lane & 3) == 0) {
-                    if (!dead[0]) P.lse[out_row(0)] = la == 0.0f ? -INFINITY : (m[0] + log2f(la)) * kLn2;
-                    if (!dead[1]) P.lse[out_row(1)] = lb == 0.0f ? -INFINITY : (m[1] + log2f(lb)) * kLn2;
-                }
-            } else {
-                const int64_t at = (int64_t)sg->slot * 128;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (dead[x]) continue;
-                    float* dst = P.part_o + (at + row[x]) * D + c0;
-#pragma unroll
-                    for (int kk = 0; kk < D / 8; ++kk)
-                        *reinterpret_cast<uint2*>(dst + 8 * kk) = make_uint2(o[4 * kk + 2 * x], o[4 * kk + 2 * x + 1]);
-                    if ((lane & 3) == 0) P.part_ml[at + row[x]] = make_float2(m[x], x ? lb : la);
-                }
-            }
             hand_back(k);
+            // maxima and sums of the rows to the storing warps
+            const float la = row_sum4(l[0]), lb = row_sum4(l[1]);
+            if (__any_sync(0xffffffffu, !wait(smem_u32(&sh->ml_empty), (segs & 1u) ^ 1u, status))) {
+                ok = false;
+                break;
+            }
+            if ((lane & 3) == 0) {
+                sh->ml[row[0]] = make_float2(m[0], la);
+                sh->ml[row[1]] = make_float2(m[1], lb);
+            }
+            mbar_arrive(smem_u32(&sh->ml_full));
+            ++segs;
             gb0 += (uint32_t)n;
+        }
+        if (!ok && lane == 0) set_abort(sh, status);
+    } else {
+        // ------------------------------------------------------------ O and LSE of a segment
+        // one thread per row
+        const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
+        const int row = qd * 32 + lane, tok = row / P.group, head = row % P.group;
+        const uint32_t t_row = tmem + ((uint32_t)(qd * 32) << 16) + kColO;
+        uint32_t g = 0, segs = 0;
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const int32_t n = sp->n, slot = sp->slot;
+            const bool dead = tok >= sp->ntok;
+            const int64_t at = (int64_t)(sp->q0 + tok) * P.H + sp->kvh * P.group + head;
+            hand_back(k);
+            __nv_bfloat16* orow = P.o + at * D;
+            if (n == 0) {
+                // no key at all: O = 0, LSE = -inf
+                if (!dead) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(orow + c) = make_uint4(0, 0, 0, 0);
+                    P.lse[at] = -INFINITY;
+                }
+                continue;
+            }
+            const uint32_t pv = place_v(g + (uint32_t)n - 1u);
+            // (the last product is the segment's: the next one waits for o_free)
+            ok = wait_warp(smem_u32(&sh->ml_full), segs & 1u, status) &&
+                 wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
+            if (!ok) break;
+            const float2 ml = sh->ml[row];
+            mbar_arrive(smem_u32(&sh->ml_empty));
+            tc_fence_after();
+            if (slot < 0) {
+                // 1 / l; 0 for a row without a key, NaN where l is
+                const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32], pk[16];
+                    tmem_ld32(t_row + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                    if (!dead) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh->o_free));
+                if (!dead)
+                    P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+            } else {
+                const int64_t part = (int64_t)slot * 128 + row;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t_row + c, o);
+                    tmem_wait_ld();
+                    if (!dead) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh->o_free));
+                if (!dead) P.part_ml[part] = ml;
+            }
+            g += (uint32_t)n;
+            ++segs;
         }
         if (!ok && lane == 0) set_abort(sh, status);
     }
@@ -1099,7 +1127,8 @@ Layout layout(const PagedForwardArgs& a) {
 
 template <int D, int kMode>
 bsa_status launch_d(const Params& P, cudaStream_t stream) {
-    const size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
+    constexpr size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
+    static_assert(smem <= 232448, "shared memory of a thread block");
     static int done[64] = {0};
     static int sms[64] = {0};
     int dev = 0;
