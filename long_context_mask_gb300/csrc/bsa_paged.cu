@@ -13,15 +13,16 @@
 // page of the block's last token.
 //
 // Work mapping.  A thread block takes one 128-position block that a sequence's
-// new tokens touch and a run of the tokens' rows, a token's rows being (key,
-// value, queries) of its key/value heads in turn.  The block that writes a
-// head's keys writes all of this position block's, so the mean needs no other's
-// work and adds in a fixed order, whatever chunks the tokens came in.  A row of
-// D values is held by D / 8 neighbouring threads, eight values each: where the
-// whole head turns by halves, four of either half (a pair meets in one thread),
-// else eight in a row, with the rotation partner's values by shuffles.  Every thread loads kUnroll rows before it
-// works on the first (one row at a time left 16 KB in flight on an SM: a prompt
-// of 8192 tokens, 32 + 8 heads of 128, took 107 us, 1.9 TB/s).
+// new tokens touch and four rows of each token: four query heads, or the key and
+// the value of two key/value heads.  The block that writes a head's keys writes
+// all of this position block's, so the mean needs no other's work and adds in a
+// fixed order, whatever chunks the tokens came in.  A row of D values is held by
+// D / 8 neighbouring threads, eight values each: where the whole head turns by
+// halves, four of either half (a pair meets in one thread), else eight in a row,
+// with the rotation partner's values by shuffles.  Every thread loads its four
+// rows before it works on the first.  (A prompt of 8192 tokens, 32 + 8 heads of
+// 128 with norms: 107 us with one row at a time, 62 us when each row found its
+// place for itself, 234 instructions a row.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -33,8 +34,7 @@
 namespace bsa {
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kUnroll = 4;  // rows that a thread holds at a time
+constexpr int kAppendThreads = 128;
 
 struct AppendParams {
     PagedBatch b;
@@ -47,8 +47,8 @@ struct AppendParams {
     const __nv_bfloat16 *q_norm, *k_norm;
     float eps;
     int32_t H_kv, group;
-    int32_t per_head;        // rows of a token and key/value head: key, value, queries
-    int32_t rows_per_block;  // rows of a token that one thread block takes
+    int32_t q_blocks;  // thread blocks (y) of query heads; those of keys and values follow
+    int32_t page_shift;
 };
 
 __device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
@@ -86,21 +86,17 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, int c, const uint4
     }
 }
 
-// RMS norm of one row over its D values; w null: left as it is.  Every thread
-// of the warp calls it.
-template <int D, bool kHalves>
-__device__ __forceinline__ void norm_row(float (&x)[8], int c, const __nv_bfloat16* w, float eps) {
+// RMS norm of one row over its D values.  Every thread of the warp calls it.
+template <int D>
+__device__ __forceinline__ void norm_row(float (&x)[8], const float (&w)[8], float eps) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
     for (int d = 1; d < D / 8; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (w == nullptr) return;
-    const float r = 1.0f / sqrtf(ss * (1.0f / D) + eps);
-    float wf[8];
-    unpack8(load_row<D, kHalves>(w, c), wf);
+    const float r = rsqrtf(ss * (1.0f / D) + eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
 }
 
 // The angles that this thread's values of a row turn by: with kHalves values i
@@ -210,71 +206,67 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     __syncthreads();
 
     const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-    const int32_t row0 = blockIdx.y * P.rows_per_block;
-    const int32_t n_rows = min(P.rows_per_block, P.H_kv * P.per_head - row0);
-    // a thread's rows: token t, rows r .. r + kUnroll - 1 of the block's n_rows
-    const int32_t groups = (n_rows + kUnroll - 1) / kUnroll;
-    const int32_t items = (hi - lo) * groups;
+    const bool queries = (int32_t)blockIdx.y < P.q_blocks;
+    const int32_t h0 = queries ? 4 * blockIdx.y : 2 * (blockIdx.y - P.q_blocks);  // first head
+    const int32_t heads = queries ? min(4, P.H_kv * P.group - h0) : min(2, P.H_kv - h0);
     if (P.rope != nullptr && hi > P.rope_len && threadIdx.x == 0) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
-    for (int32_t i0 = 0; i0 < items; i0 += kRows) {
+    const __nv_bfloat16* w = queries ? P.q_norm : P.k_norm;
+    float wf[8];
+    if (w != nullptr) unpack8(load_row<D, kHalves>(w, c), wf);
+    for (int32_t p0 = lo; p0 < hi; p0 += kRows) {
         // whole warps stay in the loop: the shuffles need them
-        const int32_t i = i0 + sub;
-        const int32_t t = i < items ? i / groups : 0;
-        const int32_t r0 = i < items ? (i - t * groups) * kUnroll : n_rows;
-        const int32_t pos = lo + t;
+        const int32_t pos = p0 + sub;
+        const bool live = pos < hi;
         const int64_t tok = (int64_t)q.q0 + (pos - first);
-        uint4 raw[kUnroll];
-        __nv_bfloat16* dst[kUnroll];
-        int kind[kUnroll];  // 0: key, 1: value, 2: query
-        const int32_t id = pages[(pos - base) / page];
-        const int64_t slot = ((int64_t)id * P.H_kv) * page + pos % page;
-        int32_t h = (row0 + r0) / P.per_head, k = row0 + r0 - h * P.per_head;
+        uint4 raw[4];
+        __nv_bfloat16* dst[4];  // null: no such row
+        if (queries) {
+            const __nv_bfloat16* src = P.q + tok * P.q_stride + h0 * D;
+            __nv_bfloat16* out = P.q_out + tok * P.qo_stride + h0 * D;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            raw[u] = make_uint4(0, 0, 0, 0);
-            dst[u] = nullptr;
-            kind[u] = 1;
-            if (r0 + u < n_rows) {
-                const __nv_bfloat16* src;
-                kind[u] = min(k, 2);
-                if (k < 2) {
-                    src = k == 0 ? P.k + tok * P.k_stride + h * D : P.v + tok * P.v_stride + h * D;
-                    if (id >= 0) dst[u] = (k == 0 ? P.k_cache : P.v_cache) + (slot + (int64_t)h * page) * D;
-                } else {
-                    const int32_t hq = h * P.group + k - 2;
-                    src = P.q + tok * P.q_stride + hq * D;
-                    dst[u] = P.q_out + tok * P.qo_stride + hq * D;
-                }
-                raw[u] = load_row<D, kHalves>(src, c);
+            for (int u = 0; u < 4; ++u) {
+                dst[u] = live && u < heads ? out + u * D : nullptr;
+                raw[u] = dst[u] != nullptr ? load_row<D, kHalves>(src + u * D, c) : make_uint4(0, 0, 0, 0);
             }
-            if (++k == P.per_head) {
-                k = 0;
-                ++h;
+        } else {
+            const __nv_bfloat16* ks = P.k + tok * P.k_stride + h0 * D;
+            const __nv_bfloat16* vs = P.v + tok * P.v_stride + h0 * D;
+            const int32_t id = live ? pages[(pos - base) >> P.page_shift] : -1;
+            const int64_t slot = ((((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1))) * D;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool mine = live && (u >> 1) < heads;
+                raw[u] = mine ? load_row<D, kHalves>((u & 1 ? vs : ks) + (u >> 1) * D, c) : make_uint4(0, 0, 0, 0);
+                dst[u] = mine && id >= 0 ? (u & 1 ? P.v_cache : P.k_cache) + slot + (int64_t)((u >> 1) * page) * D : nullptr;
             }
         }
         Angles a{};
         if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < 4; ++u) {
+            if (!queries && (u & 1)) {  // a value's row is written as it came
+                if (dst[u] != nullptr) store_row<D, kHalves>(dst[u], c, raw[u]);
+                continue;
+            }
             float x[8];
             unpack8(raw[u], x);
-            // every lane takes part in the shuffles; a value's row is written as it came
-            if (P.q_norm != nullptr || P.k_norm != nullptr)
-                norm_row<D, kHalves>(x, c, kind[u] == 0 ? P.k_norm : (kind[u] == 2 ? P.q_norm : nullptr), P.eps);
+            if (w != nullptr) norm_row<D>(x, wf, P.eps);
             if (P.rope != nullptr) rotate_row<kHalves>(P, x, c, a);
-            if (dst[u] != nullptr) store_row<D, kHalves>(dst[u], c, kind[u] == 1 ? raw[u] : pack8(x));
+            if (dst[u] != nullptr) store_row<D, kHalves>(dst[u], c, pack8(x));
         }
     }
 
+    if (queries) return;
     if (P.k_mean == nullptr || hi != base + kBlock) return;  // (the whole thread block agrees)
     // the block is full: the mean of its 128 keys as the cache holds them
     const int32_t last = pages[per - 1];
     bool whole = true;
     for (int p = 0; p < per; ++p) whole &= pages[p] >= 0;
     if (!whole) return;
-    for (int32_t h = (row0 + P.per_head - 1) / P.per_head; h * P.per_head < row0 + n_rows; ++h) {
+    for (int32_t h = h0; h < h0 + heads; ++h) {
         __syncthreads();  // the keys above are written; sums is free again
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
         for (int p = sub; p < kBlock; p += kRows) {
             const __nv_bfloat16* row = P.k_cache + (((int64_t)pages[p / page] * P.H_kv + h) * page + p % page) * D;
             float f[8];
@@ -287,7 +279,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
         __syncthreads();
         if (threadIdx.x < D) {
             float t = 0.f;
-#pragma unroll 8
+#pragma unroll
             for (int g = 0; g < kRows; ++g) t += sums[g][threadIdx.x];
             P.k_mean[((int64_t)last * P.H_kv + h) * D + threadIdx.x] = __float2bfloat16_rn(t * (1.0f / kBlock));
         }
@@ -319,19 +311,11 @@ bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaSt
     P.eps = a.eps;
     P.H_kv = a.H_kv;
     P.group = a.H / a.H_kv;
-    P.per_head = (a.q != nullptr ? P.group : 0) + 2;
+    P.page_shift = __builtin_ctz((unsigned)a.page);
+    P.q_blocks = a.q != nullptr ? (a.H + 3) / 4 : 0;
     // a sequence's n > 0 new tokens touch at most (n + 126) / 128 + 1 blocks
     const int64_t units = (int64_t)a.tokens / kBlock + 2 * (int64_t)a.seqs;
-    // About 512 rows to a thread block, four of a block's 128 tokens, but no more
-    // than a key/value head's: a decoding step's means (one block of 128 keys each,
-    // for some sequences) are read head by head (32 sequences with all 48 rows in
-    // one thread block: 16 us instead of 6).
-    const int64_t per_seq = (a.tokens + a.seqs - 1) / a.seqs;
-    const int64_t span = per_seq < kBlock ? per_seq : kBlock;
-    int64_t rows = 512 / span;
-    if (rows > P.per_head) rows = P.per_head;
-    P.rows_per_block = (int32_t)rows;
-    const dim3 grid((unsigned)units, (unsigned)(((int64_t)a.H_kv * P.per_head + rows - 1) / rows));
+    const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + (a.H_kv + 1) / 2));
     const bool halves = a.rope != nullptr && a.rot == a.D && !a.interleaved;
     const auto kernel = a.D == 128 ? (halves ? k_paged_append<128, true> : k_paged_append<128, false>)
                                    : (halves ? k_paged_append<64, true> : k_paged_append<64, false>);

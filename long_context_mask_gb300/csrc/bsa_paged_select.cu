@@ -101,11 +101,31 @@ __device__ __forceinline__ Key kth_largest(const Key (&held)[kHeld > 0 ? kHeld :
         }
         return v;
     };
-    Key lo = least(0), hi = 0;
-    each([&](Key x, bool in) { hi = in && x > hi ? x : hi; });
+    Key mine = 0;  // this lane's largest
+    each([&](Key x, bool in) { mine = in && x > mine ? x : mine; });
+    Key hi = mine;
     for (int d = 1; d < 32; d <<= 1) {
         const Key b = __shfl_xor_sync(0xffffffffu, hi, d);
         hi = b > hi ? b : hi;
+    }
+    Key lo;
+    if (k <= 32 && n >= 32) {
+        // the k-th largest of the lanes' largest is a good first bound, and cheap to find
+        lo = mine;
+        for (int d = 1; d < 32; d <<= 1) {
+            const Key a = __shfl_xor_sync(0xffffffffu, lo, d);
+            lo = a < lo ? a : lo;
+        }
+        Key top = hi;
+        for (int step = 0; lo < top; ++step) {
+            const Key mid = halfway(lo, top, step);
+            const int32_t c = __popc(__ballot_sync(0xffffffffu, mine >= mid));
+            if (c >= k) lo = mid;
+            else top = mid - 1;
+            if (c == k) break;
+        }
+    } else {
+        lo = least(0);
     }
     // at least k keys reach lo, fewer than k exceed hi
     for (int step = 0; lo < hi; ++step) {
@@ -313,17 +333,20 @@ __global__ void __launch_bounds__(kScoreThreads) k_paged_scores(const __grid_con
     }
 }
 
+constexpr int kHeld = 16;  // up to 512 scores of a row stay in registers (16 to a lane)
+
 // One warp per (token, key/value head).
 template <int D>
 __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ SelectParams P) {
     extern __shared__ __align__(16) uint8_t dyn[];
     const int lane = threadIdx.x & 31;
     const int32_t warp = threadIdx.x >> 5;
-    // the warp's own: fp64 keys of close calls, keys, blocks of close calls, chosen blocks
+    // the warp's own: fp64 keys of close calls, keys (of rows too long for registers),
+    // chosen blocks, places of close calls
     uint64_t* key64 = reinterpret_cast<uint64_t*>(dyn + (size_t)warp * P.pick_bytes);
     uint32_t* keys = reinterpret_cast<uint32_t*>(key64 + P.nb_cap);
-    int32_t* close = reinterpret_cast<int32_t*>(keys + P.nb_cap);
-    uint32_t* chosen = reinterpret_cast<uint32_t*>(close + P.nb_cap);
+    uint32_t* chosen = keys + (P.nb_cap > 32 * kHeld ? P.nb_cap : 0);
+    uint16_t* close = reinterpret_cast<uint16_t*>(chosen + P.nb_cap / 32 + 1);
     ptx::launch_dependents();
     ptx::wait_primary();
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
@@ -378,7 +401,6 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
         float most = 0.f;
         for (int32_t x = c0 / kTileBlk + lane; x <= (c1 - 1) / kTileBlk; x += 32) most = larger(norms[x], most);
         const float* scores = P.scores + row * P.nb_cap + c0;
-        constexpr int kHeld = 16;  // up to 512 scores stay in registers
         uint32_t held[kHeld];
         const bool in_regs = nc <= 32 * kHeld;
         if (in_regs) {
@@ -410,7 +432,7 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
             const uint32_t sure = __ballot_sync(0xffffffffu, x < nc && k > hi);
             const uint32_t maybe = __ballot_sync(0xffffffffu, x < nc && k <= hi && k >= lo);
             if ((sure >> lane) & 1u) atomicOr(&chosen[(c0 + x) >> 5], 1u << ((c0 + x) & 31));
-            if ((maybe >> lane) & 1u) close[n_close + __popc(maybe & ((1u << lane) - 1u))] = x;
+            if ((maybe >> lane) & 1u) close[n_close + __popc(maybe & ((1u << lane) - 1u))] = (uint16_t)x;
             n_sure += __popc(sure);
             n_close += __popc(maybe);
         };
@@ -434,17 +456,21 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
             for (int g = 0; g < P.group; ++g)
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) q[i] += (double)__bfloat162float(qrow[g * D + lane * kPer + i]);
-            for (int32_t x = 0; x < n_close; ++x) {
+            for (int32_t x0 = 0; x0 < n_close; x0 += 32) {
                 // (a bad page has been reported with the scores)
-                const int32_t id = table[(int64_t)(c0 + close[x] + 1) * per - 1];
-                const __nv_bfloat16* m =
-                    P.k_mean + ((int64_t)(id < 0 || id >= P.b.n_pages ? 0 : id) * P.H_kv + kvh) * D + lane * kPer;
-                double dot = 0.0;
+                int32_t id = x0 + lane < n_close ? table[(int64_t)(c0 + close[x0 + lane] + 1) * per - 1] : 0;
+                id = id < 0 || id >= P.b.n_pages ? 0 : id;
+#pragma unroll 4
+                for (int32_t x = x0; x < min(x0 + 32, n_close); ++x) {
+                    const __nv_bfloat16* m =
+                        P.k_mean + ((int64_t)__shfl_sync(0xffffffffu, id, x - x0) * P.H_kv + kvh) * D + lane * kPer;
+                    double dot = 0.0;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) dot = fma(q[i], (double)__bfloat162float(m[i]), dot);
+                    for (int i = 0; i < kPer; ++i) dot = fma(q[i], (double)__bfloat162float(m[i]), dot);
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-                if (lane == 0) key64[x] = key_of(dot);
+                    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+                    if (lane == 0) key64[x] = key_of(dot);
+                }
             }
             __syncwarp();
             const uint64_t none64[1] = {0ull};
@@ -546,7 +572,7 @@ bsa_status launch_paged_select(const PagedSelectArgs& a, void* workspace, int32_
     P.sel_cnt = a.sel_cnt;
     P.nb_cap = L.nb_cap;
     P.chunks = L.chunks;
-    P.pick_bytes = (L.nb_cap * 16 + (L.nb_cap / 32 + 1) * 4 + 15) & ~15;
+    P.pick_bytes = (L.nb_cap * (8 + (L.nb_cap > 32 * kHeld ? 4 : 0) + 2) + (L.nb_cap / 32 + 1) * 4 + 15) & ~15;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     P.norms = reinterpret_cast<float*>(ws + L.norms);
     P.scores = reinterpret_cast<float*>(ws + L.scores);
