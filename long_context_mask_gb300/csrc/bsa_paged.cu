@@ -163,19 +163,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     constexpr int kLanes = D / 8;
     constexpr int kRows = kAppendThreads / kLanes;  // rows in flight
     __shared__ int64_t part[33];
-    __shared__ int32_t hit[2];
+    __shared__ int32_t hit[5];
     __shared__ int32_t pages[8];  // the block's pages (128 / page of them)
     __shared__ float sums[kRows][D];
     ptx::launch_dependents();
     ptx::wait_primary();
     int32_t blk;
+    PagedSeq q;
     const int32_t s = find_unit(
         P.b, blockIdx.x,
         [](const PagedSeq& q) -> int64_t {
             // 128-position blocks that the new tokens touch (those at positions >= 0)
             return q.nq > 0 && q.kl > 0 ? (q.kl - 1) / kBlock - max(q.kl - q.nq, 0) / kBlock + 1 : 0;
         },
-        part, hit, blk);
+        part, hit, blk, q);
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         for (int32_t i = threadIdx.x; i < P.b.seqs; i += kAppendThreads) {
             PagedSeq q;
@@ -184,8 +185,6 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
         }
     }
     if (s < 0) return;
-    PagedSeq q;
-    paged_seq(P.b, s, q);
     const int32_t first = q.kl - q.nq;                  // position of the first new token
     blk += max(first, 0) / kBlock;
     const int32_t base = blk * kBlock;

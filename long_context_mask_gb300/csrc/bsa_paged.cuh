@@ -86,12 +86,12 @@ __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* part, int64_
 }
 
 // Unit u of the batch, where sequence s counts count(seq) units: the sequence
-// (-1: u is beyond the last) and the unit within it.  Called by the whole
-// thread block; the same answer in every thread.  shared: see block_prefix,
-// and hit: 2 words.
+// (-1: u is beyond the last), the unit within it and the sequence's entry.
+// Called by the whole thread block; the same answer in every thread.  part: see
+// block_prefix; hit: 5 words of shared memory.
 template <typename Count>
 __device__ __forceinline__ int32_t find_unit(const PagedBatch& b, int64_t u, Count&& count, int64_t* part, int32_t* hit,
-                                             int32_t& within) {
+                                             int32_t& within, PagedSeq& found) {
     if (threadIdx.x == 0) hit[0] = -1;
     int64_t base = 0;
     for (int32_t s0 = 0; s0 < b.seqs; s0 += blockDim.x) {
@@ -107,12 +107,16 @@ __device__ __forceinline__ int32_t find_unit(const PagedBatch& b, int64_t u, Cou
         if (n > 0 && u >= at && u < at + n) {
             hit[0] = s;
             hit[1] = (int32_t)(u - at);
+            hit[2] = q.q0;
+            hit[3] = q.nq;
+            hit[4] = q.kl;
         }
         base += total;
         if (u < base) break;
     }
     __syncthreads();
     within = hit[1];
+    found = PagedSeq{hit[2], hit[3], hit[4]};
     return hit[0];
 }
 

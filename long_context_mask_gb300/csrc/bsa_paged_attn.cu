@@ -1026,15 +1026,14 @@ struct UnionParams {
 __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_constant__ UnionParams P) {
     __shared__ uint32_t bits[kUnionWords];
     __shared__ int64_t part[33];
-    __shared__ int32_t hit[2];
+    __shared__ int32_t hit[5];
     launch_dependents();
     wait_primary();
     int32_t t;
-    const int32_t s = find_unit(
-        P.b, blockIdx.x, [&](const PagedSeq& q) -> int64_t { return (q.nq + P.tpt - 1) / P.tpt; }, part, hit, t);
-    if (s < 0) return;
     PagedSeq q;
-    paged_seq(P.b, s, q);
+    const int32_t s = find_unit(
+        P.b, blockIdx.x, [&](const PagedSeq& y) -> int64_t { return (y.nq + P.tpt - 1) / P.tpt; }, part, hit, t, q);
+    if (s < 0) return;
     const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
     const int32_t kvh = blockIdx.y;
     const int32_t nkb = (q.kl + 127) / 128;  // blocks of the sequence

@@ -76,6 +76,17 @@ __device__ __forceinline__ uint32_t halfway(uint32_t lo, uint32_t hi, int step) 
 }
 __device__ __forceinline__ uint64_t halfway(uint64_t lo, uint64_t hi, int) { return hi - (hi - lo) / 2; }
 
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t warp_min(uint32_t x) { return __reduce_min_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t y = __shfl_xor_sync(0xffffffffu, x, d);
+        x = y > x ? y : x;
+    }
+    return x;
+}
+__device__ __forceinline__ uint64_t warp_min(uint64_t x) { return ~warp_max(~x); }
+
 // The k-th largest (1 <= k <= n) of the warp's n keys, by bisection between the
 // smallest and the largest; it stops early at a bound that exactly k keys reach.
 // kHeld > 0: lane l's keys are held[i] = key number l + 32 i (0 behind the last);
@@ -95,27 +106,14 @@ __device__ __forceinline__ Key kth_largest(const Key (&held)[kHeld > 0 ? kHeld :
     auto least = [&](Key bound) -> Key {  // of the keys >= bound
         Key v = ~(Key)0;
         each([&](Key x, bool in) { v = in && x >= bound && x < v ? x : v; });
-        for (int d = 1; d < 32; d <<= 1) {
-            const Key a = __shfl_xor_sync(0xffffffffu, v, d);
-            v = a < v ? a : v;
-        }
-        return v;
+        return warp_min(v);
     };
     Key mine = 0;  // this lane's largest
     each([&](Key x, bool in) { mine = in && x > mine ? x : mine; });
-    Key hi = mine;
-    for (int d = 1; d < 32; d <<= 1) {
-        const Key b = __shfl_xor_sync(0xffffffffu, hi, d);
-        hi = b > hi ? b : hi;
-    }
-    Key lo;
+    Key hi = warp_max(mine), lo;
     if (k <= 32 && n >= 32) {
         // the k-th largest of the lanes' largest is a good first bound, and cheap to find
-        lo = mine;
-        for (int d = 1; d < 32; d <<= 1) {
-            const Key a = __shfl_xor_sync(0xffffffffu, lo, d);
-            lo = a < lo ? a : lo;
-        }
+        lo = warp_min(mine);
         Key top = hi;
         for (int step = 0; lo < top; ++step) {
             const Key mid = halfway(lo, top, step);
@@ -148,22 +146,21 @@ __global__ void __launch_bounds__(kScoreThreads) k_paged_scores(const __grid_con
     extern __shared__ __align__(16) float tile[];  // sums of the query heads [tokens][D + 4], means [blocks][D + 4]
     constexpr int kRow = D + 4;                    // (rows 4 banks apart: 16-byte reads down a column meet no conflict)
     __shared__ int64_t part[33];
-    __shared__ int32_t hit[2];
+    __shared__ int32_t hit[5];
     __shared__ int32_t ids[kTileBlk];
     __shared__ float most[kScoreThreads / 32];
     ptx::launch_dependents();
     ptx::wait_primary();
     int32_t t;
+    PagedSeq y;
     const int32_t s = find_unit(
-        P.b, blockIdx.x, [](const PagedSeq& q) -> int64_t { return (q.nq + kTileTok - 1) / kTileTok; }, part, hit, t);
+        P.b, blockIdx.x, [](const PagedSeq& q) -> int64_t { return (q.nq + kTileTok - 1) / kTileTok; }, part, hit, t, y);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         for (int32_t x = threadIdx.x; x < P.b.seqs; x += kScoreThreads) {
             PagedSeq y;
             if (!paged_seq(P.b, x, y)) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
         }
     if (s < 0) return;
-    PagedSeq y;
-    paged_seq(P.b, s, y);
     const int32_t first = t * kTileTok, ntok = min(kTileTok, y.nq - first);
     const int32_t kvh = blockIdx.z, b0 = blockIdx.y * kTileBlk;
     int32_t c0, c1;  // of the last token, which ranks the most
@@ -404,8 +401,12 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
         uint32_t held[kHeld];
         const bool in_regs = nc <= 32 * kHeld;
         if (in_regs) {
+            // (all loads first: 16 of them, each under a condition, waited one for another)
+            float sc[kHeld];
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < nc ? key_of(scores[lane + 32 * i]) : 0u;
+            for (int i = 0; i < kHeld; ++i) sc[i] = scores[min(lane + 32 * i, nc - 1)];
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < nc ? key_of(sc[i]) : 0u;
         } else {
 #pragma unroll 8
             for (int32_t x = lane; x < nc; x += 32) keys[x] = key_of(scores[x]);
@@ -426,22 +427,59 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
         const bool bound = tau - tau == 0.0f && E - E == 0.0f;
         const uint32_t hi = bound ? key_of(tau + 2.0f * E) : 0xffffffffu;  // surely chosen: keys above
         const uint32_t lo = bound ? key_of(tau - 2.0f * E) : 0u;           // surely not: keys below
+        // bits of places x0 .. x0 + 31 among the chosen blocks
+        auto choose = [&](int32_t x0, uint32_t bits) {
+            if (bits == 0u) return;
+            const int32_t b0 = c0 + x0, sh = b0 & 31;
+            atomicOr(&chosen[b0 >> 5], bits << sh);
+            if (sh != 0 && (bits >> (32 - sh)) != 0u) atomicOr(&chosen[(b0 >> 5) + 1], bits >> (32 - sh));
+        };
         // the blocks in between, in ascending order
         int32_t n_close = 0, n_sure = 0;
-        auto sort_out = [&](int32_t x, uint32_t k) {
-            const uint32_t sure = __ballot_sync(0xffffffffu, x < nc && k > hi);
-            const uint32_t maybe = __ballot_sync(0xffffffffu, x < nc && k <= hi && k >= lo);
-            if ((sure >> lane) & 1u) atomicOr(&chosen[(c0 + x) >> 5], 1u << ((c0 + x) & 31));
-            if ((maybe >> lane) & 1u) close[n_close + __popc(maybe & ((1u << lane) - 1u))] = (uint16_t)x;
-            n_sure += __popc(sure);
-            n_close += __popc(maybe);
-        };
-        if (in_regs) {
+        for (int32_t base = 0; base < nc; base += 32 * kHeld) {
+            // bit i of a lane's masks: its place base + 32 i + lane.  (The long part is in
+            // loops of few instructions: laid out 16 times and run once it waited for
+            // its instructions.)
+            uint32_t sure = 0u, maybe = 0u;
+            if (in_regs) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                if (32 * i < nc) sort_out(lane + 32 * i, held[i]);
-        } else {
-            for (int32_t x0 = 0; x0 < nc; x0 += 32) sort_out(x0 + lane, x0 + lane < nc ? keys[x0 + lane] : 0u);
+                for (int i = 0; i < kHeld; ++i) {
+                    sure |= held[i] > hi ? 1u << i : 0u;
+                    maybe |= held[i] >= lo ? 1u << i : 0u;
+                }
+            } else {
+                for (int i = 0; i < kHeld && base + 32 * i + lane < nc; ++i) {
+                    const uint32_t k = keys[base + 32 * i + lane];
+                    sure |= (uint32_t)(k > hi) << i;
+                    maybe |= (uint32_t)(k >= lo) << i;
+                }
+            }
+            // (places behind the last: their key 0 may reach lo = 0)
+            const int32_t mine = nc - base - lane;
+            const int32_t held_n = mine <= 0 ? 0 : min((mine + 31) / 32, kHeld);
+            maybe &= ((1u << held_n) - 1u) & ~sure;
+            // lane i < kHeld: the masks of places base + 32 i .. + 31
+            uint32_t sure_w = 0u, maybe_w = 0u;
+#pragma unroll 1
+            for (int i = 0; i < kHeld; ++i) {
+                const uint32_t a = __ballot_sync(0xffffffffu, (sure >> i) & 1u), b = __ballot_sync(0xffffffffu, (maybe >> i) & 1u);
+                if (lane == i) {
+                    sure_w = a;
+                    maybe_w = b;
+                }
+            }
+            choose(base + 32 * lane, sure_w);
+            int32_t at = __popc(maybe_w);
+#pragma unroll
+            for (int d = 1; d < kHeld; d <<= 1) {
+                const int32_t v = __shfl_up_sync(0xffffffffu, at, d);
+                if (lane >= d) at += v;
+            }
+            const int32_t total = __shfl_sync(0xffffffffu, at, kHeld - 1);
+            at += n_close - __popc(maybe_w);
+            for (uint32_t bits = maybe_w; bits; bits &= bits - 1u) close[at++] = (uint16_t)(base + 32 * lane + __ffs(bits) - 1);
+            n_close += total;
+            n_sure += __reduce_add_sync(0xffffffffu, __popc(sure));
         }
         __syncwarp();
         const int32_t need = P.topk - n_sure;  // places left for the close calls
@@ -453,6 +491,7 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
             double q[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) q[i] = 0.0;
+#pragma unroll 4
             for (int g = 0; g < P.group; ++g)
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) q[i] += (double)__bfloat162float(qrow[g * D + lane * kPer + i]);
@@ -473,11 +512,23 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
                 }
             }
             __syncwarp();
-            const uint64_t none64[1] = {0ull};
-            edge = kth_largest<0>(none64, key64, n_close, need);
-            int32_t better = 0;
-            for (int32_t x = lane; x < n_close; x += 32) better += key64[x] > edge;
-            left = need - __reduce_add_sync(0xffffffffu, better);  // of the equal scores at the edge, the lowest blocks
+            if (n_close <= 32) {
+                // a lane for each: how many are better (equal scores: the lower blocks)
+                const uint64_t mine = lane < n_close ? key64[lane] : 0ull;
+                int32_t better = 0;
+                for (int32_t x = 0; x < n_close; ++x) {
+                    const uint64_t k = __shfl_sync(0xffffffffu, mine, x);
+                    better += k > mine || (k == mine && x < lane);
+                }
+                if (lane < n_close && better < need) atomicOr(&chosen[(c0 + close[lane]) >> 5], 1u << ((c0 + close[lane]) & 31));
+                n_close = 0;  // (all done)
+            } else {
+                const uint64_t none64[1] = {0ull};
+                edge = kth_largest<0>(none64, key64, n_close, need);
+                int32_t better = 0;
+                for (int32_t x = lane; x < n_close; x += 32) better += key64[x] > edge;
+                left = need - __reduce_add_sync(0xffffffffu, better);  // of the equal scores at the edge, the lowest blocks
+            }
         }
         for (int32_t x0 = 0; x0 < n_close; x0 += 32) {
             const int32_t x = x0 + lane;
