@@ -145,9 +145,6 @@ struct Params {
     int4* joins;              // [runs] parts (0: none), q0, ntok, kvh
 };
 
-__device__ __forceinline__ bool aborted(const Shared* sh) {
-    return *reinterpret_cast<const volatile int32_t*>(&sh->abort) != 0;
-}
 __device__ __forceinline__ void set_abort(Shared* sh, int32_t* status) {
     *reinterpret_cast<volatile int32_t*>(&sh->abort) = 1;
     raise_status(status, BSA_ERR_TIMEOUT);
@@ -211,16 +208,16 @@ __device__ __forceinline__ uint32_t columns_below(int32_t v) {
 // One key tile of the online softmax for this thread's shares of rows a and b.
 // dead: the row holds no token (its scores are anything; m = 0, and it takes
 // part in no decision).  A live row that has seen no key yet has m = -inf.
-// As long as no row is in that state the exponentials are taken against the
-// running maxima without computing the tile's own; only a tile whose sums
-// leave 2^64 (or are NaN) is redone with its maxima.  Returns true
-// (warp-uniform) when O must be multiplied by alpha first.
+// As long as no row of the warp is in that state (fresh, warp-uniform) the
+// exponentials are taken against the running maxima without computing the
+// tile's own; only a tile whose sums leave 2^64 (or are NaN) is redone with its
+// maxima.  Returns true (warp-uniform) when O must be multiplied by alpha first.
 template <typename Reload>
-__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], float sl2, float (&m)[2],
-                                             float (&l)[2], float (&alpha)[2], Reload&& reload) {
+__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], float sl2, bool& fresh,
+                                             float (&m)[2], float (&l)[2], float (&alpha)[2], Reload&& reload) {
     alpha[0] = alpha[1] = 1.0f;
     float la, lb;
-    if (!__any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY)) {
+    if (!fresh) {
         exp_rows<0>(s, sl2, -m[0], -m[1], la, lb);
         if (!__any_sync(0xffffffffu, (!dead[0] && !(la <= kSumLimit)) || (!dead[1] && !(lb <= kSumLimit)))) {
             l[0] += la;
@@ -253,6 +250,7 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
     exp_rows<0>(s, sl2, bias[0], bias[1], la, lb);
     l[0] += la;
     l[1] += lb;
+    fresh = __any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY);
     return rescale;
 }
 
@@ -736,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         const int tok[2] = {row[0] / P.group, row[1] / P.group};
         const uint32_t t_base = tmem + ((uint32_t)(qd * 32 + half * 16) << 16);
         const int c0 = 2 * (lane & 3);  // this thread's columns: c0 + 8 k, c0 + 8 k + 1
+        const int warp_tok0 = (qd * 32 + half * 16) / P.group, warp_tok1 = (qd * 32 + half * 16 + 15) / P.group;
         const float sl2 = P.scale_log2;
         uint32_t gb0 = 0, segs = 0;  // key tiles, segments with a key so far
         bool ok = true;
@@ -748,31 +747,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 hand_back(k);
                 continue;
             }
-            // Row x sees keys lo[x] .. hi[x] - 1 and 0 .. sk[x] - 1.  Key tiles below
-            // all_hi, and with a window from all_lo on or inside the sinks, are seen
-            // whole by every row of the query tile.
+            // Row x sees keys lo[x] .. hi[x] - 1 and 0 .. sk[x] - 1.  Key tiles from
+            // some_lo on and below some_hi, or below some_sk, are seen by some row of this
+            // warp, from all_lo on and below all_hi, or below all_sk, whole by every row.
             int32_t hi[2], lo[2] = {0, 0}, sk[2] = {0, 0};
-            int32_t all_hi, all_lo = 0, all_sk = 0;
+            int32_t some_hi, all_hi, some_lo = 0, all_lo = 0, some_sk = 0, all_sk = 0;
             {
                 const int32_t kl = sg->kl, p0 = sg->pos0;
+                // this warp's first and last token with a row
+                const int32_t pa = p0 + warp_tok0, pb = p0 + min(warp_tok1, sg->ntok - 1);
+                auto end = [&](int32_t p) -> int32_t { return P.causal ? min(kl, p + 1) : kl; };
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    hi[x] = P.causal ? min(kl, p0 + tok[x] + 1) : kl;
+                    hi[x] = end(p0 + tok[x]);
                     if constexpr (kMode == kWindow) {
                         lo[x] = p0 + tok[x] - P.window + 1;
                         sk[x] = min(P.sinks, hi[x]);
                     }
                 }
-                all_hi = (P.causal ? max(min(kl, p0 + 1), 0) : kl) >> 7;
+                all_hi = max(end(pa), 0) >> 7;
+                some_hi = warp_tok0 < sg->ntok ? (max(end(pb), 0) + 127) >> 7 : 0;
                 if constexpr (kMode == kWindow) {
-                    all_lo = (max(p0 + sg->ntok - P.window, 0) + 127) >> 7;
-                    all_sk = P.sinks >> 7;
+                    all_lo = (max(pb - P.window + 1, 0) + 127) >> 7;
+                    some_lo = max(pa - P.window + 1, 0) >> 7;
+                    all_sk = min(P.sinks, max(end(pa), 0)) >> 7;
+                    some_sk = warp_tok0 < sg->ntok ? (min(P.sinks, max(end(pb), 0)) + 127) >> 7 : 0;
                 }
             }
             const int32_t* list = kLists ? P.list + (int64_t)sg->list * P.cap + j0 : nullptr;
             const uint32_t* who = kLists ? P.list_who + ((int64_t)sg->list * P.cap + j0) * P.words : nullptr;
             float m[2] = {dead[0] ? 0.0f : -INFINITY, dead[1] ? 0.0f : -INFINITY};
             float l[2] = {0.0f, 0.0f};  // this thread's share of each row
+            bool fresh = true;
             int32_t kt_next = 0;
             uint32_t who_next[2] = {0u, 0u};
             auto look = [&](int32_t j) {
@@ -792,34 +798,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 else if constexpr (kMode == kWindow) kt = j0 + j < ns ? j0 + j : lo_t + j0 + j - ns;
                 else kt = j0 + j;
                 const int32_t kb = kt * 128;
-                bool listed[2] = {true, true};
-                bool masked = true, visible = true;
-                if constexpr (kLists) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) listed[x] = (who_next[x] >> (tok[x] & 31)) & 1u;
-                    if (j + 1 < n) look(j + 1);
-                } else {
-                    masked = kt >= all_hi || (kMode == kWindow && kt < all_lo && kt >= all_sk);
-                }
                 // bit 2 kk + e of vis[x]: row x sees this thread's column c0 + 8 kk + e
                 uint32_t vis[2] = {~0u, ~0u};
-                if (masked) {
+                bool masked, visible;
+                if constexpr (kLists) {
                     bool part = false, any = false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        vis[x] = columns_below(hi[x] - kb - c0);
-                        if constexpr (kMode == kWindow)
-                            vis[x] = (vis[x] & ~columns_below(lo[x] - kb - c0)) | columns_below(sk[x] - kb - c0);
-                        if (kLists && !listed[x]) vis[x] = 0u;
+                        const bool listed = (who_next[x] >> (tok[x] & 31)) & 1u;
+                        vis[x] = listed ? columns_below(hi[x] - kb - c0) : 0u;
                         part |= !dead[x] && vis[x] != ~0u;
                         any |= !dead[x] && vis[x] != 0u;
                     }
+                    if (j + 1 < n) look(j + 1);
                     masked = __any_sync(0xffffffffu, part);
                     visible = __any_sync(0xffffffffu, any);
+                } else {
+                    visible = (kt < some_hi && kt >= some_lo) || kt < some_sk;
+                    masked = visible && !((kt < all_hi && kt >= all_lo) || kt < all_sk);
+                    if (masked) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            vis[x] = columns_below(hi[x] - kb - c0);
+                            if constexpr (kMode == kWindow)
+                                vis[x] = (vis[x] & ~columns_below(lo[x] - kb - c0)) | columns_below(sk[x] - kb - c0);
+                        }
+                    }
                 }
                 const uint32_t pk = place_k(gb);
                 const bool wt = wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, status);
-                if (__any_sync(0xffffffffu, !wt || aborted(sh))) {
+                // (a failure elsewhere raises the status word, which ends this wait too)
+                if (__any_sync(0xffffffffu, !wt)) {
                     ok = false;
                     break;
                 }
@@ -848,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 };
                 load_s();
                 float alpha[2];
-                const bool rescale = softmax_rows(sc, dead, sl2, m, l, alpha, load_s);
+                const bool rescale = softmax_rows(sc, dead, sl2, fresh, m, l, alpha, load_s);
                 tmem_st16x128_x16(t_base + sbuf, sc);
                 if (rescale) {
                     // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
