@@ -635,24 +635,32 @@ class PagedBatch(ctypes.Structure):
 # microseconds, so the host's share counts: sizes and types are compared in
 # place, and what fails goes to the helpers above for its message.
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _where(ref, *ts):
     """The device index of the call, all of whose tensors must be there."""
-    import torch
-    dev = ref.device
+    dev = ref.get_device()
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             _same_device(ref, t)
-    if dev.type != "cuda":
+    if dev < 0:
+        _same_device(ref, *ts)
         raise ValueError("expected a CUDA tensor")
-    if dev.index != torch.cuda.current_device():
-        _current_device(dev)
-    return dev.index
+    if dev != _torch.cuda.current_device():
+        _current_device(ref.device)
+    return dev
 
 
 def _array(t, name, dtype, n):
-    """The address of a contiguous array of `dtype` with at least n entries (None: none)."""
-    if t is None:
-        return None
+    """The address of a contiguous array of `dtype` with at least n entries."""
     if t.dtype is not dtype or t.numel() < n:
         _flat(t, name, n, dtype)
     if not t.is_contiguous():
@@ -664,9 +672,8 @@ def _token_rows(t, name, tokens, heads, D):
     """The address of t [tokens, heads, D] bf16 and the distance between its
     tokens in elements; the heads of a token must be contiguous, the tokens
     need not be."""
-    import torch
-    if t.dtype is not torch.bfloat16:
-        _dtype(t, name, torch.bfloat16)
+    if t.dtype is not _torch.bfloat16:
+        _dtype(t, name, _torch.bfloat16)
     if t.shape != (tokens, heads, D):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
     a, b, c = t.stride()
@@ -677,43 +684,44 @@ def _token_rows(t, name, tokens, heads, D):
 
 def _paged_cache(k_cache, v_cache):
     """(k's address, v's address, pages, H_kv, page_size, D)."""
-    import torch
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must share the shape [pages, H_kv, page_size, D]")
-    return (_array(k_cache, "k_cache", torch.bfloat16, 0), _array(v_cache, "v_cache", torch.bfloat16, 0),
-            *k_cache.shape)
+    bf16 = _torch.bfloat16
+    return _array(k_cache, "k_cache", bf16, 0), _array(v_cache, "v_cache", bf16, 0), *shape
 
 
 def _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages):
-    import torch
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [seqs, max_pages]")
-    seqs, max_pages = page_table.shape
-    return PagedBatch(_array(page_table, "page_table", torch.int32, 0), _array(q_start, "q_start", torch.int32, seqs + 1),
-                      _array(kv_len, "kv_len", torch.int32, seqs), seqs, tokens, max_pages, page_size, n_pages)
+    shape = page_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"page_table: shape {tuple(shape)}, expected [seqs, max_pages]")
+    seqs, max_pages = shape
+    i32 = _torch.int32
+    return PagedBatch(_array(page_table, "page_table", i32, 0), _array(q_start, "q_start", i32, seqs + 1),
+                      _array(kv_len, "kv_len", i32, seqs), seqs, tokens, max_pages, page_size, n_pages)
 
 
 def _block_lists(sel, sel_cnt, tokens, H_kv):
     """(address of sel, of sel_cnt, width)."""
-    import torch
-    if sel.dim() != 3 or sel.shape[0] < tokens or sel.shape[1] != H_kv:
-        raise ValueError(f"sel: shape {tuple(sel.shape)}, expected [>= {tokens}, {H_kv}, width]")
-    return (_array(sel, "sel", torch.int32, 0), _array(sel_cnt, "sel_cnt", torch.int32, tokens * H_kv), sel.shape[2])
+    shape = sel.shape
+    if len(shape) != 3 or shape[0] < tokens or shape[1] != H_kv:
+        raise ValueError(f"sel: shape {tuple(shape)}, expected [>= {tokens}, {H_kv}, width]")
+    i32 = _torch.int32
+    return _array(sel, "sel", i32, 0), _array(sel_cnt, "sel_cnt", i32, tokens * H_kv), shape[2]
 
 
 def _scratch(need, workspace, device):
     """(the tensor that holds the scratch, its address, its bytes)."""
-    import torch
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif not workspace.is_contiguous():
+        workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _raw_stream(stream, device_index):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device_index) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(device_index) if stream is None else stream.cuda_stream
 
 
 def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None, q_out=None, rope=None,
@@ -724,8 +732,7 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
     q_out) normalised by q_norm / k_norm [D] and rotated by rope [positions,
     rot] (cosines, then sines) on the way; k_mean [pages, H_kv, D] receives the
     mean key of every 128-token block that fills up (see bsa.h)."""
-    import torch
-    bf16 = torch.bfloat16
+    bf16 = (_torch or _load_torch()).bfloat16
     kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
     tokens = k.shape[0]
     kp, ks = _token_rows(k, "k", tokens, H_kv, D)
@@ -737,16 +744,18 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
         H = q.shape[1]
         qp, qs = _token_rows(q, "q", tokens, H, D)
         op, os_ = _token_rows(q_out, "q_out", tokens, H, D)
-    rope_len = rot = 0
+    rp, rope_len, rot = None, 0, 0
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError(f"rope: shape {tuple(rope.shape)}, expected [positions, rot]")
+        rp = _array(rope, "rope", _torch.float32, 0)
         rope_len, rot = rope.shape
-    rp, qn, kn = _array(rope, "rope", torch.float32, 0), _array(q_norm, "q_norm", bf16, D), _array(k_norm, "k_norm", bf16, D)
-    km = _array(k_mean, "k_mean", bf16, n_pages * H_kv * D)
+    qn = _array(q_norm, "q_norm", bf16, D) if q_norm is not None else None
+    kn = _array(k_norm, "k_norm", bf16, D) if k_norm is not None else None
+    km = _array(k_mean, "k_mean", bf16, n_pages * H_kv * D) if k_mean is not None else None
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
     dev = _where(k_cache, v_cache, k, v, page_table, q_start, kv_len, q, q_out, rope, q_norm, k_norm, k_mean)
-    code = load_library().bsa_paged_append(
+    code = (_lib or load_library()).bsa_paged_append(
         ctypes.byref(b), qp, qs, kp, ks, vp, vs, H, H_kv, D, rp, rope_len, rot, 1 if interleaved else 0, qn, kn, eps,
         op, os_, kc, vc, km, _raw_stream(stream, dev))
     if code:
@@ -767,7 +776,7 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
     width] / sel_cnt [tokens, H_kv] restrict each token to its listed 128-token
     blocks (see bsa.h).  ``workspace`` is a CUDA tensor of at least
     forward_paged_workspace_size() bytes (allocated here when omitted)."""
-    import torch
+    torch = _torch or _load_torch()
     kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
@@ -784,7 +793,7 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
         sp, cp, width = _block_lists(sel, sel_cnt, tokens, H_kv)
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
     dev = _where(k_cache, v_cache, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, workspace)
-    lib = load_library()
+    lib = _lib or load_library()
     ref = ctypes.byref(b)
     keep, ws, nbytes = _scratch(lib.bsa_forward_paged_workspace_size(ref, H, H_kv, D, width), workspace, q.device)
     code = lib.bsa_forward_paged(ref, qp, qs, kc, vc, H, H_kv, D, 1 if causal else 0, window, sinks, sp, cp, width,
@@ -807,7 +816,7 @@ def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_s
     width] (ascending, tail -1) and sel_cnt [tokens, H_kv] (see bsa.h).
     ``workspace`` is a CUDA tensor of at least select_paged_workspace_size()
     bytes (allocated here when omitted)."""
-    import torch
+    torch = _torch or _load_torch()
     if k_mean.dim() != 3 or q.dim() != 3:
         raise ValueError("select_paged: q [tokens, H, D], k_mean [pages, H_kv, D]")
     n_pages, H_kv, D = k_mean.shape
@@ -817,7 +826,7 @@ def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_s
     sp, cp, width = _block_lists(sel, sel_cnt, tokens, H_kv)
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
     dev = _where(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, workspace)
-    lib = load_library()
+    lib = _lib or load_library()
     ref = ctypes.byref(b)
     keep, ws, nbytes = _scratch(lib.bsa_select_paged_workspace_size(ref, H, H_kv, D), workspace, q.device)
     code = lib.bsa_select_paged(ref, qp, qs, mp, H, H_kv, D, topk, sink_blocks, local_blocks, ws, nbytes, sp, cp, width,
