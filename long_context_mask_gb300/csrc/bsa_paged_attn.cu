@@ -45,9 +45,12 @@
 // tile g - 3 has read it), so that the next segment's scores are there when the
 // softmax comes to them.
 //
-// Slots behind the end of a sequence hold anything, NaN included.  Their
-// scores are dropped by a select, and the value rows behind the end are
-// zeroed in shared memory before the product (0 times NaN is NaN).
+// What a row does not see may hold anything, NaN and infinities included.  Its
+// scores are dropped by a select, and the value rows behind the end of a
+// sequence are zeroed in shared memory before the product (0 times NaN is NaN).
+// A value that one row of a tile sees and another does not cannot be zeroed: a
+// row whose O comes out not finite, and that has a key hidden in its segment,
+// is computed again from its own keys alone (see own_keys_row).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -77,6 +80,9 @@ constexpr int kThreads = 32 * 16;
 constexpr int kDesc = 4;                                  // segment descriptors in flight
 constexpr int kConsumers = kSoftmaxWarps + kStoreWarps + 3;  // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 bf16
+
+// kMode: which keys a row sees besides the causal and length limits.
+enum { kPlain = 0, kWindow = 1, kListed = 2 };
 
 template <int D>
 struct Cfg {
@@ -132,6 +138,8 @@ struct Params {
     int32_t H, H_kv, group, tpt;  // tpt: tokens of a query tile
     int32_t causal, window, sinks;
     float scale_log2;
+    const __nv_bfloat16 *q, *k_cache, *v_cache;  // for own_keys_row
+    int64_t q_stride;
     __nv_bfloat16* o;
     float* lse;
     // lists (null: every visible key tile): tile f = kvh * nt_cap + i
@@ -144,6 +152,65 @@ struct Params {
     float2* part_ml;          // [runs, 2, 128] maximum (log2) and sum
     int4* joins;              // [runs] parts (0: none), q0, ntok, kvh
 };
+
+// O = sum_j 2^(s_j - m) v_j of one row over the keys of a segment that the row
+// sees, read from the cache one by one; to out (fp32, unscaled) or, times inv, to
+// orow.  The whole warp works on it, lane l values l D / 32 ..: slow, and for rows
+// next to values that are not finite only.
+template <int D, int kMode>
+__device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, int32_t tok, int32_t head, float m, float inv,
+                                          __nv_bfloat16* orow, float* out) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = D / 32;
+    const int32_t p = sg.pos0 + tok, hi = P.causal ? min(sg.kl, p + 1) : sg.kl;
+    const int32_t lo = kMode == kWindow ? p - P.window + 1 : 0, sk = kMode == kWindow ? min(P.sinks, hi) : 0;
+    const int32_t page = P.b.page;
+    const int32_t* table = P.b.table + (int64_t)sg.seq * P.b.max_pages;
+    const __nv_bfloat16* q = P.q + (int64_t)(sg.q0 + tok) * P.q_stride + (int64_t)(sg.kvh * P.group + head) * D;
+    float acc[kPer] = {};
+    for (int32_t j = 0; j < sg.n; ++j) {
+        int32_t kt;
+        bool listed = true;
+        if constexpr (kMode == kListed) {
+            const int64_t e = (int64_t)sg.list * P.cap + sg.j0 + j;
+            kt = P.list[e];
+            listed = (P.list_who[e * P.words + (tok >> 5)] >> (tok & 31)) & 1u;
+        } else {
+            kt = sg.j0 + j < sg.ns ? sg.j0 + j : sg.lo + sg.j0 + j - sg.ns;
+        }
+        if (!listed) continue;
+        for (int32_t k0 = 0; k0 < 128; k0 += 32) {
+            const int32_t key = kt * 128 + k0 + lane;
+            const bool see = (key < hi && key >= lo) || key < sk;
+            int64_t row = 0;
+            float pj = 0.f;
+            if (see) {
+                int32_t id = table[key / page];
+                if (id < 0 || id >= P.b.n_pages) id = 0;  // (reported by the loading warps)
+                row = (((int64_t)id * P.H_kv + sg.kvh) * page + key % page) * D;
+                float dot = 0.f;
+                for (int d = 0; d < D; d += 2) {
+                    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(q + d));
+                    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(P.k_cache + row + d));
+                    dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+                }
+                pj = exp2f(fmaf(dot, P.scale_log2, -m));
+            }
+            for (uint32_t bits = __ballot_sync(0xffffffffu, see); bits; bits &= bits - 1u) {
+                const int i = __ffs(bits) - 1;
+                const float w = __shfl_sync(0xffffffffu, pj, i);
+                const int64_t r = __shfl_sync(0xffffffffu, row, i);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) acc[x] = fmaf(w, __bfloat162float(P.v_cache[r + lane * kPer + x]), acc[x]);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        if (out != nullptr) out[lane * kPer + x] = acc[x];
+        else orow[lane * kPer + x] = __float2bfloat16_rn(acc[x] * inv);
+    }
+}
 
 __device__ __forceinline__ void set_abort(Shared* sh, int32_t* status) {
     *reinterpret_cast<volatile int32_t*>(&sh->abort) = 1;
@@ -191,10 +258,10 @@ __device__ __forceinline__ int32_t key_tiles(const Params& P, int32_t pos0, int3
 }
 
 // The run is cut by cost: a query tile of n key tiles counts n + kRowCost, the
-// constant for its start and epilogue (measured: a causal prompt's blocks, 7 to
-// 58 query tiles each, end within 3 % of each other with it, 20 % without).
+// constant for its start and its end.  (A causal prompt of 8192, whose blocks have
+// 8 to 50 query tiles each: 394 us with 1, 369 with 2, 358 with 4, 363 with 6.)
 // A cut x units into the query tile leaves cut_at(x) of its key tiles on the left.
-constexpr int32_t kRowCost = 2;
+constexpr int32_t kRowCost = 4;
 __device__ __forceinline__ int32_t row_units(int32_t n) { return max(n, 1) + kRowCost; }
 __device__ __forceinline__ int32_t cut_at(int32_t x) { return max(x - kRowCost, 0); }
 
@@ -253,9 +320,6 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
     fresh = __any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY);
     return rescale;
 }
-
-// kMode: which keys a row sees besides the causal and length limits.
-enum { kPlain = 0, kWindow = 1, kListed = 2 };
 
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_constant__ Params P) {
@@ -905,7 +969,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             const int32_t n = sp->n, slot = sp->slot;
             const bool dead = tok >= sp->ntok;
             const int64_t at = (int64_t)(sp->q0 + tok) * P.H + sp->kvh * P.group + head;
-            hand_back(k);
             __nv_bfloat16* orow = P.o + at * D;
             if (n == 0) {
                 // no key at all: O = 0, LSE = -inf
@@ -914,6 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(orow + c) = make_uint4(0, 0, 0, 0);
                     P.lse[at] = -INFINITY;
                 }
+                hand_back(k);
                 continue;
             }
             const uint32_t pv = place_v(g + (uint32_t)n - 1u);
@@ -924,45 +988,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             const float2 ml = sh->ml[row];
             mbar_arrive(smem_u32(&sh->ml_empty));
             tc_fence_after();
-            if (slot < 0) {
-                // 1 / l; 0 for a row without a key, NaN where l is
-                const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+            // 1 / l; 0 for a row without a key, NaN where l is
+            const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
+            const int64_t part = (int64_t)max(slot, 0) * 128 + row;
+            bool finite = true;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_row + c, o);
+                tmem_wait_ld();
+                // (a sum that overflows says "not finite" too: the row is computed again for nothing)
+                float sum = 0.0f;
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32], pk[16];
-                    tmem_ld32(t_row + c, o);
-                    tmem_wait_ld();
+                for (int i = 0; i < 32; ++i) sum += __uint_as_float(o[i]);
+                finite &= sum - sum == 0.0f;
+                if (dead) continue;
+                if (slot < 0) {
+                    uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                    if (!dead) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh->o_free));
-                if (!dead)
-                    P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
-            } else {
-                const int64_t part = (int64_t)slot * 128 + row;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(t_row + c, o);
-                    tmem_wait_ld();
-                    if (!dead) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
-                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh->o_free));
-                if (!dead) P.part_ml[part] = ml;
             }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh->o_free));
+            if (!dead) {
+                if (slot < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+                else P.part_ml[part] = ml;
+            }
+            uint32_t again = __ballot_sync(0xffffffffu, !finite && !dead);
+            if (again != 0u) {
+                // rows that see every key of the segment's tiles are what they are
+                const int32_t x = sp->j0 + n - 1, end = kLists ? sp->kl : (sp->lo + x - sp->ns + 1) * 128;
+                const bool hides = kMode != kPlain || (P.causal && sp->pos0 + tok + 1 < min(sp->kl, end));
+                again = __ballot_sync(0xffffffffu, !finite && !dead && hides);
+                __syncwarp();  // the row's own thread has written it
+                for (; again; again &= again - 1u) {
+                    const int i = __ffs(again) - 1;
+                    const float mi = __shfl_sync(0xffffffffu, ml.x, i), li = __shfl_sync(0xffffffffu, inv, i);
+                    const int64_t ai = __shfl_sync(0xffffffffu, at, i), pi = __shfl_sync(0xffffffffu, part, i);
+                    own_keys_row<D, kMode>(P, *sp, __shfl_sync(0xffffffffu, tok, i), __shfl_sync(0xffffffffu, head, i), mi, li,
+                                           P.o + ai * D, slot < 0 ? nullptr : P.part_o + pi * D);
+                }
+            }
+            hand_back(k);
             g += (uint32_t)n;
             ++segs;
         }
@@ -977,8 +1054,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
 
 // Joins the parts of split rows: O = sum_c 2^(m_c - M) O_c / l with M the
 // largest m_c and l = sum_c 2^(m_c - M) l_c, parts in key order.  Thread block
-// (c, y) takes rows y kJoinRows .. of the row tile that begins in each run p c of
-// k_paged_forward: the run's slot 1, then slot 0 of the following runs.
+// (c, y) takes kJoinThreads / (D / 4) rows of the query tile that begins in each of
+// k_paged_forward's block c's runs: the run's slot 1, then slot 0 of the runs after it.
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ Params P) {
@@ -991,25 +1068,43 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
     for (int32_t p = 0; p < kPhases; ++p) {
         const int32_t run = p * gridDim.x + blockIdx.x;
         const int4 jn = P.joins[run];
-        if (jn.x == 0 || r >= jn.z * P.group) continue;
-        auto part = [&](int32_t x) -> int64_t { return (((int64_t)run + x) * 2 + (x == 0 ? 1 : 0)) * 128 + r; };
-        float M = -INFINITY;
-#pragma unroll 4
-        for (int32_t x = 0; x < jn.x; ++x) M = fmaxf(M, P.part_ml[part(x)].x);
-        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int32_t x = 0; x < jn.x; ++x) {
-            const float2 ml = P.part_ml[part(x)];
-            const float4 v = *reinterpret_cast<const float4*>(P.part_o + part(x) * D + 4 * c);
-            // (none: no visible key in this part)
-            const bool none = ml.x == -INFINITY && ml.y == 0.0f;
-            const float f = exp2f(ml.x - M);
-            l = none ? l : fmaf(f, ml.y, l);
-            o[0] = none ? o[0] : fmaf(f, v.x, o[0]);
-            o[1] = none ? o[1] : fmaf(f, v.y, o[1]);
-            o[2] = none ? o[2] : fmaf(f, v.z, o[2]);
-            o[3] = none ? o[3] : fmaf(f, v.w, o[3]);
+        const int32_t rows = jn.z * P.group;
+        if (jn.x == 0 || (int32_t)(blockIdx.y * kRows) >= rows) continue;
+        const bool live = r < rows;  // (the others' threads take part in the shuffles)
+        auto part = [&](int32_t x) -> int64_t {
+            return (((int64_t)run + x) * 2 + (x == 0 ? 1 : 0)) * 128 + (live ? r : 0);
+        };
+        float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        // kLanes parts at a time, each thread the maximum and sum of one: all loads at once
+        for (int32_t x0 = 0; x0 < jn.x; x0 += kLanes) {
+            const int32_t n = min(jn.x - x0, kLanes);
+            const float2 ml = c < n ? P.part_ml[part(x0 + c)] : make_float2(-INFINITY, 0.0f);
+            const bool none = ml.x == -INFINITY && ml.y == 0.0f;  // no visible key in this part
+            float top = ml.x;
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float M_new = fmaxf(M, top);
+            const float keep = M == -INFINITY ? 1.0f : exp2f(M - M_new);  // (l and o are 0 still)
+            M = M_new;
+            const float f = none ? 0.0f : exp2f(ml.x - M);
+            float sum = none ? 0.0f : f * ml.y;
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l = fmaf(l, keep, sum);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= keep;
+#pragma unroll 8
+            for (int32_t x = 0; x < n; ++x) {
+                const float fx = __shfl_sync(0xffffffffu, f, x, kLanes);
+                const bool skip = __shfl_sync(0xffffffffu, (int)none, x, kLanes) != 0;
+                const float4 v = *reinterpret_cast<const float4*>(P.part_o + part(x0 + x) * D + 4 * c);
+                o[0] = skip ? o[0] : fmaf(fx, v.x, o[0]);
+                o[1] = skip ? o[1] : fmaf(fx, v.y, o[1]);
+                o[2] = skip ? o[2] : fmaf(fx, v.z, o[2]);
+                o[3] = skip ? o[3] : fmaf(fx, v.w, o[3]);
+            }
         }
+        if (!live) continue;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at = (int64_t)(jn.y + r / P.group) * P.H + jn.w * P.group + r % P.group;
         *reinterpret_cast<uint2*>(P.o + at * D + 4 * c) =
@@ -1188,6 +1283,10 @@ bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int3
     P.window = a.window;
     P.sinks = a.sinks;
     P.scale_log2 = (a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D)) * kLog2e;
+    P.q = static_cast<const __nv_bfloat16*>(a.q);
+    P.q_stride = a.q_stride;
+    P.k_cache = static_cast<const __nv_bfloat16*>(a.k_cache);
+    P.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
     P.o = static_cast<__nv_bfloat16*>(a.o);
     P.lse = a.lse;
     uint8_t* ws = static_cast<uint8_t*>(workspace);

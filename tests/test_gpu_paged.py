@@ -273,6 +273,61 @@ def test_many_sequences():
     ref.check_attention(b, q, o, lse)
 
 
+HIDDEN = dict(future=dict(), window=dict(window=150, sinks=5), lists="lists")
+
+
+@pytest.mark.parametrize("kind", HIDDEN)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H,K,D,page", [(4, 2, 128, 128), (14, 2, 64, 16), (2, 2, 128, 32)])
+def test_what_a_row_does_not_see_does_not_reach_it(H, K, D, page, bad, kind):
+    """Keys and values that are not finite, at places that some rows of a tile see and
+    others do not: those that do not get what they get without them."""
+    b = ref.make([120, 40, 1], [1500, 300, 700], H=H, H_kv=K, D=D, page=page, seed=37)
+    q = ref.rows(b, H, 38)
+    kw, sel = HIDDEN[kind], None
+    if kind == "lists":
+        s, c, sel = lists_for(b, np.random.default_rng(39), 6)
+        kw = dict(sel=s, sel_cnt=c)
+    places = [(0, 1439, 3), (0, 1290, 0), (0, 2, 1), (1, 270, 5), (1, 299, 7), (2, 400, 2)]  # sequence, position, column
+    good = b.k_cache.clone(), b.v_cache.clone()
+    o0, lse0 = run_forward(b, q, **kw)
+    ref.check_attention(b, q, o0, lse0, **(dict(sel=sel) if sel else kw))
+    sees = torch.zeros(b.tokens, K, dtype=torch.bool, device="cuda")
+    starts = b.q_start.tolist()
+    for s, pos, col in places:
+        for cache in (b.k_cache, b.v_cache):
+            cache[b.table[s, pos // page], :, pos % page, col] = bad
+        for i in range(b.new[s]):
+            p = b.length[s] - b.new[s] + i
+            see = pos <= p and (kind != "window" or pos > p - 150 or pos < 5)
+            for h in range(K):
+                sees[starts[s] + i, h] |= see and (sel is None or pos // 128 in sel[starts[s] + i][h])
+    o, lse = run_forward(b, q, **kw)
+    status_ok()
+    hit = sees.repeat_interleave(H // K, 1)
+    assert hit.any() and not hit.all()
+    assert torch.isfinite(o[~hit].float()).all()
+    b.k_cache, b.v_cache = good
+    keep = o.clone(), lse.clone()
+    keep[0][hit], keep[1][hit] = o0[hit], lse0[hit]
+    ref.check_attention(b, q, *keep, **(dict(sel=sel) if sel else kw))
+    if bad != bad:
+        assert torch.isnan(o[hit].float()).any(-1).all() and torch.isnan(lse[hit]).all()
+
+
+def test_a_query_that_is_not_finite_stays_alone():
+    b = ref.make([70, 3], [500, 300], H=8, H_kv=2, D=128, page=64, seed=40)
+    q = ref.rows(b, 8, 41)
+    o0, lse0 = run_forward(b, q)
+    q[11, 3, 7], q[40, 0, 0] = float("nan"), float("inf")
+    o, lse = run_forward(b, q)
+    status_ok()
+    same = torch.ones(b.tokens, 8, dtype=torch.bool, device="cuda")
+    same[11, 3] = same[40, 0] = False
+    assert torch.equal(bits(o)[same], bits(o0)[same]) and torch.equal(lse[same], lse0[same])
+    assert torch.isnan(o[~same].float()).all()
+
+
 def test_the_same_call_gives_the_same_bits():
     b = ref.make([1, 1, 130], [15000, 7000, 4000], H=8, H_kv=2, D=128, page=64, seed=33)
     q = ref.rows(b, 8, 34)
