@@ -13,9 +13,9 @@
 // page of the block's last token.
 //
 // Work mapping.  A thread block takes one 128-position block that a sequence's
-// new tokens touch and four rows of each token: four query heads, or the key and
-// the value of two key/value heads.  The block that writes a head's keys writes
-// all of this position block's, so the mean needs no other's work and adds in a
+// new tokens touch and either four query heads of its tokens (long chunks: of one
+// half of them), or the key and the value of one key/value head, two tokens at a
+// time.  The block that writes a head's keys writes all of this position block's, so the mean needs no other's work and adds in a
 // fixed order, whatever chunks the tokens came in.  A row of D values is held by
 // D / 8 neighbouring threads, eight values each: where the whole head turns by
 // halves, four of either half (a pair meets in one thread), else eight in a row,
@@ -48,6 +48,7 @@ struct AppendParams {
     float eps;
     int32_t H_kv, group;
     int32_t q_blocks;  // thread blocks (y) of query heads; those of keys and values follow
+    int32_t q_parts;   // of a position block's tokens that a thread block of query heads takes one of: 1 or 2
     int32_t page_shift;
 };
 
@@ -189,6 +190,52 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     blk += max(first, 0) / kBlock;
     const int32_t base = blk * kBlock;
     const int32_t lo = max(max(first, 0), base), hi = min(q.kl, base + kBlock);  // new positions of this block
+    const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    const bool queries = (int32_t)blockIdx.y < P.q_blocks;
+    const int32_t h0 = queries ? 4 * (blockIdx.y / P.q_parts) : blockIdx.y - P.q_blocks;  // first head
+    const int32_t heads = min(4, P.H_kv * P.group - h0);  // (of queries)
+    if (P.rope != nullptr && hi > P.rope_len && threadIdx.x == 0) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
+    const __nv_bfloat16* w = queries ? P.q_norm : P.k_norm;
+    float wf[8];
+    if (w != nullptr) unpack8(load_row<D, kHalves>(w, c), wf);
+    if (queries) {
+        int32_t from = lo, to = hi;
+        if (P.q_parts == 2) {
+            if (blockIdx.y & 1) from = max(lo, base + kBlock / 2);
+            else to = min(hi, base + kBlock / 2);
+        }
+        // With kHalves the next token's rows are on their way while this one's are worked
+        // on (46.7 -> 44.1 us); the other forms need the registers (11.3 us, 12.8 with it).
+        uint4 next[4];
+        auto fetch = [&](int32_t pos) {
+            const __nv_bfloat16* src = P.q + ((int64_t)q.q0 + (pos - first)) * P.q_stride + h0 * D;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                next[u] = pos < to && u < heads ? load_row<D, kHalves>(src + u * D, c) : make_uint4(0, 0, 0, 0);
+        };
+        if constexpr (kHalves) fetch(from + sub);
+        for (int32_t p0 = from; p0 < to; p0 += kRows) {
+            // whole warps stay in the loop: the shuffles need them
+            const int32_t pos = p0 + sub;
+            if constexpr (!kHalves) fetch(pos);
+            uint4 raw[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) raw[u] = next[u];
+            Angles a{};
+            if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
+            if constexpr (kHalves) fetch(pos + kRows);
+            __nv_bfloat16* out = P.q_out + ((int64_t)q.q0 + (pos - first)) * P.qo_stride + h0 * D;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float x[8];
+                unpack8(raw[u], x);
+                if (w != nullptr) norm_row<D>(x, wf, P.eps);
+                if (P.rope != nullptr) rotate_row<kHalves>(P, x, c, a);
+                if (pos < to && u < heads) store_row<D, kHalves>(out + u * D, c, pack8(x));
+            }
+        }
+        return;
+    }
     const int32_t page = P.b.page, per = kBlock / page;
     if (threadIdx.x < per) {
         const int32_t at = base / page + threadIdx.x;
@@ -204,84 +251,67 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     }
     __syncthreads();
 
-    const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-    const bool queries = (int32_t)blockIdx.y < P.q_blocks;
-    const int32_t h0 = queries ? 4 * blockIdx.y : 2 * (blockIdx.y - P.q_blocks);  // first head
-    const int32_t heads = queries ? min(4, P.H_kv * P.group - h0) : min(2, P.H_kv - h0);
-    if (P.rope != nullptr && hi > P.rope_len && threadIdx.x == 0) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
-    const __nv_bfloat16* w = queries ? P.q_norm : P.k_norm;
-    float wf[8];
-    if (w != nullptr) unpack8(load_row<D, kHalves>(w, c), wf);
-    for (int32_t p0 = lo; p0 < hi; p0 += kRows) {
-        // whole warps stay in the loop: the shuffles need them
-        const int32_t pos = p0 + sub;
-        const bool live = pos < hi;
-        const int64_t tok = (int64_t)q.q0 + (pos - first);
-        uint4 raw[4];
-        __nv_bfloat16* dst[4];  // null: no such row
-        if (queries) {
-            const __nv_bfloat16* src = P.q + tok * P.q_stride + h0 * D;
-            __nv_bfloat16* out = P.q_out + tok * P.qo_stride + h0 * D;
+    uint4 next[2][2];  // [token][key, value]
+    auto fetch = [&](int32_t p0) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                dst[u] = live && u < heads ? out + u * D : nullptr;
-                raw[u] = dst[u] != nullptr ? load_row<D, kHalves>(src + u * D, c) : make_uint4(0, 0, 0, 0);
-            }
-        } else {
-            const __nv_bfloat16* ks = P.k + tok * P.k_stride + h0 * D;
-            const __nv_bfloat16* vs = P.v + tok * P.v_stride + h0 * D;
-            const int32_t id = live ? pages[(pos - base) >> P.page_shift] : -1;
-            const int64_t slot = ((((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1))) * D;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool mine = live && (u >> 1) < heads;
-                raw[u] = mine ? load_row<D, kHalves>((u & 1 ? vs : ks) + (u >> 1) * D, c) : make_uint4(0, 0, 0, 0);
-                dst[u] = mine && id >= 0 ? (u & 1 ? P.v_cache : P.k_cache) + slot + (int64_t)((u >> 1) * page) * D : nullptr;
-            }
+        for (int u = 0; u < 2; ++u) {
+            const int32_t pos = p0 + u * kRows + sub;
+            const int64_t tok = (int64_t)q.q0 + (pos - first);
+            next[u][0] = pos < hi ? load_row<D, kHalves>(P.k + tok * P.k_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
+            next[u][1] = pos < hi ? load_row<D, kHalves>(P.v + tok * P.v_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
         }
-        Angles a{};
-        if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
+    };
+    if constexpr (kHalves) fetch(lo);
+    for (int32_t p0 = lo; p0 < hi; p0 += 2 * kRows) {
+        if constexpr (!kHalves) fetch(p0);
+        uint4 raw[2][2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (!queries && (u & 1)) {  // a value's row is written as it came
-                if (dst[u] != nullptr) store_row<D, kHalves>(dst[u], c, raw[u]);
-                continue;
-            }
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) raw[u][x] = next[u][x];
+        if constexpr (kHalves) fetch(p0 + 2 * kRows);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t pos = p0 + u * kRows + sub;
+            Angles a{};
+            if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
             float x[8];
-            unpack8(raw[u], x);
+            unpack8(raw[u][0], x);
             if (w != nullptr) norm_row<D>(x, wf, P.eps);
             if (P.rope != nullptr) rotate_row<kHalves>(P, x, c, a);
-            if (dst[u] != nullptr) store_row<D, kHalves>(dst[u], c, pack8(x));
+            const int32_t id = pos < hi ? pages[(pos - base) >> P.page_shift] : -1;
+            if (id >= 0) {
+                const int64_t slot = ((((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1))) * D;
+                store_row<D, kHalves>(P.k_cache + slot, c, pack8(x));
+                store_row<D, kHalves>(P.v_cache + slot, c, raw[u][1]);
+            }
         }
     }
 
-    if (queries) return;
     if (P.k_mean == nullptr || hi != base + kBlock) return;  // (the whole thread block agrees)
     // the block is full: the mean of its 128 keys as the cache holds them
     const int32_t last = pages[per - 1];
     bool whole = true;
     for (int p = 0; p < per; ++p) whole &= pages[p] >= 0;
     if (!whole) return;
-    for (int32_t h = h0; h < h0 + heads; ++h) {
-        __syncthreads();  // the keys above are written; sums is free again
-        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    __syncthreads();  // the keys above are written
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-        for (int p = sub; p < kBlock; p += kRows) {
-            const __nv_bfloat16* row = P.k_cache + (((int64_t)pages[p / page] * P.H_kv + h) * page + p % page) * D;
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4*>(row + 8 * c), f);
+    for (int p = sub; p < kBlock; p += kRows) {
+        const __nv_bfloat16* row = P.k_cache + (((int64_t)pages[p / page] * P.H_kv + h0) * page + p % page) * D;
+        float f[8];
+        unpack8(*reinterpret_cast<const uint4*>(row + 8 * c), f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += f[j];
-        }
+        for (int j = 0; j < 8; ++j) acc[j] += f[j];
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[sub][8 * c + j] = acc[j];
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float t = 0.f;
+    for (int j = 0; j < 8; ++j) sums[sub][8 * c + j] = acc[j];
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float t = 0.f;
 #pragma unroll
-            for (int g = 0; g < kRows; ++g) t += sums[g][threadIdx.x];
-            P.k_mean[((int64_t)last * P.H_kv + h) * D + threadIdx.x] = __float2bfloat16_rn(t * (1.0f / kBlock));
-        }
+        for (int g = 0; g < kRows; ++g) t += sums[g][threadIdx.x];
+        P.k_mean[((int64_t)last * P.H_kv + h0) * D + threadIdx.x] = __float2bfloat16_rn(t * (1.0f / kBlock));
     }
 }
 
@@ -311,10 +341,13 @@ bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaSt
     P.H_kv = a.H_kv;
     P.group = a.H / a.H_kv;
     P.page_shift = __builtin_ctz((unsigned)a.page);
-    P.q_blocks = a.q != nullptr ? (a.H + 3) / 4 : 0;
+    // long chunks: blocks of half as many tokens fill the card more evenly (8192 tokens,
+    // 32 + 8 heads: 46 us with whole ones); short ones find their place half as often
+    P.q_parts = a.tokens / a.seqs >= kBlock ? 2 : 1;
+    P.q_blocks = a.q != nullptr ? (a.H + 3) / 4 * P.q_parts : 0;
     // a sequence's n > 0 new tokens touch at most (n + 126) / 128 + 1 blocks
     const int64_t units = (int64_t)a.tokens / kBlock + 2 * (int64_t)a.seqs;
-    const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + (a.H_kv + 1) / 2));
+    const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + a.H_kv));
     const bool halves = a.rope != nullptr && a.rot == a.D && !a.interleaved;
     const auto kernel = a.D == 128 ? (halves ? k_paged_append<128, true> : k_paged_append<128, false>)
                                    : (halves ? k_paged_append<64, true> : k_paged_append<64, false>);
