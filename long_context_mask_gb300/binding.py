@@ -710,10 +710,15 @@ def _block_lists(sel, sel_cnt, tokens, H_kv):
     return _array(sel, "sel", i32, 0), _array(sel_cnt, "sel_cnt", i32, tokens * H_kv), shape[2]
 
 
-def _scratch(need, workspace, device):
+def _scratch(need, workspace, device, stream):
     """(the tensor that holds the scratch, its address, its bytes)."""
     if workspace is None:
-        workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
+        if stream is None:
+            workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
+        else:
+            # from the memory of the stream that uses it: it goes back there when the call returns
+            with _torch.cuda.stream(_torch.cuda.ExternalStream(stream.cuda_stream, device=device)):
+                workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
@@ -795,7 +800,7 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
     dev = _where(k_cache, v_cache, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, workspace)
     lib = _lib or load_library()
     ref = ctypes.byref(b)
-    keep, ws, nbytes = _scratch(lib.bsa_forward_paged_workspace_size(ref, H, H_kv, D, width), workspace, q.device)
+    keep, ws, nbytes = _scratch(lib.bsa_forward_paged_workspace_size(ref, H, H_kv, D, width), workspace, q.device, stream)
     code = lib.bsa_forward_paged(ref, qp, qs, kc, vc, H, H_kv, D, 1 if causal else 0, window, sinks, sp, cp, width,
                                  scale, ws, nbytes, op, lp, _raw_stream(stream, dev))
     if code:
@@ -828,7 +833,7 @@ def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_s
     dev = _where(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, workspace)
     lib = _lib or load_library()
     ref = ctypes.byref(b)
-    keep, ws, nbytes = _scratch(lib.bsa_select_paged_workspace_size(ref, H, H_kv, D), workspace, q.device)
+    keep, ws, nbytes = _scratch(lib.bsa_select_paged_workspace_size(ref, H, H_kv, D), workspace, q.device, stream)
     code = lib.bsa_select_paged(ref, qp, qs, mp, H, H_kv, D, topk, sink_blocks, local_blocks, ws, nbytes, sp, cp, width,
                                 _raw_stream(stream, dev))
     if code:
