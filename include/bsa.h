@@ -736,8 +736,9 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
  *     and (sel == NULL or j / 128 is among the token's listed blocks):
  *     s_j = (q . k_j) * scale,  LSE = ln sum_j exp(s_j),
  *     O = sum_j exp(s_j - LSE) v_j.
- * Without any such key O = 0 and LSE = -inf.  What lies in slots behind the
- * end of a sequence does not matter, NaN included.
+ * Without any such key O = 0 and LSE = -inf.  Keys and values that a row does
+ * not see (masked, not listed, behind the end of the sequence) do not matter,
+ * NaN and infinities included; rows next to such values take longer.
  *
  *  q          device bf16, 16-byte aligned.
  *  causal     0 or 1.   window, sinks  >= 0; window must be 0 with sel.
@@ -749,7 +750,7 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
  *             a negative count (taken as 0) and an entry that is no block of
  *             the sequence (left out) raise BSA_ERR_BOUNDS.  Blocks behind
  *             the token's position are left out in silence when causal.
- *  sel_width  >= 1 with sel, else 0.
+ *  sel_width  1 .. 2^20 with sel, else 0.
  *  scale      <= 0 selects 1/sqrt(D); a NaN or infinite scale is rejected.
  *  workspace  device scratch of at least bsa_forward_paged_workspace_size()
  *             bytes, 16-byte aligned; its contents on entry do not matter.

@@ -587,7 +587,7 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
 
 size_t bsa_forward_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
                                         int32_t sel_width) {
-    if (paged_sizes(b, H, H_kv, D) != BSA_OK || sel_width < 0) return 0;
+    if (paged_sizes(b, H, H_kv, D) != BSA_OK || sel_width < 0 || sel_width > (1 << 20)) return 0;
     return bsa::paged_forward_workspace(paged_forward_args(b, H, H_kv, D, sel_width));
 }
 
@@ -600,7 +600,7 @@ bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_
     const bsa_status c = paged_sizes(b, H, H_kv, D);
     if (c != BSA_OK) return c;
     if ((causal != 0 && causal != 1) || window < 0 || sinks < 0 || !scale_ok(scale)) return BSA_ERR_INVALID_ARG;
-    if (sel ? (!sel_cnt || sel_width < 1 || window > 0 || !aligned(sel, 4) || !aligned(sel_cnt, 4)) : sel_width != 0)
+    if (sel ? (!sel_cnt || sel_width < 1 || sel_width > (1 << 20) || window > 0 || !aligned(sel, 4) || !aligned(sel_cnt, 4)) : sel_width != 0)
         return BSA_ERR_INVALID_ARG;
     if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
     if (!paged_arrays(b) || !token_rows(q, q_stride, H, D)) return BSA_ERR_INVALID_ARG;

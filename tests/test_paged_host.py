@@ -227,3 +227,10 @@ def test_select_takes_the_documented_calls(lib, kw):
     dict(sel=i32(T, H, 6)), dict(sel=i32(T, K * 6)), dict(sel_cnt=i32(T, K - 1)), dict(kv_len=i32(S - 1))])
 def test_select_refuses(lib, kw):
     rejected(call_select, **kw)
+
+
+def test_lists_of_any_use_fit(lib):
+    """Lists are at most 2^20 entries wide."""
+    assert forward(lib, sel=FAKE, cnt=FAKE, width=(1 << 20) + 1) == INVALID
+    assert lib.bsa_forward_paged_workspace_size(ctypes.byref(batch()), 8, 4, 128, (1 << 20) + 1) == 0
+    assert lib.bsa_forward_paged_workspace_size(ctypes.byref(batch()), 8, 4, 128, 1 << 20) > 0
