@@ -66,6 +66,8 @@
 namespace bsa {
 namespace {
 
+// positions lie within 2^24 of zero: longer windows are no longer, and position - window stays in 32 bits
+constexpr int32_t kMaxWindow = 1 << 26;
 constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s per wait
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -119,6 +121,7 @@ struct Shared {
     uint64_t ml_full, ml_empty;  // a segment's maxima and sums are in ml, have been read
     uint64_t mma_done;
     uint64_t seg_full[kDesc], seg_empty[kDesc];
+    uint64_t busy;            // when a key tile of a row computed from its own keys was last done
     Segment seg[kDesc];
     float2 ml[128];           // of a segment's rows: maximum (log2) and sum (before: block_prefix's words)
     int32_t start[kPhases][5];  // of each run the first unit: key/value head, sequence, query tile, unit; tile within the head
@@ -155,11 +158,12 @@ struct Params {
 
 // O = sum_j 2^(s_j - m) v_j of one row over the keys of a segment that the row
 // sees, read from the cache one by one; to out (fp32, unscaled) or, times inv, to
-// orow.  The whole warp works on it, lane l values l D / 32 ..: slow, and for rows
-// next to values that are not finite only.
+// orow.  The whole warp works on it, lane l values l D / 32 ..: slow (a row and
+// key tile take some 10 us), and for rows next to values that are not finite only;
+// busy tells the warps that wait meanwhile that it goes on.
 template <int D, int kMode>
 __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, int32_t tok, int32_t head, float m, float inv,
-                                          __nv_bfloat16* orow, float* out) {
+                                          __nv_bfloat16* orow, float* out, uint64_t* busy) {
     const int lane = threadIdx.x & 31;
     constexpr int kPer = D / 32;
     const int32_t p = sg.pos0 + tok, hi = P.causal ? min(sg.kl, p + 1) : sg.kl;
@@ -189,21 +193,50 @@ __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, in
                 if (id < 0 || id >= P.b.n_pages) id = 0;  // (reported by the loading warps)
                 row = (((int64_t)id * P.H_kv + sg.kvh) * page + key % page) * D;
                 float dot = 0.f;
-                for (int d = 0; d < D; d += 2) {
-                    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(q + d));
-                    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(P.k_cache + row + d));
-                    dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+#pragma unroll 8
+                for (int d = 0; d < D; d += 8) {
+                    const uint4 a4 = *reinterpret_cast<const uint4*>(q + d);
+                    const uint4 b4 = *reinterpret_cast<const uint4*>(P.k_cache + row + d);
+                    const __nv_bfloat162 *a2 = reinterpret_cast<const __nv_bfloat162*>(&a4),
+                                         *b2 = reinterpret_cast<const __nv_bfloat162*>(&b4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = __bfloat1622float2(a2[i]), b = __bfloat1622float2(b2[i]);
+                        dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+                    }
                 }
                 pj = exp2f(fmaf(dot, P.scale_log2, -m));
             }
-            for (uint32_t bits = __ballot_sync(0xffffffffu, see); bits; bits &= bits - 1u) {
-                const int i = __ffs(bits) - 1;
-                const float w = __shfl_sync(0xffffffffu, pj, i);
-                const int64_t r = __shfl_sync(0xffffffffu, row, i);
+            const uint32_t seen = __ballot_sync(0xffffffffu, see);
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 8) {
+                __nv_bfloat162 v[8][kPer / 2];
 #pragma unroll
-                for (int x = 0; x < kPer; ++x) acc[x] = fmaf(w, __bfloat162float(P.v_cache[r + lane * kPer + x]), acc[x]);
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t r = __shfl_sync(0xffffffffu, row, i0 + i);
+#pragma unroll
+                    for (int x = 0; x < kPer / 2; ++x)
+                        v[i][x] = (seen >> (i0 + i)) & 1u
+                                      ? *reinterpret_cast<const __nv_bfloat162*>(P.v_cache + r + lane * kPer + 2 * x)
+                                      : __nv_bfloat162{};
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, pj, i0 + i);
+#pragma unroll
+                    for (int x = 0; x < kPer / 2; ++x) {
+                        const float2 f = __bfloat1622float2(v[i][x]);
+                        acc[2 * x] = fmaf(w, f.x, acc[2 * x]);
+                        acc[2 * x + 1] = fmaf(w, f.y, acc[2 * x + 1]);
+                    }
+                }
             }
         }
+        if (lane == 0) *reinterpret_cast<volatile uint64_t*>(busy) = globaltimer();
+        bool nan = true;  // all of them: they stay so
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) nan &= acc[x] != acc[x];
+        if (__all_sync(0xffffffffu, nan)) break;
     }
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
@@ -216,15 +249,31 @@ __device__ __forceinline__ void set_abort(Shared* sh, int32_t* status) {
     *reinterpret_cast<volatile int32_t*>(&sh->abort) = 1;
     raise_status(status, BSA_ERR_TIMEOUT);
 }
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int32_t* status) {
-    return mbar_wait(bar, parity, kWaitNs, status, BSA_ERR_TIMEOUT);
+// A bounded wait.  While rows are computed from their own keys (sh->busy moves on with
+// every key tile of them) those who wait for them have not lost a second yet.  All but
+// the first look is out of line: the kernel waits in some twenty places, and a window's
+// short rows are sensitive to its length.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const volatile uint64_t* busy, const volatile int32_t* status) {
+    const uint64_t t0 = globaltimer();
+    uint32_t n = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        if ((++n & 255u) == 0) {
+            const uint64_t now = globaltimer(), last = *busy;
+            if (now - t0 > kWaitNs && (now < last || now - last > kWaitNs)) return false;
+            if (*status == BSA_ERR_TIMEOUT) return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Shared* sh, int32_t* status) {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, &sh->busy, status);
 }
 // For copies and products in flight, after a failure too.
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int32_t* status) {
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity, int32_t* status) {
     if (!mbar_wait(bar, parity, kWaitNs, status, -1)) raise_status(status, BSA_ERR_TIMEOUT);
 }
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* status) {
-    return __all_sync(0xffffffffu, wait(bar, parity, status));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Shared* sh, int32_t* status) {
+    return __all_sync(0xffffffffu, wait(bar, parity, sh, status));
 }
 
 // a / b; nearly every dividend fits 32 bits, whose division is much shorter.
@@ -363,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         // (the producer writes them again where a row is split)
 #pragma unroll
         for (int p = 0; p < kPhases; ++p) P.joins[p * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
+        sh->busy = 0;
         // a block of this launch (or an unread earlier one) timed out: abandon
         sh->abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
     }
@@ -491,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     // Segment k, for the warps that read descriptors (null: no more); they hand
     // it back when they are through with it.
     auto next_segment = [&](uint32_t k, bool& ok) -> const Segment* {
-        if (!wait_warp(smem_u32(&sh->seg_full[k % kDesc]), (k / kDesc) & 1u, status)) {
+        if (!wait_warp(smem_u32(&sh->seg_full[k % kDesc]), (k / kDesc) & 1u, sh, status)) {
             ok = false;
             return nullptr;
         }
@@ -543,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 held += row[i] >= 0;
             }
             const uint32_t pos = is_v ? place_v(g) : place_k(g), slot = pos % S;
-            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, status)) return false;
+            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, sh, status)) return false;
             if (elect_one()) {
                 const uint32_t fb = smem_u32(&sh->full[slot]), dst = s_ring + slot * C::kTile;
                 mbar_arrive_expect_tx(fb, (uint32_t)(held * page * D * 2));
@@ -610,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 const int64_t c = end <= longer ? (end - 1) / (share + 1) : extra + (end - 1 - longer) / share;
                 P.joins[run] = make_int4((int32_t)(c - run + 1), sg.q0, ntok, kvh);
             }
-            if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
+            if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, sh, status)) {
                 ok = false;
                 break;
             }
@@ -644,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
         }
         }
-        if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, status)) {
+        if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, sh, status)) {
             if (lane == 0) {
                 sh->seg[k % kDesc].n = -1;
                 mbar_arrive(smem_u32(&sh->seg_full[k % kDesc]));
@@ -689,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             hand_back(k);
             if (n == 0) continue;
             // the segment before is done with the query tile's place
-            if (nq > 0) ok = wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, status);
+            if (nq > 0) ok = wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, sh, status);
             if (!ok) break;
             if (elect_one()) {
                 const bool one = ntok == 1;
@@ -700,15 +750,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, kvh * P.group, q0, bar);
             }
             __syncwarp();
-            ok = wait_warp(smem_u32(&sh->q_full), nq++ & 1u, status);
+            ok = wait_warp(smem_u32(&sh->q_full), nq++ & 1u, sh, status);
             for (int32_t j = 0; j < n && ok; ++j, ++g) {
                 if (g >= kSBuf) {
                     // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
                     const uint32_t pv = place_v(g - kSBuf);
-                    ok = wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
+                    ok = wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, sh, status);
                 }
                 const uint32_t pos = place_k(g), slot = pos % S;
-                ok = ok && wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
+                ok = ok && wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, sh, status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ks = dk + (uint64_t)((slot * C::kTile) >> 4);
@@ -755,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             if (n == 0) continue;
             for (int32_t j = 0; j < n && ok; ++j, ++g) {
                 const uint32_t pos = place_v(g), slot = pos % S;
-                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, status);
+                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, sh, status);
                 if (ok && j == n - 1 && tail < 128) {
                     // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
                     const uint32_t tile = s_ring + slot * C::kTile;
@@ -767,9 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                ok = ok && wait_warp(smem_u32(&sh->p_full[g % kSBuf]), (g / kSBuf) & 1u, status);
+                ok = ok && wait_warp(smem_u32(&sh->p_full[g % kSBuf]), (g / kSBuf) & 1u, sh, status);
                 // a segment's first product overwrites O: the epilogue before must have read it
-                if (ok && j == 0 && segs > 0) ok = wait_warp(smem_u32(&sh->o_free), (segs - 1u) & 1u, status);
+                if (ok && j == 0 && segs > 0) ok = wait_warp(smem_u32(&sh->o_free), (segs - 1u) & 1u, sh, status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
@@ -890,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     }
                 }
                 const uint32_t pk = place_k(gb);
-                const bool wt = wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, status);
+                const bool wt = wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, sh, status);
                 // (a failure elsewhere raises the status word, which ends this wait too)
                 if (__any_sync(0xffffffffu, !wt)) {
                     ok = false;
@@ -926,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 if (rescale) {
                     // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
                     const uint32_t pv = place_v(gb - 1u);
-                    const bool wv = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
+                    const bool wv = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, sh, status);
                     if (__any_sync(0xffffffffu, !wv)) {
                         ok = false;
                         break;
@@ -942,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             hand_back(k);
             // maxima and sums of the rows to the storing warps
             const float la = row_sum4(l[0]), lb = row_sum4(l[1]);
-            if (__any_sync(0xffffffffu, !wait(smem_u32(&sh->ml_empty), (segs & 1u) ^ 1u, status))) {
+            if (__any_sync(0xffffffffu, !wait(smem_u32(&sh->ml_empty), (segs & 1u) ^ 1u, sh, status))) {
                 ok = false;
                 break;
             }
@@ -982,8 +1032,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
             const uint32_t pv = place_v(g + (uint32_t)n - 1u);
             // (the last product is the segment's: the next one waits for o_free)
-            ok = wait_warp(smem_u32(&sh->ml_full), segs & 1u, status) &&
-                 wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, status);
+            ok = wait_warp(smem_u32(&sh->ml_full), segs & 1u, sh, status) &&
+                 wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, sh, status);
             if (!ok) break;
             const float2 ml = sh->ml[row];
             mbar_arrive(smem_u32(&sh->ml_empty));
@@ -1036,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     const float mi = __shfl_sync(0xffffffffu, ml.x, i), li = __shfl_sync(0xffffffffu, inv, i);
                     const int64_t ai = __shfl_sync(0xffffffffu, at, i), pi = __shfl_sync(0xffffffffu, part, i);
                     own_keys_row<D, kMode>(P, *sp, __shfl_sync(0xffffffffu, tok, i), __shfl_sync(0xffffffffu, head, i), mi, li,
-                                           P.o + ai * D, slot < 0 ? nullptr : P.part_o + pi * D);
+                                           P.o + ai * D, slot < 0 ? nullptr : P.part_o + pi * D, &sh->busy);
                 }
             }
             hand_back(k);
@@ -1280,7 +1330,7 @@ bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int3
     P.group = G;
     P.tpt = L.tpt;
     P.causal = a.causal;
-    P.window = a.window;
+    P.window = min(a.window, kMaxWindow);
     P.sinks = a.sinks;
     P.scale_log2 = (a.scale > 0.f ? a.scale : 1.0f / sqrtf((float)D)) * kLog2e;
     P.q = static_cast<const __nv_bfloat16*>(a.q);

@@ -664,3 +664,109 @@ def test_two_graphs_share_a_workspace_and_streams_do_not():
     for (o, lse), (wo, wl) in zip(outs, want):
         assert torch.equal(bits(o), bits(wo)) and torch.equal(lse, wl)
     status_ok()
+
+
+# ------------------------------------------------------------------ the far ends
+
+def test_caches_beyond_32_bits():
+    """The same batch in pages at the end of a cache of 2.3e9 values gives the same bits."""
+    H, K, D, page, pages = 8, 2, 128, 128, 70000
+    b = ref.make([1, 130, 257], [3000, 1500, 257], H=H, H_kv=K, D=D, page=page, seed=100)
+    q, k, v = ref.rows(b, H, 101), ref.rows(b, K, 102), ref.rows(b, K, 103)
+    rope = ref.rope_table(3000, D)
+    km = torch.randn((b.n_pages, K, D), generator=torch.Generator().manual_seed(104)).to(torch.bfloat16).cuda()
+    at = pages - b.n_pages
+    far = dict(table=torch.where(b.table >= 0, b.table + at, b.table), means=torch.zeros((pages, K, D), dtype=torch.bfloat16, device="cuda"))
+    far["means"][at:] = km
+    for x in ("k_cache", "v_cache"):
+        far[x] = torch.zeros((pages, K, page, D), dtype=torch.bfloat16, device="cuda")
+        far[x][at:] = getattr(b, x)
+    assert far["k_cache"].numel() > 1 << 31
+    outs = []
+    for kc, vc, table, means in ((b.k_cache, b.v_cache, b.table, km), (far["k_cache"], far["v_cache"], far["table"], far["means"])):
+        batch = (table, b.q_start, b.kv_len)
+        qr, o = torch.empty_like(q), torch.empty_like(q)
+        lse, o2, lse2 = torch.empty((b.tokens, H), device="cuda"), torch.empty_like(q), torch.empty((b.tokens, H), device="cuda")
+        sel = torch.empty((b.tokens, K, 6), dtype=torch.int32, device="cuda")
+        cnt = torch.empty((b.tokens, K), dtype=torch.int32, device="cuda")
+        bsa.paged_append(k, v, kc, vc, *batch, q=q, q_out=qr, rope=rope, k_mean=means)
+        bsa.select_paged(qr, means, *batch, sel, cnt, page_size=page, topk=4)
+        bsa.forward_paged(qr, kc, vc, *batch, o, lse, sel=sel, sel_cnt=cnt)
+        bsa.forward_paged(qr, kc, vc, *batch, o2, lse2)
+        status_ok()
+        first = 0 if kc is b.k_cache else at
+        outs.append((qr, o, o2, lse, lse2, sel, cnt, means[first:], kc[first:].nan_to_num(3.0), vc[first:].nan_to_num(3.0)))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+    assert not far["k_cache"][:at].any() and not far["v_cache"][:at].any() and not far["means"][:at].any()
+
+
+def test_windows_of_any_length():
+    """A window longer than any sequence is none, with tokens before position 0 too."""
+    b = ref.make([1, 300, 200], [700, 300, 150], H=4, H_kv=2, D=64, page=32, seed=105)
+    q = ref.rows(b, 4, 106)
+    o, lse = run_forward(b, q)
+    for window in (1 << 20, 2 ** 31 - 1):
+        for sinks in (0, 2 ** 31 - 1):
+            o2, lse2 = run_forward(b, q, window=window, sinks=sinks)
+            assert torch.equal(bits(o2), bits(o)) and torch.equal(lse2, lse)
+    status_ok()
+    ref.check_attention(b, q, o, lse)
+
+
+def test_scratch_of_another_stream_is_not_reused_early():
+    """Calls on a stream that is busy, without a workspace, while the current one allocates and writes."""
+    b = ref.make([1, 60, 2], [9000, 3000, 20000], H=8, H_kv=2, D=128, page=64, seed=107)
+    q = ref.rows(b, 8, 108)
+    km = torch.randn((b.n_pages, 2, 128), generator=torch.Generator().manual_seed(109)).to(torch.bfloat16).cuda()
+    sel = torch.empty((b.tokens, 2, 10), dtype=torch.int32, device="cuda")
+    cnt = torch.empty((b.tokens, 2), dtype=torch.int32, device="cuda")
+
+    def go(o, lse, stream=None):
+        bsa.select_paged(q, km, *b.arrays(), sel, cnt, page_size=64, topk=8, stream=stream)
+        bsa.forward_paged(q, b.k_cache, b.v_cache, *b.arrays(), o, lse, sel=sel, sel_cnt=cnt, stream=stream)
+
+    want, got = [(torch.empty_like(q), torch.empty((b.tokens, 8), device="cuda")) for _ in range(2)]
+    go(*want)
+    sel0, cnt0 = sel.clone(), cnt.clone()
+    sizes = (bsa.select_paged_workspace_size(3, b.tokens, b.table.shape[1], 64, 8, 2, 128),
+             bsa.forward_paged_workspace_size(3, b.tokens, b.table.shape[1], 64, 8, 2, 128, 10))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    go(*got, stream=side)
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    status_ok()
+    assert len(junk) == 6 and torch.equal(sel, sel0) and torch.equal(cnt, cnt0)
+    assert torch.equal(bits(got[0]), bits(want[0])) and torch.equal(got[1], want[1])
+
+
+def test_rows_next_to_values_that_are_not_finite_over_a_long_cache():
+    """Every row has an infinite value at its first key and all but the last of a sequence a NaN
+    behind their own: 128 rows of 2^19 keys are computed from their own keys by one thread block,
+    which takes longer than a wait may last without progress."""
+    n, L, S = 128, 1 << 19, 152
+    dev = "cuda"
+    k = torch.zeros((L // 128, 1, 128, 64), dtype=torch.bfloat16, device=dev)
+    v = torch.ones_like(k)
+    v[0, 0, 0, 0] = float("inf")
+    v[-1, 0, -1, 1] = float("nan")
+    table = torch.arange(L // 128, dtype=torch.int32, device=dev).repeat(S, 1)
+    start = torch.arange(S + 1, dtype=torch.int32, device=dev) * n
+    length = torch.full((S,), L, dtype=torch.int32, device=dev)
+    q = torch.randn((S * n, 1, 64), generator=torch.Generator().manual_seed(110)).to(torch.bfloat16).to(dev)
+    o, lse = torch.empty_like(q), torch.empty((S * n, 1), device=dev)
+    bsa.forward_paged(q, k, v, table, start, length, o, lse)
+    status_ok()
+    want = torch.ones((S, n, 64), device=dev)
+    want[:, :, 0] = float("inf")
+    want[:, -1, 1] = float("nan")
+    got = o.view(S, n, 64).float()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+    fin = want.isfinite()
+    assert ((got - want)[fin].abs() <= 2.0 ** -7).all()
+    keys = torch.arange(L - n + 1, L + 1, dtype=torch.float64, device=dev)
+    # a sum of ones in fp32, its parts at most 2^19: exact; a logarithm and a product
+    assert ((lse.view(S, n).double() - keys.log()).abs() <= 8 * 2.0 ** -24 * (1 + keys.log())).all()
