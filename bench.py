@@ -78,11 +78,15 @@ def load_peaks():
 
 def kernel_source_hash():
     """Hash of the forward kernel's code: comments and whitespace are dropped,
-    so that a comment edit does not orphan the recorded ncu counters."""
+    so that a comment edit does not orphan the recorded ncu counters.  The
+    device headers (.cuh) that these files include belong to it."""
+    csrc = os.path.join(ROOT, "long_context_mask_gb300", "csrc")
+    files = ["bsa_attn.cu", "bsa_ptx.cuh", "bsa_math.cuh", "bsa_gather0.cuh"]
     h = hashlib.sha256()
-    for f in ("bsa_attn.cu", "bsa_ptx.cuh", "bsa_math.cuh", "bsa_gather0.cuh"):
-        with open(os.path.join(ROOT, "long_context_mask_gb300", "csrc", f), encoding="utf-8") as fh:
+    for f in files:
+        with open(os.path.join(csrc, f), encoding="utf-8") as fh:
             src = fh.read()
+        files += [i for i in re.findall(r'#include "(\w+\.cuh)"', src) if i not in files]
         src = re.sub(r"/\*.*?\*/", " ", src, flags=re.S)
         src = re.sub(r"//[^\n]*", " ", src)
         h.update(" ".join(src.split()).encode())
