@@ -51,6 +51,15 @@
 // A value that one row of a tile sees and another does not cannot be zeroed: a
 // row whose O comes out not finite, and that has a key hidden in its segment,
 // is computed again from its own keys alone (see own_keys_row).
+//
+// Measured, 32 + 8 heads of 128: 64 tokens over 1.7 GB of keys and values 254 us
+// (the copy rate); one token over 131072 86 us and 5 for the join (6.2 TB/s); a
+// prompt of 8192 344 us (0.84 of the burst rate of a plain product), where the
+// tensor core is busy 70 % of the time and the softmax hardly ever waits: 1,370
+// cycles a tile pair, of which loading the scores takes 160, the exponentials of two
+// warps to a scheduler 800 (512 is the least), storing 130.  Two groups of softmax
+// warps on alternate tiles (392 us) and halves of a tile loaded ahead (378 us) were
+// slower: what they overlap they lose to a tile's longer way.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
