@@ -171,9 +171,9 @@ struct Params {
 // key tile take some 10 us), and for rows next to values that are not finite only;
 // busy tells the warps that wait meanwhile that it goes on.
 template <int D, int kMode>
-__device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, int32_t tok, int32_t head, float m, float inv,
-                                          __nv_bfloat16* orow, float* out, uint64_t* busy) {
+__device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, int32_t row_of_tile, float m, float inv, uint64_t* busy) {
     const int lane = threadIdx.x & 31;
+    const int32_t tok = row_of_tile / P.group, head = row_of_tile - tok * P.group;
     constexpr int kPer = D / 32;
     const int32_t p = sg.pos0 + tok, hi = P.causal ? min(sg.kl, p + 1) : sg.kl;
     const int32_t lo = kMode == kWindow ? p - P.window + 1 : 0, sk = kMode == kWindow ? min(P.sinks, hi) : 0;
@@ -202,7 +202,7 @@ __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, in
                 if (id < 0 || id >= P.b.n_pages) id = 0;  // (reported by the loading warps)
                 row = (((int64_t)id * P.H_kv + sg.kvh) * page + key % page) * D;
                 float dot = 0.f;
-#pragma unroll 8
+#pragma unroll 4
                 for (int d = 0; d < D; d += 8) {
                     const uint4 a4 = *reinterpret_cast<const uint4*>(q + d);
                     const uint4 b4 = *reinterpret_cast<const uint4*>(P.k_cache + row + d);
@@ -247,9 +247,11 @@ __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, in
         for (int x = 0; x < kPer; ++x) nan &= acc[x] != acc[x];
         if (__all_sync(0xffffffffu, nan)) break;
     }
+    __nv_bfloat16* orow = P.o + ((int64_t)(sg.q0 + tok) * P.H + sg.kvh * P.group + head) * D;
+    float* part = P.part_o + ((int64_t)max(sg.slot, 0) * 128 + row_of_tile) * D;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-        if (out != nullptr) out[lane * kPer + x] = acc[x];
+        if (sg.slot >= 0) part[lane * kPer + x] = acc[x];
         else orow[lane * kPer + x] = __float2bfloat16_rn(acc[x] * inv);
     }
 }
@@ -1093,9 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 for (; again; again &= again - 1u) {
                     const int i = __ffs(again) - 1;
                     const float mi = __shfl_sync(0xffffffffu, ml.x, i), li = __shfl_sync(0xffffffffu, inv, i);
-                    const int64_t ai = __shfl_sync(0xffffffffu, at, i), pi = __shfl_sync(0xffffffffu, part, i);
-                    own_keys_row<D, kMode>(P, *sp, __shfl_sync(0xffffffffu, tok, i), __shfl_sync(0xffffffffu, head, i), mi, li,
-                                           P.o + ai * D, slot < 0 ? nullptr : P.part_o + pi * D, &sh->busy);
+                    own_keys_row<D, kMode>(P, *sp, qd * 32 + i, mi, li, &sh->busy);
                 }
             }
             hand_back(k);
