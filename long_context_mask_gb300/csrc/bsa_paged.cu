@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     ptx::wait_primary();
     int32_t blk;
     PagedSeq q;
-    const int32_t s = find_unit(
+    const int32_t s = find_unit<kAppendThreads>(
         P.b, blockIdx.x,
         [](const PagedSeq& q) -> int64_t {
             // 128-position blocks that the new tokens touch (those at positions >= 0)

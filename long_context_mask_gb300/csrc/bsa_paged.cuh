@@ -62,10 +62,12 @@ __device__ __forceinline__ bool paged_seq(const PagedBatch& b, int32_t s, PagedS
     return ok;
 }
 
-// Exclusive prefix sum over the thread block (a multiple of 32 threads, at
-// most 1024); total receives the block's sum.  part: 33 words of shared memory.
+// Exclusive prefix sum over the thread block of kThreads; total receives the
+// block's sum.  part: kThreads / 32 words of shared memory.
+template <int kThreads>
 __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* part, int64_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    constexpr int warps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t incl = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -76,6 +78,7 @@ __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* part, int64_
     if (lane == 31) part[warp] = incl;
     __syncthreads();
     int64_t before = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < warps; ++w) {
         const int64_t v = part[w];
         before += w < warp ? v : 0;
@@ -89,12 +92,12 @@ __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* part, int64_
 // (-1: u is beyond the last), the unit within it and the sequence's entry.
 // Called by the whole thread block; the same answer in every thread.  part: see
 // block_prefix; hit: 5 words of shared memory.
-template <typename Count>
+template <int kThreads, typename Count>
 __device__ __forceinline__ int32_t find_unit(const PagedBatch& b, int64_t u, Count&& count, int64_t* part, int32_t* hit,
                                              int32_t& within, PagedSeq& found) {
     if (threadIdx.x == 0) hit[0] = -1;
     int64_t base = 0;
-    for (int32_t s0 = 0; s0 < b.seqs; s0 += blockDim.x) {
+    for (int32_t s0 = 0; s0 < b.seqs; s0 += kThreads) {
         const int32_t s = s0 + threadIdx.x;
         PagedSeq q{0, 0, 0};
         int64_t n = 0;
@@ -103,7 +106,7 @@ __device__ __forceinline__ int32_t find_unit(const PagedBatch& b, int64_t u, Cou
             n = count(q);
         }
         int64_t total;
-        const int64_t at = base + block_prefix(n, part, total);
+        const int64_t at = base + block_prefix<kThreads>(n, part, total);
         if (n > 0 && u >= at && u < at + n) {
             hit[0] = s;
             hit[1] = (int32_t)(u - at);

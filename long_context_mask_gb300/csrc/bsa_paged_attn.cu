@@ -134,6 +134,7 @@ struct Shared {
     Segment seg[kDesc];
     float2 ml[128];           // of a segment's rows: maximum (log2) and sum (before: block_prefix's words)
     int32_t start[kPhases][5];  // of each run the first unit: key/value head, sequence, query tile, unit; tile within the head
+    PagedSeq start_seq[kPhases];  // its sequence's entry
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     }
     launch_dependents();
     wait_primary();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kThreads - 1) {  // (the first threads have the batch to read)
         // (the producer writes them again where a row is split)
 #pragma unroll
         for (int p = 0; p < kPhases; ++p) P.joins[p * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             seq_kl[s] = q.kl;
             mine += (q.nq + P.tpt - 1) / P.tpt + (q.nq > 0 ? (int64_t)((q.kl + 127) >> 7) << 32 : 0);
         }
-        int64_t at = block_prefix(mine, reinterpret_cast<int64_t*>(sh->ml), all) & 0xffffffff;
+        int64_t at = block_prefix<kThreads>(mine, reinterpret_cast<int64_t*>(sh->ml), all) & 0xffffffff;
         kv_tiles = all >> 32;
         all &= 0xffffffff;
         for (int32_t s = a; s < e; ++s) {
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 const int32_t first = t * P.tpt, nq = seq_nq[s], kl = seq_kl[s];
                 n = key_tiles(P, kl - nq + first, min(P.tpt, nq - first), kl, lo, ns);
             }
-            if (visit(kvh, i, s, t, row_units(n))) return;
+            if (visit(kvh, i, s, t, row_units(n)) || f + 1 == f1) return;
             ++i;
             if (i == nt) {
                 i = 0;
@@ -497,11 +498,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         }
     };
     int64_t mine = 0, total;
-    walk([&](int32_t, int32_t, int32_t, int32_t, int32_t n) {
+    int4 only = make_int4(0, 0, 0, 0);  // a thread with one tile need not walk again,
+    PagedSeq only_seq{0, 0, 0};         // and has its sequence at hand when it is asked for
+    walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
         mine += n;
+        only = make_int4(kvh, s, t, i);
+        if (f1 - f0 == 1) paged_seq(P.b, s, only_seq);
         return false;
     });
-    const int64_t before = block_prefix(mine, reinterpret_cast<int64_t*>(sh->ml), total);
+    const int64_t before = block_prefix<kThreads>(mine, reinterpret_cast<int64_t*>(sh->ml), total);
     const int64_t units = kLists ? total : total * P.H_kv;
     // runs: one for each thread block, or where key tiles are read several times and
     // do not all stay in L2, several (of 16 units at least)
@@ -521,19 +526,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         const int64_t u0 = run_start(p * blocks + blockIdx.x);
         const int64_t head = kLists ? 0 : divide(u0, total), r = kLists ? u0 : u0 - head * total;
         if (r >= before && r < before + mine) {
-            int64_t at = before;
-            walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
-                if (r < at + n) {
-                    sh->start[p][0] = kLists ? kvh : (int32_t)head;
-                    sh->start[p][1] = s;
-                    sh->start[p][2] = t;
-                    sh->start[p][3] = (int32_t)(r - at);
-                    sh->start[p][4] = i;
-                    return true;
-                }
-                at += n;
-                return false;
-            });
+            auto begin = [&](int32_t kvh, int32_t i, int32_t s, int32_t t, int64_t at) {
+                sh->start[p][0] = kLists ? kvh : (int32_t)head;
+                sh->start[p][1] = s;
+                sh->start[p][2] = t;
+                sh->start[p][3] = (int32_t)(r - at);
+                sh->start[p][4] = i;
+            };
+            if (f1 - f0 == 1) {
+                begin(only.x, only.w, only.y, only.z, before);
+                sh->start_seq[p] = only_seq;
+            } else {
+                int64_t at = before;
+                walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
+                    if (r < at + n) {
+                        begin(kvh, i, s, t, at);
+                        paged_seq(P.b, s, sh->start_seq[p]);
+                        return true;
+                    }
+                    at += n;
+                    return false;
+                });
+            }
         }
     }
     const bool abandoned = sh->abort != 0;
@@ -637,8 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         const int32_t run = p * blocks + blockIdx.x;
         int32_t kvh = sh->start[p][0], s = sh->start[p][1], t = sh->start[p][2], x0 = sh->start[p][3], i = sh->start[p][4];
         int64_t u = run_start(run), left = run_start(run + 1) - u;
-        PagedSeq q;
-        paged_seq(P.b, s, q);
+        PagedSeq q = sh->start_seq[p];
         while (left > 0 && ok) {
             const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
             Segment sg;
@@ -664,13 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             sg.j0 = j0;
             sg.n = n_row == 0 ? 0 : j1 - j0;
             sg.slot = j0 == 0 && j1 == n_eff ? -1 : 2 * run + (j0 == 0 ? 1 : 0);
-            if (lane == 0 && last && j0 == 0) {
-                // a split row begins here; its last part is in the run of its last unit
-                const int64_t end = u + (w - x0);
-                const int64_t longer = (share + 1) * extra;  // units of the longer runs
-                const int64_t c = end <= longer ? (end - 1) / (share + 1) : extra + (end - 1 - longer) / share;
-                P.joins[run] = make_int4((int32_t)(c - run + 1), sg.q0, ntok, kvh);
-            }
             if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, sh, status)) {
                 ok = false;
                 break;
@@ -687,6 +693,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             __syncwarp();
             ++k;
             ok = load_tiles(sg, false, g);
+            if (lane == 0 && last && j0 == 0) {
+                // a split row begins here; its last part is in the run of its last unit
+                const int64_t end = u + (w - x0);
+                const int64_t longer = (share + 1) * extra;  // units of the longer runs
+                const int64_t c = end <= longer ? divide(end - 1, share + 1) : extra + divide(end - 1 - longer, share);
+                P.joins[run] = make_int4((int32_t)(c - run + 1), sg.q0, ntok, kvh);
+            }
             // on to the next query tile
             left -= w - x0;
             u += w - x0;
@@ -1194,7 +1207,7 @@ __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_cons
     wait_primary();
     int32_t t;
     PagedSeq q;
-    const int32_t s = find_unit(
+    const int32_t s = find_unit<kUnionThreads>(
         P.b, blockIdx.x, [&](const PagedSeq& y) -> int64_t { return (y.nq + P.tpt - 1) / P.tpt; }, part, hit, t, q);
     if (s < 0) return;
     const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
@@ -1230,7 +1243,7 @@ __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_cons
             if (x < nb)
                 for (int32_t w = 0; w < P.words; ++w) any |= bits[x * P.words + w];
             int64_t total;
-            const int32_t at = done + (int32_t)block_prefix(any != 0u ? 1 : 0, part, total);
+            const int32_t at = done + (int32_t)block_prefix<kUnionThreads>(any != 0u ? 1 : 0, part, total);
             if (any != 0u && at < P.cap) {
                 P.list[f * P.cap + at] = b0 + x;
                 for (int32_t w = 0; w < P.words; ++w) P.who[(f * P.cap + at) * P.words + w] = bits[x * P.words + w];

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_paged_scores(const __grid_con
     ptx::wait_primary();
     int32_t t;
     PagedSeq y;
-    const int32_t s = find_unit(
+    const int32_t s = find_unit<kScoreThreads>(
         P.b, blockIdx.x, [](const PagedSeq& q) -> int64_t { return (q.nq + kTileTok - 1) / kTileTok; }, part, hit, t, y);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         for (int32_t x = threadIdx.x; x < P.b.seqs; x += kScoreThreads) {
