@@ -28,7 +28,7 @@ namespace bsa {
 namespace {
 
 constexpr int kScoreThreads = 256;
-constexpr int kTileTok = 64, kTileBlk = 128;  // tokens and blocks of a score tile
+constexpr int kTileTok = 64, kTileBlk = 64;  // tokens and blocks of a score tile
 constexpr int kFewTok = 4;                    // tokens up to which a tile is read as a decoding step
 // Most roundings on a product's way into a score: its own and the additions of
 // the 64-long chain (D / 2 values, every second) of the product tile, the last
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_paged_scores(const __grid_con
         float* qs = tile;
         float* ms = tile + kTileTok * kRow;
         __syncthreads();
-        constexpr int kDeep = 4;  // loads in flight for each thread
+        constexpr int kDeep = kTileBlk / kRows < 4 ? kTileBlk / kRows : 4;  // loads in flight for each thread
         for (int32_t x0 = 0; x0 < kTileBlk; x0 += kRows * kDeep) {
             uint4 v[kDeep];
 #pragma unroll
@@ -288,25 +288,26 @@ __global__ void __launch_bounds__(kScoreThreads) k_paged_scores(const __grid_con
             *reinterpret_cast<float4*>(qs + k * kRow + 8 * c + 4) = make_float4(f[4], f[5], f[6], f[7]);
         }
         __syncthreads();
-        // thread (ty, tx): tokens 4 ty .. 4 ty + 3, blocks tx + 16 j (j < 8); even and
+        // thread (ty, tx): tokens 4 ty .. 4 ty + 3, blocks tx + 16 j (j < kCols); even and
         // odd values of d add up apart
         const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+        constexpr int kCols = kTileBlk / 16;
         if (4 * ty < ntok) {
-            uint64_t acc[4][8];
+            uint64_t acc[4][kCols];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i][j] = 0ull;
+                for (int j = 0; j < kCols; ++j) acc[i][j] = 0ull;
 #pragma unroll 1
             for (int d = 0; d < D; d += 4) {
-                ulonglong2 m[8];
+                ulonglong2 m[kCols];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[j] = *reinterpret_cast<const ulonglong2*>(ms + (tx + 16 * j) * kRow + d);
+                for (int j = 0; j < kCols; ++j) m[j] = *reinterpret_cast<const ulonglong2*>(ms + (tx + 16 * j) * kRow + d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qs + (4 * ty + i) * kRow + d);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[i][j] = fma2(q.y, m[j].y, fma2(q.x, m[j].x, acc[i][j]));
+                    for (int j = 0; j < kCols; ++j) acc[i][j] = fma2(q.y, m[j].y, fma2(q.x, m[j].x, acc[i][j]));
                 }
             }
 #pragma unroll
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_paged_scores(const __grid_con
                 const int32_t k = 4 * ty + i;
                 if (k >= ntok) break;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kCols; ++j) {
                     const int32_t x = tx + 16 * j;
                     float a, b;
                     f2unpack(acc[i][j], a, b);
