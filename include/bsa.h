@@ -669,7 +669,7 @@ bsa_status bsa_upscale_threshold(const float* T_base, int64_t heads, int32_t Ub,
  *   seqs 0 .. 16384; tokens 0 .. 2^24 with tokens * H < 2^31 (0 of either:
  *   nothing to do); page_size 16, 32, 64 or 128; max_pages * page_size <=
  *   2^24; n_pages * H_kv * page_size < 2^31; D 64 or 128; H_kv divides H,
- *   H / H_kv <= 128, H <= 65535.  Index arrays are 4-byte aligned, the caches
+ *   H / H_kv <= 128, H <= 16384.  Index arrays are 4-byte aligned, the caches
  *   and k_mean 16-byte aligned.
  *   Queries, keys and values of the new tokens are [tokens, heads, D] with D
  *   and the heads contiguous; `*_stride` is the distance between tokens in

@@ -477,7 +477,7 @@ bsa_status paged_sizes(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_
     if (D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
     if (b->page_size != 16 && b->page_size != 32 && b->page_size != 64 && b->page_size != 128)
         return BSA_ERR_UNSUPPORTED;
-    if (H_kv < 1 || H < H_kv || H % H_kv != 0 || H / H_kv > 128 || H > 65535) return BSA_ERR_INVALID_ARG;
+    if (H_kv < 1 || H < H_kv || H % H_kv != 0 || H / H_kv > 128 || H > 16384) return BSA_ERR_INVALID_ARG;
     if (b->seqs < 0 || b->seqs > 16384 || b->tokens < 0 || b->tokens > (1 << 24) ||
         (int64_t)b->tokens * H >= ((int64_t)1 << 31))
         return BSA_ERR_INVALID_ARG;

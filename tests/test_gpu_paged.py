@@ -770,3 +770,29 @@ def test_rows_next_to_values_that_are_not_finite_over_a_long_cache():
     keys = torch.arange(L - n + 1, L + 1, dtype=torch.float64, device=dev)
     # a sum of ones in fp32, its parts at most 2^19: exact; a logarithm and a product
     assert ((lse.view(S, n).double() - keys.log()).abs() <= 8 * 2.0 ** -24 * (1 + keys.log())).all()
+
+
+def test_very_many_heads():
+    b = ref.make([1, 3], [5, 200], H=16384, H_kv=16384, D=64, page=128, seed=111, poison=False)
+    q, k, v = ref.rows(b, 16384, 112), ref.rows(b, 16384, 113), ref.rows(b, 16384, 114)
+    rope = ref.rope_table(200, 64)
+    bk, bv = b.k_cache.clone(), b.v_cache.clone()
+    q_out, k_mean = run_append(b, q, k, v, rope=rope)
+    status_ok()
+    check_append(b, q, k, v, bk, bv, q_out, k_mean, rope=rope)
+    o, lse = run_forward(b, q_out)
+    sel = torch.empty((b.tokens, 16384, 2), dtype=torch.int32, device="cuda")
+    cnt = torch.empty((b.tokens, 16384), dtype=torch.int32, device="cuda")
+    bsa.select_paged(q_out, k_mean, *b.arrays(), sel, cnt, page_size=128, topk=1, sink_blocks=0)
+    o2, lse2 = run_forward(b, q_out, sel=sel, sel_cnt=cnt)  # (all blocks there are)
+    status_ok()
+    assert torch.equal(cnt[0], torch.ones_like(cnt[0])) and torch.equal(cnt[1:], torch.full_like(cnt[1:], 2))
+    # both within the bound of ref.check_attention, where A is at most the largest |v| and
+    # the fp32 term, 2 (D + 16) 2^-24 (R + 1) A with R < 20 and |v| < 6, below 2^-10
+    far = 2.0 ** -7 * 1.01 * (b.v_cache.abs().max().float() + 1.01 * o.float().abs()) + 2.0 ** -9
+    assert ((o2.float() - o.float()).abs() <= far).all()
+    for h in (0, 1, 9000, 16383):  # against the reference, a head at a time
+        one = ref.Batch(b.new, b.length, 1, 1, 64, 128, "cuda", table=b.table, q_start=b.q_start, kv_len=b.kv_len,
+                        k_cache=b.k_cache[:, h:h + 1], v_cache=b.v_cache[:, h:h + 1], n_pages=b.n_pages, tokens=b.tokens)
+        ref.check_attention(one, q_out[:, h:h + 1], o[:, h:h + 1], lse[:, h:h + 1])
+        ref.check_attention(one, q_out[:, h:h + 1], o2[:, h:h + 1], lse2[:, h:h + 1])

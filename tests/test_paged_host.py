@@ -234,3 +234,10 @@ def test_lists_of_any_use_fit(lib):
     assert forward(lib, sel=FAKE, cnt=FAKE, width=(1 << 20) + 1) == INVALID
     assert lib.bsa_forward_paged_workspace_size(ctypes.byref(batch()), 8, 4, 128, (1 << 20) + 1) == 0
     assert lib.bsa_forward_paged_workspace_size(ctypes.byref(batch()), 8, 4, 128, 1 << 20) > 0
+
+
+@pytest.mark.parametrize("call", [append, forward, select])
+def test_heads_fit_the_launches(lib, call):
+    """A launch has a thread block for each group of heads along one axis, of at most 65535."""
+    assert call(lib, batch(tokens=0), H=16384, H_kv=16384) == OK
+    assert call(lib, batch(tokens=0), H=16385, H_kv=16385) == INVALID
