@@ -13,15 +13,15 @@
 // page of the block's last token.
 //
 // Work mapping.  A thread block takes one 128-position block that a sequence's
-// new tokens touch and either four query heads of its tokens (long chunks: of one
-// half of them), or the key and the value of one key/value head, two tokens at a
+// new tokens touch and either four query heads of its tokens (long chunks: of a
+// half or a quarter of them), or the key and the value of one key/value head, two tokens at a
 // time.  The block that writes a head's keys writes all of this position block's, so the mean needs no other's work and adds in a
 // fixed order, whatever chunks the tokens came in.  A row of D values is held by
 // D / 8 neighbouring threads, eight values each: where the whole head turns by
 // halves, four of either half (a pair meets in one thread), else eight in a row,
 // with the rotation partner's values by shuffles.  Every thread loads its four
 // rows before it works on the first.  (A prompt of 8192 tokens, 32 + 8 heads of
-// 128 with norms, 206 MB: 44 us, 0.69 of the copy rate; 107 us with one row at a time,
+// 128 with norms, 206 MB: 42 us, 0.72 of the copy rate; 107 us with one row at a time,
 // 62 us when each row found its place for itself, 234 instructions a row.  A step of 32
 // tokens: 5.7 us, most of it the launch.)
 #include <cuda_bf16.h>
@@ -49,7 +49,7 @@ struct AppendParams {
     float eps;
     int32_t H_kv, group;
     int32_t q_blocks;  // thread blocks (y) of query heads; those of keys and values follow
-    int32_t q_parts;   // of a position block's tokens that a thread block of query heads takes one of: 1 or 2
+    int32_t q_parts;   // of a position block's tokens that a thread block of query heads takes one of: 1, 2 or 4
     int32_t page_shift;
 };
 
@@ -200,11 +200,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     float wf[8];
     if (w != nullptr) unpack8(load_row<D, kHalves>(w, c), wf);
     if (queries) {
-        int32_t from = lo, to = hi;
-        if (P.q_parts == 2) {
-            if (blockIdx.y & 1) from = max(lo, base + kBlock / 2);
-            else to = min(hi, base + kBlock / 2);
-        }
+        const int32_t span = kBlock / P.q_parts, at = base + span * (blockIdx.y % P.q_parts);
+        const int32_t from = max(lo, at), to = min(hi, at + span);
         // With kHalves the next token's rows are on their way while this one's are worked
         // on (46.7 -> 44.1 us); the other forms need the registers (11.3 us, 12.8 with it).
         uint4 next[4];
@@ -342,14 +339,16 @@ bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaSt
     P.H_kv = a.H_kv;
     P.group = a.H / a.H_kv;
     P.page_shift = __builtin_ctz((unsigned)a.page);
-    // long chunks: blocks of half as many tokens fill the card more evenly (8192 tokens,
-    // 32 + 8 heads: 46 us with whole ones); short ones find their place half as often
-    P.q_parts = a.tokens / a.seqs >= kBlock ? 2 : 1;
+    // long chunks: blocks of fewer tokens fill the card more evenly (8192 tokens, 32 + 8
+    // heads of 128: whole ones 46 us, halves 43.8, quarters 42.2; chunks of up to 700, 14 + 2
+    // heads of 64 without kHalves: halves 10.8 us, quarters 12.0); short ones find their
+    // place less often
+    const bool halves = a.rope != nullptr && a.rot == a.D && !a.interleaved;
+    P.q_parts = a.tokens / a.seqs >= kBlock ? (halves ? 4 : 2) : 1;
     P.q_blocks = a.q != nullptr ? (a.H + 3) / 4 * P.q_parts : 0;
     // a sequence's n > 0 new tokens touch at most (n + 126) / 128 + 1 blocks
     const int64_t units = (int64_t)a.tokens / kBlock + 2 * (int64_t)a.seqs;
     const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + a.H_kv));
-    const bool halves = a.rope != nullptr && a.rot == a.D && !a.interleaved;
     const auto kernel = a.D == 128 ? (halves ? k_paged_append<128, true> : k_paged_append<128, false>)
                                    : (halves ? k_paged_append<64, true> : k_paged_append<64, false>);
     const cudaError_t e = launch_chained(kernel, grid, kAppendThreads, 0, stream, P);
