@@ -1,5 +1,9 @@
 """Paged cache: append, attention and block selection against fp64, element by
 element, with bounds that count the roundings (see paged_ref)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -796,3 +800,34 @@ def test_very_many_heads():
                         k_cache=b.k_cache[:, h:h + 1], v_cache=b.v_cache[:, h:h + 1], n_pages=b.n_pages, tokens=b.tokens)
         ref.check_attention(one, q_out[:, h:h + 1], o[:, h:h + 1], lse[:, h:h + 1])
         ref.check_attention(one, q_out[:, h:h + 1], o2[:, h:h + 1], lse2[:, h:h + 1])
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch, paged_ref as ref, long_context_mask_gb300 as bsa
+b = ref.make([1, 60], [900, 300], H=8, H_kv=2, D=128, page=64, seed=120, poison=False)
+q, k, v = ref.rows(b, 8, 1), ref.rows(b, 2, 2), ref.rows(b, 2, 3)
+km = torch.zeros((b.n_pages, 2, 128), dtype=torch.bfloat16, device="cuda")
+qr, o, lse = torch.empty_like(q), torch.empty_like(q), torch.empty((b.tokens, 8), device="cuda")
+sel = torch.empty((b.tokens, 2, 6), dtype=torch.int32, device="cuda")
+cnt = torch.empty((b.tokens, 2), dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    bsa.paged_append(k, v, b.k_cache, b.v_cache, *b.arrays(), q=q, q_out=qr, k_mean=km)
+    bsa.select_paged(qr, km, *b.arrays(), sel, cnt, page_size=64, topk=4)
+    bsa.forward_paged(qr, b.k_cache, b.v_cache, *b.arrays(), o, lse, sel=sel, sel_cnt=cnt)
+graph.replay()
+torch.cuda.synchronize()
+assert bsa.device_status() == 0
+ref.check_attention(b, qr, o, lse, sel=ref.select(b, qr, km, 4, 1, 1))
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """Nothing has been loaded or set up before the capture begins."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stderr[-2000:]
