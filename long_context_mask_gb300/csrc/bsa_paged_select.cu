@@ -8,7 +8,7 @@
 // fp32 score is off by at most
 //     E = (n + G + 2) 2^-24 |a| max_j |mean_j|
 // (n roundings on a product's way into the sum, kSteps of them; G - 1 of the
-// query heads' sum; by the Cauchy-Schwarz inequality), so with tau the k-th largest fp32 score every
+// query heads' sum; by the Cauchy-Schwarz inequality; and what underflows), so with tau the k-th largest fp32 score every
 // block above tau + 2E is among the k best and none below tau - 2E is.  Blocks
 // in between are scored again in fp64 where there are more of them than places.
 //
@@ -35,6 +35,10 @@ constexpr int kFewTok = 4;                    // tokens up to which a tile is re
 // the 64-long chain (D / 2 values, every second) of the product tile, the last
 // addition; a decoding step's path (8 in a thread, then D / 8 threads) has fewer.
 constexpr int kSteps = 128 / 2 + 1;
+// What a sum of at most 128 squares loses where they underflow: each of its fused
+// additions rounds to a multiple of 2^-149, off by half of it at most.  (Means around
+// 2^-80 have squares below all fp32 numbers, and products with q that are far above.)
+constexpr float kLost = 0x1p-143f;
 
 struct SelectParams {
     PagedBatch b;
@@ -425,8 +429,8 @@ __global__ void __launch_bounds__(128) k_paged_pick(const __grid_constant__ Sele
             most = larger(__shfl_xor_sync(0xffffffffu, most, d), most);
         }
         __syncwarp();
-        // (1.01 covers the rounding of E itself, 1e-36 products that underflow)
-        const float E = 1.01f * (float)(kSteps + P.group + 2) * 5.9604645e-8f * sqrtf(norm_a) * sqrtf(most) + 1e-36f;
+        // (1.01 covers the rounding of E itself, 1e-36 products that underflow, kLost squares that do)
+        const float E = 1.01f * (float)(kSteps + P.group + 2) * 5.9604645e-8f * sqrtf(norm_a + kLost) * sqrtf(most + kLost) + 1e-36f;
         const uint32_t none32[1] = {0u};
         const float tau = of_key(in_regs ? kth_largest<kHeld>(held, keys, nc, P.topk) : kth_largest<0>(none32, keys, nc, P.topk));
         // without a finite bound every block is a close call
