@@ -67,6 +67,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "bsa_device_setup.h"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
 #include "bsa_rows.cuh"
@@ -1304,17 +1305,16 @@ template <int D, int kMode>
 bsa_status launch_d(const Params& P, cudaStream_t stream) {
     constexpr size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
     static_assert(smem <= 232448, "shared memory of a thread block");
-    static int done[64] = {0};
-    static int sms[64] = {0};
+    static DeviceSetup setup;
+    static int sms[kMaxDevices];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return BSA_ERR_CUDA;
-    if (!done[dev]) {
-        if (cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(k_paged_forward<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-                cudaSuccess)
-            return BSA_ERR_CUDA;
-        done[dev] = 1;
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+    const bool ready = setup.once(dev, [&] {
+        return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+               cudaFuncSetAttribute(k_paged_forward<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) ==
+                   cudaSuccess;
+    });
+    if (!ready) return BSA_ERR_CUDA;
     const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
     if (launch_chained(k_paged_forward<D, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P) != cudaSuccess ||
         launch_chained(k_paged_join<D>, dim3((unsigned)grid, 128 / (kJoinThreads / (D / 4))), kJoinThreads, 0, stream, P) != cudaSuccess)

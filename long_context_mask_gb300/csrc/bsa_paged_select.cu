@@ -21,6 +21,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "bsa_device_setup.h"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
 #include "bsa_rows.cuh"
@@ -595,15 +596,14 @@ bsa_status launch_d(const SelectParams& P, cudaStream_t stream) {
     // warps to a thread block of k_paged_pick: four, or as many as its shared memory holds
     const int32_t most = 196608 / P.pick_bytes, warps = most < 4 ? most : 4;
     constexpr size_t tile = (size_t)(kTileTok + kTileBlk) * (D + 4) * sizeof(float);
-    static int ready[64] = {0};
+    static DeviceSetup setup;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return BSA_ERR_CUDA;
-    if (!ready[dev]) {
-        if (cudaFuncSetAttribute(k_paged_scores<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile) != cudaSuccess ||
-            cudaFuncSetAttribute(k_paged_pick<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 196608) != cudaSuccess)
-            return BSA_ERR_CUDA;
-        ready[dev] = 1;
-    }
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+    const bool ready = setup.once(dev, [&] {
+        return cudaFuncSetAttribute(k_paged_scores<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile) == cudaSuccess &&
+               cudaFuncSetAttribute(k_paged_pick<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 196608) == cudaSuccess;
+    });
+    if (!ready) return BSA_ERR_CUDA;
     // sum over sequences of ceil(n / kTileTok) <= tokens / kTileTok + seqs
     const dim3 tiles((unsigned)(P.b.tokens / kTileTok + P.b.seqs), (unsigned)P.chunks, (unsigned)P.H_kv);
     if (launch_chained(k_paged_scores<D>, tiles, kScoreThreads, tile, stream, P) != cudaSuccess ||

@@ -1,6 +1,10 @@
 """Paged cache: scores of any magnitude, thread blocks with several runs of
 work, long waits, and first calls from several threads, against fp64 (bounds
 as in paged_ref)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -47,3 +51,50 @@ def test_close_and_equal_scores_of_any_magnitude(kind, q_exp, m_exp):
     for t in range(30):
         for h in range(2):
             assert sel[t, h].tolist() == want[t][h] and int(cnt[t, h]) == 18, (t, h)
+
+
+# ------------------------------------------------------------------ first calls
+
+FIRST_CALLS = """
+import sys, threading
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch, paged_ref as ref, long_context_mask_gb300 as bsa
+n = 8
+bs = [ref.make([1, 40], [900, 300], H=8, H_kv=2, D=64 + 64 * (x % 2), page=64, seed=x, poison=False) for x in range(n)]
+qs = [ref.rows(b, 8, 1) for b in bs]
+outs = [(torch.empty_like(q), torch.empty((41, 8), device="cuda"), torch.empty((41, 2, 6), dtype=torch.int32, device="cuda"),
+         torch.empty((41, 2), dtype=torch.int32, device="cuda")) for q in qs]
+kms = [torch.randn((b.n_pages, 2, b.D), device="cuda").to(torch.bfloat16) for b in bs]
+streams = [torch.cuda.Stream() for _ in bs]
+failed, together = [], threading.Barrier(n)
+torch.cuda.synchronize()
+bsa.load_library()
+
+def go(x):
+    b, q, (o, lse, sel, cnt) = bs[x], qs[x], outs[x]
+    try:
+        with torch.cuda.stream(streams[x]):
+            together.wait()
+            bsa.select_paged(q, kms[x], *b.arrays(), sel, cnt, page_size=64, topk=4)
+            bsa.forward_paged(q, b.k_cache, b.v_cache, *b.arrays(), o, lse)
+    except Exception as e:
+        failed.append(e)
+
+threads = [threading.Thread(target=go, args=(x,)) for x in range(n)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not failed, failed
+assert bsa.device_status() == 0
+for b, q, km, (o, lse, sel, cnt) in zip(bs, qs, kms, outs):
+    ref.check_attention(b, q, o, lse)
+    want = ref.select(b, q, km, 4, 1, 1)
+    assert all(sel[t, h, :len(want[t][h])].tolist() == want[t][h] for t in range(41) for h in range(2))
+"""
+
+
+def test_first_calls_from_several_threads_at_once():
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stderr[-2000:]
