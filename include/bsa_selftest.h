@@ -1,6 +1,6 @@
 /*
- * bsa_selftest.h - self-test entry points of libbsa.so.  They check two
- * building blocks of bsa_forward on the device and are meant for test
+ * bsa_selftest.h - self-test entry points of libbsa.so.  They check
+ * building blocks of the forward calls on the device and are meant for test
  * suites, not for the attention path.  Conventions as in bsa.h.
  */
 #ifndef BSA_SELFTEST_H
@@ -33,6 +33,21 @@ bsa_status bsa_selftest_exp2(const float* x, float* y_fma, float* y_mufu, float*
  * bsa_device_status().  Nothing faults, traps or hangs.
  */
 bsa_status bsa_selftest_wait_timeout(int64_t limit_ns, void* stream);
+
+typedef enum {
+    BSA_PAGED_WAIT_NOTHING = 0, /* nothing completes the barrier                            */
+    BSA_PAGED_WAIT_BUSY = 1     /* another warp completes it after 50 ms of visible progress */
+} bsa_paged_wait_kind;
+
+/*
+ * bsa_selftest_paged_wait - launch one warp that waits, for 2 ms at most, on
+ * an mbarrier with bsa_forward_paged's wait, which lasts as long as the work
+ * it waits for shows progress.  A wait that gives up records BSA_ERR_TIMEOUT
+ * in the device status word.  Nothing faults, traps or hangs.
+ *  elapsed_ns  device int64 [1] out: how long the warp waited, negative where
+ *              it gave up.
+ */
+bsa_status bsa_selftest_paged_wait(int32_t kind, int64_t* elapsed_ns, void* stream);
 
 #ifdef __cplusplus
 }

@@ -45,6 +45,9 @@ from .binding import (  # noqa: F401
     set_forward_options,
     selftest_exp2,
     selftest_wait_timeout,
+    selftest_paged_wait,
+    PAGED_WAIT_BUSY,
+    PAGED_WAIT_NOTHING,
     spectral_order,
     spectral_order_noalloc,
     spectral_order_workspace_size,

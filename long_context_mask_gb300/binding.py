@@ -29,7 +29,7 @@ EXPORTS = ("bsa_build_index", "bsa_build_crm", "bsa_forward_crm", "bsa_upscale_t
            "bsa_paged_append", "bsa_forward_paged", "bsa_forward_paged_workspace_size",
            "bsa_select_paged", "bsa_select_paged_workspace_size",
            "bsa_device_status", "bsa_resident_ctas", "bsa_status_string", "bsa_selftest_exp2",
-           "bsa_selftest_wait_timeout")
+           "bsa_selftest_wait_timeout", "bsa_selftest_paged_wait")
 
 
 class BsaError(RuntimeError):
@@ -116,10 +116,11 @@ def load_library():
     lib.bsa_status_string.restype = ctypes.c_char_p
     lib.bsa_selftest_exp2.argtypes = [P, P, P, P, i64, P]
     lib.bsa_selftest_wait_timeout.argtypes = [i64, P]
+    lib.bsa_selftest_paged_wait.argtypes = [i32, P, P]
     for name in ("bsa_build_index", "bsa_reorder_rows", "bsa_spectral_order", "bsa_sample_blocks",
                  "bsa_forward",
                  "bsa_device_status", "bsa_resident_ctas", "bsa_selftest_exp2",
-                 "bsa_selftest_wait_timeout"):
+                 "bsa_selftest_wait_timeout", "bsa_selftest_paged_wait"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -863,6 +864,17 @@ def selftest_wait_timeout(limit_ns: int, *, stream=None):
            load_library().bsa_selftest_wait_timeout(int(limit_ns), _stream(stream)))
 
 
+PAGED_WAIT_NOTHING, PAGED_WAIT_BUSY = 0, 1
+
+
+def selftest_paged_wait(kind: int, elapsed_ns, *, stream=None):
+    """Launch the self-test of the paged forward's waits (int64 [1] on the device: see bsa_selftest.h)."""
+    import torch
+    _flat(elapsed_ns, "elapsed_ns", 1, torch.int64)
+    _check("bsa_selftest_paged_wait",
+           load_library().bsa_selftest_paged_wait(int(kind), _ptr(elapsed_ns), _stream(stream)))
+
+
 def resident_ctas(D: int) -> int:
     n = load_library().bsa_resident_ctas(int(D))
     if n <= 0:
@@ -891,4 +903,4 @@ __all__ = ["BLOCK", "BsaError", "IDX_MASK_U8", "IDX_THRESHOLD_F32", "IDX_TOPK_F3
            "select_paged_workspace_size",
            "spectral_order", "spectral_order_workspace_size", "spectral_order_noalloc",
            "NOALLOC_SCRATCH_BYTES", "reorder_guard", "set_forward_options",
-           "selftest_exp2", "selftest_wait_timeout"]
+           "selftest_exp2", "selftest_wait_timeout", "selftest_paged_wait", "PAGED_WAIT_NOTHING", "PAGED_WAIT_BUSY"]

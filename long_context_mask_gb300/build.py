@@ -23,7 +23,7 @@ SOURCES = ["bsa_api.cu", "bsa_index.cu", "bsa_scores.cu", "bsa_order.cu", "bsa_a
            "bsa_noalloc.cu", "bsa_gather.cu", "bsa_paged.cu", "bsa_paged_select.cu",
            "bsa_paged_attn.cu"]
 HEADERS = ["bsa_internal.h", "bsa_ptx.cuh", "bsa_math.cuh", "bsa_gather0.cuh", "bsa_rows.cuh", "bsa_tma_host.h",
-           "bsa_paged.cuh", "bsa_device_setup.h"]
+           "bsa_paged.cuh", "bsa_device_setup.h", "bsa_paged_wait.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

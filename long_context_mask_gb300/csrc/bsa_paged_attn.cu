@@ -70,6 +70,7 @@
 #include "bsa_device_setup.h"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
+#include "bsa_paged_wait.cuh"
 #include "bsa_rows.cuh"
 #include "bsa_tma_host.h"
 
@@ -78,7 +79,6 @@ namespace {
 
 // positions lie within 2^24 of zero: longer windows are no longer, and position - window stays in 32 bits
 constexpr int32_t kMaxWindow = 1 << 26;
-constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s per wait
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;                          // rescale O when a maximum grows by > 2^8
@@ -131,13 +131,12 @@ struct Shared {
     uint64_t ml_full, ml_empty;  // a segment's maxima and sums are in ml, have been read
     uint64_t mma_done;
     uint64_t seg_full[kDesc], seg_empty[kDesc];
-    uint64_t busy;            // when a key tile of a row computed from its own keys was last done
+    Watch watch;
     Segment seg[kDesc];
     float2 ml[128];           // of a segment's rows: maximum (log2) and sum (before: block_prefix's words)
     int32_t start[kPhases][5];  // of each run the first unit: key/value head, sequence, query tile, unit; tile within the head
     PagedSeq start_seq[kPhases];  // its sequence's entry
     uint32_t tmem_base;
-    int32_t abort;
 };
 
 template <int n>
@@ -258,35 +257,8 @@ __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, in
     }
 }
 
-__device__ __forceinline__ void set_abort(Shared* sh, int32_t* status) {
-    *reinterpret_cast<volatile int32_t*>(&sh->abort) = 1;
-    raise_status(status, BSA_ERR_TIMEOUT);
-}
-// A bounded wait.  While rows are computed from their own keys (sh->busy moves on with
-// every key tile of them) those who wait for them have not lost a second yet.  All but
-// the first look is out of line: the kernel waits in some twenty places, and a window's
-// short rows are sensitive to its length.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const volatile uint64_t* busy, const volatile int32_t* status) {
-    const uint64_t t0 = globaltimer();
-    uint32_t n = 0;
-    while (!mbar_try_wait(bar, parity)) {
-        if ((++n & 255u) == 0) {
-            const uint64_t now = globaltimer(), last = *busy;
-            if (now - t0 > kWaitNs && (now < last || now - last > kWaitNs)) return false;
-            if (*status == BSA_ERR_TIMEOUT) return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Shared* sh, int32_t* status) {
-    return mbar_try_wait(bar, parity) || wait_on(bar, parity, &sh->busy, status);
-}
-// For copies and products in flight, after a failure too.
-__device__ __noinline__ void drain(uint32_t bar, uint32_t parity, int32_t* status) {
-    if (!mbar_wait(bar, parity, kWaitNs, status, -1)) raise_status(status, BSA_ERR_TIMEOUT);
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Shared* sh, int32_t* status) {
-    return __all_sync(0xffffffffu, wait(bar, parity, sh, status));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, int32_t* status) {
+    return __all_sync(0xffffffffu, paged_wait(bar, parity, w, status));
 }
 
 // a / b; nearly every dividend fits 32 bits, whose division is much shorter.
@@ -425,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         // (the producer writes them again where a row is split)
 #pragma unroll
         for (int p = 0; p < kPhases; ++p) P.joins[p * gridDim.x + blockIdx.x] = make_int4(0, 0, 0, 0);
-        sh->busy = 0;
+        sh->watch.busy = 0;
         // a block of this launch (or an unread earlier one) timed out: abandon
-        sh->abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
+        sh->watch.abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
     }
 
     // ---------------------------------------------------------------- this block's run
@@ -551,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
         }
     }
-    const bool abandoned = sh->abort != 0;
+    const bool abandoned = sh->watch.abort != 0;
     if (warp == kMmaQK && !abandoned) {
         tmem_alloc(smem_u32(&sh->tmem_base), kTmemCols);
         tmem_relinquish();
@@ -567,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     // Segment k, for the warps that read descriptors (null: no more); they hand
     // it back when they are through with it.
     auto next_segment = [&](uint32_t k, bool& ok) -> const Segment* {
-        if (!wait_warp(smem_u32(&sh->seg_full[k % kDesc]), (k / kDesc) & 1u, sh, status)) {
+        if (!wait_warp(smem_u32(&sh->seg_full[k % kDesc]), (k / kDesc) & 1u, &sh->watch, status)) {
             ok = false;
             return nullptr;
         }
@@ -619,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 held += row[i] >= 0;
             }
             const uint32_t pos = is_v ? place_v(g) : place_k(g), slot = pos % S;
-            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, sh, status)) return false;
+            if (!wait_warp(smem_u32(&sh->empty[slot]), ((pos / S) & 1u) ^ 1u, &sh->watch, status)) return false;
             if (elect_one()) {
                 const uint32_t fb = smem_u32(&sh->full[slot]), dst = s_ring + slot * C::kTile;
                 mbar_arrive_expect_tx(fb, (uint32_t)(held * page * D * 2));
@@ -678,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             sg.j0 = j0;
             sg.n = n_row == 0 ? 0 : j1 - j0;
             sg.slot = j0 == 0 && j1 == n_eff ? -1 : 2 * run + (j0 == 0 ? 1 : 0);
-            if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, sh, status)) {
+            if (!wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh->watch, status)) {
                 ok = false;
                 break;
             }
@@ -719,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
         }
         }
-        if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, sh, status)) {
+        if (ok && wait_warp(smem_u32(&sh->seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh->watch, status)) {
             if (lane == 0) {
                 sh->seg[k % kDesc].n = -1;
                 mbar_arrive(smem_u32(&sh->seg_full[k % kDesc]));
@@ -727,11 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         } else {
             ok = false;
         }
-        if (!ok && lane == 0) set_abort(sh, status);
+        if (!ok && lane == 0) set_abort(&sh->watch, status);
         // every issued copy must land before the block exits
         if (lane == 0)
             for (uint32_t x = g > S / 2 ? g - S / 2 : 0; x < g; ++x)
-                drain(smem_u32(&sh->full[place_k(x) % S]), (place_k(x) / S) & 1u, status);
+                paged_drain(smem_u32(&sh->full[place_k(x) % S]), (place_k(x) / S) & 1u, status);
         __syncwarp();
     } else if (warp == kVLoad) {
         // ------------------------------------------------------------ V tiles
@@ -744,10 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             hand_back(k);
             ok = load_tiles(sg, true, g);
         }
-        if (!ok && lane == 0) set_abort(sh, status);
+        if (!ok && lane == 0) set_abort(&sh->watch, status);
         if (lane == 0)
             for (uint32_t x = g > S / 2 ? g - S / 2 : 0; x < g; ++x)
-                drain(smem_u32(&sh->full[place_v(x) % S]), (place_v(x) / S) & 1u, status);
+                paged_drain(smem_u32(&sh->full[place_v(x) % S]), (place_v(x) / S) & 1u, status);
         __syncwarp();
     } else if (warp == kMmaQK) {
         // ------------------------------------------------------------ query tiles, S = Q K^T
@@ -764,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             hand_back(k);
             if (n == 0) continue;
             // the segment before is done with the query tile's place
-            if (nq > 0) ok = wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, sh, status);
+            if (nq > 0) ok = wait_warp(smem_u32(&sh->q_empty), (nq - 1u) & 1u, &sh->watch, status);
             if (!ok) break;
             if (elect_one()) {
                 const bool one = ntok == 1;
@@ -775,15 +747,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     tma_load_3d(s_q + h * kBox, one ? &P.map_q1 : &P.map_q, h * 64, kvh * P.group, q0, bar);
             }
             __syncwarp();
-            ok = wait_warp(smem_u32(&sh->q_full), nq++ & 1u, sh, status);
+            ok = wait_warp(smem_u32(&sh->q_full), nq++ & 1u, &sh->watch, status);
             for (int32_t j = 0; j < n && ok; ++j, ++g) {
                 if (g >= kSBuf) {
                     // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
                     const uint32_t pv = place_v(g - kSBuf);
-                    ok = wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, sh, status);
+                    ok = wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, &sh->watch, status);
                 }
                 const uint32_t pos = place_k(g), slot = pos % S;
-                ok = ok && wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, sh, status);
+                ok = ok && wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, &sh->watch, status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ks = dk + (uint64_t)((slot * C::kTile) >> 4);
@@ -800,13 +772,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 __syncwarp();
             }
         }
-        if (!ok && lane == 0) set_abort(sh, status);
-        if (nq > 0 && lane == 0) drain(smem_u32(&sh->q_full), (nq - 1u) & 1u, status);
+        if (!ok && lane == 0) set_abort(&sh->watch, status);
+        if (nq > 0 && lane == 0) paged_drain(smem_u32(&sh->q_full), (nq - 1u) & 1u, status);
         __syncwarp();
         // nothing of ours may still be running when TMEM is freed
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
         __syncwarp();
-        drain(smem_u32(&sh->mma_done), 0, status);
+        paged_drain(smem_u32(&sh->mma_done), 0, status);
         __syncwarp();
     } else if (warp == kMmaPV) {
         // ------------------------------------------------------------ O += P V
@@ -830,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             if (n == 0) continue;
             for (int32_t j = 0; j < n && ok; ++j, ++g) {
                 const uint32_t pos = place_v(g), slot = pos % S;
-                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, sh, status);
+                ok = wait_warp(smem_u32(&sh->full[slot]), (pos / S) & 1u, &sh->watch, status);
                 if (ok && j == n - 1 && tail < 128) {
                     // 16-byte pieces of rows tail .. 127 (a zero is the same in any swizzle)
                     const uint32_t tile = s_ring + slot * C::kTile;
@@ -842,9 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                ok = ok && wait_warp(smem_u32(&sh->p_full[g % kSBuf]), (g / kSBuf) & 1u, sh, status);
+                ok = ok && wait_warp(smem_u32(&sh->p_full[g % kSBuf]), (g / kSBuf) & 1u, &sh->watch, status);
                 // a segment's first product overwrites O: the epilogue before must have read it
-                if (ok && j == 0 && segs > 0) ok = wait_warp(smem_u32(&sh->o_free), (segs - 1u) & 1u, sh, status);
+                if (ok && j == 0 && segs > 0) ok = wait_warp(smem_u32(&sh->o_free), (segs - 1u) & 1u, &sh->watch, status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
@@ -860,10 +832,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
             ++segs;
         }
-        if (!ok && lane == 0) set_abort(sh, status);
+        if (!ok && lane == 0) set_abort(&sh->watch, status);
         if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
         __syncwarp();
-        drain(smem_u32(&sh->mma_done), 0, status);
+        paged_drain(smem_u32(&sh->mma_done), 0, status);
         __syncwarp();
     } else if (warp < kStore0) {
         // ------------------------------------------------------------ softmax
@@ -965,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                     }
                 }
                 const uint32_t pk = place_k(gb);
-                const bool wt = wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, sh, status);
+                const bool wt = paged_wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, &sh->watch, status);
                 // (a failure elsewhere raises the status word, which ends this wait too)
                 if (__any_sync(0xffffffffu, !wt)) {
                     ok = false;
@@ -1001,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 if (rescale) {
                     // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
                     const uint32_t pv = place_v(gb - 1u);
-                    const bool wv = wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, sh, status);
+                    const bool wv = paged_wait(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, &sh->watch, status);
                     if (__any_sync(0xffffffffu, !wv)) {
                         ok = false;
                         break;
@@ -1017,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             hand_back(k);
             // maxima and sums of the rows to the storing warps
             const float la = row_sum4(l[0]), lb = row_sum4(l[1]);
-            if (__any_sync(0xffffffffu, !wait(smem_u32(&sh->ml_empty), (segs & 1u) ^ 1u, sh, status))) {
+            if (__any_sync(0xffffffffu, !paged_wait(smem_u32(&sh->ml_empty), (segs & 1u) ^ 1u, &sh->watch, status))) {
                 ok = false;
                 break;
             }
@@ -1029,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             ++segs;
             gb0 += (uint32_t)n;
         }
-        if (!ok && lane == 0) set_abort(sh, status);
+        if (!ok && lane == 0) set_abort(&sh->watch, status);
     } else {
         // ------------------------------------------------------------ O and LSE of a segment
         // one thread per row
@@ -1057,8 +1029,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
             const uint32_t pv = place_v(g + (uint32_t)n - 1u);
             // (the last product is the segment's: the next one waits for o_free)
-            ok = wait_warp(smem_u32(&sh->ml_full), segs & 1u, sh, status) &&
-                 wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, sh, status);
+            ok = wait_warp(smem_u32(&sh->ml_full), segs & 1u, &sh->watch, status) &&
+                 wait_warp(smem_u32(&sh->empty[pv % S]), (pv / S) & 1u, &sh->watch, status);
             if (!ok) break;
             const float2 ml = sh->ml[row];
             mbar_arrive(smem_u32(&sh->ml_empty));
@@ -1109,14 +1081,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 for (; again; again &= again - 1u) {
                     const int i = __ffs(again) - 1;
                     const float mi = __shfl_sync(0xffffffffu, ml.x, i), li = __shfl_sync(0xffffffffu, inv, i);
-                    own_keys_row<D, kMode>(P, *sp, qd * 32 + i, mi, li, &sh->busy);
+                    own_keys_row<D, kMode>(P, *sp, qd * 32 + i, mi, li, &sh->watch.busy);
                 }
             }
             hand_back(k);
             g += (uint32_t)n;
             ++segs;
         }
-        if (!ok && lane == 0) set_abort(sh, status);
+        if (!ok && lane == 0) set_abort(&sh->watch, status);
     }
 
     tc_fence_before();

@@ -1,5 +1,5 @@
 // Self-test entry points (see include/bsa_selftest.h): the FMA-pipe exp2 next
-// to CUDA's exp2f, and the bounded mbarrier wait giving up on a barrier that
+// to CUDA's exp2f, and the bounded mbarrier waits giving up on a barrier that
 // nothing will ever complete.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -7,6 +7,7 @@
 
 #include "bsa_internal.h"
 #include "bsa_math.cuh"
+#include "bsa_paged_wait.cuh"
 #include "bsa_ptx.cuh"
 #include "bsa_selftest.h"
 
@@ -36,6 +37,39 @@ __global__ void k_selftest_wait(uint64_t limit_ns, int32_t* status) {
         atomicCAS(status, 0, BSA_ERR_TIMEOUT);
 }
 
+// The paged forward's waits: warp 0 waits on an mbarrier (2 ms), lane 0 of warp 1 does
+// what the kind says.  out[0]: the ns that warp 0 waited, negative where it gave up.
+constexpr uint64_t kShortNs = 2000000ull, kBusyNs = 50000000ull;
+__global__ void k_selftest_paged_wait(int32_t kind, int64_t* out, int32_t* status) {
+    __shared__ uint64_t bar;
+    __shared__ Watch watch;
+    const uint32_t b = ptx::smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(b, 1);
+        ptx::fence_mbar_init();
+        watch.busy = 0;
+        watch.abort = 0;
+    }
+    __syncthreads();
+    const uint64_t t0 = ptx::globaltimer();
+    if (threadIdx.x < 32) {
+        const bool ok = __all_sync(0xffffffffu, paged_wait<kShortNs>(b, 0, &watch, status));
+        const int64_t ns = (int64_t)(ptx::globaltimer() - t0);
+        if (threadIdx.x == 0) {
+            if (!ok) set_abort(&watch, status);
+            out[0] = ok ? ns : -ns;
+        }
+    } else if (threadIdx.x == 32 && kind == BSA_PAGED_WAIT_BUSY) {
+        // what it waits for goes on, and is there after 50 ms (each turn takes 10 ns at the least)
+        for (int32_t i = 0; i < 10000000; ++i) {
+            const uint64_t now = ptx::globaltimer();
+            *reinterpret_cast<volatile uint64_t*>(&watch.busy) = now;
+            if (now - t0 > kBusyNs) break;
+        }
+        ptx::mbar_arrive(b);
+    }
+}
+
 }  // namespace
 }  // namespace bsa
 
@@ -56,6 +90,15 @@ bsa_status bsa_selftest_wait_timeout(int64_t limit_ns, void* stream) {
     int32_t* status = bsa::status_word_ptr();
     if (!status) return BSA_ERR_CUDA;
     bsa::k_selftest_wait<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>((uint64_t)limit_ns, status);
+    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+bsa_status bsa_selftest_paged_wait(int32_t kind, int64_t* elapsed_ns, void* stream) {
+    if (kind != BSA_PAGED_WAIT_NOTHING && kind != BSA_PAGED_WAIT_BUSY) return BSA_ERR_INVALID_ARG;
+    if (!elapsed_ns) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    bsa::k_selftest_paged_wait<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(kind, elapsed_ns, status);
     return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

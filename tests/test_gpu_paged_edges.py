@@ -15,6 +15,7 @@ from gpu_util import status_ok
 from test_gpu_paged import bits, check_select, lists_for, mean_keys, run_forward, run_select
 
 pytestmark = pytest.mark.gpu
+BOUNDS, TIMEOUT = 6, 5
 
 
 # ------------------------------------------------------------------ selection
@@ -98,3 +99,25 @@ def test_first_calls_from_several_threads_at_once():
     code = FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ long waits
+
+def wait_selftest(kind):
+    ns = torch.zeros(1, dtype=torch.int64, device="cuda")
+    bsa.selftest_paged_wait(kind, ns)
+    return bsa.device_status(), ns.item() * 1e-6
+
+
+def test_a_wait_for_what_never_comes_ends():
+    status_ok()
+    st, ms = wait_selftest(bsa.PAGED_WAIT_NOTHING)
+    assert st == TIMEOUT and -1000 < ms <= -2
+    status_ok()
+
+
+def test_a_wait_for_what_goes_on_goes_on():
+    """Progress is noted all the time, between the waiting warp's looks at clock and note too."""
+    for _ in range(3):
+        st, ms = wait_selftest(bsa.PAGED_WAIT_BUSY)
+        assert st == 0 and 50 <= ms < 1000
