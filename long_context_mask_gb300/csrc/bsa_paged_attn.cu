@@ -616,6 +616,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         }
     };
 
+    // No product may still be running when TMEM is freed.  The issuer that is through
+    // first waits for the other one's, and that one perhaps for rows that are computed
+    // from their own keys.
+    auto finish_products = [&](bool ok) {
+        if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
+        __syncwarp();
+        if (!ok || !wait_warp(smem_u32(&sh->mma_done), 0, &sh->watch, status)) {
+            if (ok && lane == 0) set_abort(&sh->watch, status);
+            paged_drain(smem_u32(&sh->mma_done), 0, status);
+        }
+        __syncwarp();
+    };
+
     if (warp == kProducer) {
         // ------------------------------------------------------------ segments and K tiles
         uint32_t k = 0, g = 0;  // segments and tiles so far
@@ -775,11 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
         if (!ok && lane == 0) set_abort(&sh->watch, status);
         if (nq > 0 && lane == 0) paged_drain(smem_u32(&sh->q_full), (nq - 1u) & 1u, status);
         __syncwarp();
-        // nothing of ours may still be running when TMEM is freed
-        if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
-        __syncwarp();
-        paged_drain(smem_u32(&sh->mma_done), 0, status);
-        __syncwarp();
+        finish_products(ok);
     } else if (warp == kMmaPV) {
         // ------------------------------------------------------------ O += P V
         const uint64_t dv = smem_desc_sw128(s_ring, kBox, 1024);
@@ -833,10 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             ++segs;
         }
         if (!ok && lane == 0) set_abort(&sh->watch, status);
-        if (elect_one()) mma_commit(smem_u32(&sh->mma_done));
-        __syncwarp();
-        paged_drain(smem_u32(&sh->mma_done), 0, status);
-        __syncwarp();
+        finish_products(ok);
     } else if (warp < kStore0) {
         // ------------------------------------------------------------ softmax
         const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31

@@ -121,3 +121,37 @@ def test_a_wait_for_what_goes_on_goes_on():
     for _ in range(3):
         st, ms = wait_selftest(bsa.PAGED_WAIT_BUSY)
         assert st == 0 and 50 <= ms < 1000
+
+
+@pytest.mark.parametrize("behind", [1, 1000])
+def test_short_sequences_behind_rows_that_take_long(behind):
+    """Each thread block's run is a sequence of 2^19 keys, whose rows are computed from their own
+    keys for more than a second, and two short ones: whoever waits for those rows has not lost its
+    time.  behind 1: all scores of the run are there early, and their issuer waits for the last product."""
+    n, L, S = 128, 1 << 19, min(152, torch.cuda.get_device_properties(0).multi_processor_count)
+    dev = "cuda"
+    k = torch.zeros((L // 128, 1, 128, 64), dtype=torch.bfloat16, device=dev)
+    v = torch.ones_like(k)
+    v[0, 0, 0, 0] = float("inf")       # every long row's O is not finite,
+    v[-1, 0, -1, 1] = float("nan")     # and this one all but the last do not see
+    table = torch.full((3 * S, L // 128), -1, dtype=torch.int32, device=dev)
+    table[::3] = torch.arange(L // 128, dtype=torch.int32, device=dev)
+    pages = (behind + 127) // 128
+    table[1::3, :pages] = table[2::3, :pages] = torch.arange(1, 1 + pages, dtype=torch.int32, device=dev)
+    new = torch.tensor([n, 1, 1], dtype=torch.int32).repeat(S)
+    start = torch.cat([torch.zeros(1, dtype=torch.int32), new.cumsum(0).to(torch.int32)]).to(dev)
+    length = torch.tensor([L, behind, behind], dtype=torch.int32, device=dev).repeat(S)
+    q = torch.randn((S * (n + 2), 1, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(dev)
+    o, lse = torch.empty_like(q), torch.empty((S * (n + 2), 1), device=dev)
+    bsa.forward_paged(q, k, v, table, start, length, o, lse)
+    status_ok()
+    want = torch.ones((S, n + 2, 64), device=dev)
+    want[:, :n, 0] = float("inf")
+    want[:, n - 1, 1] = float("nan")
+    got = o.view(S, n + 2, 64).float()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+    fin = want.isfinite()
+    assert ((got - want)[fin].abs() <= 2.0 ** -7).all()
+    keys = torch.cat([torch.arange(L - n + 1, L + 1), torch.full((2,), behind)]).double().to(dev)
+    # a sum of ones in fp32, at most 2^19: exact; a logarithm and a product
+    assert ((lse.view(S, n + 2).double() - keys.log()).abs() <= 8 * 2.0 ** -24 * (1 + keys.log())).all()
