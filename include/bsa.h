@@ -13,8 +13,10 @@
  *    unsupported head dimension) are returned immediately and nothing is
  *    launched.  Conditions only the device can see (an index list longer
  *    than max_kv, an index or map entry out of range, a wait that timed out)
- *    are recorded in a per-device status word: the first such code wins and
- *    bsa_device_status() reads and clears it.  No kernel traps.
+ *    are recorded in a per-device status word: the first such code wins
+ *    (a time-out of bsa_forward_paged, whose output is incomplete then,
+ *    takes the place of another code) and bsa_device_status() reads and
+ *    clears it.  No kernel traps.
  *  - Tensors are row-major and contiguous.  "rows" of an index list are the
  *    (batch, head, query block) triples in that nesting order:
  *    row = (b * H + h) * nQB + qb.

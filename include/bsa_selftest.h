@@ -36,16 +36,18 @@ bsa_status bsa_selftest_wait_timeout(int64_t limit_ns, void* stream);
 
 typedef enum {
     BSA_PAGED_WAIT_NOTHING = 0, /* nothing completes the barrier                            */
-    BSA_PAGED_WAIT_BUSY = 1     /* another warp completes it after 50 ms of visible progress */
+    BSA_PAGED_WAIT_BUSY = 1,    /* a second warp completes it after 50 ms of visible progress */
+    BSA_PAGED_WAIT_TWO = 2      /* nothing does, and a second warp waits for up to 1 s       */
 } bsa_paged_wait_kind;
 
 /*
  * bsa_selftest_paged_wait - launch one warp that waits, for 2 ms at most, on
  * an mbarrier with bsa_forward_paged's wait, which lasts as long as the work
  * it waits for shows progress.  A wait that gives up records BSA_ERR_TIMEOUT
- * in the device status word.  Nothing faults, traps or hangs.
- *  elapsed_ns  device int64 [1] out: how long the warp waited, negative where
- *              it gave up.
+ * in the device status word and ends the other waits of its thread block.
+ * Nothing faults, traps or hangs.
+ *  elapsed_ns  device int64 [2] out: how long either warp waited, negative
+ *              where it gave up (0: it did not wait).
  */
 bsa_status bsa_selftest_paged_wait(int32_t kind, int64_t* elapsed_ns, void* stream);
 

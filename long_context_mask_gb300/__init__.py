@@ -48,6 +48,7 @@ from .binding import (  # noqa: F401
     selftest_paged_wait,
     PAGED_WAIT_BUSY,
     PAGED_WAIT_NOTHING,
+    PAGED_WAIT_TWO,
     spectral_order,
     spectral_order_noalloc,
     spectral_order_workspace_size,

@@ -864,13 +864,13 @@ def selftest_wait_timeout(limit_ns: int, *, stream=None):
            load_library().bsa_selftest_wait_timeout(int(limit_ns), _stream(stream)))
 
 
-PAGED_WAIT_NOTHING, PAGED_WAIT_BUSY = 0, 1
+PAGED_WAIT_NOTHING, PAGED_WAIT_BUSY, PAGED_WAIT_TWO = 0, 1, 2
 
 
 def selftest_paged_wait(kind: int, elapsed_ns, *, stream=None):
-    """Launch the self-test of the paged forward's waits (int64 [1] on the device: see bsa_selftest.h)."""
+    """Launch the self-test of the paged forward's waits (int64 [2] on the device: see bsa_selftest.h)."""
     import torch
-    _flat(elapsed_ns, "elapsed_ns", 1, torch.int64)
+    _flat(elapsed_ns, "elapsed_ns", 2, torch.int64)
     _check("bsa_selftest_paged_wait",
            load_library().bsa_selftest_paged_wait(int(kind), _ptr(elapsed_ns), _stream(stream)))
 
@@ -903,4 +903,5 @@ __all__ = ["BLOCK", "BsaError", "IDX_MASK_U8", "IDX_THRESHOLD_F32", "IDX_TOPK_F3
            "select_paged_workspace_size",
            "spectral_order", "spectral_order_workspace_size", "spectral_order_noalloc",
            "NOALLOC_SCRATCH_BYTES", "reorder_guard", "set_forward_options",
-           "selftest_exp2", "selftest_wait_timeout", "selftest_paged_wait", "PAGED_WAIT_NOTHING", "PAGED_WAIT_BUSY"]
+           "selftest_exp2", "selftest_wait_timeout", "selftest_paged_wait", "PAGED_WAIT_NOTHING", "PAGED_WAIT_BUSY",
+           "PAGED_WAIT_TWO"]

@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 }
                 const uint32_t pk = place_k(gb);
                 const bool wt = paged_wait(smem_u32(&sh->empty[pk % S]), (pk / S) & 1u, &sh->watch, status);
-                // (a failure elsewhere raises the status word, which ends this wait too)
+                // (a failure elsewhere in the block or in another one ends this wait too)
                 if (__any_sync(0xffffffffu, !wt)) {
                     ok = false;
                     break;

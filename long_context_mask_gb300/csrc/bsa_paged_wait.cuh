@@ -5,7 +5,6 @@
 
 #include "bsa.h"
 #include "bsa_ptx.cuh"
-#include "bsa_rows.cuh"
 
 namespace bsa {
 
@@ -14,12 +13,15 @@ constexpr uint64_t kPagedWaitNs = 1000000000ull;  // 1 s per wait
 // What the warps of a thread block know of one another (shared memory).
 struct Watch {
     uint64_t busy;   // when a key tile of a row computed from its own keys was last done
-    int32_t abort;
+    int32_t abort;   // a wait of the block has been given up: all others end too
 };
 
+// A call that timed out has rows it did not write, where the other codes speak of what
+// was left out of an otherwise whole result: it takes their place in the status word.
+__device__ __forceinline__ void raise_timeout(int32_t* status) { atomicExch(status, BSA_ERR_TIMEOUT); }
 __device__ __forceinline__ void set_abort(Watch* w, int32_t* status) {
     *reinterpret_cast<volatile int32_t*>(&w->abort) = 1;
-    raise_status(status, BSA_ERR_TIMEOUT);
+    raise_timeout(status);
 }
 // A bounded wait.  While rows are computed from their own keys (busy moves on with
 // every key tile of them) those who wait for them have not lost their time yet.  All but
@@ -35,7 +37,7 @@ __device__ __noinline__ bool paged_wait_on(uint32_t bar, uint32_t parity, const 
             // (busy may move on between the two looks, and be ahead of the clock's)
             const int64_t now = (int64_t)ptx::globaltimer(), last = (int64_t)w->busy;
             if (now - t0 > limit && now - last > limit) return false;
-            if (*status == BSA_ERR_TIMEOUT) return false;
+            if (w->abort != 0 || *status == BSA_ERR_TIMEOUT) return false;  // (or one of another block)
         }
     }
     return true;
@@ -46,7 +48,7 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const 
 }
 // For copies and products in flight, after a failure too.
 inline __device__ __noinline__ void paged_drain(uint32_t bar, uint32_t parity, int32_t* status) {
-    if (!ptx::mbar_wait(bar, parity, kPagedWaitNs, status, -1)) raise_status(status, BSA_ERR_TIMEOUT);
+    if (!ptx::mbar_wait(bar, parity, kPagedWaitNs, status, -1)) raise_timeout(status);
 }
 
 }  // namespace bsa

@@ -37,16 +37,18 @@ __global__ void k_selftest_wait(uint64_t limit_ns, int32_t* status) {
         atomicCAS(status, 0, BSA_ERR_TIMEOUT);
 }
 
-// The paged forward's waits: warp 0 waits on an mbarrier (2 ms), lane 0 of warp 1 does
-// what the kind says.  out[0]: the ns that warp 0 waited, negative where it gave up.
+// The paged forward's waits: warp 0 waits on an mbarrier (2 ms), warp 1 does what the
+// kind says.  out[w]: the ns that warp w waited, negative where it gave up.
 constexpr uint64_t kShortNs = 2000000ull, kBusyNs = 50000000ull;
 __global__ void k_selftest_paged_wait(int32_t kind, int64_t* out, int32_t* status) {
-    __shared__ uint64_t bar;
+    __shared__ uint64_t bar[2];
     __shared__ Watch watch;
-    const uint32_t b = ptx::smem_u32(&bar);
+    const uint32_t b = ptx::smem_u32(&bar[0]);
     if (threadIdx.x == 0) {
         ptx::mbar_init(b, 1);
+        ptx::mbar_init(ptx::smem_u32(&bar[1]), 1);
         ptx::fence_mbar_init();
+        out[0] = out[1] = 0;
         watch.busy = 0;
         watch.abort = 0;
     }
@@ -59,6 +61,10 @@ __global__ void k_selftest_paged_wait(int32_t kind, int64_t* out, int32_t* statu
             if (!ok) set_abort(&watch, status);
             out[0] = ok ? ns : -ns;
         }
+    } else if (kind == BSA_PAGED_WAIT_TWO) {
+        const bool ok = __all_sync(0xffffffffu, paged_wait(ptx::smem_u32(&bar[1]), 0, &watch, status));
+        const int64_t ns = (int64_t)(ptx::globaltimer() - t0);
+        if (threadIdx.x == 32) out[1] = ok ? ns : -ns;
     } else if (threadIdx.x == 32 && kind == BSA_PAGED_WAIT_BUSY) {
         // what it waits for goes on, and is there after 50 ms (each turn takes 10 ns at the least)
         for (int32_t i = 0; i < 10000000; ++i) {
@@ -94,8 +100,7 @@ bsa_status bsa_selftest_wait_timeout(int64_t limit_ns, void* stream) {
 }
 
 bsa_status bsa_selftest_paged_wait(int32_t kind, int64_t* elapsed_ns, void* stream) {
-    if (kind != BSA_PAGED_WAIT_NOTHING && kind != BSA_PAGED_WAIT_BUSY) return BSA_ERR_INVALID_ARG;
-    if (!elapsed_ns) return BSA_ERR_INVALID_ARG;
+    if (kind < BSA_PAGED_WAIT_NOTHING || kind > BSA_PAGED_WAIT_TWO || !elapsed_ns) return BSA_ERR_INVALID_ARG;
     int32_t* status = bsa::status_word_ptr();
     if (!status) return BSA_ERR_CUDA;
     bsa::k_selftest_paged_wait<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(kind, elapsed_ns, status);

@@ -104,15 +104,15 @@ def test_first_calls_from_several_threads_at_once():
 # ------------------------------------------------------------------ long waits
 
 def wait_selftest(kind):
-    ns = torch.zeros(1, dtype=torch.int64, device="cuda")
+    ns = torch.zeros(2, dtype=torch.int64, device="cuda")
     bsa.selftest_paged_wait(kind, ns)
-    return bsa.device_status(), ns.item() * 1e-6
+    return bsa.device_status(), (ns.double() * 1e-6).tolist()
 
 
 def test_a_wait_for_what_never_comes_ends():
     status_ok()
     st, ms = wait_selftest(bsa.PAGED_WAIT_NOTHING)
-    assert st == TIMEOUT and -1000 < ms <= -2
+    assert st == TIMEOUT and -1000 < ms[0] <= -2
     status_ok()
 
 
@@ -120,7 +120,21 @@ def test_a_wait_for_what_goes_on_goes_on():
     """Progress is noted all the time, between the waiting warp's looks at clock and note too."""
     for _ in range(3):
         st, ms = wait_selftest(bsa.PAGED_WAIT_BUSY)
-        assert st == 0 and 50 <= ms < 1000
+        assert st == 0 and 50 <= ms[0] < 1000
+
+
+@pytest.mark.parametrize("before", [0, BOUNDS])
+def test_a_time_out_is_told_whatever_was_to_be_told_before(before):
+    """It ends the block's other waits, and takes the place of a code that means less."""
+    status_ok()
+    if before:
+        b = ref.make([1], [40], H=1, H_kv=1, D=64, page=32, seed=1, poison=False)
+        b.kv_len.fill_(-1)
+        run_forward(b, ref.rows(b, 1, 2))                 # (BOUNDS: nothing is read through a bad length)
+    st, ms = wait_selftest(bsa.PAGED_WAIT_TWO)
+    assert st == TIMEOUT
+    assert -500 < ms[0] <= -2 and -500 < ms[1] <= -2
+    status_ok()
 
 
 @pytest.mark.parametrize("behind", [1, 1000])
