@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
     }
     const bool abandoned = sh->watch.abort != 0;
     if (warp == kMmaQK && !abandoned) {
+        __syncwarp();  // some lanes have looked for the runs' starts
         tmem_alloc(smem_u32(&sh->tmem_base), kTmemCols);
         tmem_relinquish();
     }
@@ -1048,6 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
+                __syncwarp();  // the lanes without a row skip the stores below
                 tmem_ld32(t_row + c, o);
                 tmem_wait_ld();
                 // (a sum that overflows says "not finite" too: the row is computed again for nothing)
