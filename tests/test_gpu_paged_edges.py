@@ -169,3 +169,89 @@ def test_short_sequences_behind_rows_that_take_long(behind):
     keys = torch.cat([torch.arange(L - n + 1, L + 1), torch.full((2,), behind)]).double().to(dev)
     # a sum of ones in fp32, at most 2^19: exact; a logarithm and a product
     assert ((lse.view(S, n + 2).double() - keys.log()).abs() <= 8 * 2.0 ** -24 * (1 + keys.log())).all()
+
+
+# ------------------------------------------------------------------ several runs a thread block
+
+def runs_per_block(b, window=0, sinks=0, causal=True, sel=None):
+    """How many runs of work a thread block of the attention takes: a batch whose key tiles are
+    read more than twice and hold more than 64 MB is gone through in up to four phases."""
+    tpt, grid = 128 // (b.H // b.H_kv), min(152, torch.cuda.get_device_properties(0).multi_processor_count)
+    starts = b.q_start.tolist()
+    tiles = pairs = cache = 0
+    for s, (n, length) in enumerate(zip(b.new, b.length)):
+        cache += (length + 127) // 128 * b.H_kv if n else 0
+        for t in range(0, n, tpt):
+            pos, last = length - n + t, length - n + min(t + tpt, n) - 1
+            tiles += b.H_kv
+            if sel is not None:
+                toks = range(starts[s] + t, starts[s] + min(t + tpt, n))
+                pairs += sum(max(1, len({x for i in toks for x in sel[i][h] if 128 * x <= length - n + i - starts[s]}))
+                             for h in range(b.H_kv))
+                continue
+            hi = last // 128 + 1 if causal else (length + 127) // 128
+            lo = min(max(pos - window + 1, 0) // 128, hi) if window else 0
+            pairs += b.H_kv * (hi - lo + (min((min(sinks, last + 1) + 127) // 128, lo) if window else 0))
+    units, size = pairs + 4 * tiles, cache * 128 * b.D * 4
+    if size <= 64 << 20 or pairs <= 2 * cache:
+        return 1
+    return min(4, -(-size // (64 << 20)), max(units // (16 * grid), 1))
+
+
+def check_heads(b, q, o, lse, kv_heads, sel=None, **kw):
+    """Some key/value heads against fp64."""
+    G = b.H // b.H_kv
+    for h in kv_heads:
+        one = ref.Batch(b.new, b.length, G, 1, b.D, b.page, "cuda", table=b.table, q_start=b.q_start, kv_len=b.kv_len,
+                        k_cache=b.k_cache[:, h:h + 1], v_cache=b.v_cache[:, h:h + 1], n_pages=b.n_pages, tokens=b.tokens)
+        x = slice(h * G, (h + 1) * G)
+        ref.check_attention(one, q[:, x], o[:, x], lse[:, x], sel=None if sel is None else [[t[h]] for t in sel], **kw)
+
+
+LARGE = {
+    # many chunks over caches of their own, some sequences without a new token
+    "batch": (4, dict(new=[89, 0, 90, 1, 70] * 15, length=[989, 300, 1000, 900, 1100] * 15, H=40, H_kv=8, D=128, page=32), {}),
+    "chunk": (3, dict(new=[1000], length=[36007], H=32, H_kv=8, D=128, page=128), {}),
+    "two": (2, dict(new=[400, 500], length=[12000, 9100], H=32, H_kv=8, D=128, page=16), {}),
+    "window": (3, dict(new=[2000] * 6, length=[3001] * 6, H=64, H_kv=16, D=128, page=64), dict(window=1000, sinks=130)),
+    "all": (2, dict(new=[300, 200], length=[80000, 60001], H=14, H_kv=2, D=64, page=128), dict(causal=False)),
+    "lists": (2, dict(new=[128, 40, 128, 128, 128], length=[40000, 40001, 39000, 41000, 128 * 300], H=14, H_kv=2, D=64, page=16),
+              "lists"),
+}
+
+
+@pytest.mark.parametrize("name", LARGE)
+def test_several_runs_to_a_thread_block(name):
+    """Batches whose key tiles are read by many query tiles and do not stay in L2."""
+    runs, shape, kw = LARGE[name]
+    b = ref.make(**shape, seed=130, poison=False)
+    q, sel = ref.rows(b, b.H, 131), None
+    if kw == "lists":
+        s, c, sel = lists_for(b, np.random.default_rng(132), 100)
+        kw = dict(sel=s, sel_cnt=c)
+        assert runs_per_block(b, sel=sel) == runs
+    else:
+        assert runs_per_block(b, **kw) == runs
+    o, lse = run_forward(b, q, **kw)
+    status_ok()
+    check_heads(b, q, o, lse, sorted({0, b.H_kv // 2, b.H_kv - 1}), sel,
+                **{k: v for k, v in kw.items() if k in ("causal", "window", "sinks")})
+    # every head: the same rows in a batch of one head (one run to a block, other cuts), within both bounds
+    o2, lse2 = run_forward(b, q, **kw)
+    assert torch.equal(bits(o), bits(o2)) and torch.equal(lse, lse2)
+    G = b.H // b.H_kv
+    for h in range(b.H_kv):
+        x = slice(h * G, (h + 1) * G)
+        oh, lh = torch.empty_like(o[:, x].contiguous()), torch.empty((b.tokens, G), device="cuda")
+        k1 = dict(kw)
+        if sel is not None:
+            k1.update(sel=kw["sel"][:, h:h + 1].contiguous(), sel_cnt=kw["sel_cnt"][:, h:h + 1].contiguous())
+        bsa.forward_paged(q[:, x].contiguous(), b.k_cache[:, h:h + 1].contiguous(), b.v_cache[:, h:h + 1].contiguous(),
+                          *b.arrays(), oh, lh, **k1)
+        # both sides within check_attention's bounds: weights rounded to bf16 (A is at most the
+        # largest |v|, below 8), O itself, and in fp32 d = (D + 16) 2^-24 (R + 1) < 2^-12, R < 27
+        far = 2 * 1.01 * 2.0 ** -8 * (b.v_cache.abs().max().float() + oh.float().abs()) + 2.0 ** -7
+        assert ((o[:, x].float() - oh.float()).abs() <= far).all()
+        fin = torch.isfinite(lh)
+        assert torch.equal(torch.isfinite(lse[:, x]), fin) and ((lse[:, x] - lh).abs()[fin] <= 2.0 ** -10).all()
+    status_ok()
