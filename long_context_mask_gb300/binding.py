@@ -740,6 +740,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
     mean key of every 128-token block that fills up (see bsa.h)."""
     bf16 = (_torch or _load_torch()).bfloat16
     kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+    if len(k.shape) != 3:
+        raise ValueError(f"k: shape {tuple(k.shape)}, expected [tokens, H_kv, D]")
     tokens = k.shape[0]
     kp, ks = _token_rows(k, "k", tokens, H_kv, D)
     vp, vs = _token_rows(v, "v", tokens, H_kv, D)
@@ -747,6 +749,8 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
     if q is not None:
         if q_out is None:
             raise ValueError("paged_append: pass q_out with q")
+        if len(q.shape) != 3:
+            raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
         H = q.shape[1]
         qp, qs = _token_rows(q, "q", tokens, H, D)
         op, os_ = _token_rows(q_out, "q_out", tokens, H, D)

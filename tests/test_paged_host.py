@@ -241,3 +241,11 @@ def test_heads_fit_the_launches(lib, call):
     """A launch has a thread block for each group of heads along one axis, of at most 65535."""
     assert call(lib, batch(tokens=0), H=16384, H_kv=16384) == OK
     assert call(lib, batch(tokens=0), H=16385, H_kv=16385) == INVALID
+
+
+# ------------------------------------------------------------------ other ranks, numbers that do not fit
+
+@pytest.mark.parametrize("kw", [dict(q=bf16(T)), dict(q=bf16(T * H * D)), dict(q=bf16(T, H * D)), dict(q_out=bf16(T)),
+                                dict(k=bf16(T)), dict(k=torch.zeros((), dtype=torch.bfloat16)), dict(v=bf16(T * K, D))])
+def test_append_refuses_other_ranks(lib, kw):
+    rejected(call_append, **kw)
