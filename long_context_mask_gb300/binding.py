@@ -683,6 +683,13 @@ def _token_rows(t, name, tokens, heads, D):
     return t.data_ptr(), a if tokens > 1 else heads * D
 
 
+def _fits(**numbers):
+    """Numbers that the C ABI takes as int32 (ctypes would cut the others)."""
+    for name, x in numbers.items():
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{name}: {x} does not fit 32 bits")
+
+
 def _paged_cache(k_cache, v_cache):
     """(k's address, v's address, pages, H_kv, page_size, D)."""
     shape = k_cache.shape
@@ -697,6 +704,8 @@ def _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages):
     if len(shape) != 2:
         raise ValueError(f"page_table: shape {tuple(shape)}, expected [seqs, max_pages]")
     seqs, max_pages = shape
+    if (seqs | tokens | max_pages | page_size | n_pages) >> 31:
+        _fits(seqs=seqs, tokens=tokens, max_pages=max_pages, page_size=page_size, n_pages=n_pages)
     i32 = _torch.int32
     return PagedBatch(_array(page_table, "page_table", i32, 0), _array(q_start, "q_start", i32, seqs + 1),
                       _array(kv_len, "kv_len", i32, seqs), seqs, tokens, max_pages, page_size, n_pages)
@@ -774,6 +783,7 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
 
 def forward_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
                                  D: int, sel_width: int = 0) -> int:
+    _fits(seqs=seqs, tokens=tokens, max_pages=max_pages, page_size=page_size, H=H, H_kv=H_kv, D=D, sel_width=sel_width)
     b = PagedBatch(None, None, None, seqs, tokens, max_pages, page_size, 1)
     return int(load_library().bsa_forward_paged_workspace_size(ctypes.byref(b), H, H_kv, D, sel_width))
 
@@ -787,6 +797,8 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
     blocks (see bsa.h).  ``workspace`` is a CUDA tensor of at least
     forward_paged_workspace_size() bytes (allocated here when omitted)."""
     torch = _torch or _load_torch()
+    if (window | sinks) >> 31:
+        _fits(window=window, sinks=sinks)
     kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
@@ -814,6 +826,7 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
 
 def select_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
                                 D: int) -> int:
+    _fits(seqs=seqs, tokens=tokens, max_pages=max_pages, page_size=page_size, H=H, H_kv=H_kv, D=D)
     b = PagedBatch(None, None, None, seqs, tokens, max_pages, page_size, 1)
     return int(load_library().bsa_select_paged_workspace_size(ctypes.byref(b), H, H_kv, D))
 
@@ -827,6 +840,8 @@ def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_s
     ``workspace`` is a CUDA tensor of at least select_paged_workspace_size()
     bytes (allocated here when omitted)."""
     torch = _torch or _load_torch()
+    if (topk | sink_blocks | local_blocks) >> 31:
+        _fits(topk=topk, sink_blocks=sink_blocks, local_blocks=local_blocks)
     if k_mean.dim() != 3 or q.dim() != 3:
         raise ValueError("select_paged: q [tokens, H, D], k_mean [pages, H_kv, D]")
     n_pages, H_kv, D = k_mean.shape

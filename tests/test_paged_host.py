@@ -249,3 +249,24 @@ def test_heads_fit_the_launches(lib, call):
                                 dict(k=bf16(T)), dict(k=torch.zeros((), dtype=torch.bfloat16)), dict(v=bf16(T * K, D))])
 def test_append_refuses_other_ranks(lib, kw):
     rejected(call_append, **kw)
+
+
+@pytest.mark.parametrize("call,kw", [
+    (call_forward, dict(window=1 << 32)), (call_forward, dict(window=(1 << 32) + 575, sinks=64)),
+    (call_forward, dict(window=64, sinks=1 << 31)), (call_forward, dict(sinks=-(1 << 32))),
+    (call_select, dict(topk=(1 << 32) + 4)), (call_select, dict(sink_blocks=1 << 32)),
+    (call_select, dict(local_blocks=(1 << 32) + 1)), (call_select, dict(page_size=(1 << 32) + P))])
+def test_numbers_beyond_32_bits_are_not_cut(lib, call, kw):
+    """(cut to 32 bits they would be another window, another number of blocks)"""
+    rejected(call, **kw)
+
+
+def test_workspace_sizes_of_numbers_beyond_32_bits(lib):
+    sizes = dict(seqs=S, tokens=T, max_pages=8, page_size=P, H=H, H_kv=K, D=D)
+    assert bsa.forward_paged_workspace_size(**sizes) > 0 and bsa.select_paged_workspace_size(**sizes) > 0
+    for name in sizes:
+        for fn in (bsa.forward_paged_workspace_size, bsa.select_paged_workspace_size):
+            with pytest.raises(ValueError):
+                fn(**{**sizes, name: sizes[name] + (1 << 32)})
+    with pytest.raises(ValueError):
+        bsa.forward_paged_workspace_size(**sizes, sel_width=1 << 32)
