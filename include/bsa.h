@@ -740,7 +740,9 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
  *     O = sum_j exp(s_j - LSE) v_j.
  * Without any such key O = 0 and LSE = -inf.  Keys and values that a row does
  * not see (masked, not listed, behind the end of the sequence) do not matter,
- * NaN and infinities included; rows next to such values take longer.
+ * NaN and infinities included.  A row beside such a value (one of the 128
+ * keys at an edge of what it sees, or of a block that a neighbour lists) takes
+ * some hundred times as long.
  *
  *  q          device bf16, 16-byte aligned.
  *  causal     0 or 1.   window, sinks  >= 0; window must be 0 with sel.

@@ -49,8 +49,10 @@
 // scores are dropped by a select, and the value rows behind the end of a
 // sequence are zeroed in shared memory before the product (0 times NaN is NaN).
 // A value that one row of a tile sees and another does not cannot be zeroed: a
-// row whose O comes out not finite, and that has a key hidden in its segment,
-// is computed again from its own keys alone (see own_keys_row).
+// row whose O comes out not finite, and that hides such a value in its segment
+// (see bad_values), is computed again from its own keys alone (see own_keys_row).
+// (One bad value that all rows see: 4000 rows over 4250 keys took 33 ms without the look
+// at what they hide, 0.15 ms with it, as without the value.)
 //
 // Measured, 32 + 8 heads of 128: 64 tokens over 1.7 GB of keys and values 254 us
 // (the copy rate); one token over 131072 86 us and 5 for the join (6.2 TB/s); a
@@ -165,6 +167,38 @@ struct Params {
     float2* part_ml;          // [runs, 2, 128] maximum (log2) and sum
     int4* joins;              // [runs] parts (0: none), q0, ntok, kvh
 };
+
+// The first and the last of a sequence's keys from .. to - 1 whose value row is not
+// finite (first > last: none).  The whole warp works on it.
+struct BadKeys {
+    int32_t first, last;
+};
+template <int D>
+__device__ __noinline__ BadKeys bad_values(const Params& P, int32_t seq, int32_t kvh, int32_t from, int32_t to) {
+    const int lane = threadIdx.x & 31;
+    const int32_t* table = P.b.table + (int64_t)seq * P.b.max_pages;
+    int32_t first = INT32_MAX, last = -1;
+    for (int32_t key = max(from, 0) + lane; key < to; key += 32) {
+        int32_t id = table[key / P.b.page];
+        if (id < 0 || id >= P.b.n_pages) id = 0;  // (reported by the loading warps)
+        const __nv_bfloat16* row = P.v_cache + (((int64_t)id * P.H_kv + kvh) * P.b.page + key % P.b.page) * D;
+        bool bad = false;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + d);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // (all bits of an exponent are set)
+                bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+        }
+        if (bad) {
+            first = min(first, key);
+            last = key;
+        }
+    }
+    __syncwarp();
+    return {__reduce_min_sync(0xffffffffu, first), __reduce_max_sync(0xffffffffu, last)};
+}
 
 // O = sum_j 2^(s_j - m) v_j of one row over the keys of a segment that the row
 // sees, read from the cache one by one; to out (fp32, unscaled) or, times inv, to
@@ -1081,9 +1115,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
             }
             uint32_t again = __ballot_sync(0xffffffffu, !finite && !dead);
             if (again != 0u) {
-                // rows that see every key of the segment's tiles are what they are
-                const int32_t x = sp->j0 + n - 1, end = kLists ? sp->kl : (sp->lo + x - sp->ns + 1) * 128;
-                const bool hides = kMode != kPlain || (P.causal && sp->pos0 + tok + 1 < min(sp->kl, end));
+                // A row that hides no value that is not finite is what it is.  What rows of the
+                // segment hide lies at the edges of what they see: behind their own positions,
+                // before their windows, behind the sinks.  (With lists it may be anywhere, but a row has
+                // no more keys than it lists.)
+                bool hides = true;
+                if constexpr (!kLists) {
+                    const int32_t x = sp->j0 + n - 1, p0 = sp->pos0, last = p0 + sp->ntok - 1, p = p0 + tok;
+                    const int32_t end = min(sp->kl, ((x < sp->ns ? x : sp->lo + x - sp->ns) + 1) * 128);  // of the tiles' keys
+                    hides = P.causal && bad_values<D>(P, sp->seq, sp->kvh, p0 + 1, end).last > p;
+                    if constexpr (kMode == kWindow) {
+                        const int32_t lo = sp->lo * 128;
+                        hides |= bad_values<D>(P, sp->seq, sp->kvh, max(lo, P.sinks), min(end, last - P.window + 1)).first <= p - P.window;
+                        const BadKeys sink = bad_values<D>(P, sp->seq, sp->kvh, P.sinks, min(sp->kl, sp->ns * 128));
+                        hides |= sink.first <= sink.last;
+                    }
+                }
                 again = __ballot_sync(0xffffffffu, !finite && !dead && hides);
                 __syncwarp();  // the row's own thread has written it
                 for (; again; again &= again - 1u) {

@@ -255,3 +255,64 @@ def test_several_runs_to_a_thread_block(name):
         fin = torch.isfinite(lh)
         assert torch.equal(torch.isfinite(lse[:, x]), fin) and ((lse[:, x] - lh).abs()[fin] <= 2.0 ** -10).all()
     status_ok()
+
+
+# ------------------------------------------------------------------ values that are not finite and seen
+
+def elapsed(f, n=5):
+    f()
+    times = []
+    for _ in range(n):
+        a, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        e.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(e))
+    return sorted(times)[n // 2]
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=1500, sinks=100)])
+def test_a_value_that_all_rows_see_costs_no_time(kw):
+    """Rows next to hidden values that are not finite are computed key by key, which takes some
+    hundred times as long; one bad value in the far past, which every row sees, is not such a case."""
+    S = 16  # (enough for whole rows in a thread block's run)
+    b = ref.make([250] * S, [4250 + 64 * s for s in range(S)], H=8, H_kv=2, D=128, page=64, seed=140, poison=False)
+    q = ref.rows(b, 8, 141)
+    clean = elapsed(lambda: run_forward(b, q, **kw))
+    o0, lse0 = run_forward(b, q, **kw)
+    pos = 7 if kw else 3000
+    b.v_cache[b.table[:, pos // 64].long(), :, pos % 64, 5] = float("nan")
+    b.v_cache[b.table[:, pos // 64].long(), :, pos % 64, 9] = float("inf")
+    took = elapsed(lambda: run_forward(b, q, **kw))
+    o, lse = run_forward(b, q, **kw)
+    status_ok()
+    assert torch.isnan(o[:, :, 5]).all() and torch.isinf(o[:, :, 9]).all()
+    rest = torch.ones(128, dtype=torch.bool, device="cuda")
+    rest[5] = rest[9] = False
+    assert torch.equal(bits(o)[..., rest], bits(o0)[..., rest]) and torch.equal(lse, lse0)
+    assert took < 5 * clean + 0.1, (took, clean)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("place", [70, 127, 1079, 1080, 1081, 1150, 1199, 1381, 1400, 1499])
+@pytest.mark.parametrize("H,K,D,page", [(4, 2, 128, 32), (14, 2, 64, 128)])
+def test_one_bad_value_at_an_edge_of_what_rows_see(H, K, D, page, place, causal):
+    """Behind the sinks, before and within the windows' first keys, behind the rows' own positions:
+    each alone, so that each edge is looked at for itself."""
+    window, sinks = 300, 70
+    b = ref.make([120, 33], [1500, 700], H=H, H_kv=K, D=D, page=page, seed=150, poison=False)
+    q = ref.rows(b, H, 151)
+    kw = dict(causal=causal, window=window, sinks=sinks)
+    o0, lse0 = run_forward(b, q, **kw)
+    good = b.v_cache.clone()
+    b.v_cache[b.table[0, place // page], :, place % page, 3] = float("nan")
+    o, lse = run_forward(b, q, **kw)
+    status_ok()
+    p = torch.arange(1380, 1500, device="cuda")
+    sees = ((place <= p) | (not causal)) & ((place > p - window) | (place < sinks))
+    hit = torch.cat([sees, torch.zeros(33, dtype=torch.bool, device="cuda")])
+    assert torch.isnan(o[hit][:, :, 3]).all() and torch.isfinite(o[~hit].float()).all()
+    b.v_cache = good
+    o[hit] = o0[hit]
+    ref.check_attention(b, q, o, lse, **kw)
