@@ -291,6 +291,32 @@ __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, in
     }
 }
 
+// The rows of a segment, a row a lane, whose O is not finite: those that hide a value
+// that is not either are computed from their own keys.  The others are what they are.
+// What rows of a segment hide lies at the edges of what they see: behind their own
+// positions, before their windows, behind the sinks.  (With lists it may be anywhere,
+// but a row has no more keys than it lists.)
+template <int D, int kMode>
+__device__ __noinline__ void rows_again(const Params& P, const Segment& sg, int32_t row, uint32_t again, float m, float inv, uint64_t* busy) {
+    bool hides = true;
+    if constexpr (kMode != kListed) {
+        const int32_t x = sg.j0 + sg.n - 1, p0 = sg.pos0, last = p0 + sg.ntok - 1, p = p0 + row / P.group;
+        const int32_t end = min(sg.kl, ((x < sg.ns ? x : sg.lo + x - sg.ns) + 1) * 128);  // of the tiles' keys
+        hides = P.causal && bad_values<D>(P, sg.seq, sg.kvh, p0 + 1, end).last > p;
+        if constexpr (kMode == kWindow) {
+            hides |= bad_values<D>(P, sg.seq, sg.kvh, max(sg.lo * 128, P.sinks), min(end, last - P.window + 1)).first <= p - P.window;
+            const BadKeys sink = bad_values<D>(P, sg.seq, sg.kvh, P.sinks, min(sg.kl, sg.ns * 128));
+            hides |= sink.first <= sink.last;
+        }
+    }
+    __syncwarp();  // the rows' own threads have written them
+    for (again &= __ballot_sync(0xffffffffu, hides); again; again &= again - 1u) {
+        const int i = __ffs(again) - 1;
+        const float mi = __shfl_sync(0xffffffffu, m, i), li = __shfl_sync(0xffffffffu, inv, i);
+        own_keys_row<D, kMode>(P, sg, (row & ~31) + i, mi, li, busy);
+    }
+}
+
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, int32_t* status) {
     return __all_sync(0xffffffffu, paged_wait(bar, parity, w, status));
 }
@@ -1113,32 +1139,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_forward(const __grid_cons
                 if (slot < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
                 else P.part_ml[part] = ml;
             }
-            uint32_t again = __ballot_sync(0xffffffffu, !finite && !dead);
-            if (again != 0u) {
-                // A row that hides no value that is not finite is what it is.  What rows of the
-                // segment hide lies at the edges of what they see: behind their own positions,
-                // before their windows, behind the sinks.  (With lists it may be anywhere, but a row has
-                // no more keys than it lists.)
-                bool hides = true;
-                if constexpr (!kLists) {
-                    const int32_t x = sp->j0 + n - 1, p0 = sp->pos0, last = p0 + sp->ntok - 1, p = p0 + tok;
-                    const int32_t end = min(sp->kl, ((x < sp->ns ? x : sp->lo + x - sp->ns) + 1) * 128);  // of the tiles' keys
-                    hides = P.causal && bad_values<D>(P, sp->seq, sp->kvh, p0 + 1, end).last > p;
-                    if constexpr (kMode == kWindow) {
-                        const int32_t lo = sp->lo * 128;
-                        hides |= bad_values<D>(P, sp->seq, sp->kvh, max(lo, P.sinks), min(end, last - P.window + 1)).first <= p - P.window;
-                        const BadKeys sink = bad_values<D>(P, sp->seq, sp->kvh, P.sinks, min(sp->kl, sp->ns * 128));
-                        hides |= sink.first <= sink.last;
-                    }
-                }
-                again = __ballot_sync(0xffffffffu, !finite && !dead && hides);
-                __syncwarp();  // the row's own thread has written it
-                for (; again; again &= again - 1u) {
-                    const int i = __ffs(again) - 1;
-                    const float mi = __shfl_sync(0xffffffffu, ml.x, i), li = __shfl_sync(0xffffffffu, inv, i);
-                    own_keys_row<D, kMode>(P, *sp, qd * 32 + i, mi, li, &sh->watch.busy);
-                }
-            }
+            const uint32_t again = __ballot_sync(0xffffffffu, !finite && !dead);
+            if (again != 0u) rows_again<D, kMode>(P, *sp, row, again, ml.x, inv, &sh->watch.busy);
             hand_back(k);
             g += (uint32_t)n;
             ++segs;
