@@ -294,13 +294,23 @@ __device__ __noinline__ void own_keys_row(const Params& P, const Segment& sg, in
 // The rows of a segment, a row a lane, whose O is not finite: those that hide a value
 // that is not either are computed from their own keys.  The others are what they are.
 // What rows of a segment hide lies at the edges of what they see: behind their own
-// positions, before their windows, behind the sinks.  (With lists it may be anywhere,
-// but a row has no more keys than it lists.)
+// positions, before their windows, behind the sinks.  With lists it is what they do
+// not list, too.
 template <int D, int kMode>
 __device__ __noinline__ void rows_again(const Params& P, const Segment& sg, int32_t row, uint32_t again, float m, float inv, uint64_t* busy) {
-    bool hides = true;
-    if constexpr (kMode != kListed) {
-        const int32_t x = sg.j0 + sg.n - 1, p0 = sg.pos0, last = p0 + sg.ntok - 1, p = p0 + row / P.group;
+    const int32_t p0 = sg.pos0, tok = row / P.group, p = p0 + tok;
+    bool hides = false;
+    if constexpr (kMode == kListed) {
+        for (int32_t j = 0; j < sg.n && (again & ~__ballot_sync(0xffffffffu, hides)) != 0u; ++j) {
+            const int64_t e = (int64_t)sg.list * P.cap + sg.j0 + j;
+            const int32_t kt = P.list[e];
+            const int32_t last = bad_values<D>(P, sg.seq, sg.kvh, kt * 128, min(sg.kl, kt * 128 + 128)).last;
+            const bool listed = tok < sg.ntok && ((P.list_who[e * P.words + (tok >> 5)] >> (tok & 31)) & 1u);
+            hides |= last >= 0 && (!listed || (P.causal && last > p));
+            if ((threadIdx.x & 31) == 0) *reinterpret_cast<volatile uint64_t*>(busy) = globaltimer();
+        }
+    } else {
+        const int32_t x = sg.j0 + sg.n - 1, last = p0 + sg.ntok - 1;
         const int32_t end = min(sg.kl, ((x < sg.ns ? x : sg.lo + x - sg.ns) + 1) * 128);  // of the tiles' keys
         hides = P.causal && bad_values<D>(P, sg.seq, sg.kvh, p0 + 1, end).last > p;
         if constexpr (kMode == kWindow) {

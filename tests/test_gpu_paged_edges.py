@@ -272,13 +272,17 @@ def elapsed(f, n=5):
     return sorted(times)[n // 2]
 
 
-@pytest.mark.parametrize("kw", [{}, dict(window=1500, sinks=100)])
+@pytest.mark.parametrize("kw", [{}, dict(window=1500, sinks=100), "lists"])
 def test_a_value_that_all_rows_see_costs_no_time(kw):
     """Rows next to hidden values that are not finite are computed key by key, which takes some
     hundred times as long; one bad value in the far past, which every row sees, is not such a case."""
     S = 16  # (enough for whole rows in a thread block's run)
     b = ref.make([250] * S, [4250 + 64 * s for s in range(S)], H=8, H_kv=2, D=128, page=64, seed=140, poison=False)
     q = ref.rows(b, 8, 141)
+    if kw == "lists":
+        sel, cnt, _ = lists_for(b, np.random.default_rng(142), 12)
+        sel[..., 0] = 0
+        kw = dict(sel=sel.clamp(min=0), sel_cnt=cnt.clamp(min=1))
     clean = elapsed(lambda: run_forward(b, q, **kw))
     o0, lse0 = run_forward(b, q, **kw)
     pos = 7 if kw else 3000
