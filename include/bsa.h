@@ -718,6 +718,10 @@ typedef struct {
  *  k_cache, v_cache, k_mean  as above; k_mean NULL: no means.
  *  Two new tokens must not share a slot of the cache (two sequences, or two
  *  table entries of one, that name the same page for positions both written).
+ *  What a sequence held before the call must be in the cache before it: with
+ *  k_mean, a block that fills up must not hold tokens that another sequence
+ *  writes in the same call (append a shared prefix in a call of its own).
+ *  Apart from q_out over q, outputs must not overlap inputs.
  *  A sequence with more new tokens than kv_len raises BSA_ERR_BOUNDS; the
  *  tokens before position 0 are left out.
  */
@@ -742,7 +746,11 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
  * not see (masked, not listed, behind the end of the sequence) do not matter,
  * NaN and infinities included.  A row beside such a value (one of the 128
  * keys at an edge of what it sees, or of a block that a neighbour lists) takes
- * some hundred times as long.
+ * some hundred times as long, and its last bits may differ from what they are
+ * beside finite values (its weights are not rounded to bf16).
+ * The weights exp(s_j - LSE) are rounded to bf16 before they meet v_j; sums and
+ * LSE take them unrounded.  Values beyond 2^44 in magnitude may overflow on the
+ * way (a sum is kept against an earlier maximum until it exceeds 2^64).
  *
  *  q          device bf16, 16-byte aligned.
  *  causal     0 or 1.   window, sinks  >= 0; window must be 0 with sel.
@@ -761,6 +769,7 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
  *             Calls that share a workspace must not overlap on the GPU.
  *  o          device bf16 [tokens, H, D], 16-byte aligned, out.
  *  lse        device fp32 [tokens, H] out.
+ *  o and lse must not overlap inputs.
  *  A row's result does not depend on timing; it may depend in its last bits
  *  on the rest of the batch (which decides where a long row is split).
  */
@@ -792,7 +801,9 @@ size_t bsa_forward_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int
  *             takes it).
  *  k_mean     device bf16 [n_pages, H_kv, D].
  *  topk, sink_blocks  >= 0.   local_blocks  >= 1.
- *  max_pages * page_size <= 2^20 (else BSA_ERR_UNSUPPORTED).
+ *  max_pages * page_size <= 2^20 (else BSA_ERR_UNSUPPORTED).  The call takes
+ *  longer the wider the table is, whatever kv_len says (16 tokens over up to
+ *  512 blocks: 21 us with room for 512, 48 us with room for 7700).
  *  workspace  as in bsa_forward_paged (may be NULL where the size is 0).
  *  sel        device int32 [tokens, H_kv, width] out: ascending, tail -1.
  *  sel_cnt    device int32 [tokens, H_kv] out.

@@ -21,7 +21,7 @@
 // halves, four of either half (a pair meets in one thread), else eight in a row,
 // with the rotation partner's values by shuffles.  Every thread loads its four
 // rows before it works on the first.  (A prompt of 8192 tokens, 32 + 8 heads of
-// 128 with norms, 206 MB: 42 us, 0.72 of the copy rate; 107 us with one row at a time,
+// 128 with norms, 206 MB: 43 us, 0.71 of the copy rate; 107 us with one row at a time,
 // 62 us when each row found its place for itself, 234 instructions a row.  A step of 32
 // tokens: 5.7 us, most of it the launch.)
 #include <cuda_bf16.h>

@@ -45,6 +45,12 @@
 // tile g - 3 has read it), so that the next segment's scores are there when the
 // softmax comes to them.
 //
+// Rounding.  The weights exp(s - m) are rounded to bf16 for the product P V: the tensor
+// core takes both operands in one type, and the values are bf16 (fp16 has not the range for
+// weights up to 2^64, see softmax_rows; tf32 would have V converted and half the rate).
+// Row sums add them unrounded.  O is 2.0 to 2.4e-3 (relative, in norm) from 64-bit values,
+// where its own rounding to bf16 alone is 1.7e-3.
+//
 // What a row does not see may hold anything, NaN and infinities included.  Its
 // scores are dropped by a select, and the value rows behind the end of a
 // sequence are zeroed in shared memory before the product (0 times NaN is NaN).
@@ -55,8 +61,9 @@
 // at what they hide, 0.15 ms with it, as without the value.)
 //
 // Measured, 32 + 8 heads of 128: 64 tokens over 1.7 GB of keys and values 254 us
-// (the copy rate); one token over 131072 86 us and 5 for the join (6.2 TB/s); a
-// prompt of 8192 344 us (0.84 of the burst rate of a plain product), where the
+// (the copy rate); one token over 131072 90 us with the join (6.2 TB/s while it reads); a
+// prompt of 8192 344 us (0.84 of the burst rate of a plain product; 387 us called in a
+// loop, under the power limit), where the
 // tensor core is busy 70 % of the time and the softmax hardly ever waits: 1,370
 // cycles a tile pair, of which loading the scores takes 160, the exponentials of two
 // warps to a scheduler 800 (512 is the least), storing 130.  Two groups of softmax

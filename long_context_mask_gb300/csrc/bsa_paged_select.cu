@@ -12,8 +12,8 @@
 // block above tau + 2E is among the k best and none below tau - 2E is.  Blocks
 // in between are scored again in fp64 where there are more of them than places.
 //
-// Measured, 32 + 8 heads of 128, 16 of up to 512 blocks: 16 tokens 26 us (both kernels
-// wait for their loads: 12 MB, 128 rows), 1024 tokens 67 us (39 the scores, 1.1 GFLOP in
+// Measured, 32 + 8 heads of 128, 16 of up to 512 blocks: 16 tokens 21 us (both kernels
+// wait for their loads: 12 MB, 128 rows), 1024 tokens 62 us (39 the scores, 1.1 GFLOP in
 // packed fp32: tensor cores would not give sums with a bound on their rounding; tiles of
 // 128 blocks, two to an SM instead of three, take 41).
 #include <cuda_bf16.h>
