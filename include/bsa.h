@@ -43,7 +43,8 @@ typedef enum {
     BSA_ERR_OVERFLOW = 3,    /* device: a list longer than max_kv (truncated)  */
     BSA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed               */
     BSA_ERR_TIMEOUT = 5,     /* device: a bounded wait gave up                  */
-    BSA_ERR_BOUNDS = 6       /* device: an index/map/perm entry out of range    */
+    BSA_ERR_BOUNDS = 6,      /* device: an index/map/perm entry out of range    */
+    BSA_ERR_NONFINITE = 7    /* device: a value a 4-bit cache cannot hold        */
 } bsa_status;
 
 typedef enum {
@@ -817,6 +818,112 @@ bsa_status bsa_select_paged(const bsa_paged_batch* b, const void* q, int64_t q_s
 
 /* Bytes of workspace bsa_select_paged needs.  Only b's sizes are read. */
 size_t bsa_select_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D);
+
+/*
+ * A cache in 4 bits.
+ *
+ * The pages hold, in place of bf16 rows, rows of 4-bit codes with a scale for
+ * every 16 values: 4.5 bits a value.  Value d of a row stands for
+ *     level(code_d) * scale_(d / 16) * gain
+ * code   a 4-bit float e2m1: bit 3 the sign, bits 0 .. 2 one of the levels 0,
+ *        0.5, 1, 1.5, 2, 3, 4, 6; value 2i of a row is the low half of byte i.
+ * scale  an 8-bit float e4m3 (at most 448; a negative or NaN byte, which
+ *        bsa_paged_append_fp4 never writes, counts as 0).
+ * gain   one fp32 number for each key/value head, positive and finite (1
+ *        where the array is NULL): the head's values should lie between some
+ *        0.02 and 2688 gains, the range that scales and levels reach.
+ * A row x is quantised group by group as
+ *     t = x / gain,  scale = e4m3(max |t| / 6),  code = e2m1(t / scale),
+ * quotients in fp32, both roundings to the nearest with halves to even; codes
+ * are 0 where the scale is 0.  Infinities, and magnitudes beyond 2688 gains,
+ * become the largest a code can hold; a NaN becomes 0.  An infinity or a NaN
+ * raises BSA_ERR_NONFINITE.
+ *
+ *   k, v              device [n_pages, H_kv, page_size, D / 2] bytes of codes,
+ *   k_scale, v_scale  device [n_pages, H_kv, page_size, D / 16] bytes, all
+ *                     16-byte aligned;
+ *   k_gain, v_gain    device fp32 [H_kv], 4-byte aligned, or NULL.
+ *
+ * bsa_select_paged chooses blocks of such a cache as of any other: its k_mean
+ * is bf16 here too.
+ */
+typedef struct {
+    void* k;
+    void* k_scale;
+    void* v;
+    void* v_scale;
+    const float* k_gain;
+    const float* v_gain;
+} bsa_fp4_cache;
+
+/*
+ * bsa_paged_append_fp4 - bsa_paged_append into a cache in 4 bits: norms and
+ * rotation as there (fp32, not rounded to bf16 before they are quantised),
+ * queries to q_out in bf16, keys and values quantised.  k_mean receives the
+ * means of the keys as the cache holds them.  A norm's squares are summed in
+ * two fp32 words and every product of a key's rotation is rounded by itself,
+ * so that codes do not depend on the order of a sum.
+ *
+ *  cache      host struct, read during the call.
+ *  All else, and all limits, as in bsa_paged_append.
+ */
+bsa_status bsa_paged_append_fp4(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, int32_t H,
+                                int32_t H_kv, int32_t D, const float* rope, int32_t rope_len,
+                                int32_t rot, int32_t interleaved, const void* q_norm,
+                                const void* k_norm, float eps, void* q_out, int64_t q_out_stride,
+                                const bsa_fp4_cache* cache, void* k_mean, void* stream);
+
+/*
+ * bsa_paged_read_fp4 - the tokens of a batch out of a cache in 4 bits, as bf16.
+ *
+ * For every sequence, the last q_start[s+1] - q_start[s] of its kv_len[s]
+ * tokens go to packed tokens q_start[s] .. of k_out and v_out [tokens, H_kv,
+ * D]: level * scale * gain, rounded once (exact without gains).  To read
+ * tokens a .. b - 1 of a sequence, give it b for kv_len and b - a tokens.
+ *
+ *  k_out, v_out  device bf16, 16-byte aligned; either may be NULL.  *_stride
+ *             as in the batch's description.  They must not overlap inputs.
+ *  The same tokens may be read into several places (several sequences with the
+ *  same pages).  A sequence that asks for more tokens than kv_len raises
+ *  BSA_ERR_BOUNDS; the rows of tokens before position 0, and of tokens whose
+ *  page entry is out of range, are left as they were.
+ */
+bsa_status bsa_paged_read_fp4(const bsa_paged_batch* b, int32_t H_kv, int32_t D,
+                              const bsa_fp4_cache* cache, void* k_out, int64_t k_out_stride,
+                              void* v_out, int64_t v_out_stride, void* stream);
+
+/*
+ * bsa_forward_paged_fp4 - bsa_forward_paged over a cache in 4 bits.
+ *
+ * The same formulas, masks, lists and limits, with k_j and v_j as the cache
+ * holds them.  Levels times scales are exact in fp16, and gains are applied in
+ * fp32 to the scores and to O.  Queries are rounded to fp16 after a power of
+ * two has brought their row's largest value to 2^14 .. 2^15 (a bf16 value loses
+ * bits only where it lies 2^30 below its row's largest); the weights are
+ * rounded to fp16 (2^-11 relative, 2^-25 of the largest absolute) before they
+ * meet the values; sums and LSE take them unrounded.
+ * What a row does not see does not matter; what it sees is always finite.  A
+ * query that holds an infinity or a NaN makes its own rows' results NaN.
+ *
+ *  max_new    the most new tokens that any of the sequences has, if the host
+ *             knows (1 for a step of single tokens), else 0.  It decides how the
+ *             work is done, not what comes out: a sequence may have more.
+ *  workspace  of at least bsa_forward_paged_fp4_workspace_size() bytes.
+ *  (tokens + seqs) * H_kv must be below 2^31 with lists.
+ *  All else as in bsa_forward_paged.
+ */
+bsa_status bsa_forward_paged_fp4(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                                 const bsa_fp4_cache* cache, int32_t H, int32_t H_kv, int32_t D,
+                                 int32_t causal, int32_t window, int32_t sinks, const int32_t* sel,
+                                 const int32_t* sel_cnt, int32_t sel_width, float scale,
+                                 int32_t max_new, void* workspace, size_t workspace_bytes, void* o,
+                                 float* lse, void* stream);
+
+/* Bytes of workspace bsa_forward_paged_fp4 needs (0 for sizes it rejects);
+ * sel_width 0: without lists.  Only b's sizes are read. */
+size_t bsa_forward_paged_fp4_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
+                                            int32_t sel_width);
 
 /*
  * bsa_set_forward_options - how this host thread's later forward calls

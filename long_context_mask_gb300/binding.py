@@ -17,7 +17,7 @@ IDX_MASK_U8, IDX_THRESHOLD_F32, IDX_TOPK_F32 = 0, 1, 2
 
 STATUS_NAMES = {0: "BSA_OK", 1: "BSA_ERR_INVALID_ARG", 2: "BSA_ERR_UNSUPPORTED",
                 3: "BSA_ERR_OVERFLOW", 4: "BSA_ERR_CUDA", 5: "BSA_ERR_TIMEOUT",
-                6: "BSA_ERR_BOUNDS"}
+                6: "BSA_ERR_BOUNDS", 7: "BSA_ERR_NONFINITE"}
 
 EXPORTS = ("bsa_build_index", "bsa_build_crm", "bsa_forward_crm", "bsa_upscale_threshold",
            "bsa_block_scores", "bsa_block_scores_workspace_size",
@@ -28,6 +28,8 @@ EXPORTS = ("bsa_build_index", "bsa_build_crm", "bsa_forward_crm", "bsa_upscale_t
            "bsa_forward_scatter",
            "bsa_paged_append", "bsa_forward_paged", "bsa_forward_paged_workspace_size",
            "bsa_select_paged", "bsa_select_paged_workspace_size",
+           "bsa_paged_append_fp4", "bsa_paged_read_fp4", "bsa_forward_paged_fp4",
+           "bsa_forward_paged_fp4_workspace_size",
            "bsa_device_status", "bsa_resident_ctas", "bsa_status_string", "bsa_selftest_exp2",
            "bsa_selftest_wait_timeout", "bsa_selftest_paged_wait")
 
@@ -106,6 +108,16 @@ def load_library():
     lib.bsa_select_paged.restype = i32
     lib.bsa_select_paged_workspace_size.argtypes = [P, i32, i32, i32]
     lib.bsa_select_paged_workspace_size.restype = sz
+    lib.bsa_paged_append_fp4.argtypes = [P, P, i64, P, i64, P, i64, i32, i32, i32, P, i32, i32, i32, P, P, f32,
+                                         P, i64, P, P, P]
+    lib.bsa_paged_append_fp4.restype = i32
+    lib.bsa_paged_read_fp4.argtypes = [P, i32, i32, P, P, i64, P, i64, P]
+    lib.bsa_paged_read_fp4.restype = i32
+    lib.bsa_forward_paged_fp4.argtypes = [P, P, i64, P, i32, i32, i32, i32, i32, i32, P, P, i32, f32, i32, P, sz,
+                                          P, P, P]
+    lib.bsa_forward_paged_fp4.restype = i32
+    lib.bsa_forward_paged_fp4_workspace_size.argtypes = [P, i32, i32, i32, i32]
+    lib.bsa_forward_paged_fp4_workspace_size.restype = sz
     lib.bsa_set_forward_options.argtypes = [P]
     lib.bsa_set_forward_options.restype = i32
     lib.bsa_reorder_guard.argtypes = [P, P]
@@ -739,16 +751,10 @@ def _raw_stream(stream, device_index):
     return _torch._C._cuda_getCurrentRawStream(device_index) if stream is None else stream.cuda_stream
 
 
-def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None, q_out=None, rope=None,
-                 interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, k_mean=None,
-                 stream=None):
-    """Write the new tokens' keys and values [tokens, H_kv, D] into the pages
-    [pages, H_kv, page_size, D] of the cache, keys (and q [tokens, H, D], into
-    q_out) normalised by q_norm / k_norm [D] and rotated by rope [positions,
-    rot] (cosines, then sines) on the way; k_mean [pages, H_kv, D] receives the
-    mean key of every 128-token block that fills up (see bsa.h)."""
-    bf16 = (_torch or _load_torch()).bfloat16
-    kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+def _append_args(k, v, n_pages, H_kv, page_size, D, page_table, q_start, kv_len, q, q_out, rope, interleaved, q_norm,
+                 k_norm, eps, k_mean):
+    """What both appends pass on: (arguments from q to eps, q_out and its stride, address of k_mean, batch)."""
+    bf16 = _torch.bfloat16
     if len(k.shape) != 3:
         raise ValueError(f"k: shape {tuple(k.shape)}, expected [tokens, H_kv, D]")
     tokens = k.shape[0]
@@ -773,10 +779,24 @@ def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None,
     kn = _array(k_norm, "k_norm", bf16, D) if k_norm is not None else None
     km = _array(k_mean, "k_mean", bf16, n_pages * H_kv * D) if k_mean is not None else None
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    return ((qp, qs, kp, ks, vp, vs, H, H_kv, D, rp, rope_len, rot, 1 if interleaved else 0, qn, kn, eps), (op, os_), km, b)
+
+
+def paged_append(k, v, k_cache, v_cache, page_table, q_start, kv_len, *, q=None, q_out=None, rope=None,
+                 interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, k_mean=None,
+                 stream=None):
+    """Write the new tokens' keys and values [tokens, H_kv, D] into the pages
+    [pages, H_kv, page_size, D] of the cache, keys (and q [tokens, H, D], into
+    q_out) normalised by q_norm / k_norm [D] and rotated by rope [positions,
+    rot] (cosines, then sines) on the way; k_mean [pages, H_kv, D] receives the
+    mean key of every 128-token block that fills up (see bsa.h)."""
+    if _torch is None:
+        _load_torch()
+    kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
+    front, q_to, km, b = _append_args(k, v, n_pages, H_kv, page_size, D, page_table, q_start, kv_len, q, q_out, rope,
+                                      interleaved, q_norm, k_norm, eps, k_mean)
     dev = _where(k_cache, v_cache, k, v, page_table, q_start, kv_len, q, q_out, rope, q_norm, k_norm, k_mean)
-    code = (_lib or load_library()).bsa_paged_append(
-        ctypes.byref(b), qp, qs, kp, ks, vp, vs, H, H_kv, D, rp, rope_len, rot, 1 if interleaved else 0, qn, kn, eps,
-        op, os_, kc, vc, km, _raw_stream(stream, dev))
+    code = (_lib or load_library()).bsa_paged_append(ctypes.byref(b), *front, *q_to, kc, vc, km, _raw_stream(stream, dev))
     if code:
         _check("bsa_paged_append", code)
 
@@ -788,6 +808,24 @@ def forward_paged_workspace_size(seqs: int, tokens: int, max_pages: int, page_si
     return int(load_library().bsa_forward_paged_workspace_size(ctypes.byref(b), H, H_kv, D, sel_width))
 
 
+def _attention_args(call, q, o, lse, sel, sel_cnt, H_kv, D):
+    """(tokens, H, q's address and stride, o's, lse's, sel's and sel_cnt's addresses, width)."""
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
+    tokens, H, _ = q.shape
+    qp, qs = _token_rows(q, "q", tokens, H, D)
+    if o.shape != q.shape:
+        raise ValueError("o must have q's shape [tokens, H, D]")
+    op, lp = _array(o, "o", _torch.bfloat16, 0), _array(lse, "lse", _torch.float32, tokens * H)
+    sp = cp = None
+    width = 0
+    if sel is not None or sel_cnt is not None:
+        if sel is None or sel_cnt is None:
+            raise ValueError(f"{call}: sel and sel_cnt go together")
+        sp, cp, width = _block_lists(sel, sel_cnt, tokens, H_kv)
+    return tokens, H, qp, qs, op, lp, sp, cp, width
+
+
 def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, causal: bool = True,
                   window: int = 0, sinks: int = 0, sel=None, sel_cnt=None, scale: float = 0.0,
                   workspace=None, stream=None):
@@ -796,23 +834,12 @@ def forward_paged(q, k_cache, v_cache, page_table, q_start, kv_len, o, lse, *, c
     width] / sel_cnt [tokens, H_kv] restrict each token to its listed 128-token
     blocks (see bsa.h).  ``workspace`` is a CUDA tensor of at least
     forward_paged_workspace_size() bytes (allocated here when omitted)."""
-    torch = _torch or _load_torch()
+    if _torch is None:
+        _load_torch()
     if (window | sinks) >> 31:
         _fits(window=window, sinks=sinks)
     kc, vc, n_pages, H_kv, page_size, D = _paged_cache(k_cache, v_cache)
-    if q.dim() != 3:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [tokens, H, D]")
-    tokens, H, _ = q.shape
-    qp, qs = _token_rows(q, "q", tokens, H, D)
-    if o.shape != q.shape:
-        raise ValueError("o must have q's shape [tokens, H, D]")
-    op, lp = _array(o, "o", torch.bfloat16, 0), _array(lse, "lse", torch.float32, tokens * H)
-    sp = cp = None
-    width = 0
-    if sel is not None or sel_cnt is not None:
-        if sel is None or sel_cnt is None:
-            raise ValueError("forward_paged: sel and sel_cnt go together")
-        sp, cp, width = _block_lists(sel, sel_cnt, tokens, H_kv)
+    tokens, H, qp, qs, op, lp, sp, cp, width = _attention_args("forward_paged", q, o, lse, sel, sel_cnt, H_kv, D)
     b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
     dev = _where(k_cache, v_cache, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, workspace)
     lib = _lib or load_library()
@@ -858,6 +885,108 @@ def select_paged(q, k_mean, page_table, q_start, kv_len, sel, sel_cnt, *, page_s
                                 _raw_stream(stream, dev))
     if code:
         _check("bsa_select_paged", code)
+
+
+class Fp4Cache(ctypes.Structure):
+    """The pages of a cache in 4 bits (see bsa.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_gain", ctypes.c_void_p), ("v_gain", ctypes.c_void_p)]
+
+
+def _fp4_cache(k_cache, k_scale, v_cache, v_scale, k_gain, v_gain):
+    """(cache, pages, H_kv, page_size, D)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must share the shape [pages, H_kv, page_size, D / 2]")
+    n_pages, H_kv, page_size, half = shape
+    D = 2 * half
+    want = (n_pages, H_kv, page_size, D // 16)
+    if k_scale.shape != want or v_scale.shape != want:
+        raise ValueError(f"k_scale and v_scale must have the shape [pages, H_kv, page_size, D / 16], here {want}")
+    u8, e4m3, f32 = _torch.uint8, _torch.float8_e4m3fn, _torch.float32
+    c = Fp4Cache(_array(k_cache, "k_cache", u8, 0), _array(k_scale, "k_scale", e4m3, 0), _array(v_cache, "v_cache", u8, 0),
+                 _array(v_scale, "v_scale", e4m3, 0), _array(k_gain, "k_gain", f32, H_kv) if k_gain is not None else None,
+                 _array(v_gain, "v_gain", f32, H_kv) if v_gain is not None else None)
+    return c, n_pages, H_kv, page_size, D
+
+
+def paged_append_fp4(k, v, k_cache, k_scale, v_cache, v_scale, page_table, q_start, kv_len, *, q=None, q_out=None,
+                     rope=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, k_mean=None,
+                     k_gain=None, v_gain=None, stream=None):
+    """paged_append() into a cache in 4 bits: codes uint8 [pages, H_kv,
+    page_size, D / 2], scales float8_e4m3fn [pages, H_kv, page_size, D / 16],
+    gains fp32 [H_kv] (see bsa.h).  k and v stay bf16 [tokens, H_kv, D], and so
+    does k_mean, which select_paged() reads."""
+    if _torch is None:
+        _load_torch()
+    c, n_pages, H_kv, page_size, D = _fp4_cache(k_cache, k_scale, v_cache, v_scale, k_gain, v_gain)
+    front, q_to, km, b = _append_args(k, v, n_pages, H_kv, page_size, D, page_table, q_start, kv_len, q, q_out, rope,
+                                      interleaved, q_norm, k_norm, eps, k_mean)
+    dev = _where(k_cache, k_scale, v_cache, v_scale, k, v, page_table, q_start, kv_len, q, q_out, rope, q_norm, k_norm,
+                 k_mean, k_gain, v_gain)
+    code = (_lib or load_library()).bsa_paged_append_fp4(ctypes.byref(b), *front, *q_to, ctypes.byref(c), km,
+                                                         _raw_stream(stream, dev))
+    if code:
+        _check("bsa_paged_append_fp4", code)
+
+
+def paged_read_fp4(k_cache, k_scale, v_cache, v_scale, page_table, q_start, kv_len, k_out=None, v_out=None, *,
+                   k_gain=None, v_gain=None, stream=None):
+    """Read tokens out of a cache in 4 bits into k_out and v_out [tokens, H_kv,
+    D] bf16 (either may be None): of sequence s the last q_start[s + 1] -
+    q_start[s] of its kv_len[s] tokens, to the packed tokens from q_start[s] on
+    (see bsa.h)."""
+    if _torch is None:
+        _load_torch()
+    c, n_pages, H_kv, page_size, D = _fp4_cache(k_cache, k_scale, v_cache, v_scale, k_gain, v_gain)
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        raise ValueError("paged_read_fp4: pass k_out, v_out or both")
+    if out.dim() != 3:
+        raise ValueError(f"k_out, v_out: shape {tuple(out.shape)}, expected [tokens, H_kv, D]")
+    tokens = out.shape[0]
+    kp, ks = _token_rows(k_out, "k_out", tokens, H_kv, D) if k_out is not None else (None, 0)
+    vp, vs = _token_rows(v_out, "v_out", tokens, H_kv, D) if v_out is not None else (None, 0)
+    b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    dev = _where(k_cache, k_scale, v_cache, v_scale, page_table, q_start, kv_len, k_out, v_out, k_gain, v_gain)
+    code = (_lib or load_library()).bsa_paged_read_fp4(ctypes.byref(b), H_kv, D, ctypes.byref(c), kp, ks, vp, vs,
+                                                       _raw_stream(stream, dev))
+    if code:
+        _check("bsa_paged_read_fp4", code)
+
+
+def forward_paged_fp4_workspace_size(seqs: int, tokens: int, max_pages: int, page_size: int, H: int, H_kv: int,
+                                     D: int, sel_width: int = 0) -> int:
+    _fits(seqs=seqs, tokens=tokens, max_pages=max_pages, page_size=page_size, H=H, H_kv=H_kv, D=D, sel_width=sel_width)
+    b = PagedBatch(None, None, None, seqs, tokens, max_pages, page_size, 1)
+    return int(load_library().bsa_forward_paged_fp4_workspace_size(ctypes.byref(b), H, H_kv, D, sel_width))
+
+
+def forward_paged_fp4(q, k_cache, k_scale, v_cache, v_scale, page_table, q_start, kv_len, o, lse, *, causal: bool = True,
+                      window: int = 0, sinks: int = 0, sel=None, sel_cnt=None, k_gain=None, v_gain=None,
+                      scale: float = 0.0, max_new: int = 0, workspace=None, stream=None):
+    """forward_paged() over a cache in 4 bits, as paged_append_fp4() writes it.
+    max_new: the most new tokens that any of the sequences has, where the caller
+    knows it (1 for a step of single tokens); it changes the time, not the result.
+    ``workspace`` is a CUDA tensor of at least forward_paged_fp4_workspace_size()
+    bytes (allocated here when omitted)."""
+    if _torch is None:
+        _load_torch()
+    if (window | sinks | max_new) >> 31:
+        _fits(window=window, sinks=sinks, max_new=max_new)
+    c, n_pages, H_kv, page_size, D = _fp4_cache(k_cache, k_scale, v_cache, v_scale, k_gain, v_gain)
+    tokens, H, qp, qs, op, lp, sp, cp, width = _attention_args("forward_paged_fp4", q, o, lse, sel, sel_cnt, H_kv, D)
+    b = _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages)
+    dev = _where(k_cache, k_scale, v_cache, v_scale, q, page_table, q_start, kv_len, o, lse, sel, sel_cnt, k_gain, v_gain,
+                 workspace)
+    lib = _lib or load_library()
+    ref = ctypes.byref(b)
+    keep, ws, nbytes = _scratch(lib.bsa_forward_paged_fp4_workspace_size(ref, H, H_kv, D, width), workspace, q.device,
+                                stream)
+    code = lib.bsa_forward_paged_fp4(ref, qp, qs, ctypes.byref(c), H, H_kv, D, 1 if causal else 0, window, sinks, sp, cp,
+                                     width, scale, max_new, ws, nbytes, op, lp, _raw_stream(stream, dev))
+    if code:
+        _check("bsa_forward_paged_fp4", code)
 
 
 def device_status(stream=None) -> int:
@@ -919,7 +1048,8 @@ __all__ = ["BLOCK", "BsaError", "IDX_MASK_U8", "IDX_THRESHOLD_F32", "IDX_TOPK_F3
            "block_scores", "SCORE_MEAN_DOT", "SCORE_CENTROID_EXP", "build_crm", "forward_crm",
            "upscale_threshold", "gather_rows", "forward_masked", "forward_packed", "forward_gather0", "forward_scatter", "gather0_sizes",
            "gather0_layout", "paged_append", "forward_paged", "forward_paged_workspace_size", "select_paged",
-           "select_paged_workspace_size",
+           "select_paged_workspace_size", "paged_append_fp4", "paged_read_fp4", "forward_paged_fp4",
+           "forward_paged_fp4_workspace_size",
            "spectral_order", "spectral_order_workspace_size", "spectral_order_noalloc",
            "NOALLOC_SCRATCH_BYTES", "reorder_guard", "set_forward_options",
            "selftest_exp2", "selftest_wait_timeout", "selftest_paged_wait", "PAGED_WAIT_NOTHING", "PAGED_WAIT_BUSY",

@@ -54,6 +54,7 @@ const char* bsa_status_string(int32_t s) {
         case BSA_ERR_CUDA: return "BSA_ERR_CUDA";
         case BSA_ERR_TIMEOUT: return "BSA_ERR_TIMEOUT";
         case BSA_ERR_BOUNDS: return "BSA_ERR_BOUNDS";
+        case BSA_ERR_NONFINITE: return "BSA_ERR_NONFINITE";
         default: return "BSA_ERR_UNKNOWN";
     }
 }
@@ -531,12 +532,13 @@ bsa::PagedSelectArgs paged_select_args(const bsa_paged_batch* b, int32_t H, int3
 
 }  // namespace
 
-bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k,
-                            int64_t k_stride, const void* v, int64_t v_stride, int32_t H, int32_t H_kv,
-                            int32_t D, const float* rope, int32_t rope_len, int32_t rot,
-                            int32_t interleaved, const void* q_norm, const void* k_norm, float eps,
-                            void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
-                            void* k_mean, void* stream) {
+namespace {
+
+// What both appends check and pass on; the cache's pointers are set by the caller.
+bsa_status append_args(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, int32_t H, int32_t H_kv, int32_t D, const float* rope,
+                       int32_t rope_len, int32_t rot, int32_t interleaved, const void* q_norm, const void* k_norm,
+                       float eps, void* q_out, int64_t q_out_stride, void* k_mean, bsa::PagedAppendArgs& a) {
     const bsa_status c = paged_sizes(b, H, H_kv, D);
     if (c != BSA_OK) return c;
     if (rope && (rope_len < 1 || rot < 16 || rot > D || rot % 16 != 0 || !aligned(rope, 16))) return BSA_ERR_INVALID_ARG;
@@ -548,11 +550,7 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
         return BSA_ERR_INVALID_ARG;
     if (q && (!token_rows(q, q_stride, H, D) || !token_rows(q_out, q_out_stride, H, D))) return BSA_ERR_INVALID_ARG;
     if (q && q == q_out && q_stride != q_out_stride) return BSA_ERR_INVALID_ARG;
-    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16) || (k_mean && !aligned(k_mean, 16)))
-        return BSA_ERR_INVALID_ARG;
-    int32_t* status = bsa::status_word_ptr();
-    if (!status) return BSA_ERR_CUDA;
-    bsa::PagedAppendArgs a{};
+    if (k_mean && !aligned(k_mean, 16)) return BSA_ERR_INVALID_ARG;
     a.q = q;
     a.k = k;
     a.v = v;
@@ -561,8 +559,6 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
     a.v_stride = v_stride;
     a.qo_stride = q_out_stride;
     a.q_out = q_out;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
     a.k_mean = k_mean;
     a.n_pages = b->n_pages;
     a.page = b->page_size;
@@ -582,7 +578,96 @@ bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_s
     a.q_norm = q ? q_norm : nullptr;
     a.k_norm = k_norm;
     a.eps = eps;
+    return BSA_OK;
+}
+
+bool fp4_side(const void* codes, const void* scales) {
+    return codes && scales && aligned(codes, 16) && aligned(scales, 16);
+}
+bool fp4_cache_ok(const bsa_fp4_cache* c) {
+    return c && fp4_side(c->k, c->k_scale) && fp4_side(c->v, c->v_scale) && (!c->k_gain || aligned(c->k_gain, 4)) &&
+           (!c->v_gain || aligned(c->v_gain, 4));
+}
+
+}  // namespace
+
+bsa_status bsa_paged_append(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, int32_t H, int32_t H_kv,
+                            int32_t D, const float* rope, int32_t rope_len, int32_t rot,
+                            int32_t interleaved, const void* q_norm, const void* k_norm, float eps,
+                            void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                            void* k_mean, void* stream) {
+    bsa::PagedAppendArgs a{};
+    const bsa_status c = append_args(b, q, q_stride, k, k_stride, v, v_stride, H, H_kv, D, rope, rope_len, rot, interleaved,
+                                     q_norm, k_norm, eps, q_out, q_out_stride, k_mean, a);
+    if (c != BSA_OK) return c;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
     return bsa::launch_paged_append(a, status, static_cast<cudaStream_t>(stream));
+}
+
+bsa_status bsa_paged_append_fp4(const bsa_paged_batch* b, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, int32_t H,
+                                int32_t H_kv, int32_t D, const float* rope, int32_t rope_len,
+                                int32_t rot, int32_t interleaved, const void* q_norm,
+                                const void* k_norm, float eps, void* q_out, int64_t q_out_stride,
+                                const bsa_fp4_cache* cache, void* k_mean, void* stream) {
+    bsa::PagedAppendArgs a{};
+    const bsa_status c = append_args(b, q, q_stride, k, k_stride, v, v_stride, H, H_kv, D, rope, rope_len, rot, interleaved,
+                                     q_norm, k_norm, eps, q_out, q_out_stride, k_mean, a);
+    if (c != BSA_OK) return c;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!fp4_cache_ok(cache)) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    a.k_cache = cache->k;
+    a.v_cache = cache->v;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.k_gain = cache->k_gain;
+    a.v_gain = cache->v_gain;
+    return bsa::launch_paged_append(a, status, static_cast<cudaStream_t>(stream));
+}
+
+bsa_status bsa_paged_read_fp4(const bsa_paged_batch* b, int32_t H_kv, int32_t D,
+                              const bsa_fp4_cache* cache, void* k_out, int64_t k_out_stride,
+                              void* v_out, int64_t v_out_stride, void* stream) {
+    const bsa_status c = paged_sizes(b, H_kv, H_kv, D);
+    if (c != BSA_OK) return c;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!paged_arrays(b) || !cache || (!k_out && !v_out)) return BSA_ERR_INVALID_ARG;
+    if (k_out && (!token_rows(k_out, k_out_stride, H_kv, D) || !fp4_side(cache->k, cache->k_scale) || !aligned(cache->k_gain, 4)))
+        return BSA_ERR_INVALID_ARG;
+    if (v_out && (!token_rows(v_out, v_out_stride, H_kv, D) || !fp4_side(cache->v, cache->v_scale) || !aligned(cache->v_gain, 4)))
+        return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    bsa::PagedReadArgs a{};
+    a.k = cache->k;
+    a.k_scale = cache->k_scale;
+    a.v = cache->v;
+    a.v_scale = cache->v_scale;
+    a.k_gain = cache->k_gain;
+    a.v_gain = cache->v_gain;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_stride = k_out_stride;
+    a.v_stride = v_out_stride;
+    a.n_pages = b->n_pages;
+    a.page = b->page_size;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.table = b->page_table;
+    a.q_start = b->q_start;
+    a.kv_len = b->kv_len;
+    a.seqs = b->seqs;
+    a.tokens = b->tokens;
+    a.max_pages = b->max_pages;
+    return bsa::launch_paged_read(a, status, static_cast<cudaStream_t>(stream));
 }
 
 size_t bsa_forward_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
@@ -591,12 +676,13 @@ size_t bsa_forward_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int
     return bsa::paged_forward_workspace(paged_forward_args(b, H, H_kv, D, sel_width));
 }
 
-bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_stride,
-                             const void* k_cache, const void* v_cache, int32_t H, int32_t H_kv,
-                             int32_t D, int32_t causal, int32_t window, int32_t sinks,
-                             const int32_t* sel, const int32_t* sel_cnt, int32_t sel_width,
-                             float scale, void* workspace, size_t workspace_bytes, void* o,
-                             float* lse, void* stream) {
+namespace {
+
+// What both forwards check and pass on; the cache's and the workspace's pointers are the caller's.
+bsa_status forward_args(const bsa_paged_batch* b, const void* q, int64_t q_stride, int32_t H, int32_t H_kv, int32_t D,
+                        int32_t causal, int32_t window, int32_t sinks, const int32_t* sel, const int32_t* sel_cnt,
+                        int32_t sel_width, float scale, const void* workspace, void* o, float* lse,
+                        bsa::PagedForwardArgs& a) {
     const bsa_status c = paged_sizes(b, H, H_kv, D);
     if (c != BSA_OK) return c;
     if ((causal != 0 && causal != 1) || window < 0 || sinks < 0 || !scale_ok(scale)) return BSA_ERR_INVALID_ARG;
@@ -604,17 +690,11 @@ bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_
         return BSA_ERR_INVALID_ARG;
     if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
     if (!paged_arrays(b) || !token_rows(q, q_stride, H, D)) return BSA_ERR_INVALID_ARG;
-    if (!k_cache || !v_cache || !o || !lse || !workspace) return BSA_ERR_INVALID_ARG;
-    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
-        return BSA_ERR_INVALID_ARG;
-    bsa::PagedForwardArgs a = paged_forward_args(b, H, H_kv, D, sel_width);
-    if (workspace_bytes < bsa::paged_forward_workspace(a)) return BSA_ERR_INVALID_ARG;
-    int32_t* status = bsa::status_word_ptr();
-    if (!status) return BSA_ERR_CUDA;
+    if (!o || !lse || !workspace) return BSA_ERR_INVALID_ARG;
+    if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return BSA_ERR_INVALID_ARG;
+    a = paged_forward_args(b, H, H_kv, D, sel_width);
     a.q = q;
     a.q_stride = q_stride;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
     a.causal = causal;
     a.window = window;
     a.sinks = sinks;
@@ -623,7 +703,67 @@ bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_
     a.scale = scale;
     a.o = o;
     a.lse = lse;
+    return BSA_OK;
+}
+
+// Sizes of the forward over a cache in 4 bits: with lists, one for each token.
+bool fp4_lists_fit(const bsa_paged_batch* b, int32_t H_kv, int32_t sel_width) {
+    return sel_width == 0 || ((int64_t)b->tokens + b->seqs) * H_kv < ((int64_t)1 << 31);
+}
+
+}  // namespace
+
+bsa_status bsa_forward_paged(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                             const void* k_cache, const void* v_cache, int32_t H, int32_t H_kv,
+                             int32_t D, int32_t causal, int32_t window, int32_t sinks,
+                             const int32_t* sel, const int32_t* sel_cnt, int32_t sel_width,
+                             float scale, void* workspace, size_t workspace_bytes, void* o,
+                             float* lse, void* stream) {
+    bsa::PagedForwardArgs a{};
+    const bsa_status c = forward_args(b, q, q_stride, H, H_kv, D, causal, window, sinks, sel, sel_cnt, sel_width, scale,
+                                      workspace, o, lse, a);
+    if (c != BSA_OK) return c;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return BSA_ERR_INVALID_ARG;
+    if (workspace_bytes < bsa::paged_forward_workspace(a)) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
     return bsa::launch_paged_forward(a, workspace, status, static_cast<cudaStream_t>(stream));
+}
+
+size_t bsa_forward_paged_fp4_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D,
+                                            int32_t sel_width) {
+    if (paged_sizes(b, H, H_kv, D) != BSA_OK || sel_width < 0 || sel_width > (1 << 20) || !fp4_lists_fit(b, H_kv, sel_width))
+        return 0;
+    return bsa::fp4_forward_workspace(paged_forward_args(b, H, H_kv, D, sel_width));
+}
+
+bsa_status bsa_forward_paged_fp4(const bsa_paged_batch* b, const void* q, int64_t q_stride,
+                                 const bsa_fp4_cache* cache, int32_t H, int32_t H_kv, int32_t D,
+                                 int32_t causal, int32_t window, int32_t sinks, const int32_t* sel,
+                                 const int32_t* sel_cnt, int32_t sel_width, float scale,
+                                 int32_t max_new, void* workspace, size_t workspace_bytes, void* o,
+                                 float* lse, void* stream) {
+    bsa::Fp4ForwardArgs x{};
+    const bsa_status c = forward_args(b, q, q_stride, H, H_kv, D, causal, window, sinks, sel, sel_cnt, sel_width, scale,
+                                      workspace, o, lse, x.f);
+    if (c != BSA_OK) return c;
+    if (max_new < 0 || !fp4_lists_fit(b, H_kv, sel_width)) return BSA_ERR_INVALID_ARG;
+    if (b->seqs == 0 || b->tokens == 0) return BSA_OK;
+    if (!fp4_cache_ok(cache)) return BSA_ERR_INVALID_ARG;
+    if (workspace_bytes < bsa::fp4_forward_workspace(x.f)) return BSA_ERR_INVALID_ARG;
+    int32_t* status = bsa::status_word_ptr();
+    if (!status) return BSA_ERR_CUDA;
+    x.f.k_cache = cache->k;
+    x.f.v_cache = cache->v;
+    x.k_scale = cache->k_scale;
+    x.v_scale = cache->v_scale;
+    x.k_gain = cache->k_gain;
+    x.v_gain = cache->v_gain;
+    x.max_new = max_new;
+    return bsa::launch_fp4_forward(x, workspace, status, static_cast<cudaStream_t>(stream));
 }
 
 size_t bsa_select_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int32_t H_kv, int32_t D) {

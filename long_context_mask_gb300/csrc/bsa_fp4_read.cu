@@ -1,0 +1,131 @@
+// Reading a key/value cache held in 4 bits back: the last new tokens of every
+// sequence of a ragged batch, out of their pages, as bf16 rows [tokens, H_kv, D].
+//
+// A value is level * scale, exact in fp32, times the head's gain, rounded once.
+// The work is bound by its bytes (nine read for every 32 written).  A thread block takes up to
+// 64 tokens' keys or values; a thread has one place of a token's H_kv D values, eight of
+// them, and goes through the tokens, four loads under way at a time, so that the
+// block's threads write whole tokens one after another.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bsa_fp4.cuh"
+#include "bsa_internal.h"
+#include "bsa_paged.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kReadThreads = 256;
+constexpr int kReadTokens = 64;
+
+struct ReadParams {
+    PagedBatch b;
+    const uint8_t *codes[2], *scales[2];  // keys, values
+    const float* gain[2];
+    __nv_bfloat16* out[2];
+    int64_t stride[2];
+    int32_t H_kv;
+    int32_t first;  // blockIdx.y 0 is this one of the two
+};
+
+template <int D>
+__global__ void __launch_bounds__(kReadThreads) k_paged_read(const __grid_constant__ ReadParams P) {
+    __shared__ int64_t part[33];
+    __shared__ int32_t hit[5];
+    __shared__ int32_t slot[kReadTokens];  // row of head 0 of each token (-1: none)
+    ptx::launch_dependents();
+    ptx::wait_primary();
+    int32_t chunk;
+    PagedSeq q;
+    const int32_t s = find_unit<kReadThreads>(
+        P.b, blockIdx.x, [](const PagedSeq& q) -> int64_t { return (q.nq + kReadTokens - 1) / kReadTokens; }, part, hit, chunk, q);
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int32_t i = threadIdx.x; i < P.b.seqs; i += kReadThreads) {
+            PagedSeq x;
+            // more tokens than the sequence has: those before position 0 are left out
+            if (!paged_seq(P.b, i, x) || x.nq > x.kl) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
+        }
+    }
+    if (s < 0) return;
+    const int32_t t0 = chunk * kReadTokens, n = min(kReadTokens, q.nq - t0);
+    const int32_t page = P.b.page;
+    if (threadIdx.x < n) {
+        const int32_t pos = q.kl - q.nq + t0 + threadIdx.x;
+        int32_t at = -1;
+        if (pos >= 0) {
+            const int32_t id = P.b.table[(int64_t)s * P.b.max_pages + pos / page];
+            if (id >= 0 && id < P.b.n_pages) at = id * P.H_kv * page + pos % page;
+            else atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
+        }
+        slot[threadIdx.x] = at;
+    }
+    __syncthreads();
+    const int which = P.first + blockIdx.y;
+    const uint8_t* codes = which ? P.codes[1] : P.codes[0];
+    const uint8_t* scales = which ? P.scales[1] : P.scales[0];
+    const float* gain = which ? P.gain[1] : P.gain[0];
+    __nv_bfloat16* out = which ? P.out[1] : P.out[0];
+    const int64_t stride = which ? P.stride[1] : P.stride[0];
+    const int32_t places = P.H_kv * (D / 8), wide = min(places, kReadThreads);
+    const int32_t abreast = kReadThreads / wide, sub = threadIdx.x / wide;
+    if (sub >= abreast) return;
+    for (int32_t x = threadIdx.x - sub * wide; x < places; x += wide) {
+        const int32_t head = x / (D / 8), c = x % (D / 8);
+        const float g = gain != nullptr ? gain[head] : 1.0f;
+        for (int32_t t = sub; t < n; t += 4 * abreast) {
+            uint32_t w[4], y[4];
+            int32_t at[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int32_t tu = t + u * abreast;
+                at[u] = tu < n ? slot[tu] : -1;
+                const int64_t row = (int64_t)max(at[u], 0) + head * page;
+                w[u] = at[u] >= 0 ? *reinterpret_cast<const uint32_t*>(codes + row * (D / 2) + 4 * c) : 0u;
+                y[u] = at[u] >= 0 ? scales[row * (D / kFp4Group) + (c >> 1)] : 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (at[u] < 0) continue;
+                __half2 h[4];
+                fp4_levels(w[u], h);
+                const __half2 sc = __half2half2(__low2half(fp4_scales(y[u])));
+                __nv_bfloat162 r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __half22float2(__hmul2(h[i], sc));
+                    r[i] = __floats2bfloat162_rn(f.x * g, f.y * g);
+                }
+                __nv_bfloat16* to = out + ((int64_t)q.q0 + t0 + t + u * abreast) * stride + head * D + 8 * c;
+                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(r);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+bsa_status launch_paged_read(const PagedReadArgs& a, int32_t* status, cudaStream_t stream) {
+    ReadParams P{};
+    P.b = PagedBatch{a.q_start, a.kv_len, a.table, a.seqs, a.tokens, a.max_pages, a.page, a.n_pages, status};
+    P.codes[0] = static_cast<const uint8_t*>(a.k);
+    P.codes[1] = static_cast<const uint8_t*>(a.v);
+    P.scales[0] = static_cast<const uint8_t*>(a.k_scale);
+    P.scales[1] = static_cast<const uint8_t*>(a.v_scale);
+    P.gain[0] = a.k_gain;
+    P.gain[1] = a.v_gain;
+    P.out[0] = static_cast<__nv_bfloat16*>(a.k_out);
+    P.out[1] = static_cast<__nv_bfloat16*>(a.v_out);
+    P.stride[0] = a.k_stride;
+    P.stride[1] = a.v_stride;
+    P.H_kv = a.H_kv;
+    P.first = a.k_out != nullptr ? 0 : 1;
+    // sum over sequences of ceil(n / kReadTokens) <= tokens / kReadTokens + seqs
+    const dim3 grid((unsigned)(a.tokens / kReadTokens + a.seqs), a.k_out != nullptr && a.v_out != nullptr ? 2u : 1u);
+    const cudaError_t e = a.D == 128 ? launch_chained(k_paged_read<128>, grid, kReadThreads, 0, stream, P)
+                                     : launch_chained(k_paged_read<64>, grid, kReadThreads, 0, stream, P);
+    return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace bsa

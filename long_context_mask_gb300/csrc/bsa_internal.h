@@ -120,9 +120,25 @@ struct PagedAppendArgs {
     int32_t rope_len, rot, interleaved;
     const void *q_norm, *k_norm;
     float eps;
+    // a cache in 4 bits (k_cache and v_cache hold codes): its scales; NULL else
+    void *k_scale = nullptr, *v_scale = nullptr;
+    const float *k_gain = nullptr, *v_gain = nullptr;
 };
 // bsa_paged.cu
 bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaStream_t stream);
+
+// Rows of a cache in 4 bits, as bf16.
+struct PagedReadArgs {
+    const void *k, *k_scale, *v, *v_scale;
+    const float *k_gain, *v_gain;
+    void *k_out, *v_out;          // either may be NULL
+    int64_t k_stride, v_stride;   // elements between tokens
+    int32_t n_pages, page, H_kv, D;
+    const int32_t *table, *q_start, *kv_len;
+    int32_t seqs, tokens, max_pages;
+};
+// bsa_fp4_read.cu
+bsa_status launch_paged_read(const PagedReadArgs& a, int32_t* status, cudaStream_t stream);
 
 struct PagedForwardArgs {
     const void* q;
@@ -145,6 +161,22 @@ constexpr int kPagedRuns = 4 * kPagedBlocks;
 // bsa_paged_attn.cu
 size_t paged_forward_workspace(const PagedForwardArgs& a);
 bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int32_t* status, cudaStream_t stream);
+
+// Tile lists out of tokens' lists (bsa_paged_attn.cu, see k_paged_union): for each
+// tile of tpt tokens and key/value head the listed and visible blocks, ascending, with words
+// words of token bits each.
+bsa_status launch_paged_union(const PagedForwardArgs& a, int32_t tpt, int32_t nt_cap, int32_t cap, int32_t words, int32_t* list,
+                              int32_t* cnt, uint32_t* who, int32_t* status, cudaStream_t stream);
+
+// Attention over a cache in 4 bits (bsa_fp4_attn.cu): k_cache and v_cache hold codes.
+struct Fp4ForwardArgs {
+    PagedForwardArgs f;
+    const void *k_scale, *v_scale;
+    const float *k_gain, *v_gain;
+    int32_t max_new;  // 0: not known
+};
+size_t fp4_forward_workspace(const PagedForwardArgs& a);
+bsa_status launch_fp4_forward(const Fp4ForwardArgs& a, void* workspace, int32_t* status, cudaStream_t stream);
 
 struct PagedSelectArgs {
     const void* q;

@@ -29,6 +29,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "bsa_fp4.cuh"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
 
@@ -51,6 +52,9 @@ struct AppendParams {
     int32_t q_blocks;  // thread blocks (y) of query heads; those of keys and values follow
     int32_t q_parts;   // of a position block's tokens that a thread block of query heads takes one of: 1, 2 or 4
     int32_t page_shift;
+    // a cache in 4 bits: k_cache and v_cache hold codes
+    uint8_t *k_scale, *v_scale;
+    const float *k_gain, *v_gain;
 };
 
 __device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
@@ -124,15 +128,27 @@ __device__ __forceinline__ void load_angles(const AppendParams& P, int c, int32_
     *reinterpret_cast<float4*>(a.si + 4) = *reinterpret_cast<const float4*>(cs + half + at + 4);
 }
 
+// u a - v b and u a + v b; kEach: each product rounded by itself.
+template <bool kEach>
+__device__ __forceinline__ float turn_minus(float u, float a, float v, float b) {
+    if constexpr (kEach) return __fsub_rn(__fmul_rn(u, a), __fmul_rn(v, b));
+    return u * a - v * b;
+}
+template <bool kEach>
+__device__ __forceinline__ float turn_plus(float u, float a, float v, float b) {
+    if constexpr (kEach) return __fadd_rn(__fmul_rn(u, a), __fmul_rn(v, b));
+    return u * a + v * b;
+}
+
 // Rotation of one row.  Every thread of the warp calls it.
-template <bool kHalves>
+template <bool kHalves, bool kEach = false>
 __device__ __forceinline__ void rotate_row(const AppendParams& P, float (&x)[8], int c, const Angles& a) {
     if constexpr (kHalves) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float u = x[i], v = x[4 + i];
-            x[i] = u * a.co[i] - v * a.si[i];
-            x[4 + i] = v * a.co[i] + u * a.si[i];
+            x[i] = turn_minus<kEach>(u, a.co[i], v, a.si[i]);
+            x[4 + i] = turn_plus<kEach>(v, a.co[i], u, a.si[i]);
         }
         return;
     }
@@ -141,8 +157,8 @@ __device__ __forceinline__ void rotate_row(const AppendParams& P, float (&x)[8],
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float u = x[2 * i], v = x[2 * i + 1];
-                x[2 * i] = u * a.co[i] - v * a.si[i];
-                x[2 * i + 1] = v * a.co[i] + u * a.si[i];
+                x[2 * i] = turn_minus<kEach>(u, a.co[i], v, a.si[i]);
+                x[2 * i + 1] = turn_plus<kEach>(v, a.co[i], u, a.si[i]);
             }
         }
         return;
@@ -156,11 +172,118 @@ __device__ __forceinline__ void rotate_row(const AppendParams& P, float (&x)[8],
     for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
     if (turned) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * a.co[i] - y[i] * a.si[i] : x[i] * a.co[i] + y[i] * a.si[i];
+        for (int i = 0; i < 8; ++i)
+            x[i] = first ? turn_minus<kEach>(x[i], a.co[i], y[i], a.si[i]) : turn_plus<kEach>(x[i], a.co[i], y[i], a.si[i]);
     }
 }
 
+// ---------------------------------------------------------------- a cache in 4 bits
+// A value next to the middle between two levels goes one way or the other by its last
+// bit.  So that the codes do not hang on the order of a sum or on a product and a sum
+// being one instruction, keys are worked on in steps that are each rounded by
+// themselves, and the norm's factor is 1 / sqrt(mean(x^2) + eps) rounded once (but for
+// one row in some 10^5).
+
+// a + b = s + the returned error, exactly (Knuth's two-sum).
+__device__ __forceinline__ float two_sum(float a, float b, float& s) {
+    s = __fadd_rn(a, b);
+    const float t = __fsub_rn(s, a);
+    return __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+// RMS norm of one row.  Squares of bf16 numbers are exact in fp32; their sum is held
+// in two words, and one Newton step on the device's reciprocal root takes its error out.
+template <int D>
+__device__ __forceinline__ void norm_row_each(float (&x)[8], const float (&w)[8], float eps) {
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo = __fadd_rn(lo, two_sum(hi, __fmul_rn(x[i], x[i]), hi));
+#pragma unroll
+    for (int d = 1; d < D / 8; d <<= 1) {
+        const float h2 = __shfl_xor_sync(0xffffffffu, hi, d), l2 = __shfl_xor_sync(0xffffffffu, lo, d);
+        const float e = two_sum(fmaxf(hi, h2), fminf(hi, h2), hi);  // (the same in every thread)
+        lo = __fadd_rn(__fadd_rn(lo, l2), e);
+    }
+    float m;
+    const float e = two_sum(hi * (1.0f / D), eps, m);
+    const float rest = __fadd_rn(lo * (1.0f / D), e);
+    const float r0 = rsqrtf(m), t = __fmul_rn(m, r0);
+    float off = fmaf(-t, r0, 1.0f);              // 1 - (m + rest) r0^2
+    off = fmaf(-fmaf(m, r0, -t), r0, off);
+    off = fmaf(-rest * r0, r0, off);
+    const float r = fmaf(0.5f * r0, off, r0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+}
+
+// Quantises and stores this thread's eight values of a row (load_row's places).  Every
+// thread of the warp calls it; row < 0: nothing is stored.  Returns whether a value of a stored
+// row is not finite.
 template <int D, bool kHalves>
+__device__ __forceinline__ bool store_row_fp4(float (&x)[8], const float* gain, uint8_t* codes, uint8_t* scales, int64_t row,
+                                              int c) {
+    if (gain != nullptr) {
+        const float g = *gain;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], g);
+    }
+    bool bad = false;
+    float top[2] = {0.f, 0.f};  // of values 0 .. 3 and 4 .. 7
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bad |= x[i] - x[i] != 0.0f;
+        top[i >> 2] = fmaxf(top[i >> 2], fabsf(x[i]));
+    }
+    if constexpr (kHalves) {  // four threads hold a group, in either half
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
+            top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], d));
+        }
+    } else {                  // two threads
+        top[0] = fmaxf(top[0], top[1]);
+        top[0] = top[1] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 1));
+    }
+    float scale[2];
+    uint32_t byte[2], code[2];
+    byte[0] = fp4_scale_of(top[0], scale[0]);
+    byte[1] = byte[0];
+    scale[1] = scale[0];
+    if constexpr (kHalves) byte[1] = fp4_scale_of(top[1], scale[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        code[h] = fp4_codes4(fp4_ratio(x[4 * h], scale[h]), fp4_ratio(x[4 * h + 1], scale[h]),
+                             fp4_ratio(x[4 * h + 2], scale[h]), fp4_ratio(x[4 * h + 3], scale[h]));
+    if (row < 0) return false;
+    uint8_t* to = codes + row * (D / 2);
+    uint8_t* ts = scales + row * (D / kFp4Group);
+    if constexpr (kHalves) {
+        *reinterpret_cast<uint16_t*>(to + 2 * c) = (uint16_t)code[0];
+        *reinterpret_cast<uint16_t*>(to + D / 4 + 2 * c) = (uint16_t)code[1];
+        if ((c & 3) == 0) {
+            ts[c >> 2] = (uint8_t)byte[0];
+            ts[D / 32 + (c >> 2)] = (uint8_t)byte[1];
+        }
+    } else {
+        *reinterpret_cast<uint32_t*>(to + 4 * c) = code[0] | code[1] << 16;
+        if ((c & 1) == 0) ts[c >> 1] = (uint8_t)byte[0];
+    }
+    return bad;
+}
+// Values 8 c .. 8 c + 7 of a row, without the gain.
+template <int D>
+__device__ __forceinline__ void load_row_fp4(const uint8_t* codes, const uint8_t* scales, int64_t row, int c, float (&x)[8]) {
+    __half2 h[4];
+    fp4_levels(*reinterpret_cast<const uint32_t*>(codes + row * (D / 2) + 4 * c), h);
+    const __half2 s = __half2half2(__low2half(fp4_scales(scales[row * (D / kFp4Group) + (c >> 1)])));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(__hmul2(h[i], s));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <int D, bool kHalves, bool kFp4>
 __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_constant__ AppendParams P) {
     constexpr int kLanes = D / 8;
     constexpr int kRows = kAppendThreads / kLanes;  // rows in flight
@@ -256,9 +379,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
             const int32_t pos = p0 + u * kRows + sub;
             const int64_t tok = (int64_t)q.q0 + (pos - first);
             next[u][0] = pos < hi ? load_row<D, kHalves>(P.k + tok * P.k_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
-            next[u][1] = pos < hi ? load_row<D, kHalves>(P.v + tok * P.v_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
+            next[u][1] = pos < hi ? load_row<D, kHalves && !kFp4>(P.v + tok * P.v_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
         }
     };
+    bool bad = false;  // (kFp4: a value that is not finite)
     if constexpr (kHalves) fetch(lo);
     for (int32_t p0 = lo; p0 < hi; p0 += 2 * kRows) {
         if constexpr (!kHalves) fetch(p0);
@@ -275,9 +399,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
             if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
             float x[8];
             unpack8(raw[u][0], x);
+            const int32_t id = pos < hi ? pages[(pos - base) >> P.page_shift] : -1;
+            if constexpr (kFp4) {
+                if (w != nullptr) norm_row_each<D>(x, wf, P.eps);
+                if (P.rope != nullptr) rotate_row<kHalves, true>(P, x, c, a);
+                const int64_t slot = id >= 0 ? (((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1)) : -1;
+                bad |= store_row_fp4<D, kHalves>(x, P.k_gain ? P.k_gain + h0 : nullptr,
+                                                 reinterpret_cast<uint8_t*>(P.k_cache), P.k_scale, slot, c);
+                unpack8(raw[u][1], x);
+                bad |= store_row_fp4<D, false>(x, P.v_gain ? P.v_gain + h0 : nullptr,
+                                               reinterpret_cast<uint8_t*>(P.v_cache), P.v_scale, slot, c);
+                continue;
+            }
             if (w != nullptr) norm_row<D>(x, wf, P.eps);
             if (P.rope != nullptr) rotate_row<kHalves>(P, x, c, a);
-            const int32_t id = pos < hi ? pages[(pos - base) >> P.page_shift] : -1;
             if (id >= 0) {
                 const int64_t slot = ((((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1))) * D;
                 store_row<D, kHalves>(P.k_cache + slot, c, pack8(x));
@@ -286,6 +421,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
         }
     }
 
+    if (kFp4 && bad) atomicCAS(P.b.status, 0, BSA_ERR_NONFINITE);
     if (P.k_mean == nullptr || hi != base + kBlock) return;  // (the whole thread block agrees)
     // the block is full: the mean of its 128 keys as the cache holds them
     const int32_t last = pages[per - 1];
@@ -296,9 +432,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
     for (int p = sub; p < kBlock; p += kRows) {
-        const __nv_bfloat16* row = P.k_cache + (((int64_t)pages[p / page] * P.H_kv + h0) * page + p % page) * D;
+        const int64_t row = ((int64_t)pages[p / page] * P.H_kv + h0) * page + p % page;
         float f[8];
-        unpack8(*reinterpret_cast<const uint4*>(row + 8 * c), f);
+        if constexpr (kFp4) load_row_fp4<D>(reinterpret_cast<const uint8_t*>(P.k_cache), P.k_scale, row, c, f);
+        else unpack8(*reinterpret_cast<const uint4*>(P.k_cache + row * D + 8 * c), f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += f[j];
     }
@@ -309,6 +446,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
         float t = 0.f;
 #pragma unroll
         for (int g = 0; g < kRows; ++g) t += sums[g][threadIdx.x];
+        if (kFp4 && P.k_gain != nullptr) t *= P.k_gain[h0];
         P.k_mean[((int64_t)last * P.H_kv + h0) * D + threadIdx.x] = __float2bfloat16_rn(t * (1.0f / kBlock));
     }
 }
@@ -349,8 +487,16 @@ bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaSt
     // a sequence's n > 0 new tokens touch at most (n + 126) / 128 + 1 blocks
     const int64_t units = (int64_t)a.tokens / kBlock + 2 * (int64_t)a.seqs;
     const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + a.H_kv));
-    const auto kernel = a.D == 128 ? (halves ? k_paged_append<128, true> : k_paged_append<128, false>)
-                                   : (halves ? k_paged_append<64, true> : k_paged_append<64, false>);
+    const bool fp4 = a.k_scale != nullptr;
+    P.k_scale = static_cast<uint8_t*>(a.k_scale);
+    P.v_scale = static_cast<uint8_t*>(a.v_scale);
+    P.k_gain = a.k_gain;
+    P.v_gain = a.v_gain;
+    const auto kernel =
+        fp4 ? (a.D == 128 ? (halves ? k_paged_append<128, true, true> : k_paged_append<128, false, true>)
+                          : (halves ? k_paged_append<64, true, true> : k_paged_append<64, false, true>))
+            : (a.D == 128 ? (halves ? k_paged_append<128, true, false> : k_paged_append<128, false, false>)
+                          : (halves ? k_paged_append<64, true, false> : k_paged_append<64, false, false>));
     const cudaError_t e = launch_chained(kernel, grid, kAppendThreads, 0, stream, P);
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

@@ -1372,6 +1372,15 @@ bsa_status launch_d(const Params& P, cudaStream_t stream) {
 
 size_t paged_forward_workspace(const PagedForwardArgs& a) { return layout(a).total; }
 
+bsa_status launch_paged_union(const PagedForwardArgs& a, int32_t tpt, int32_t nt_cap, int32_t cap, int32_t words, int32_t* list,
+                              int32_t* cnt, uint32_t* who, int32_t* status, cudaStream_t stream) {
+    const PagedBatch b{a.q_start, a.kv_len, a.table, a.seqs, a.tokens, a.max_pages, a.page, a.n_pages, status};
+    UnionParams U{b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, tpt, a.causal, list, cnt, who, nt_cap, cap, words};
+    return launch_chained(k_paged_union, dim3((unsigned)nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream, U) == cudaSuccess
+               ? BSA_OK
+               : BSA_ERR_CUDA;
+}
+
 bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int32_t* status, cudaStream_t stream) {
     const Layout L = layout(a);
     Params P;
@@ -1421,9 +1430,8 @@ bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int3
         P.list_cnt = cnt;
         P.list = list;
         P.list_who = who;
-        UnionParams U{P.b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, L.tpt, a.causal, list, cnt, who, L.nt_cap, L.cap, L.words};
-        if (launch_chained(k_paged_union, dim3((unsigned)L.nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream, U) != cudaSuccess)
-            return BSA_ERR_CUDA;
+        const bsa_status u = launch_paged_union(a, L.tpt, L.nt_cap, L.cap, L.words, list, cnt, who, status, stream);
+        if (u != BSA_OK) return u;
         return D == 128 ? launch_d<128, kListed>(P, stream) : launch_d<64, kListed>(P, stream);
     }
     if (a.window > 0) return D == 128 ? launch_d<128, kWindow>(P, stream) : launch_d<64, kWindow>(P, stream);
