@@ -37,6 +37,7 @@
 #include "bsa_fp4.cuh"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
+#include "bsa_paged_wait.cuh"
 #include "bsa_rows.cuh"
 
 namespace bsa {
@@ -45,8 +46,10 @@ namespace {
 constexpr int32_t kMaxWindow = 1 << 26;  // (positions lie within 2^24 of zero)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                    // that compute
+constexpr int kTeam = 4;                     // of them to a key tile, 32 keys each
+constexpr int kLoad = kWarps, kStore = kWarps + 1;
+constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kRuns = 2 * kPagedBlocks;
 constexpr int kMaxNT = 2;
 constexpr float kRaise = 10.0f;  // log2 of how far a weight may pass its row's maximum
@@ -126,27 +129,98 @@ struct Tiles {
     }
 };
 
+// Shared memory of a thread block: a ring of key tiles (codes of keys and of values, then their
+// scales), the parts of O that the warps join, query rows, and what the warps tell one another.
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kBlocks = NT == 1 ? 2 : 1;      // of an SM
+    static constexpr int kStages = NT == 1 ? 4 : 8;
+    static constexpr int kCodes = 128 * D / 2, kScales = 128 * D / 16;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kRowO = D + 4;                  // a row of O, padded
+    static constexpr int kJoin = kWarps * 8 * NT * kRowO * 4;
+    static constexpr int kSmem = kRing + kJoin;
+};
+
+// A row tile's part in a run, as the producer tells it.
+struct Segment {
+    int32_t n;              // key tiles (0: no key at all; -1: no more segments)
+    int32_t kvh, q0;        // head; the sequence's first packed token
+    int32_t row0, nrows;    // rows (token of the sequence * group + head)
+    int32_t pos_of0, kl;    // position of the sequence's first new token, keys in the cache
+    int32_t part;           // -1: the whole row tile is here; else its part slot: 2 block + 0 or 1
+};
+constexpr int kDesc = 3;    // descriptors in flight
+
+template <int D, int NT>
+struct Shared {
+    __nv_bfloat16 q[kDesc][8 * NT][D];  // the segments' query rows
+    uint64_t full[Cfg<D, NT>::kStages], empty[Cfg<D, NT>::kStages];
+    uint64_t seg_full[kDesc], seg_empty[kDesc];
+    uint64_t joined, freed;           // the warps' parts are there, have been read
+    Watch watch;
+    Segment seg[kDesc];
+    int32_t key[Cfg<D, NT>::kStages]; // first key of the tile in each slot
+    int64_t prefix[33];
+    int32_t start[4];                 // this run's first unit: kvh, sequence, row tile, tile of the head
+    int32_t start_x0;                 // .. unit within the row tile
+    PagedSeq start_seq;
+    float2 ml[kWarps][8 * NT];
+};
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, const int32_t* status) {
+    return __all_sync(0xffffffffu, paged_wait(bar, parity, w, status));
+}
+
+// a / b; nearly every dividend fits 32 bits, whose division is much shorter.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (a >> 32) == 0 && (b >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 template <int D, int NT, int kMode>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __grid_constant__ Fp4Params P) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(const __grid_constant__ Fp4Params P) {
+    using C = Cfg<D, NT>;
     constexpr bool kLists = kMode == kListed;
+    constexpr uint32_t S = C::kStages;
     constexpr int R = 8 * NT;
     constexpr int kSteps = D / 16;          // products of S^T for 16 keys; of O^T as well
-    constexpr int kKW = D / 32;             // words of a K row that a lane loads
-    constexpr int kVW = D / 64;             // words of a V row that a lane loads
-    constexpr int kRowO = D + 4;            // a row of O in shared memory, padded
+    constexpr int kKW = D / 32;             // words of a K row that a lane takes
+    constexpr int kVW = D / 64;             // words of a V row that a lane takes
+    constexpr int kRowO = C::kRowO;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t prefix[33];
-    __shared__ int32_t start[5];            // this run's first unit: kvh, sequence, row tile, unit within it, tile of the head
-    __shared__ float2 ml[kWarps][R];
+    __shared__ __align__(16) Shared<D, NT> sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = lane >> 2, c = lane & 3;
+    int32_t* const status = P.b.status;
+    if (threadIdx.x == kThreads - 1) {
+        for (uint32_t x = 0; x < S; ++x) {
+            mbar_init(smem_u32(&sh.full[x]), 33);
+            mbar_init(smem_u32(&sh.empty[x]), kTeam);
+        }
+        for (int x = 0; x < kDesc; ++x) {
+            mbar_init(smem_u32(&sh.seg_full[x]), 1);
+            mbar_init(smem_u32(&sh.seg_empty[x]), kWarps + 1);
+        }
+        mbar_init(smem_u32(&sh.joined), kWarps);
+        mbar_init(smem_u32(&sh.freed), 1);
+        fence_mbar_init();
+    }
     launch_dependents();
     wait_primary();
-    if (threadIdx.x == 0) P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == kThreads - 1) {
+        P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+        sh.watch.busy = 0;
+        // a block of this launch (or an unread earlier one) timed out: abandon
+        sh.watch.abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
+    }
 
     // ---------------------------------------------------------------- this block's run
+    // of sequence s: the row tiles of the sequences before it, its new tokens and its
+    // length (the ring is free here)
     const Tiles<kLists> tiles{P.group, R};
-    int32_t* cum = reinterpret_cast<int32_t*>(smem);  // row tiles of the sequences before
+    int32_t* cum = reinterpret_cast<int32_t*>(smem);
+    int32_t* seq_nq = cum + P.b.seqs;
+    int32_t* seq_kl = seq_nq + P.b.seqs;
     int32_t nt;
     {
         const int32_t per = (P.b.seqs + kThreads - 1) / kThreads;
@@ -154,15 +228,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
         int64_t mine = 0, all;
         for (int32_t s = a; s < e; ++s) {
             PagedSeq q;
-            if (!paged_seq(P.b, s, q) && blockIdx.x == 0) raise_status(P.b.status, BSA_ERR_BOUNDS);
-            cum[s] = tiles.count(q.nq);
-            mine += cum[s];
+            if (!paged_seq(P.b, s, q) && blockIdx.x == 0) raise_status(status, BSA_ERR_BOUNDS);
+            seq_nq[s] = q.nq;
+            seq_kl[s] = q.kl;
+            mine += tiles.count(q.nq);
         }
-        int64_t at = block_prefix<kThreads>(mine, prefix, all);
+        int64_t at = block_prefix<kThreads>(mine, sh.prefix, all);
         for (int32_t s = a; s < e; ++s) {
-            const int32_t n = cum[s];
             cum[s] = (int32_t)min(at, (int64_t)INT32_MAX);
-            at += n;
+            at += tiles.count(seq_nq[s]);
         }
         // (beyond this: only with starts that decrease, reported above)
         const int64_t most = kLists ? (int64_t)P.nt_cap * tiles.per_token() : (int64_t)P.b.tokens * P.group / R + P.b.seqs;
@@ -172,25 +246,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
     auto list_of = [&](int32_t kvh, int32_t i) -> int64_t {  // (row tile i of the head)
         return (int64_t)kvh * P.nt_cap + i / tiles.per_token();
     };
-    auto tile_count = [&](int32_t kvh, int32_t i, int32_t t, const PagedSeq& q, int32_t& lo, int32_t& ns) -> int32_t {
+    // key tiles of row tile i of the head, tile t of its sequence of nq new tokens and kl keys
+    auto tile_count = [&](int32_t kvh, int32_t i, int32_t t, int32_t nq, int32_t kl, int32_t& lo, int32_t& ns) -> int32_t {
         if constexpr (kLists) {
             lo = ns = 0;
             return P.list_cnt[list_of(kvh, i)];
         } else {
             int32_t row0, n;
-            tiles.rows(t, q.nq, row0, n);
+            tiles.rows(t, nq, row0, n);
             const int32_t first = row0 / P.group, last = (row0 + n - 1) / P.group;
-            return key_tiles(P, q.kl - q.nq + first, last - first + 1, q.kl, lo, ns);
+            return key_tiles(P, kl - nq + first, last - first + 1, kl, lo, ns);
         }
     };
     const int64_t rows = kLists ? (int64_t)nt * P.H_kv : nt;  // tiles whose counts differ
-    const int64_t per_row = (rows + kThreads - 1) / kThreads;
+    const int64_t per_row = divide(rows + kThreads - 1, kThreads);
     const int64_t f0 = min((int64_t)threadIdx.x * per_row, rows), f1 = min(f0 + per_row, rows);
     // walks this thread's tiles: visit(kvh, i, s, t, units)
     auto walk = [&](auto&& visit) {
         if (f0 >= f1) return;
-        int32_t kvh = kLists ? (int32_t)(f0 / nt) : 0, i = (int32_t)(f0 - (int64_t)kvh * nt), s = 0;
-        PagedSeq q;
+        int32_t kvh = kLists ? (int32_t)divide(f0, nt) : 0, i = (int32_t)(f0 - (int64_t)kvh * nt), s = 0;
         auto find = [&]() {
             int32_t lo = 0, hi = P.b.seqs;  // the last s with cum[s] <= i
             while (hi - lo > 1) {
@@ -199,13 +273,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
                 else hi = mid;
             }
             s = lo;
-            paged_seq(P.b, s, q);
         };
         find();
         for (int64_t f = f0; f < f1; ++f) {
             const int32_t t = i - cum[s];
             int32_t lo, ns;
-            if (visit(kvh, i, s, t, row_units(tile_count(kvh, i, t, q, lo, ns)))) return;
+            if (visit(kvh, i, s, t, row_units(tile_count(kvh, i, t, seq_nq[s], seq_kl[s], lo, ns)))) return;
             ++i;
             if (i == nt) {
                 i = 0;
@@ -217,70 +290,305 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
         }
     };
     int64_t mine = 0, total;
-    walk([&](int32_t, int32_t, int32_t, int32_t, int32_t n) {
+    int4 only = make_int4(0, 0, 0, 0);  // (a thread with one tile need not walk again)
+    walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
         mine += n;
+        only = make_int4(kvh, s, t, i);
         return false;
     });
-    const int64_t before = block_prefix<kThreads>(mine, prefix, total);
+    const int64_t before = block_prefix<kThreads>(mine, sh.prefix, total);
     const int64_t units = kLists ? total : total * P.H_kv;
     const int32_t blocks = (int32_t)min((int64_t)gridDim.x, units);
     if ((int32_t)blockIdx.x >= blocks) return;
-    const int64_t share = units / blocks;  // equal runs, the first `extra` of them one unit longer
+    const int64_t share = divide(units, blocks);  // equal runs, the first `extra` of them one unit longer
     const int32_t extra = (int32_t)(units - share * blocks);
     auto run_start = [&](int32_t x) -> int64_t { return share * x + min(x, extra); };
     {
-        const int64_t u0 = run_start(blockIdx.x), head = kLists ? 0 : u0 / total, x = kLists ? u0 : u0 - head * total;
+        const int64_t u0 = run_start(blockIdx.x), head = kLists ? 0 : divide(u0, total), x = kLists ? u0 : u0 - head * total;
         if (x >= before && x < before + mine) {
-            int64_t at = before;
-            walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
-                if (x < at + n) {
-                    start[0] = kLists ? kvh : (int32_t)head;
-                    start[1] = s;
-                    start[2] = t;
-                    start[3] = (int32_t)(x - at);
-                    start[4] = i;
-                    return true;
-                }
-                at += n;
-                return false;
-            });
+            auto begin = [&](int32_t kvh, int32_t s, int32_t t, int32_t i, int64_t at) {
+                sh.start[0] = kLists ? kvh : (int32_t)head;
+                sh.start[1] = s;
+                sh.start[2] = t;
+                sh.start[3] = i;
+                sh.start_x0 = (int32_t)(x - at);
+                sh.start_seq.nq = seq_nq[s];
+                sh.start_seq.kl = seq_kl[s];
+                sh.start_seq.q0 = P.b.q_start[s];
+            };
+            if (f1 - f0 == 1) {
+                begin(only.x, only.y, only.z, only.w, before);
+            } else {
+                int64_t at = before;
+                walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
+                    if (x < at + n) {
+                        begin(kvh, s, t, i, at);
+                        return true;
+                    }
+                    at += n;
+                    return false;
+                });
+            }
         }
     }
+    // cum and the others, written by ordinary stores, make room for bulk copies
+    fence_proxy_async_smem();
     __syncthreads();
+    if (sh.watch.abort != 0) return;
 
-    // ---------------------------------------------------------------- the run's row tiles
-    float* const so = reinterpret_cast<float*>(smem);  // [warp][row][kRowO] (cum makes room)
-    int32_t kvh = start[0], s = start[1], t = start[2], x0 = start[3], i = start[4];
-    const int64_t u_end = run_start(blockIdx.x + 1);
-    int64_t u = run_start(blockIdx.x);
-    PagedSeq q;
-    paged_seq(P.b, s, q);
-    while (u < u_end) {
-        int32_t lo_t, ns;
-        const int32_t n_row = tile_count(kvh, i, t, q, lo_t, ns);
-        const int32_t n_eff = max(n_row, 1), w = row_units(n_row);
-        const int64_t left = u_end - u;
-        const bool last = left < w - x0;  // the run ends within this row tile
-        const int32_t j0 = cut_at(x0), j1 = min(last ? cut_at(x0 + (int32_t)left) : n_eff, n_row);
-        const bool whole = j0 == 0 && !(last && j1 < n_eff);
-        if (last && j1 <= j0) break;      // (nothing of it: only where the run ends)
-        int32_t row0, nrows;
-        tiles.rows(t, q.nq, row0, nrows);
-        const int32_t tok0 = row0 / P.group;
-        const int32_t pos_of0 = q.kl - q.nq;
-        const float kg = P.k_gain != nullptr ? P.k_gain[kvh] : 1.0f;
+    if (warp == kLoad) {
+        // ------------------------------------------------------------ segments, query rows and key tiles
+        const int64_t u_end = run_start(blockIdx.x + 1);
+        int64_t u = run_start(blockIdx.x);
+        int32_t kvh = sh.start[0], s = sh.start[1], t = sh.start[2], x0 = sh.start_x0, i = sh.start[3];
+        PagedSeq q = sh.start_seq;
+        uint32_t k = 0, g = 0;  // segments and tiles so far
+        bool ok = true;
+        const int32_t page = P.b.page, N = 128 / page, per_window = page >> 2;  // pages of a tile; tiles whose pages one read of 32 lanes brings
+        const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
+        const uint32_t ring = smem_u32(smem);
+        // scales: 16 bytes a lane and copy, of the page that holds them
+        constexpr int kCopies = C::kScales / 512, kBytes = D / 16;  // (a row's scales)
+        const int32_t page_scales = page * kBytes;
+        int32_t sc_page[kCopies], sc_at[kCopies];
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) {
+            sc_page[x] = (x * 512 + lane * 16) / page_scales;
+            sc_at[x] = (x * 512 + lane * 16) % page_scales;
+        }
+        while (u < u_end && ok) {
+            int32_t lo_t, ns;
+            const int32_t n_row = tile_count(kvh, i, t, q.nq, q.kl, lo_t, ns);
+            const int32_t n_eff = max(n_row, 1), w = row_units(n_row);
+            const int64_t left = u_end - u;
+            const bool last = left < w - x0;  // the run ends within this row tile
+            const int32_t j0 = cut_at(x0), j1 = min(last ? cut_at(x0 + (int32_t)left) : n_eff, n_row);
+            if (last && j1 <= j0) break;      // (nothing of it: only where the run ends)
+            const int32_t* table = P.b.table + (int64_t)s * P.b.max_pages;
+            const int32_t* list = kLists ? P.list + list_of(kvh, i) * P.cap : nullptr;
+            // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
+            // sequence's end), and the tile's first key
+            auto fetch = [&](int32_t w0, int32_t& key) -> int32_t {
+                const int32_t j = w0 + lane_tile;
+                key = 0;
+                if (j >= j1) return -1;
+                if constexpr (kLists) key = list[j] * 128;
+                else key = (j < ns ? j : lo_t + j - ns) * 128;
+                const int32_t pg = key / page + lane_page;
+                if (pg * page >= q.kl) return -1;
+                int32_t id = table[pg];
+                if (id < 0 || id >= P.b.n_pages) {
+                    raise_status(status, BSA_ERR_BOUNDS);
+                    id = 0;  // (this row's result is unspecified)
+                }
+                return (id * P.H_kv + kvh) * page;
+            };
+            int32_t key_nxt, key_cur, w0 = j0, cur = fetch(j0, key_cur), nxt = fetch(j0 + per_window, key_nxt);
+            Segment sg;
+            sg.n = j1 - j0;
+            sg.kvh = kvh;
+            sg.q0 = q.q0;
+            tiles.rows(t, q.nq, sg.row0, sg.nrows);
+            sg.pos_of0 = q.kl - q.nq;
+            sg.kl = q.kl;
+            sg.part = j0 == 0 && !(last && j1 < n_eff) ? -1 : 2 * (int32_t)blockIdx.x + (j0 == 0 ? 1 : 0);
+            const uint32_t d = k % kDesc, seg_bar = smem_u32(&sh.seg_full[d]);
+            if (!wait_warp(smem_u32(&sh.seg_empty[d]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                sh.seg[d] = sg;
+                mbar_arrive_expect_tx(seg_bar, (uint32_t)(sg.nrows * D * 2));
+                if (last && j0 == 0) {
+                    // a split row tile begins here; its last part is in the run of its last unit
+                    const int64_t stop = u + (w - x0);
+                    const int64_t longer = (share + 1) * extra;  // units of the longer runs
+                    const int64_t z = stop <= longer ? divide(stop - 1, share + 1) : extra + divide(stop - 1 - longer, share);
+                    P.joins[blockIdx.x] = make_int4((int32_t)(z - blockIdx.x + 1), q.q0 * P.group + sg.row0, sg.nrows, kvh);
+                }
+            }
+            __syncwarp();
+            if (lane < sg.nrows) {
+                const int32_t row = sg.row0 + lane, tok = row / P.group, head = row - tok * P.group;
+                bulk_load(smem_u32(sh.q[d][lane]), P.q + ((int64_t)q.q0 + tok) * P.q_stride + (int64_t)(kvh * P.group + head) * D,
+                          D * 2, seg_bar);
+            }
+            __syncwarp();
+            ++k;
+            for (int32_t j = j0; j < j1; ++j, ++g) {
+                if (j >= w0 + per_window) {
+                    w0 += per_window;
+                    cur = nxt;
+                    key_cur = key_nxt;
+                    nxt = fetch(w0 + per_window, key_nxt);
+                }
+                const bool mine = lane_tile == j - w0 && cur >= 0;
+                const int32_t held = __popc(__ballot_sync(0xffffffffu, mine));
+                const uint32_t at = g % S;
+                if (!wait_warp(smem_u32(&sh.empty[at]), ((g / S) & 1u) ^ 1u, &sh.watch, status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_u32(&sh.full[at]), to = ring + at * C::kStage;
+                if (lane_tile == j - w0 && lane_page == 0) {
+                    sh.key[at] = key_cur;
+                    mbar_arrive_expect_tx(bar, (uint32_t)(held * page * D));
+                }
+                __syncwarp();
+                if (mine) {
+                    bulk_load(to + lane_page * page * (D / 2), P.k + (int64_t)cur * (D / 2), page * (D / 2), bar);
+                    bulk_load(to + C::kCodes + lane_page * page * (D / 2), P.v + (int64_t)cur * (D / 2), page * (D / 2), bar);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < kCopies; ++x) {
+                    const int32_t row = __shfl_sync(0xffffffffu, cur, (j - w0) * N + sc_page[x]);
+                    if (row >= 0) {
+                        const int64_t from = (int64_t)row * kBytes + sc_at[x];
+                        cp_async16(to + 2 * C::kCodes + x * 512 + lane * 16, P.k_scale + from);
+                        cp_async16(to + 2 * C::kCodes + C::kScales + x * 512 + lane * 16, P.v_scale + from);
+                    }
+                }
+                cp_async_arrive_noinc(bar);
+            }
+            // on to the next row tile
+            u += w - x0;
+            x0 = 0;
+            if (u < u_end) {
+                ++t;
+                if (++i == nt) {  // the next head
+                    i = t = s = 0;
+                    ++kvh;
+                    paged_seq(P.b, 0, q);
+                }
+                while (t >= tiles.count(q.nq) && s + 1 < P.b.seqs) {
+                    t = 0;
+                    paged_seq(P.b, ++s, q);
+                }
+            }
+        }
+        if (ok && wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
+            if (lane == 0) {
+                sh.seg[k % kDesc].n = -1;
+                mbar_arrive(smem_u32(&sh.seg_full[k % kDesc]));
+            }
+        } else {
+            ok = false;
+        }
+        if (!ok && lane == 0) set_abort(&sh.watch, status);
+        // every issued copy must land before the block exits
+        cp_async_wait_all();
+        if (lane == 0) {
+            for (uint32_t x = g > S ? g - S : 0; x < g; ++x) paged_drain(smem_u32(&sh.full[x % S]), (x / S) & 1u, status);
+            // (the last descriptor's slot has been handed back: its query rows had landed)
+            const uint32_t known = k + (ok ? 1u : 0u);
+            for (uint32_t x = known > kDesc ? known - kDesc : 0; x < k; ++x)
+                paged_drain(smem_u32(&sh.seg_full[x % kDesc]), (x / kDesc) & 1u, status);
+        }
+        return;
+    }
+
+    float* const so = reinterpret_cast<float*>(smem + C::kRing);  // [warp][row][kRowO]
+    uint32_t k = 0;  // segments so far
+    bool ok = true;
+    if (warp == kStore) {
+        // ------------------------------------------------------------ joins the warps' parts
+        constexpr int kLanes = D / 4, kAbreast = 32 / kLanes;
+        const int col = lane % kLanes;
+        for (;; ++k) {
+            if (!wait_warp(smem_u32(&sh.seg_full[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status)) {
+                ok = false;
+                break;
+            }
+            const Segment sg = sh.seg[k % kDesc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[k % kDesc]));
+            if (sg.n < 0) break;
+            const float vg = P.v_gain != nullptr ? P.v_gain[sg.kvh] : 1.0f;
+            if (!wait_warp(smem_u32(&sh.joined), k & 1u, &sh.watch, status)) {
+                ok = false;
+                break;
+            }
+            for (int32_t row = lane / kLanes; row < sg.nrows; row += kAbreast) {
+                float M = -INFINITY, sum = 0.0f, out[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 z[kWarps];
+#pragma unroll
+                for (int y = 0; y < kWarps; ++y) {
+                    z[y] = sh.ml[y][row];
+                    M = fmaxf(M, z[y].x);
+                }
+#pragma unroll
+                for (int y = 0; y < kWarps; ++y) {
+                    if (z[y].x == -INFINITY && z[y].y == 0.0f) continue;  // no visible key
+                    const float f = ex2(z[y].x - M);
+                    sum = fmaf(f, z[y].y, sum);
+                    const float4 v = *reinterpret_cast<const float4*>(so + (y * R + row) * kRowO + 4 * col);
+                    out[0] = fmaf(f, v.x, out[0]);
+                    out[1] = fmaf(f, v.y, out[1]);
+                    out[2] = fmaf(f, v.z, out[2]);
+                    out[3] = fmaf(f, v.w, out[3]);
+                }
+                if (sg.part < 0) {
+                    const float inv = (sum == 0.0f ? 0.0f : 1.0f / sum) * vg;
+                    const int32_t x = sg.row0 + row, tok = x / P.group;
+                    const int64_t at = ((int64_t)sg.q0 + tok) * P.H + sg.kvh * P.group + (x - tok * P.group);
+                    *reinterpret_cast<uint2*>(P.o + at * D + 4 * col) =
+                        make_uint2(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv));
+                    if (col == 0) P.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+                } else {
+                    const int64_t at = (int64_t)sg.part * R + row;
+                    *reinterpret_cast<float4*>(P.part_o + at * D + 4 * col) = make_float4(out[0], out[1], out[2], out[3]);
+                    if (col == 0) P.part_ml[at] = make_float2(M, sum);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.freed));
+        }
+        if (!ok && lane == 0) set_abort(&sh.watch, status);
+        return;
+    }
+
+    // ---------------------------------------------------------------- the others: products and softmax
+    const int r = lane >> 2, c = lane & 3;
+    // which of the sixteen keys is row i of S^T, so that neither lane (r, c)'s rows r and r + 8 of
+    // K nor its keys key_of(2 c + (y & 1)) + 8 (y / 2) of V, y < 4, meet those of too many other lanes in a bank
+    auto key_of = [](int i) -> int {  // (key_of(i + 8) = key_of(i) + 8)
+        return ((i ^ (i >> 1)) & 1) + (i & 2) + (i & 4) + (i & 8);
+    };
+    const int k_row = key_of(r);
+    // this lane's places in a tile: of K and its scales, of V's keys y = 0 and 1 and theirs (the
+    // other keys lie eight rows on, the second sixteen sixteen)
+    const uint32_t w0 = (warp % kTeam) * 32;
+    const uint32_t off_k = (w0 + k_row) * (D / 2) + c * (D / 8);
+    const uint32_t off_ks = 2 * C::kCodes + (w0 + k_row) * (D / 16) + (D == 128 ? 2 * c : c);
+    const uint32_t v0 = w0 + key_of(2 * c), v1 = w0 + key_of(2 * c + 1);
+    const uint32_t off_v[2] = {C::kCodes + v0 * (D / 2) + r * (D / 16), C::kCodes + v1 * (D / 2) + r * (D / 16)};
+    const uint32_t at_s = 2 * C::kCodes + C::kScales + (D == 128 ? r : r >> 1);
+    const uint32_t off_vs[2] = {at_s + v0 * (D / 16), at_s + v1 * (D / 16)};
+    // this warp's team takes every other tile of the run: slots team, team + 2, ..
+    const uint32_t team = warp / kTeam;
+    uint32_t slot = team, phase = 0;  // of the team's next tile
+    uint32_t g0 = 0;                  // tiles of the segments before
+    for (; ok; ++k) {
+        if (!wait_warp(smem_u32(&sh.seg_full[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status)) {
+            ok = false;
+            break;
+        }
+        const Segment sg = sh.seg[k % kDesc];
+        if (sg.n < 0) break;
+        const int32_t row0 = sg.row0, nrows = sg.nrows;
 
         // queries: lane (r, c) has D / 4 values of rows r, r + 8, ..
         uint32_t qf[NT][kSteps][2];
         float fac[NT][2];               // of the rows of this lane's columns 2 c, 2 c + 1
         int32_t hi[NT][2], lo[NT][2], sk[NT][2];
-        auto end = [&](int32_t p) -> int32_t { return P.causal ? min(q.kl, p + 1) : q.kl; };
+        auto end = [&](int32_t p) -> int32_t { return P.causal ? min(sg.kl, p + 1) : sg.kl; };
+        const float kg = (P.k_gain != nullptr ? P.k_gain[sg.kvh] : 1.0f) * P.scale_log2;
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
-            const int32_t row = row0 + min(8 * b + r, nrows - 1);  // (rows beyond the tile's: any; they are not stored)
-            const int32_t tok = row / P.group, head = row - tok * P.group;
-            const uint4* src = reinterpret_cast<const uint4*>(P.q + ((int64_t)q.q0 + tok) * P.q_stride +
-                                                              (int64_t)(kvh * P.group + head) * D + c * (D / 4));
+            // (rows beyond the tile's: any; they are not stored)
+            const uint4* src = reinterpret_cast<const uint4*>(sh.q[k % kDesc][min(8 * b + r, nrows - 1)] + c * (D / 4));
             uint4 raw[D / 32];
 #pragma unroll
             for (int y = 0; y < D / 32; ++y) raw[y] = src[y];
@@ -297,15 +605,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
             const float up = __int_as_float((127 - e) << 23);
 #pragma unroll
             for (int y = 0; y < D / 8; ++y) {
-                const float a = __uint_as_float(wd[y] << 16) * up, d = __uint_as_float(wd[y] & 0xffff0000u) * up;
-                qf[b][y >> 1][y & 1] = bits(__floats2half2_rn(a, d));
+                const float f0 = __uint_as_float(wd[y] << 16) * up, f1 = __uint_as_float(wd[y] & 0xffff0000u) * up;
+                qf[b][y >> 1][y & 1] = bits(__floats2half2_rn(f0, f1));
             }
-            const float down = __int_as_float((127 + e) << 23) * kg * P.scale_log2;
+            const float down = __int_as_float((127 + e) << 23) * kg;
             fac[b][0] = __shfl_sync(0xffffffffu, down, 8 * c);
             fac[b][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const int32_t p = pos_of0 + (row0 + min(8 * b + 2 * c + y, nrows - 1)) / P.group;
+                const int32_t p = sg.pos_of0 + (row0 + min(8 * b + 2 * c + y, nrows - 1)) / P.group;
                 hi[b][y] = end(p);
                 if constexpr (kMode == kWindow) {
                     lo[b][y] = p - P.window + 1;
@@ -313,63 +621,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
                 }
             }
         }
-        const int32_t p_first = pos_of0 + tok0, p_last = pos_of0 + (row0 + nrows - 1) / P.group;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[k % kDesc]));
+        const int32_t p_first = sg.pos_of0 + row0 / P.group, p_last = sg.pos_of0 + (row0 + nrows - 1) / P.group;
         const int32_t all_hi = end(p_first), all_lo = p_last - P.window + 1, all_sk = min(P.sinks, all_hi);
 
-        // ---- this warp's 16 keys of the key tiles j0 .. j1 - 1
-        const int32_t* table = P.b.table + (int64_t)s * P.b.max_pages;
-        const int32_t* list = kLists ? P.list + list_of(kvh, i) * P.cap : nullptr;
-        auto key_tile = [&](int32_t j) -> int32_t {
-            if constexpr (kLists) return list[j];
-            else return j < ns ? j : lo_t + j - ns;
-        };
-        // lane l of a window of tiles: first key of tile w0 + l's sixteen, and its row in the cache (-1: none)
-        int32_t key_cur, row_cur, key_nxt, row_nxt;
-        const int32_t in_page = (warp * 16) % P.b.page;
-        auto look = [&](int32_t w0, int32_t& key, int32_t& row) {
-            key = 0;
-            row = -1;
-            const int32_t j = w0 + lane;
-            if (j >= j1) return;
-            key = key_tile(j) * 128 + warp * 16;
-            if (key >= q.kl) return;
-            int32_t id = table[key / P.b.page];
-            if (id < 0 || id >= P.b.n_pages) {
-                raise_status(P.b.status, BSA_ERR_BOUNDS);
-                id = 0;  // (this row's result is unspecified)
-            }
-            row = (id * P.H_kv + kvh) * P.b.page + in_page;
-        };
-        struct Raw {
-            uint32_t k[2][kKW];
-            uint32_t ks[2];   // scales of the lane's groups, one or two bytes
-            uint32_t v[4][kVW];
-            uint32_t vs[4];
-        };
-        auto load = [&](int32_t row, Raw& x) {
-            if (row < 0) return;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int64_t at = row + r + 8 * y;
-                const uint8_t* src = P.k + at * (D / 2) + c * (D / 8);
-                const uint8_t* ss = P.k_scale + at * (D / 16);
-                if constexpr (D == 128) {
-                    *reinterpret_cast<uint4*>(x.k[y]) = *reinterpret_cast<const uint4*>(src);
-                    x.ks[y] = *reinterpret_cast<const uint16_t*>(ss + 2 * c);
-                } else {
-                    *reinterpret_cast<uint2*>(x.k[y]) = *reinterpret_cast<const uint2*>(src);
-                    x.ks[y] = ss[c];
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int64_t at = row + 2 * c + (y & 1) + 8 * (y >> 1);
-                const uint8_t* src = P.v + at * (D / 2) + r * (D / 16);
-                if constexpr (D == 128) *reinterpret_cast<uint2*>(x.v[y]) = *reinterpret_cast<const uint2*>(src);
-                else x.v[y][0] = *reinterpret_cast<const uint32_t*>(src);
-                x.vs[y] = P.v_scale[at * (D / 16) + (D == 128 ? r : r >> 1)];
-            }
-        };
         float acc[NT][kSteps][4] = {};
         float m[NT][2], l[NT][2];
 #pragma unroll
@@ -379,73 +635,104 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
                 m[b][y] = -INFINITY;
                 l[b][y] = 0.0f;
             }
-        int32_t w0 = j0;
-        look(j0, key_cur, row_cur);
-        look(j0 + 32, key_nxt, row_nxt);
-        Raw nxt;
-        int32_t row_next = __shfl_sync(0xffffffffu, row_cur, 0), key_next = __shfl_sync(0xffffffffu, key_cur, 0);
-        load(row_next, nxt);
-        for (int32_t j = j0; j < j1; ++j) {
-            const Raw x = nxt;
-            const int32_t row = row_next, kb = key_next;
-            if (j + 1 - w0 == 32) {
-                w0 += 32;
-                key_cur = key_nxt;
-                row_cur = row_nxt;
-                look(w0 + 32, key_nxt, row_nxt);
+        const uint32_t first = (g0 ^ team) & 1u;  // (the segment's first tile is the other team's)
+        g0 += (uint32_t)sg.n;
+#pragma unroll 1
+        for (int32_t n = sg.n - (int32_t)first; n > 0; n -= 2) {
+            if (!wait_warp(smem_u32(&sh.full[slot]), phase, &sh.watch, status)) {
+                ok = false;
+                break;
             }
-            row_next = __shfl_sync(0xffffffffu, row_cur, (j + 1 - w0) & 31);
-            key_next = __shfl_sync(0xffffffffu, key_cur, (j + 1 - w0) & 31);
-            if (j + 1 < j1) load(row_next, nxt);
-            if (row < 0) continue;
-            // S^T = K Q^T
-            float sc[NT][4] = {};
-            {
+            const int32_t kb = sh.key[slot] + (int32_t)w0;
+            const uint32_t done = smem_u32(&sh.empty[slot]);
+            const uint8_t* at = smem + slot * C::kStage;
+            slot += 2;
+            if (slot >= S) {
+                slot = team;
+                phase ^= 1u;
+            }
+            if (kb >= sg.kl) {  // behind the sequence's end
+                if (lane == 0) mbar_arrive(done);
+                continue;
+            }
+            // S^T = K Q^T, twice sixteen keys
+            float sc[2][NT][4] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t kw[2][kKW];
                 __half2 s2[2];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) s2[y] = fp4_scales(x.ks[y]);
+                for (int y = 0; y < 2; ++y) {
+                    const uint8_t* src = at + off_k + (16 * h + 8 * y) * (D / 2);
+                    const uint8_t* ss = at + off_ks + (16 * h + 8 * y) * (D / 16);
+                    if constexpr (D == 128) {
+                        *reinterpret_cast<uint4*>(kw[y]) = *reinterpret_cast<const uint4*>(src);
+                        s2[y] = fp4_scales(*reinterpret_cast<const uint16_t*>(ss));
+                    } else {
+                        *reinterpret_cast<uint2*>(kw[y]) = *reinterpret_cast<const uint2*>(src);
+                        s2[y] = fp4_scales(*ss);
+                    }
+                }
 #pragma unroll
                 for (int wd = 0; wd < kKW; ++wd) {
-                    __half2 a[4], d[4];
-                    fp4_levels(x.k[0][wd], a);
-                    fp4_levels(x.k[1][wd], d);
-                    const __half2 sa = D == 128 && wd >= kKW / 2 ? __high2half2(s2[0]) : __low2half2(s2[0]);
-                    const __half2 sd = D == 128 && wd >= kKW / 2 ? __high2half2(s2[1]) : __low2half2(s2[1]);
+                    __half2 f[4], e[4];
+                    fp4_levels(kw[0][wd], f);
+                    fp4_levels(kw[1][wd], e);
+                    const __half2 sf = D == 128 && wd >= kKW / 2 ? __high2half2(s2[0]) : __low2half2(s2[0]);
+                    const __half2 se = D == 128 && wd >= kKW / 2 ? __high2half2(s2[1]) : __low2half2(s2[1]);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const uint32_t op[4] = {bits(__hmul2(a[2 * y], sa)), bits(__hmul2(d[2 * y], sd)),
-                                                bits(__hmul2(a[2 * y + 1], sa)), bits(__hmul2(d[2 * y + 1], sd))};
+                        const uint32_t op[4] = {bits(__hmul2(f[2 * y], sf)), bits(__hmul2(e[2 * y], se)),
+                                                bits(__hmul2(f[2 * y + 1], sf)), bits(__hmul2(e[2 * y + 1], se))};
 #pragma unroll
-                        for (int b = 0; b < NT; ++b) mma16816(sc[b], op, qf[b][2 * wd + y][0], qf[b][2 * wd + y][1]);
+                        for (int b = 0; b < NT; ++b) mma16816(sc[h][b], op, qf[b][2 * wd + y][0], qf[b][2 * wd + y][1]);
                     }
                 }
             }
-            bool seen = kb + 16 <= all_hi;
-            if constexpr (kMode == kWindow) seen = (seen && kb >= all_lo) || kb + 16 <= all_sk;
-            bool over = false;
+            // exponents against the rows' maxima so far; +inf where a row has none yet
+            bool seen = kb + 32 <= all_hi;
+            if constexpr (kMode == kWindow) seen = (seen && kb >= all_lo) || kb + 32 <= all_sk;
+            auto vis = [&](int h, int b, int y) -> bool {
+                const int32_t key = kb + k_row + 16 * h + 8 * (y >> 1);
+                bool v = key < hi[b][y & 1];
+                if constexpr (kMode == kWindow) v = (v && key >= lo[b][y & 1]) || key < sk[b][y & 1];
+                return v;
+            };
+            float ex[2][NT][4], top = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < NT; ++b)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    sc[b][y] *= fac[b][y & 1];
-                    if (!seen) {
-                        const int32_t key = kb + r + 8 * (y >> 1);
-                        bool vis = key < hi[b][y & 1];
-                        if constexpr (kMode == kWindow) vis = (vis && key >= lo[b][y & 1]) || key < sk[b][y & 1];
-                        if (!vis) sc[b][y] = -INFINITY;
-                    }
-                    over |= !(sc[b][y] <= m[b][y & 1] + kRaise);
-                }
-            if (__any_sync(0xffffffffu, over)) {
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) ex[h][b][y] = fmaf(sc[h][b][y], fac[b][y & 1], -m[b][y & 1]);
+            if (!seen) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) ex[h][b][y] = vis(h, b, y) ? ex[h][b][y] : -INFINITY;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int b = 0; b < NT; ++b) top = fmax3(fmax3(top, ex[h][b][0], ex[h][b][1]), ex[h][b][2], ex[h][b][3]);
+            if (__any_sync(0xffffffffu, top > kRaise)) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float top = fmaxf(sc[b][y], sc[b][y + 2]);
+                        float s4[4], best = -INFINITY;
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        for (int x = 0; x < 4; ++x) {
+                            const int h = x >> 1, z = y + 2 * (x & 1);
+                            s4[x] = seen || vis(h, b, z) ? sc[h][b][z] * fac[b][y] : -INFINITY;
+                            best = fmaxf(best, s4[x]);
+                        }
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
                         // (row by row: what one row holds does not show in another's last bits)
-                        const float m_new = top > m[b][y] + kRaise ? top : m[b][y];
+                        const float m_new = best > m[b][y] + kRaise ? best : m[b][y];
                         const float keep = m[b][y] == -INFINITY ? 1.0f : ex2(m[b][y] - m_new);  // (l and O are 0 still)
                         m[b][y] = m_new;
                         l[b][y] *= keep;
@@ -454,46 +741,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
                             acc[b][z][y] *= keep;
                             acc[b][z][y + 2] *= keep;
                         }
+                        const float base = m_new == -INFINITY ? 0.0f : m_new;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) ex[x >> 1][b][y + 2 * (x & 1)] = s4[x] - base;
                     }
             }
-            uint32_t pt[NT][2];
+            uint32_t pt[2][NT][2];
 #pragma unroll
-            for (int b = 0; b < NT; ++b) {
-                float p[4];
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    float p[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        p[y] = ex2(ex[h][b][y]);
+                        l[b][y & 1] += p[y];
+                    }
+                    pt[h][b][0] = transpose8(bits(__floats2half2_rn(p[0], p[1])));
+                    pt[h][b][1] = transpose8(bits(__floats2half2_rn(p[2], p[3])));
+                }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t vw[4][kVW], vs[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const float base = m[b][y & 1] == -INFINITY ? 0.0f : m[b][y & 1];
-                    p[y] = ex2(sc[b][y] - base);
-                    l[b][y & 1] += p[y];
+                    const uint8_t* src = at + off_v[y & 1] + (16 * h + 8 * (y >> 1)) * (D / 2);
+                    if constexpr (D == 128) *reinterpret_cast<uint2*>(vw[y]) = *reinterpret_cast<const uint2*>(src);
+                    else vw[y][0] = *reinterpret_cast<const uint32_t*>(src);
+                    vs[y] = at[off_vs[y & 1] + (16 * h + 8 * (y >> 1)) * (D / 16)];
                 }
-                pt[b][0] = transpose8(bits(__floats2half2_rn(p[0], p[1])));
-                pt[b][1] = transpose8(bits(__floats2half2_rn(p[2], p[3])));
-            }
-            // O^T += V^T P^T
-            {
-                const __half2 sa = fp4_scales(x.vs[0] | x.vs[1] << 8), sd = fp4_scales(x.vs[2] | x.vs[3] << 8);
+                if (h == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(done);
+                }
+                const __half2 sf = fp4_scales(__byte_perm(vs[0], vs[1], 0x40)), se = fp4_scales(__byte_perm(vs[2], vs[3], 0x40));
                 constexpr uint32_t kLow = 0x0f0f0f0fu;
 #pragma unroll
                 for (int wd = 0; wd < kVW; ++wd) {
-                    __half2 a[4], b0[4], d[4], e[4];
-                    const uint32_t v0 = x.v[0][wd], v1 = x.v[1][wd], v2 = x.v[2][wd], v3 = x.v[3][wd];
-                    fp4_levels((v0 & kLow) | (v1 << 4 & ~kLow), a);
-                    fp4_levels((v0 >> 4 & kLow) | (v1 & ~kLow), b0);
-                    fp4_levels((v2 & kLow) | (v3 << 4 & ~kLow), d);
-                    fp4_levels((v2 >> 4 & kLow) | (v3 & ~kLow), e);
+                    __half2 f0[4], f1[4], e0[4], e1[4];
+                    const uint32_t a0 = vw[0][wd], a1 = vw[1][wd], a2 = vw[2][wd], a3 = vw[3][wd];
+                    fp4_levels((a0 & kLow) | (a1 << 4 & ~kLow), f0);
+                    fp4_levels((a0 >> 4 & kLow) | (a1 & ~kLow), f1);
+                    fp4_levels((a2 & kLow) | (a3 << 4 & ~kLow), e0);
+                    fp4_levels((a2 >> 4 & kLow) | (a3 & ~kLow), e1);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const uint32_t op[4] = {bits(__hmul2(a[y], sa)), bits(__hmul2(b0[y], sa)), bits(__hmul2(d[y], sd)),
-                                                bits(__hmul2(e[y], sd))};
+                        const uint32_t op[4] = {bits(__hmul2(f0[y], sf)), bits(__hmul2(f1[y], sf)), bits(__hmul2(e0[y], se)),
+                                                bits(__hmul2(e1[y], se))};
 #pragma unroll
-                        for (int b = 0; b < NT; ++b) mma16816(acc[b][4 * wd + y], op, pt[b][0], pt[b][1]);
+                        for (int b = 0; b < NT; ++b) mma16816(acc[b][4 * wd + y], op, pt[h][b][0], pt[h][b][1]);
                     }
                 }
             }
         }
+        if (!ok) break;
 
-        // ---- the eight warps' parts
-        __syncthreads();  // the part before (and cum) has been read
+        // ---- this warp's part
+        if (!wait_warp(smem_u32(&sh.freed), (k & 1u) ^ 1u, &sh.watch, status)) {
+            ok = false;
+            break;
+        }
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -502,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
                 for (int d = 4; d < 32; d <<= 1) l[b][y] += __shfl_xor_sync(0xffffffffu, l[b][y], d);
                 const int row = 8 * b + 2 * c + y;
                 if (row < nrows) {
-                    if (r == 0) ml[warp][row] = make_float2(m[b][y], l[b][y]);
+                    if (r == 0) sh.ml[warp][row] = make_float2(m[b][y], l[b][y]);
                     float* to = so + (warp * R + row) * kRowO + r * (D / 8);
 #pragma unroll
                     for (int z = 0; z < kSteps; z += 2)
@@ -510,111 +818,71 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_fp4_rows(const __
                             make_float4(acc[b][z][y], acc[b][z][y + 2], acc[b][z + 1][y], acc[b][z + 1][y + 2]);
                 }
             }
-        __syncthreads();
-        {
-            constexpr int kLanes = D / 4;
-            const int col = threadIdx.x % kLanes;
-            const int32_t slot = 2 * blockIdx.x + (j0 == 0 ? 1 : 0);
-            for (int32_t row = threadIdx.x / kLanes; row < nrows; row += kThreads / kLanes) {
-                float M = -INFINITY, sum = 0.0f, out[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) M = fmaxf(M, ml[x][row].x);
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float2 y = ml[x][row];
-                    if (y.x == -INFINITY && y.y == 0.0f) continue;  // no visible key
-                    const float f = ex2(y.x - M);
-                    sum = fmaf(f, y.y, sum);
-                    const float4 v = *reinterpret_cast<const float4*>(so + (x * R + row) * kRowO + 4 * col);
-                    out[0] = fmaf(f, v.x, out[0]);
-                    out[1] = fmaf(f, v.y, out[1]);
-                    out[2] = fmaf(f, v.z, out[2]);
-                    out[3] = fmaf(f, v.w, out[3]);
-                }
-                if (whole) {
-                    const float inv = (sum == 0.0f ? 0.0f : 1.0f / sum) * (P.v_gain != nullptr ? P.v_gain[kvh] : 1.0f);
-                    const int32_t x = row0 + row, tok = x / P.group;
-                    const int64_t at = ((int64_t)q.q0 + tok) * P.H + kvh * P.group + (x - tok * P.group);
-                    *reinterpret_cast<uint2*>(P.o + at * D + 4 * col) =
-                        make_uint2(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv));
-                    if (col == 0) P.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
-                } else {
-                    const int64_t at = (int64_t)slot * R + row;
-                    *reinterpret_cast<float4*>(P.part_o + at * D + 4 * col) = make_float4(out[0], out[1], out[2], out[3]);
-                    if (col == 0) P.part_ml[at] = make_float2(M, sum);
-                }
-            }
-        }
-        if (threadIdx.x == 0 && last && j0 == 0) {
-            // a split row tile begins here; its last part is in the run of its last unit
-            const int64_t stop = u + (w - x0);
-            const int64_t longer = (share + 1) * extra;  // units of the longer runs
-            const int64_t z = stop <= longer ? (stop - 1) / (share + 1) : extra + (stop - 1 - longer) / share;
-            P.joins[blockIdx.x] = make_int4((int32_t)(z - blockIdx.x + 1), q.q0 * P.group + row0, nrows, kvh);
-        }
-        // on to the next row tile
-        u += w - x0;
-        x0 = 0;
-        if (u < u_end) {
-            ++t;
-            if (++i == nt) {  // the next head
-                i = t = s = 0;
-                ++kvh;
-                paged_seq(P.b, 0, q);
-            }
-            while (t >= tiles.count(q.nq) && s + 1 < P.b.seqs) {
-                t = 0;
-                paged_seq(P.b, ++s, q);
-            }
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.joined));
     }
+    if (!ok && lane == 0) set_abort(&sh.watch, status);
 }
 
 // Joins the parts of split row tiles: O = sum_c 2^(m_c - M) O_c / l with M the largest m_c
-// and l = sum_c 2^(m_c - M) l_c, parts in key order.  Thread block (c, y) takes kJoinThreads /
-// (D / 4) rows of the tile that begins in k_fp4_rows' block c: its slot 1, then slot 0 of the blocks after it.
+// and l = sum_c 2^(m_c - M) l_c.  Thread block (c, y) takes row y of the tile that begins in
+// k_fp4_rows' block c: its slot 1, then slot 0 of the blocks after it.  Lane group w of D / 4 lanes adds
+// parts w, w + kGroups, .., four loads under way at a time; the groups' sums are added in order.
 constexpr int kJoinThreads = 256;
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_fp4_join(const __grid_constant__ Fp4Params P) {
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, R = 8 * NT;
+    __shared__ float4 so[kGroups][kLanes];
+    __shared__ float2 ml[kGroups];
     launch_dependents();
     wait_primary();
-    constexpr int kLanes = D / 4, R = 8 * NT;
-    const int c = threadIdx.x % kLanes;
-    const int32_t row = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
-    const int32_t run = blockIdx.x;
+    const int c = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int32_t row = blockIdx.y, run = blockIdx.x;
     const int4 jn = P.joins[run];
     if (jn.x == 0 || row >= jn.z) return;
-    const uint32_t peers = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);  // this row's lanes
     auto part = [&](int32_t x) -> int64_t { return (((int64_t)run + x) * 2 + (x == 0 ? 1 : 0)) * R + row; };
     float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    // kLanes parts at a time, each thread the maximum and sum of one: all loads at once
-    for (int32_t x0 = 0; x0 < jn.x; x0 += kLanes) {
-        const int32_t n = min(jn.x - x0, kLanes);
-        const float2 y = c < n ? P.part_ml[part(x0 + c)] : make_float2(-INFINITY, 0.0f);
-        const bool none = y.x == -INFINITY && y.y == 0.0f;  // no visible key in this part
-        float top = y.x;
+    for (int32_t x0 = group; x0 < jn.x; x0 += 4 * kGroups) {
+        float2 y[4];
+        float4 v[4];
 #pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(peers, top, d));
-        const float M_new = fmaxf(M, top);
-        const float keep = M == -INFINITY ? 1.0f : ex2(M - M_new);  // (l and o are 0 still)
-        M = M_new;
-        const float f = none ? 0.0f : ex2(y.x - M);
-        float sum = none ? 0.0f : f * y.y;
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(peers, sum, d);
-        l = fmaf(l, keep, sum);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] *= keep;
-#pragma unroll 8
-        for (int32_t x = 0; x < n; ++x) {
-            const float fx = __shfl_sync(peers, f, x, kLanes);
-            const bool skip = __shfl_sync(peers, (int)none, x, kLanes) != 0;
-            const float4 v = *reinterpret_cast<const float4*>(P.part_o + part(x0 + x) * D + 4 * c);
-            o[0] = skip ? o[0] : fmaf(fx, v.x, o[0]);
-            o[1] = skip ? o[1] : fmaf(fx, v.y, o[1]);
-            o[2] = skip ? o[2] : fmaf(fx, v.z, o[2]);
-            o[3] = skip ? o[3] : fmaf(fx, v.w, o[3]);
+        for (int u = 0; u < 4; ++u) {
+            const int32_t x = x0 + u * kGroups;
+            y[u] = x < jn.x ? P.part_ml[part(x)] : make_float2(-INFINITY, 0.0f);
+            v[u] = x < jn.x ? *reinterpret_cast<const float4*>(P.part_o + part(x) * D + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (y[u].x == -INFINITY && y[u].y == 0.0f) continue;  // no visible key in this part
+            const float M_new = fmaxf(M, y[u].x);
+            const float keep = M == -INFINITY ? 1.0f : ex2(M - M_new), f = ex2(y[u].x - M_new);  // (l and o are 0 still)
+            M = M_new;
+            l = fmaf(f, y[u].y, l * keep);
+            o[0] = fmaf(f, v[u].x, o[0] * keep);
+            o[1] = fmaf(f, v[u].y, o[1] * keep);
+            o[2] = fmaf(f, v[u].z, o[2] * keep);
+            o[3] = fmaf(f, v[u].w, o[3] * keep);
+        }
+    }
+    so[group][c] = make_float4(o[0], o[1], o[2], o[3]);
+    if (c == 0) ml[group] = make_float2(M, l);
+    __syncthreads();
+    if (group != 0) return;
+    M = -INFINITY;
+    l = o[0] = o[1] = o[2] = o[3] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) M = fmaxf(M, ml[g].x);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const float2 y = ml[g];
+        if (y.x == -INFINITY && y.y == 0.0f) continue;
+        const float f = ex2(y.x - M);
+        const float4 v = so[g][c];
+        l = fmaf(f, y.y, l);
+        o[0] = fmaf(f, v.x, o[0]);
+        o[1] = fmaf(f, v.y, o[1]);
+        o[2] = fmaf(f, v.z, o[2]);
+        o[3] = fmaf(f, v.w, o[3]);
     }
     const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (P.v_gain != nullptr ? P.v_gain[jn.w] : 1.0f);
     const int32_t x = jn.y + row, tok = x / P.group;
@@ -656,9 +924,10 @@ Layout layout(const PagedForwardArgs& a) {
 
 template <int D, int NT, int kMode>
 bsa_status launch_rows(const Fp4Params& P, cudaStream_t stream) {
-    const size_t merge = sizeof(float) * kWarps * 8 * NT * (D + 4), cum = sizeof(int32_t) * (size_t)P.b.seqs;
-    constexpr size_t most = 72 << 10;
-    const size_t smem = merge > cum ? merge : cum;
+    using C = Cfg<D, NT>;
+    constexpr size_t most = C::kSmem > 3 * sizeof(int32_t) * 16384 ? C::kSmem : 3 * sizeof(int32_t) * 16384;  // (of 16384 sequences)
+    const size_t lists = 3 * sizeof(int32_t) * (size_t)P.b.seqs;
+    const size_t smem = C::kSmem > lists ? C::kSmem : lists;
     static DeviceSetup setup;
     static int sms[kMaxDevices];
     int dev = 0;
@@ -669,11 +938,10 @@ bsa_status launch_rows(const Fp4Params& P, cudaStream_t stream) {
                    cudaSuccess;
     });
     if (!ready) return BSA_ERR_CUDA;
-    const int want = sms[dev] * (NT == 1 ? 2 : 1);
+    const int want = sms[dev] * C::kBlocks;
     const int grid = want < kRuns ? want : kRuns;
-    constexpr int per_join = kJoinThreads / (D / 4);
     if (launch_chained(k_fp4_rows<D, NT, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P) != cudaSuccess ||
-        launch_chained(k_fp4_join<D, NT>, dim3((unsigned)grid, (8 * NT + per_join - 1) / per_join), kJoinThreads, 0, stream, P) !=
+        launch_chained(k_fp4_join<D, NT>, dim3((unsigned)grid, 8 * NT), kJoinThreads, 0, stream, P) !=
             cudaSuccess)
         return BSA_ERR_CUDA;
     return BSA_OK;
