@@ -35,6 +35,7 @@
 
 #include "bsa_device_setup.h"
 #include "bsa_fp4.cuh"
+#include "bsa_fp4_runs.cuh"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
 #include "bsa_paged_wait.cuh"
@@ -45,36 +46,18 @@ namespace {
 
 constexpr int32_t kMaxWindow = 1 << 26;  // (positions lie within 2^24 of zero)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8;                    // that compute
 constexpr int kTeam = 4;                     // of them to a key tile, 32 keys each
 constexpr int kLoad = kWarps, kStore = kWarps + 1;
 constexpr int kThreads = 32 * (kWarps + 2);
 constexpr int kRuns = 2 * kPagedBlocks;
 constexpr int kMaxNT = 2;
+constexpr int32_t kFewRows = 16;             // rows of a sequence that are done here
+// A row tile of n key tiles counts n + kRowCost in a run.
+constexpr int32_t kRowCost = 2;
 constexpr float kRaise = 10.0f;  // log2 of how far a weight may pass its row's maximum
 
 enum { kPlain = 0, kWindow = 1, kListed = 2 };
-
-struct Fp4Params {
-    PagedBatch b;
-    const uint8_t *k, *k_scale, *v, *v_scale;
-    const float *k_gain, *v_gain;
-    const __nv_bfloat16* q;
-    int64_t q_stride;
-    int32_t H, H_kv, group;
-    int32_t causal, window, sinks;
-    float scale_log2;
-    __nv_bfloat16* o;
-    float* lse;
-    // lists: of token tile f = kvh * nt_cap + token of the batch (in sequence order)
-    const int32_t *list, *list_cnt;
-    int32_t nt_cap, cap;
-    // parts of split tiles
-    float* part_o;    // [runs, 2, 8 NT, D]
-    float2* part_ml;  // [runs, 2, 8 NT] maximum (log2) and sum
-    int4* joins;      // [runs] parts (0: none), first packed row (token * group + head), rows, kvh
-};
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -88,46 +71,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 __device__ __forceinline__ uint32_t bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
-
-// Key tiles that the tokens at positions pos0 .. pos0 + ntok - 1 see some key
-// of: the sink tiles 0 .. ns - 1 and lo .. lo + (n - ns) - 1.
-__device__ __forceinline__ int32_t key_tiles(const Fp4Params& P, int32_t pos0, int32_t ntok, int32_t kl, int32_t& lo,
-                                             int32_t& ns) {
-    const int32_t hi = P.causal ? min(kl, pos0 + ntok) : kl;  // keys 0 .. hi - 1
-    lo = ns = 0;
-    if (hi <= 0) return 0;
-    const int32_t hi_t = (hi + 127) >> 7;
-    if (P.window > 0) {
-        lo = min(max(pos0 - P.window + 1, 0) >> 7, hi_t);
-        ns = min((min(P.sinks, hi) + 127) >> 7, lo);
-    }
-    return hi_t - lo + ns;
-}
-
-// A row tile of n key tiles counts n + kRowCost in a run, the constant for its start and end.
-constexpr int32_t kRowCost = 2;
-__device__ __forceinline__ int32_t row_units(int32_t n) { return max(n, 1) + kRowCost; }
-__device__ __forceinline__ int32_t cut_at(int32_t x) { return max(x - kRowCost, 0); }
-
-// Row tile t of a sequence: its rows are `rows` from row0 on (token * group + head).
-template <bool kLists>
-struct Tiles {
-    int32_t group, wide;  // rows of a tile, at most
-    __device__ __forceinline__ int32_t per_token() const { return (group + wide - 1) / wide; }
-    __device__ __forceinline__ int32_t count(int32_t nq) const {
-        return kLists ? nq * per_token() : (int32_t)(((int64_t)nq * group + wide - 1) / wide);
-    }
-    __device__ __forceinline__ void rows(int32_t t, int32_t nq, int32_t& row0, int32_t& n) const {
-        if constexpr (kLists) {
-            const int32_t per = per_token(), tok = t / per, h = (t - tok * per) * wide;
-            row0 = tok * group + h;
-            n = min(wide, group - h);
-        } else {
-            row0 = t * wide;
-            n = min(wide, nq * group - row0);
-        }
-    }
-};
 
 // Shared memory of a thread block: a ring of key tiles (codes of keys and of values, then their
 // scales), the parts of O that the warps join, query rows, and what the warps tell one another.
@@ -143,14 +86,6 @@ struct Cfg {
     static constexpr int kSmem = kRing + kJoin;
 };
 
-// A row tile's part in a run, as the producer tells it.
-struct Segment {
-    int32_t n;              // key tiles (0: no key at all; -1: no more segments)
-    int32_t kvh, q0;        // head; the sequence's first packed token
-    int32_t row0, nrows;    // rows (token of the sequence * group + head)
-    int32_t pos_of0, kl;    // position of the sequence's first new token, keys in the cache
-    int32_t part;           // -1: the whole row tile is here; else its part slot: 2 block + 0 or 1
-};
 constexpr int kDesc = 3;    // descriptors in flight
 
 template <int D, int NT>
@@ -160,22 +95,15 @@ struct Shared {
     uint64_t seg_full[kDesc], seg_empty[kDesc];
     uint64_t joined, freed;           // the warps' parts are there, have been read
     Watch watch;
-    Segment seg[kDesc];
+    Fp4Segment seg[kDesc];
     int32_t key[Cfg<D, NT>::kStages]; // first key of the tile in each slot
     int64_t prefix[33];
-    int32_t start[4];                 // this run's first unit: kvh, sequence, row tile, tile of the head
-    int32_t start_x0;                 // .. unit within the row tile
-    PagedSeq start_seq;
+    Fp4Start start;
     float2 ml[kWarps][8 * NT];
 };
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, const int32_t* status) {
     return __all_sync(0xffffffffu, paged_wait(bar, parity, w, status));
-}
-
-// a / b; nearly every dividend fits 32 bits, whose division is much shorter.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    return (a >> 32) == 0 && (b >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 template <int D, int NT, int kMode>
@@ -215,133 +143,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
     }
 
     // ---------------------------------------------------------------- this block's run
-    // of sequence s: the row tiles of the sequences before it, its new tokens and its
-    // length (the ring is free here)
-    const Tiles<kLists> tiles{P.group, R};
-    int32_t* cum = reinterpret_cast<int32_t*>(smem);
-    int32_t* seq_nq = cum + P.b.seqs;
-    int32_t* seq_kl = seq_nq + P.b.seqs;
-    int32_t nt;
-    {
-        const int32_t per = (P.b.seqs + kThreads - 1) / kThreads;
-        const int32_t a = min((int32_t)threadIdx.x * per, P.b.seqs), e = min(a + per, P.b.seqs);
-        int64_t mine = 0, all;
-        for (int32_t s = a; s < e; ++s) {
-            PagedSeq q;
-            if (!paged_seq(P.b, s, q) && blockIdx.x == 0) raise_status(status, BSA_ERR_BOUNDS);
-            seq_nq[s] = q.nq;
-            seq_kl[s] = q.kl;
-            mine += tiles.count(q.nq);
-        }
-        int64_t at = block_prefix<kThreads>(mine, sh.prefix, all);
-        for (int32_t s = a; s < e; ++s) {
-            cum[s] = (int32_t)min(at, (int64_t)INT32_MAX);
-            at += tiles.count(seq_nq[s]);
-        }
-        // (beyond this: only with starts that decrease, reported above)
-        const int64_t most = kLists ? (int64_t)P.nt_cap * tiles.per_token() : (int64_t)P.b.tokens * P.group / R + P.b.seqs;
-        nt = (int32_t)min(all, most);
-    }
-    __syncthreads();
-    auto list_of = [&](int32_t kvh, int32_t i) -> int64_t {  // (row tile i of the head)
-        return (int64_t)kvh * P.nt_cap + i / tiles.per_token();
-    };
-    // key tiles of row tile i of the head, tile t of its sequence of nq new tokens and kl keys
-    auto tile_count = [&](int32_t kvh, int32_t i, int32_t t, int32_t nq, int32_t kl, int32_t& lo, int32_t& ns) -> int32_t {
-        if constexpr (kLists) {
-            lo = ns = 0;
-            return P.list_cnt[list_of(kvh, i)];
-        } else {
-            int32_t row0, n;
-            tiles.rows(t, nq, row0, n);
-            const int32_t first = row0 / P.group, last = (row0 + n - 1) / P.group;
-            return key_tiles(P, kl - nq + first, last - first + 1, kl, lo, ns);
-        }
-    };
-    const int64_t rows = kLists ? (int64_t)nt * P.H_kv : nt;  // tiles whose counts differ
-    const int64_t per_row = divide(rows + kThreads - 1, kThreads);
-    const int64_t f0 = min((int64_t)threadIdx.x * per_row, rows), f1 = min(f0 + per_row, rows);
-    // walks this thread's tiles: visit(kvh, i, s, t, units)
-    auto walk = [&](auto&& visit) {
-        if (f0 >= f1) return;
-        int32_t kvh = kLists ? (int32_t)divide(f0, nt) : 0, i = (int32_t)(f0 - (int64_t)kvh * nt), s = 0;
-        auto find = [&]() {
-            int32_t lo = 0, hi = P.b.seqs;  // the last s with cum[s] <= i
-            while (hi - lo > 1) {
-                const int32_t mid = (lo + hi) >> 1;
-                if (cum[mid] <= i) lo = mid;
-                else hi = mid;
-            }
-            s = lo;
-        };
-        find();
-        for (int64_t f = f0; f < f1; ++f) {
-            const int32_t t = i - cum[s];
-            int32_t lo, ns;
-            if (visit(kvh, i, s, t, row_units(tile_count(kvh, i, t, seq_nq[s], seq_kl[s], lo, ns)))) return;
-            ++i;
-            if (i == nt) {
-                i = 0;
-                ++kvh;
-                if (f + 1 < f1) find();
-            } else if (s + 1 < P.b.seqs && cum[s + 1] <= i) {
-                find();
-            }
-        }
-    };
-    int64_t mine = 0, total;
-    int4 only = make_int4(0, 0, 0, 0);  // (a thread with one tile need not walk again)
-    walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
-        mine += n;
-        only = make_int4(kvh, s, t, i);
-        return false;
-    });
-    const int64_t before = block_prefix<kThreads>(mine, sh.prefix, total);
-    const int64_t units = kLists ? total : total * P.H_kv;
-    const int32_t blocks = (int32_t)min((int64_t)gridDim.x, units);
-    if ((int32_t)blockIdx.x >= blocks) return;
-    const int64_t share = divide(units, blocks);  // equal runs, the first `extra` of them one unit longer
-    const int32_t extra = (int32_t)(units - share * blocks);
-    auto run_start = [&](int32_t x) -> int64_t { return share * x + min(x, extra); };
-    {
-        const int64_t u0 = run_start(blockIdx.x), head = kLists ? 0 : divide(u0, total), x = kLists ? u0 : u0 - head * total;
-        if (x >= before && x < before + mine) {
-            auto begin = [&](int32_t kvh, int32_t s, int32_t t, int32_t i, int64_t at) {
-                sh.start[0] = kLists ? kvh : (int32_t)head;
-                sh.start[1] = s;
-                sh.start[2] = t;
-                sh.start[3] = i;
-                sh.start_x0 = (int32_t)(x - at);
-                sh.start_seq.nq = seq_nq[s];
-                sh.start_seq.kl = seq_kl[s];
-                sh.start_seq.q0 = P.b.q_start[s];
-            };
-            if (f1 - f0 == 1) {
-                begin(only.x, only.y, only.z, only.w, before);
-            } else {
-                int64_t at = before;
-                walk([&](int32_t kvh, int32_t i, int32_t s, int32_t t, int32_t n) {
-                    if (x < at + n) {
-                        begin(kvh, s, t, i, at);
-                        return true;
-                    }
-                    at += n;
-                    return false;
-                });
-            }
-        }
-    }
-    // cum and the others, written by ordinary stores, make room for bulk copies
+    // (its scratch is in the ring, which is free here)
+    Fp4Run run;
+    if (!Fp4Work<R, kRowCost, kLists>{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run)) return;
+    // what was written there by ordinary stores makes room for bulk copies
     fence_proxy_async_smem();
     __syncthreads();
     if (sh.watch.abort != 0) return;
 
     if (warp == kLoad) {
         // ------------------------------------------------------------ segments, query rows and key tiles
-        const int64_t u_end = run_start(blockIdx.x + 1);
-        int64_t u = run_start(blockIdx.x);
-        int32_t kvh = sh.start[0], s = sh.start[1], t = sh.start[2], x0 = sh.start_x0, i = sh.start[3];
-        PagedSeq q = sh.start_seq;
+        Fp4Walk<R, kRowCost, kLists> walk(P, run, sh.start);
+        Fp4Segment sg;
         uint32_t k = 0, g = 0;  // segments and tiles so far
         bool ok = true;
         const int32_t page = P.b.page, N = 128 / page, per_window = page >> 2;  // pages of a tile; tiles whose pages one read of 32 lanes brings
@@ -356,16 +169,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
             sc_page[x] = (x * 512 + lane * 16) / page_scales;
             sc_at[x] = (x * 512 + lane * 16) % page_scales;
         }
-        while (u < u_end && ok) {
-            int32_t lo_t, ns;
-            const int32_t n_row = tile_count(kvh, i, t, q.nq, q.kl, lo_t, ns);
-            const int32_t n_eff = max(n_row, 1), w = row_units(n_row);
-            const int64_t left = u_end - u;
-            const bool last = left < w - x0;  // the run ends within this row tile
-            const int32_t j0 = cut_at(x0), j1 = min(last ? cut_at(x0 + (int32_t)left) : n_eff, n_row);
-            if (last && j1 <= j0) break;      // (nothing of it: only where the run ends)
-            const int32_t* table = P.b.table + (int64_t)s * P.b.max_pages;
-            const int32_t* list = kLists ? P.list + list_of(kvh, i) * P.cap : nullptr;
+        for (; ok && walk.open(sg); walk.advance()) {
+            const int32_t j0 = sg.j0, j1 = j0 + sg.n, kvh = sg.kvh;
+            const int32_t* table = P.b.table + (int64_t)walk.s * P.b.max_pages;
+            const int32_t* list = kLists ? P.list + walk.work.list_of(kvh, walk.i) * P.cap : nullptr;
             // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
             // sequence's end), and the tile's first key
             auto fetch = [&](int32_t w0, int32_t& key) -> int32_t {
@@ -373,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
                 key = 0;
                 if (j >= j1) return -1;
                 if constexpr (kLists) key = list[j] * 128;
-                else key = (j < ns ? j : lo_t + j - ns) * 128;
+                else key = (j < sg.ns ? j : sg.lo + j - sg.ns) * 128;
                 const int32_t pg = key / page + lane_page;
-                if (pg * page >= q.kl) return -1;
+                if (pg * page >= sg.kl) return -1;
                 int32_t id = table[pg];
                 if (id < 0 || id >= P.b.n_pages) {
                     raise_status(status, BSA_ERR_BOUNDS);
@@ -384,14 +191,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
                 return (id * P.H_kv + kvh) * page;
             };
             int32_t key_nxt, key_cur, w0 = j0, cur = fetch(j0, key_cur), nxt = fetch(j0 + per_window, key_nxt);
-            Segment sg;
-            sg.n = j1 - j0;
-            sg.kvh = kvh;
-            sg.q0 = q.q0;
-            tiles.rows(t, q.nq, sg.row0, sg.nrows);
-            sg.pos_of0 = q.kl - q.nq;
-            sg.kl = q.kl;
-            sg.part = j0 == 0 && !(last && j1 < n_eff) ? -1 : 2 * (int32_t)blockIdx.x + (j0 == 0 ? 1 : 0);
             const uint32_t d = k % kDesc, seg_bar = smem_u32(&sh.seg_full[d]);
             if (!wait_warp(smem_u32(&sh.seg_empty[d]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
                 ok = false;
@@ -400,18 +199,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
             if (lane == 0) {
                 sh.seg[d] = sg;
                 mbar_arrive_expect_tx(seg_bar, (uint32_t)(sg.nrows * D * 2));
-                if (last && j0 == 0) {
-                    // a split row tile begins here; its last part is in the run of its last unit
-                    const int64_t stop = u + (w - x0);
-                    const int64_t longer = (share + 1) * extra;  // units of the longer runs
-                    const int64_t z = stop <= longer ? divide(stop - 1, share + 1) : extra + divide(stop - 1 - longer, share);
-                    P.joins[blockIdx.x] = make_int4((int32_t)(z - blockIdx.x + 1), q.q0 * P.group + sg.row0, sg.nrows, kvh);
-                }
+                walk.note(sg);
             }
             __syncwarp();
             if (lane < sg.nrows) {
                 const int32_t row = sg.row0 + lane, tok = row / P.group, head = row - tok * P.group;
-                bulk_load(smem_u32(sh.q[d][lane]), P.q + ((int64_t)q.q0 + tok) * P.q_stride + (int64_t)(kvh * P.group + head) * D,
+                bulk_load(smem_u32(sh.q[d][lane]), P.q + ((int64_t)sg.q0 + tok) * P.q_stride + (int64_t)(kvh * P.group + head) * D,
                           D * 2, seg_bar);
             }
             __syncwarp();
@@ -452,21 +245,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
                 }
                 cp_async_arrive_noinc(bar);
             }
-            // on to the next row tile
-            u += w - x0;
-            x0 = 0;
-            if (u < u_end) {
-                ++t;
-                if (++i == nt) {  // the next head
-                    i = t = s = 0;
-                    ++kvh;
-                    paged_seq(P.b, 0, q);
-                }
-                while (t >= tiles.count(q.nq) && s + 1 < P.b.seqs) {
-                    t = 0;
-                    paged_seq(P.b, ++s, q);
-                }
-            }
         }
         if (ok && wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
             if (lane == 0) {
@@ -501,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
                 ok = false;
                 break;
             }
-            const Segment sg = sh.seg[k % kDesc];
+            const Fp4Segment sg = sh.seg[k % kDesc];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[k % kDesc]));
             if (sg.n < 0) break;
@@ -535,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
                     const int64_t at = ((int64_t)sg.q0 + tok) * P.H + sg.kvh * P.group + (x - tok * P.group);
                     *reinterpret_cast<uint2*>(P.o + at * D + 4 * col) =
                         make_uint2(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv));
-                    if (col == 0) P.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+                    if (col == 0) P.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kFp4Ln2;
                 } else {
                     const int64_t at = (int64_t)sg.part * R + row;
                     *reinterpret_cast<float4*>(P.part_o + at * D + 4 * col) = make_float4(out[0], out[1], out[2], out[3]);
@@ -575,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
             ok = false;
             break;
         }
-        const Segment sg = sh.seg[k % kDesc];
+        const Fp4Segment sg = sh.seg[k % kDesc];
         if (sg.n < 0) break;
         const int32_t row0 = sg.row0, nrows = sg.nrows;
 
@@ -824,74 +602,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
     if (!ok && lane == 0) set_abort(&sh.watch, status);
 }
 
-// Joins the parts of split row tiles: O = sum_c 2^(m_c - M) O_c / l with M the largest m_c
-// and l = sum_c 2^(m_c - M) l_c.  Thread block (c, y) takes row y of the tile that begins in
-// k_fp4_rows' block c: its slot 1, then slot 0 of the blocks after it.  Lane group w of D / 4 lanes adds
-// parts w, w + kGroups, .., four loads under way at a time; the groups' sums are added in order.
-constexpr int kJoinThreads = 256;
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) k_fp4_join(const __grid_constant__ Fp4Params P) {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, R = 8 * NT;
-    __shared__ float4 so[kGroups][kLanes];
-    __shared__ float2 ml[kGroups];
-    launch_dependents();
-    wait_primary();
-    const int c = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const int32_t row = blockIdx.y, run = blockIdx.x;
-    const int4 jn = P.joins[run];
-    if (jn.x == 0 || row >= jn.z) return;
-    auto part = [&](int32_t x) -> int64_t { return (((int64_t)run + x) * 2 + (x == 0 ? 1 : 0)) * R + row; };
-    float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int32_t x0 = group; x0 < jn.x; x0 += 4 * kGroups) {
-        float2 y[4];
-        float4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int32_t x = x0 + u * kGroups;
-            y[u] = x < jn.x ? P.part_ml[part(x)] : make_float2(-INFINITY, 0.0f);
-            v[u] = x < jn.x ? *reinterpret_cast<const float4*>(P.part_o + part(x) * D + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (y[u].x == -INFINITY && y[u].y == 0.0f) continue;  // no visible key in this part
-            const float M_new = fmaxf(M, y[u].x);
-            const float keep = M == -INFINITY ? 1.0f : ex2(M - M_new), f = ex2(y[u].x - M_new);  // (l and o are 0 still)
-            M = M_new;
-            l = fmaf(f, y[u].y, l * keep);
-            o[0] = fmaf(f, v[u].x, o[0] * keep);
-            o[1] = fmaf(f, v[u].y, o[1] * keep);
-            o[2] = fmaf(f, v[u].z, o[2] * keep);
-            o[3] = fmaf(f, v[u].w, o[3] * keep);
-        }
-    }
-    so[group][c] = make_float4(o[0], o[1], o[2], o[3]);
-    if (c == 0) ml[group] = make_float2(M, l);
-    __syncthreads();
-    if (group != 0) return;
-    M = -INFINITY;
-    l = o[0] = o[1] = o[2] = o[3] = 0.0f;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) M = fmaxf(M, ml[g].x);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        const float2 y = ml[g];
-        if (y.x == -INFINITY && y.y == 0.0f) continue;
-        const float f = ex2(y.x - M);
-        const float4 v = so[g][c];
-        l = fmaf(f, y.y, l);
-        o[0] = fmaf(f, v.x, o[0]);
-        o[1] = fmaf(f, v.y, o[1]);
-        o[2] = fmaf(f, v.z, o[2]);
-        o[3] = fmaf(f, v.w, o[3]);
-    }
-    const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (P.v_gain != nullptr ? P.v_gain[jn.w] : 1.0f);
-    const int32_t x = jn.y + row, tok = x / P.group;
-    const int64_t at = (int64_t)tok * P.H + jn.w * P.group + (x - tok * P.group);
-    *reinterpret_cast<uint2*>(P.o + at * D + 4 * c) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-    if (c == 0) P.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
-}
-
 // ---------------------------------------------------------------- host side
 // Workspace: joins, maxima and sums, O parts; then the tokens' lists.
 struct Layout {
@@ -906,9 +616,11 @@ Layout layout(const PagedForwardArgs& a) {
         at += (bytes + 255) & ~(size_t)255;
         return p;
     };
+    // rows of all parts, of either kernel (one comes after the other)
+    constexpr size_t few = (size_t)kRuns * 2 * 8 * kMaxNT, many = (size_t)kPagedBlocks * 2 * kFp4PromptWide;
     L.joins = take(sizeof(int4) * kRuns);
-    L.ml = take(sizeof(float2) * kRuns * 2 * 8 * kMaxNT);
-    L.o = take(sizeof(float) * kRuns * 2 * 8 * kMaxNT * (size_t)a.D);
+    L.ml = take(sizeof(float2) * (few > many ? few : many));
+    L.o = take(sizeof(float) * (few > many ? few : many) * (size_t)a.D);
     if (a.sel_width > 0) {
         const int64_t blocks = ((int64_t)a.max_pages * a.page + 127) / 128;
         L.cap = (int32_t)(blocks < a.sel_width ? blocks : a.sel_width);
@@ -941,7 +653,7 @@ bsa_status launch_rows(const Fp4Params& P, cudaStream_t stream) {
     const int want = sms[dev] * C::kBlocks;
     const int grid = want < kRuns ? want : kRuns;
     if (launch_chained(k_fp4_rows<D, NT, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P) != cudaSuccess ||
-        launch_chained(k_fp4_join<D, NT>, dim3((unsigned)grid, 8 * NT), kJoinThreads, 0, stream, P) !=
+        launch_chained(k_fp4_join<D, 8 * NT, 1>, dim3((unsigned)grid, 8 * NT), kFp4JoinThreads, 0, stream, P) !=
             cudaSuccess)
         return BSA_ERR_CUDA;
     return BSA_OK;
@@ -984,8 +696,9 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     P.joins = reinterpret_cast<int4*>(ws + L.joins);
     P.part_ml = reinterpret_cast<float2*>(ws + L.ml);
     P.part_o = reinterpret_cast<float*>(ws + L.o);
-    // rows of a sequence's new tokens, at most: more than eight want the wider tile
-    const int64_t most = (int64_t)(x.max_new > 0 && x.max_new < a.tokens ? x.max_new : a.tokens) * P.group;
+    P.least = 1;
+    P.most = INT32_MAX;
+    const bool wide = P.group > 8;  // (a token's rows in one tile)
     if (a.sel != nullptr) {
         P.nt_cap = L.list_rows;
         P.cap = L.cap;
@@ -996,9 +709,17 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
         if (c != BSA_OK) return c;
         P.list = list;
         P.list_cnt = cnt;
-        return launch_mode<kListed>(P, a.D, P.group > 8, stream);
+        return launch_mode<kListed>(P, a.D, wide, stream);
     }
-    return a.window > 0 ? launch_mode<kWindow>(P, a.D, most > 8, stream) : launch_mode<kPlain>(P, a.D, most > 8, stream);
+    // sequences of few rows here, the others on large tiles, unless the host knows of no others (what it
+    // was told may be wrong: then all of them are done here)
+    const int64_t most = (int64_t)(x.max_new > 0 && x.max_new < a.tokens ? x.max_new : a.tokens) * P.group;
+    P.most = most > kFewRows ? kFewRows : INT32_MAX;
+    const bsa_status c = a.window > 0 ? launch_mode<kWindow>(P, a.D, wide, stream) : launch_mode<kPlain>(P, a.D, wide, stream);
+    if (c != BSA_OK || most <= kFewRows) return c;
+    P.least = kFewRows + 1;
+    P.most = INT32_MAX;
+    return launch_fp4_prompt(P, a.D, stream);
 }
 
 }  // namespace bsa

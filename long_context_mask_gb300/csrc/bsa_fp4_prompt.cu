@@ -1,0 +1,785 @@
+// Attention over a paged key/value cache held in 4 bits, for sequences with many new rows
+// (chunks, prompts), on the tensor core's large tiles (tcgen05 + TMEM).  What it computes, and how
+// rows are laid out and cut, is bsa_fp4_attn.cu's and bsa_fp4_runs.cuh's.
+//
+// A row tile is 128 rows, S = Q K^T and O += P V are 128 x 128 (x D) products of fp16 operands.
+// Warps (20):  0 cuts the run into segments, tells them to the others through a ring of descriptors and
+// loads codes and scales of key tiles by bulk copies; 16 .. 19 unpack them to fp16 tiles in the swizzled
+// layout the products read (levels times scales, exact), and the segment's queries (each row times
+// the power of two that brings its largest value to 2^14, rounded to fp16); 1 issues Q K^T, 2 P V;
+// 4 .. 11 are the softmax (four threads a row, see bsa_rows.cuh); 12 .. 15 normalise and store a
+// segment's rows while the softmax is at the next one.
+// Shared memory: the Q tile, two K and two V tiles, three tiles of codes.  Tensor memory: three score
+// buffers and O.  Tiles are numbered through the whole run, across the borders of segments.
+//
+// Rounding.  Weights are rounded to fp16 for the product P V; they stay below 2^15 against an
+// earlier maximum of their row (see softmax_rows).  Row sums add them unrounded.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "bsa_device_setup.h"
+#include "bsa_fp4.cuh"
+#include "bsa_fp4_runs.cuh"
+#include "bsa_internal.h"
+#include "bsa_paged.cuh"
+#include "bsa_paged_wait.cuh"
+#include "bsa_rows.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kWide = kFp4PromptWide;
+constexpr int32_t kRowCost = 4;
+constexpr float kRescale = 8.0f;                          // raise a row's maximum when it grows by > 2^8
+constexpr float kSumLimit = 32768.0f;                     // 2^15, see softmax_rows
+constexpr int kSBuf = 3;                                  // TMEM score buffers
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 384;
+constexpr int kLoad = 0, kMmaQK = 1, kMmaPV = 2, kSoftmax0 = 4, kSoftmaxWarps = 8, kStore0 = 12, kStoreWarps = 4,
+              kUnpack0 = 16, kUnpackWarps = 4;
+constexpr int kThreads = 32 * 20;
+constexpr int kDesc = 4;                                  // segment descriptors in flight
+constexpr int kReaders = 2 + kSoftmaxWarps + kStoreWarps + kUnpackWarps;  // warps that read a descriptor
+constexpr int kBox = 128 * 128;                           // 128 rows of 64 fp16
+
+enum { kPlain = 0, kWindow = 1 };
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = kBox * kHalves;
+    static constexpr int kTiles = D == 128 ? 2 : 4;       // K tiles, and V tiles
+    static constexpr int kCodeStages = 3;
+    static constexpr int kCodes = 128 * D / 2, kScales = 128 * D / 16;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kData = kTile * (1 + 2 * kTiles) + kCodeStages * kStage;
+    static constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, 0, 0);
+    static constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, 0, 1);
+};
+
+struct Shared {
+    uint64_t code_full[3], code_empty[3];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t q_ready[kDesc], q_empty;
+    uint64_t s_full[kSBuf];   // S_g is there
+    uint64_t p_full[kSBuf];   // P_g has been written (and O rescaled)
+    uint64_t pv_done[kSBuf];  // O holds P_g V_g
+    uint64_t o_free;          // the segment's O has been read
+    uint64_t ml_full, ml_empty;  // a segment's maxima and sums are in ml, have been read
+    uint64_t mma_done;
+    uint64_t seg_full[kDesc], seg_empty[kDesc];
+    Watch watch;
+    Fp4Segment seg[kDesc];
+    float fac[kDesc][kWide];  // of a segment's rows: what turns a product of operands into a score (log2)
+    float2 ml[kWide];         // of a segment's rows: maximum (log2) and sum
+    int64_t prefix[33];
+    Fp4Start start;
+    uint32_t tmem_base;
+};
+
+__device__ __forceinline__ uint32_t bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ void store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, const int32_t* status) {
+    return __all_sync(0xffffffffu, paged_wait(bar, parity, w, status));
+}
+
+// Which of a thread's columns 8 kk and 8 kk + 1 (kk = 0 .. 15; bit 2 kk and the
+// next) are below v.
+__device__ __forceinline__ uint32_t columns_below(int32_t v) {
+    const int32_t n = v <= 0 ? 0 : 2 * (v >> 3) + min(v & 7, 2);
+    return n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
+// exp_rows of bsa_rows.cuh with a factor for each row and fp16 weights.
+__device__ __forceinline__ void exp_rows_f16(uint32_t (&s)[64], const float (&f)[2], float bias_a, float bias_b, float& la,
+                                             float& lb) {
+    const uint64_t fa = f2pack(f[0], f[0]), fb = f2pack(f[1], f[1]), ba = f2pack(bias_a, bias_a), bb = f2pack(bias_b, bias_b);
+    uint64_t acc_a0 = f2pack(0.f, 0.f), acc_a1 = acc_a0, acc_b0 = acc_a0, acc_b1 = acc_a0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        float x[4];
+        f2unpack(fma2(f2pack(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])), fa, ba), x[0], x[1]);
+        f2unpack(fma2(f2pack(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])), fb, bb), x[2], x[3]);
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = ex2(x[i]);
+        if (k & 1) {
+            acc_a1 = add2(acc_a1, f2pack(p[0], p[1]));
+            acc_b1 = add2(acc_b1, f2pack(p[2], p[3]));
+        } else {
+            acc_a0 = add2(acc_a0, f2pack(p[0], p[1]));
+            acc_b0 = add2(acc_b0, f2pack(p[2], p[3]));
+        }
+        s[2 * k] = bits(__floats2half2_rn(p[0], p[1]));
+        s[2 * k + 1] = bits(__floats2half2_rn(p[2], p[3]));
+    }
+    float x0, x1;
+    f2unpack(add2(acc_a0, acc_a1), x0, x1);
+    la = x0 + x1;
+    f2unpack(add2(acc_b0, acc_b1), x0, x1);
+    lb = x0 + x1;
+}
+
+// One key tile of the online softmax for this thread's shares of rows a and b.
+// dead: the row holds no token (its scores are 0; m = 0, and it takes part in no
+// decision).  A live row that has seen no key yet has m = -inf.  As long as no
+// row of the warp is in that state (fresh, warp-uniform) the exponentials are
+// taken against the running maxima without computing the tile's own; only a
+// tile whose sums leave 2^15 (or are NaN) is redone with its maxima.  Returns
+// true (warp-uniform) when O must be multiplied by alpha first.
+template <typename Reload>
+__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], const float (&f)[2], bool& fresh,
+                                             float (&m)[2], float (&l)[2], float (&alpha)[2], Reload&& reload) {
+    alpha[0] = alpha[1] = 1.0f;
+    float la, lb;
+    if (!fresh) {
+        exp_rows_f16(s, f, -m[0], -m[1], la, lb);
+        if (!__any_sync(0xffffffffu, (!dead[0] && !(la <= kSumLimit)) || (!dead[1] && !(lb <= kSumLimit)))) {
+            l[0] += la;
+            l[1] += lb;
+            return false;
+        }
+        reload();
+    }
+    float mt[2];
+    max_rows(s, mt[0], mt[1]);
+    bool raised = false;
+    float bias[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        mt[i] *= f[i];
+        if (!dead[i]) {
+            if (m[i] == -INFINITY) {
+                m[i] = mt[i];  // O and l of the row are still 0
+            } else if (mt[i] > m[i] + kRescale) {
+                alpha[i] = ex2(m[i] - mt[i]);
+                l[i] *= alpha[i];
+                m[i] = mt[i];
+                raised = true;
+            }
+        }
+        bias[i] = m[i] == -INFINITY ? 0.0f : -m[i];  // (no key yet: every exponential is 0)
+    }
+    exp_rows_f16(s, f, bias[0], bias[1], la, lb);
+    l[0] += la;
+    l[1] += lb;
+    fresh = __any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY);
+    return __any_sync(0xffffffffu, raised);
+}
+
+template <int D, int kMode>
+__global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constant__ Fp4Params P) {
+    using C = Cfg<D>;
+    constexpr uint32_t S = C::kTiles, CS = C::kCodeStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_q = smem_u32(smem), s_k = s_q + C::kTile, s_v = s_k + S * C::kTile;
+    uint8_t* const codes = smem + C::kTile * (1 + 2 * S);
+    Shared& sh = *reinterpret_cast<Shared*>(smem + C::kData);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    int32_t* const status = P.b.status;
+
+    if (threadIdx.x == kThreads - 1) {
+        for (int x = 0; x < 3; ++x) {
+            mbar_init(smem_u32(&sh.code_full[x]), 33);
+            mbar_init(smem_u32(&sh.code_empty[x]), kUnpackWarps);
+        }
+        for (int x = 0; x < 4; ++x) {
+            mbar_init(smem_u32(&sh.k_full[x]), kUnpackWarps);
+            mbar_init(smem_u32(&sh.v_full[x]), kUnpackWarps);
+            mbar_init(smem_u32(&sh.k_empty[x]), 1);
+            mbar_init(smem_u32(&sh.v_empty[x]), 1);
+        }
+        for (int x = 0; x < kSBuf; ++x) {
+            mbar_init(smem_u32(&sh.s_full[x]), 1);
+            mbar_init(smem_u32(&sh.p_full[x]), 32 * kSoftmaxWarps);
+            mbar_init(smem_u32(&sh.pv_done[x]), 1);
+        }
+        mbar_init(smem_u32(&sh.q_empty), 1);
+        mbar_init(smem_u32(&sh.o_free), 32 * kStoreWarps);
+        mbar_init(smem_u32(&sh.ml_full), 32 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sh.ml_empty), 32 * kStoreWarps);
+        mbar_init(smem_u32(&sh.mma_done), 2);
+        for (int x = 0; x < kDesc; ++x) {
+            mbar_init(smem_u32(&sh.q_ready[x]), kUnpackWarps);
+            mbar_init(smem_u32(&sh.seg_full[x]), 1);
+            mbar_init(smem_u32(&sh.seg_empty[x]), kReaders);
+        }
+        fence_mbar_init();
+    }
+    launch_dependents();
+    wait_primary();
+    if (threadIdx.x == kThreads - 1) {
+        P.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+        sh.watch.busy = 0;
+        // a block of this launch (or an unread earlier one) timed out: abandon
+        sh.watch.abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
+    }
+    // this block's run (the scratch is in the data area, which is free here)
+    Fp4Run run;
+    if (!Fp4Work<kWide, kRowCost, false>{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run))
+        return;
+    __syncthreads();
+    const bool abandoned = sh.watch.abort != 0;
+    if (warp == kMmaQK && !abandoned) {
+        __syncwarp();
+        tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    // what was written there by ordinary stores makes room for bulk copies
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (abandoned) return;
+    const uint32_t tmem = sh.tmem_base;
+
+    // Segment k, for the warps that read descriptors (null: no more); they hand
+    // it back when they are through with it.
+    auto next_segment = [&](uint32_t k, bool& ok) -> const Fp4Segment* {
+        if (!wait_warp(smem_u32(&sh.seg_full[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status)) {
+            ok = false;
+            return nullptr;
+        }
+        const Fp4Segment* sg = &sh.seg[k % kDesc];
+        return sg->n >= 0 ? sg : nullptr;
+    };
+    auto hand_back = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[k % kDesc]));
+    };
+    // No product may still be running when TMEM is freed.
+    auto finish_products = [&](bool ok) {
+        if (elect_one()) mma_commit(smem_u32(&sh.mma_done));
+        __syncwarp();
+        if (!ok || !wait_warp(smem_u32(&sh.mma_done), 0, &sh.watch, status)) {
+            if (ok && lane == 0) set_abort(&sh.watch, status);
+            paged_drain(smem_u32(&sh.mma_done), 0, status);
+        }
+        __syncwarp();
+    };
+
+    if (warp < kSoftmax0) {
+        if (warp == kLoad) {
+            // -------------------------------------------------------- segments, codes and scales
+            Fp4Walk<kWide, kRowCost, false> walk(P, run, sh.start);
+            Fp4Segment sg;
+            uint32_t k = 0, g = 0;  // segments and tiles so far
+            bool ok = true;
+            const int32_t page = P.b.page, N = 128 / page, per_window = page >> 2;
+            const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
+            const uint32_t ring = smem_u32(codes);
+            constexpr int kCopies = C::kScales / 512, kBytes = D / 16;  // of scales, 16 bytes a lane; a row's
+            const int32_t page_scales = page * kBytes;
+            int32_t sc_page[kCopies], sc_at[kCopies];
+#pragma unroll
+            for (int x = 0; x < kCopies; ++x) {
+                sc_page[x] = (x * 512 + lane * 16) / page_scales;
+                sc_at[x] = (x * 512 + lane * 16) % page_scales;
+            }
+            for (; ok && walk.open(sg); walk.advance()) {
+                if (!wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    sh.seg[k % kDesc] = sg;
+                    mbar_arrive(smem_u32(&sh.seg_full[k % kDesc]));
+                    walk.note(sg);
+                }
+                __syncwarp();
+                ++k;
+                const int32_t j0 = sg.j0, j1 = j0 + sg.n;
+                const int32_t* table = P.b.table + (int64_t)walk.s * P.b.max_pages;
+                // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
+                // sequence's end)
+                auto fetch = [&](int32_t w0) -> int32_t {
+                    const int32_t j = w0 + lane_tile;
+                    if (j >= j1) return -1;
+                    const int32_t pg = (j < sg.ns ? j : sg.lo + j - sg.ns) * N + lane_page;
+                    if (pg * page >= sg.kl) return -1;
+                    int32_t id = table[pg];
+                    if (id < 0 || id >= P.b.n_pages) {
+                        raise_status(status, BSA_ERR_BOUNDS);
+                        id = 0;  // (this row's result is unspecified)
+                    }
+                    return (id * P.H_kv + sg.kvh) * page;
+                };
+                int32_t w0 = j0, cur = fetch(j0), nxt = fetch(j0 + per_window);
+                for (int32_t j = j0; j < j1; ++j, ++g) {
+                    if (j >= w0 + per_window) {
+                        w0 += per_window;
+                        cur = nxt;
+                        nxt = fetch(w0 + per_window);
+                    }
+                    const bool mine = lane_tile == j - w0 && cur >= 0;
+                    const int32_t held = __popc(__ballot_sync(0xffffffffu, mine));
+                    const uint32_t at = g % CS;
+                    if (!wait_warp(smem_u32(&sh.code_empty[at]), ((g / CS) & 1u) ^ 1u, &sh.watch, status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&sh.code_full[at]), to = ring + at * C::kStage;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(held * page * D));
+                    __syncwarp();
+                    if (mine) {
+                        bulk_load(to + lane_page * page * (D / 2), P.k + (int64_t)cur * (D / 2), page * (D / 2), bar);
+                        bulk_load(to + C::kCodes + lane_page * page * (D / 2), P.v + (int64_t)cur * (D / 2), page * (D / 2), bar);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < kCopies; ++x) {
+                        const int32_t row = __shfl_sync(0xffffffffu, cur, (j - w0) * N + sc_page[x]);
+                        if (row >= 0) {
+                            const int64_t from = (int64_t)row * kBytes + sc_at[x];
+                            cp_async16(to + 2 * C::kCodes + x * 512 + lane * 16, P.k_scale + from);
+                            cp_async16(to + 2 * C::kCodes + C::kScales + x * 512 + lane * 16, P.v_scale + from);
+                        }
+                    }
+                    cp_async_arrive_noinc(bar);
+                }
+            }
+            if (ok && wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
+                if (lane == 0) {
+                    sh.seg[k % kDesc].n = -1;
+                    mbar_arrive(smem_u32(&sh.seg_full[k % kDesc]));
+                }
+            } else {
+                ok = false;
+            }
+            if (!ok && lane == 0) set_abort(&sh.watch, status);
+            // every issued copy must land before the block exits
+            cp_async_wait_all();
+            if (lane == 0)
+                for (uint32_t x = g > CS ? g - CS : 0; x < g; ++x)
+                    paged_drain(smem_u32(&sh.code_full[x % CS]), (x / CS) & 1u, status);
+            __syncwarp();
+        } else if (warp == kMmaQK) {
+            // -------------------------------------------------------- S = Q K^T
+            // (the whole warp walks the schedule; one elected lane issues a tile's MMAs
+            // and their commits)
+            const uint64_t dq = smem_desc_sw128(s_q, 16, 1024);
+            const uint64_t dk = smem_desc_sw128(s_k, 16, 1024);
+            uint32_t g = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const Fp4Segment* sp = next_segment(k, ok);
+                if (sp == nullptr) break;
+                const int32_t n = sp->n;
+                hand_back(k);
+                if (n == 0) continue;
+                ok = wait_warp(smem_u32(&sh.q_ready[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status);
+                for (int32_t j = 0; j < n && ok; ++j, ++g) {
+                    // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
+                    if (g >= kSBuf) ok = wait_warp(smem_u32(&sh.pv_done[g % kSBuf]), (g / kSBuf - 1u) & 1u, &sh.watch, status);
+                    const uint32_t slot = g % S;
+                    ok = ok && wait_warp(smem_u32(&sh.k_full[slot]), (g / S) & 1u, &sh.watch, status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ks = dk + (uint64_t)((slot * C::kTile) >> 4);
+                    const uint32_t d_col = (g % kSBuf) * 128u;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+                            mma_ss(tmem + d_col, dq + off, ks + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(smem_u32(&sh.s_full[g % kSBuf]));
+                        mma_commit(smem_u32(&sh.k_empty[slot]));
+                        if (j == n - 1) mma_commit(smem_u32(&sh.q_empty));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) set_abort(&sh.watch, status);
+            finish_products(ok);
+        } else if (warp == kMmaPV) {
+            // -------------------------------------------------------- O += P V
+            const uint64_t dv = smem_desc_sw128(s_v, kBox, 1024);
+            uint32_t g = 0, segs = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const Fp4Segment* sp = next_segment(k, ok);
+                if (sp == nullptr) break;
+                const int32_t n = sp->n;
+                hand_back(k);
+                if (n == 0) continue;
+                for (int32_t j = 0; j < n && ok; ++j, ++g) {
+                    const uint32_t slot = g % S;
+                    ok = wait_warp(smem_u32(&sh.v_full[slot]), (g / S) & 1u, &sh.watch, status) &&
+                         wait_warp(smem_u32(&sh.p_full[g % kSBuf]), (g / kSBuf) & 1u, &sh.watch, status);
+                    // a segment's first product overwrites O: the epilogue before must have read it
+                    if (ok && j == 0 && segs > 0) ok = wait_warp(smem_u32(&sh.o_free), (segs - 1u) & 1u, &sh.watch, status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vs = dv + (uint64_t)((slot * C::kTile) >> 4);
+                    const uint32_t p_col = (g % kSBuf) * 128u;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ts(tmem + kColO, tmem + p_col + kk * 8, vs + (uint64_t)(kk * 2048 >> 4), C::kIdescPV,
+                                   (j > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(smem_u32(&sh.pv_done[g % kSBuf]));
+                        mma_commit(smem_u32(&sh.v_empty[slot]));
+                    }
+                    __syncwarp();
+                }
+                ++segs;
+            }
+            if (!ok && lane == 0) set_abort(&sh.watch, status);
+            finish_products(ok);
+        }
+    } else if (warp >= kUnpack0) {
+        // ------------------------------------------------------------ fp16 tiles of K, Q and V
+        const int uw = warp - kUnpack0;
+        uint32_t g = 0, nq = 0;
+        bool ok = true;
+        // 32 keys of a tile by this warp, 32 values (a piece) by a lane at a time; pieces of the upper
+        // box start with the other half of their chunks, so that no two lanes meet in a bank
+        constexpr int PR = D / 32;  // pieces of a row
+        const int piece = lane % PR;
+        const uint32_t upper = D == 128 ? (uint32_t)(piece & 2) : 0u;
+        const uint32_t box = (uint32_t)(piece >> 1) * kBox, chunk0 = (uint32_t)(piece & 1) * 4;
+        auto unpack = [&](const uint8_t* from, const uint8_t* scales, uint32_t to) {
+#pragma unroll
+            for (int x = 0; x < PR; ++x) {
+                const int row = 32 * uw + x * (32 / PR) + lane / PR;
+                uint4 w = *reinterpret_cast<const uint4*>(from + row * (D / 2) + piece * 16);
+                const __half2 s2 = fp4_scales(*reinterpret_cast<const uint16_t*>(scales + row * (D / 16) + piece * 2));
+                const __half2 s_lo = __low2half2(s2), s_hi = __high2half2(s2);
+                if (upper) w = make_uint4(w.z, w.w, w.x, w.y);
+                const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t line = to + box + row * 128;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t chunk = chunk0 + ((uint32_t)y ^ upper);
+                    const __half2 sc = ((y >> 1) ^ (upper >> 1)) != 0u ? s_hi : s_lo;
+                    __half2 v[4];
+                    fp4_levels(wd[y], v);
+                    store16(line + ((chunk ^ (uint32_t)(row & 7)) << 4), bits(__hmul2(v[0], sc)), bits(__hmul2(v[1], sc)),
+                            bits(__hmul2(v[2], sc)), bits(__hmul2(v[3], sc)));
+                }
+            }
+        };
+        auto publish = [&](uint64_t* bar) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(bar));
+        };
+        for (uint32_t k = 0; ok; ++k) {
+            const Fp4Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const Fp4Segment sg = *sp;
+            for (int32_t j = 0; j < sg.n && ok; ++j, ++g) {
+                const uint32_t cs = g % CS, slot = g % S;
+                const uint8_t* at = codes + cs * C::kStage;
+                ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
+                     wait_warp(smem_u32(&sh.k_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
+                if (!ok) break;
+                unpack(at, at + 2 * C::kCodes, s_k + slot * C::kTile);
+                publish(&sh.k_full[slot]);
+                if (j == 0) {
+                    // the segment's queries: D / 8 lanes a row, eight values each
+                    // (the segment before is done with the query tile's place)
+                    if (nq > 0) ok = wait_warp(smem_u32(&sh.q_empty), (nq - 1u) & 1u, &sh.watch, status);
+                    if (!ok) break;
+                    ++nq;
+                    constexpr int kLanes = D / 8, kAbreast = 32 / kLanes;
+                    const int c = lane % kLanes;
+                    const float kg = (P.k_gain != nullptr ? P.k_gain[sg.kvh] : 1.0f) * P.scale_log2;
+#pragma unroll 4
+                    for (int x = 0; x < 32 / kAbreast; ++x) {
+                        const int row = 32 * uw + x * kAbreast + lane / kLanes;
+                        const bool live = row < sg.nrows;
+                        const int32_t z = sg.row0 + (live ? row : 0), tok = z / P.group, head = z - tok * P.group;
+                        uint4 raw = *reinterpret_cast<const uint4*>(P.q + ((int64_t)sg.q0 + tok) * P.q_stride +
+                                                                    (int64_t)(sg.kvh * P.group + head) * D + 8 * c);
+                        if (!live) raw = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
+                        uint32_t top = 0u;  // the largest exponent field of a finite value
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t e0 = wd[y] >> 7 & 0xffu, e1 = wd[y] >> 23 & 0xffu;
+                            top = max(top, max(e0 == 0xffu ? 0u : e0, e1 == 0xffu ? 0u : e1));
+                        }
+#pragma unroll
+                        for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const int32_t e = max((int32_t)top - 127, -100) - 14;
+                        const float up = __int_as_float((127 - e) << 23);
+                        uint32_t h[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            h[y] = bits(__floats2half2_rn(__uint_as_float(wd[y] << 16) * up, __uint_as_float(wd[y] & 0xffff0000u) * up));
+                        store16(s_q + (c >> 3) * kBox + row * 128 + ((uint32_t)((c & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                        // (never 0: a hidden score is -inf, and times 0 it would be NaN)
+                        if (c == 0) sh.fac[k % kDesc][row] = fmaxf(__int_as_float((127 + e) << 23) * kg, FLT_MIN);
+                    }
+                    publish(&sh.q_ready[k % kDesc]);
+                }
+                ok = wait_warp(smem_u32(&sh.v_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
+                if (!ok) break;
+                unpack(at + C::kCodes, at + 2 * C::kCodes + C::kScales, s_v + slot * C::kTile);
+                publish(&sh.v_full[slot]);
+                if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
+            }
+            if (sg.n == 0) publish(&sh.q_ready[k % kDesc]);  // (its phases go with the descriptors')
+            hand_back(k);
+        }
+        if (!ok && lane == 0) set_abort(&sh.watch, status);
+    } else if (warp < kStore0) {
+        // ------------------------------------------------------------ softmax
+        const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
+        const int half = (warp - kSoftmax0) >> 2;
+        const int row[2] = {qd * 32 + half * 16 + (lane >> 2), qd * 32 + half * 16 + (lane >> 2) + 8};
+        const uint32_t t_base = tmem + ((uint32_t)(qd * 32 + half * 16) << 16);
+        const int c0 = 2 * (lane & 3);  // this thread's columns: c0 + 8 k, c0 + 8 k + 1
+        uint32_t gb0 = 0, segs = 0;  // key tiles, segments with a key so far
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const Fp4Segment* sg = next_segment(k, ok);
+            if (sg == nullptr) break;
+            const int32_t n = sg->n, j0 = sg->j0, lo_t = sg->lo, ns = sg->ns;
+            if (n == 0) {
+                hand_back(k);
+                continue;
+            }
+            const bool dead[2] = {row[0] >= sg->nrows, row[1] >= sg->nrows};
+            // Row x sees keys lo[x] .. hi[x] - 1 and 0 .. sk[x] - 1.  Key tiles from
+            // some_lo on and below some_hi, or below some_sk, are seen by some row of this
+            // warp, from all_lo on and below all_hi, or below all_sk, whole by every row.
+            int32_t hi[2], lo[2] = {0, 0}, sk[2] = {0, 0};
+            int32_t some_hi, all_hi, some_lo = 0, all_lo = 0, some_sk = 0, all_sk = 0;
+            {
+                const int32_t kl = sg->kl, p0 = sg->pos_of0, row0 = sg->row0, most = sg->nrows - 1;
+                // this warp's first and last row
+                const int32_t ra = qd * 32 + half * 16, rb = min(ra + 15, most);
+                const int32_t pa = p0 + (row0 + min(ra, most)) / P.group, pb = p0 + (row0 + rb) / P.group;
+                auto end = [&](int32_t p) -> int32_t { return P.causal ? min(kl, p + 1) : kl; };
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int32_t p = p0 + (row0 + min(row[x], most)) / P.group;
+                    hi[x] = end(p);
+                    if constexpr (kMode == kWindow) {
+                        lo[x] = p - P.window + 1;
+                        sk[x] = min(P.sinks, hi[x]);
+                    }
+                }
+                const bool some = ra <= most;
+                all_hi = max(end(pa), 0) >> 7;
+                some_hi = some ? (max(end(pb), 0) + 127) >> 7 : 0;
+                if constexpr (kMode == kWindow) {
+                    all_lo = (max(pb - P.window + 1, 0) + 127) >> 7;
+                    some_lo = max(pa - P.window + 1, 0) >> 7;
+                    all_sk = min(P.sinks, max(end(pa), 0)) >> 7;
+                    some_sk = some ? (min(P.sinks, max(end(pb), 0)) + 127) >> 7 : 0;
+                }
+            }
+            if (__any_sync(0xffffffffu, !paged_wait(smem_u32(&sh.q_ready[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status))) {
+                ok = false;
+                break;
+            }
+            const float fac[2] = {sh.fac[k % kDesc][row[0]], sh.fac[k % kDesc][row[1]]};
+            hand_back(k);
+            float m[2] = {dead[0] ? 0.0f : -INFINITY, dead[1] ? 0.0f : -INFINITY};
+            float l[2] = {0.0f, 0.0f};  // this thread's share of each row
+            bool fresh = true;
+            for (int32_t j = 0; j < n; ++j) {
+                const uint32_t gb = gb0 + (uint32_t)j;
+                const uint32_t sbuf = (gb % kSBuf) * 128u;
+                int32_t kt;
+                if constexpr (kMode == kWindow) kt = j0 + j < ns ? j0 + j : lo_t + j0 + j - ns;
+                else kt = j0 + j;
+                const int32_t kb = kt * 128;
+                // bit 2 kk + e of vis[x]: row x sees this thread's column c0 + 8 kk + e
+                uint32_t vis[2] = {~0u, ~0u};
+                const bool visible = (kt < some_hi && kt >= some_lo) || kt < some_sk;
+                const bool masked = visible && !((kt < all_hi && kt >= all_lo) || kt < all_sk);
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        vis[x] = columns_below(hi[x] - kb - c0);
+                        if constexpr (kMode == kWindow)
+                            vis[x] = (vis[x] & ~columns_below(lo[x] - kb - c0)) | columns_below(sk[x] - kb - c0);
+                    }
+                }
+                const bool wt = paged_wait(smem_u32(&sh.s_full[gb % kSBuf]), (gb / kSBuf) & 1u, &sh.watch, status);
+                // (a failure elsewhere in the block or in another one ends this wait too)
+                if (__any_sync(0xffffffffu, !wt)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (!visible) {
+                    // no row of this warp sees a key of the tile: P = 0
+                    store_p_zero(t_base + sbuf);
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sh.p_full[gb % kSBuf]));
+                    continue;
+                }
+                uint32_t sc[64];
+                auto load_s = [&]() {
+                    tmem_ld16x256_x16(t_base + sbuf, sc);
+                    tmem_wait_ld();
+                    if (masked) {
+                        const uint32_t ninf = __float_as_uint(-INFINITY);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int kk = 0; kk < 16; ++kk)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    sc[4 * kk + 2 * x + e] = (vis[x] >> (2 * kk + e)) & 1u ? sc[4 * kk + 2 * x + e] : ninf;
+                    }
+                };
+                load_s();
+                float alpha[2];
+                const bool raised = softmax_rows(sc, dead, fac, fresh, m, l, alpha, load_s);
+                tmem_st16x128_x16(t_base + sbuf, sc);
+                if (raised) {
+                    // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
+                    const uint32_t pv = gb - 1u;
+                    const bool wv = paged_wait(smem_u32(&sh.pv_done[pv % kSBuf]), (pv / kSBuf) & 1u, &sh.watch, status);
+                    if (__any_sync(0xffffffffu, !wv)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    scale_o_rows<D>(t_base + kColO, alpha[0], alpha[1]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[gb % kSBuf]));
+            }
+            if (!ok) break;
+            // maxima and sums of the rows to the storing warps
+            const float la = row_sum4(l[0]), lb = row_sum4(l[1]);
+            if (__any_sync(0xffffffffu, !paged_wait(smem_u32(&sh.ml_empty), (segs & 1u) ^ 1u, &sh.watch, status))) {
+                ok = false;
+                break;
+            }
+            if ((lane & 3) == 0) {
+                sh.ml[row[0]] = make_float2(m[0], la);
+                sh.ml[row[1]] = make_float2(m[1], lb);
+            }
+            mbar_arrive(smem_u32(&sh.ml_full));
+            ++segs;
+            gb0 += (uint32_t)n;
+        }
+        if (!ok && lane == 0) set_abort(&sh.watch, status);
+    } else {
+        // ------------------------------------------------------------ O and LSE of a segment
+        // one thread per row
+        const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
+        const int row = qd * 32 + lane;
+        const uint32_t t_row = tmem + ((uint32_t)(qd * 32) << 16) + kColO;
+        uint32_t g = 0, segs = 0;
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const Fp4Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const int32_t n = sp->n, part_slot = sp->part, kvh = sp->kvh, nrows = sp->nrows;
+            const bool dead = row >= nrows;
+            const int32_t x = sp->row0 + (dead ? 0 : row), tok = x / P.group;
+            const int64_t at = ((int64_t)sp->q0 + tok) * P.H + kvh * P.group + (x - tok * P.group);
+            hand_back(k);
+            __nv_bfloat16* orow = P.o + at * D;
+            if (n == 0) {
+                // no key at all: O = 0, LSE = -inf
+                if (!dead) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(orow + c) = make_uint4(0, 0, 0, 0);
+                    P.lse[at] = -INFINITY;
+                }
+                continue;
+            }
+            const uint32_t pv = g + (uint32_t)n - 1u;
+            // (the last product is the segment's: the next one waits for o_free)
+            ok = wait_warp(smem_u32(&sh.ml_full), segs & 1u, &sh.watch, status) &&
+                 wait_warp(smem_u32(&sh.pv_done[pv % kSBuf]), (pv / kSBuf) & 1u, &sh.watch, status);
+            if (!ok) break;
+            const float2 ml = sh.ml[row];
+            mbar_arrive(smem_u32(&sh.ml_empty));
+            tc_fence_after();
+            // 1 / l; 0 for a row without a key, NaN where l is
+            const float inv = (ml.y == 0.0f ? 0.0f : 1.0f / ml.y) * (P.v_gain != nullptr ? P.v_gain[kvh] : 1.0f);
+            const int64_t part = (int64_t)max(part_slot, 0) * kWide + row;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                __syncwarp();  // the lanes without a row skip the stores below
+                tmem_ld32(t_row + c, o);
+                tmem_wait_ld();
+                if (dead) continue;
+                if (part_slot < 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+                        reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh.o_free));
+            if (!dead) {
+                if (part_slot < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kFp4Ln2;
+                else P.part_ml[part] = ml;
+            }
+            g += (uint32_t)n;
+            ++segs;
+        }
+        if (!ok && lane == 0) set_abort(&sh.watch, status);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaQK) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, int kMode>
+bsa_status launch_d(const Fp4Params& P, cudaStream_t stream) {
+    constexpr size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
+    static_assert(smem <= 232448, "shared memory of a thread block");
+    static_assert(Cfg<D>::kData >= 3 * sizeof(int32_t) * 16384 || D == 64, "room for the sequences");
+    static DeviceSetup setup;
+    static int sms[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+    const bool ready = setup.once(dev, [&] {
+        return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+               cudaFuncSetAttribute(k_fp4_prompt<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) ==
+                   cudaSuccess;
+    });
+    if (!ready) return BSA_ERR_CUDA;
+    const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
+    constexpr int kRows = kFp4JoinThreads / (D / 4);
+    if (launch_chained(k_fp4_prompt<D, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P) != cudaSuccess ||
+        launch_chained(k_fp4_join<D, kWide, kRows>, dim3((unsigned)grid, kWide / kRows), kFp4JoinThreads, 0, stream, P) != cudaSuccess)
+        return BSA_ERR_CUDA;
+    return BSA_OK;
+}
+
+}  // namespace
+
+bsa_status launch_fp4_prompt(const Fp4Params& P, int32_t D, cudaStream_t stream) {
+    if (P.window > 0) return D == 128 ? launch_d<128, kWindow>(P, stream) : launch_d<64, kWindow>(P, stream);
+    return D == 128 ? launch_d<128, kPlain>(P, stream) : launch_d<64, kPlain>(P, stream);
+}
+
+}  // namespace bsa
