@@ -39,11 +39,11 @@ constexpr float kSumLimit = 32768.0f;                     // 2^15, see softmax_r
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 384;
-constexpr int kLoad = 0, kMmaQK = 1, kMmaPV = 2, kSoftmax0 = 4, kSoftmaxWarps = 8, kStore0 = 12, kStoreWarps = 4,
-              kUnpack0 = 16, kUnpackWarps = 4;
+constexpr int kLoad = 0, kMmaQK = 1, kMmaPV = 2, kSoftmax0 = 4, kSoftmaxWarps = 8, kUnpackV0 = 12, kUnpackK0 = 16,
+              kUnpackWarps = 4;
 constexpr int kThreads = 32 * 20;
 constexpr int kDesc = 4;                                  // segment descriptors in flight
-constexpr int kReaders = 2 + kSoftmaxWarps + kStoreWarps + kUnpackWarps;  // warps that read a descriptor
+constexpr int kReaders = 2 + kSoftmaxWarps + 2 * kUnpackWarps;  // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 fp16
 
 enum { kPlain = 0, kWindow = 1 };
@@ -83,7 +83,8 @@ struct Shared {
 
 __device__ __forceinline__ uint32_t bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ void store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    // (no "memory": what is loaded next need not wait for it; publish() orders it before what reads it)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, const int32_t* status) {
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     if (threadIdx.x == kThreads - 1) {
         for (int x = 0; x < 3; ++x) {
             mbar_init(smem_u32(&sh.code_full[x]), 33);
-            mbar_init(smem_u32(&sh.code_empty[x]), kUnpackWarps);
+            mbar_init(smem_u32(&sh.code_empty[x]), 2 * kUnpackWarps);
         }
         for (int x = 0; x < 4; ++x) {
             mbar_init(smem_u32(&sh.k_full[x]), kUnpackWarps);
@@ -204,12 +205,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             mbar_init(smem_u32(&sh.pv_done[x]), 1);
         }
         mbar_init(smem_u32(&sh.q_empty), 1);
-        mbar_init(smem_u32(&sh.o_free), 32 * kStoreWarps);
+        mbar_init(smem_u32(&sh.o_free), 32 * kUnpackWarps);
         mbar_init(smem_u32(&sh.ml_full), 32 * kSoftmaxWarps);
-        mbar_init(smem_u32(&sh.ml_empty), 32 * kStoreWarps);
+        mbar_init(smem_u32(&sh.ml_empty), 32 * kUnpackWarps);
         mbar_init(smem_u32(&sh.mma_done), 2);
         for (int x = 0; x < kDesc; ++x) {
-            mbar_init(smem_u32(&sh.q_ready[x]), kUnpackWarps);
+            mbar_init(smem_u32(&sh.q_ready[x]), 2 * kUnpackWarps);
             mbar_init(smem_u32(&sh.seg_full[x]), 1);
             mbar_init(smem_u32(&sh.seg_empty[x]), kReaders);
         }
@@ -437,35 +438,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             if (!ok && lane == 0) set_abort(&sh.watch, status);
             finish_products(ok);
         }
-    } else if (warp >= kUnpack0) {
-        // ------------------------------------------------------------ fp16 tiles of K, Q and V
-        const int uw = warp - kUnpack0;
-        uint32_t g = 0, nq = 0;
-        bool ok = true;
-        // 32 keys of a tile by this warp, 32 values (a piece) by a lane at a time; pieces of the upper
-        // box start with the other half of their chunks, so that no two lanes meet in a bank
-        constexpr int PR = D / 32;  // pieces of a row
-        const int piece = lane % PR;
-        const uint32_t upper = D == 128 ? (uint32_t)(piece & 2) : 0u;
-        const uint32_t box = (uint32_t)(piece >> 1) * kBox, chunk0 = (uint32_t)(piece & 1) * 4;
+    } else if (warp >= kUnpackV0) {
+        // ------------------------------------------------------------ fp16 tiles of K and Q, of V; O and LSE
+        const int uw = warp & 3;
+        // 32 keys of a tile by this warp, 32 values (a piece) by a lane at a time; eight lanes store to one
+        // box and eight places of its lines (no bank conflicts)
+        constexpr int PR = D / 32, kRowsOnce = 32 / PR;  // pieces of a row, rows at a time (a multiple of 8)
+        const int piece = D == 128 ? (lane & 1) + (lane >> 2 & 2) : lane & 1;
+        const int row0 = 32 * uw + (D == 128 ? (lane >> 1 & 3) + (lane >> 2 & 4) : lane >> 1);
+        const uint32_t from_at = row0 * (D / 2) + piece * 16, scale_at = row0 * (D / 16) + piece * 2;
+        uint32_t to_at[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            to_at[y] = (uint32_t)(piece >> 1) * kBox + row0 * 128 + ((uint32_t)((4 * (piece & 1) + y) ^ (row0 & 7)) << 4);
         auto unpack = [&](const uint8_t* from, const uint8_t* scales, uint32_t to) {
+            uint4 w[PR];
+            uint32_t s2[PR];
 #pragma unroll
             for (int x = 0; x < PR; ++x) {
-                const int row = 32 * uw + x * (32 / PR) + lane / PR;
-                uint4 w = *reinterpret_cast<const uint4*>(from + row * (D / 2) + piece * 16);
-                const __half2 s2 = fp4_scales(*reinterpret_cast<const uint16_t*>(scales + row * (D / 16) + piece * 2));
-                const __half2 s_lo = __low2half2(s2), s_hi = __high2half2(s2);
-                if (upper) w = make_uint4(w.z, w.w, w.x, w.y);
-                const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
-                const uint32_t line = to + box + row * 128;
+                w[x] = *reinterpret_cast<const uint4*>(from + from_at + x * kRowsOnce * (D / 2));
+                s2[x] = *reinterpret_cast<const uint16_t*>(scales + scale_at + x * kRowsOnce * (D / 16));
+            }
+#pragma unroll
+            for (int x = 0; x < PR; ++x) {
+                const __half2 both = fp4_scales(s2[x]);
+                const __half2 sc[2] = {__low2half2(both), __high2half2(both)};
+                const uint32_t wd[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const uint32_t chunk = chunk0 + ((uint32_t)y ^ upper);
-                    const __half2 sc = ((y >> 1) ^ (upper >> 1)) != 0u ? s_hi : s_lo;
                     __half2 v[4];
                     fp4_levels(wd[y], v);
-                    store16(line + ((chunk ^ (uint32_t)(row & 7)) << 4), bits(__hmul2(v[0], sc)), bits(__hmul2(v[1], sc)),
-                            bits(__hmul2(v[2], sc)), bits(__hmul2(v[3], sc)));
+                    store16(to + to_at[y] + x * kRowsOnce * 128, bits(__hmul2(v[0], sc[y >> 1])), bits(__hmul2(v[1], sc[y >> 1])),
+                            bits(__hmul2(v[2], sc[y >> 1])), bits(__hmul2(v[3], sc[y >> 1])));
                 }
             }
         };
@@ -474,67 +478,189 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(bar));
         };
-        for (uint32_t k = 0; ok; ++k) {
-            const Fp4Segment* sp = next_segment(k, ok);
-            if (sp == nullptr) break;
-            const Fp4Segment sg = *sp;
-            for (int32_t j = 0; j < sg.n && ok; ++j, ++g) {
-                const uint32_t cs = g % CS, slot = g % S;
-                const uint8_t* at = codes + cs * C::kStage;
-                ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
-                     wait_warp(smem_u32(&sh.k_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
-                if (!ok) break;
-                unpack(at, at + 2 * C::kCodes, s_k + slot * C::kTile);
-                publish(&sh.k_full[slot]);
-                if (j == 0) {
-                    // the segment's queries: D / 8 lanes a row, eight values each
-                    // (the segment before is done with the query tile's place)
-                    if (nq > 0) ok = wait_warp(smem_u32(&sh.q_empty), (nq - 1u) & 1u, &sh.watch, status);
-                    if (!ok) break;
-                    ++nq;
-                    constexpr int kLanes = D / 8, kAbreast = 32 / kLanes;
-                    const int c = lane % kLanes;
-                    const float kg = (P.k_gain != nullptr ? P.k_gain[sg.kvh] : 1.0f) * P.scale_log2;
-#pragma unroll 4
-                    for (int x = 0; x < 32 / kAbreast; ++x) {
-                        const int row = 32 * uw + x * kAbreast + lane / kLanes;
-                        const bool live = row < sg.nrows;
-                        const int32_t z = sg.row0 + (live ? row : 0), tok = z / P.group, head = z - tok * P.group;
-                        uint4 raw = *reinterpret_cast<const uint4*>(P.q + ((int64_t)sg.q0 + tok) * P.q_stride +
-                                                                    (int64_t)(sg.kvh * P.group + head) * D + 8 * c);
-                        if (!live) raw = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
-                        uint32_t top = 0u;  // the largest exponent field of a finite value
+        // A segment's queries: D / 8 lanes a row, eight values each; sixteen rows by this warp (loaded
+        // ahead, put in place when the segment before is done with the query tile's place)
+        constexpr int kLanes = D / 8, kAbreast = 32 / kLanes, kLot = 16 / kAbreast;
+        const int qc = lane % kLanes, q_row = 32 * uw + (warp >= kUnpackK0 ? 0 : 16) + lane / kLanes;
+        const uint32_t by_group = (65536u + P.group - 1u) / P.group;  // x / group = x by_group >> 16 for x < 256
+        // (a short loop, four rows under way: it runs once a segment, and unrolled it waits for its own instructions)
+        constexpr int kAhead = 4;
+        uint4 raw[kAhead];
+        const __nv_bfloat16* q_src;
+        int32_t q_head0, q_rows;
+        auto load_row = [&](int x) -> uint4 {
+            const int32_t row = q_row + x * kAbreast, z = q_head0 + row, tok = (int32_t)((uint32_t)z * by_group >> 16);
+            return x < kLot && row < q_rows ? *reinterpret_cast<const uint4*>(q_src + tok * P.q_stride + (z - tok * P.group) * D)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto fetch_rows = [&](const Fp4Segment& sg) {
+            const int32_t tok0 = sg.row0 / P.group;
+            q_head0 = sg.row0 - tok0 * P.group;
+            q_rows = sg.nrows;
+            q_src = P.q + ((int64_t)sg.q0 + tok0) * P.q_stride + (int64_t)sg.kvh * P.group * D + 8 * qc;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const uint32_t e0 = wd[y] >> 7 & 0xffu, e1 = wd[y] >> 23 & 0xffu;
-                            top = max(top, max(e0 == 0xffu ? 0u : e0, e1 == 0xffu ? 0u : e1));
-                        }
+            for (int x = 0; x < kAhead; ++x) raw[x] = load_row(x);
+        };
+        auto place_rows = [&](const Fp4Segment& sg, uint32_t k) {
+            const float kg = (P.k_gain != nullptr ? P.k_gain[sg.kvh] : 1.0f) * P.scale_log2;
+            const uint32_t line = s_q + (qc >> 3) * kBox;
+            float* fac = sh.fac[k % kDesc];
+#pragma unroll 1
+            for (int x = 0; x < kLot; ++x) {
+                const int row = q_row + x * kAbreast;
+                const uint32_t wd[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
 #pragma unroll
-                        for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const int32_t e = max((int32_t)top - 127, -100) - 14;
-                        const float up = __int_as_float((127 - e) << 23);
-                        uint32_t h[4];
+                for (int y = 0; y < kAhead - 1; ++y) raw[y] = raw[y + 1];
+                raw[kAhead - 1] = load_row(x + kAhead);
+                // the row's largest magnitude, by its bits (their order is that of the numbers)
+                uint32_t top = 0u;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            h[y] = bits(__floats2half2_rn(__uint_as_float(wd[y] << 16) * up, __uint_as_float(wd[y] & 0xffff0000u) * up));
-                        store16(s_q + (c >> 3) * kBox + row * 128 + ((uint32_t)((c & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-                        // (never 0: a hidden score is -inf, and times 0 it would be NaN)
-                        if (c == 0) sh.fac[k % kDesc][row] = fmaxf(__int_as_float((127 + e) << 23) * kg, FLT_MIN);
-                    }
-                    publish(&sh.q_ready[k % kDesc]);
-                }
-                ok = wait_warp(smem_u32(&sh.v_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
-                if (!ok) break;
-                unpack(at + C::kCodes, at + 2 * C::kCodes + C::kScales, s_v + slot * C::kTile);
-                publish(&sh.v_full[slot]);
-                if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
+                for (int y = 0; y < 4; ++y) top = __vmaxu2(top, wd[y] & 0x7fff7fffu);
+#pragma unroll
+                for (int d = 1; d < kLanes; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = max(top & 0xffffu, top >> 16) >> 7;
+                // (a row that holds an infinity or a NaN gets NaN scores, whatever its factor)
+                const int32_t e = min(max((int32_t)top - 127, -100), 127) - 14;
+                const float up = __int_as_float((127 - e) << 23);
+                uint32_t h[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    h[y] = bits(__floats2half2_rn(__uint_as_float(wd[y] << 16) * up, __uint_as_float(wd[y] & 0xffff0000u) * up));
+                store16(line + row * 128 + ((uint32_t)((qc & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                // (never 0: a hidden score is -inf, and times 0 it would be NaN)
+                if (qc == 0) fac[row] = fmaxf(__int_as_float((127 + e) << 23) * kg, FLT_MIN);
             }
-            if (sg.n == 0) publish(&sh.q_ready[k % kDesc]);  // (its phases go with the descriptors')
-            hand_back(k);
+            publish(&sh.q_ready[k % kDesc]);
+        };
+        uint32_t g = 0, segs = 0;  // tiles, segments with a key so far
+        bool ok = true;
+        if (warp >= kUnpackK0) {
+            for (uint32_t k = 0; ok; ++k) {
+                const Fp4Segment* sp = next_segment(k, ok);
+                if (sp == nullptr) break;
+                const Fp4Segment sg = *sp;
+                if (sg.n == 0) {
+                    publish(&sh.q_ready[k % kDesc]);  // (its phases go with the descriptors')
+                    hand_back(k);
+                    continue;
+                }
+                fetch_rows(sg);
+                for (int32_t j = 0; j < sg.n && ok; ++j, ++g) {
+                    const uint32_t cs = g % CS, slot = g % S;
+                    const uint8_t* at = codes + cs * C::kStage;
+                    ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
+                         wait_warp(smem_u32(&sh.k_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
+                    if (!ok) break;
+                    unpack(at, at + 2 * C::kCodes, s_k + slot * C::kTile);
+                    publish(&sh.k_full[slot]);
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
+                    if (j > 0) continue;
+                    if (segs > 0) ok = wait_warp(smem_u32(&sh.q_empty), (segs - 1u) & 1u, &sh.watch, status);
+                    if (!ok) break;
+                    place_rows(sg, k);
+                }
+                hand_back(k);
+                ++segs;
+            }
+        } else {
+            // O and LSE of a segment, one thread per row
+            const int row = uw * 32 + lane;  // (a warp reaches TMEM lanes 32 (warp % 4) .. + 31)
+            const uint32_t t_row = tmem + ((uint32_t)(uw * 32) << 16) + kColO;
+            Fp4Segment was;      // a segment whose rows are still to be stored (n > 0), ..
+            uint32_t last = 0u;  // .. and its last tile
+            was.n = 0;
+            auto address = [&](const Fp4Segment& sg) -> int64_t {
+                const int32_t x = sg.row0 + (row < sg.nrows ? row : 0), tok = x / P.group;
+                return ((int64_t)sg.q0 + tok) * P.H + sg.kvh * P.group + (x - tok * P.group);
+            };
+            auto store_rows = [&]() {
+                const bool dead = row >= was.nrows;
+                const int64_t at = address(was);
+                __nv_bfloat16* orow = P.o + at * D;
+                // (the last product is the segment's: the next one waits for o_free)
+                ok = wait_warp(smem_u32(&sh.ml_full), segs & 1u, &sh.watch, status) &&
+                     wait_warp(smem_u32(&sh.pv_done[last % kSBuf]), (last / kSBuf) & 1u, &sh.watch, status);
+                if (!ok) return;
+                const float2 ml = sh.ml[row];
+                mbar_arrive(smem_u32(&sh.ml_empty));
+                tc_fence_after();
+                // 1 / l; 0 for a row without a key, NaN where l is
+                const float inv = (ml.y == 0.0f ? 0.0f : 1.0f / ml.y) * (P.v_gain != nullptr ? P.v_gain[was.kvh] : 1.0f);
+                const int64_t part = (int64_t)max(was.part, 0) * kWide + row;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    __syncwarp();  // the lanes without a row skip the stores below
+                    tmem_ld32(t_row + c, o);
+                    tmem_wait_ld();
+                    if (dead) continue;
+                    if (was.part < 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+                            reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.o_free));
+                if (!dead) {
+                    if (was.part < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kFp4Ln2;
+                    else P.part_ml[part] = ml;
+                }
+                was.n = 0;
+                ++segs;
+            };
+            for (uint32_t k = 0; ok; ++k) {
+                const Fp4Segment* sp = next_segment(k, ok);
+                if (sp == nullptr) break;
+                const Fp4Segment sg = *sp;
+                if (sg.n == 0) {
+                    publish(&sh.q_ready[k % kDesc]);
+                    hand_back(k);
+                    // no key at all: O = 0, LSE = -inf
+                    if (row < sg.nrows) {
+                        const int64_t at = address(sg);
+#pragma unroll
+                        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(P.o + at * D + c) = make_uint4(0, 0, 0, 0);
+                        P.lse[at] = -INFINITY;
+                    }
+                    continue;
+                }
+                fetch_rows(sg);
+                // (the number of segments whose queries have been put in place: one more than are stored, if one waits)
+                const uint32_t placed = segs + (was.n > 0 ? 1u : 0u);
+                if (placed > 0) ok = wait_warp(smem_u32(&sh.q_empty), (placed - 1u) & 1u, &sh.watch, status);
+                if (!ok) break;
+                place_rows(sg, k);
+                hand_back(k);
+                for (int32_t j = 0; j < sg.n && ok; ++j, ++g) {
+                    const uint32_t cs = g % CS, slot = g % S;
+                    const uint8_t* at = codes + cs * C::kStage + C::kCodes;
+                    ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
+                         wait_warp(smem_u32(&sh.v_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
+                    if (!ok) break;
+                    unpack(at, at + C::kCodes + C::kScales, s_v + slot * C::kTile);
+                    publish(&sh.v_full[slot]);
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
+                    // the rows of the segment before, which this one's first product waits for
+                    if (j == 0 && was.n > 0) store_rows();
+                }
+                was = sg;
+                last = g - 1u;
+            }
+            if (ok && was.n > 0) store_rows();
         }
         if (!ok && lane == 0) set_abort(&sh.watch, status);
-    } else if (warp < kStore0) {
+    } else {
         // ------------------------------------------------------------ softmax
         const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
         const int half = (warp - kSoftmax0) >> 2;
@@ -672,76 +798,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             mbar_arrive(smem_u32(&sh.ml_full));
             ++segs;
             gb0 += (uint32_t)n;
-        }
-        if (!ok && lane == 0) set_abort(&sh.watch, status);
-    } else {
-        // ------------------------------------------------------------ O and LSE of a segment
-        // one thread per row
-        const int qd = warp & 3;  // a warp reaches TMEM lanes 32 (warp % 4) .. + 31
-        const int row = qd * 32 + lane;
-        const uint32_t t_row = tmem + ((uint32_t)(qd * 32) << 16) + kColO;
-        uint32_t g = 0, segs = 0;
-        bool ok = true;
-        for (uint32_t k = 0;; ++k) {
-            const Fp4Segment* sp = next_segment(k, ok);
-            if (sp == nullptr) break;
-            const int32_t n = sp->n, part_slot = sp->part, kvh = sp->kvh, nrows = sp->nrows;
-            const bool dead = row >= nrows;
-            const int32_t x = sp->row0 + (dead ? 0 : row), tok = x / P.group;
-            const int64_t at = ((int64_t)sp->q0 + tok) * P.H + kvh * P.group + (x - tok * P.group);
-            hand_back(k);
-            __nv_bfloat16* orow = P.o + at * D;
-            if (n == 0) {
-                // no key at all: O = 0, LSE = -inf
-                if (!dead) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(orow + c) = make_uint4(0, 0, 0, 0);
-                    P.lse[at] = -INFINITY;
-                }
-                continue;
-            }
-            const uint32_t pv = g + (uint32_t)n - 1u;
-            // (the last product is the segment's: the next one waits for o_free)
-            ok = wait_warp(smem_u32(&sh.ml_full), segs & 1u, &sh.watch, status) &&
-                 wait_warp(smem_u32(&sh.pv_done[pv % kSBuf]), (pv / kSBuf) & 1u, &sh.watch, status);
-            if (!ok) break;
-            const float2 ml = sh.ml[row];
-            mbar_arrive(smem_u32(&sh.ml_empty));
-            tc_fence_after();
-            // 1 / l; 0 for a row without a key, NaN where l is
-            const float inv = (ml.y == 0.0f ? 0.0f : 1.0f / ml.y) * (P.v_gain != nullptr ? P.v_gain[kvh] : 1.0f);
-            const int64_t part = (int64_t)max(part_slot, 0) * kWide + row;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                __syncwarp();  // the lanes without a row skip the stores below
-                tmem_ld32(t_row + c, o);
-                tmem_wait_ld();
-                if (dead) continue;
-                if (part_slot < 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t pk[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
-                        reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
-                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                }
-            }
-            tc_fence_before();
-            mbar_arrive(smem_u32(&sh.o_free));
-            if (!dead) {
-                if (part_slot < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kFp4Ln2;
-                else P.part_ml[part] = ml;
-            }
-            g += (uint32_t)n;
-            ++segs;
         }
         if (!ok && lane == 0) set_abort(&sh.watch, status);
     }
