@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
         constexpr int kLanes = D / 8, kAbreast = 32 / kLanes, kLot = 16 / kAbreast;
         const int qc = lane % kLanes, q_row = 32 * uw + (warp >= kUnpackK0 ? 0 : 16) + lane / kLanes;
         const uint32_t by_group = (65536u + P.group - 1u) / P.group;  // x / group = x by_group >> 16 for x < 256
-        // (a short loop, four rows under way: it runs once a segment, and unrolled it waits for its own instructions)
+        // (a short loop, four rows under way: it runs once a segment, and all unrolled it waits for its own instructions)
         constexpr int kAhead = 4;
         uint4 raw[kAhead];
         const __nv_bfloat16* q_src;
@@ -506,159 +506,143 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             const uint32_t line = s_q + (qc >> 3) * kBox;
             float* fac = sh.fac[k % kDesc];
 #pragma unroll 1
-            for (int x = 0; x < kLot; ++x) {
-                const int row = q_row + x * kAbreast;
-                const uint32_t wd[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+            for (int x0 = 0; x0 < kLot; x0 += kAhead) {
 #pragma unroll
-                for (int y = 0; y < kAhead - 1; ++y) raw[y] = raw[y + 1];
-                raw[kAhead - 1] = load_row(x + kAhead);
-                // the row's largest magnitude, by its bits (their order is that of the numbers)
-                uint32_t top = 0u;
+                for (int u = 0; u < kAhead; ++u) {
+                    const int row = q_row + (x0 + u) * kAbreast;
+                    const uint32_t wd[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                    raw[u] = load_row(x0 + u + kAhead);  // (in its own place: a move would wait for it)
+                    // the row's largest magnitude, by its bits (their order is that of the numbers)
+                    uint32_t top = 0u;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) top = __vmaxu2(top, wd[y] & 0x7fff7fffu);
+                    for (int y = 0; y < 4; ++y) top = __vmaxu2(top, wd[y] & 0x7fff7fffu);
 #pragma unroll
-                for (int d = 1; d < kLanes; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
-                top = max(top & 0xffffu, top >> 16) >> 7;
-                // (a row that holds an infinity or a NaN gets NaN scores, whatever its factor)
-                const int32_t e = min(max((int32_t)top - 127, -100), 127) - 14;
-                const float up = __int_as_float((127 - e) << 23);
-                uint32_t h[4];
+                    for (int d = 1; d < kLanes; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    top = max(top & 0xffffu, top >> 16) >> 7;
+                    // (a row that holds an infinity or a NaN gets NaN scores, whatever its factor)
+                    const int32_t e = min(max((int32_t)top - 127, -100), 127) - 14;
+                    const float up = __int_as_float((127 - e) << 23);
+                    uint32_t h[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    h[y] = bits(__floats2half2_rn(__uint_as_float(wd[y] << 16) * up, __uint_as_float(wd[y] & 0xffff0000u) * up));
-                store16(line + row * 128 + ((uint32_t)((qc & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-                // (never 0: a hidden score is -inf, and times 0 it would be NaN)
-                if (qc == 0) fac[row] = fmaxf(__int_as_float((127 + e) << 23) * kg, FLT_MIN);
+                    for (int y = 0; y < 4; ++y)
+                        h[y] = bits(__floats2half2_rn(__uint_as_float(wd[y] << 16) * up, __uint_as_float(wd[y] & 0xffff0000u) * up));
+                    store16(line + row * 128 + ((uint32_t)((qc & 7) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    // (never 0: a hidden score is -inf, and times 0 it would be NaN)
+                    if (qc == 0) fac[row] = fmaxf(__int_as_float((127 + e) << 23) * kg, FLT_MIN);
+                }
             }
             publish(&sh.q_ready[k % kDesc]);
         };
-        uint32_t g = 0, segs = 0;  // tiles, segments with a key so far
         bool ok = true;
-        if (warp >= kUnpackK0) {
-            for (uint32_t k = 0; ok; ++k) {
-                const Fp4Segment* sp = next_segment(k, ok);
-                if (sp == nullptr) break;
-                const Fp4Segment sg = *sp;
-                if (sg.n == 0) {
-                    publish(&sh.q_ready[k % kDesc]);  // (its phases go with the descriptors')
-                    hand_back(k);
-                    continue;
+        // O and LSE of a segment, one thread per row
+        const int row = uw * 32 + lane;  // (a warp reaches TMEM lanes 32 (warp % 4) .. + 31)
+        const uint32_t t_row = tmem + ((uint32_t)(uw * 32) << 16) + kColO;
+        Fp4Segment was;      // a segment whose rows are still to be stored (n > 0), ..
+        uint32_t last = 0u;  // .. and its last tile
+        was.n = 0;
+        auto address = [&](const Fp4Segment& sg) -> int64_t {
+            const int32_t x = sg.row0 + (row < sg.nrows ? row : 0), tok = x / P.group;
+            return ((int64_t)sg.q0 + tok) * P.H + sg.kvh * P.group + (x - tok * P.group);
+        };
+        uint32_t stored = 0u;  // segments whose rows have been stored
+        auto store_rows = [&]() {
+            const bool dead = row >= was.nrows;
+            const int64_t at = address(was);
+            __nv_bfloat16* orow = P.o + at * D;
+            // (the last product is the segment's: the next one waits for o_free)
+            ok = wait_warp(smem_u32(&sh.ml_full), stored & 1u, &sh.watch, status) &&
+                 wait_warp(smem_u32(&sh.pv_done[last % kSBuf]), (last / kSBuf) & 1u, &sh.watch, status);
+            if (!ok) return;
+            const float2 ml = sh.ml[row];
+            mbar_arrive(smem_u32(&sh.ml_empty));
+            tc_fence_after();
+            // 1 / l; 0 for a row without a key, NaN where l is
+            const float inv = (ml.y == 0.0f ? 0.0f : 1.0f / ml.y) * (P.v_gain != nullptr ? P.v_gain[was.kvh] : 1.0f);
+            const int64_t part = (int64_t)max(was.part, 0) * kWide + row;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                __syncwarp();  // the lanes without a row skip the stores below
+                tmem_ld32(t_row + c, o);
+                tmem_wait_ld();
+                if (dead) continue;
+                if (was.part < 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+                        reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                fetch_rows(sg);
-                for (int32_t j = 0; j < sg.n && ok; ++j, ++g) {
-                    const uint32_t cs = g % CS, slot = g % S;
-                    const uint8_t* at = codes + cs * C::kStage;
-                    ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
-                         wait_warp(smem_u32(&sh.k_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
-                    if (!ok) break;
-                    unpack(at, at + 2 * C::kCodes, s_k + slot * C::kTile);
-                    publish(&sh.k_full[slot]);
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
-                    if (j > 0) continue;
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh.o_free));
+            if (!dead) {
+                if (was.part < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kFp4Ln2;
+                else P.part_ml[part] = ml;
+            }
+            was.n = 0;
+            ++stored;
+        };
+        // K tiles and V tiles by the same instructions: eight warps run them side by side
+        const bool is_v = warp < kUnpackK0;
+        const uint32_t tiles = is_v ? s_v : s_k, codes_at = is_v ? C::kCodes : 0, scales_at = 2 * C::kCodes + (is_v ? C::kScales : 0);
+        uint64_t *const full = is_v ? sh.v_full : sh.k_full, *const empty = is_v ? sh.v_empty : sh.k_empty;
+        uint32_t g = 0, segs = 0;  // tiles, segments with a key so far
+        for (uint32_t k = 0; ok; ++k) {
+            const Fp4Segment* sp = next_segment(k, ok);
+            if (sp == nullptr) break;
+            const Fp4Segment sg = *sp;
+            if (sg.n == 0) {
+                publish(&sh.q_ready[k % kDesc]);  // (its phases go with the descriptors')
+                hand_back(k);
+                // no key at all: O = 0, LSE = -inf
+                if (is_v && row < sg.nrows) {
+                    const int64_t at = address(sg);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(P.o + at * D + c) = make_uint4(0, 0, 0, 0);
+                    P.lse[at] = -INFINITY;
+                }
+                continue;
+            }
+            fetch_rows(sg);
+            // the queries come before the first V tile, and after the first K tile
+            const int32_t q_at = is_v ? 0 : 1;
+            for (int32_t x = 0; x <= sg.n; ++x) {
+                if (x == q_at) {
+                    // (the segment before is done with the query tile's place)
                     if (segs > 0) ok = wait_warp(smem_u32(&sh.q_empty), (segs - 1u) & 1u, &sh.watch, status);
                     if (!ok) break;
                     place_rows(sg, k);
-                }
-                hand_back(k);
-                ++segs;
-            }
-        } else {
-            // O and LSE of a segment, one thread per row
-            const int row = uw * 32 + lane;  // (a warp reaches TMEM lanes 32 (warp % 4) .. + 31)
-            const uint32_t t_row = tmem + ((uint32_t)(uw * 32) << 16) + kColO;
-            Fp4Segment was;      // a segment whose rows are still to be stored (n > 0), ..
-            uint32_t last = 0u;  // .. and its last tile
-            was.n = 0;
-            auto address = [&](const Fp4Segment& sg) -> int64_t {
-                const int32_t x = sg.row0 + (row < sg.nrows ? row : 0), tok = x / P.group;
-                return ((int64_t)sg.q0 + tok) * P.H + sg.kvh * P.group + (x - tok * P.group);
-            };
-            auto store_rows = [&]() {
-                const bool dead = row >= was.nrows;
-                const int64_t at = address(was);
-                __nv_bfloat16* orow = P.o + at * D;
-                // (the last product is the segment's: the next one waits for o_free)
-                ok = wait_warp(smem_u32(&sh.ml_full), segs & 1u, &sh.watch, status) &&
-                     wait_warp(smem_u32(&sh.pv_done[last % kSBuf]), (last / kSBuf) & 1u, &sh.watch, status);
-                if (!ok) return;
-                const float2 ml = sh.ml[row];
-                mbar_arrive(smem_u32(&sh.ml_empty));
-                tc_fence_after();
-                // 1 / l; 0 for a row without a key, NaN where l is
-                const float inv = (ml.y == 0.0f ? 0.0f : 1.0f / ml.y) * (P.v_gain != nullptr ? P.v_gain[was.kvh] : 1.0f);
-                const int64_t part = (int64_t)max(was.part, 0) * kWide + row;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    __syncwarp();  // the lanes without a row skip the stores below
-                    tmem_ld32(t_row + c, o);
-                    tmem_wait_ld();
-                    if (dead) continue;
-                    if (was.part < 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t pk[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
-                            reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<uint4*>(P.part_o + part * D + c)[i] =
-                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh.o_free));
-                if (!dead) {
-                    if (was.part < 0) P.lse[at] = ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kFp4Ln2;
-                    else P.part_ml[part] = ml;
-                }
-                was.n = 0;
-                ++segs;
-            };
-            for (uint32_t k = 0; ok; ++k) {
-                const Fp4Segment* sp = next_segment(k, ok);
-                if (sp == nullptr) break;
-                const Fp4Segment sg = *sp;
-                if (sg.n == 0) {
-                    publish(&sh.q_ready[k % kDesc]);
                     hand_back(k);
-                    // no key at all: O = 0, LSE = -inf
-                    if (row < sg.nrows) {
-                        const int64_t at = address(sg);
-#pragma unroll
-                        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(P.o + at * D + c) = make_uint4(0, 0, 0, 0);
-                        P.lse[at] = -INFINITY;
-                    }
                     continue;
                 }
-                fetch_rows(sg);
-                // (the number of segments whose queries have been put in place: one more than are stored, if one waits)
-                const uint32_t placed = segs + (was.n > 0 ? 1u : 0u);
-                if (placed > 0) ok = wait_warp(smem_u32(&sh.q_empty), (placed - 1u) & 1u, &sh.watch, status);
+                const uint32_t cs = g % CS, slot = g % S;
+                const uint8_t* at = codes + cs * C::kStage;
+                ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
+                     wait_warp(smem_u32(&empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
                 if (!ok) break;
-                place_rows(sg, k);
-                hand_back(k);
-                for (int32_t j = 0; j < sg.n && ok; ++j, ++g) {
-                    const uint32_t cs = g % CS, slot = g % S;
-                    const uint8_t* at = codes + cs * C::kStage + C::kCodes;
-                    ok = wait_warp(smem_u32(&sh.code_full[cs]), (g / CS) & 1u, &sh.watch, status) &&
-                         wait_warp(smem_u32(&sh.v_empty[slot]), ((g / S) & 1u) ^ 1u, &sh.watch, status);
-                    if (!ok) break;
-                    unpack(at, at + C::kCodes + C::kScales, s_v + slot * C::kTile);
-                    publish(&sh.v_full[slot]);
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
-                    // the rows of the segment before, which this one's first product waits for
-                    if (j == 0 && was.n > 0) store_rows();
-                }
-                was = sg;
-                last = g - 1u;
+                unpack(at + codes_at, at + scales_at, tiles + slot * C::kTile);
+                publish(&full[slot]);
+                if (lane == 0) mbar_arrive(smem_u32(&sh.code_empty[cs]));
+                ++g;
+                // the rows of the segment before, which this one's first product waits for
+                if (is_v && was.n > 0) store_rows();
+                if (!ok) break;
             }
-            if (ok && was.n > 0) store_rows();
+            was = sg;
+            if (!is_v) was.n = 0;
+            last = g - 1u;
+            ++segs;
         }
+        if (ok && was.n > 0) store_rows();
         if (!ok && lane == 0) set_abort(&sh.watch, status);
     } else {
         // ------------------------------------------------------------ softmax
