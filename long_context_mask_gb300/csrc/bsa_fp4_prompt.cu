@@ -33,7 +33,10 @@ namespace bsa {
 namespace {
 
 constexpr int kWide = kFp4PromptWide;
-constexpr int32_t kRowCost = 4;
+// A row tile of n key tiles counts n + row_cost in a run.  (A causal prompt of 8192, whose blocks
+// have 8 to 50 row tiles each: 471 us with 4, 483 with 8, 501 with 12; two chunks of 2048 through a window of
+// 575, 6 key tiles to a row tile: 106, 102, 98 us.)
+constexpr int32_t row_cost(int mode) { return mode == 1 ? 12 : 4; }
 constexpr float kRescale = 8.0f;                          // raise a row's maximum when it grows by > 2^8
 constexpr float kSumLimit = 32768.0f;                     // 2^15, see softmax_rows
 constexpr int kSBuf = 3;                                  // TMEM score buffers
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     }
     // this block's run (the scratch is in the data area, which is free here)
     Fp4Run run;
-    if (!Fp4Work<kWide, kRowCost, false>{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run))
+    if (!Fp4Work<kWide, row_cost(kMode), false>{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run))
         return;
     __syncthreads();
     const bool abandoned = sh.watch.abort != 0;
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     if (warp < kSoftmax0) {
         if (warp == kLoad) {
             // -------------------------------------------------------- segments, codes and scales
-            Fp4Walk<kWide, kRowCost, false> walk(P, run, sh.start);
+            Fp4Walk<kWide, row_cost(kMode), false> walk(P, run, sh.start);
             Fp4Segment sg;
             uint32_t k = 0, g = 0;  // segments and tiles so far
             bool ok = true;
@@ -298,6 +301,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                 }
                 __syncwarp();
                 ++k;
+                // the queries, which others will wait for, into L2
+                for (int32_t row = lane; row < sg.nrows; row += 32) {
+                    const int32_t z = sg.row0 + row, tok = z / P.group, head = z - tok * P.group;
+                    const __nv_bfloat16* src = P.q + ((int64_t)sg.q0 + tok) * P.q_stride + (int64_t)(sg.kvh * P.group + head) * D;
+#pragma unroll
+                    for (int d = 0; d < D; d += 64) prefetch_l2(src + d);
+                }
                 const int32_t j0 = sg.j0, j1 = j0 + sg.n;
                 const int32_t* table = P.b.table + (int64_t)walk.s * P.b.max_pages;
                 // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
