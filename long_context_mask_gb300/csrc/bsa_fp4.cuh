@@ -37,19 +37,23 @@ __device__ __forceinline__ void fp4_levels(uint32_t w, __half2 (&x)[4]) {
     for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<__half2*>(&r[i]);
 }
 
-// The scale byte of a group whose largest magnitude is `most`, and the scale.
+// x / y rounded to nearest, given recip = 1 / y rounded to nearest: a product, and one step of the
+// remainder (Markstein's theorem, IBM J. Res. Dev. 34 (1990), makes it the rounded quotient where
+// nothing over- or underflows).  Not finite where x or the quotient is not, or recip.
+__device__ __forceinline__ float fp4_quotient(float x, float y, float recip) {
+    const float q = x * recip;
+    return fmaf(fmaf(-q, y, x), recip, q);
+}
+
+// The scale byte of a group whose largest magnitude is `most` (finite), and the scale.
 __device__ __forceinline__ uint32_t fp4_scale_of(float most, float& scale) {
     uint32_t r;
     asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
-        : "=r"(r) : "f"(0.0f), "f"(__fdiv_rn(most, kFp4Most)));
+        : "=r"(r) : "f"(0.0f), "f"(fp4_quotient(most, kFp4Most, 1.0f / kFp4Most)));
     scale = __low2float(fp4_scales(r));
     return r;
 }
 
-// The code of x / scale, halves to the even level; 0 where the scale is 0 or x is NaN.
-__device__ __forceinline__ float fp4_ratio(float x, float scale) {
-    return scale > 0.0f && x == x ? __fdiv_rn(x, scale) : 0.0f;
-}
 // Codes of four ratios, the first in the lowest bits.
 __device__ __forceinline__ uint32_t fp4_codes4(float a, float b, float c, float d) {
     uint32_t r;

@@ -26,6 +26,7 @@
 // tokens: 5.7 us, most of it the launch.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -216,23 +217,26 @@ __device__ __forceinline__ void norm_row_each(float (&x)[8], const float (&w)[8]
 }
 
 // Quantises and stores this thread's eight values of a row (load_row's places).  Every
-// thread of the warp calls it; row < 0: nothing is stored.  Returns whether a value of a stored
-// row is not finite.
+// thread of the warp calls it; row < 0: nothing is stored.  recip = 1 / gain, rounded.  Returns
+// whether a value of a stored row is not finite.
 template <int D, bool kHalves>
-__device__ __forceinline__ bool store_row_fp4(float (&x)[8], const float* gain, uint8_t* codes, uint8_t* scales, int64_t row,
-                                              int c) {
-    if (gain != nullptr) {
-        const float g = *gain;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], g);
-    }
+__device__ __forceinline__ bool store_row_fp4(float (&x)[8], float gain, float recip, uint8_t* codes, uint8_t* scales,
+                                              int64_t row, int c) {
     bool bad = false;
-    float top[2] = {0.f, 0.f};  // of values 0 .. 3 and 4 .. 7
+    float top[2] = {0.f, 0.f}, t[8];  // (of values 0 .. 3 and 4 .. 7)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        bad |= x[i] - x[i] != 0.0f;
-        top[i >> 2] = fmaxf(top[i >> 2], fabsf(x[i]));
+        t[i] = fp4_quotient(x[i], gain, recip);
+        bad |= !(fabsf(t[i]) <= FLT_MAX);
     }
+    if (__any_sync(0xffffffffu, bad)) {
+        // infinities, and what the gain makes one: the largest number; NaN: 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t[i] = fabsf(t[i]) <= FLT_MAX ? t[i] : x[i] == x[i] ? copysignf(FLT_MAX, x[i]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i >> 2] = fmaxf(top[i >> 2], fabsf(t[i]));
     if constexpr (kHalves) {  // four threads hold a group, in either half
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
@@ -250,9 +254,12 @@ __device__ __forceinline__ bool store_row_fp4(float (&x)[8], const float* gain, 
     scale[1] = scale[0];
     if constexpr (kHalves) byte[1] = fp4_scale_of(top[1], scale[1]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        code[h] = fp4_codes4(fp4_ratio(x[4 * h], scale[h]), fp4_ratio(x[4 * h + 1], scale[h]),
-                             fp4_ratio(x[4 * h + 2], scale[h]), fp4_ratio(x[4 * h + 3], scale[h]));
+    for (int h = 0; h < 2; ++h) {
+        // (no level but 0 where the scale is 0)
+        const float s = scale[h] > 0.0f ? scale[h] : FLT_MAX, r = scale[h] > 0.0f ? __frcp_rn(scale[h]) : 0.0f;
+        code[h] = fp4_codes4(fp4_quotient(t[4 * h], s, r), fp4_quotient(t[4 * h + 1], s, r), fp4_quotient(t[4 * h + 2], s, r),
+                             fp4_quotient(t[4 * h + 3], s, r));
+    }
     if (row < 0) return false;
     uint8_t* to = codes + row * (D / 2);
     uint8_t* ts = scales + row * (D / kFp4Group);
@@ -316,7 +323,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     const int32_t lo = max(max(first, 0), base), hi = min(q.kl, base + kBlock);  // new positions of this block
     const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
     const bool queries = (int32_t)blockIdx.y < P.q_blocks;
-    const int32_t h0 = queries ? 4 * (blockIdx.y / P.q_parts) : blockIdx.y - P.q_blocks;  // first head
+    // a cache in 4 bits: keys and values of a head are two blocks' work
+    const bool values = kFp4 && ((blockIdx.y - P.q_blocks) & 1u) != 0u;
+    const int32_t h0 = queries ? 4 * (blockIdx.y / P.q_parts) : (int32_t)(blockIdx.y - P.q_blocks) / (kFp4 ? 2 : 1);  // first head
     const int32_t heads = min(4, P.H_kv * P.group - h0);  // (of queries)
     if (P.rope != nullptr && hi > P.rope_len && threadIdx.x == 0) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
     const __nv_bfloat16* w = queries ? P.q_norm : P.k_norm;
@@ -372,56 +381,77 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     }
     __syncthreads();
 
-    uint4 next[2][2];  // [token][key, value]
-    auto fetch = [&](int32_t p0) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int32_t pos = p0 + u * kRows + sub;
-            const int64_t tok = (int64_t)q.q0 + (pos - first);
-            next[u][0] = pos < hi ? load_row<D, kHalves>(P.k + tok * P.k_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
-            next[u][1] = pos < hi ? load_row<D, kHalves && !kFp4>(P.v + tok * P.v_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    bool bad = false;  // (kFp4: a value that is not finite)
-    if constexpr (kHalves) fetch(lo);
-    for (int32_t p0 = lo; p0 < hi; p0 += 2 * kRows) {
-        if constexpr (!kHalves) fetch(p0);
-        uint4 raw[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) raw[u][x] = next[u][x];
-        if constexpr (kHalves) fetch(p0 + 2 * kRows);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int32_t pos = p0 + u * kRows + sub;
-            Angles a{};
-            if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
+    if constexpr (kFp4) {
+        // one row at a time in a short loop, the next one under way; whole warps stay in it
+        const __nv_bfloat16* src = (values ? P.v : P.k) + h0 * D;
+        const int64_t stride = values ? P.v_stride : P.k_stride;
+        const float* gains = values ? P.v_gain : P.k_gain;
+        const float gain = gains != nullptr ? gains[h0] : 1.0f, recip = __frcp_rn(gain);
+        uint8_t* codes = reinterpret_cast<uint8_t*>(values ? P.v_cache : P.k_cache);
+        uint8_t* scales = values ? P.v_scale : P.k_scale;
+        auto fetch = [&](int32_t pos) -> uint4 {
+            return pos < hi ? load_row<D, kHalves>(src + ((int64_t)q.q0 + (pos - first)) * stride, c) : make_uint4(0, 0, 0, 0);
+        };
+        bool bad = false;  // a value that is not finite
+        uint4 next = fetch(lo + sub);
+#pragma unroll 1
+        for (int32_t pos = lo + sub; pos - sub < hi; pos += kRows) {
             float x[8];
-            unpack8(raw[u][0], x);
-            const int32_t id = pos < hi ? pages[(pos - base) >> P.page_shift] : -1;
-            if constexpr (kFp4) {
+            unpack8(next, x);
+            next = fetch(pos + kRows);
+            if (!values) {
                 if (w != nullptr) norm_row_each<D>(x, wf, P.eps);
-                if (P.rope != nullptr) rotate_row<kHalves, true>(P, x, c, a);
-                const int64_t slot = id >= 0 ? (((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1)) : -1;
-                bad |= store_row_fp4<D, kHalves>(x, P.k_gain ? P.k_gain + h0 : nullptr,
-                                                 reinterpret_cast<uint8_t*>(P.k_cache), P.k_scale, slot, c);
-                unpack8(raw[u][1], x);
-                bad |= store_row_fp4<D, false>(x, P.v_gain ? P.v_gain + h0 : nullptr,
-                                               reinterpret_cast<uint8_t*>(P.v_cache), P.v_scale, slot, c);
-                continue;
+                if (P.rope != nullptr) {
+                    Angles a{};
+                    load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
+                    rotate_row<kHalves, true>(P, x, c, a);
+                }
             }
-            if (w != nullptr) norm_row<D>(x, wf, P.eps);
-            if (P.rope != nullptr) rotate_row<kHalves>(P, x, c, a);
-            if (id >= 0) {
-                const int64_t slot = ((((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1))) * D;
-                store_row<D, kHalves>(P.k_cache + slot, c, pack8(x));
-                store_row<D, kHalves>(P.v_cache + slot, c, raw[u][1]);
+            const int32_t id = pos < hi ? pages[(pos - base) >> P.page_shift] : -1;
+            const int64_t slot = id >= 0 ? (((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1)) : -1;
+            bad |= store_row_fp4<D, kHalves>(x, gain, recip, codes, scales, slot, c);
+        }
+        if (bad) atomicCAS(P.b.status, 0, BSA_ERR_NONFINITE);
+        if (values) return;
+    } else {
+        uint4 next[2][2];  // [token][key, value]
+        auto fetch = [&](int32_t p0) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int32_t pos = p0 + u * kRows + sub;
+                const int64_t tok = (int64_t)q.q0 + (pos - first);
+                next[u][0] = pos < hi ? load_row<D, kHalves>(P.k + tok * P.k_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
+                next[u][1] = pos < hi ? load_row<D, kHalves>(P.v + tok * P.v_stride + h0 * D, c) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        if constexpr (kHalves) fetch(lo);
+        for (int32_t p0 = lo; p0 < hi; p0 += 2 * kRows) {
+            if constexpr (!kHalves) fetch(p0);
+            uint4 raw[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) raw[u][x] = next[u][x];
+            if constexpr (kHalves) fetch(p0 + 2 * kRows);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int32_t pos = p0 + u * kRows + sub;
+                Angles a{};
+                if (P.rope != nullptr) load_angles<kHalves>(P, c, min(pos, P.rope_len - 1), a);
+                float x[8];
+                unpack8(raw[u][0], x);
+                if (w != nullptr) norm_row<D>(x, wf, P.eps);
+                if (P.rope != nullptr) rotate_row<kHalves>(P, x, c, a);
+                const int32_t id = pos < hi ? pages[(pos - base) >> P.page_shift] : -1;
+                if (id >= 0) {
+                    const int64_t slot = ((((int64_t)id * P.H_kv + h0) << P.page_shift) + (pos & (page - 1))) * D;
+                    store_row<D, kHalves>(P.k_cache + slot, c, pack8(x));
+                    store_row<D, kHalves>(P.v_cache + slot, c, raw[u][1]);
+                }
             }
         }
     }
 
-    if (kFp4 && bad) atomicCAS(P.b.status, 0, BSA_ERR_NONFINITE);
     if (P.k_mean == nullptr || hi != base + kBlock) return;  // (the whole thread block agrees)
     // the block is full: the mean of its 128 keys as the cache holds them
     const int32_t last = pages[per - 1];
@@ -486,8 +516,8 @@ bsa_status launch_paged_append(const PagedAppendArgs& a, int32_t* status, cudaSt
     P.q_blocks = a.q != nullptr ? (a.H + 3) / 4 * P.q_parts : 0;
     // a sequence's n > 0 new tokens touch at most (n + 126) / 128 + 1 blocks
     const int64_t units = (int64_t)a.tokens / kBlock + 2 * (int64_t)a.seqs;
-    const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + a.H_kv));
     const bool fp4 = a.k_scale != nullptr;
+    const dim3 grid((unsigned)units, (unsigned)(P.q_blocks + (fp4 ? 2 : 1) * a.H_kv));
     P.k_scale = static_cast<uint8_t*>(a.k_scale);
     P.v_scale = static_cast<uint8_t*>(a.v_scale);
     P.k_gain = a.k_gain;

@@ -2,6 +2,7 @@
 C ABI, shapes, strides, types and devices through the binding (no GPU)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -226,3 +227,30 @@ def test_workspace_sizes_of_numbers_beyond_32_bits(lib):
     for name in sizes:
         with pytest.raises(ValueError):
             bsa.forward_paged_fp4_workspace_size(**{**sizes, name: sizes[name] + (1 << 32)})
+
+
+# ------------------------------------------------------------------ quotients
+
+def quotient(x, y):
+    """The library's x / y: fp32 steps, each rounded once (a fused product and sum included)."""
+    f32 = np.float32
+    recip = f32(1) / y
+    q = x * recip
+    rest = f32(x.astype(np.longdouble) - q.astype(np.longdouble) * y.astype(np.longdouble))
+    return f32(q.astype(np.longdouble) + rest.astype(np.longdouble) * recip.astype(np.longdouble))
+
+
+def test_quotients_by_scales_are_rounded_quotients():
+    """By every scale, by 6 and by gains of any kind, for numbers of any kind a row may hold: the
+    division's result, bit by bit (so that halves between levels are met exactly)."""
+    rng = np.random.default_rng(1)
+    scales = [m / 8 * 2.0 ** -6 for m in range(1, 8)] + [(1 + m / 8) * 2.0 ** (e - 7) for e in range(1, 16) for m in range(8)]
+    gains = np.exp(rng.uniform(-20, 20, 300))
+    edges = np.array([0.25, 0.5, 0.75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6])
+    for y in np.concatenate([scales, [6.0], gains]).astype(np.float32):
+        at = (edges * np.float64(y)).astype(np.float32)
+        near = np.concatenate([at, np.nextafter(at, np.float32(0)), np.nextafter(at, np.float32(1e30))])
+        x = np.concatenate([near, (rng.normal(size=2000) * y).astype(np.float32),
+                            (rng.normal(size=500) * np.exp(rng.uniform(-30, 30, 500))).astype(np.float32)])
+        yy = np.full_like(x, y)
+        assert np.array_equal(quotient(x, yy), x / yy), y
