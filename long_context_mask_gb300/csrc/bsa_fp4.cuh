@@ -12,6 +12,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "bsa_rows.cuh"
+
 namespace bsa {
 
 constexpr int kFp4Group = 16;        // values that share a scale
@@ -43,6 +45,15 @@ __device__ __forceinline__ void fp4_levels(uint32_t w, __half2 (&x)[4]) {
 __device__ __forceinline__ float fp4_quotient(float x, float y, float recip) {
     const float q = x * recip;
     return fmaf(fmaf(-q, y, x), recip, q);
+}
+// The same for eight numbers, two at a time.
+__device__ __forceinline__ void fp4_quotients(const uint64_t (&x)[4], float y, float recip, uint64_t (&out)[4]) {
+    const uint64_t y2 = f2pack(-y, -y), r2 = f2pack(recip, recip), none = f2pack(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t q = fma2(x[i], r2, none);
+        out[i] = fma2(fma2(q, y2, x[i]), r2, q);
+    }
 }
 
 // The scale byte of a group whose largest magnitude is `most` (finite), and the scale.

@@ -195,14 +195,28 @@ __device__ __forceinline__ float two_sum(float a, float b, float& s) {
 // in two words, and one Newton step on the device's reciprocal root takes its error out.
 template <int D>
 __device__ __forceinline__ void norm_row_each(float (&x)[8], const float (&w)[8], float eps) {
-    float hi = 0.f, lo = 0.f;
+    // (two chains of four values side by side)
+    const uint64_t minus = f2pack(-1.0f, -1.0f);
+    uint64_t h2 = f2pack(0.f, 0.f), l2 = h2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo = __fadd_rn(lo, two_sum(hi, __fmul_rn(x[i], x[i]), hi));
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t v = f2pack(x[2 * i], x[2 * i + 1]), p = fma2(v, v, f2pack(0.f, 0.f));
+        const uint64_t sum = add2(h2, p), t = fma2(h2, minus, sum);
+        l2 = add2(l2, add2(fma2(fma2(t, minus, sum), minus, h2), fma2(t, minus, p)));
+        h2 = sum;
+    }
+    float ha, hb, la, lb, hi;
+    f2unpack(h2, ha, hb);
+    f2unpack(l2, la, lb);
+    float lo = two_sum(ha, hb, hi);
+    lo = __fadd_rn(__fadd_rn(la, lb), lo);
 #pragma unroll
     for (int d = 1; d < D / 8; d <<= 1) {
-        const float h2 = __shfl_xor_sync(0xffffffffu, hi, d), l2 = __shfl_xor_sync(0xffffffffu, lo, d);
-        const float e = two_sum(fmaxf(hi, h2), fminf(hi, h2), hi);  // (the same in every thread)
-        lo = __fadd_rn(__fadd_rn(lo, l2), e);
+        const float h = __shfl_xor_sync(0xffffffffu, hi, d), l = __shfl_xor_sync(0xffffffffu, lo, d);
+        // (the larger first: hi is not less than what is left of the sum; the same in every thread)
+        const float big = fmaxf(hi, h), small = fminf(hi, h);
+        hi = __fadd_rn(big, small);
+        lo = __fadd_rn(__fadd_rn(lo, l), __fsub_rn(small, __fsub_rn(hi, big)));
     }
     float m;
     const float e = two_sum(hi * (1.0f / D), eps, m);
@@ -222,13 +236,18 @@ __device__ __forceinline__ void norm_row_each(float (&x)[8], const float (&w)[8]
 template <int D, bool kHalves>
 __device__ __forceinline__ bool store_row_fp4(float (&x)[8], float gain, float recip, uint8_t* codes, uint8_t* scales,
                                               int64_t row, int c) {
-    bool bad = false;
-    float top[2] = {0.f, 0.f}, t[8];  // (of values 0 .. 3 and 4 .. 7)
+    uint64_t t2[4], z = f2pack(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        t[i] = fp4_quotient(x[i], gain, recip);
-        bad |= !(fabsf(t[i]) <= FLT_MAX);
+    for (int i = 0; i < 4; ++i) t2[i] = f2pack(x[2 * i], x[2 * i + 1]);
+    if (gain != 1.0f) fp4_quotients(t2, gain, recip, t2);
+    float t[8], z0, z1, top[2] = {0.f, 0.f};  // (top: of values 0 .. 3 and 4 .. 7)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        z = fma2(t2[i], f2pack(0.0f, 0.0f), z);  // (NaN where a number is not finite)
+        f2unpack(t2[i], t[2 * i], t[2 * i + 1]);
     }
+    f2unpack(z, z0, z1);
+    const bool bad = !(z0 + z1 == 0.0f);
     if (__any_sync(0xffffffffu, bad)) {
         // infinities, and what the gain makes one: the largest number; NaN: 0
 #pragma unroll
@@ -253,12 +272,30 @@ __device__ __forceinline__ bool store_row_fp4(float (&x)[8], float gain, float r
     byte[1] = byte[0];
     scale[1] = scale[0];
     if constexpr (kHalves) byte[1] = fp4_scale_of(top[1], scale[1]);
+    // (no level but 0 where the scale is 0)
+    uint64_t y2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y2[i] = f2pack(t[2 * i], t[2 * i + 1]);
+    float s[2], r[2];
+    s[0] = scale[0] > 0.0f ? scale[0] : FLT_MAX;
+    r[0] = scale[0] > 0.0f ? __frcp_rn(scale[0]) : 0.0f;
+    if constexpr (kHalves) {
+        s[1] = scale[1] > 0.0f ? scale[1] : FLT_MAX;
+        r[1] = scale[1] > 0.0f ? __frcp_rn(scale[1]) : 0.0f;
+    } else {
+        s[1] = s[0];
+        r[1] = r[0];
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        // (no level but 0 where the scale is 0)
-        const float s = scale[h] > 0.0f ? scale[h] : FLT_MAX, r = scale[h] > 0.0f ? __frcp_rn(scale[h]) : 0.0f;
-        code[h] = fp4_codes4(fp4_quotient(t[4 * h], s, r), fp4_quotient(t[4 * h + 1], s, r), fp4_quotient(t[4 * h + 2], s, r),
-                             fp4_quotient(t[4 * h + 3], s, r));
+        const uint64_t r2 = f2pack(r[h], r[h]), s2 = f2pack(-s[h], -s[h]);
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t v = y2[2 * h + i], q = fma2(v, r2, f2pack(0.0f, 0.0f));
+            f2unpack(fma2(fma2(q, s2, v), r2, q), y[2 * i], y[2 * i + 1]);
+        }
+        code[h] = fp4_codes4(y[0], y[1], y[2], y[3]);
     }
     if (row < 0) return false;
     uint8_t* to = codes + row * (D / 2);
@@ -322,17 +359,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
     const int32_t base = blk * kBlock;
     const int32_t lo = max(max(first, 0), base), hi = min(q.kl, base + kBlock);  // new positions of this block
     const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-    const bool queries = (int32_t)blockIdx.y < P.q_blocks;
+    // (a cache in 4 bits: its keys, which take longest, and values come first)
+    const int32_t kv_first = kFp4 ? 2 * P.H_kv : 0;
+    const int32_t by = (int32_t)blockIdx.y < kv_first ? P.q_blocks + (int32_t)blockIdx.y : (int32_t)blockIdx.y - kv_first;
+    const bool queries = by < P.q_blocks;
     // a cache in 4 bits: keys and values of a head are two blocks' work
-    const bool values = kFp4 && ((blockIdx.y - P.q_blocks) & 1u) != 0u;
-    const int32_t h0 = queries ? 4 * (blockIdx.y / P.q_parts) : (int32_t)(blockIdx.y - P.q_blocks) / (kFp4 ? 2 : 1);  // first head
+    const bool values = kFp4 && ((by - P.q_blocks) & 1) != 0;
+    const int32_t h0 = queries ? 4 * (by / P.q_parts) : (by - P.q_blocks) / (kFp4 ? 2 : 1);  // first head
     const int32_t heads = min(4, P.H_kv * P.group - h0);  // (of queries)
     if (P.rope != nullptr && hi > P.rope_len && threadIdx.x == 0) atomicCAS(P.b.status, 0, BSA_ERR_BOUNDS);
     const __nv_bfloat16* w = queries ? P.q_norm : P.k_norm;
     float wf[8];
     if (w != nullptr) unpack8(load_row<D, kHalves>(w, c), wf);
     if (queries) {
-        const int32_t span = kBlock / P.q_parts, at = base + span * (blockIdx.y % P.q_parts);
+        const int32_t span = kBlock / P.q_parts, at = base + span * (by % P.q_parts);
         const int32_t from = max(lo, at), to = min(hi, at + span);
         // With kHalves the next token's rows are on their way while this one's are worked
         // on (46.7 -> 44.1 us); the other forms need the registers (11.3 us, 12.8 with it).
