@@ -7,6 +7,7 @@ stream.  No arithmetic of the method happens here.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -719,8 +720,12 @@ def _paged_batch(page_table, q_start, kv_len, tokens, page_size, n_pages):
     if (seqs | tokens | max_pages | page_size | n_pages) >> 31:
         _fits(seqs=seqs, tokens=tokens, max_pages=max_pages, page_size=page_size, n_pages=n_pages)
     i32 = _torch.int32
-    return PagedBatch(_array(page_table, "page_table", i32, 0), _array(q_start, "q_start", i32, seqs + 1),
-                      _array(kv_len, "kv_len", i32, seqs), seqs, tokens, max_pages, page_size, n_pages)
+    if not (page_table.dtype is i32 and q_start.dtype is i32 and kv_len.dtype is i32 and q_start.numel() > seqs and
+            kv_len.numel() >= seqs and page_table.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous()):
+        for t, name, n in ((page_table, "page_table", 0), (q_start, "q_start", seqs + 1), (kv_len, "kv_len", seqs)):
+            _array(t, name, i32, n)
+    return PagedBatch(page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), seqs, tokens, max_pages, page_size,
+                      n_pages)
 
 
 def _block_lists(sel, sel_cnt, tokens, H_kv):
@@ -895,19 +900,24 @@ class Fp4Cache(ctypes.Structure):
 
 def _fp4_cache(k_cache, k_scale, v_cache, v_scale, k_gain, v_gain):
     """(cache, pages, H_kv, page_size, D)."""
-    shape = k_cache.shape
+    shape, scales = k_cache.shape, k_scale.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must share the shape [pages, H_kv, page_size, D / 2]")
     n_pages, H_kv, page_size, half = shape
-    D = 2 * half
-    want = (n_pages, H_kv, page_size, D // 16)
-    if k_scale.shape != want or v_scale.shape != want:
-        raise ValueError(f"k_scale and v_scale must have the shape [pages, H_kv, page_size, D / 16], here {want}")
-    u8, e4m3, f32 = _torch.uint8, _torch.float8_e4m3fn, _torch.float32
-    c = Fp4Cache(_array(k_cache, "k_cache", u8, 0), _array(k_scale, "k_scale", e4m3, 0), _array(v_cache, "v_cache", u8, 0),
-                 _array(v_scale, "v_scale", e4m3, 0), _array(k_gain, "k_gain", f32, H_kv) if k_gain is not None else None,
-                 _array(v_gain, "v_gain", f32, H_kv) if v_gain is not None else None)
-    return c, n_pages, H_kv, page_size, D
+    if scales != (n_pages, H_kv, page_size, half // 8) or v_scale.shape != scales:
+        raise ValueError("k_scale and v_scale must have the shape [pages, H_kv, page_size, D / 16], here "
+                         f"{(n_pages, H_kv, page_size, half // 8)}")
+    u8, e4m3 = _torch.uint8, _torch.float8_e4m3fn
+    if not (k_cache.dtype is u8 and v_cache.dtype is u8 and k_scale.dtype is e4m3 and v_scale.dtype is e4m3 and
+            k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        for t, name, dtype in ((k_cache, "k_cache", u8), (k_scale, "k_scale", e4m3), (v_cache, "v_cache", u8),
+                               (v_scale, "v_scale", e4m3)):
+            _array(t, name, dtype, 0)
+    f32 = _torch.float32
+    c = Fp4Cache(k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(),
+                 None if k_gain is None else _array(k_gain, "k_gain", f32, H_kv),
+                 None if v_gain is None else _array(v_gain, "v_gain", f32, H_kv))
+    return c, n_pages, H_kv, page_size, 2 * half
 
 
 def paged_append_fp4(k, v, k_cache, k_scale, v_cache, v_scale, page_table, q_start, kv_len, *, q=None, q_out=None,
@@ -962,6 +972,12 @@ def forward_paged_fp4_workspace_size(seqs: int, tokens: int, max_pages: int, pag
     return int(load_library().bsa_forward_paged_fp4_workspace_size(ctypes.byref(b), H, H_kv, D, sel_width))
 
 
+@functools.lru_cache(maxsize=4096)
+def _fp4_workspace(seqs, tokens, max_pages, page_size, n_pages, H, H_kv, D, sel_width):
+    b = PagedBatch(None, None, None, seqs, tokens, max_pages, page_size, n_pages)
+    return int(load_library().bsa_forward_paged_fp4_workspace_size(ctypes.byref(b), H, H_kv, D, sel_width))
+
+
 def forward_paged_fp4(q, k_cache, k_scale, v_cache, v_scale, page_table, q_start, kv_len, o, lse, *, causal: bool = True,
                       window: int = 0, sinks: int = 0, sel=None, sel_cnt=None, k_gain=None, v_gain=None,
                       scale: float = 0.0, max_new: int = 0, workspace=None, stream=None):
@@ -981,8 +997,8 @@ def forward_paged_fp4(q, k_cache, k_scale, v_cache, v_scale, page_table, q_start
                  workspace)
     lib = _lib or load_library()
     ref = ctypes.byref(b)
-    keep, ws, nbytes = _scratch(lib.bsa_forward_paged_fp4_workspace_size(ref, H, H_kv, D, width), workspace, q.device,
-                                stream)
+    need = 0 if workspace is not None else _fp4_workspace(b.seqs, tokens, b.max_pages, page_size, n_pages, H, H_kv, D, width)
+    keep, ws, nbytes = _scratch(need, workspace, q.device, stream)
     code = lib.bsa_forward_paged_fp4(ref, qp, qs, ctypes.byref(c), H, H_kv, D, 1 if causal else 0, window, sinks, sp, cp,
                                      width, scale, max_new, ws, nbytes, op, lp, _raw_stream(stream, dev))
     if code:
