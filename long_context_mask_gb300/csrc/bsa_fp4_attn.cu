@@ -40,17 +40,14 @@
 #include "bsa_paged.cuh"
 #include "bsa_paged_wait.cuh"
 #include "bsa_rows.cuh"
+#include "bsa_tma_host.h"
 
 namespace bsa {
 namespace {
 
 constexpr int32_t kMaxWindow = 1 << 26;  // (positions lie within 2^24 of zero)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 8;                    // that compute
-constexpr int kTeam = 4;                     // of them to a key tile, 32 keys each
-constexpr int kLoad = kWarps, kStore = kWarps + 1;
-constexpr int kThreads = 32 * (kWarps + 2);
-constexpr int kRuns = 2 * kPagedBlocks;
+constexpr int kTeam = 4;                     // warps to a key tile, 32 keys each
 constexpr int kMaxNT = 2;
 constexpr int32_t kFewRows = 16;             // rows of a sequence that are done here
 // A row tile of n key tiles counts n + kRowCost in a run.
@@ -76,14 +73,17 @@ __device__ __forceinline__ uint32_t bits(__half2 x) { return *reinterpret_cast<u
 // scales), the parts of O that the warps join, query rows, and what the warps tell one another.
 template <int D, int NT>
 struct Cfg {
-    static constexpr int kBlocks = NT == 1 ? 2 : 1;      // of an SM
-    static constexpr int kStages = NT == 1 ? 4 : 8;
+    static constexpr int kWarps = NT == 1 ? 16 : 8;      // that compute; two more load, one joins their parts
+    static constexpr int kLoadK = kWarps, kLoadV = kWarps + 1, kStore = kWarps + 2;
+    static constexpr int kThreads = 32 * (kWarps + 3);
+    static constexpr int kTeams = kWarps / kTeam;
+    static constexpr int kStages = 8;                    // (a multiple of the teams)
     static constexpr int kCodes = 128 * D / 2, kScales = 128 * D / 16;
     static constexpr int kStage = 2 * (kCodes + kScales);
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRowO = D + 4;                  // a row of O, padded
     static constexpr int kJoin = kWarps * 8 * NT * kRowO * 4;
-    static constexpr int kSmem = kRing + kJoin;
+    static constexpr int kSmem = kRing + kJoin;          // (and 128 bytes to align it)
 };
 
 constexpr int kDesc = 3;    // descriptors in flight
@@ -99,7 +99,7 @@ struct Shared {
     int32_t key[Cfg<D, NT>::kStages]; // first key of the tile in each slot
     int64_t prefix[33];
     Fp4Start start;
-    float2 ml[kWarps][8 * NT];
+    float2 ml[Cfg<D, NT>::kWarps][8 * NT];
 };
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Watch* w, const int32_t* status) {
@@ -107,27 +107,30 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const W
 }
 
 template <int D, int NT, int kMode>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(const __grid_constant__ Fp4Params P) {
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __grid_constant__ Fp4Params P) {
     using C = Cfg<D, NT>;
     constexpr bool kLists = kMode == kListed;
-    constexpr uint32_t S = C::kStages;
+    constexpr uint32_t S = C::kStages, T = C::kTeams;
+    constexpr int kWarps = C::kWarps, kLoadK = C::kLoadK, kLoadV = C::kLoadV, kStore = C::kStore, kThreads = C::kThreads;
     constexpr int R = 8 * NT;
     constexpr int kSteps = D / 16;          // products of S^T for 16 keys; of O^T as well
     constexpr int kKW = D / 32;             // words of a K row that a lane takes
     constexpr int kVW = D / 64;             // words of a V row that a lane takes
     constexpr int kRowO = C::kRowO;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    // (an offset, not a rounded pointer: the compiler has to see that it is shared memory)
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 127u);
     __shared__ __align__(16) Shared<D, NT> sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* const status = P.b.status;
     if (threadIdx.x == kThreads - 1) {
         for (uint32_t x = 0; x < S; ++x) {
-            mbar_init(smem_u32(&sh.full[x]), 33);
+            mbar_init(smem_u32(&sh.full[x]), 2 * (1 + (P.b.page < kFp4LongPage ? 32 : 0)));
             mbar_init(smem_u32(&sh.empty[x]), kTeam);
         }
         for (int x = 0; x < kDesc; ++x) {
             mbar_init(smem_u32(&sh.seg_full[x]), 1);
-            mbar_init(smem_u32(&sh.seg_empty[x]), kWarps + 1);
+            mbar_init(smem_u32(&sh.seg_empty[x]), kWarps + 2);
         }
         mbar_init(smem_u32(&sh.joined), kWarps);
         mbar_init(smem_u32(&sh.freed), 1);
@@ -145,52 +148,96 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
     // ---------------------------------------------------------------- this block's run
     // (its scratch is in the ring, which is free here)
     Fp4Run run;
-    if (!Fp4Work<R, kRowCost, kLists>{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run)) return;
+    using Work = Fp4Work<R, kRowCost, kLists>;
+    if (!Work{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run)) return;
     // what was written there by ordinary stores makes room for bulk copies
     fence_proxy_async_smem();
     __syncthreads();
     if (sh.watch.abort != 0) return;
 
-    if (warp == kLoad) {
-        // ------------------------------------------------------------ segments, query rows and key tiles
+    // ---------------------------------------------------------------- loading warps
+    // The K (V) tiles of a segment, whose numbers in the run begin at g, four at a time: lane l has page
+    // l % N of tile l / N.  Codes: see fp4_load_codes; scales come by a bulk copy a page from long pages,
+    // else 16 bytes a lane.
+    auto load_tiles = [&](const Fp4Segment& sg, bool is_v, uint32_t& g) -> bool {
+        constexpr int kAtOnce = 4, kCopies = C::kScales / 512, kBytes = D / 16;  // (scales of a row)
+        const int32_t page = P.b.page, N = 128 / page;  // pages of a tile
+        const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
+        const int32_t page_codes = page * (D / 2), page_scales = page * kBytes;
+        const bool short_pages = page < kFp4LongPage;
+        const int32_t j0 = sg.j0, j1 = j0 + sg.n, kvh = sg.kvh;
+        const int32_t* table = P.b.table + (int64_t)sg.seq * P.b.max_pages;
+        const int32_t* list = kLists ? P.list + Work{P}.list_of(kvh, sg.tile) * P.cap : nullptr;
+        const uint8_t *codes = is_v ? P.v : P.k, *scales = is_v ? P.v_scale : P.k_scale;
+        const uint32_t to_codes = smem_u32(smem) + (is_v ? C::kCodes : 0) + lane_page * page_codes;
+        const uint32_t to_scales = smem_u32(smem) + 2 * C::kCodes + (is_v ? C::kScales : 0);
+        // the cache row of this lane's page (-1: behind the sequence's end, or no tile), and the tile's first key
+        auto fetch = [&](int32_t jb, int32_t& key) -> int32_t {
+            const int32_t j = jb + lane_tile;
+            key = 0;
+            if (lane_tile >= kAtOnce || j >= j1) return -1;
+            if constexpr (kLists) key = list[j] * 128;
+            else key = (j < sg.ns ? j : sg.lo + j - sg.ns) * 128;
+            const int32_t pg = key / page + lane_page;
+            if (pg * page >= sg.kl) return -1;
+            int32_t id = table[pg];
+            if (id < 0 || id >= P.b.n_pages) {
+                raise_status(status, BSA_ERR_BOUNDS);
+                id = 0;  // (this row's result is unspecified)
+            }
+            return (id * P.H_kv + kvh) * page;
+        };
+        int32_t key_nxt, nxt = fetch(j0, key_nxt);
+        for (int32_t jb = j0; jb < j1; jb += kAtOnce) {
+            const int32_t row = nxt, key = key_nxt, tiles = min(kAtOnce, j1 - jb);
+            nxt = fetch(jb + kAtOnce, key_nxt);
+            const bool live = lane_tile < tiles;
+            const uint32_t gl = g + (live ? lane_tile : 0), at = gl % S, bar = smem_u32(&sh.full[at]);
+            if (!wait_warp(smem_u32(&sh.empty[at]), ((gl / S) & 1u) ^ 1u, &sh.watch, status)) return false;
+            const uint32_t held = __ballot_sync(0xffffffffu, row >= 0);
+            if (live && lane_page == 0) {
+                const int32_t pages = __popc(held >> lane & ((1u << N) - 1u));
+                if (!is_v) sh.key[at] = key;
+                mbar_arrive_expect_tx(bar, fp4_code_bytes(page, pages, D / 2) + (uint32_t)(short_pages ? 0 : pages * page_scales));
+            }
+            __syncwarp();
+            fp4_load_codes(codes, is_v ? &P.map_v : &P.map_k, page, D / 2, live, row,
+                           __shfl_sync(0xffffffffu, row, lane - lane_page), to_codes + at * C::kStage, bar);
+            if (row >= 0 && !short_pages)
+                bulk_load(to_scales + at * C::kStage + lane_page * page_scales, scales + (int64_t)row * kBytes, page_scales, bar);
+            __syncwarp();
+            if (short_pages) {
+                for (int32_t x = 0; x < tiles; ++x) {
+                    const uint32_t slot = (g + x) % S;
+#pragma unroll
+                    for (int y = 0; y < kCopies; ++y) {
+                        const int32_t byte = y * 512 + lane * 16, pg = byte / page_scales;
+                        const int32_t from = __shfl_sync(0xffffffffu, row, x * N + pg);
+                        if (from >= 0)
+                            cp_async16(to_scales + slot * C::kStage + byte, scales + (int64_t)from * kBytes + byte - pg * page_scales);
+                    }
+                    cp_async_arrive_noinc(smem_u32(&sh.full[slot]));
+                }
+            }
+            g += tiles;
+        }
+        return true;
+    };
+    // (every issued copy must land before the block exits)
+    auto land = [&](uint32_t g) {
+        cp_async_wait_all();
+        if (lane == 0)
+            for (uint32_t x = g > S ? g - S : 0; x < g; ++x) paged_drain(smem_u32(&sh.full[x % S]), (x / S) & 1u, status);
+        __syncwarp();
+    };
+    uint32_t k = 0;  // segments so far
+    bool ok = true;
+    if (warp == kLoadK) {
+        // ------------------------------------------------------------ segments, query rows and K tiles
         Fp4Walk<R, kRowCost, kLists> walk(P, run, sh.start);
         Fp4Segment sg;
-        uint32_t k = 0, g = 0;  // segments and tiles so far
-        bool ok = true;
-        const int32_t page = P.b.page, N = 128 / page, per_window = page >> 2;  // pages of a tile; tiles whose pages one read of 32 lanes brings
-        const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
-        const uint32_t ring = smem_u32(smem);
-        // scales: 16 bytes a lane and copy, of the page that holds them
-        constexpr int kCopies = C::kScales / 512, kBytes = D / 16;  // (a row's scales)
-        const int32_t page_scales = page * kBytes;
-        int32_t sc_page[kCopies], sc_at[kCopies];
-#pragma unroll
-        for (int x = 0; x < kCopies; ++x) {
-            sc_page[x] = (x * 512 + lane * 16) / page_scales;
-            sc_at[x] = (x * 512 + lane * 16) % page_scales;
-        }
+        uint32_t g = 0;  // tiles so far
         for (; ok && walk.open(sg); walk.advance()) {
-            const int32_t j0 = sg.j0, j1 = j0 + sg.n, kvh = sg.kvh;
-            const int32_t* table = P.b.table + (int64_t)walk.s * P.b.max_pages;
-            const int32_t* list = kLists ? P.list + walk.work.list_of(kvh, walk.i) * P.cap : nullptr;
-            // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
-            // sequence's end), and the tile's first key
-            auto fetch = [&](int32_t w0, int32_t& key) -> int32_t {
-                const int32_t j = w0 + lane_tile;
-                key = 0;
-                if (j >= j1) return -1;
-                if constexpr (kLists) key = list[j] * 128;
-                else key = (j < sg.ns ? j : sg.lo + j - sg.ns) * 128;
-                const int32_t pg = key / page + lane_page;
-                if (pg * page >= sg.kl) return -1;
-                int32_t id = table[pg];
-                if (id < 0 || id >= P.b.n_pages) {
-                    raise_status(status, BSA_ERR_BOUNDS);
-                    id = 0;  // (this row's result is unspecified)
-                }
-                return (id * P.H_kv + kvh) * page;
-            };
-            int32_t key_nxt, key_cur, w0 = j0, cur = fetch(j0, key_cur), nxt = fetch(j0 + per_window, key_nxt);
             const uint32_t d = k % kDesc, seg_bar = smem_u32(&sh.seg_full[d]);
             if (!wait_warp(smem_u32(&sh.seg_empty[d]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
                 ok = false;
@@ -204,47 +251,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
             __syncwarp();
             if (lane < sg.nrows) {
                 const int32_t row = sg.row0 + lane, tok = row / P.group, head = row - tok * P.group;
-                bulk_load(smem_u32(sh.q[d][lane]), P.q + ((int64_t)sg.q0 + tok) * P.q_stride + (int64_t)(kvh * P.group + head) * D,
-                          D * 2, seg_bar);
+                bulk_load(smem_u32(sh.q[d][lane]),
+                          P.q + ((int64_t)sg.q0 + tok) * P.q_stride + (int64_t)(sg.kvh * P.group + head) * D, D * 2, seg_bar);
             }
             __syncwarp();
             ++k;
-            for (int32_t j = j0; j < j1; ++j, ++g) {
-                if (j >= w0 + per_window) {
-                    w0 += per_window;
-                    cur = nxt;
-                    key_cur = key_nxt;
-                    nxt = fetch(w0 + per_window, key_nxt);
-                }
-                const bool mine = lane_tile == j - w0 && cur >= 0;
-                const int32_t held = __popc(__ballot_sync(0xffffffffu, mine));
-                const uint32_t at = g % S;
-                if (!wait_warp(smem_u32(&sh.empty[at]), ((g / S) & 1u) ^ 1u, &sh.watch, status)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = smem_u32(&sh.full[at]), to = ring + at * C::kStage;
-                if (lane_tile == j - w0 && lane_page == 0) {
-                    sh.key[at] = key_cur;
-                    mbar_arrive_expect_tx(bar, (uint32_t)(held * page * D));
-                }
-                __syncwarp();
-                if (mine) {
-                    bulk_load(to + lane_page * page * (D / 2), P.k + (int64_t)cur * (D / 2), page * (D / 2), bar);
-                    bulk_load(to + C::kCodes + lane_page * page * (D / 2), P.v + (int64_t)cur * (D / 2), page * (D / 2), bar);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int x = 0; x < kCopies; ++x) {
-                    const int32_t row = __shfl_sync(0xffffffffu, cur, (j - w0) * N + sc_page[x]);
-                    if (row >= 0) {
-                        const int64_t from = (int64_t)row * kBytes + sc_at[x];
-                        cp_async16(to + 2 * C::kCodes + x * 512 + lane * 16, P.k_scale + from);
-                        cp_async16(to + 2 * C::kCodes + C::kScales + x * 512 + lane * 16, P.v_scale + from);
-                    }
-                }
-                cp_async_arrive_noinc(bar);
-            }
+            ok = load_tiles(sg, false, g);
         }
         if (ok && wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
             if (lane == 0) {
@@ -255,10 +267,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
             ok = false;
         }
         if (!ok && lane == 0) set_abort(&sh.watch, status);
-        // every issued copy must land before the block exits
-        cp_async_wait_all();
+        land(g);
         if (lane == 0) {
-            for (uint32_t x = g > S ? g - S : 0; x < g; ++x) paged_drain(smem_u32(&sh.full[x % S]), (x / S) & 1u, status);
             // (the last descriptor's slot has been handed back: its query rows had landed)
             const uint32_t known = k + (ok ? 1u : 0u);
             for (uint32_t x = known > kDesc ? known - kDesc : 0; x < k; ++x)
@@ -266,10 +276,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
         }
         return;
     }
+    if (warp == kLoadV) {
+        // ------------------------------------------------------------ V tiles
+        uint32_t g = 0;
+        for (; ok; ++k) {
+            if (!wait_warp(smem_u32(&sh.seg_full[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status)) {
+                ok = false;
+                break;
+            }
+            const Fp4Segment sg = sh.seg[k % kDesc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[k % kDesc]));
+            if (sg.n < 0) break;
+            ok = load_tiles(sg, true, g);
+        }
+        if (!ok && lane == 0) set_abort(&sh.watch, status);
+        land(g);
+        return;
+    }
 
     float* const so = reinterpret_cast<float*>(smem + C::kRing);  // [warp][row][kRowO]
-    uint32_t k = 0;  // segments so far
-    bool ok = true;
     if (warp == kStore) {
         // ------------------------------------------------------------ joins the warps' parts
         constexpr int kLanes = D / 4, kAbreast = 32 / kLanes;
@@ -344,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
     const uint32_t off_v[2] = {C::kCodes + v0 * (D / 2) + r * (D / 16), C::kCodes + v1 * (D / 2) + r * (D / 16)};
     const uint32_t at_s = 2 * C::kCodes + C::kScales + (D == 128 ? r : r >> 1);
     const uint32_t off_vs[2] = {at_s + v0 * (D / 16), at_s + v1 * (D / 16)};
-    // this warp's team takes every other tile of the run: slots team, team + 2, ..
+    // this warp's team takes every T-th tile of the run: slots team, team + T, ..
     const uint32_t team = warp / kTeam;
     uint32_t slot = team, phase = 0;  // of the team's next tile
     uint32_t g0 = 0;                  // tiles of the segments before
@@ -413,10 +439,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
                 m[b][y] = -INFINITY;
                 l[b][y] = 0.0f;
             }
-        const uint32_t first = (g0 ^ team) & 1u;  // (the segment's first tile is the other team's)
+        const uint32_t first = (team - g0) & (T - 1u);  // the team's first tile of the segment
         g0 += (uint32_t)sg.n;
 #pragma unroll 1
-        for (int32_t n = sg.n - (int32_t)first; n > 0; n -= 2) {
+        for (int32_t n = sg.n - (int32_t)first; n > 0; n -= (int32_t)T) {
             if (!wait_warp(smem_u32(&sh.full[slot]), phase, &sh.watch, status)) {
                 ok = false;
                 break;
@@ -424,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kBlocks) k_fp4_rows(cons
             const int32_t kb = sh.key[slot] + (int32_t)w0;
             const uint32_t done = smem_u32(&sh.empty[slot]);
             const uint8_t* at = smem + slot * C::kStage;
-            slot += 2;
+            slot += T;
             if (slot >= S) {
                 slot = team;
                 phase ^= 1u;
@@ -617,8 +643,8 @@ Layout layout(const PagedForwardArgs& a) {
         return p;
     };
     // rows of all parts, of either kernel (one comes after the other)
-    constexpr size_t few = (size_t)kRuns * 2 * 8 * kMaxNT, many = (size_t)kPagedBlocks * 2 * kFp4PromptWide;
-    L.joins = take(sizeof(int4) * kRuns);
+    constexpr size_t few = (size_t)kPagedBlocks * 2 * 8 * kMaxNT, many = (size_t)kPagedBlocks * 2 * kFp4PromptWide;
+    L.joins = take(sizeof(int4) * kPagedBlocks);
     L.ml = take(sizeof(float2) * (few > many ? few : many));
     L.o = take(sizeof(float) * (few > many ? few : many) * (size_t)a.D);
     if (a.sel_width > 0) {
@@ -637,9 +663,9 @@ Layout layout(const PagedForwardArgs& a) {
 template <int D, int NT, int kMode>
 bsa_status launch_rows(const Fp4Params& P, cudaStream_t stream) {
     using C = Cfg<D, NT>;
-    constexpr size_t most = C::kSmem > 3 * sizeof(int32_t) * 16384 ? C::kSmem : 3 * sizeof(int32_t) * 16384;  // (of 16384 sequences)
+    constexpr size_t most = 128 + C::kSmem > 3 * sizeof(int32_t) * 16384 ? 128 + C::kSmem : 128 + 3 * sizeof(int32_t) * 16384;  // (of 16384 sequences)
     const size_t lists = 3 * sizeof(int32_t) * (size_t)P.b.seqs;
-    const size_t smem = C::kSmem > lists ? C::kSmem : lists;
+    const size_t smem = 128 + (C::kSmem > lists ? C::kSmem : lists);
     static DeviceSetup setup;
     static int sms[kMaxDevices];
     int dev = 0;
@@ -650,9 +676,8 @@ bsa_status launch_rows(const Fp4Params& P, cudaStream_t stream) {
                    cudaSuccess;
     });
     if (!ready) return BSA_ERR_CUDA;
-    const int want = sms[dev] * C::kBlocks;
-    const int grid = want < kRuns ? want : kRuns;
-    if (launch_chained(k_fp4_rows<D, NT, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P) != cudaSuccess ||
+    const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
+    if (launch_chained(k_fp4_rows<D, NT, kMode>, dim3((unsigned)grid), C::kThreads, smem, stream, P) != cudaSuccess ||
         launch_chained(k_fp4_join<D, 8 * NT, 1>, dim3((unsigned)grid, 8 * NT), kFp4JoinThreads, 0, stream, P) !=
             cudaSuccess)
         return BSA_ERR_CUDA;
@@ -683,6 +708,17 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     P.v_gain = x.v_gain;
     P.q = static_cast<const __nv_bfloat16*>(a.q);
     P.q_stride = a.q_stride;
+    if (a.page < kFp4LongPage) {
+        const cuuint64_t row = (cuuint64_t)a.page * a.D / 2, dims[2] = {row / 8, (cuuint64_t)a.n_pages * a.H_kv};
+        const cuuint32_t box[2] = {(cuuint32_t)(row / 8), 1}, ones[2] = {1, 1};
+        auto enc = get_encode();
+        auto encode = [&](CUtensorMap* map, const void* base) {
+            return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<void*>(base), dims, &row, box, ones,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        };
+        if (!encode(&P.map_k, a.k_cache) || !encode(&P.map_v, a.v_cache)) return BSA_ERR_CUDA;
+    }
     P.H = a.H;
     P.H_kv = a.H_kv;
     P.group = a.H / a.H_kv;

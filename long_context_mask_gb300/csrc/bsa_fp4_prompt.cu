@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     using C = Cfg<D>;
     constexpr uint32_t S = C::kTiles, CS = C::kCodeStages;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (an offset, not a rounded pointer: the compiler has to see that it is shared memory)
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const uint32_t s_q = smem_u32(smem), s_k = s_q + C::kTile, s_v = s_k + S * C::kTile;
     uint8_t* const codes = smem + C::kTile * (1 + 2 * S);
     Shared& sh = *reinterpret_cast<Shared*>(smem + C::kData);
@@ -339,12 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                         break;
                     }
                     const uint32_t bar = smem_u32(&sh.code_full[at]), to = ring + at * C::kStage;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(held * page * D));
+                    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * fp4_code_bytes(page, held, D / 2));
                     __syncwarp();
-                    if (mine) {
-                        bulk_load(to + lane_page * page * (D / 2), P.k + (int64_t)cur * (D / 2), page * (D / 2), bar);
-                        bulk_load(to + C::kCodes + lane_page * page * (D / 2), P.v + (int64_t)cur * (D / 2), page * (D / 2), bar);
-                    }
+                    const int32_t here = mine ? cur : -1, first = __shfl_sync(0xffffffffu, cur, (j - w0) * N);
+                    const bool live = lane_tile == j - w0;
+                    const uint32_t place = to + lane_page * page * (D / 2);
+                    fp4_load_codes(P.k, &P.map_k, page, D / 2, live, here, first, place, bar);
+                    fp4_load_codes(P.v, &P.map_v, page, D / 2, live, here, first, place + C::kCodes, bar);
                     __syncwarp();
 #pragma unroll
                     for (int x = 0; x < kCopies; ++x) {

@@ -9,6 +9,7 @@
 // that a call's result does not depend on timing.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -23,6 +24,7 @@ namespace bsa {
 constexpr float kFp4Ln2 = 0.6931471805599453f;
 
 struct Fp4Params {
+    CUtensorMap map_k, map_v;  // codes of short pages: a row a page and head
     PagedBatch b;
     const uint8_t *k, *k_scale, *v, *v_scale;
     const float *k_gain, *v_gain;
@@ -226,6 +228,26 @@ struct Fp4Work {
     }
 };
 
+// The codes of pages, a lane each, to shared memory; every thread of the warp calls it.  Lane l has page l % N
+// of its tile (cache row `row`, -1: none; `first`: of the tile's first page; live: the tile is there), dst its
+// place.  Long pages come by a bulk copy each.  Short ones come four to a copy (a bulk copy keeps the
+// issuing warp some 100 cycles: pages of 16 and one copy each, 155 us where pages of 128 took 115): a page behind the
+// sequence's end as the tile's first.  Returns the bytes that a tile's first lane has to expect.
+constexpr int32_t kFp4LongPage = 64;
+__device__ __forceinline__ uint32_t fp4_code_bytes(int32_t page, int32_t pages_there, int32_t row_bytes) {
+    return (uint32_t)((page < kFp4LongPage ? 128 / page : pages_there) * page * row_bytes);
+}
+__device__ __forceinline__ void fp4_load_codes(const uint8_t* codes, const CUtensorMap* map, int32_t page, int32_t row_bytes, bool live,
+                                               int32_t row, int32_t first, uint32_t dst, uint32_t bar) {
+    if (page >= kFp4LongPage) {
+        if (row >= 0) bulk_load(dst, codes + (int64_t)row * row_bytes, page * row_bytes, bar);
+        return;
+    }
+    const int32_t y = (row >= 0 ? row : max(first, 0)) / page;  // (a cache row is a multiple of the page)
+    const int32_t y1 = __shfl_down_sync(0xffffffffu, y, 1), y2 = __shfl_down_sync(0xffffffffu, y, 2), y3 = __shfl_down_sync(0xffffffffu, y, 3);
+    if (live && (threadIdx.x & 3) == 0) tma_gather4(dst, map, 0, y, y1, y2, y3, bar);
+}
+
 // A row tile's part in a run, as a kernel's loading warp tells the others.
 struct Fp4Segment {
     int32_t n;              // key tiles (0: no key at all; -1: no more segments)
@@ -233,6 +255,7 @@ struct Fp4Segment {
     int32_t row0, nrows;    // rows (token of the sequence * group + head)
     int32_t pos_of0, kl;    // position of the sequence's first new token, keys in the cache
     int32_t part;           // -1: the whole row tile is here; else its part slot: 2 block + 0 or 1
+    int32_t seq, tile;      // the sequence; the row tile's number within the head
     int32_t j0, lo, ns;     // key tile j (j0 .. j0 + n - 1) is j < ns ? j : lo + j - ns (without lists)
 };
 
@@ -262,6 +285,8 @@ struct Fp4Walk {
         sg.n = j1 - sg.j0;
         sg.kvh = kvh;
         sg.q0 = q.q0;
+        sg.seq = s;
+        sg.tile = i;
         work.rows(t, q.nq, sg.row0, sg.nrows);
         sg.pos_of0 = q.kl - q.nq;
         sg.kl = q.kl;
