@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
     int32_t* const status = P.b.status;
     if (threadIdx.x == kThreads - 1) {
         for (uint32_t x = 0; x < S; ++x) {
-            mbar_init(smem_u32(&sh.full[x]), 2 * (1 + (P.b.page < kFp4LongPage ? 32 : 0)));
+            mbar_init(smem_u32(&sh.full[x]), 2);
             mbar_init(smem_u32(&sh.empty[x]), kTeam);
         }
         for (int x = 0; x < kDesc; ++x) {
@@ -157,20 +157,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
 
     // ---------------------------------------------------------------- loading warps
     // The K (V) tiles of a segment, whose numbers in the run begin at g, four at a time: lane l has page
-    // l % N of tile l / N.  Codes: see fp4_load_codes; scales come by a bulk copy a page from long pages,
-    // else 16 bytes a lane.
+    // l % N of tile l / N.
     auto load_tiles = [&](const Fp4Segment& sg, bool is_v, uint32_t& g) -> bool {
-        constexpr int kAtOnce = 4, kCopies = C::kScales / 512, kBytes = D / 16;  // (scales of a row)
+        constexpr int kAtOnce = 4;
         const int32_t page = P.b.page, N = 128 / page;  // pages of a tile
         const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
-        const int32_t page_codes = page * (D / 2), page_scales = page * kBytes;
-        const bool short_pages = page < kFp4LongPage;
         const int32_t j0 = sg.j0, j1 = j0 + sg.n, kvh = sg.kvh;
         const int32_t* table = P.b.table + (int64_t)sg.seq * P.b.max_pages;
         const int32_t* list = kLists ? P.list + Work{P}.list_of(kvh, sg.tile) * P.cap : nullptr;
         const uint8_t *codes = is_v ? P.v : P.k, *scales = is_v ? P.v_scale : P.k_scale;
-        const uint32_t to_codes = smem_u32(smem) + (is_v ? C::kCodes : 0) + lane_page * page_codes;
-        const uint32_t to_scales = smem_u32(smem) + 2 * C::kCodes + (is_v ? C::kScales : 0);
+        const CUtensorMap *map = is_v ? &P.map_v : &P.map_k, *map_s = is_v ? &P.map_vs : &P.map_ks;
+        const uint32_t to_codes = smem_u32(smem) + (is_v ? C::kCodes : 0) + lane_page * page * (D / 2);
+        const uint32_t to_scales = smem_u32(smem) + 2 * C::kCodes + (is_v ? C::kScales : 0) + lane_page * page * (D / 16);
         // the cache row of this lane's page (-1: behind the sequence's end, or no tile), and the tile's first key
         auto fetch = [&](int32_t jb, int32_t& key) -> int32_t {
             const int32_t j = jb + lane_tile;
@@ -195,37 +193,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
             const uint32_t gl = g + (live ? lane_tile : 0), at = gl % S, bar = smem_u32(&sh.full[at]);
             if (!wait_warp(smem_u32(&sh.empty[at]), ((gl / S) & 1u) ^ 1u, &sh.watch, status)) return false;
             const uint32_t held = __ballot_sync(0xffffffffu, row >= 0);
+            const int32_t first = __shfl_sync(0xffffffffu, row, lane - lane_page);
             if (live && lane_page == 0) {
-                const int32_t pages = __popc(held >> lane & ((1u << N) - 1u));
                 if (!is_v) sh.key[at] = key;
-                mbar_arrive_expect_tx(bar, fp4_code_bytes(page, pages, D / 2) + (uint32_t)(short_pages ? 0 : pages * page_scales));
+                mbar_arrive_expect_tx(bar, fp4_page_bytes(page, __popc(held >> lane & ((1u << N) - 1u)), D / 2 + D / 16));
             }
             __syncwarp();
-            fp4_load_codes(codes, is_v ? &P.map_v : &P.map_k, page, D / 2, live, row,
-                           __shfl_sync(0xffffffffu, row, lane - lane_page), to_codes + at * C::kStage, bar);
-            if (row >= 0 && !short_pages)
-                bulk_load(to_scales + at * C::kStage + lane_page * page_scales, scales + (int64_t)row * kBytes, page_scales, bar);
+            fp4_load_pages(codes, map, page, D / 2, live, row, first, to_codes + at * C::kStage, bar);
+            fp4_load_pages(scales, map_s, page, D / 16, live, row, first, to_scales + at * C::kStage, bar);
             __syncwarp();
-            if (short_pages) {
-                for (int32_t x = 0; x < tiles; ++x) {
-                    const uint32_t slot = (g + x) % S;
-#pragma unroll
-                    for (int y = 0; y < kCopies; ++y) {
-                        const int32_t byte = y * 512 + lane * 16, pg = byte / page_scales;
-                        const int32_t from = __shfl_sync(0xffffffffu, row, x * N + pg);
-                        if (from >= 0)
-                            cp_async16(to_scales + slot * C::kStage + byte, scales + (int64_t)from * kBytes + byte - pg * page_scales);
-                    }
-                    cp_async_arrive_noinc(smem_u32(&sh.full[slot]));
-                }
-            }
             g += tiles;
         }
         return true;
     };
     // (every issued copy must land before the block exits)
     auto land = [&](uint32_t g) {
-        cp_async_wait_all();
         if (lane == 0)
             for (uint32_t x = g > S ? g - S : 0; x < g; ++x) paged_drain(smem_u32(&sh.full[x % S]), (x / S) & 1u, status);
         __syncwarp();
@@ -709,15 +691,18 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     P.q = static_cast<const __nv_bfloat16*>(a.q);
     P.q_stride = a.q_stride;
     if (a.page < kFp4LongPage) {
-        const cuuint64_t row = (cuuint64_t)a.page * a.D / 2, dims[2] = {row / 8, (cuuint64_t)a.n_pages * a.H_kv};
-        const cuuint32_t box[2] = {(cuuint32_t)(row / 8), 1}, ones[2] = {1, 1};
         auto enc = get_encode();
-        auto encode = [&](CUtensorMap* map, const void* base) {
-            return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<void*>(base), dims, &row, box, ones,
+        // (in elements of eight bytes: a box is at most 256 of them long)
+        auto encode = [&](CUtensorMap* map, const void* base, int32_t row_bytes) {
+            const cuuint64_t bytes = (cuuint64_t)a.page * row_bytes, dims[2] = {bytes / 8, (cuuint64_t)a.n_pages * a.H_kv};
+            const cuuint32_t box[2] = {(cuuint32_t)(bytes / 8), 1}, ones[2] = {1, 1};
+            return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<void*>(base), dims, &bytes, box, ones,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
         };
-        if (!encode(&P.map_k, a.k_cache) || !encode(&P.map_v, a.v_cache)) return BSA_ERR_CUDA;
+        if (!encode(&P.map_k, a.k_cache, a.D / 2) || !encode(&P.map_v, a.v_cache, a.D / 2) ||
+            !encode(&P.map_ks, x.k_scale, a.D / 16) || !encode(&P.map_vs, x.v_scale, a.D / 16))
+            return BSA_ERR_CUDA;
     }
     P.H = a.H;
     P.H_kv = a.H_kv;

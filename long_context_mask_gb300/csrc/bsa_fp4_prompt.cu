@@ -42,11 +42,11 @@ constexpr float kSumLimit = 32768.0f;                     // 2^15, see softmax_r
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 384;
-constexpr int kLoad = 0, kMmaQK = 1, kMmaPV = 2, kSoftmax0 = 4, kSoftmaxWarps = 8, kUnpackV0 = 12, kUnpackK0 = 16,
+constexpr int kLoad = 0, kMmaQK = 1, kMmaPV = 2, kLoadV = 3, kSoftmax0 = 4, kSoftmaxWarps = 8, kUnpackV0 = 12, kUnpackK0 = 16,
               kUnpackWarps = 4;
 constexpr int kThreads = 32 * 20;
 constexpr int kDesc = 4;                                  // segment descriptors in flight
-constexpr int kReaders = 2 + kSoftmaxWarps + 2 * kUnpackWarps;  // warps that read a descriptor
+constexpr int kReaders = 3 + kSoftmaxWarps + 2 * kUnpackWarps;  // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 fp16
 
 enum { kPlain = 0, kWindow = 1 };
@@ -191,10 +191,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     int32_t* const status = P.b.status;
+    // pages of 16 have too many copies for one warp (a prompt of 8192: 542 us with one, 484 with two; longer pages 459, 475)
+    const bool two_load = P.b.page < 32;
 
     if (threadIdx.x == kThreads - 1) {
         for (int x = 0; x < 3; ++x) {
-            mbar_init(smem_u32(&sh.code_full[x]), 33);
+            mbar_init(smem_u32(&sh.code_full[x]), two_load ? 2 : 1);
             mbar_init(smem_u32(&sh.code_empty[x]), 2 * kUnpackWarps);
         }
         for (int x = 0; x < 4; ++x) {
@@ -273,23 +275,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     };
 
     if (warp < kSoftmax0) {
+        // The codes and scales of a segment's tiles, whose numbers in the run begin at g: K's, V's or both.
+        auto load_tiles = [&](const Fp4Segment& sg, bool k_too, bool v_too, uint32_t& g) -> bool {
+            const int32_t page = P.b.page, N = 128 / page, per_window = page >> 2;  // pages of a tile; tiles whose pages one read of 32 lanes brings
+            const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
+            const int32_t j0 = sg.j0, j1 = j0 + sg.n;
+            const int32_t* table = P.b.table + (int64_t)sg.seq * P.b.max_pages;
+            const uint32_t to_codes = smem_u32(codes) + lane_page * page * (D / 2);
+            const uint32_t to_scales = smem_u32(codes) + 2 * C::kCodes + lane_page * page * (D / 16);
+            // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
+            // sequence's end)
+            auto fetch = [&](int32_t w0) -> int32_t {
+                const int32_t j = w0 + lane_tile;
+                if (j >= j1) return -1;
+                const int32_t pg = (j < sg.ns ? j : sg.lo + j - sg.ns) * N + lane_page;
+                if (pg * page >= sg.kl) return -1;
+                int32_t id = table[pg];
+                if (id < 0 || id >= P.b.n_pages) {
+                    raise_status(status, BSA_ERR_BOUNDS);
+                    id = 0;  // (this row's result is unspecified)
+                }
+                return (id * P.H_kv + sg.kvh) * page;
+            };
+            int32_t w0 = j0, cur = fetch(j0), nxt = fetch(j0 + per_window);
+            for (int32_t j = j0; j < j1; ++j, ++g) {
+                if (j >= w0 + per_window) {
+                    w0 += per_window;
+                    cur = nxt;
+                    nxt = fetch(w0 + per_window);
+                }
+                const bool live = lane_tile == j - w0;
+                const int32_t row = live ? cur : -1, first = __shfl_sync(0xffffffffu, cur, (j - w0) * N);
+                const int32_t held = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                const uint32_t at = g % CS, bar = smem_u32(&sh.code_full[at]), stage = at * C::kStage;
+                if (!wait_warp(smem_u32(&sh.code_empty[at]), ((g / CS) & 1u) ^ 1u, &sh.watch, status)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(bar, (k_too && v_too ? 2 : 1) * fp4_page_bytes(page, held, D / 2 + D / 16));
+                __syncwarp();
+                if (k_too) {
+                    fp4_load_pages(P.k, &P.map_k, page, D / 2, live, row, first, to_codes + stage, bar);
+                    fp4_load_pages(P.k_scale, &P.map_ks, page, D / 16, live, row, first, to_scales + stage, bar);
+                }
+                if (v_too) {
+                    fp4_load_pages(P.v, &P.map_v, page, D / 2, live, row, first, to_codes + stage + C::kCodes, bar);
+                    fp4_load_pages(P.v_scale, &P.map_vs, page, D / 16, live, row, first, to_scales + stage + C::kScales, bar);
+                }
+                __syncwarp();
+            }
+            return true;
+        };
+        // (every issued copy must land before the block exits)
+        auto land = [&](uint32_t g) {
+            if (lane == 0)
+                for (uint32_t x = g > CS ? g - CS : 0; x < g; ++x)
+                    paged_drain(smem_u32(&sh.code_full[x % CS]), (x / CS) & 1u, status);
+            __syncwarp();
+        };
         if (warp == kLoad) {
             // -------------------------------------------------------- segments, codes and scales
             Fp4Walk<kWide, row_cost(kMode), false> walk(P, run, sh.start);
             Fp4Segment sg;
             uint32_t k = 0, g = 0;  // segments and tiles so far
             bool ok = true;
-            const int32_t page = P.b.page, N = 128 / page, per_window = page >> 2;
-            const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
-            const uint32_t ring = smem_u32(codes);
-            constexpr int kCopies = C::kScales / 512, kBytes = D / 16;  // of scales, 16 bytes a lane; a row's
-            const int32_t page_scales = page * kBytes;
-            int32_t sc_page[kCopies], sc_at[kCopies];
-#pragma unroll
-            for (int x = 0; x < kCopies; ++x) {
-                sc_page[x] = (x * 512 + lane * 16) / page_scales;
-                sc_at[x] = (x * 512 + lane * 16) % page_scales;
-            }
             for (; ok && walk.open(sg); walk.advance()) {
                 if (!wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
                     ok = false;
@@ -309,56 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
 #pragma unroll
                     for (int d = 0; d < D; d += 64) prefetch_l2(src + d);
                 }
-                const int32_t j0 = sg.j0, j1 = j0 + sg.n;
-                const int32_t* table = P.b.table + (int64_t)walk.s * P.b.max_pages;
-                // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
-                // sequence's end)
-                auto fetch = [&](int32_t w0) -> int32_t {
-                    const int32_t j = w0 + lane_tile;
-                    if (j >= j1) return -1;
-                    const int32_t pg = (j < sg.ns ? j : sg.lo + j - sg.ns) * N + lane_page;
-                    if (pg * page >= sg.kl) return -1;
-                    int32_t id = table[pg];
-                    if (id < 0 || id >= P.b.n_pages) {
-                        raise_status(status, BSA_ERR_BOUNDS);
-                        id = 0;  // (this row's result is unspecified)
-                    }
-                    return (id * P.H_kv + sg.kvh) * page;
-                };
-                int32_t w0 = j0, cur = fetch(j0), nxt = fetch(j0 + per_window);
-                for (int32_t j = j0; j < j1; ++j, ++g) {
-                    if (j >= w0 + per_window) {
-                        w0 += per_window;
-                        cur = nxt;
-                        nxt = fetch(w0 + per_window);
-                    }
-                    const bool mine = lane_tile == j - w0 && cur >= 0;
-                    const int32_t held = __popc(__ballot_sync(0xffffffffu, mine));
-                    const uint32_t at = g % CS;
-                    if (!wait_warp(smem_u32(&sh.code_empty[at]), ((g / CS) & 1u) ^ 1u, &sh.watch, status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = smem_u32(&sh.code_full[at]), to = ring + at * C::kStage;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * fp4_code_bytes(page, held, D / 2));
-                    __syncwarp();
-                    const int32_t here = mine ? cur : -1, first = __shfl_sync(0xffffffffu, cur, (j - w0) * N);
-                    const bool live = lane_tile == j - w0;
-                    const uint32_t place = to + lane_page * page * (D / 2);
-                    fp4_load_codes(P.k, &P.map_k, page, D / 2, live, here, first, place, bar);
-                    fp4_load_codes(P.v, &P.map_v, page, D / 2, live, here, first, place + C::kCodes, bar);
-                    __syncwarp();
-#pragma unroll
-                    for (int x = 0; x < kCopies; ++x) {
-                        const int32_t row = __shfl_sync(0xffffffffu, cur, (j - w0) * N + sc_page[x]);
-                        if (row >= 0) {
-                            const int64_t from = (int64_t)row * kBytes + sc_at[x];
-                            cp_async16(to + 2 * C::kCodes + x * 512 + lane * 16, P.k_scale + from);
-                            cp_async16(to + 2 * C::kCodes + C::kScales + x * 512 + lane * 16, P.v_scale + from);
-                        }
-                    }
-                    cp_async_arrive_noinc(bar);
-                }
+                ok = load_tiles(sg, true, !two_load, g);
             }
             if (ok && wait_warp(smem_u32(&sh.seg_empty[k % kDesc]), ((k / kDesc) & 1u) ^ 1u, &sh.watch, status)) {
                 if (lane == 0) {
@@ -369,12 +366,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                 ok = false;
             }
             if (!ok && lane == 0) set_abort(&sh.watch, status);
-            // every issued copy must land before the block exits
-            cp_async_wait_all();
-            if (lane == 0)
-                for (uint32_t x = g > CS ? g - CS : 0; x < g; ++x)
-                    paged_drain(smem_u32(&sh.code_full[x % CS]), (x / CS) & 1u, status);
-            __syncwarp();
+            land(g);
+        } else if (warp == kLoadV) {
+            // -------------------------------------------------------- V's codes, of short pages
+            uint32_t g = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const Fp4Segment* sp = next_segment(k, ok);
+                if (sp == nullptr) break;
+                const Fp4Segment sg = *sp;
+                hand_back(k);
+                if (two_load) ok = load_tiles(sg, false, true, g);
+            }
+            if (!ok && lane == 0) set_abort(&sh.watch, status);
+            land(g);
         } else if (warp == kMmaQK) {
             // -------------------------------------------------------- S = Q K^T
             // (the whole warp walks the schedule; one elected lane issues a tile's MMAs

@@ -24,7 +24,7 @@ namespace bsa {
 constexpr float kFp4Ln2 = 0.6931471805599453f;
 
 struct Fp4Params {
-    CUtensorMap map_k, map_v;  // codes of short pages: a row a page and head
+    CUtensorMap map_k, map_ks, map_v, map_vs;  // codes and scales of short pages: a row a page and head
     PagedBatch b;
     const uint8_t *k, *k_scale, *v, *v_scale;
     const float *k_gain, *v_gain;
@@ -228,24 +228,25 @@ struct Fp4Work {
     }
 };
 
-// The codes of pages, a lane each, to shared memory; every thread of the warp calls it.  Lane l has page l % N
-// of its tile (cache row `row`, -1: none; `first`: of the tile's first page; live: the tile is there), dst its
-// place.  Long pages come by a bulk copy each.  Short ones come four to a copy (a bulk copy keeps the
-// issuing warp some 100 cycles: pages of 16 and one copy each, 155 us where pages of 128 took 115): a page behind the
-// sequence's end as the tile's first.  Returns the bytes that a tile's first lane has to expect.
+// Codes (or scales) of pages, a lane each, to shared memory; every thread of the warp calls it.  Lane l has
+// page l % N of its tile (cache row `row`, -1: none; `first`: of the tile's first page; live: the tile is there),
+// dst its place, row_bytes a row's bytes.  Long pages come by a bulk copy each.  Short ones come four to a
+// copy, a page behind the sequence's end as the tile's first: every copy keeps the issuing warp some 100
+// cycles (64 tokens over pages of 16: 155 us with a copy a page, where pages of 128 took 115).
 constexpr int32_t kFp4LongPage = 64;
-__device__ __forceinline__ uint32_t fp4_code_bytes(int32_t page, int32_t pages_there, int32_t row_bytes) {
-    return (uint32_t)((page < kFp4LongPage ? 128 / page : pages_there) * page * row_bytes);
-}
-__device__ __forceinline__ void fp4_load_codes(const uint8_t* codes, const CUtensorMap* map, int32_t page, int32_t row_bytes, bool live,
+__device__ __forceinline__ void fp4_load_pages(const uint8_t* src, const CUtensorMap* map, int32_t page, int32_t row_bytes, bool live,
                                                int32_t row, int32_t first, uint32_t dst, uint32_t bar) {
     if (page >= kFp4LongPage) {
-        if (row >= 0) bulk_load(dst, codes + (int64_t)row * row_bytes, page * row_bytes, bar);
+        if (row >= 0) bulk_load(dst, src + (int64_t)row * row_bytes, page * row_bytes, bar);
         return;
     }
-    const int32_t y = (row >= 0 ? row : max(first, 0)) / page;  // (a cache row is a multiple of the page)
+    const int32_t y = (row >= 0 ? row : max(first, 0)) >> (__ffs(page) - 1);  // (a multiple of the page)
     const int32_t y1 = __shfl_down_sync(0xffffffffu, y, 1), y2 = __shfl_down_sync(0xffffffffu, y, 2), y3 = __shfl_down_sync(0xffffffffu, y, 3);
     if (live && (threadIdx.x & 3) == 0) tma_gather4(dst, map, 0, y, y1, y2, y3, bar);
+}
+// What a tile's first lane has to expect of that, pages_there of the tile's being there.
+__device__ __forceinline__ uint32_t fp4_page_bytes(int32_t page, int32_t pages_there, int32_t row_bytes) {
+    return (uint32_t)((page < kFp4LongPage ? 128 / page : pages_there) * page * row_bytes);
 }
 
 // A row tile's part in a run, as a kernel's loading warp tells the others.
