@@ -97,7 +97,6 @@ struct Shared {
     Watch watch;
     Fp4Segment seg[kDesc];
     int32_t key[Cfg<D, NT>::kStages]; // first key of the tile in each slot
-    int64_t prefix[33];
     Fp4Start start;
     float2 ml[Cfg<D, NT>::kWarps][8 * NT];
 };
@@ -147,13 +146,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
 
     // ---------------------------------------------------------------- this block's run
     // (its scratch is in the ring, which is free here)
-    Fp4Run run;
     using Work = Fp4Work<R, kRowCost, kLists>;
-    if (!Work{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run)) return;
+    constexpr int kScan = kLists ? kThreads : 128;  // (lists: many counts to read)
+    if (threadIdx.x < kScan) Work{P}.template find<kScan>(reinterpret_cast<int32_t*>(smem), sh.start);
     // what was written there by ordinary stores makes room for bulk copies
     fence_proxy_async_smem();
     __syncthreads();
-    if (sh.watch.abort != 0) return;
+    if (sh.start.any == 0 || sh.watch.abort != 0) return;
 
     // ---------------------------------------------------------------- loading warps
     // The K (V) tiles of a segment, whose numbers in the run begin at g, four at a time: lane l has page
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
     bool ok = true;
     if (warp == kLoadK) {
         // ------------------------------------------------------------ segments, query rows and K tiles
-        Fp4Walk<R, kRowCost, kLists> walk(P, run, sh.start);
+        Fp4Walk<R, kRowCost, kLists> walk(P, sh.start);
         Fp4Segment sg;
         uint32_t g = 0;  // tiles so far
         for (; ok && walk.open(sg); walk.advance()) {

@@ -79,7 +79,6 @@ struct Shared {
     Fp4Segment seg[kDesc];
     float fac[kDesc][kWide];  // of a segment's rows: what turns a product of operands into a score (log2)
     float2 ml[kWide];         // of a segment's rows: maximum (log2) and sum
-    int64_t prefix[33];
     Fp4Start start;
     uint32_t tmem_base;
 };
@@ -231,10 +230,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
         sh.watch.abort = *reinterpret_cast<const volatile int32_t*>(status) == BSA_ERR_TIMEOUT;
     }
     // this block's run (the scratch is in the data area, which is free here)
-    Fp4Run run;
-    if (!Fp4Work<kWide, row_cost(kMode), false>{P}.template find<kThreads>(reinterpret_cast<int32_t*>(smem), sh.prefix, sh.start, run))
-        return;
+    constexpr int kScan = 256;
+    if (threadIdx.x < kScan)
+        Fp4Work<kWide, row_cost(kMode), false>{P}.template find<kScan>(reinterpret_cast<int32_t*>(smem), sh.start);
     __syncthreads();
+    if (sh.start.any == 0) return;
     const bool abandoned = sh.watch.abort != 0;
     if (warp == kMmaQK && !abandoned) {
         __syncwarp();
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
         };
         if (warp == kLoad) {
             // -------------------------------------------------------- segments, codes and scales
-            Fp4Walk<kWide, row_cost(kMode), false> walk(P, run, sh.start);
+            Fp4Walk<kWide, row_cost(kMode), false> walk(P, sh.start);
             Fp4Segment sg;
             uint32_t k = 0, g = 0;  // segments and tiles so far
             bool ok = true;

@@ -76,11 +76,40 @@ struct Fp4Run {
         return (int32_t)(u < longer ? fp4_divide(u, share + 1) : extra + fp4_divide(u - longer, share));
     }
 };
-// Its first unit (shared memory).
+// Its first unit, and what all threads have to know of it (shared memory).
 struct Fp4Start {
     int32_t kvh, s, t, i, x0;  // head, sequence, row tile of the sequence and of the head, unit within the row tile
     PagedSeq q;
+    Fp4Run run;
+    int32_t any;               // 0: this thread block has no run
+    int64_t part[20];          // of the prefix sums
 };
+
+// Exclusive prefix sum over the first kScan threads of the block, which alone call it.
+template <int kScan>
+__device__ __forceinline__ int64_t fp4_prefix(int64_t x, int64_t* part, int64_t& total) {
+    constexpr int warps = kScan / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kScan) : "memory"); };
+    meet();  // an earlier call's readers are done with part
+    if (lane == 31) part[warp] = incl;
+    meet();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < warps; ++w) {
+        const int64_t v = part[w];
+        before += w < warp ? v : 0;
+        all += v;
+    }
+    total = all;
+    return before + incl - x;
+}
 
 // kCost: a row tile of n key tiles counts n + kCost in a run, the constant for its start and its end.
 template <int kWide, int kCost, bool kLists>
@@ -124,16 +153,16 @@ struct Fp4Work {
     // a cut x units into a row tile leaves so many of its key tiles on the left
     static __device__ __forceinline__ int32_t cut_at(int32_t x) { return max(x - kCost, 0); }
 
-    // This thread block's run and its first unit; false: it has none.  Called by all kThreads of the
-    // block.  scratch: 3 seqs words of shared memory; prefix: see block_prefix.  The caller puts a
-    // __syncthreads() between this and what uses `start` or writes to scratch.
-    template <int kThreads>
-    __device__ __forceinline__ bool find(int32_t* scratch, int64_t* prefix, Fp4Start& start, Fp4Run& run) const {
+    // This thread block's run and its first unit, by the first kScan threads of the block (which alone
+    // call it; the others would only wait for one another).  scratch: 3 seqs words of shared memory.  The
+    // caller puts a __syncthreads() between this and what uses `start` or writes to scratch.
+    template <int kScan>
+    __device__ __forceinline__ void find(int32_t* scratch, Fp4Start& start) const {
         // of sequence s: the row tiles of the sequences before it, its new tokens and its length
         int32_t *cum = scratch, *seq_nq = cum + P.b.seqs, *seq_kl = seq_nq + P.b.seqs;
         int32_t nt;
         {
-            const int32_t per = (P.b.seqs + kThreads - 1) / kThreads;
+            const int32_t per = (P.b.seqs + kScan - 1) / kScan;
             const int32_t a = min((int32_t)threadIdx.x * per, P.b.seqs), e = min(a + per, P.b.seqs);
             int64_t mine = 0, all;
             for (int32_t s = a; s < e; ++s) {
@@ -143,7 +172,7 @@ struct Fp4Work {
                 seq_kl[s] = q.kl;
                 mine += tiles(q.nq);
             }
-            int64_t at = block_prefix<kThreads>(mine, prefix, all);
+            int64_t at = fp4_prefix<kScan>(mine, start.part, all);
             for (int32_t s = a; s < e; ++s) {
                 cum[s] = (int32_t)min(at, (int64_t)INT32_MAX);
                 at += tiles(seq_nq[s]);
@@ -152,9 +181,9 @@ struct Fp4Work {
             const int64_t most = kLists ? (int64_t)P.nt_cap * per_token() : (int64_t)P.b.tokens * P.group / kWide + P.b.seqs;
             nt = (int32_t)min(all, most);
         }
-        __syncthreads();
+        asm volatile("bar.sync 1, %0;" ::"n"(kScan) : "memory");
         const int64_t rows = kLists ? (int64_t)nt * P.H_kv : nt;  // tiles whose counts differ
-        const int64_t per_row = fp4_divide(rows + kThreads - 1, kThreads);
+        const int64_t per_row = fp4_divide(rows + kScan - 1, kScan);
         const int64_t f0 = min((int64_t)threadIdx.x * per_row, rows), f1 = min(f0 + per_row, rows);
         // walks this thread's tiles: visit(kvh, i, s, t, units)
         auto walk = [&](auto&& visit) {
@@ -191,13 +220,17 @@ struct Fp4Work {
             only = make_int4(kvh, s, t, i);
             return false;
         });
-        const int64_t before = block_prefix<kThreads>(mine, prefix, total);
+        const int64_t before = fp4_prefix<kScan>(mine, start.part, total);
         const int64_t all = kLists ? total : total * P.H_kv;
         const int32_t blocks = (int32_t)min((int64_t)gridDim.x, all);
-        if ((int32_t)blockIdx.x >= blocks) return false;
+        const bool any = (int32_t)blockIdx.x < blocks;
+        if (threadIdx.x == 0) start.any = any;
+        if (!any) return;
+        Fp4Run run;
         run.share = fp4_divide(all, blocks);
         run.extra = (int32_t)(all - run.share * blocks);
         run.nt = nt;
+        if (threadIdx.x == 0) start.run = run;
         const int64_t u0 = run.start(blockIdx.x), head = kLists ? 0 : fp4_divide(u0, total), x = kLists ? u0 : u0 - head * total;
         if (x >= before && x < before + mine) {
             auto begin = [&](int32_t kvh, int32_t s, int32_t t, int32_t i, int64_t at) {
@@ -224,7 +257,6 @@ struct Fp4Work {
                 });
             }
         }
-        return true;
     }
 };
 
@@ -270,8 +302,8 @@ struct Fp4Walk {
     PagedSeq q;
     bool last;  // the run ends within the row tile
 
-    __device__ __forceinline__ Fp4Walk(const Fp4Params& P, const Fp4Run& r, const Fp4Start& a)
-        : work{P}, run(r), u(r.start(blockIdx.x)), u_end(r.start(blockIdx.x + 1)), kvh(a.kvh), s(a.s), t(a.t), i(a.i), x0(a.x0),
+    __device__ __forceinline__ Fp4Walk(const Fp4Params& P, const Fp4Start& a)
+        : work{P}, run(a.run), u(a.run.start(blockIdx.x)), u_end(a.run.start(blockIdx.x + 1)), kvh(a.kvh), s(a.s), t(a.t), i(a.i), x0(a.x0),
           q(a.q) {}
     // the row tile at hand; false: no more in this run
     __device__ __forceinline__ bool open(Fp4Segment& sg) {
