@@ -718,7 +718,11 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     P.part_o = reinterpret_cast<float*>(ws + L.o);
     P.least = 1;
     P.most = INT32_MAX;
-    const bool wide = P.group > 8;  // (a token's rows in one tile)
+    // Rows of a sequence, at most, as far as the host knows.  Row tiles of 16 for tokens of more than eight rows and
+    // where some sequence has 9 to 16 (64 x 4 tokens of 4 rows over 4096: 111 us, 129 with two tiles of 8), else
+    // of 8 (64 tokens over 8192: 99 us, 138 with tiles of 16).
+    const int64_t most = (int64_t)(x.max_new > 0 && x.max_new < a.tokens ? x.max_new : a.tokens) * P.group;
+    const bool wide = P.group > 8 || (a.sel == nullptr && most > 8 && most <= kFewRows);
     if (a.sel != nullptr) {
         P.nt_cap = L.list_rows;
         P.cap = L.cap;
@@ -733,7 +737,6 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     }
     // sequences of few rows here, the others on large tiles, unless the host knows of no others (what it
     // was told may be wrong: then all of them are done here)
-    const int64_t most = (int64_t)(x.max_new > 0 && x.max_new < a.tokens ? x.max_new : a.tokens) * P.group;
     P.most = most > kFewRows ? kFewRows : INT32_MAX;
     const bsa_status c = a.window > 0 ? launch_mode<kWindow>(P, a.D, wide, stream) : launch_mode<kPlain>(P, a.D, wide, stream);
     if (c != BSA_OK || most <= kFewRows) return c;

@@ -341,7 +341,7 @@ def test_masks(causal, window, sinks, H, K, D, page):
     assert untouched(b, o, lse)
 
 
-@pytest.mark.parametrize("max_new", [0, 1, 2, 1000])
+@pytest.mark.parametrize("max_new", [0, 1, 2, 3, 4, 1000])
 def test_the_hint_does_not_matter(max_new):
     """Sequences with more and with fewer new tokens than told."""
     b = ref.make([1, 3, 90, 2], [500, 1000, 700, 2], H=8, H_kv=2, D=128, page=32, seed=25)
