@@ -24,7 +24,8 @@ SOURCES = ["bsa_api.cu", "bsa_index.cu", "bsa_scores.cu", "bsa_order.cu", "bsa_a
            "bsa_paged_attn.cu", "bsa_fp4_read.cu", "bsa_fp4_attn.cu",
            "bsa_fp4_prompt.cu"]
 HEADERS = ["bsa_internal.h", "bsa_ptx.cuh", "bsa_math.cuh", "bsa_gather0.cuh", "bsa_rows.cuh", "bsa_tma_host.h",
-           "bsa_paged.cuh", "bsa_device_setup.h", "bsa_paged_wait.cuh", "bsa_fp4.cuh", "bsa_fp4_runs.cuh"]
+           "bsa_paged.cuh", "bsa_device_setup.h", "bsa_paged_wait.cuh", "bsa_fp4.cuh",
+           "bsa_fp4_ptx.cuh", "bsa_fp4_runs.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -15,6 +15,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "bsa_fp4_ptx.cuh"
 #include "bsa_internal.h"
 #include "bsa_paged.cuh"
 #include "bsa_rows.cuh"
