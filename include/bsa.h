@@ -14,9 +14,9 @@
  *    launched.  Conditions only the device can see (an index list longer
  *    than max_kv, an index or map entry out of range, a wait that timed out)
  *    are recorded in a per-device status word: the first such code wins
- *    (a time-out of bsa_forward_paged, whose output is incomplete then,
- *    takes the place of another code) and bsa_device_status() reads and
- *    clears it.  No kernel traps.
+ *    (a time-out of bsa_forward_paged or bsa_forward_paged_fp4, whose output is
+ *    incomplete then, takes the place of another code) and
+ *    bsa_device_status() reads and clears it.  No kernel traps.
  *  - Tensors are row-major and contiguous.  "rows" of an index list are the
  *    (batch, head, query block) triples in that nesting order:
  *    row = (b * H + h) * nQB + qb.
@@ -904,7 +904,9 @@ bsa_status bsa_paged_read_fp4(const bsa_paged_batch* b, int32_t H_kv, int32_t D,
  * rounded to fp16 (2^-11 relative, 2^-25 of the largest absolute) before they
  * meet the values; sums and LSE take them unrounded.
  * What a row does not see does not matter; what it sees is always finite.  A
- * query that holds an infinity or a NaN makes its own rows' results NaN.
+ * query that holds an infinity or a NaN changes no other row's results; its
+ * own are NaN, or, where all its scores come out as -infinity, those of a row
+ * without a key (O = 0, LSE = -infinity).
  *
  *  max_new    the most new tokens that any of the sequences has, if the host
  *             knows (1 for a step of single tokens), else 0.  It decides how the

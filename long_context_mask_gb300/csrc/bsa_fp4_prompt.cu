@@ -59,7 +59,9 @@ struct Cfg {
     static constexpr int kCodeStages = 3;
     static constexpr int kCodes = 128 * D / 2, kScales = 128 * D / 16;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kData = kTile * (1 + 2 * kTiles) + kCodeStages * kStage;
+    static constexpr int kTilesData = kTile * (1 + 2 * kTiles) + kCodeStages * kStage;
+    static constexpr int kLists = 3 * 4 * 16384;          // three words for each of as many sequences as there may be
+    static constexpr int kData = kTilesData > kLists ? kTilesData : kLists;
     static constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, 0, 0);
     static constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, 0, 1);
 };
@@ -813,7 +815,6 @@ template <int D, int kMode>
 bsa_status launch_d(const Fp4Params& P, cudaStream_t stream) {
     constexpr size_t smem = 1024 + Cfg<D>::kData + sizeof(Shared);
     static_assert(smem <= 232448, "shared memory of a thread block");
-    static_assert(Cfg<D>::kData >= 3 * sizeof(int32_t) * 16384 || D == 64, "room for the sequences");
     static DeviceSetup setup;
     static int sms[kMaxDevices];
     int dev = 0;

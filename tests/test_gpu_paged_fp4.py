@@ -41,6 +41,8 @@ def check_append(b, c, q, k, v, before, q_out, k_mean, rope=None, interleaved=Fa
     filled = {}
     kg, vg = c.k_gain, c.v_gain
     for s, (n, length) in enumerate(zip(b.new, b.length)):
+        if n == 0:
+            continue
         pos = torch.arange(length - n, length, device="cuda")
         t = slice(starts[s], starts[s] + n)
         page, at = b.table[s].long()[pos // b.page], pos % b.page
