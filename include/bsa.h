@@ -829,7 +829,7 @@ size_t bsa_select_paged_workspace_size(const bsa_paged_batch* b, int32_t H, int3
  *        0.5, 1, 1.5, 2, 3, 4, 6; value 2i of a row is the low half of byte i.
  * scale  an 8-bit float e4m3 (at most 448; a negative or NaN byte, which
  *        bsa_paged_append_fp4 never writes, counts as 0).
- * gain   one fp32 number for each key/value head, positive and finite (1
+ * gain   one fp32 number for each key/value head, finite and at least 2^-126 (1
  *        where the array is NULL): the head's values should lie between some
  *        0.02 and 2688 gains, the range that scales and levels reach.
  * A row x is quantised group by group as

@@ -231,6 +231,29 @@ def test_the_longest_sequence_out_of_one_page(new, max_new, D, page):
     assert ((lse.double() - L - math.log(copies)).abs() <= 2.0 ** -12 + d + 8 * 2.0 ** -24 * (1 + L.abs() + 17)).all()
 
 
+def test_the_smallest_and_largest_gains():
+    """Gains from the smallest normal number to 2^125, with values of their sizes and zeros among them: append and read."""
+    b = ref.make([300, 1], [300, 200], H=4, H_kv=4, D=64, page=32, seed=74, poison=False)
+    c = f4.Cache(b, 74)
+    c.k_gain = torch.tensor([2.0 ** -126, 1e-20, 3e20, 2.0 ** 125], device="cuda")
+    c.v_gain = c.k_gain.flip(0).contiguous()
+    q, k, v = ref.rows(b, 4, 75), ref.rows(b, 4, 76), ref.rows(b, 4, 77)
+    k, v = ((x.double() * g.double()[:, None]).to(torch.bfloat16) for x, g in ((k, c.k_gain), (v, c.v_gain)))
+    k[:, :, 3], v[5] = 0, 0
+    before = c.clone()
+    q_out, _ = run_append(b, c, q, k, v, means=False)
+    status_ok()
+    check_append(b, c, q, k, v, before, q_out, None)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    bsa.paged_read_fp4(*c.arrays(), *b.arrays(), ko, vo, **c.gains())
+    status_ok()
+    for h in range(4):
+        for out, cache in ((ko, b.k_cache), (vo, b.v_cache)):
+            want = b.keys(0, h, cache)
+            # half a step, of the smallest numbers 2^-134
+            assert ((out[:300, h].double() - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + 2.0 ** -134).all()
+
+
 def test_a_page_may_be_there_twice():
     """Two sequences, and two places of one, share pages."""
     b = ref.make([3, 40], [500, 500], H=8, H_kv=2, D=128, page=64, seed=70, poison=False)
