@@ -5,15 +5,18 @@
 //     s_j = scale q . k_j,   LSE = ln sum_j exp(s_j),   O = sum_j exp(s_j - LSE) v_j
 // with k_j and v_j as bsa_fp4.cuh reads them.
 //
+// Here: lists, and the sequences of few rows (a step of single tokens, a few tokens each); the
+// others are bsa_fp4_prompt.cu's.
+//
 // Rows.  The new tokens of a sequence and the G query heads of a key/value head are rows,
 // token by token; a row tile is 8 NT of them (with lists: of one token).  A key tile is 128
-// positions, 16 for each of the thread block's eight warps.  Few rows want the keys as the
-// long side of the products: with mma m16n8k16, S^T = K Q^T has 16 keys by 8 rows,
-// O^T = V^T P^T has 16 values of D by 8 rows.  Codes go from memory to registers and become
-// fp16 operands there, with no shared memory between:
-//   K    lane (r, c) = (lane / 4, lane % 4) loads D / 4 values of keys r and r + 8.  The order
+// positions.  Few rows want the keys as the long side of the products: with mma m16n8k16,
+// S^T = K Q^T has 16 keys by 8 rows, O^T = V^T P^T has 16 values of D by 8 rows.  (The tensor core's
+// large tiles have 64 rows or more: a token of 4 rows would leave 15 in 16 unused, and K and V would
+// have to be written to shared memory as fp16 first.)  Codes become fp16 operands in registers:
+//   K    lane (r, c) = (lane / 4, lane % 4) takes D / 4 values of keys r and r + 8.  The order
 //        of the D values in the sum is free, so a byte's two values are one operand register.
-//   V^T  lane (r, c) loads D / 8 values of keys 2c, 2c + 1, 2c + 8, 2c + 9.  An operand register
+//   V^T  lane (r, c) takes D / 8 values of keys 2c, 2c + 1, 2c + 8, 2c + 9.  An operand register
 //        holds two keys' values at one place: their nibbles are brought together in a byte
 //        before it is converted.
 //   P^T  comes out of S^T's accumulators by two 8 x 8 transposes (movmatrix).
@@ -22,10 +25,26 @@
 // lies 2^39 below the row's largest).  Weights are rounded to fp16: they are kept below
 // 2^11 by raising the row's maximum when a score passes it by 2^10.
 //
+// Warps.  One thread block an SM.  Two warps copy K's and V's codes and scales of key tiles into a
+// ring of eight, and the query rows of the segments; 16 warps (8 for row tiles of 16, whose state is
+// twice as large) multiply, in teams of four that take every fourth (second) tile, 32 keys a warp;
+// one warp joins their parts of O in shared memory and stores the rows.  (64 tokens over caches up to
+// 8192, 32 + 8 heads of 128, 483 MB of codes and scales: 130 us with eight warps that loaded their 16
+// keys of a tile themselves, 95 with one loading warp and two thread blocks an SM, 99 in this
+// form, which has two blocks' warps without two blocks' unequal shares of the SM: 64 tokens over
+// 32768 403 -> 396, over pages of 16 of 64 values 85 -> 72.)
+//
 // Split.  All (key/value head, sequence, row tile, key tile) units are laid out in that order
 // and cut into equal runs, one for each thread block.  A row tile's part in a run is joined
-// over the eight warps in shared memory; a tile that a cut splits leaves its parts in the workspace
+// over the warps in shared memory; a tile that a cut splits leaves its parts in the workspace
 // for k_fp4_join, which adds them in key order.
+//
+// What bounds it.  The step of 64 tokens: 99 us, 4.9 TB/s, 0.72 of the copy rate.  The conversion of a
+// byte of codes runs at 64 lanes a cycle and SM, as do the nibbles' moves: that pipe is busy 53 % of the
+// time, issue slots 60 %, and the rest are waits that four warps a scheduler do not cover.  The same copies without
+// the arithmetic take 82 us (64 tokens over 32768: 403 us, 346 without, which is the copy rate).  One token over
+// 131072: 38 us, 31 without the arithmetic, 22 at the copy rate: the start, the last parts and the join.
+// One token over 1000: 9.5 us, latency: finding the run, the page table, the first tile, the parts, the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -3,14 +3,29 @@
 // rows are laid out and cut, is bsa_fp4_attn.cu's and bsa_fp4_runs.cuh's.
 //
 // A row tile is 128 rows, S = Q K^T and O += P V are 128 x 128 (x D) products of fp16 operands.
-// Warps (20):  0 cuts the run into segments, tells them to the others through a ring of descriptors and
-// loads codes and scales of key tiles by bulk copies; 16 .. 19 unpack them to fp16 tiles in the swizzled
-// layout the products read (levels times scales, exact), and the segment's queries (each row times
-// the power of two that brings its largest value to 2^14, rounded to fp16); 1 issues Q K^T, 2 P V;
-// 4 .. 11 are the softmax (four threads a row, see bsa_rows.cuh); 12 .. 15 normalise and store a
-// segment's rows while the softmax is at the next one.
-// Shared memory: the Q tile, two K and two V tiles, three tiles of codes.  Tensor memory: three score
-// buffers and O.  Tiles are numbered through the whole run, across the borders of segments.
+// Warps (20):
+//   0         cuts the run into segments, tells them to the others through a ring of descriptors and
+//             loads codes and scales of key tiles (pages of 16: K's, and warp 3 V's)
+//   1, 2      issue Q K^T and P V
+//   4 .. 11   are the softmax (four threads a row, see bsa_rows.cuh)
+//   12 .. 15  unpack V's codes to fp16 tiles in the swizzled layout the products read (levels times
+//             scales, exact), and normalise and store a segment's rows while the softmax is at the next
+//   16 .. 19  unpack K's codes
+//   12 .. 19  put the segment's queries in place, 16 rows each: a row times the power of two that brings
+//             its largest value to 2^14, rounded to fp16
+// Shared memory: the Q tile, two K and two V tiles (four with D = 64), three tiles of codes.  Tensor memory:
+// three score buffers and O.  Tiles are numbered through the whole run, across the borders of segments.
+//
+// What bounds it.  A prompt of 8192 (32 + 8 heads of 128): 471 us, 1.17 PFLOP/s of visible products, 0.61 of the
+// burst rate of a plain product; the tensor pipe is busy half the time.  The softmax takes some 1,700
+// cycles a key tile (the products 1,024) beside the unpacking warps, which issue every third
+// instruction (issue slots 64 % full), and a segment's start costs some 4,000 more: its queries are put in
+// place after the segment before is through with theirs.  (A chunk of 1024 over 64512, whose segments are long: 787 us,
+// 1.39 PFLOP/s, 0.72.)  One set of warps for K, V and the queries: 897 us; K's and V's apart 530; the same
+// loop for both, so that it stays in the instruction cache, and each query load in its own register: 470.
+// Slower than this: row tiles of 256, each unpacked tile used twice, with one tile of codes and two score
+// buffers (510 us: unpacking is not what bounds it, and loads and buffers are missed); queries through the ring
+// of codes (484); a segment told and its queries loaded before the end of the one before (485 and 495).
 //
 // Rounding.  Weights are rounded to fp16 for the product P V; they stay below 2^15 against an
 // earlier maximum of their row (see softmax_rows).  Row sums add them unrounded.
