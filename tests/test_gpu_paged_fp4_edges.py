@@ -293,3 +293,37 @@ def test_infinite_queries_against_keys_of_one_sign():
     none, nan = torch.isneginf(q).any(-1), torch.isposinf(q).any(-1)
     assert (o[none] == 0).all() and torch.isneginf(lse[none]).all()
     assert torch.isnan(o[nan].float()).all() and torch.isnan(lse[nan]).all()
+
+
+# ------------------------------------------------------------------ scratch that the binding brings
+
+def test_scratch_of_a_call_goes_back_when_it_returns():
+    """On the current stream, on another one, in a capture, and when the call is refused."""
+    b = ref.make([1, 40], [900, 300], H=8, H_kv=2, D=128, page=64, seed=78)
+    c = f4.Cache(b, 78)
+    q = ref.rows(b, 8, 79)
+    want = run_forward(b, c, q)
+    side = torch.cuda.Stream()
+    o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bsa.forward_paged_fp4(q, *c.arrays(), *b.arrays(), o, lse)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for kw in ({}, dict(stream=side)):
+        side.wait_stream(torch.cuda.current_stream())
+        bsa.forward_paged_fp4(q, *c.arrays(), *b.arrays(), o, lse, **kw)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() == before
+        assert torch.equal(bits(o), bits(want[0])) and torch.equal(lse, want[1])
+        o.zero_()
+    with pytest.raises(bsa.BsaError):
+        bsa.forward_paged_fp4(q, *c.arrays(), *b.arrays(), o, lse, scale=float("nan"))
+    assert torch.cuda.memory_allocated() == before
+    # the graph's scratch is its own: what is allocated in between does not get it
+    held = [torch.full((1 << 22,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(o), bits(want[0])) and torch.equal(lse, want[1])
+    assert all(bool((x == 0x7f).all()) for x in held)
+    status_ok()
