@@ -19,7 +19,7 @@ namespace bsa {
 namespace {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 64;
+constexpr int kReadTokens = 64;   // of a thread block, at most
 
 struct ReadParams {
     PagedBatch b;
@@ -29,6 +29,7 @@ struct ReadParams {
     int64_t stride[2];
     int32_t H_kv;
     int32_t first;  // blockIdx.y 0 is this one of the two
+    int32_t span;   // tokens of a thread block, at most kReadTokens
 };
 
 template <int D>
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(kReadThreads) k_paged_read(const __grid_consta
     int32_t chunk;
     PagedSeq q;
     const int32_t s = find_unit<kReadThreads>(
-        P.b, blockIdx.x, [](const PagedSeq& q) -> int64_t { return (q.nq + kReadTokens - 1) / kReadTokens; }, part, hit, chunk, q);
+        P.b, blockIdx.x, [&](const PagedSeq& q) -> int64_t { return ((int64_t)q.nq + P.span - 1) / P.span; }, part, hit, chunk, q);
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         for (int32_t i = threadIdx.x; i < P.b.seqs; i += kReadThreads) {
             PagedSeq x;
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kReadThreads) k_paged_read(const __grid_consta
         }
     }
     if (s < 0) return;
-    const int32_t t0 = chunk * kReadTokens, n = min(kReadTokens, q.nq - t0);
+    const int32_t t0 = chunk * P.span, n = min(P.span, q.nq - t0);
     const int32_t page = P.b.page;
     if (threadIdx.x < n) {
         const int32_t pos = q.kl - q.nq + t0 + threadIdx.x;
@@ -122,8 +123,18 @@ bsa_status launch_paged_read(const PagedReadArgs& a, int32_t* status, cudaStream
     P.stride[1] = a.v_stride;
     P.H_kv = a.H_kv;
     P.first = a.k_out != nullptr ? 0 : 1;
-    // sum over sequences of ceil(n / kReadTokens) <= tokens / kReadTokens + seqs
-    const dim3 grid((unsigned)(a.tokens / kReadTokens + a.seqs), a.k_out != nullptr && a.v_out != nullptr ? 2u : 1u);
+    // Tokens of a thread block: fewer where there would be too few blocks to hide the loads (an SM holds eight), as long as
+    // a thread keeps a few pieces.  (8 heads of 128, spans of 64, 32, 16, 8: 8192 tokens 14.6, 11.0, 8.8, 10.9 us; 32768
+    // 35.2, 31.7, 33.5, 40.9; 131072 110.0, 111.5, 123, 155; 40 heads, 8192: 76, 50, 46, 40.)
+    const int64_t sides = a.k_out != nullptr && a.v_out != nullptr ? 2 : 1;
+    P.span = kReadTokens;
+    while (P.span > 8) {
+        const int64_t blocks = ((int64_t)a.tokens / P.span + a.seqs) * sides, pieces = (int64_t)P.span * a.H_kv * (a.D / 8);
+        if (!(pieces > 16 * kReadThreads && blocks < 8 * kPagedBlocks) && !(pieces > 4 * kReadThreads && blocks < 4 * kPagedBlocks)) break;
+        P.span /= 2;
+    }
+    // sum over sequences of ceil(n / span) <= tokens / span + seqs
+    const dim3 grid((unsigned)(a.tokens / P.span + a.seqs), (unsigned)sides);
     const cudaError_t e = a.D == 128 ? launch_chained(k_paged_read<128>, grid, kReadThreads, 0, stream, P)
                                      : launch_chained(k_paged_read<64>, grid, kReadThreads, 0, stream, P);
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
