@@ -756,12 +756,16 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     }
     // sequences of few rows here, the others on large tiles, unless the host knows of no others (what it
     // was told may be wrong: then all of them are done here)
+    // One sequence that may have many: all of it there, whatever it has (two launches less: 64 tokens over 4096 25.0 -> 21.5 us,
+    // a prompt of 8192 469 -> 460.  A single token where 256 may come, over 1000 keys, 12.6 us, over 131072 64; whoever
+    // tells max_new = 1 has it in 9.5 and 38.)
+    if (a.seqs == 1 && most > kFewRows) return launch_fp4_prompt(P, a.D, true, stream);
     P.most = most > kFewRows ? kFewRows : INT32_MAX;
     const bsa_status c = a.window > 0 ? launch_mode<kWindow>(P, a.D, wide, stream) : launch_mode<kPlain>(P, a.D, wide, stream);
     if (c != BSA_OK || most <= kFewRows) return c;
     P.least = kFewRows + 1;
     P.most = INT32_MAX;
-    return launch_fp4_prompt(P, a.D, stream);
+    return launch_fp4_prompt(P, a.D, false, stream);
 }
 
 }  // namespace bsa

@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(kFp4JoinThreads) k_fp4_join(const __grid_const
     if (c == 0) P.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kFp4Ln2;
 }
 
-// bsa_fp4_prompt.cu: the sequences with P.least .. P.most rows, on the tensor core's large tiles.
+// bsa_fp4_prompt.cu: the sequences with P.least .. P.most rows, on the tensor core's large tiles.  first: the call's
+// first kernel.
 constexpr int kFp4PromptWide = 128;
-bsa_status launch_fp4_prompt(const Fp4Params& P, int32_t D, cudaStream_t stream);
+bsa_status launch_fp4_prompt(const Fp4Params& P, int32_t D, bool first, cudaStream_t stream);
 
 }  // namespace bsa

@@ -169,6 +169,21 @@ def test_masks_of_few_rows(H, K, D, page, kw):
         assert untouched(b, o, lse)
 
 
+@pytest.mark.parametrize("kw", [{}, dict(window=100, sinks=5), dict(causal=False)])
+@pytest.mark.parametrize("H,K,D,page", [(14, 2, 64, 16), (32, 8, 128, 128), (3, 3, 128, 32), (128, 1, 64, 64)])
+def test_one_sequence_with_room_for_many_tokens(H, K, D, page, kw):
+    """A single sequence, whose tokens the host knows only as a number they do not exceed."""
+    for new, length in ((0, 50), (1, 1), (1, 1500), (2, 129), (5, 700), (40, 40), (300, 1000)):
+        b = ref.make([new], [length], H=H, H_kv=K, D=D, page=page, seed=80 + new, first=1, pad_tokens=330 - new)
+        c = f4.Cache(b, 80)
+        q = ref.rows(b, H, 81)
+        o, lse = run_forward(b, c, q, **kw)
+        status_ok()
+        if new:
+            f4.check_attention(b, q, o, lse, **kw)
+        assert untouched(b, o, lse)
+
+
 # ------------------------------------------------------------------ the far ends
 
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
