@@ -16,12 +16,12 @@
 // Shared memory: the Q tile, two K and two V tiles (four with D = 64), three tiles of codes.  Tensor memory:
 // three score buffers and O.  Tiles are numbered through the whole run, across the borders of segments.
 //
-// What bounds it.  A prompt of 8192 (32 + 8 heads of 128): 471 us, 1.17 PFLOP/s of visible products, 0.61 of the
+// What bounds it.  A prompt of 8192 (32 + 8 heads of 128): 460 us, 1.19 PFLOP/s of visible products, 0.62 of the
 // burst rate of a plain product; the tensor pipe is busy half the time.  The softmax takes some 1,700
 // cycles a key tile (the products 1,024) beside the unpacking warps, which issue every third
 // instruction (issue slots 64 % full), and a segment's start costs some 4,000 more: its queries are put in
-// place after the segment before is through with theirs.  (A chunk of 1024 over 64512, whose segments are long: 787 us,
-// 1.39 PFLOP/s, 0.72.)  One set of warps for K, V and the queries: 897 us; K's and V's apart 530; the same
+// place after the segment before is through with theirs.  (A chunk of 1024 over 64512, whose segments are long: 780 us,
+// 1.40 PFLOP/s, 0.73.)  One set of warps for K, V and the queries: 897 us; K's and V's apart 530; the same
 // loop for both, so that it stays in the instruction cache, and each query load in its own register: 470.
 // Slower than this: row tiles of 256, each unpacked tile used twice, with one tile of codes and two score
 // buffers (510 us: unpacking is not what bounds it, and loads and buffers are missed); queries through the ring

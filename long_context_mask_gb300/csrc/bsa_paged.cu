@@ -28,7 +28,7 @@
 // Into a cache in 4 bits.  Keys and values are quantised on the way (bsa_fp4.cuh's formulas): some 1.5 times
 // the instructions of a bf16 row, most of them for the codes.  Keys and values of a head are two thread blocks' work,
 // keys', which take longest, come first in the grid, and a thread block goes through its rows one at a time in a short
-// loop; products and quotients are two to an instruction.  (The prompt of 8192: 52 us, 182 MB, 0.51 of the copy rate,
+// loop; products and quotients are two to an instruction.  (The prompt of 8192: 48 us, 182 MB, 0.56 of the copy rate,
 // issue slots 69 % full: the instructions bound it; 75 us with keys and values of two tokens at a time
 // in one block, 62 before values went by two.  A step of 32 tokens 5.7 us, 24 ragged chunks 11.5.)
 #include <cuda_bf16.h>
