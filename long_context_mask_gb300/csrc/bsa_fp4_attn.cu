@@ -5,8 +5,8 @@
 //     s_j = scale q . k_j,   LSE = ln sum_j exp(s_j),   O = sum_j exp(s_j - LSE) v_j
 // with k_j and v_j as bsa_fp4.cuh reads them.
 //
-// Here: lists, and the sequences of few rows (a step of single tokens, a few tokens each); the
-// others are bsa_fp4_prompt.cu's.
+// Here: the sequences of few rows (a step of single tokens, a few tokens each); the others are
+// bsa_fp4_prompt.cu's.
 //
 // Rows.  The new tokens of a sequence and the G query heads of a key/value head are rows,
 // token by token; a row tile is 8 NT of them (with lists: of one token).  A key tile is 128
@@ -69,6 +69,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTeam = 4;                     // warps to a key tile, 32 keys each
 constexpr int kMaxNT = 2;
 constexpr int32_t kFewRows = 16;             // rows of a sequence that are done here
+// With lists: so many tokens, where a token is one row tile.  (32 sequences over 16384, 18 random blocks of 129 for each token, 32 + 8
+// heads: 16, 24, 32 tokens each by themselves 302, 445, 585 us, as tiles of tokens 241, 262, 276; 64 of 6 tokens, 10 blocks:
+// 168, 196.)
+constexpr int32_t kFewListed = 8;
 // A row tile of n key tiles counts n + kRowCost in a run.
 constexpr int32_t kRowCost = 2;
 constexpr float kRaise = 10.0f;  // log2 of how far a weight may pass its row's maximum
@@ -631,8 +635,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
 // ---------------------------------------------------------------- host side
 // Workspace: joins, maxima and sums, O parts; then the tokens' lists.
 struct Layout {
-    size_t joins, ml, o, cnt, list, who, total;
-    int32_t list_rows, cap;
+    size_t joins, ml, o, total;
+    struct Lists {  // of tiles of tpt tokens
+        size_t cnt, list, who;
+        int32_t tpt, rows, cap, words;
+    } lists[2];     // few rows, many
 };
 Layout layout(const PagedForwardArgs& a) {
     Layout L{};
@@ -649,12 +656,18 @@ Layout layout(const PagedForwardArgs& a) {
     L.o = take(sizeof(float) * (few > many ? few : many) * (size_t)a.D);
     if (a.sel_width > 0) {
         const int64_t blocks = ((int64_t)a.max_pages * a.page + 127) / 128;
-        L.cap = (int32_t)(blocks < a.sel_width ? blocks : a.sel_width);
-        L.list_rows = a.tokens + a.seqs;
-        const size_t rows = (size_t)a.H_kv * L.list_rows;
-        L.cnt = take(sizeof(int32_t) * rows);
-        L.list = take(sizeof(int32_t) * rows * L.cap);
-        L.who = take(sizeof(uint32_t) * rows * L.cap);
+        for (int x = 0; x < 2; ++x) {
+            Layout::Lists& l = L.lists[x];
+            l.tpt = x == 0 ? 1 : kFp4PromptWide / (a.H / a.H_kv);
+            const int64_t most = (int64_t)l.tpt * a.sel_width;
+            l.cap = (int32_t)(blocks < most ? blocks : most);
+            l.words = (l.tpt + 31) / 32;
+            l.rows = a.tokens / l.tpt + a.seqs;
+            const size_t rows = (size_t)a.H_kv * l.rows;
+            l.cnt = take(sizeof(int32_t) * rows);
+            l.list = take(sizeof(int32_t) * rows * l.cap);
+            l.who = take(sizeof(uint32_t) * rows * l.cap * l.words);
+        }
     }
     L.total = at;
     return L;
@@ -742,29 +755,49 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     // of 8 (64 tokens over 8192: 99 us, 138 with tiles of 16).
     const int64_t most = (int64_t)(x.max_new > 0 && x.max_new < a.tokens ? x.max_new : a.tokens) * P.group;
     const bool wide = P.group > 8 || (a.sel == nullptr && most > 8 && most <= kFewRows);
-    if (a.sel != nullptr) {
-        P.nt_cap = L.list_rows;
-        P.cap = L.cap;
-        int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
-        int32_t* list = reinterpret_cast<int32_t*>(ws + L.list);
-        const bsa_status c = launch_paged_union(a, 1, L.list_rows, L.cap, 1, list, cnt, reinterpret_cast<uint32_t*>(ws + L.who),
-                                                status, stream);
-        if (c != BSA_OK) return c;
+    // Tokens of few rows take the blocks that they list one by one; of many, a tile of tokens takes what any of them lists,
+    // whose bits say who (2048 tokens over 257 blocks, 66 random ones each: 3250 us one by one, 885).
+    auto with_lists = [&](int x) -> bsa_status {
+        const Layout::Lists& l = L.lists[x];
+        int32_t* cnt = reinterpret_cast<int32_t*>(ws + l.cnt);
+        int32_t* list = reinterpret_cast<int32_t*>(ws + l.list);
+        uint32_t* who = reinterpret_cast<uint32_t*>(ws + l.who);
         P.list = list;
         P.list_cnt = cnt;
-        return launch_mode<kListed>(P, a.D, wide, stream);
-    }
+        P.who = who;
+        P.nt_cap = l.rows;
+        P.cap = l.cap;
+        P.words = l.words;
+        P.tpt = l.tpt;
+        return launch_paged_union(a, l.tpt, l.rows, l.cap, l.words, list, cnt, who, status, stream, P.least, P.most);
+    };
     // sequences of few rows here, the others on large tiles, unless the host knows of no others (what it
     // was told may be wrong: then all of them are done here)
     // One sequence that may have many: all of it there, whatever it has (two launches less: 64 tokens over 4096 25.0 -> 21.5 us,
     // a prompt of 8192 469 -> 460.  A single token where 256 may come, over 1000 keys, 12.6 us, over 131072 64; whoever
     // tells max_new = 1 has it in 9.5 and 38.)
-    if (a.seqs == 1 && most > kFewRows) return launch_fp4_prompt(P, a.D, true, stream);
-    P.most = most > kFewRows ? kFewRows : INT32_MAX;
-    const bsa_status c = a.window > 0 ? launch_mode<kWindow>(P, a.D, wide, stream) : launch_mode<kPlain>(P, a.D, wide, stream);
-    if (c != BSA_OK || most <= kFewRows) return c;
-    P.least = kFewRows + 1;
+    const bool lists = a.sel != nullptr;
+    const int32_t few = lists && P.group <= 16 ? kFewListed * P.group : kFewRows;
+    if (a.seqs == 1 && most > few) {
+        if (lists) {
+            const bsa_status c = with_lists(1);
+            if (c != BSA_OK) return c;
+        }
+        return launch_fp4_prompt(P, a.D, true, stream);
+    }
+    P.most = most > few ? few : INT32_MAX;
+    bsa_status c = lists ? with_lists(0) : BSA_OK;
+    if (c != BSA_OK) return c;
+    c = lists          ? launch_mode<kListed>(P, a.D, wide, stream)
+        : a.window > 0 ? launch_mode<kWindow>(P, a.D, wide, stream)
+                       : launch_mode<kPlain>(P, a.D, wide, stream);
+    if (c != BSA_OK || most <= few) return c;
+    P.least = few + 1;
     P.most = INT32_MAX;
+    if (lists) {
+        c = with_lists(1);
+        if (c != BSA_OK) return c;
+    }
     return launch_fp4_prompt(P, a.D, false, stream);
 }
 

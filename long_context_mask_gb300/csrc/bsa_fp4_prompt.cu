@@ -29,6 +29,9 @@
 //
 // Rounding.  Weights are rounded to fp16 for the product P V; they stay below 2^15 against an
 // earlier maximum of their row (see softmax_rows).  Row sums add them unrounded.
+//
+// Lists.  A row tile is as many whole tokens as 128 rows hold, and its key tiles are those that any of its tokens
+// lists; a bit for each token says whose.  The rows of a token that does not list a tile take no part in it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -64,7 +67,7 @@ constexpr int kDesc = 4;                                  // segment descriptors
 constexpr int kReaders = 3 + kSoftmaxWarps + 2 * kUnpackWarps;  // warps that read a descriptor
 constexpr int kBox = 128 * 128;                           // 128 rows of 64 fp16
 
-enum { kPlain = 0, kWindow = 1 };
+enum { kPlain = 0, kWindow = 1, kListed = 2 };
 
 template <int D>
 struct Cfg {
@@ -149,18 +152,19 @@ __device__ __forceinline__ void exp_rows_f16(uint32_t (&s)[64], const float (&f)
 
 // One key tile of the online softmax for this thread's shares of rows a and b.
 // dead: the row holds no token (its scores are 0; m = 0, and it takes part in no
-// decision).  A live row that has seen no key yet has m = -inf.  As long as no
+// decision).  hidden: the row sees nothing of the tile (as a dead row, and its weights are 0).  A live
+// row that has seen no key yet has m = -inf.  As long as no
 // row of the warp is in that state (fresh, warp-uniform) the exponentials are
 // taken against the running maxima without computing the tile's own; only a
 // tile whose sums leave 2^15 (or are NaN) is redone with its maxima.  Returns
 // true (warp-uniform) when O must be multiplied by alpha first.
 template <typename Reload>
-__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], const float (&f)[2], bool& fresh,
+__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], const bool (&hidden)[2], const float (&f)[2], bool& fresh,
                                              float (&m)[2], float (&l)[2], float (&alpha)[2], Reload&& reload) {
     alpha[0] = alpha[1] = 1.0f;
     float la, lb;
     if (!fresh) {
-        exp_rows_f16(s, f, -m[0], -m[1], la, lb);
+        exp_rows_f16(s, f, hidden[0] ? -INFINITY : -m[0], hidden[1] ? -INFINITY : -m[1], la, lb);
         if (!__any_sync(0xffffffffu, (!dead[0] && !(la <= kSumLimit)) || (!dead[1] && !(lb <= kSumLimit)))) {
             l[0] += la;
             l[1] += lb;
@@ -175,7 +179,7 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         mt[i] *= f[i];
-        if (!dead[i]) {
+        if (!dead[i] && !hidden[i]) {
             if (m[i] == -INFINITY) {
                 m[i] = mt[i];  // O and l of the row are still 0
             } else if (mt[i] > m[i] + kRescale) {
@@ -185,7 +189,7 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
                 raised = true;
             }
         }
-        bias[i] = m[i] == -INFINITY ? 0.0f : -m[i];  // (no key yet: every exponential is 0)
+        bias[i] = hidden[i] ? -INFINITY : m[i] == -INFINITY ? 0.0f : -m[i];  // (no key yet: every exponential is 0)
     }
     exp_rows_f16(s, f, bias[0], bias[1], la, lb);
     l[0] += la;
@@ -197,6 +201,7 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constant__ Fp4Params P) {
     using C = Cfg<D>;
+    constexpr bool kLists = kMode == kListed;
     constexpr uint32_t S = C::kTiles, CS = C::kCodeStages;
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded pointer: the compiler has to see that it is shared memory)
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     // this block's run (the scratch is in the data area, which is free here)
     constexpr int kScan = 256;
     if (threadIdx.x < kScan)
-        Fp4Work<kWide, row_cost(kMode), false>{P}.template find<kScan>(reinterpret_cast<int32_t*>(smem), sh.start);
+        Fp4Work<kWide, row_cost(kMode), kLists>{P}.template find<kScan>(reinterpret_cast<int32_t*>(smem), sh.start);
     __syncthreads();
     if (sh.start.any == 0) return;
     const bool abandoned = sh.watch.abort != 0;
@@ -298,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             const int32_t lane_tile = lane / N, lane_page = lane - lane_tile * N;
             const int32_t j0 = sg.j0, j1 = j0 + sg.n;
             const int32_t* table = P.b.table + (int64_t)sg.seq * P.b.max_pages;
+            const int32_t* list = kLists ? P.list + ((int64_t)sg.kvh * P.nt_cap + sg.tile) * P.cap : nullptr;
             const uint32_t to_codes = smem_u32(codes) + lane_page * page * (D / 2);
             const uint32_t to_scales = smem_u32(codes) + 2 * C::kCodes + lane_page * page * (D / 16);
             // lane l of a window: the cache row of page l % N of tile w0 + l / N (-1: behind the
@@ -305,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             auto fetch = [&](int32_t w0) -> int32_t {
                 const int32_t j = w0 + lane_tile;
                 if (j >= j1) return -1;
-                const int32_t pg = (j < sg.ns ? j : sg.lo + j - sg.ns) * N + lane_page;
+                int32_t tile;
+                if constexpr (kLists) tile = list[j];
+                else tile = j < sg.ns ? j : sg.lo + j - sg.ns;
+                const int32_t pg = tile * N + lane_page;
                 if (pg * page >= sg.kl) return -1;
                 int32_t id = table[pg];
                 if (id < 0 || id >= P.b.n_pages) {
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
         };
         if (warp == kLoad) {
             // -------------------------------------------------------- segments, codes and scales
-            Fp4Walk<kWide, row_cost(kMode), false> walk(P, sh.start);
+            Fp4Walk<kWide, row_cost(kMode), kLists> walk(P, sh.start);
             Fp4Segment sg;
             uint32_t k = 0, g = 0;  // segments and tiles so far
             bool ok = true;
@@ -690,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
         for (uint32_t k = 0;; ++k) {
             const Fp4Segment* sg = next_segment(k, ok);
             if (sg == nullptr) break;
-            const int32_t n = sg->n, j0 = sg->j0, lo_t = sg->lo, ns = sg->ns;
+            const int32_t n = sg->n, j0 = sg->j0, lo_t = sg->lo, ns = sg->ns, most = sg->nrows - 1;
+            const int64_t list_at = kLists ? ((int64_t)sg->kvh * P.nt_cap + sg->tile) * P.cap : 0;
             if (n == 0) {
                 hand_back(k);
                 continue;
@@ -702,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             int32_t hi[2], lo[2] = {0, 0}, sk[2] = {0, 0};
             int32_t some_hi, all_hi, some_lo = 0, all_lo = 0, some_sk = 0, all_sk = 0;
             {
-                const int32_t kl = sg->kl, p0 = sg->pos_of0, row0 = sg->row0, most = sg->nrows - 1;
+                const int32_t kl = sg->kl, p0 = sg->pos_of0, row0 = sg->row0;
                 // this warp's first and last row
                 const int32_t ra = qd * 32 + half * 16, rb = min(ra + 15, most);
                 const int32_t pa = p0 + (row0 + min(ra, most)) / P.group, pb = p0 + (row0 + rb) / P.group;
@@ -735,17 +745,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             float m[2] = {dead[0] ? 0.0f : -INFINITY, dead[1] ? 0.0f : -INFINITY};
             float l[2] = {0.0f, 0.0f};  // this thread's share of each row
             bool fresh = true;
+            // lists: the next key tile, and the words that hold this thread's rows' bits
+            const int32_t* list = nullptr;
+            const uint32_t* who = nullptr;
+            int32_t tile_next = 0, tok[2] = {0, 0};
+            uint32_t who_next[2] = {0u, 0u};
+            auto look = [&](int32_t j) {
+                if (j >= n) return;
+                tile_next = list[j];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) who_next[x] = who[(int64_t)j * P.words + (tok[x] >> 5)];
+            };
+            if constexpr (kLists) {
+                list = P.list + list_at + j0;
+                who = P.who + (list_at + j0) * P.words;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) tok[x] = min(row[x], most) / P.group;
+                look(0);
+            }
             for (int32_t j = 0; j < n; ++j) {
                 const uint32_t gb = gb0 + (uint32_t)j;
                 const uint32_t sbuf = (gb % kSBuf) * 128u;
                 int32_t kt;
-                if constexpr (kMode == kWindow) kt = j0 + j < ns ? j0 + j : lo_t + j0 + j - ns;
+                if constexpr (kLists) kt = tile_next;
+                else if constexpr (kMode == kWindow) kt = j0 + j < ns ? j0 + j : lo_t + j0 + j - ns;
                 else kt = j0 + j;
                 const int32_t kb = kt * 128;
+                bool hidden[2] = {false, false};
                 // bit 2 kk + e of vis[x]: row x sees this thread's column c0 + 8 kk + e
                 uint32_t vis[2] = {~0u, ~0u};
-                const bool visible = (kt < some_hi && kt >= some_lo) || kt < some_sk;
+                bool visible = (kt < some_hi && kt >= some_lo) || kt < some_sk;
                 const bool masked = visible && !((kt < all_hi && kt >= all_lo) || kt < all_sk);
+                if constexpr (kLists) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) hidden[x] = dead[x] || (who_next[x] >> (tok[x] & 31) & 1u) == 0u;
+                    visible = __any_sync(0xffffffffu, !hidden[0] || !hidden[1]);
+                    look(j + 1);
+                }
                 if (masked) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -785,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                 };
                 load_s();
                 float alpha[2];
-                const bool raised = softmax_rows(sc, dead, fac, fresh, m, l, alpha, load_s);
+                const bool raised = softmax_rows(sc, dead, hidden, fac, fresh, m, l, alpha, load_s);
                 tmem_st16x128_x16(t_base + sbuf, sc);
                 if (raised) {
                     // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}
@@ -855,6 +891,7 @@ bsa_status launch_d(const Fp4Params& P, bool first, cudaStream_t stream) {
 }  // namespace
 
 bsa_status launch_fp4_prompt(const Fp4Params& P, int32_t D, bool first, cudaStream_t stream) {
+    if (P.list != nullptr) return D == 128 ? launch_d<128, kListed>(P, first, stream) : launch_d<64, kListed>(P, first, stream);
     if (P.window > 0) return D == 128 ? launch_d<128, kWindow>(P, first, stream) : launch_d<64, kWindow>(P, first, stream);
     return D == 128 ? launch_d<128, kPlain>(P, first, stream) : launch_d<64, kPlain>(P, first, stream);
 }

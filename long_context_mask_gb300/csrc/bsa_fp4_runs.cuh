@@ -2,7 +2,7 @@
 // work into equal runs, a run's row tiles one by one, and the join of rows that a cut splits.
 //
 // Rows are the new tokens of a sequence times the G query heads of a key/value head, token by token;
-// a row tile is `wide` of them (with lists: of one token), a key tile 128 positions.  All (key/value
+// a row tile is `wide` of them (with lists: of one token or of tpt whole ones), a key tile 128 positions.  All (key/value
 // head, sequence, row tile, key tile) units are laid out in that order and cut into equal runs, one for
 // each thread block; no host knowledge of the lengths is needed.  A row tile that a cut splits leaves
 // its parts (O, maximum, sum, all fp32) in the workspace, and the join adds them in key order, so
@@ -23,6 +23,7 @@
 namespace bsa {
 
 constexpr float kFp4Ln2 = 0.6931471805599453f;
+constexpr int kFp4PromptWide = 128;  // rows of a large row tile
 
 struct Fp4Params {
     CUtensorMap map_k, map_ks, map_v, map_vs;  // codes and scales of short pages: a row a page and head
@@ -37,9 +38,10 @@ struct Fp4Params {
     float scale_log2;
     __nv_bfloat16* o;
     float* lse;
-    // lists: of token tile f = kvh * nt_cap + token of the batch (in sequence order)
+    // lists: of tile f = kvh * nt_cap + i, the i-th tpt tokens of the kernel's sequences; who: words words of token bits for each entry
     const int32_t *list, *list_cnt;
-    int32_t nt_cap, cap;
+    const uint32_t* who;
+    int32_t nt_cap, cap, words, tpt;
     // parts of split tiles
     float* part_o;    // [runs, 2, wide, D]
     float2* part_ml;  // [runs, 2, wide] maximum (log2) and sum
@@ -118,17 +120,20 @@ struct Fp4Work {
     const Fp4Params& P;
 
     __device__ __forceinline__ int32_t per_token() const { return (P.group + kWide - 1) / kWide; }
+    // with lists: tokens of a tile (of the narrow row tiles, one)
+    __device__ __forceinline__ int32_t tpt() const { return kWide < kFp4PromptWide ? 1 : P.tpt; }
     __device__ __forceinline__ int32_t tiles(int32_t nq) const {
-        if constexpr (kLists) return nq * per_token();
         const int32_t rows = nq * P.group;
-        return rows < P.least || rows > P.most ? 0 : (rows + kWide - 1) / kWide;
+        if (rows < P.least || rows > P.most) return 0;
+        if constexpr (kLists) return (nq + tpt() - 1) / tpt() * per_token();
+        return (rows + kWide - 1) / kWide;
     }
     // rows of row tile t: `n` from row0 on (token * group + head)
     __device__ __forceinline__ void rows(int32_t t, int32_t nq, int32_t& row0, int32_t& n) const {
         if constexpr (kLists) {
-            const int32_t per = per_token(), tok = t / per, h = (t - tok * per) * kWide;
-            row0 = tok * P.group + h;
-            n = min(kWide, P.group - h);
+            const int32_t per = per_token(), x = t / per, h = (t - x * per) * kWide;
+            row0 = x * tpt() * P.group + h;
+            n = min(min(kWide, tpt() * P.group - h), nq * P.group - row0);
         } else {
             row0 = t * kWide;
             n = min(kWide, nq * P.group - row0);
@@ -425,7 +430,6 @@ __global__ void __launch_bounds__(kFp4JoinThreads) k_fp4_join(const __grid_const
 
 // bsa_fp4_prompt.cu: the sequences with P.least .. P.most rows, on the tensor core's large tiles.  first: the call's
 // first kernel.
-constexpr int kFp4PromptWide = 128;
 bsa_status launch_fp4_prompt(const Fp4Params& P, int32_t D, bool first, cudaStream_t stream);
 
 }  // namespace bsa

@@ -164,9 +164,10 @@ bsa_status launch_paged_forward(const PagedForwardArgs& a, void* workspace, int3
 
 // Tile lists out of tokens' lists (bsa_paged_attn.cu, see k_paged_union): for each
 // tile of tpt tokens and key/value head the listed and visible blocks, ascending, with words
-// words of token bits each.
+// words of token bits each.  Only the sequences with least .. most rows (tokens times query heads of a
+// key/value head) have tiles.
 bsa_status launch_paged_union(const PagedForwardArgs& a, int32_t tpt, int32_t nt_cap, int32_t cap, int32_t words, int32_t* list,
-                              int32_t* cnt, uint32_t* who, int32_t* status, cudaStream_t stream);
+                              int32_t* cnt, uint32_t* who, int32_t* status, cudaStream_t stream, int32_t least = 0, int32_t most = 0x7fffffff);
 
 // Attention over a cache in 4 bits (bsa_fp4_attn.cu): k_cache and v_cache hold codes.
 struct Fp4ForwardArgs {

@@ -1245,6 +1245,7 @@ struct UnionParams {
     int32_t *list, *cnt;
     uint32_t* who;
     int32_t nt_cap, cap, words;
+    int32_t group, least, most;    // only the sequences with least .. most rows (tokens * group)
 };
 __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_constant__ UnionParams P) {
     __shared__ uint32_t bits[kUnionWords];
@@ -1255,7 +1256,12 @@ __global__ void __launch_bounds__(kUnionThreads) k_paged_union(const __grid_cons
     int32_t t;
     PagedSeq q;
     const int32_t s = find_unit<kUnionThreads>(
-        P.b, blockIdx.x, [&](const PagedSeq& y) -> int64_t { return (y.nq + P.tpt - 1) / P.tpt; }, part, hit, t, q);
+        P.b, blockIdx.x,
+        [&](const PagedSeq& y) -> int64_t {
+            const int32_t rows = y.nq * P.group;
+            return rows < P.least || rows > P.most ? 0 : (y.nq + P.tpt - 1) / P.tpt;
+        },
+        part, hit, t, q);
     if (s < 0) return;
     const int32_t first = t * P.tpt, ntok = min(P.tpt, q.nq - first);
     const int32_t kvh = blockIdx.y;
@@ -1373,9 +1379,9 @@ bsa_status launch_d(const Params& P, cudaStream_t stream) {
 size_t paged_forward_workspace(const PagedForwardArgs& a) { return layout(a).total; }
 
 bsa_status launch_paged_union(const PagedForwardArgs& a, int32_t tpt, int32_t nt_cap, int32_t cap, int32_t words, int32_t* list,
-                              int32_t* cnt, uint32_t* who, int32_t* status, cudaStream_t stream) {
+                              int32_t* cnt, uint32_t* who, int32_t* status, cudaStream_t stream, int32_t least, int32_t most) {
     const PagedBatch b{a.q_start, a.kv_len, a.table, a.seqs, a.tokens, a.max_pages, a.page, a.n_pages, status};
-    UnionParams U{b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, tpt, a.causal, list, cnt, who, nt_cap, cap, words};
+    UnionParams U{b, a.sel, a.sel_cnt, a.sel_width, a.H_kv, tpt, a.causal, list, cnt, who, nt_cap, cap, words, a.H / a.H_kv, least, most};
     return launch_chained(k_paged_union, dim3((unsigned)nt_cap, (unsigned)a.H_kv), kUnionThreads, 0, stream, U) == cudaSuccess
                ? BSA_OK
                : BSA_ERR_CUDA;

@@ -342,3 +342,44 @@ def test_scratch_of_a_call_goes_back_when_it_returns():
     assert torch.equal(bits(o), bits(want[0])) and torch.equal(lse, want[1])
     assert all(bool((x == 0x7f).all()) for x in held)
     status_ok()
+
+
+# ------------------------------------------------------------------ lists of few and of many tokens
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,K,D,page", [(14, 2, 64, 16), (32, 8, 128, 64), (3, 3, 128, 128), (128, 1, 64, 32), (40, 2, 128, 16), (16, 1, 64, 128)])
+def test_lists_of_few_and_of_many_tokens(H, K, D, page, causal):
+    """Sequences on either side of where tokens' lists are taken together, one whose lists are empty, one
+    alone, and what the host is told."""
+    for new, length in (([1, 8, 9, 0, 200, 2, 17], [900, 1500, 700, 50, 1300, 2, 4000]), ([150], [2500]), ([3], [600]), ([0], [70])):
+        b = ref.make(new, length, H=H, H_kv=K, D=D, page=page, seed=90, first=1, pad_tokens=40)
+        c = f4.Cache(b, 90, gains=True)
+        q = ref.rows(b, H, 91)
+        sel, cnt, want = lists_for(b, np.random.default_rng(92), 6, empty=0.15)
+        if len(new) > 1:
+            t = b.q_start[2].item()  # a sequence of empty lists
+            cnt[t:t + 9] = 0
+            for x in range(t, t + 9):
+                want[x] = [[] for _ in want[x]]
+        for max_new in (0, 1, max(new), 10 ** 6):
+            o, lse = run_forward(b, c, q, sel=sel, sel_cnt=cnt, causal=causal, max_new=max_new)
+            status_ok()
+            f4.check_attention(b, q, o, lse, sel=want, causal=causal)
+            assert untouched(b, o, lse)
+
+
+def test_lists_of_a_query_that_is_not_finite():
+    """It changes no other row, whether they list the same blocks or others."""
+    b = ref.make([70, 3], [1500, 600], H=8, H_kv=2, D=128, page=64, seed=94)
+    c = f4.Cache(b, 94)
+    q = ref.rows(b, 8, 95)
+    sel, cnt, want = lists_for(b, np.random.default_rng(96), 4)
+    o0, lse0 = run_forward(b, c, q, sel=sel, sel_cnt=cnt)
+    f4.check_attention(b, q, o0, lse0, sel=want)
+    q[11, 3, 7], q[40, 0, 0], q[71, 5, 1] = float("nan"), float("inf"), float("nan")
+    o, lse = run_forward(b, c, q, sel=sel, sel_cnt=cnt)
+    status_ok()
+    same = torch.ones(b.tokens, 8, dtype=torch.bool, device="cuda")
+    same[11, 3] = same[40, 0] = same[71, 5] = False
+    assert torch.equal(bits(o)[same], bits(o0)[same]) and torch.equal(lse[same], lse0[same])
+    assert torch.isnan(o[11, 3].float()).all() and torch.isnan(o[71, 5].float()).all()
