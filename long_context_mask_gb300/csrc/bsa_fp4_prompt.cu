@@ -880,8 +880,13 @@ bsa_status launch_d(const Fp4Params& P, bool first, cudaStream_t stream) {
     constexpr int kRows = kFp4JoinThreads / (D / 4);
     // As a call's first kernel it does not start beside the one before it, whose SMs its blocks would take as they fall free,
     // in any order (a chunk of 1024 over 64512, again and again: 832 us so, 780 in order).
-    if (first) k_fp4_prompt<D, kMode><<<grid, kThreads, smem, stream>>>(P);
-    const cudaError_t e = first ? cudaGetLastError() : launch_chained(k_fp4_prompt<D, kMode>, dim3((unsigned)grid), kThreads, smem, stream, P);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    const cudaError_t e = first ? cudaLaunchKernelEx(&cfg, k_fp4_prompt<D, kMode>, P)
+                                : launch_chained(k_fp4_prompt<D, kMode>, cfg.gridDim, kThreads, smem, stream, P);
     if (e != cudaSuccess ||
         launch_chained(k_fp4_join<D, kWide, kRows>, dim3((unsigned)grid, kWide / kRows), kFp4JoinThreads, 0, stream, P) != cudaSuccess)
         return BSA_ERR_CUDA;

@@ -383,3 +383,30 @@ def test_lists_of_a_query_that_is_not_finite():
     same[11, 3] = same[40, 0] = same[71, 5] = False
     assert torch.equal(bits(o)[same], bits(o0)[same]) and torch.equal(lse[same], lse0[same])
     assert torch.isnan(o[11, 3].float()).all() and torch.isnan(o[71, 5].float()).all()
+
+
+def test_one_sequence_captured_and_replayed_with_fewer_tokens():
+    """A graph for up to 40 tokens of one sequence, with lists and without, replayed with 40, 3 and none."""
+    b = ref.make([40], [600], H=8, H_kv=2, D=128, page=64, seed=97)
+    c = f4.Cache(b, 97)
+    q = ref.rows(b, 8, 98)
+    sel, cnt, want = lists_for(b, np.random.default_rng(99), 4)
+    o, lse = torch.empty_like(q), torch.empty((40, 8), device="cuda")
+    o2, lse2 = torch.empty_like(q), torch.empty((40, 8), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        bsa.forward_paged_fp4(q, *c.arrays(), *b.arrays(), o, lse)
+        bsa.forward_paged_fp4(q, *c.arrays(), *b.arrays(), o2, lse2, sel=sel, sel_cnt=cnt)
+    for n in (40, 3, 0, 40):
+        b.q_start.copy_(torch.tensor([0, n], dtype=torch.int32))
+        b.new = [n]
+        for x in (o, o2, lse, lse2):
+            x.fill_(7.0)
+        graph.replay()
+        status_ok()
+        if n:
+            f4.check_attention(b, q, o, lse)
+            f4.check_attention(b, q, o2, lse2, sel=want)
+        for x in (o, o2, lse, lse2):
+            assert (x[n:] == 7.0).all()
