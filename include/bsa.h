@@ -910,7 +910,8 @@ bsa_status bsa_paged_read_fp4(const bsa_paged_batch* b, int32_t H_kv, int32_t D,
  *
  *  max_new    the most new tokens that any of the sequences has, if the host
  *             knows (1 for a step of single tokens), else 0.  It decides how the
- *             work is done, not what comes out: a sequence may have more.
+ *             work is done, not what comes out but for its last bits: a sequence
+ *             may have more.
  *  workspace  of at least bsa_forward_paged_fp4_workspace_size() bytes.
  *  (tokens + seqs) * H_kv must be below 2^31 with lists.
  *  All else as in bsa_forward_paged.

@@ -983,7 +983,8 @@ def forward_paged_fp4(q, k_cache, k_scale, v_cache, v_scale, page_table, q_start
                       scale: float = 0.0, max_new: int = 0, workspace=None, stream=None):
     """forward_paged() over a cache in 4 bits, as paged_append_fp4() writes it.
     max_new: the most new tokens that any of the sequences has, where the caller
-    knows it (1 for a step of single tokens); it changes the time, not the result.
+    knows it (1 for a step of single tokens); it changes the time, and of the result
+    at most the last bits.
     ``workspace`` is a CUDA tensor of at least forward_paged_fp4_workspace_size()
     bytes (allocated here when omitted)."""
     if _torch is None:
