@@ -418,9 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                 const Fp4Segment* sp = next_segment(k, ok);
                 if (sp == nullptr) break;
                 const int32_t n = sp->n;
+                // (the descriptor guards q_ready's phase too: handed back before, and with segments behind it that have
+                // no key and so nothing of this warp to wait for, the phase could go by unseen)
+                if (n > 0) ok = wait_warp(smem_u32(&sh.q_ready[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status);
                 hand_back(k);
                 if (n == 0) continue;
-                ok = wait_warp(smem_u32(&sh.q_ready[k % kDesc]), (k / kDesc) & 1u, &sh.watch, status);
                 for (int32_t j = 0; j < n && ok; ++j, ++g) {
                     // S buffer g % 3 is free once PV_{g-3} has read P_{g-3}
                     if (g >= kSBuf) ok = wait_warp(smem_u32(&sh.pv_done[g % kSBuf]), (g / kSBuf - 1u) & 1u, &sh.watch, status);

@@ -1,0 +1,46 @@
+"""A cache in 4 bits: rows of one call apart from one another, and the far ends of weights, gains and
+roundings, against fp64 or bit by bit."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_ref as f4
+import long_context_mask_gb300 as bsa
+import paged_ref as ref
+from gpu_util import status_ok
+from test_gpu_paged import bits, lists_for
+from test_gpu_paged_fp4 import run_append, run_forward
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+# ------------------------------------------------------------------ row tiles without a key
+
+@pytest.mark.parametrize("D,page", [(64, 64), (128, 128)])
+def test_short_row_tiles_before_row_tiles_without_a_key(D, page):
+    """A thread block's run of some 40 row tiles (a token each): again and again one of one or two key tiles, and
+    eight or nine without any, by lists that are empty; and tokens before position 0."""
+    H, n = 128, 152 * 40 + 5
+    b = ref.make([n], [n], H=H, H_kv=1, D=D, page=page, seed=140)
+    c = f4.Cache(b, 140)
+    q = ref.rows(b, H, 141)
+    t = torch.arange(n)
+    own = t // 128
+    sel = torch.stack([torch.zeros_like(own), own], 1)[:, None].to(torch.int32).contiguous().cuda()
+    cnt = torch.where((t % 9 == 0) | (t % 90 == 4), torch.where(own > 0, 1 + t % 2, torch.ones_like(t)), torch.zeros_like(t))
+    lists = [[[0, int(own[x])][:int(cnt[x])]] for x in range(n)]
+    cnt = cnt[:, None].to(torch.int32).contiguous().cuda()
+    first = None
+    for _ in range(20):
+        o, lse = run_forward(b, c, q, sel=sel, sel_cnt=cnt)
+        status_ok()
+        if first is None:
+            first = o, lse
+            f4.check_attention(b, q, o, lse, sel=lists)
+        assert torch.equal(bits(o), bits(first[0])) and torch.equal(lse, first[1])
+    short = torch.tensor([140], dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty((n, H), device="cuda")
+    bsa.forward_paged_fp4(q, *c.arrays(), b.table, b.q_start, short, o, lse)
+    status_ok()
+    assert (o[:n - 140] == 0).all() and torch.isneginf(lse[:n - 140]).all() and torch.isfinite(lse[n - 140:]).all()
