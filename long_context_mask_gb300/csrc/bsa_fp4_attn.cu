@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -76,6 +77,9 @@ constexpr int32_t kFewListed = 8;
 // A row tile of n key tiles counts n + kRowCost in a run.
 constexpr int32_t kRowCost = 2;
 constexpr float kRaise = 10.0f;  // log2 of how far a weight may pass its row's maximum
+// A row's maximum while it has seen no score above -infinity.  (Finite: -infinity less it is -infinity, a weight of 0, not
+// NaN; any other score passes it by more than kRaise.)
+constexpr float kNoKey = -FLT_MAX;
 
 enum { kPlain = 0, kWindow = 1, kListed = 2 };
 
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                 }
 #pragma unroll
                 for (int y = 0; y < kWarps; ++y) {
-                    if (z[y].x == -INFINITY && z[y].y == 0.0f) continue;  // no visible key
+                    if (z[y].y == 0.0f) continue;  // no visible key
                     const float f = ex2(z[y].x - M);
                     sum = fmaf(f, z[y].y, sum);
                     const float4 v = *reinterpret_cast<const float4*>(so + (y * R + row) * kRowO + 4 * col);
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                m[b][y] = -INFINITY;
+                m[b][y] = kNoKey;
                 l[b][y] = 0.0f;
             }
         const uint32_t first = (team - g0) & (T - 1u);  // the team's first tile of the segment
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                     }
                 }
             }
-            // exponents against the rows' maxima so far; +inf where a row has none yet
+            // exponents against the rows' maxima so far
             bool seen = kb + 32 <= all_hi;
             if constexpr (kMode == kWindow) seen = (seen && kb >= all_lo) || kb + 32 <= all_sk;
             auto vis = [&](int h, int b, int y) -> bool {
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                         for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
                         // (row by row: what one row holds does not show in another's last bits)
                         const float m_new = best > m[b][y] + kRaise ? best : m[b][y];
-                        const float keep = m[b][y] == -INFINITY ? 1.0f : ex2(m[b][y] - m_new);  // (l and O are 0 still)
+                        const float keep = ex2(m[b][y] - m_new);
                         m[b][y] = m_new;
                         l[b][y] *= keep;
 #pragma unroll
@@ -549,9 +553,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                             acc[b][z][y] *= keep;
                             acc[b][z][y + 2] *= keep;
                         }
-                        const float base = m_new == -INFINITY ? 0.0f : m_new;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) ex[x >> 1][b][y + 2 * (x & 1)] = s4[x] - base;
+                        for (int x = 0; x < 4; ++x) ex[x >> 1][b][y + 2 * (x & 1)] = s4[x] - m_new;
                     }
             }
             uint32_t pt[2][NT][2];

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kFp4JoinThreads) k_fp4_join(const __grid_const
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (y[u].x == -INFINITY && y[u].y == 0.0f) continue;  // no visible key in this part
+            if (y[u].y == 0.0f) continue;  // no visible key in this part
             const float M_new = fmaxf(M, y[u].x);
             const float keep = M == -INFINITY ? 1.0f : ex2(M - M_new), f = ex2(y[u].x - M_new);  // (l and o are 0 still)
             M = M_new;
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kFp4JoinThreads) k_fp4_join(const __grid_const
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
             const float2 y = ml[all + g];
-            if (y.x == -INFINITY && y.y == 0.0f) continue;
+            if (y.y == 0.0f) continue;
             const float f = ex2(y.x - M);
             const float4 v = so[all + g][c];
             l = fmaf(f, y.y, l);

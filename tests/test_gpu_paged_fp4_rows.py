@@ -44,3 +44,19 @@ def test_short_row_tiles_before_row_tiles_without_a_key(D, page):
     bsa.forward_paged_fp4(q, *c.arrays(), b.table, b.q_start, short, o, lse)
     status_ok()
     assert (o[:n - 140] == 0).all() and torch.isneginf(lse[:n - 140]).all() and torch.isfinite(lse[n - 140:]).all()
+
+
+@pytest.mark.parametrize("max_new", [0, 1])
+@pytest.mark.parametrize("H,K,D", [(1, 1, 128), (2, 2, 64), (4, 1, 64), (12, 1, 128)])
+def test_a_token_whose_scores_are_all_minus_infinity(H, K, D, max_new):
+    """It is a row without a key, with no other row beside it too."""
+    b = ref.make([1, 1], [700, 40], H=H, H_kv=K, D=D, page=64, seed=147)
+    c = f4.Cache(b, 147)
+    c.k = (c.k & 0x77) | 0x11
+    raw = c.k_scale.view(torch.uint8)
+    raw.copy_(torch.where(raw == 0, torch.full_like(raw, 0x20), raw))
+    q = ref.rows(b, H, 148)
+    q[..., 17] = -INF
+    o, lse = run_forward(b, c, q, max_new=max_new)
+    status_ok()
+    assert (o == 0).all() and torch.isneginf(lse).all()
