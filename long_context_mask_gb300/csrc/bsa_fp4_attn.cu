@@ -529,23 +529,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int b = 0; b < NT; ++b) top = fmax3(fmax3(top, ex[h][b][0], ex[h][b][1]), ex[h][b][2], ex[h][b][3]);
+            // A row that passes the limit takes a new maximum; the others' exponents come out as above, bit by bit,
+            // so that what one row holds does not show in another.  (The largest exponent of a row is that of its
+            // largest product: fmaf rounds in order.)
             if (__any_sync(0xffffffffu, top > kRaise)) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float s4[4], best = -INFINITY;
+                        bool v[4];
+                        float best = -INFINITY;
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int h = x >> 1, z = y + 2 * (x & 1);
-                            s4[x] = seen || vis(h, b, z) ? sc[h][b][z] * fac[b][y] : -INFINITY;
-                            best = fmaxf(best, s4[x]);
+                            v[x] = seen || vis(x >> 1, b, y + 2 * (x & 1));
+                            best = fmaxf(best, v[x] ? sc[x >> 1][b][y + 2 * (x & 1)] : -INFINITY);
                         }
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
-                        // (row by row: what one row holds does not show in another's last bits)
-                        const float m_new = best > m[b][y] + kRaise ? best : m[b][y];
-                        const float keep = ex2(m[b][y] - m_new);
+                        const bool raise = fmaf(best, fac[b][y], -m[b][y]) > kRaise;
+                        const float m_new = raise ? best * fac[b][y] : m[b][y];
+                        const float keep = raise ? ex2(m[b][y] - m_new) : 1.0f;
                         m[b][y] = m_new;
                         l[b][y] *= keep;
 #pragma unroll
@@ -554,7 +557,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                             acc[b][z][y + 2] *= keep;
                         }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) ex[x >> 1][b][y + 2 * (x & 1)] = s4[x] - m_new;
+                        for (int x = 0; x < 4; ++x)
+                            ex[x >> 1][b][y + 2 * (x & 1)] =
+                                v[x] ? fmaf(sc[x >> 1][b][y + 2 * (x & 1)], fac[b][y], -m_new) : -INFINITY;
                     }
             }
             uint32_t pt[2][NT][2];

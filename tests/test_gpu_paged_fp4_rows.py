@@ -60,3 +60,56 @@ def test_a_token_whose_scores_are_all_minus_infinity(H, K, D, max_new):
     o, lse = run_forward(b, c, q, max_new=max_new)
     status_ok()
     assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+# ------------------------------------------------------------------ rows apart from one another
+
+def rising(new, length, H, K, D, page, seed):
+    """A batch whose scores grow along the keys, past every maximum again and again; values 16 and 17 of a key
+    are positive, so that a query's infinity there makes scores of its sign alone."""
+    b = ref.make(new, length, H=H, H_kv=K, D=D, page=page, seed=seed)
+    c = f4.Cache(b, seed)
+    raw = c.k_scale.view(torch.uint8)
+    for s, n in enumerate(b.length):
+        p = torch.arange(n, device="cuda")
+        size = torch.exp2(6.0 * p / n - 5.0).to(torch.float8_e4m3fn).view(torch.uint8)
+        raw[b.table[s].long()[p // page], :, p % page] = size[:, None, None]
+    c.k[..., 8] = (c.k[..., 8] & 0x77) | 0x11
+    return b, c.refresh()
+
+
+def with_row(q, rows, value):
+    """q with the given rows ([tokens, heads] truth values) not finite, or 64 times as large."""
+    x = q.clone()
+    if value is None:
+        x[rows] *= 64
+    else:
+        x[..., 17] = torch.where(rows, torch.full_like(x[..., 17], value), x[..., 17])
+    return x
+
+
+def check_apart(b, c, q, bad, **kw):
+    """No other row has other bits for what the bad rows hold."""
+    o0, lse0 = run_forward(b, c, q, **kw)
+    status_ok()
+    for value in (None, float("nan"), INF, -INF):
+        o, lse = run_forward(b, c, with_row(q, bad, value), **kw)
+        status_ok()
+        assert torch.equal(bits(o)[~bad], bits(o0)[~bad]) and torch.equal(lse[~bad], lse0[~bad]), value
+        seen = bad & torch.isfinite(lse0)
+        if value == -INF:
+            assert (o[bad] == 0).all() and torch.isneginf(lse[bad]).all()
+        elif value is not None:
+            assert torch.isnan(o[seen].float()).all() and torch.isnan(lse[seen]).all()
+    return o0, lse0
+
+
+@pytest.mark.parametrize("new,H,K,D,page", [(1, 8, 2, 128, 64), (1, 8, 1, 64, 16), (1, 32, 2, 128, 128), (2, 8, 2, 64, 32)])
+def test_rows_of_few_tokens_do_not_show_in_one_another(new, H, K, D, page):
+    """Row tiles of 8 and of 16, some four to eight key tiles to a warp."""
+    b, c = rising([new] * 12, [16000 + 700 * s for s in range(12)], H, K, D, page, 142)
+    q = ref.rows(b, H, 143)
+    bad = torch.zeros((b.tokens, H), dtype=torch.bool, device="cuda")
+    bad[:, 1::H // K] = True
+    o, lse = check_apart(b, c, q, bad, max_new=new)
+    f4.check_attention(b, q, o, lse)
