@@ -48,7 +48,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -77,9 +76,6 @@ constexpr int32_t kFewListed = 8;
 // A row tile of n key tiles counts n + kRowCost in a run.
 constexpr int32_t kRowCost = 2;
 constexpr float kRaise = 10.0f;  // log2 of how far a weight may pass its row's maximum
-// A row's maximum while it has seen no score above -infinity.  (Finite: -infinity less it is -infinity, a weight of 0, not
-// NaN; any other score passes it by more than kRaise.)
-constexpr float kNoKey = -FLT_MAX;
 
 enum { kPlain = 0, kWindow = 1, kListed = 2 };
 
@@ -444,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                m[b][y] = kNoKey;
+                m[b][y] = kFp4NoKey;
                 l[b][y] = 0.0f;
             }
         const uint32_t first = (team - g0) & (T - 1u);  // the team's first tile of the segment

@@ -55,7 +55,6 @@ constexpr int kWide = kFp4PromptWide;
 // have 8 to 50 row tiles each: 471 us with 4, 483 with 8, 501 with 12; two chunks of 2048 through a window of
 // 575, 6 key tiles to a row tile: 106, 102, 98 us.)
 constexpr int32_t row_cost(int mode) { return mode == 1 ? 12 : 4; }
-constexpr float kRescale = 8.0f;                          // raise a row's maximum when it grows by > 2^8
 constexpr float kSumLimit = 32768.0f;                     // 2^15, see softmax_rows
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
@@ -151,21 +150,25 @@ __device__ __forceinline__ void exp_rows_f16(uint32_t (&s)[64], const float (&f)
 }
 
 // One key tile of the online softmax for this thread's shares of rows a and b.
-// dead: the row holds no token (its scores are 0; m = 0, and it takes part in no
-// decision).  hidden: the row sees nothing of the tile (as a dead row, and its weights are 0).  A live
-// row that has seen no key yet has m = -inf.  As long as no
-// row of the warp is in that state (fresh, warp-uniform) the exponentials are
-// taken against the running maxima without computing the tile's own; only a
-// tile whose sums leave 2^15 (or are NaN) is redone with its maxima.  Returns
-// true (warp-uniform) when O must be multiplied by alpha first.
+// hidden: the row sees nothing of the tile (its weights are 0).  A row that has seen no key yet has
+// m = kFp4NoKey; one that holds no token has scores of 0.  Exponentials are taken against the running maxima
+// without computing the tile's own.  Where a row's sums leave 2^15 (its first key makes them infinite) or are
+// NaN, the tile is redone with that row's new maximum, and against the maxima that the warp's other rows had,
+// to the same bits: what one row holds does not show in another.  (So a row's redone tile is paid for by 128
+// rows; the redo itself is mostly the wait for its instructions, some 600 cycles of all of them.)  first: no row of
+// the warp has seen a key, and all take their first maximum at once.  Returns true (warp-uniform) when O must be
+// multiplied by alpha first.
 template <typename Reload>
-__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dead)[2], const bool (&hidden)[2], const float (&f)[2], bool& fresh,
-                                             float (&m)[2], float (&l)[2], float (&alpha)[2], Reload&& reload) {
+__device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&hidden)[2], const float (&f)[2], bool first, float (&m)[2],
+                                             float (&l)[2], float (&alpha)[2], Reload&& reload) {
     alpha[0] = alpha[1] = 1.0f;
     float la, lb;
-    if (!fresh) {
+    uint32_t over[2] = {~0u, ~0u};  // lanes whose share of their row a, b has left the limit
+    if (!first) {
         exp_rows_f16(s, f, hidden[0] ? -INFINITY : -m[0], hidden[1] ? -INFINITY : -m[1], la, lb);
-        if (!__any_sync(0xffffffffu, (!dead[0] && !(la <= kSumLimit)) || (!dead[1] && !(lb <= kSumLimit)))) {
+        over[0] = __ballot_sync(0xffffffffu, !(la <= kSumLimit));
+        over[1] = __ballot_sync(0xffffffffu, !(lb <= kSumLimit));
+        if ((over[0] | over[1]) == 0u) {
             l[0] += la;
             l[1] += lb;
             return false;
@@ -179,23 +182,19 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&dea
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         mt[i] *= f[i];
-        if (!dead[i] && !hidden[i]) {
-            if (m[i] == -INFINITY) {
-                m[i] = mt[i];  // O and l of the row are still 0
-            } else if (mt[i] > m[i] + kRescale) {
-                alpha[i] = ex2(m[i] - mt[i]);
-                l[i] *= alpha[i];
-                m[i] = mt[i];
-                raised = true;
-            }
+        // (a row's four threads are neighbours)
+        if ((over[i] >> (threadIdx.x & 28u) & 15u) != 0u && !hidden[i] && mt[i] > m[i]) {
+            alpha[i] = ex2(m[i] - mt[i]);
+            raised |= m[i] != kFp4NoKey;  // (else O and l are 0 still)
+            l[i] *= alpha[i];
+            m[i] = mt[i];
         }
-        bias[i] = hidden[i] ? -INFINITY : m[i] == -INFINITY ? 0.0f : -m[i];  // (no key yet: every exponential is 0)
+        bias[i] = hidden[i] ? -INFINITY : -m[i];
     }
     exp_rows_f16(s, f, bias[0], bias[1], la, lb);
     l[0] += la;
     l[1] += lb;
-    fresh = __any_sync(0xffffffffu, m[0] == -INFINITY || m[1] == -INFINITY);
-    return __any_sync(0xffffffffu, raised);
+    return !first && __any_sync(0xffffffffu, raised);
 }
 
 template <int D, int kMode>
@@ -744,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             }
             const float fac[2] = {sh.fac[k % kDesc][row[0]], sh.fac[k % kDesc][row[1]]};
             hand_back(k);
-            float m[2] = {dead[0] ? 0.0f : -INFINITY, dead[1] ? 0.0f : -INFINITY};
+            float m[2] = {kFp4NoKey, kFp4NoKey};
             float l[2] = {0.0f, 0.0f};  // this thread's share of each row
-            bool fresh = true;
+            bool first = true;
             // lists: the next key tile, and the words that hold this thread's rows' bits
             const int32_t* list = nullptr;
             const uint32_t* who = nullptr;
@@ -823,7 +822,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                 };
                 load_s();
                 float alpha[2];
-                const bool raised = softmax_rows(sc, dead, hidden, fac, fresh, m, l, alpha, load_s);
+                const bool raised = softmax_rows(sc, hidden, fac, first, m, l, alpha, load_s);
+                first = false;
                 tmem_st16x128_x16(t_base + sbuf, sc);
                 if (raised) {
                     // O must hold P_0 .. P_{j-1} V: wait for PV_{j-1}

@@ -12,6 +12,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -24,6 +25,9 @@ namespace bsa {
 
 constexpr float kFp4Ln2 = 0.6931471805599453f;
 constexpr int kFp4PromptWide = 128;  // rows of a large row tile
+// A row's maximum while it has seen no score above -infinity.  (Finite: -infinity less it is -infinity, a weight of 0, not
+// NaN; any other score passes it by more than a maximum may be passed.)
+constexpr float kFp4NoKey = -FLT_MAX;
 
 struct Fp4Params {
     CUtensorMap map_k, map_ks, map_v, map_vs;  // codes and scales of short pages: a row a page and head

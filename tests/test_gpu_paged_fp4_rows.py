@@ -113,3 +113,18 @@ def test_rows_of_few_tokens_do_not_show_in_one_another(new, H, K, D, page):
     bad[:, 1::H // K] = True
     o, lse = check_apart(b, c, q, bad, max_new=new)
     f4.check_attention(b, q, o, lse)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=900, sinks=300), dict(causal=False), "lists"])
+@pytest.mark.parametrize("H,K,D,page", [(8, 2, 128, 64), (14, 2, 64, 16)])
+def test_rows_of_many_tokens_do_not_show_in_one_another(H, K, D, page, kw):
+    b, c = rising([200, 70], [5000, 3000], H, K, D, page, 144)
+    q = ref.rows(b, H, 145)
+    want = {}
+    if kw == "lists":
+        sel, cnt, listed = lists_for(b, np.random.default_rng(146), 12)
+        kw, want = dict(sel=sel, sel_cnt=cnt), dict(sel=listed)
+    bad = torch.zeros((b.tokens, H), dtype=torch.bool, device="cuda")
+    bad[2::5, 1], bad[3::7, H - 1] = True, True
+    o, lse = check_apart(b, c, q, bad, **kw)
+    f4.check_attention(b, q, o, lse, **(want or kw))
