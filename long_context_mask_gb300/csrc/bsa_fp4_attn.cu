@@ -338,11 +338,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                     out[3] = fmaf(f, v.w, out[3]);
                 }
                 if (sg.part < 0) {
-                    const float inv = (sum == 0.0f ? 0.0f : 1.0f / sum) * vg;
+                    // (the gain after the quotient: the smallest gain over a long sum is no normal number)
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     const int32_t x = sg.row0 + row, tok = x / P.group;
                     const int64_t at = ((int64_t)sg.q0 + tok) * P.H + sg.kvh * P.group + (x - tok * P.group);
                     *reinterpret_cast<uint2*>(P.o + at * D + 4 * col) =
-                        make_uint2(pack_bf16(out[0] * inv, out[1] * inv), pack_bf16(out[2] * inv, out[3] * inv));
+                        make_uint2(pack_bf16(out[0] * inv * vg, out[1] * inv * vg), pack_bf16(out[2] * inv * vg, out[3] * inv * vg));
                     if (col == 0) P.lse[at] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kFp4Ln2;
                 } else {
                     const int64_t at = (int64_t)sg.part * R + row;

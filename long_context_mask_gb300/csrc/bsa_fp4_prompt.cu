@@ -601,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
             mbar_arrive(smem_u32(&sh.ml_empty));
             tc_fence_after();
             // 1 / l; 0 for a row without a key, NaN where l is
-            const float inv = (ml.y == 0.0f ? 0.0f : 1.0f / ml.y) * (P.v_gain != nullptr ? P.v_gain[was.kvh] : 1.0f);
+            // (the gain after the quotient: the smallest gain over a long sum is no normal number)
+            const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y, vg = P.v_gain != nullptr ? P.v_gain[was.kvh] : 1.0f;
             const int64_t part = (int64_t)max(was.part, 0) * kWide + row;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
                         uint32_t pk[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+                            pk[y] = pack_bf16(__uint_as_float(o[8 * i + 2 * y]) * inv * vg, __uint_as_float(o[8 * i + 2 * y + 1]) * inv * vg);
                         reinterpret_cast<uint4*>(orow + c)[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                 } else {

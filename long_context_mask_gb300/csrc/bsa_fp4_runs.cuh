@@ -424,11 +424,12 @@ __global__ void __launch_bounds__(kFp4JoinThreads) k_fp4_join(const __grid_const
         }
     }
     if (row >= jn.z) return;
-    const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (P.v_gain != nullptr ? P.v_gain[jn.w] : 1.0f);
+    // (the gain after the quotient: the smallest gain over a long sum is no normal number)
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l, vg = P.v_gain != nullptr ? P.v_gain[jn.w] : 1.0f;
     const int32_t x = jn.y + row, tok = x / P.group;
     const int64_t at = (int64_t)tok * P.H + jn.w * P.group + (x - tok * P.group);
     *reinterpret_cast<uint2*>(P.o + at * D + 4 * c) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        make_uint2(pack_bf16(o[0] * inv * vg, o[1] * inv * vg), pack_bf16(o[2] * inv * vg, o[3] * inv * vg));
     if (c == 0) P.lse[at] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kFp4Ln2;
 }
 

@@ -128,3 +128,28 @@ def test_rows_of_many_tokens_do_not_show_in_one_another(H, K, D, page, kw):
     bad[2::5, 1], bad[3::7, H - 1] = True, True
     o, lse = check_apart(b, c, q, bad, **kw)
     f4.check_attention(b, q, o, lse, **(want or kw))
+
+
+# ------------------------------------------------------------------ gains and roundings
+
+@pytest.mark.parametrize("new,heads", [(1, 4), (1, 12), (40, 4)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
+def test_the_smallest_and_largest_gains_of_attention(D, page, new, heads):
+    """A long row of even weights, out of one page that the table names again and again: O is the mean
+    value, a normal number with any gain.  The bound is test_the_longest_sequence_out_of_one_page's (of fewer additions)."""
+    b = ref.make([new], [page], H=2 * heads, H_kv=2, D=D, page=page, seed=151, poison=False)
+    c = f4.Cache(b, 151)
+    c.v &= 0x77
+    c.v_scale.copy_(torch.full(c.v_scale.shape, 128.0).to(torch.float8_e4m3fn))
+    c.v_gain = torch.tensor([2.0 ** -126, 2.0 ** 117], device="cuda")
+    c.refresh()
+    q = torch.zeros((new, 2 * heads, D), dtype=torch.bfloat16, device="cuda")
+    copies = (29 << 16) // page   # (a sum whose reciprocal is no power of two)
+    table = b.table[:, :1].expand(1, copies).contiguous()
+    o, lse = torch.empty_like(q), torch.empty((new, 2 * heads), device="cuda")
+    bsa.forward_paged_fp4(q, *c.arrays(), table, b.q_start, torch.tensor([29 << 16], dtype=torch.int32, device="cuda"), o, lse,
+                          causal=False, max_new=new, **c.gains())
+    status_ok()
+    O = b.v_cache[b.table[0, 0].long()].double().mean(1).repeat_interleave(heads, 0)  # [2 * heads, D]
+    assert ((o.double() - O).abs() <= (2.0 ** -8 * 1.01 + 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12) * O.abs()).all()
+    assert ((lse.double() - np.log(29 << 16)).abs() <= 2.0 ** -12 + 8 * 2.0 ** -24 * 15).all()
