@@ -901,8 +901,8 @@ bsa_status bsa_paged_read_fp4(const bsa_paged_batch* b, int32_t H_kv, int32_t D,
  * fp32 to the scores and to O.  Queries are rounded to fp16 after a power of
  * two has brought their row's largest value to 2^14 .. 2^15 (a bf16 value loses
  * bits only where it lies 2^30 below its row's largest); the weights are
- * rounded to fp16 (2^-11 relative, 2^-25 of the largest absolute) before they
- * meet the values; sums and LSE take them unrounded.
+ * rounded to fp16 (2^-11 relative, 2^-31 of the row's largest absolute) before
+ * they meet the values; sums and LSE take them unrounded.
  * What a row does not see does not matter; what it sees is always finite.  A
  * query that holds an infinity or a NaN changes no other row's results; its
  * own are NaN, or, where all its scores come out as -infinity, those of a row

@@ -22,8 +22,8 @@
 //   P^T  comes out of S^T's accumulators by two 8 x 8 transposes (movmatrix).
 // Levels times scales are exact in fp16.  Queries are multiplied by the power of two that
 // brings their row's largest value to 2^14, and rounded to fp16 (what a bf16 value loses
-// lies 2^39 below the row's largest).  Weights are rounded to fp16: they are kept below
-// 2^11 by raising the row's maximum when a score passes it by 2^10.
+// lies 2^39 below the row's largest).  Weights are rounded to fp16: they start at 2^6 (kFp4Start) and are
+// kept below 2^16 by raising the row's maximum.
 //
 // Warps.  One thread block an SM.  Two warps copy K's and V's codes and scales of key tiles into a
 // ring of eight, and the query rows of the segments; 16 warps (8 for row tiles of 16, whose state is
@@ -75,7 +75,7 @@ constexpr int32_t kFewRows = 16;             // rows of a sequence that are done
 constexpr int32_t kFewListed = 8;
 // A row tile of n key tiles counts n + kRowCost in a run.
 constexpr int32_t kRowCost = 2;
-constexpr float kRaise = 10.0f;  // log2 of how far a weight may pass its row's maximum
+constexpr float kMost = 15.9f;  // log2 of the largest weight (fp16 numbers end at 2^16)
 
 enum { kPlain = 0, kWindow = 1, kListed = 2 };
 
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
             // A row that passes the limit takes a new maximum; the others' exponents come out as above, bit by bit,
             // so that what one row holds does not show in another.  (The largest exponent of a row is that of its
             // largest product: fmaf rounds in order.)
-            if (__any_sync(0xffffffffu, top > kRaise)) {
+            if (__any_sync(0xffffffffu, top > kMost)) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) k_fp4_rows(const __gr
                         }
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
-                        const bool raise = fmaf(best, fac[b][y], -m[b][y]) > kRaise;
-                        const float m_new = raise ? best * fac[b][y] : m[b][y];
+                        const bool raise = fmaf(best, fac[b][y], -m[b][y]) > kMost;
+                        const float m_new = raise ? fmaf(best, fac[b][y], -kFp4Start) : m[b][y];
                         const float keep = raise ? ex2(m[b][y] - m_new) : 1.0f;
                         m[b][y] = m_new;
                         l[b][y] *= keep;

@@ -27,8 +27,8 @@
 // buffers (510 us: unpacking is not what bounds it, and loads and buffers are missed); queries through the ring
 // of codes (484); a segment told and its queries loaded before the end of the one before (485 and 495).
 //
-// Rounding.  Weights are rounded to fp16 for the product P V; they stay below 2^15 against an
-// earlier maximum of their row (see softmax_rows).  Row sums add them unrounded.
+// Rounding.  Weights are rounded to fp16 for the product P V; they start at 2^6 (kFp4Start) and stay below 2^16 against
+// an earlier maximum of their row (see softmax_rows).  Row sums add them unrounded.
 //
 // Lists.  A row tile is as many whole tokens as 128 rows hold, and its key tiles are those that any of its tokens
 // lists; a bit for each token says whose.  The rows of a token that does not list a tile take no part in it.
@@ -55,7 +55,7 @@ constexpr int kWide = kFp4PromptWide;
 // have 8 to 50 row tiles each: 471 us with 4, 483 with 8, 501 with 12; two chunks of 2048 through a window of
 // 575, 6 key tiles to a row tile: 106, 102, 98 us.)
 constexpr int32_t row_cost(int mode) { return mode == 1 ? 12 : 4; }
-constexpr float kSumLimit = 32768.0f;                     // 2^15, see softmax_rows
+constexpr float kSumLimit = 65504.0f;                     // fp16's largest number, see softmax_rows
 constexpr int kSBuf = 3;                                  // TMEM score buffers
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 384;
@@ -152,7 +152,7 @@ __device__ __forceinline__ void exp_rows_f16(uint32_t (&s)[64], const float (&f)
 // One key tile of the online softmax for this thread's shares of rows a and b.
 // hidden: the row sees nothing of the tile (its weights are 0).  A row that has seen no key yet has
 // m = kFp4NoKey; one that holds no token has scores of 0.  Exponentials are taken against the running maxima
-// without computing the tile's own.  Where a row's sums leave 2^15 (its first key makes them infinite) or are
+// without computing the tile's own.  Where a row's sums leave fp16's range (its first key makes them infinite) or are
 // NaN, the tile is redone with that row's new maximum, and against the maxima that the warp's other rows had,
 // to the same bits: what one row holds does not show in another.  (So a row's redone tile is paid for by 128
 // rows; the redo itself is mostly the wait for its instructions, some 600 cycles of all of them.)  first: no row of
@@ -181,7 +181,7 @@ __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&hid
     float bias[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        mt[i] *= f[i];
+        mt[i] = fmaf(mt[i], f[i], -kFp4Start);
         // (a row's four threads are neighbours)
         if ((over[i] >> (threadIdx.x & 28u) & 15u) != 0u && !hidden[i] && mt[i] > m[i]) {
             alpha[i] = ex2(m[i] - mt[i]);

@@ -153,3 +153,42 @@ def test_the_smallest_and_largest_gains_of_attention(D, page, new, heads):
     O = b.v_cache[b.table[0, 0].long()].double().mean(1).repeat_interleave(heads, 0)  # [2 * heads, D]
     assert ((o.double() - O).abs() <= (2.0 ** -8 * 1.01 + 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12) * O.abs()).all()
     assert ((lse.double() - np.log(29 << 16)).abs() <= 2.0 ** -12 + 8 * 2.0 ** -24 * 15).all()
+
+
+# ------------------------------------------------------------------ weights far below a row's largest
+
+@pytest.mark.parametrize("even", [False, True])
+@pytest.mark.parametrize("nats", [12, 15, 17])
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_small_weights_beside_a_sink(D, page, new, nats, even):
+    """The first key takes nearly all of the weight and has a value of 0: O is what the others leave, of many weights or
+    (even) of one.
+
+    fp4_ref.check_attention's bound with its last term as small as it has to be: a weight is rounded where its row's
+    largest is at least 2^6, so what fp16's smallest step 2^-24 takes is at most 2^-25 / 2^6 of that."""
+    b = ref.make([new, new], [8192, 30 if new < 30 else 60], H=4, H_kv=1, D=D, page=page, seed=149)
+    c = f4.Cache(b, 149)
+    c.v &= 0x77
+    c.k[..., :8] = 0                                # values 0 .. 15 are the sink's alone
+    per = 16 * 6 * D ** -0.5                        # nats to a scale of 1 there, against queries of 1
+    size = torch.tensor(nats / per).to(torch.float8_e4m3fn)
+    for s in range(2):
+        at = b.table[s, 0].long()
+        c.k[at, :, 0], c.v[at, :, 0] = 0, 0
+        c.k[at, :, 0, :8] = 0x77
+        c.k_scale[at, :, 0, 0] = size
+    c.refresh()
+    q = ref.rows(b, 4, 150)
+    q[..., :16] = 1
+    if even:
+        q[..., 16:] = 0
+    for kw in (dict(max_new=0), dict(max_new=new)):
+        o, lse = run_forward(b, c, q, **kw)
+        status_ok()
+        O, L, A, R = ref.attend(b, q)
+        assert float((L - size.double().item() * per).amax()) < 0.2  # (the sink has the weight)
+        d = (D + 16) * 2.0 ** -24 * (R + 1)
+        bound = 2.0 ** -8 * 1.01 * O.abs() + (2.0 ** -11 * 1.01 + 2 * d[..., None]) * A + 2.0 ** -31 * f4.visible(b)
+        err = (o.double() - O).abs()
+        assert (err <= bound).all(), f"{float((err / bound).max()):.2f} of the bound"
