@@ -1,7 +1,7 @@
 // Reading a key/value cache held in 4 bits back: the last new tokens of every
 // sequence of a ragged batch, out of their pages, as bf16 rows [tokens, H_kv, D].
 //
-// A value is level * scale, exact in fp32, times the head's gain, rounded once.
+// A value is level * scale, exact in fp32, times the head's gain, rounded once (see read_values).
 // The work is bound by its bytes (nine read for every 64 written; 131072 tokens of 8 heads of 128, 687 MB:
 // 110 us, 0.92 of the copy rate; 6 tails of up to 150 tokens: 2.8 us, a launch's latency).  A thread block takes up to
 // 64 tokens' keys or values; a thread has one place of a token's H_kv D values, eight of
@@ -32,8 +32,49 @@ struct ReadParams {
     int32_t span;   // tokens of a thread block, at most kReadTokens
 };
 
-template <int D>
-__global__ void __launch_bounds__(kReadThreads) k_paged_read(const __grid_constant__ ReadParams P) {
+// Eight values of codes w under a scale y, as they are (exact) or times the gain g: the bf16 numbers nearest to the
+// products.  A product rounded to fp32 and then to bf16 goes astray only where the first rounding has ended halfway
+// between two bf16 numbers (low half 0x8000: one value in some 2^16); read_halfway moves it there by its last bit towards
+// the product, which is exact in fp64 (6 + 24 bits).
+__device__ __forceinline__ void fp4_products(uint32_t w, uint32_t y, float2 (&x)[4]) {
+    __half2 h[4];
+    fp4_levels(w, h);
+    const __half2 sc = __half2half2(__low2half(fp4_scales(y)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __half22float2(__hmul2(h[i], sc));
+}
+__device__ __noinline__ uint4 read_halfway(uint32_t w, uint32_t y, float g) {
+    float2 x[4];
+    fp4_products(w, y, x);
+    auto nearest = [&](float v) -> float {
+        const float p = v * g;
+        const double off = fma((double)v, (double)g, -(double)p);
+        if ((__float_as_uint(p) & 0xffffu) != 0x8000u || off == 0.0) return p;
+        return __uint_as_float(__float_as_uint(p) + ((off > 0.0) == (p > 0.0f) ? 1u : ~0u));
+    };
+    return make_uint4(pack_bf16(nearest(x[0].x), nearest(x[0].y)), pack_bf16(nearest(x[1].x), nearest(x[1].y)),
+                      pack_bf16(nearest(x[2].x), nearest(x[2].y)), pack_bf16(nearest(x[3].x), nearest(x[3].y)));
+}
+template <bool kGain>
+__device__ __forceinline__ uint4 read_values(uint32_t w, uint32_t y, float g) {
+    float2 x[4];
+    fp4_products(w, y, x);
+    if constexpr (kGain) {
+        uint32_t low[4];  // two products' low halves: as signed numbers, 0x8000 is the smallest
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i].x *= g;
+            x[i].y *= g;
+            low[i] = __byte_perm(__float_as_uint(x[i].x), __float_as_uint(x[i].y), 0x5410);
+        }
+        const uint32_t least = __vimin3_s16x2(__vimin3_s16x2(low[0], low[1], low[2]), low[3], low[3]);
+        if ((least & 0xffffu) == 0x8000u || least >> 16 == 0x8000u) return read_halfway(w, y, g);
+    }
+    return make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
+}
+
+template <int D, bool kGain>
+__global__ void __launch_bounds__(kReadThreads, 8) k_paged_read(const __grid_constant__ ReadParams P) {
     __shared__ int64_t part[33];
     __shared__ int32_t hit[5];
     __shared__ int32_t slot[kReadTokens];  // row of head 0 of each token (-1: none)
@@ -75,7 +116,7 @@ __global__ void __launch_bounds__(kReadThreads) k_paged_read(const __grid_consta
     if (sub >= abreast) return;
     for (int32_t x = threadIdx.x - sub * wide; x < places; x += wide) {
         const int32_t head = x / (D / 8), c = x % (D / 8);
-        const float g = gain != nullptr ? gain[head] : 1.0f;
+        const float g = kGain && gain != nullptr ? gain[head] : 1.0f;
         for (int32_t t = sub; t < n; t += 4 * abreast) {
             uint32_t w[4], y[4];
             int32_t at[4];
@@ -90,17 +131,8 @@ __global__ void __launch_bounds__(kReadThreads) k_paged_read(const __grid_consta
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (at[u] < 0) continue;
-                __half2 h[4];
-                fp4_levels(w[u], h);
-                const __half2 sc = __half2half2(__low2half(fp4_scales(y[u])));
-                __nv_bfloat162 r[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = __half22float2(__hmul2(h[i], sc));
-                    r[i] = __floats2bfloat162_rn(f.x * g, f.y * g);
-                }
                 __nv_bfloat16* to = out + ((int64_t)q.q0 + t0 + t + u * abreast) * stride + head * D + 8 * c;
-                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(r);
+                *reinterpret_cast<uint4*>(to) = read_values<kGain>(w[u], y[u], g);
             }
         }
     }
@@ -135,8 +167,10 @@ bsa_status launch_paged_read(const PagedReadArgs& a, int32_t* status, cudaStream
     }
     // sum over sequences of ceil(n / span) <= tokens / span + seqs
     const dim3 grid((unsigned)(a.tokens / P.span + a.seqs), (unsigned)sides);
-    const cudaError_t e = a.D == 128 ? launch_chained(k_paged_read<128>, grid, kReadThreads, 0, stream, P)
-                                     : launch_chained(k_paged_read<64>, grid, kReadThreads, 0, stream, P);
+    const bool gains = (a.k_out != nullptr && a.k_gain != nullptr) || (a.v_out != nullptr && a.v_gain != nullptr);
+    const auto kernel = a.D == 128 ? (gains ? k_paged_read<128, true> : k_paged_read<128, false>)
+                                   : (gains ? k_paged_read<64, true> : k_paged_read<64, false>);
+    const cudaError_t e = launch_chained(kernel, grid, kReadThreads, 0, stream, P);
     return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

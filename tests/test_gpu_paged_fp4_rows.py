@@ -192,3 +192,35 @@ def test_small_weights_beside_a_sink(D, page, new, nats, even):
         bound = 2.0 ** -8 * 1.01 * O.abs() + (2.0 ** -11 * 1.01 + 2 * d[..., None]) * A + 2.0 ** -31 * f4.visible(b)
         err = (o.double() - O).abs()
         assert (err <= bound).all(), f"{float((err / bound).max()):.2f} of the bound"
+
+
+def nearest_bf16(x):
+    """fp64 numbers whose nearest bf16 is a normal one, rounded to it once, halves to even."""
+    i = x.contiguous().view(torch.int64)
+    i = i + ((1 << 44) - 1) + (i >> 45 & 1)
+    return (i & ~((1 << 45) - 1)).view(torch.float64)
+
+
+def test_reading_back_rounds_once():
+    """Every level under every scale, times 4096 gains: the bf16 number nearest to the product.  Among them 0.625 times
+    0x1.78ccccp-4, whose nearest fp32 number lies halfway between two of bf16's."""
+    K = 4096
+    b = ref.make([32], [32], H=K, H_kv=K, D=64, page=16, seed=152, poison=False)
+    c = f4.Cache(b, 152)
+    order = b.pages_of(0)
+    c.k[:] = torch.tensor([i | (i + 1) << 4 for i in range(0, 16, 2)], dtype=torch.uint8, device="cuda").repeat(4)
+    scale = torch.arange(128, dtype=torch.uint8, device="cuda").clamp(1, 126).reshape(2, 1, 16, 4).expand(2, K, 16, 4)
+    c.k_scale.view(torch.uint8)[order] = scale
+    g = torch.Generator().manual_seed(153)
+    c.k_gain = (torch.rand(K, generator=g) + 0.5).cuda()
+    c.k_gain[7] = float.fromhex("0x1.78ccccp-4")
+    c.refresh()
+    out = torch.empty((32, K, 64), dtype=torch.bfloat16, device="cuda")
+    bsa.paged_read_fp4(*c.arrays(), *b.arrays(), out, **c.gains())
+    status_ok()
+    held = b.k_cache[order].double().permute(0, 2, 1, 3).reshape(32, K, 64)
+    # (levels, scales and gains are multiples in fp64 without a rounding: 6 + 24 bits)
+    off = out.double() != nearest_bf16(held)
+    assert not off.any(), f"{int(off.sum())} of {off.numel()} values are not the nearest"
+    half = (held[:, 7] == 0.625 * c.k_gain[7].double()).nonzero()
+    assert len(half) and float(out[half[0, 0], 7, half[0, 1]]) == 0.057373046875
