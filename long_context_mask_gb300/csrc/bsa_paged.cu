@@ -523,8 +523,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const __grid_co
         float t = 0.f;
 #pragma unroll
         for (int g = 0; g < kRows; ++g) t += sums[g][threadIdx.x];
+        t *= 1.0f / kBlock;  // (before the gain: fp32 holds the mean where it may not hold the sum)
         if (kFp4 && P.k_gain != nullptr) t *= P.k_gain[h0];
-        P.k_mean[((int64_t)last * P.H_kv + h0) * D + threadIdx.x] = __float2bfloat16_rn(t * (1.0f / kBlock));
+        P.k_mean[((int64_t)last * P.H_kv + h0) * D + threadIdx.x] = __float2bfloat16_rn(t);
     }
 }
 

@@ -224,3 +224,20 @@ def test_reading_back_rounds_once():
     assert not off.any(), f"{int(off.sum())} of {off.numel()} values are not the nearest"
     half = (held[:, 7] == 0.625 * c.k_gain[7].double()).nonzero()
     assert len(half) and float(out[half[0, 0], 7, half[0, 1]]) == 0.057373046875
+
+
+def test_mean_keys_with_large_and_small_gains():
+    """Sums of 128 keys that 32 bits cannot hold, or hold with few bits only, where the means are normal numbers."""
+    b = ref.make([256], [256], H=4, H_kv=4, D=64, page=32, seed=154, poison=False)
+    c = f4.Cache(b, 154)
+    c.k_gain = torch.tensor([2.0 ** -126, 1.0, 2.0 ** 120, 2.0 ** 124], device="cuda")
+    k = ((ref.rows(b, 4, 155).double().abs() + 8) * c.k_gain.double()[:, None]).to(torch.bfloat16)
+    _, k_mean = run_append(b, c, None, k, k)
+    status_ok()
+    c.refresh()
+    for j in range(2):
+        pages = b.table[0, 4 * j:4 * j + 4].long()
+        keys = b.k_cache[pages]
+        mean, size = keys.mean((0, 2)), keys.abs().mean((0, 2))
+        # (as in check_append)
+        assert ((k_mean[pages[-1]].double() - mean).abs() <= 2.0 ** -8 * mean.abs() * 1.01 + 2.0 ** -16 * size).all()
