@@ -239,7 +239,7 @@ __device__ __forceinline__ void norm_row_each(float (&x)[8], const float (&w)[8]
 
 // Quantises and stores this thread's eight values of a row (load_row's places).  Every
 // thread of the warp calls it; row < 0: nothing is stored.  recip = 1 / gain, rounded.  Returns
-// whether a value of a stored row is not finite.
+// whether a value of a stored row is not finite (a quotient by the gain that is not is only out of range).
 template <int D, bool kHalves>
 __device__ __forceinline__ bool store_row_fp4(float (&x)[8], float gain, float recip, uint8_t* codes, uint8_t* scales,
                                               int64_t row, int c) {
@@ -254,12 +254,14 @@ __device__ __forceinline__ bool store_row_fp4(float (&x)[8], float gain, float r
         f2unpack(t2[i], t[2 * i], t[2 * i + 1]);
     }
     f2unpack(z, z0, z1);
-    const bool bad = !(z0 + z1 == 0.0f);
-    if (__any_sync(0xffffffffu, bad)) {
+    bool bad = false;
+    if (__any_sync(0xffffffffu, !(z0 + z1 == 0.0f))) {
         // infinities, and what the gain makes one: the largest number; NaN: 0
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+            bad |= !(fabsf(x[i]) <= FLT_MAX);
             t[i] = fabsf(t[i]) <= FLT_MAX ? t[i] : x[i] == x[i] ? copysignf(FLT_MAX, x[i]) : 0.0f;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) top[i >> 2] = fmaxf(top[i >> 2], fabsf(t[i]));

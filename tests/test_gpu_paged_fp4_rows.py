@@ -241,3 +241,26 @@ def test_mean_keys_with_large_and_small_gains():
         mean, size = keys.mean((0, 2)), keys.abs().mean((0, 2))
         # (as in check_append)
         assert ((k_mean[pages[-1]].double() - mean).abs() <= 2.0 ** -8 * mean.abs() * 1.01 + 2.0 ** -16 * size).all()
+
+
+def test_finite_numbers_beyond_the_range_are_no_error():
+    """However far: a quotient by the gain that 32 bits cannot hold is a magnitude beyond 2688 gains as any other."""
+    b = ref.make([3], [3], H=2, H_kv=2, D=64, page=16, seed=156, poison=False)
+    c = f4.Cache(b, 156)
+    c.k_gain = torch.tensor([2.0 ** -66, 2.0 ** -126], device="cuda")
+    c.v_gain = c.k_gain.flip(0).contiguous()
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    x[0, :, 5], x[0, :, 6], x[2, :, 40] = 1e30, 2.0 ** -60, -3e38
+    bsa.paged_append_fp4(x, x, *c.arrays(), *b.arrays(), **c.gains())
+    status_ok()
+    c.refresh()
+    for cache, gain in ((b.k_cache, c.k_gain), (b.v_cache, c.v_gain)):
+        for h in range(2):
+            got = b.keys(0, h, cache) / gain[h].double()
+            want = torch.zeros_like(got)
+            want[0, 5], want[2, 40] = 2688.0, -2688.0
+            want[0, 6] = 2688.0 if gain[h] == 2.0 ** -126 else 0.0   # (2^66 gains, 64 gains under a scale of 448)
+            assert torch.equal(got, want)
+    x[1, 1, 9] = INF
+    bsa.paged_append_fp4(x, x, *c.arrays(), *b.arrays(), **c.gains())
+    assert bsa.device_status() == 7
