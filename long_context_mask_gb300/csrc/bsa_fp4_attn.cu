@@ -31,8 +31,8 @@
 // one warp joins their parts of O in shared memory and stores the rows.  (64 tokens over caches up to
 // 8192, 32 + 8 heads of 128, 483 MB of codes and scales: 130 us with eight warps that loaded their 16
 // keys of a tile themselves, 95 with one loading warp and two thread blocks an SM, 99 in this
-// form, which has two blocks' warps without two blocks' unequal shares of the SM: 64 tokens over
-// 32768 403 -> 396, over pages of 16 of 64 values 85 -> 72.)
+// form, which has two blocks' warps without two blocks' unequal shares of the SM: 2 % faster on 64 tokens over
+// 32768 keys each, 15 % on short heads in short pages.)
 //
 // Split.  All (key/value head, sequence, row tile, key tile) units are laid out in that order
 // and cut into equal runs, one for each thread block.  A row tile's part in a run is joined
@@ -42,9 +42,9 @@
 // What bounds it.  The step of 64 tokens: 99 us, 4.9 TB/s, 0.72 of the copy rate.  The conversion of a
 // byte of codes runs at 64 lanes a cycle and SM, as do the nibbles' moves: that pipe is busy 53 % of the
 // time, issue slots 60 %, and the rest are waits that four warps a scheduler do not cover.  The same copies without
-// the arithmetic take 82 us (64 tokens over 32768: 403 us, 346 without, which is the copy rate).  One token over
+// the arithmetic take 82 us (64 tokens over 32768 keys each: 403 us, 346 without, which is the copy rate).  One token over
 // 131072: 38 us, 31 without the arithmetic, 22 at the copy rate: the start, the last parts and the join.
-// One token over 1000: 9.5 us, latency: finding the run, the page table, the first tile, the parts, the join.
+// One token over 1000: 9.7 us, latency: finding the run, the page table, the first tile, the parts, the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -756,12 +756,12 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     P.least = 1;
     P.most = INT32_MAX;
     // Rows of a sequence, at most, as far as the host knows.  Row tiles of 16 for tokens of more than eight rows and
-    // where some sequence has 9 to 16 (64 x 4 tokens of 4 rows over 4096: 111 us, 129 with two tiles of 8), else
-    // of 8 (64 tokens over 8192: 99 us, 138 with tiles of 16).
+    // where some sequence has 9 to 16 (64 x 4 tokens of 4 rows over 4096: 110 us, 126 with two tiles of 8), else
+    // of 8 (64 tokens over up to 8192: 101 us, 143 with tiles of 16).
     const int64_t most = (int64_t)(x.max_new > 0 && x.max_new < a.tokens ? x.max_new : a.tokens) * P.group;
     const bool wide = P.group > 8 || (a.sel == nullptr && most > 8 && most <= kFewRows);
     // Tokens of few rows take the blocks that they list one by one; of many, a tile of tokens takes what any of them lists,
-    // whose bits say who (2048 tokens over 257 blocks, 66 random ones each: 3250 us one by one, 885).
+    // whose bits say who (2048 tokens over 257 blocks, 66 random ones each: 3250 us one by one, 878).
     auto with_lists = [&](int x) -> bsa_status {
         const Layout::Lists& l = L.lists[x];
         int32_t* cnt = reinterpret_cast<int32_t*>(ws + l.cnt);
@@ -778,9 +778,9 @@ bsa_status launch_fp4_forward(const Fp4ForwardArgs& x, void* workspace, int32_t*
     };
     // sequences of few rows here, the others on large tiles, unless the host knows of no others (what it
     // was told may be wrong: then all of them are done here)
-    // One sequence that may have many: all of it there, whatever it has (two launches less: 64 tokens over 4096 25.0 -> 21.5 us,
-    // a prompt of 8192 469 -> 460.  A single token where 256 may come, over 1000 keys, 12.6 us, over 131072 64; whoever
-    // tells max_new = 1 has it in 9.5 and 38.)
+    // One sequence that may have many: all of it there, whatever it has (two launches less: 64 tokens over 4096 26.9 -> 22.4 us,
+    // a prompt of 8192 470 -> 454.  A single token where 256 may come, over 1000 keys, 12.6 us, over 131072 64; whoever
+    // tells max_new = 1 has it in 9.7 and 38.)
     const bool lists = a.sel != nullptr;
     const int32_t few = lists && P.group <= 16 ? kFewListed * P.group : kFewRows;
     if (a.seqs == 1 && most > few) {

@@ -16,16 +16,20 @@
 // Shared memory: the Q tile, two K and two V tiles (four with D = 64), three tiles of codes.  Tensor memory:
 // three score buffers and O.  Tiles are numbered through the whole run, across the borders of segments.
 //
-// What bounds it.  A prompt of 8192 (32 + 8 heads of 128): 460 us, 1.19 PFLOP/s of visible products, 0.62 of the
-// burst rate of a plain product; the tensor pipe is busy half the time.  The softmax takes some 1,700
+// What bounds it.  A prompt of 8192 (32 + 8 heads of 128): 455 us, 1.21 PFLOP/s of visible products, 0.63 of the
+// burst rate of a plain product; the tensor pipe is busy half the time.  The softmax takes some 1,750
 // cycles a key tile (the products 1,024) beside the unpacking warps, which issue every third
-// instruction (issue slots 64 % full), and a segment's start costs some 4,000 more: its queries are put in
-// place after the segment before is through with theirs.  (A chunk of 1024 over 64512, whose segments are long: 780 us,
-// 1.40 PFLOP/s, 0.73.)  One set of warps for K, V and the queries: 897 us; K's and V's apart 530; the same
-// loop for both, so that it stays in the instruction cache, and each query load in its own register: 470.
-// Slower than this: row tiles of 256, each unpacked tile used twice, with one tile of codes and two score
+// instruction (issue slots 65 % full): so much where segments are long (a chunk of 1024 over 64512: 781 us,
+// 1.40 PFLOP/s, 0.73, 856 key tiles a thread block).  The rest is by row tile: a block of the prompt has 438 key tiles
+// and 13.5 row tiles, which leaves some 9,000 cycles for a row tile's start, end and masked tile (queries are put in
+// place after the segment before is through with theirs); through a window of 575 + 64 sinks (105 us, 45.5 key tiles and
+// 6.7 row tiles a block) it leaves 18,000.
+// One set of warps for K, V and the queries took 897 us; K's and V's apart 530; the same
+// loop for both, so that it stays in the instruction cache, and each query load in its own register 470.
+// Slower, when the prompt took 460: row tiles of 256, each unpacked tile used twice, with one tile of codes and two score
 // buffers (510 us: unpacking is not what bounds it, and loads and buffers are missed); queries through the ring
 // of codes (484); a segment told and its queries loaded before the end of the one before (485 and 495).
+// All warps share 96 registers a thread: what the softmax holds over a tile decides the time (see softmax_rows).
 //
 // Rounding.  Weights are rounded to fp16 for the product P V; they start at 2^6 (kFp4Start) and stay below 2^16 against
 // an earlier maximum of their row (see softmax_rows).  Row sums add them unrounded.
@@ -52,8 +56,8 @@ namespace {
 
 constexpr int kWide = kFp4PromptWide;
 // A row tile of n key tiles counts n + row_cost in a run.  (A causal prompt of 8192, whose blocks
-// have 8 to 50 row tiles each: 471 us with 4, 483 with 8, 501 with 12; two chunks of 2048 through a window of
-// 575, 6 key tiles to a row tile: 106, 102, 98 us.)
+// have 8 to 50 row tiles each: 453 us with 4, 471 with 8, 490 with 12; two chunks of 2048 through a window of
+// 575, 6 key tiles to a row tile: 117, 110, 107 us.)
 constexpr int32_t row_cost(int mode) { return mode == 1 ? 12 : 4; }
 constexpr float kSumLimit = 65504.0f;                     // fp16's largest number, see softmax_rows
 constexpr int kSBuf = 3;                                  // TMEM score buffers
@@ -154,10 +158,11 @@ __device__ __forceinline__ void exp_rows_f16(uint32_t (&s)[64], const float (&f)
 // m = kFp4NoKey; one that holds no token has scores of 0.  Exponentials are taken against the running maxima
 // without computing the tile's own.  Where a row's sums leave fp16's range (its first key makes them infinite) or are
 // NaN, the tile is redone with that row's new maximum, and against the maxima that the warp's other rows had,
-// to the same bits: what one row holds does not show in another.  (So a row's redone tile is paid for by 128
-// rows; the redo itself is mostly the wait for its instructions, some 600 cycles of all of them.)  first: no row of
-// the warp has seen a key, and all take their first maximum at once.  Returns true (warp-uniform) when O must be
-// multiplied by alpha first.
+// to the same bits: what one row holds does not show in another.  first: no row of the warp has seen a key, and
+// all take their first maximum at once.  Returns true (warp-uniform) when O must be multiplied by alpha first.
+// A tile redone for one row holds up 128, some 600 cycles, most of them the wait for instructions that have left the cache.
+// (Prompt of 8192: the votes of both rows kept as they come 456 us; made truth values 492, one mask 454, but lists of 2048
+// tokens 878, 914, 936; maxima looked for at tiles 1, 2, 4, .. so that fewer rows pass their limit 510 and more.)
 template <typename Reload>
 __device__ __forceinline__ bool softmax_rows(uint32_t (&s)[64], const bool (&hidden)[2], const float (&f)[2], bool first, float (&m)[2],
                                              float (&l)[2], float (&alpha)[2], Reload&& reload) {
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_fp4_prompt(const __grid_constan
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     int32_t* const status = P.b.status;
-    // pages of 16 have too many copies for one warp (a prompt of 8192: 542 us with one, 484 with two; longer pages 459, 475)
+    // pages of 16 have too many copies for one warp (a prompt of 8192: 531 us with one, 472 with two; pages of 128 454, 459)
     const bool two_load = P.b.page < 32;
 
     if (threadIdx.x == kThreads - 1) {
@@ -882,7 +887,7 @@ bsa_status launch_d(const Fp4Params& P, bool first, cudaStream_t stream) {
     const int grid = sms[dev] < kPagedBlocks ? sms[dev] : kPagedBlocks;
     constexpr int kRows = kFp4JoinThreads / (D / 4);
     // As a call's first kernel it does not start beside the one before it, whose SMs its blocks would take as they fall free,
-    // in any order (a chunk of 1024 over 64512, again and again: 832 us so, 780 in order).
+    // in any order (a chunk of 1024 over 64512, again and again: 846 us so, 781 in order).
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);

@@ -3,7 +3,7 @@
 //
 // A value is level * scale, exact in fp32, times the head's gain, rounded once (see read_values).
 // The work is bound by its bytes (nine read for every 64 written; 131072 tokens of 8 heads of 128, 687 MB:
-// 110 us, 0.92 of the copy rate; 6 tails of up to 150 tokens: 2.8 us, a launch's latency).  A thread block takes up to
+// 109 us, 0.93 of the copy rate, 114 with gains; 6 tails of up to 150 tokens: 3.1 us, a launch's latency).  A thread block takes up to
 // 64 tokens' keys or values; a thread has one place of a token's H_kv D values, eight of
 // them, and goes through the tokens, four loads under way at a time, so that the
 // block's threads write whole tokens one after another.
